@@ -11,9 +11,17 @@ from ._lib import LibsconvError, load
 from .ops import (
     causal_conv1d_update,
     causal_conv1d_update_tokens,
+    causal_conv1d_varlen_bwd,
     causal_conv1d_varlen_fwd,
+    gated_linear_recurrence_checkpoints,
+    gated_linear_recurrence_update,
+    gated_linear_recurrence_varlen_bwd,
+    gated_linear_recurrence_varlen_fwd,
     gather_intermediate_conv_window,
     gather_intermediate_ssm_state,
+    rms_norm_bwd,
+    rms_norm_fwd,
+    rms_norm_quant,
     sconv_fused_insert_conv,
     sconv_fused_insert_conv_gather,
     sconv_fused_insert_conv_qsl,
@@ -28,9 +36,17 @@ __all__ = [
     "LibsconvError",
     "causal_conv1d_update",
     "causal_conv1d_update_tokens",
+    "causal_conv1d_varlen_bwd",
     "causal_conv1d_varlen_fwd",
+    "gated_linear_recurrence_checkpoints",
+    "gated_linear_recurrence_update",
+    "gated_linear_recurrence_varlen_bwd",
+    "gated_linear_recurrence_varlen_fwd",
     "gather_intermediate_conv_window",
     "gather_intermediate_ssm_state",
+    "rms_norm_bwd",
+    "rms_norm_fwd",
+    "rms_norm_quant",
     "sconv_fused_insert_conv",
     "sconv_fused_insert_conv_gather",
     "sconv_fused_insert_conv_qsl",

@@ -16,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsconv.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_HIP = 0, 1, 2, 3
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 ACT_NONE, ACT_SILU = 0, 1
 
 EXPORTS = (
@@ -34,11 +34,21 @@ EXPORTS = (
     "causal_conv1d_update_tokens",
     "gather_intermediate_conv_window",
     "gather_intermediate_ssm_state",
+    "gated_linear_recurrence_checkpoint_rows",
+    "gated_linear_recurrence_varlen_fwd",
+    "gated_linear_recurrence_varlen_bwd",
+    "gated_linear_recurrence_update",
+    "causal_conv1d_varlen_bwd",
+    "rms_norm_fwd",
+    "rms_norm_bwd_workspace",
+    "rms_norm_bwd",
 )
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
 I64 = ctypes.c_int64
+FLT = ctypes.c_float
+PI64 = ctypes.POINTER(I64)
 
 
 class StreamT(ctypes.Structure):
@@ -91,6 +101,22 @@ _SIGS = {
                                     I32, P],
     "gather_intermediate_conv_window": [P, I64, I32, I64, I64, P, P, I32, P, I64, I32, I32, P],
     "gather_intermediate_ssm_state": [P, I64, I64, I64, P, P, I32, P, I64, I32, P],
+    "gated_linear_recurrence_checkpoint_rows": [I64, I32, PI64],
+    "gated_linear_recurrence_varlen_fwd": [P, I64, I64, P, I64, I64, P, I64, I64, P, FLT, P, I64,
+                                           I64, P, I32, P, P, P, I64, I64, P, I64, I32, I64, I32,
+                                           I32, P],
+    "gated_linear_recurrence_varlen_bwd": [P, I64, I64, P, I64, I64, P, I64, I64, P, I64, I64, P,
+                                           FLT, P, I64, P, I32, P, P, I64, P, I64, P, I64, P,
+                                           I64, I64, P, I64, I64, P, I64, I64, P, P, I64, I32,
+                                           I64, I32, I32, P],
+    "gated_linear_recurrence_update": [P, I64, P, I64, P, I64, P, FLT, P, I64, I64, P, P, I64,
+                                       I32, I32, I32, I32, P],
+    "causal_conv1d_varlen_bwd": [P, I64, I64, P, I64, I64, P, I64, I64, P, P, I64, I64, I64, I64,
+                                 P, I32, P, P, P, I64, I64, I64, P, I64, I64, I64, P, I64, I64, P,
+                                 P, P, I64, I32, I64, I32, I32, I32, I32, P],
+    "rms_norm_fwd": [P, I64, P, I64, P, FLT, P, I64, P, I64, P, I64, I32, I64, I32, I32, I32, P],
+    "rms_norm_bwd_workspace": [I64, I32, PI64],
+    "rms_norm_bwd": [P, I64, P, I64, P, FLT, P, I64, P, I64, P, P, I64, I64, I32, I32, P],
 }
 
 

@@ -1,0 +1,97 @@
+// recurrence_device.h -- the gate arithmetic of the gated linear recurrence,
+// shared by its forward, backward and one-token kernels.
+//
+//   r = sigmoid(gate_a), i = sigmoid(gate_x)
+//   log a = -k r,  k = decay_scale * softplus(decay)   (per channel)
+//   m = sqrt(1 - a^2),  h_t = a_t h_{t-1} + m_t i_t x_t
+//
+// Everything is fp32.  The hardware exp2, reciprocal and square roots are
+// good to about 1 ulp, and every use of them here is relative: a gate near
+// one keeps 1 - a^2 exact to a few ulp through expm1 (below), so a state
+// that decays over thousands of tokens keeps the precision of its inputs.
+#pragma once
+
+#include "sconv_device.h"
+
+namespace sconv {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kMarkTokens = 128;  // tokens between two checkpoints of the state
+
+// Per-channel constants of the decay.
+struct Decay {
+  float k;       // decay_scale * softplus(decay)
+  float k_log2;  // the same in powers of two
+};
+
+__device__ __forceinline__ Decay make_decay(float decay, float scale) {
+  // softplus; past 20 it equals its argument in fp32
+  const float sp = decay > 20.f ? decay : log1pf(expf(decay));
+  Decay d;
+  d.k = scale * sp;
+  d.k_log2 = d.k * kLog2e;
+  return d;
+}
+
+__device__ __forceinline__ float sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -kLog2e));
+}
+
+// 1 - a^2 from y = 2 log a <= 0 and a itself.  For y > -0.7 it is
+// -y (e^y - 1)/y with the quotient's Chebyshev interpolant of degree 5 on
+// [-0.7, 0] (relative error 1.1e-8, coefficients computed for this file);
+// below, 1 - a^2 >= 0.5 and the difference loses at most one bit.  A result
+// below the smallest normal number counts as zero.
+__device__ __forceinline__ float one_minus_square(float y, float a) {
+  float q = 1.0332433739677072e-3f;
+  q = __builtin_fmaf(q, y, 8.06795246899128e-3f);
+  q = __builtin_fmaf(q, y, 4.157276451587677e-2f);
+  q = __builtin_fmaf(q, y, 1.6665145754814148e-1f);
+  q = __builtin_fmaf(q, y, 4.9999910593032837e-1f);
+  q = __builtin_fmaf(q, y, 1.0f);
+  const float near = -y * q, far = __builtin_fmaf(-a, a, 1.0f);
+  return y > -0.7f ? near : far;
+}
+
+// One token's gates.
+struct Gates {
+  float r, i, a, m;
+};
+
+__device__ __forceinline__ Gates make_gates(float ga, float gx, const Decay& d) {
+  Gates g;
+  g.r = sigmoid(ga);
+  g.i = sigmoid(gx);
+  g.a = __builtin_amdgcn_exp2f(-d.k_log2 * g.r);
+  g.m = __builtin_amdgcn_sqrtf(one_minus_square(-2.0f * d.k * g.r, g.a));
+  return g;
+}
+
+// The same with 1/m for the backward pass: zero where m is zero (the limit
+// of every gradient that it enters, since it comes with a factor m^2).
+struct GatesInv {
+  float r, i, a, m, inv_m;
+};
+
+__device__ __forceinline__ GatesInv make_gates_inv(float ga, float gx, const Decay& d) {
+  GatesInv g;
+  g.r = sigmoid(ga);
+  g.i = sigmoid(gx);
+  g.a = __builtin_amdgcn_exp2f(-d.k_log2 * g.r);
+  const float m2 = one_minus_square(-2.0f * d.k * g.r, g.a);
+  // Zero below the normal range, but a NaN stays one.
+  const float inv = __builtin_amdgcn_rsqf(m2);
+  g.inv_m = m2 < 1.17549435e-38f ? 0.0f : inv;
+  g.m = m2 * g.inv_m;
+  return g;
+}
+
+template <typename D>
+__device__ __forceinline__ typename D::storage round_to(float v) {
+  if constexpr (sizeof(typename D::storage) == 2)
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
+  else
+    return v;
+}
+
+}  // namespace sconv

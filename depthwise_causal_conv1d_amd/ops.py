@@ -509,3 +509,360 @@ def gather_intermediate_ssm_state(states: torch.Tensor, chunk_indices: torch.Ten
         _ptr(chunk_indices), _ptr(real_count_gpu), max_count, _ptr(out),
         out.stride(0) if out.dim() > 1 else 1, dt, _stream(states))
     _lib.check(rc, "gather_intermediate_ssm_state")
+
+
+# ---------------------------------------------------------------- the layer around the conv
+
+def _one_device(first: torch.Tensor, *ts):
+    """Every tensor on the first one's GPU."""
+    if not first.is_cuda:
+        raise ValueError("libsconv tensors must live on the GPU")
+    dev = first.device
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device} in one call")
+
+
+def _call(name: str, on: torch.Tensor, *args):
+    """One library call on the current stream of `on`'s device."""
+    fn = getattr(_lib.load(), name)
+    index = on.device.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, torch.cuda.current_stream(index).cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, torch.cuda.current_stream(index).cuda_stream)
+    if rc:
+        _lib.check(rc, name)
+
+
+def _same_type(x: torch.Tensor, what: str, *ts) -> int:
+    dt = _dtype(x)
+    for t in ts:
+        if t is not None and t.dtype != x.dtype:
+            raise TypeError(f"{what} must share one element type")
+    return dt
+
+
+def _planes(shape, *ts):
+    """[ptr, stride_c, stride_t] of each [dim, total_T] tensor."""
+    args = []
+    for t in ts:
+        if t.shape != shape:
+            raise ValueError("the [dim, total_T] tensors of a call must have one shape")
+        args += [t.data_ptr(), t.stride(0), t.stride(1)]
+    return args
+
+
+def _packing(query_start_loc, cache_indices, has_initial_state):
+    """(batch, has_initial_state as uint8) after checks."""
+    batch = query_start_loc.numel() - 1
+    _vec(query_start_loc, torch.int32, "query_start_loc", 1)
+    if cache_indices is not None:
+        _vec(cache_indices, torch.int32, "cache_indices", batch)
+    hi = has_initial_state
+    if hi is not None:
+        if hi.dtype == torch.bool:
+            hi = hi.view(torch.uint8)
+        _vec(hi, torch.uint8, "has_initial_state", batch)
+    return batch, hi
+
+
+def _pool(t: Optional[torch.Tensor], dim: int, name: str):
+    """Checks of an fp32 [num_slots, dim] state pool."""
+    if t is None:
+        return
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != dim:
+        raise ValueError(f"{name} must be [num_slots, dim]")
+    if dim > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} needs contiguous channels")
+
+
+def gated_linear_recurrence_checkpoints(x: torch.Tensor, query_start_loc: torch.Tensor
+                                        ) -> torch.Tensor:
+    """The buffer in which gated_linear_recurrence_varlen_fwd leaves what its
+    backward call needs, for inputs like x [dim, total_T]."""
+    if x.dim() != 2:
+        raise ValueError("x [dim, total_T]")
+    rows = ctypes.c_int64()
+    _lib.check(_lib.load().gated_linear_recurrence_checkpoint_rows(
+        x.shape[1], query_start_loc.numel() - 1, ctypes.byref(rows)),
+        "gated_linear_recurrence_checkpoint_rows")
+    return torch.empty(rows.value, x.shape[0], dtype=torch.float32, device=x.device)
+
+
+def gated_linear_recurrence_varlen_fwd(x: torch.Tensor, gate_a: torch.Tensor,
+                                       gate_x: torch.Tensor, decay: torch.Tensor,
+                                       states: Optional[torch.Tensor],
+                                       query_start_loc: torch.Tensor,
+                                       cache_indices: Optional[torch.Tensor] = None,
+                                       has_initial_state: Optional[torch.Tensor] = None,
+                                       decay_scale: float = 8.0, pad_slot_id: int = -1,
+                                       out: Optional[torch.Tensor] = None,
+                                       checkpoints: Optional[torch.Tensor] = None
+                                       ) -> torch.Tensor:
+    """h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(gate_x) x over packed
+    sequences, a = exp(-decay_scale softplus(decay) sigmoid(gate_a)).
+
+    x, gate_a, gate_x [dim, total_T] (any strides), decay float32 [dim].
+    states float32 [num_slots, dim] is updated in place (None: start at zero,
+    keep nothing).  ``checkpoints`` (gated_linear_recurrence_checkpoints) is
+    filled for the backward call.  With ``out`` None a new tensor is returned,
+    whose rows outside the sequences (or in skipped ones) are undefined.
+    """
+    if x.dim() != 2 or decay.dim() != 1:
+        raise ValueError("x, gate_a, gate_x [dim, total_T], decay [dim]")
+    if out is None:
+        out = torch.empty_like(x)
+    dim, total_T = x.shape
+    _one_device(x, gate_a, gate_x, decay, states, query_start_loc, cache_indices,
+                has_initial_state, out, checkpoints)
+    dt = _same_type(x, "x, the gates and out", gate_a, gate_x, out)
+    batch, hi = _packing(query_start_loc, cache_indices, has_initial_state)
+    _vec(decay, torch.float32, "decay", dim)
+    _pool(states, dim, "states")
+    rows = 0
+    if checkpoints is not None:
+        if checkpoints.dtype != torch.float32 or checkpoints.dim() != 2 or \
+                checkpoints.shape[1] != dim or not checkpoints.is_contiguous():
+            raise ValueError("checkpoints must be a dense float32 [rows, dim] tensor")
+        rows = checkpoints.shape[0]
+    pl = _planes(x.shape, x, gate_a, gate_x, out)
+    _call("gated_linear_recurrence_varlen_fwd", x, *pl[:9], decay.data_ptr(), decay_scale,
+          _ptr(states), states.shape[0] if states is not None else 0,
+          states.stride(0) if states is not None else 0, query_start_loc.data_ptr(), batch,
+          _ptr(cache_indices), _ptr(hi), *pl[9:], _ptr(checkpoints), rows, dim, total_T, dt,
+          int(pad_slot_id))
+    return out
+
+
+def gated_linear_recurrence_varlen_bwd(dout: torch.Tensor, x: torch.Tensor, gate_a: torch.Tensor,
+                                       gate_x: torch.Tensor, decay: torch.Tensor,
+                                       checkpoints: torch.Tensor, query_start_loc: torch.Tensor,
+                                       cache_indices: Optional[torch.Tensor] = None,
+                                       has_initial_state: Optional[torch.Tensor] = None,
+                                       decay_scale: float = 8.0, pad_slot_id: int = -1,
+                                       dfinal_states: Optional[torch.Tensor] = None,
+                                       dinitial_states: Optional[torch.Tensor] = None,
+                                       dx: Optional[torch.Tensor] = None,
+                                       dgate_a: Optional[torch.Tensor] = None,
+                                       dgate_x: Optional[torch.Tensor] = None):
+    """Gradients of gated_linear_recurrence_varlen_fwd: (dx, dgate_a, dgate_x,
+    ddecay).  ``checkpoints`` is what the forward call left; the other inputs
+    are the forward's.  dfinal_states / dinitial_states float32 [num_slots,
+    dim]: gradient of each sequence's last state (read) and of its initial
+    state (written).  Gradients made here are undefined at tokens outside the
+    sequences (or in skipped ones)."""
+    if x.dim() != 2 or decay.dim() != 1:
+        raise ValueError("dout, x, gate_a, gate_x [dim, total_T], decay [dim]")
+    dim, total_T = x.shape
+    dx = torch.empty_like(x) if dx is None else dx
+    dgate_a = torch.empty_like(gate_a) if dgate_a is None else dgate_a
+    dgate_x = torch.empty_like(gate_x) if dgate_x is None else dgate_x
+    _one_device(x, dout, gate_a, gate_x, decay, checkpoints, query_start_loc, cache_indices,
+                has_initial_state, dfinal_states, dinitial_states, dx, dgate_a, dgate_x)
+    dt = _same_type(x, "dout, x, the gates and their gradients", dout, gate_a, gate_x, dx, dgate_a,
+                    dgate_x)
+    batch, hi = _packing(query_start_loc, cache_indices, has_initial_state)
+    _vec(decay, torch.float32, "decay", dim)
+    _pool(dfinal_states, dim, "dfinal_states")
+    _pool(dinitial_states, dim, "dinitial_states")
+    slots = 0
+    if dfinal_states is not None and dinitial_states is not None and \
+            dfinal_states.shape != dinitial_states.shape:
+        raise ValueError("dfinal_states and dinitial_states must have one shape")
+    for t in (dfinal_states, dinitial_states):
+        slots = t.shape[0] if t is not None else slots
+    if checkpoints.dtype != torch.float32 or checkpoints.dim() != 2 or \
+            checkpoints.shape[1] != dim or not checkpoints.is_contiguous():
+        raise ValueError("checkpoints must be a dense float32 [rows, dim] tensor")
+    pl = _planes(x.shape, dout, x, gate_a, gate_x, dx, dgate_a, dgate_x)
+    ddecay = torch.empty(dim, dtype=torch.float32, device=x.device)
+    ws = torch.empty(batch * dim, dtype=torch.float32, device=x.device)
+    _call("gated_linear_recurrence_varlen_bwd", x, *pl[:12], decay.data_ptr(), decay_scale,
+          checkpoints.data_ptr(), checkpoints.shape[0], query_start_loc.data_ptr(), batch,
+          _ptr(cache_indices), _ptr(hi), slots, _ptr(dfinal_states),
+          dfinal_states.stride(0) if dfinal_states is not None else 0, _ptr(dinitial_states),
+          dinitial_states.stride(0) if dinitial_states is not None else 0, *pl[12:],
+          ddecay.data_ptr(), ws.data_ptr(), ws.numel(), dim, total_T, dt, int(pad_slot_id))
+    return dx, dgate_a, dgate_x, ddecay
+
+
+def gated_linear_recurrence_update(x: torch.Tensor, gate_a: torch.Tensor, gate_x: torch.Tensor,
+                                   decay: torch.Tensor, states: torch.Tensor,
+                                   state_indices: Optional[torch.Tensor] = None,
+                                   decay_scale: float = 8.0, pad_slot_id: int = -1,
+                                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One decode token per row: x, gate_a, gate_x [batch, dim]; states
+    float32 [num_slots, dim] updated in place.  With ``out`` None a new tensor
+    is returned, whose skipped rows are undefined."""
+    if x.dim() != 2 or decay.dim() != 1:
+        raise ValueError("x, gate_a, gate_x [batch, dim], decay [dim]")
+    if out is None:
+        out = torch.empty_like(x)
+    batch, dim = x.shape
+    _one_device(x, gate_a, gate_x, decay, states, state_indices, out)
+    dt = _same_type(x, "x, the gates and out", gate_a, gate_x, out)
+    rows = []
+    for t in (x, gate_a, gate_x, out):
+        if t.shape != x.shape or (dim > 1 and t.stride(1) != 1):
+            raise ValueError("x, the gates and out need one shape and contiguous channels")
+        rows += [t.data_ptr(), t.stride(0)]
+    _vec(decay, torch.float32, "decay", dim)
+    _pool(states, dim, "states")
+    if state_indices is not None:
+        _vec(state_indices, torch.int32, "state_indices", batch)
+    _call("gated_linear_recurrence_update", x, *rows[:6], decay.data_ptr(), decay_scale,
+          states.data_ptr(), states.shape[0], states.stride(0), _ptr(state_indices), *rows[6:],
+          batch, dim, dt, int(pad_slot_id))
+    return out
+
+
+def causal_conv1d_varlen_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                             bias: Optional[torch.Tensor], initial_states: Optional[torch.Tensor],
+                             query_start_loc: torch.Tensor,
+                             cache_indices: Optional[torch.Tensor],
+                             has_initial_state: Optional[torch.Tensor], silu_activation: bool,
+                             pad_slot_id: int = -1,
+                             dfinal_states: Optional[torch.Tensor] = None,
+                             dinitial_states: Optional[torch.Tensor] = None,
+                             dx: Optional[torch.Tensor] = None):
+    """Gradients of causal_conv1d_varlen_fwd: (dx, dweight float32 [dim, W],
+    dbias float32 [dim] or None).  dout, x [dim, total_T] (x as it was before
+    the forward call, which may run in place); initial_states [num_slots, dim,
+    W-1]: the state pool before the forward call.  dfinal_states /
+    dinitial_states, same shape: gradient of the state that the forward left
+    (read) and of the initial state (written).  A dx made here is undefined at
+    tokens outside the sequences (or in skipped ones)."""
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("dout, x [dim, total_T], weight [dim, W]")
+    dim, total_T = x.shape
+    W = weight.shape[1]
+    dx = torch.empty_like(x) if dx is None else dx
+    pools = (initial_states, dfinal_states, dinitial_states)
+    _one_device(x, dout, weight, bias, query_start_loc, cache_indices, has_initial_state, dx,
+                *pools)
+    dt = _same_type(x, "dout, x, weight, bias, the states and dx", dout, weight, bias, dx, *pools)
+    if weight.shape[0] != dim:
+        raise ValueError("weight must be [dim, W]")
+    if bias is not None:
+        _vec(bias, x.dtype, "bias", dim)
+    batch, hi = _packing(query_start_loc, cache_indices, has_initial_state)
+    slots, pool_args = 0, []
+    for t in pools:
+        if t is None:
+            pool_args.append((None, 0, 0, 0))
+            continue
+        if t.dim() != 3 or t.shape[1] != dim or t.shape[2] != W - 1:
+            raise ValueError("states and their gradients must be [num_slots, dim, W-1]")
+        if slots and t.shape[0] != slots:
+            raise ValueError("states and their gradients must have one number of slots")
+        slots = t.shape[0]
+        pool_args.append((t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
+    pl = _planes(x.shape, dout, x, dx)
+    dweight = torch.empty(dim, W, dtype=torch.float32, device=x.device)
+    dbias = torch.empty(dim, dtype=torch.float32, device=x.device) if bias is not None else None
+    ws = torch.empty(batch * dim * (W + 1), dtype=torch.float32, device=x.device)
+    _call("causal_conv1d_varlen_bwd", x, *pl[:6], weight.data_ptr(), weight.stride(0),
+          weight.stride(1), _ptr(bias), *pool_args[0], slots, query_start_loc.data_ptr(), batch,
+          _ptr(cache_indices), _ptr(hi), *pool_args[1], *pool_args[2], *pl[6:],
+          dweight.data_ptr(), _ptr(dbias), ws.data_ptr(), ws.numel(), dim, total_T, W, dt,
+          _lib.ACT_SILU if silu_activation else _lib.ACT_NONE, int(pad_slot_id))
+    return dx, dweight, dbias
+
+
+def _rows(shape, *ts):
+    """[ptr, row stride] of each [rows, dim] tensor (None: NULL, 0)."""
+    args = []
+    for t in ts:
+        if t is None:
+            args += [None, 0]
+            continue
+        if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError("the [rows, dim] tensors of a call need one shape and contiguous "
+                             "channels")
+        args += [t.data_ptr(), t.stride(0)]
+    return args
+
+
+def _norm(x, weight, eps, residual, residual_out, out, scales, group_size, out_dt):
+    if x.dim() != 2 or weight.dim() != 1:
+        raise ValueError("x [rows, dim], weight [dim]")
+    rows, dim = x.shape
+    if residual is not None and residual_out is None:
+        residual_out = residual
+    _one_device(x, weight, residual, residual_out, out, scales)
+    dt = _same_type(x, "x, weight, residual and residual_out", weight, residual, residual_out)
+    _vec(weight, x.dtype, "weight", dim)
+    a = _rows(x.shape, x, residual, residual_out, out)
+    _call("rms_norm_fwd", x, *a[:4], weight.data_ptr(), eps, *a[4:], _ptr(scales),
+          scales.stride(0) if scales is not None else 0, group_size, rows, dim, dt,
+          dt if out_dt is None else out_dt)
+
+
+def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                 residual: Optional[torch.Tensor] = None,
+                 residual_out: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """s / sqrt(mean(s^2) + eps) * weight over rows, s = x + residual.
+
+    x, residual [rows, dim], weight [dim].  The sum goes to ``residual_out``,
+    or back to residual if that is None (in place, as a layer's stream does).
+    """
+    if out is None:
+        out = torch.empty_like(x)
+    if out.dtype != x.dtype:
+        raise TypeError("x and out must share one element type")
+    _norm(x, weight, eps, residual, residual_out, out, None, 0, None)
+    return out
+
+
+def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, group_size: int = 0,
+                   residual: Optional[torch.Tensor] = None,
+                   residual_out: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+    """rms_norm_fwd with an 8-bit output: (codes float8_e4m3fn [rows, dim],
+    scales float32 [rows, dim / group_size]).  group_size 32, 64, 128 or 256
+    channels share a scale; 0: a whole row does ([rows, 1])."""
+    if x.dim() != 2:
+        raise ValueError("x [rows, dim]")
+    rows, dim = x.shape
+    if group_size < 0 or (group_size and dim % group_size):
+        raise ValueError(f"group_size {group_size} does not divide dim {dim}")
+    n = dim // group_size if group_size else 1
+    if out is None:
+        out = torch.empty(rows, dim, dtype=torch.float8_e4m3fn, device=x.device)
+    if scales is None:
+        scales = torch.empty(rows, n, dtype=torch.float32, device=x.device)
+    if out.dtype != torch.float8_e4m3fn or scales.dtype != torch.float32:
+        raise TypeError("codes are float8_e4m3fn, scales float32")
+    if scales.shape != (rows, n) or (n > 1 and scales.stride(1) != 1):
+        raise ValueError("scales must be [rows, groups] with contiguous groups")
+    _norm(x, weight, eps, residual, residual_out, out, scales, int(group_size), _lib.E4M3)
+    return out, scales
+
+
+def rms_norm_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                 dresidual: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None):
+    """Gradients of rms_norm_fwd at the rows x that it normalised (its
+    residual_out, or its x): (dx, dweight float32 [dim]).  ``dresidual``, the
+    gradient that reaches residual_out from elsewhere, is added to dx, which
+    is then the gradient of x and of residual."""
+    if x.dim() != 2 or weight.dim() != 1:
+        raise ValueError("dout, x [rows, dim], weight [dim]")
+    rows, dim = x.shape
+    dx = torch.empty_like(x) if dx is None else dx
+    _one_device(x, dout, weight, dresidual, dx)
+    dt = _same_type(x, "dout, x, weight, dresidual and dx", dout, weight, dresidual, dx)
+    _vec(weight, x.dtype, "weight", dim)
+    a = _rows(x.shape, dout, x, dresidual, dx)
+    need = ctypes.c_int64()
+    _lib.check(_lib.load().rms_norm_bwd_workspace(rows, dim, ctypes.byref(need)),
+               "rms_norm_bwd_workspace")
+    dweight = torch.empty(dim, dtype=torch.float32, device=x.device)
+    ws = torch.empty(need.value, dtype=torch.float32, device=x.device)
+    _call("rms_norm_bwd", x, *a[:4], weight.data_ptr(), eps, *a[4:], dweight.data_ptr(),
+          ws.data_ptr(), ws.numel(), rows, dim, dt)
+    return dx, dweight

@@ -10,7 +10,8 @@
  * - Every buffer is a caller-owned DEVICE pointer (hipMalloc / torch).  The
  *   library allocates nothing, never synchronizes and never reads device data
  *   on the host: each call enqueues one kernel on `stream` (NULL = the null
- *   stream; sconv_fused_insert_conv_gather may enqueue two) and returns.
+ *   stream; sconv_fused_insert_conv_gather and the gradient entry points may
+ *   enqueue two) and returns.
  *   This makes every call capturable in a hipGraph; grids depend on host
  *   scalars only.
  * - Strides are in ELEMENTS.  Only host scalars are validated.  Properties of
@@ -40,7 +41,9 @@ enum {
   SCONV_ERR_HIP = 3          /* the HIP runtime reported a launch error   */
 };
 
-typedef enum { SCONV_F32 = 0, SCONV_BF16 = 1 } sconv_dtype_t;
+/* SCONV_E4M3 (8-bit float, 4 exponent and 3 mantissa bits, largest value 448)
+ * is an output type of rms_norm_fwd only. */
+typedef enum { SCONV_F32 = 0, SCONV_BF16 = 1, SCONV_E4M3 = 2 } sconv_dtype_t;
 typedef enum { SCONV_ACT_NONE = 0, SCONV_ACT_SILU = 1 } sconv_act_t;
 
 /* Message describing the last failed call on this thread ("" if none). */
@@ -531,6 +534,227 @@ int gather_intermediate_ssm_state(const void* states, int64_t num_chunks, int64_
                                   int64_t states_row_stride, const int64_t* chunk_indices,
                                   const int32_t* real_count_dev, int32_t max_count, void* out,
                                   int64_t out_row_stride, int32_t dtype, hipStream_t stream);
+
+/*
+ * Gated linear recurrence
+ * -----------------------
+ * The recurrent step of a layer whose mixer is the short conv followed by a
+ * diagonal recurrence.  Per channel c and token t of one sequence, with the
+ * gates given before their sigmoid:
+ *     r_t = sigmoid(gate_a[c, t]),  i_t = sigmoid(gate_x[c, t])
+ *     a_t = exp(-decay_scale * softplus(decay[c]) * r_t)
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x[c, t],   out[c, t] = h_t
+ * x, the gates and out share one element type; decay, the states, the
+ * checkpoints and every gradient of them are fp32, and so is the arithmetic.
+ * Packing, state slots, PAD and has_initial_state are those of
+ * causal_conv1d_varlen_fwd.  Planes are [dim, total_T] at any strides >= 0
+ * (out and gradients: no two elements in one place): tokens contiguous
+ * (channel-major) and channels contiguous (rows of tokens) with 16-byte
+ * aligned rows run with vector lanes.
+ *
+ * gated_linear_recurrence_checkpoint_rows -- rows of the checkpoint buffer
+ * that a forward call leaves for its backward call:
+ *     *rows = ceil(total_T / 128) + batch
+ * The buffer is fp32 [rows, dim], dense; row t / 128 + b holds sequence b's
+ * state before its first token at or after token 128 * (t / 128).  Rows that
+ * no sequence has are not written.  Host only; launches nothing.
+ */
+int gated_linear_recurrence_checkpoint_rows(int64_t total_T, int32_t batch, int64_t* rows);
+
+/*
+ * gated_linear_recurrence_varlen_fwd -- the recurrence over packed sequences.
+ *
+ *   x, gate_a, gate_x, out  [dim, total_T] strides (stride_c, stride_t); out
+ *            may be x itself, otherwise it overlaps neither x nor a gate
+ *   decay    fp32 [dim]; decay_scale > 0
+ *   states   fp32 [num_slots, dim], slot stride st_stride_slot, channels
+ *            contiguous (read where has_initial_state, then written with the
+ *            state after the sequence's last token); NULL: every sequence
+ *            starts at zero and its last state is dropped
+ *   query_start_loc, cache_indices, has_initial_state, pad_slot_id: as
+ *            causal_conv1d_varlen_fwd (a sequence of no tokens leaves its
+ *            initial state, or zeros, in its slot)
+ *   checkpoints  fp32 [checkpoint_rows, dim] for the backward call, or NULL
+ *
+ * Rows of out outside every sequence, or in a skipped one, are not written.
+ *
+ * Device-data contract: offsets non-decreasing within [0, total_T]; non-PAD
+ * slots distinct and in [0, num_slots).
+ *
+ * Host errors (SCONV_ERR_INVALID): negative sizes, decay_scale not positive
+ * and finite, NULL required pointer, unknown dtype, has_initial_state without
+ * states, too few slots or checkpoint rows, overlapping buffers.
+ * SCONV_ERR_UNSUPPORTED: batch * dim beyond one launch.
+ * batch == 0 or dim == 0 is a successful no-op.
+ */
+int gated_linear_recurrence_varlen_fwd(
+    const void* x, int64_t x_stride_c, int64_t x_stride_t, const void* gate_a,
+    int64_t ga_stride_c, int64_t ga_stride_t, const void* gate_x, int64_t gx_stride_c,
+    int64_t gx_stride_t, const float* decay, float decay_scale, float* states, int64_t num_slots,
+    int64_t st_stride_slot, const int32_t* query_start_loc, int32_t batch,
+    const int32_t* cache_indices, const uint8_t* has_initial_state, void* out,
+    int64_t out_stride_c, int64_t out_stride_t, float* checkpoints, int64_t checkpoint_rows,
+    int32_t dim, int64_t total_T, int32_t dtype, int32_t pad_slot_id, hipStream_t stream);
+
+/*
+ * gated_linear_recurrence_varlen_bwd -- its gradients.  With dh the gradient
+ * of a state (dh_t = dout_t + a_{t+1} dh_{t+1}, the last one plus the
+ * sequence's dfinal_states) and k = decay_scale * softplus(decay):
+ *     dx = dh sqrt(1 - a^2) i,         dgate_x = dx x (1 - i)
+ *     dlog a = dh a (h_{t-1} - a i x / sqrt(1 - a^2))
+ *     dgate_a = -k r (1 - r) dlog a
+ *     ddecay = -decay_scale sigmoid(decay) sum_t r dlog a
+ * Where 1 - a^2 is zero (a closed gate), the terms divided by it are zero,
+ * their limit.
+ *
+ *   dout, x, gate_a, gate_x  as the forward's; dx, dgate_a, dgate_x [dim,
+ *            total_T], which overlap nothing (written inside the sequences
+ *            that are not skipped, elsewhere left as they were)
+ *   checkpoints  as the forward call left them, for the same x, gates, decay,
+ *            offsets, indices and initial states
+ *   dfinal_states  fp32 [num_slots, dim] gradient of each sequence's last
+ *            state, by its slot, or NULL (zeros)
+ *   dinitial_states  fp32 [num_slots, dim], written with the gradient of each
+ *            sequence's initial state (zero without has_initial_state), or
+ *            NULL; may be dfinal_states itself
+ *   ddecay   fp32 [dim] (written)
+ *   workspace  fp32 [batch * dim], the call's own until it has finished;
+ *            workspace_floats says how many it holds
+ *
+ * The sums over tokens and sequences have a fixed order: equal inputs give
+ * equal bits.  Errors as the forward's, and too small a workspace.  dim == 0
+ * is a no-op; batch == 0 writes zeros to ddecay.
+ */
+int gated_linear_recurrence_varlen_bwd(
+    const void* dout, int64_t do_stride_c, int64_t do_stride_t, const void* x,
+    int64_t x_stride_c, int64_t x_stride_t, const void* gate_a, int64_t ga_stride_c,
+    int64_t ga_stride_t, const void* gate_x, int64_t gx_stride_c, int64_t gx_stride_t,
+    const float* decay, float decay_scale, const float* checkpoints, int64_t checkpoint_rows,
+    const int32_t* query_start_loc, int32_t batch, const int32_t* cache_indices,
+    const uint8_t* has_initial_state, int64_t num_slots, const float* dfinal_states,
+    int64_t df_stride_slot, float* dinitial_states, int64_t di_stride_slot, void* dx,
+    int64_t dx_stride_c, int64_t dx_stride_t, void* dgate_a, int64_t dga_stride_c,
+    int64_t dga_stride_t, void* dgate_x, int64_t dgx_stride_c, int64_t dgx_stride_t,
+    float* ddecay, float* workspace, int64_t workspace_floats, int32_t dim, int64_t total_T,
+    int32_t dtype, int32_t pad_slot_id, hipStream_t stream);
+
+/*
+ * gated_linear_recurrence_update -- one decode token per row against the
+ * state pool: x, gate_a, gate_x, out [batch, dim] rows of their strides,
+ * channels contiguous (out may be x itself); states fp32 [num_slots, dim]
+ * (read and written); state_indices int32 [batch] (NULL: the row's own
+ * number), a row whose slot equals pad_slot_id is skipped.
+ *
+ * Device-data contract: slots of non-PAD rows distinct and in [0, num_slots).
+ *
+ * Host errors as gated_linear_recurrence_varlen_fwd.
+ */
+int gated_linear_recurrence_update(
+    const void* x, int64_t x_stride_b, const void* gate_a, int64_t ga_stride_b,
+    const void* gate_x, int64_t gx_stride_b, const float* decay, float decay_scale,
+    float* states, int64_t num_slots, int64_t st_stride_slot, const int32_t* state_indices,
+    void* out, int64_t out_stride_b, int32_t batch, int32_t dim, int32_t dtype,
+    int32_t pad_slot_id, hipStream_t stream);
+
+/*
+ * causal_conv1d_varlen_bwd -- gradients of causal_conv1d_varlen_fwd.  With u
+ * a sequence's initial state (oldest first) followed by its inputs and
+ * z_t = bias + sum_k weight[k] u[t - (W-1) + k] (recomputed here):
+ *     dz_t = dout_t act'(z_t)
+ *     du[i] = sum_l weight[W-1-l] dz[i + l], plus dfinal_states for the last
+ *             W-1 entries of u; dx and dinitial_states are its two parts
+ *     dweight[k] = sum_t dz_t u[t - (W-1) + k],   dbias = sum_t dz_t
+ *
+ *   dout, x, dx   [dim, total_T] at any strides (dx overlaps neither)
+ *   weight [dim, W], bias [dim] or NULL: as the forward's
+ *   initial_states [num_slots, dim, W-1]: the state pool as it was BEFORE the
+ *            forward call (which overwrites it), read where
+ *            has_initial_state; NULL: every sequence started at zeros
+ *   dfinal_states  [num_slots, dim, W-1] gradient of the state that the
+ *            forward left in each sequence's slot, or NULL (zeros)
+ *   dinitial_states [num_slots, dim, W-1], written with the gradient of each
+ *            sequence's initial state (zeros without has_initial_state), or
+ *            NULL; overlaps nothing
+ *   dweight  fp32 [dim, W] dense, dbias fp32 [dim] or NULL (written)
+ *   workspace  fp32 [batch * dim * (W + 1)], the call's own until it has
+ *            finished; workspace_floats says how many it holds
+ *   the other arguments as causal_conv1d_varlen_fwd's
+ *
+ * Rows of dx outside every sequence, or in a skipped one, are not written.
+ * The sums have a fixed order: equal inputs give equal bits.
+ *
+ * Host errors (SCONV_ERR_INVALID): those of the forward, has_initial_state
+ * without initial_states, too small a workspace, an output that overlaps
+ * another buffer.  dim == 0 is a no-op; batch == 0 writes zeros to dweight
+ * and dbias.
+ */
+int causal_conv1d_varlen_bwd(
+    const void* dout, int64_t do_stride_c, int64_t do_stride_t, const void* x,
+    int64_t x_stride_c, int64_t x_stride_t, const void* weight, int64_t w_stride_c,
+    int64_t w_stride_k, const void* bias, const void* initial_states, int64_t is_stride_slot,
+    int64_t is_stride_c, int64_t is_stride_k, int64_t num_slots, const int32_t* query_start_loc,
+    int32_t batch, const int32_t* cache_indices, const uint8_t* has_initial_state,
+    const void* dfinal_states, int64_t df_stride_slot, int64_t df_stride_c, int64_t df_stride_k,
+    void* dinitial_states, int64_t di_stride_slot, int64_t di_stride_c, int64_t di_stride_k,
+    void* dx, int64_t dx_stride_c, int64_t dx_stride_t, float* dweight, float* dbias,
+    float* workspace, int64_t workspace_floats, int32_t dim, int64_t total_T, int32_t W,
+    int32_t dtype, int32_t activation, int32_t pad_slot_id, hipStream_t stream);
+
+/*
+ * rms_norm_fwd -- root-mean-square norm of rows, with the residual's addition
+ * and, if asked, an 8-bit output with scales:
+ *     s = x + residual (s = x without one; fp32, not rounded)
+ *     y = s / sqrt(mean(s^2) + eps) * weight
+ *   out_dtype == dtype:       out = y
+ *   out_dtype == SCONV_E4M3:  per group of group_size channels (0: the whole
+ *     row) scale = max(max |y| / 448, 2^-126), out = y / scale in e4m3, and
+ *     scales[row, group] = scale; y is not rounded before.  A NaN in a group
+ *     makes its scale and all its codes NaN.
+ *
+ *   x, residual, residual_out, out  [rows, dim] rows of their strides,
+ *            channels contiguous; weight [dim]; x, residual, weight and
+ *            residual_out share dtype.  residual may be NULL; residual_out
+ *            (needs residual; NULL: not kept) receives s rounded to dtype,
+ *            and may be residual or x itself; so may out
+ *   scales   fp32 [rows, dim / group_size] row stride scales_stride_r
+ *            (row groups: [rows, 1]); NULL unless 8 bits
+ *
+ * Host errors (SCONV_ERR_INVALID): negative sizes, eps negative or not
+ * finite, NULL required pointer, unknown types, group_size that does not
+ * divide dim or comes without an 8-bit output, partially overlapping buffers.
+ * SCONV_ERR_UNSUPPORTED: group_size none of 0, 32, 64, 128, 256; rows beyond
+ * one launch.  rows == 0 or dim == 0 is a successful no-op.
+ */
+int rms_norm_fwd(const void* x, int64_t x_stride_r, const void* residual,
+                 int64_t residual_stride_r, const void* weight, float eps, void* residual_out,
+                 int64_t residual_out_stride_r, void* out, int64_t out_stride_r, float* scales,
+                 int64_t scales_stride_r, int32_t group_size, int64_t rows, int32_t dim,
+                 int32_t dtype, int32_t out_dtype, hipStream_t stream);
+
+/* Floats of workspace that rms_norm_bwd needs.  Host only. */
+int rms_norm_bwd_workspace(int64_t rows, int32_t dim, int64_t* floats);
+
+/*
+ * rms_norm_bwd -- gradients of rms_norm_fwd (out in the input's type) at the
+ * rows x it normalised (the forward's residual_out, or its x without a
+ * residual).  With rstd = 1 / sqrt(mean(x^2) + eps) and n = x rstd:
+ *     dx = rstd (weight dout - n mean(weight dout n)) + dresidual
+ *     dweight = sum over rows of dout n
+ *   dresidual [rows, dim] or NULL: the gradient that reaches residual_out
+ *            from elsewhere; dx is then the gradient of x and of residual
+ *   dx       may be dout, x or dresidual itself
+ *   dweight  fp32 [dim] (written)
+ *   workspace  fp32, rms_norm_bwd_workspace floats, the call's own until it
+ *            has finished
+ * The sums have a fixed order: equal inputs give equal bits.  Errors as
+ * rms_norm_fwd's, and too small a workspace.  dim == 0 is a no-op; rows == 0
+ * writes zeros to dweight.
+ */
+int rms_norm_bwd(const void* dout, int64_t dout_stride_r, const void* x, int64_t x_stride_r,
+                 const void* weight, float eps, const void* dresidual,
+                 int64_t dresidual_stride_r, void* dx, int64_t dx_stride_r, float* dweight,
+                 float* workspace, int64_t workspace_floats, int64_t rows, int32_t dim,
+                 int32_t dtype, hipStream_t stream);
 
 #ifdef __cplusplus
 }
