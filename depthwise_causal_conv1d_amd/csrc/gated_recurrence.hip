@@ -4,6 +4,8 @@
 //
 // The recurrence is the layer step behind the short conv: it takes the
 // conv's packing (query_start_loc), state slots and layouts.
+#include <initializer_list>
+
 #include "recurrence_device.h"
 #include "sconv_host.h"
 
@@ -23,32 +25,222 @@ struct RecFwdParams {
   int32_t batch, dim, pad_slot_id;
 };
 
-// One thread per (sequence, channel), token by token.
-template <typename D>
-__global__ __launch_bounds__(64) void rec_fwd_simple(const RecFwdParams p) {
+// ---------------------------------------------------------------- tokens in lanes
+
+// A wave takes a chunk of 512 tokens of one channel, lane l the tokens
+// [8 l, 8 l + 8) of it, on the grid of absolute multiples of 512.  The
+// recurrence is a composition of maps h -> a h + u: a lane composes its
+// eight, the wave its lanes (six DPP steps), and NW waves that walk one
+// sequence together exchange their chunks' maps through LDS, so that no
+// state ever waits for another workgroup and every input is read once.
+// Tokens outside the sequence are the identity (a = 1, u = 0).
+template <typename D, bool VEC, int NW>
+__global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_fwd_kernel(const RecFwdParams p) {
   using S = typename D::storage;
-  const int64_t id = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (id >= p.num_pairs) return;
-  const int b = (int)(id / p.dim), c = (int)(id - (int64_t)b * p.dim);
+  constexpr int kWaves = NW > 4 ? NW : 4;
+  constexpr int kPairs = kWaves / NW;  // (sequence, channel) pairs of a workgroup
+  static_assert(kPairs == 1 || NW == 1, "a barrier is met by one pair only");
+  __shared__ float2 maps[2][kPairs][NW];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int sub = wave % NW, mine = wave / NW;
+  int64_t pair = (int64_t)xcd_contiguous(blockIdx.x, gridDim.x) * kPairs + mine;
+  if (pair >= p.num_pairs) return;  // NW waves of one pair leave together
+  const int b = (int)(pair / p.dim), c = (int)(pair - (int64_t)b * p.dim);
   const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
   if (slot == p.pad_slot_id) return;
-  const Decay d = make_decay(p.decay[c], p.scale);
-  const bool init = p.states && p.has_init && p.has_init[b] != 0;
-  float h = init ? p.states[slot * p.ss_slot + c] : 0.f;
   const int64_t start = p.qsl[b], end = p.qsl[b + 1];
-  const S* x = static_cast<const S*>(p.x) + c * p.x_sc;
+  const Decay d = make_decay(p.decay[c], p.scale);
+  float carry = p.has_init && p.has_init[b] != 0 ? p.states[slot * p.ss_slot + c] : 0.f;
+  const S* x = static_cast<const S*>(p.x) + c * p.x_sc;  // may be out
   const S* ga = static_cast<const S*>(p.ga) + c * p.ga_sc;
   const S* gx = static_cast<const S*>(p.gx) + c * p.gx_sc;
   S* out = static_cast<S*>(p.out) + c * p.o_sc;
-  for (int64_t t = start; t < end; ++t) {
-    if (p.marks && (t == start || t % kMarkTokens == 0))
+
+  Raw8<D> rx, ra, rg;
+  auto fetch = [&](int64_t base) {
+    const int64_t t = base + lane * kLaneTokens;
+    if (base < end) {
+      rx.template load<VEC>(x, p.x_st, t, p.total_T);
+      ra.template load<VEC>(ga, p.ga_st, t, p.total_T);
+      rg.template load<VEC>(gx, p.gx_st, t, p.total_T);
+    }
+  };
+  const int64_t first = start / kChunkTokens * kChunkTokens + sub * kChunkTokens;
+  if (end > start) fetch(first);
+  int turn = 0;
+  for (int64_t base = first; base - sub * kChunkTokens < end; base += NW * kChunkTokens, turn ^= 1) {
+    const int64_t t = base + lane * kLaneTokens;
+    float a[kLaneTokens], u[kLaneTokens];
+    float P = 1.f, H = 0.f;
+    const bool any = base < end;
+    if (any) {
+      float xf[kLaneTokens], gf[kLaneTokens];
+      rx.to_float(xf);
+      ra.to_float(a);
+      rg.to_float(gf);
+#pragma unroll
+      for (int e = 0; e < kLaneTokens; ++e) {
+        const Gates g = make_gates(a[e], gf[e], d);
+        a[e] = g.a;
+        u[e] = g.m * (g.i * xf[e]);
+      }
+      if (base < start || base + kChunkTokens > end) {
+#pragma unroll
+        for (int e = 0; e < kLaneTokens; ++e) {
+          const bool in = t + e >= start && t + e < end;
+          a[e] = in ? a[e] : 1.f;
+          u[e] = in ? u[e] : 0.f;
+        }
+      }
+      fetch(base + NW * kChunkTokens);
+#pragma unroll
+      for (int e = 0; e < kLaneTokens; ++e) {
+        H = __builtin_fmaf(a[e], H, u[e]);
+        P *= a[e];
+      }
+      scan_wave_up(P, H);
+    }
+    float h = carry;
+    if constexpr (NW == 1) {
+      carry = __builtin_fmaf(last_lane(P), carry, last_lane(H));
+    } else {
+      if (lane == 63) maps[turn][mine][sub] = make_float2(P, H);
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < NW; ++q) {
+        const float2 f = maps[turn][mine][q];
+        if (q == sub) h = carry;
+        carry = __builtin_fmaf(f.x, carry, f.y);
+      }
+    }
+    if (!any) continue;
+    h = __builtin_fmaf(lane_move<0x138>(1.0f, P), h, lane_move<0x138>(0.0f, H));
+    if (p.marks && lane % (kMarkTokens / kLaneTokens) == 0 && t + kMarkTokens > start && t < end)
       p.marks[(t / kMarkTokens + b) * p.dim + c] = h;
-    const Gates g = make_gates(load_as_float<D>(ga + t * p.ga_st), load_as_float<D>(gx + t * p.gx_st), d);
-    h = __builtin_fmaf(g.a, h, g.m * (g.i * load_as_float<D>(x + t * p.x_st)));
-    out[t * p.o_st] = round_to<D>(h);
+#pragma unroll
+    for (int e = 0; e < kLaneTokens; ++e) {
+      h = __builtin_fmaf(a[e], h, u[e]);
+      u[e] = h;
+    }
+    Raw8<D> o;
+    o.from_float(u);
+    o.template store<VEC>(out, p.o_st, t, start, end);
   }
-  if (p.states) p.states[slot * p.ss_slot + c] = h;
+  if (p.states && sub == 0 && lane == 0) p.states[slot * p.ss_slot + c] = carry;
 }
+
+// ---------------------------------------------------------------- channels in lanes
+
+// For channels that lie side by side (rows of tokens): lane l takes V
+// channels, wave w of a workgroup the rows [R w, R w + R) of each tile of
+// NW * R tokens, and the tile's maps meet in LDS as above.
+constexpr int kRowWaves = 8, kRowTokens = 8;
+
+template <typename D, int V>
+__global__ __launch_bounds__(kRowWaves * 64) void rec_fwd_rows_kernel(const RecFwdParams p) {
+  using S = typename D::storage;
+  using P_ = Pack<D, V>;
+  constexpr int R = kRowTokens, NW = kRowWaves, kTile = R * NW;
+  struct alignas(8 * V) Map { float P[V], H[V]; };
+  __shared__ Map maps[2][NW][64];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
+  const uint32_t wg = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int b = (int)(wg / slabs), slab = (int)(wg % slabs);
+  const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
+  if (slot == p.pad_slot_id) return;
+  const int64_t start = p.qsl[b], end = p.qsl[b + 1];
+  // lanes past the last channel read it and write nothing
+  const int ch = (slab * 64 + lane) * V;
+  const bool live = ch < p.dim;
+  const int c = live ? ch : p.dim - V;
+  const S* x = static_cast<const S*>(p.x) + c;  // may be out
+  const S* ga = static_cast<const S*>(p.ga) + c;
+  const S* gx = static_cast<const S*>(p.gx) + c;
+  S* out = static_cast<S*>(p.out) + c;
+  Decay d[V];
+  float carry[V];
+  const bool init = p.has_init && p.has_init[b] != 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    d[v] = make_decay(p.decay[c + v], p.scale);
+    carry[v] = init ? p.states[slot * p.ss_slot + c + v] : 0.f;
+  }
+  P_ rx[R], ra[R], rg[R];
+  auto fetch = [&](int64_t row0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      // outside the sequence: the nearest row inside it, unused
+      int64_t row = row0 + r < start ? start : row0 + r;
+      row = row < end ? row : end - 1;
+      rx[r].load_nt(x + row * p.x_st);
+      ra[r].load_nt(ga + row * p.ga_st);
+      rg[r].load_nt(gx + row * p.gx_st);
+    }
+  };
+  int64_t base = start / kTile * kTile;
+  if (end > start) fetch(base + wave * R);
+  for (int turn = 0; base < end; base += kTile, turn ^= 1) {
+    const int64_t row0 = base + wave * R;
+    float pl[R][V], hl[R][V];
+    Map m;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      m.P[v] = 1.f;
+      m.H[v] = 0.f;
+    }
+    const bool whole = row0 >= start && row0 + R <= end;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float xf[V], af[V], gf[V];
+      rx[r].to_float(xf);
+      ra[r].to_float(af);
+      rg[r].to_float(gf);
+      const bool in = whole || (row0 + r >= start && row0 + r < end);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Gates g = make_gates(af[v], gf[v], d[v]);
+        const float a = in ? g.a : 1.f, u = in ? g.m * (g.i * xf[v]) : 0.f;
+        m.H[v] = __builtin_fmaf(a, m.H[v], u);
+        m.P[v] *= a;
+        pl[r][v] = m.P[v];
+        hl[r][v] = m.H[v];
+      }
+    }
+    if (base + kTile < end) fetch(row0 + kTile);
+    maps[turn][wave][lane] = m;
+    if (p.marks && wave == 0 && live && base % kMarkTokens == 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.marks[(base / kMarkTokens + b) * p.dim + c + v] = carry[v];
+    }
+    __syncthreads();
+    float h[V];
+#pragma unroll
+    for (int q = 0; q < NW; ++q) {
+      const Map f = maps[turn][q][lane];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (q == wave) h[v] = carry[v];
+        carry[v] = __builtin_fmaf(f.P[v], carry[v], f.H[v]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float y[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) y[v] = __builtin_fmaf(pl[r][v], h[v], hl[r][v]);
+      P_ o;
+      o.from_float(y);
+      if (live && row0 + r >= start && row0 + r < end) o.store_nt(out + (row0 + r) * p.o_st);
+    }
+  }
+  if (p.states && wave == 0 && live) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.states[slot * p.ss_slot + c + v] = carry[v];
+  }
+}
+
+// ---------------------------------------------------------------- gradients
 
 struct RecBwdParams {
   const void *dout, *x, *ga, *gx;
@@ -67,21 +259,31 @@ struct RecBwdParams {
   int32_t batch, dim, pad_slot_id;
 };
 
-// One thread per (sequence, channel): block by block of 128 tokens from the
-// end, the states of a block from its checkpoint, then its gradients.
-template <typename D>
-__global__ __launch_bounds__(64) void rec_bwd_simple(const RecBwdParams p) {
+// Tokens in lanes, from the end of the sequence: lane l of a chunk takes
+// tokens [8 (63 - l), 8 (63 - l) + 8), so that the gradient of the state,
+// which runs against time, runs up the lanes.  The states come from the
+// checkpoints: each row of 16 lanes (128 tokens) starts from its own, and
+// only composes inside the row.  The gates are computed once per token.
+template <typename D, bool VEC, int NW>
+__global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_bwd_kernel(const RecBwdParams p) {
   using S = typename D::storage;
-  const int64_t id = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (id >= p.num_pairs) return;
-  const int b = (int)(id / p.dim), c = (int)(id - (int64_t)b * p.dim);
+  constexpr int kWaves = NW > 4 ? NW : 4;
+  constexpr int kPairs = kWaves / NW;
+  static_assert(kPairs == 1 || NW == 1, "a barrier is met by one pair only");
+  __shared__ float2 maps[2][kPairs][NW];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int sub = wave % NW, mine = wave / NW;
+  const int64_t pair = (int64_t)xcd_contiguous(blockIdx.x, gridDim.x) * kPairs + mine;
+  if (pair >= p.num_pairs) return;
+  const int b = (int)(pair / p.dim), c = (int)(pair - (int64_t)b * p.dim);
   const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
   if (slot == p.pad_slot_id) {
-    p.partial[id] = 0.f;
+    if (sub == 0 && lane == 0) p.partial[pair] = 0.f;
     return;
   }
-  const Decay d = make_decay(p.decay[c], p.scale);
   const int64_t start = p.qsl[b], end = p.qsl[b + 1];
+  const Decay d = make_decay(p.decay[c], p.scale);
+  float carry = p.dfinal ? p.dfinal[slot * p.df_slot + c] : 0.f;  // a_{t+1} dh_{t+1}
   const S* dout = static_cast<const S*>(p.dout) + c * p.do_sc;
   const S* x = static_cast<const S*>(p.x) + c * p.x_sc;
   const S* ga = static_cast<const S*>(p.ga) + c * p.ga_sc;
@@ -89,34 +291,294 @@ __global__ __launch_bounds__(64) void rec_bwd_simple(const RecBwdParams p) {
   S* dx = static_cast<S*>(p.dx) + c * p.dx_sc;
   S* dga = static_cast<S*>(p.dga) + c * p.dga_sc;
   S* dgx = static_cast<S*>(p.dgx) + c * p.dgx_sc;
-  float s = p.dfinal ? p.dfinal[slot * p.df_slot + c] : 0.f;  // a_{t+1} dh_{t+1}
-  float acc = 0.f;
-  float before[kMarkTokens];
-  for (int64_t blk = (end - 1) / kMarkTokens; end > start && blk >= start / kMarkTokens; --blk) {
-    const int64_t lo = blk * kMarkTokens > start ? blk * kMarkTokens : start;
-    const int64_t hi = (blk + 1) * kMarkTokens < end ? (blk + 1) * kMarkTokens : end;
-    float h = p.marks[(blk + b) * p.dim + c];
-    for (int64_t t = lo; t < hi; ++t) {
-      before[t - lo] = h;
-      const Gates g = make_gates(load_as_float<D>(ga + t * p.ga_st), load_as_float<D>(gx + t * p.gx_st), d);
-      h = __builtin_fmaf(g.a, h, g.m * (g.i * load_as_float<D>(x + t * p.x_st)));
+  const int64_t first_mark = start / kMarkTokens;
+
+  Raw8<D> rd, rx, ra, rg;
+  float mark = 0.f;
+  const int back = (63 - lane) * kLaneTokens;
+  auto fetch = [&](int64_t base) {
+    const int64_t t = base + back;
+    if (base >= 0 && base + kChunkTokens > start) {
+      rd.template load<VEC>(dout, p.do_st, t, p.total_T);
+      rx.template load<VEC>(x, p.x_st, t, p.total_T);
+      ra.template load<VEC>(ga, p.ga_st, t, p.total_T);
+      rg.template load<VEC>(gx, p.gx_st, t, p.total_T);
+      // the row's first 64-token block that the sequence reaches
+      int64_t blk = t / 128 * (128 / kMarkTokens);
+      blk = blk < first_mark ? first_mark : blk;
+      const bool reached = t / 128 * 128 + 128 > start && blk * kMarkTokens < end;
+      mark = reached ? p.marks[(blk + b) * p.dim + c] : 0.f;
     }
-    for (int64_t t = hi - 1; t >= lo; --t) {
-      const GatesInv g = make_gates_inv(load_as_float<D>(ga + t * p.ga_st), load_as_float<D>(gx + t * p.gx_st), d);
-      const float xv = load_as_float<D>(x + t * p.x_st);
-      const float dh = s + load_as_float<D>(dout + t * p.do_st);
-      s = g.a * dh;
-      const float vx = dh * (g.m * g.i);
-      const float dlog = s * (before[t - lo] - g.a * g.inv_m * (g.i * xv));
-      acc = __builtin_fmaf(dlog, g.r, acc);
-      dx[t * p.dx_st] = round_to<D>(vx);
-      dgx[t * p.dgx_st] = round_to<D>(vx * xv * (1.f - g.i));
-      dga[t * p.dga_st] = round_to<D>(-d.k * dlog * (g.r * (1.f - g.r)));
+  };
+  float acc = 0.f;
+  const int64_t top = (end - 1) / kChunkTokens * kChunkTokens;  // the last chunk
+  if (end > start) fetch(top - sub * kChunkTokens);
+  int turn = 0;
+  for (int64_t high = top; end > start && high + kChunkTokens > start;
+       high -= NW * kChunkTokens, turn ^= 1) {
+    const int64_t base = high - sub * kChunkTokens, t = base + back;
+    const bool any = base >= 0 && base + kChunkTokens > start;
+    float g[kLaneTokens], xf[kLaneTokens], a[kLaneTokens], r[kLaneTokens], i[kLaneTokens];
+    float m[kLaneTokens], over[kLaneTokens];  // over: a i x / m
+    float P = 1.f, H = 0.f, T = 0.f;
+    if (any) {
+      rd.to_float(g);
+      rx.to_float(xf);
+      ra.to_float(r);
+      rg.to_float(i);
+      const float h0 = mark;
+      if (base < start || base + kChunkTokens > end) {
+#pragma unroll
+        for (int e = 0; e < kLaneTokens; ++e) {
+          const bool in = t + e >= start && t + e < end;
+          g[e] = in ? g[e] : 0.f;
+          xf[e] = in ? xf[e] : 0.f;
+          r[e] = in ? r[e] : -INFINITY;  // r = 0: a = 1, u = 0, no part in a sum
+          i[e] = in ? i[e] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kLaneTokens; ++e) {
+        const GatesInv q = make_gates_inv(r[e], i[e], d);
+        const float ix = q.i * xf[e];
+        r[e] = q.r;
+        i[e] = q.i;
+        a[e] = q.a;
+        m[e] = q.m;
+        over[e] = q.a * q.inv_m * ix;
+        H = __builtin_fmaf(q.a, H, q.m * ix);
+        P *= q.a;
+      }
+      fetch(base - NW * kChunkTokens);
+      // states before each token, less a i x / m
+      float A = P;
+      scan_row_down(P, H);
+      float h = __builtin_fmaf(lane_move<0x101>(1.0f, P), h0, lane_move<0x101>(0.0f, H));
+#pragma unroll
+      for (int e = 0; e < kLaneTokens; ++e) {
+        const float next = __builtin_fmaf(a[e], h, m[e] * (i[e] * xf[e]));
+        over[e] = h - over[e];
+        h = next;
+      }
+      // s -> a (dout + s), from the last token to the first
+#pragma unroll
+      for (int e = kLaneTokens - 1; e >= 0; --e) T = a[e] * (T + g[e]);
+      P = A;
+      scan_wave_up(P, T);
+    }
+    float s = carry;
+    if constexpr (NW == 1) {
+      carry = __builtin_fmaf(last_lane(P), carry, last_lane(T));
+    } else {
+      if (lane == 63) maps[turn][mine][sub] = make_float2(P, T);
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < NW; ++q) {
+        const float2 f = maps[turn][mine][q];
+        if (q == sub) s = carry;
+        carry = __builtin_fmaf(f.x, carry, f.y);
+      }
+    }
+    if (!any) continue;
+    s = __builtin_fmaf(lane_move<0x138>(1.0f, P), s, lane_move<0x138>(0.0f, T));
+#pragma unroll
+    for (int e = kLaneTokens - 1; e >= 0; --e) {
+      const float dh = g[e] + s;
+      s = a[e] * dh;
+      const float vx = dh * (m[e] * i[e]);
+      const float dlog = s * over[e];
+      acc = __builtin_fmaf(dlog, r[e], acc);
+      g[e] = vx;
+      i[e] = vx * xf[e] * (1.f - i[e]);
+      r[e] = -d.k * dlog * (r[e] * (1.f - r[e]));
+    }
+    Raw8<D> o;
+    o.from_float(g);
+    o.template store<VEC>(dx, p.dx_st, t, start, end);
+    o.from_float(i);
+    o.template store<VEC>(dgx, p.dgx_st, t, start, end);
+    o.from_float(r);
+    o.template store<VEC>(dga, p.dga_st, t, start, end);
+  }
+#pragma unroll
+  for (int w = 32; w > 0; w >>= 1) acc += __shfl_xor(acc, w, 64);
+  if constexpr (NW > 1) {
+    __syncthreads();  // the last tile's maps have been read
+    if (lane == 0) maps[0][0][sub].x = acc;
+    __syncthreads();
+    acc = 0.f;
+#pragma unroll
+    for (int q = 0; q < NW; ++q) acc += maps[0][0][q].x;
+  }
+  if (sub == 0 && lane == 0) {
+    p.partial[pair] = acc;
+    const bool init = p.has_init && p.has_init[b] != 0;
+    if (p.dinitial) p.dinitial[slot * p.di_slot + c] = init ? carry : 0.f;
+  }
+}
+
+// Channels in lanes, from the end: wave w takes the rows of a tile of 64
+// tokens (one checkpoint) that are w * R from its end.  The forward maps and
+// the backward ones, which share their factor, meet in LDS together.
+constexpr int kRowBwdWaves = 16, kRowBwdTokens = 4;
+
+template <typename D, int V>
+__global__ __launch_bounds__(kRowBwdWaves * 64) void rec_bwd_rows_kernel(const RecBwdParams p) {
+  using S = typename D::storage;
+  using P_ = Pack<D, V>;
+  constexpr int R = kRowBwdTokens, NW = kRowBwdWaves, kTile = R * NW;
+  static_assert(kTile == kMarkTokens, "a tile starts at a checkpoint");
+  __shared__ float mp[2][NW][V][64], mh[2][NW][V][64], mt[2][NW][V][64];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
+  const uint32_t wg = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int b = (int)(wg / slabs), slab = (int)(wg % slabs);
+  const int ch = (slab * 64 + lane) * V;
+  const bool live = ch < p.dim;
+  const int c = live ? ch : p.dim - V;
+  const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
+  if (slot == p.pad_slot_id) {
+    if (wave == 0 && live) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.partial[(int64_t)b * p.dim + c + v] = 0.f;
+    }
+    return;
+  }
+  const int64_t start = p.qsl[b], end = p.qsl[b + 1];
+  const S* dout = static_cast<const S*>(p.dout) + c;
+  const S* x = static_cast<const S*>(p.x) + c;
+  const S* ga = static_cast<const S*>(p.ga) + c;
+  const S* gx = static_cast<const S*>(p.gx) + c;
+  S* dx = static_cast<S*>(p.dx) + c;
+  S* dga = static_cast<S*>(p.dga) + c;
+  S* dgx = static_cast<S*>(p.dgx) + c;
+  Decay d[V];
+  float carry[V], acc[V], mark[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    d[v] = make_decay(p.decay[c + v], p.scale);
+    carry[v] = p.dfinal ? p.dfinal[slot * p.df_slot + c + v] : 0.f;
+    acc[v] = mark[v] = 0.f;
+  }
+  P_ rd[R], rx[R], ra[R], rg[R];
+  auto fetch = [&](int64_t base) {
+    const int64_t row0 = base + (NW - 1 - wave) * R;
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      int64_t row = row0 + q < start ? start : row0 + q;
+      row = row < end ? row : end - 1;
+      rd[q].load_nt(dout + row * p.do_st);
+      rx[q].load_nt(x + row * p.x_st);
+      ra[q].load_nt(ga + row * p.ga_st);
+      rg[q].load_nt(gx + row * p.gx_st);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) mark[v] = p.marks[(base / kMarkTokens + b) * p.dim + c + v];
+  };
+  int64_t base = (end - 1) / kTile * kTile;
+  if (end > start) fetch(base);
+  for (int turn = 0; end > start && base + kTile > start; base -= kTile, turn ^= 1) {
+    const int64_t row0 = base + (NW - 1 - wave) * R;
+    const bool whole = row0 >= start && row0 + R <= end;
+    float g[R][V], xf[R][V], a[R][V], r[R][V], i[R][V], m[R][V], over[R][V];
+    float P[V], H[V], T[V], h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      P[v] = 1.f;
+      H[v] = T[v] = 0.f;
+      h[v] = mark[v];
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      rd[q].to_float(g[q]);
+      rx[q].to_float(xf[q]);
+      ra[q].to_float(r[q]);
+      rg[q].to_float(i[q]);
+      const bool in = whole || (row0 + q >= start && row0 + q < end);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        g[q][v] = in ? g[q][v] : 0.f;
+        xf[q][v] = in ? xf[q][v] : 0.f;
+        r[q][v] = in ? r[q][v] : -INFINITY;  // r = 0: a = 1, u = 0, no part in a sum
+        i[q][v] = in ? i[q][v] : 0.f;
+        const GatesInv f = make_gates_inv(r[q][v], i[q][v], d[v]);
+        const float ix = f.i * xf[q][v];
+        r[q][v] = f.r;
+        i[q][v] = f.i;
+        a[q][v] = f.a;
+        m[q][v] = f.m;
+        over[q][v] = f.a * f.inv_m * ix;
+        H[v] = __builtin_fmaf(f.a, H[v], f.m * ix);
+        P[v] *= f.a;
+      }
+    }
+    if (base > start) fetch(base - kTile);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int q = R - 1; q >= 0; --q) T[v] = a[q][v] * (T[v] + g[q][v]);
+      mp[turn][wave][v][lane] = P[v];
+      mh[turn][wave][v][lane] = H[v];
+      mt[turn][wave][v][lane] = T[v];
+    }
+    __syncthreads();
+    float s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int q = 0; q < NW; ++q) {
+        if (q == wave) s[v] = carry[v];
+        carry[v] = __builtin_fmaf(mp[turn][q][v][lane], carry[v], mt[turn][q][v][lane]);
+      }
+      for (int q = NW - 1; q > wave; --q)  // the rows before this wave's
+        h[v] = __builtin_fmaf(mp[turn][q][v][lane], h[v], mh[turn][q][v][lane]);
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const float next = __builtin_fmaf(a[q][v], h[v], m[q][v] * (i[q][v] * xf[q][v]));
+        over[q][v] = h[v] - over[q][v];
+        h[v] = next;
+      }
+    }
+#pragma unroll
+    for (int q = R - 1; q >= 0; --q) {
+      float ox[V], oa[V], og[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float dh = g[q][v] + s[v];
+        s[v] = a[q][v] * dh;
+        ox[v] = dh * (m[q][v] * i[q][v]);
+        const float dlog = s[v] * over[q][v];
+        acc[v] = __builtin_fmaf(dlog, r[q][v], acc[v]);
+        og[v] = ox[v] * xf[q][v] * (1.f - i[q][v]);
+        oa[v] = -d[v].k * dlog * (r[q][v] * (1.f - r[q][v]));
+      }
+      if (live && row0 + q >= start && row0 + q < end) {
+        const int64_t row = row0 + q;
+        P_ o;
+        o.from_float(ox);
+        o.store_nt(dx + row * p.dx_st);
+        o.from_float(og);
+        o.store_nt(dgx + row * p.dgx_st);
+        o.from_float(oa);
+        o.store_nt(dga + row * p.dga_st);
+      }
     }
   }
-  p.partial[id] = acc;
+  // ddecay's sum over the waves, in their order
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) mp[0][wave][v][lane] = acc[v];
+  __syncthreads();
+  if (wave != 0 || !live) return;
   const bool init = p.has_init && p.has_init[b] != 0;
-  if (p.dinitial) p.dinitial[slot * p.di_slot + c] = init ? s : 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < NW; ++q) sum += mp[0][q][v][lane];
+    p.partial[(int64_t)b * p.dim + c + v] = sum;
+    if (p.dinitial) p.dinitial[slot * p.di_slot + c + v] = init ? carry[v] : 0.f;
+  }
 }
 
 // ddecay[c] = -scale sigmoid(decay[c]) * the sequences' sums, in their order.
@@ -125,9 +587,9 @@ __global__ __launch_bounds__(64) void rec_ddecay_kernel(const float* partial, co
                                                         float scale) {
   const int c = blockIdx.x * 64 + threadIdx.x;
   if (c >= dim) return;
-  float acc = 0.f;
-  for (int b = 0; b < batch; ++b) acc += partial[(int64_t)b * dim + c];
-  ddecay[c] = -scale * sigmoid(decay[c]) * acc;
+  double acc = 0.0;
+  for (int b = 0; b < batch; ++b) acc += (double)partial[(int64_t)b * dim + c];
+  ddecay[c] = -scale * sigmoid(decay[c]) * (float)acc;
 }
 
 struct RecUpdParams {
@@ -159,6 +621,24 @@ __global__ __launch_bounds__(64) void rec_update_kernel(const RecUpdParams p) {
   static_cast<S*>(p.out)[b * p.o_rs + c] = round_to<D>(h);
 }
 
+template <typename D, bool VEC>
+static void launch_fwd(int nw, const RecFwdParams& p, uint32_t grid, hipStream_t s) {
+  switch (nw) {
+    case 1: hipLaunchKernelGGL((rec_fwd_kernel<D, VEC, 1>), dim3(grid), dim3(256), 0, s, p); break;
+    case 4: hipLaunchKernelGGL((rec_fwd_kernel<D, VEC, 4>), dim3(grid), dim3(256), 0, s, p); break;
+    default: hipLaunchKernelGGL((rec_fwd_kernel<D, VEC, 16>), dim3(grid), dim3(1024), 0, s, p); break;
+  }
+}
+
+template <typename D, bool VEC>
+static void launch_bwd(int nw, const RecBwdParams& p, uint32_t grid, hipStream_t s) {
+  switch (nw) {
+    case 1: hipLaunchKernelGGL((rec_bwd_kernel<D, VEC, 1>), dim3(grid), dim3(256), 0, s, p); break;
+    case 4: hipLaunchKernelGGL((rec_bwd_kernel<D, VEC, 4>), dim3(grid), dim3(256), 0, s, p); break;
+    default: hipLaunchKernelGGL((rec_bwd_kernel<D, VEC, 16>), dim3(grid), dim3(1024), 0, s, p); break;
+  }
+}
+
 // ---------------------------------------------------------------- host
 
 // Checks shared by the two packed entry points; `fn` names the caller.
@@ -170,6 +650,36 @@ static int rec_check(const char* fn, int32_t batch, int32_t dim, int64_t total_T
   if (!(scale > 0.f) || !(scale <= 3.0e38f))
     return fail(SCONV_ERR_INVALID, "%s: decay_scale must be positive and finite", fn);
   return SCONV_OK;
+}
+
+// Whether a packed call runs with channels in lanes (every plane has its
+// channels side by side).
+static bool side_by_side(std::initializer_list<Plane> planes) {
+  for (const Plane& a : planes)
+    if (a.sc != 1) return false;
+  return true;
+}
+
+// Vector lanes of V channels: every row starts on a multiple of V elements.
+static bool row_lanes(std::initializer_list<Plane> planes, int64_t V) {
+  for (const Plane& a : planes)
+    if (a.nc % V != 0 || a.st % V != 0 || !aligned_to(a.p, V * a.es)) return false;
+  return true;
+}
+
+// Vector lanes of eight tokens: tokens side by side, rows 16-byte aligned.
+static bool token_lanes(std::initializer_list<Plane> planes) {
+  for (const Plane& a : planes)
+    if (a.st != 1 || (a.sc * a.es) % 16 != 0 || !aligned16(a.p)) return false;
+  return true;
+}
+
+// Waves that walk one sequence together.
+static int waves_per_pair(int64_t pairs, int64_t total_T, int32_t batch) {
+  const int64_t mean = total_T / batch;
+  if (pairs < 512 && mean >= 8 * kChunkTokens) return 16;
+  if (pairs < 8192 && mean >= 2 * kChunkTokens) return 4;
+  return 1;
 }
 
 static int64_t mark_rows(int64_t total_T, int32_t batch) {
@@ -241,12 +751,34 @@ extern "C" int gated_linear_recurrence_varlen_fwd(
   p.gx_st = pg.st; p.o_sc = po.sc; p.o_st = po.st; p.ss_slot = st_stride_slot;
   p.total_T = total_T; p.num_pairs = (int64_t)batch * dim; p.scale = decay_scale;
   p.batch = batch; p.dim = dim; p.pad_slot_id = pad_slot_id;
-  const int64_t grid = cdiv(p.num_pairs, 64);
-  if (!valid_grid(grid, 64)) return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
-  if (dtype == SCONV_BF16)
-    hipLaunchKernelGGL(rec_fwd_simple<Bf16>, dim3((uint32_t)grid), dim3(64), 0, stream, p);
-  else
-    hipLaunchKernelGGL(rec_fwd_simple<F32>, dim3((uint32_t)grid), dim3(64), 0, stream, p);
+  const auto planes = {px, pa, pg, po};
+  if (side_by_side(planes) && dim > 1) {
+    const bool two = row_lanes(planes, 2);
+    const int64_t grid = batch * cdiv(dim, two ? 128 : 64);
+    if (!valid_grid(grid, kRowWaves * 64))
+      return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
+    const dim3 g((uint32_t)grid), th(kRowWaves * 64);
+    if (dtype == SCONV_BF16) {
+      if (two) hipLaunchKernelGGL((rec_fwd_rows_kernel<Bf16, 2>), g, th, 0, stream, p);
+      else hipLaunchKernelGGL((rec_fwd_rows_kernel<Bf16, 1>), g, th, 0, stream, p);
+    } else {
+      if (two) hipLaunchKernelGGL((rec_fwd_rows_kernel<F32, 2>), g, th, 0, stream, p);
+      else hipLaunchKernelGGL((rec_fwd_rows_kernel<F32, 1>), g, th, 0, stream, p);
+    }
+    return check_launch(fn);
+  }
+  const bool vec = token_lanes(planes);
+  const int nw = waves_per_pair(p.num_pairs, total_T, batch);
+  const int64_t grid = nw == 1 ? cdiv(p.num_pairs, 4) : p.num_pairs;
+  if (!valid_grid(grid, nw > 4 ? nw * 64 : 256))
+    return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
+  if (dtype == SCONV_BF16) {
+    if (vec) launch_fwd<Bf16, true>(nw, p, (uint32_t)grid, stream);
+    else launch_fwd<Bf16, false>(nw, p, (uint32_t)grid, stream);
+  } else {
+    if (vec) launch_fwd<F32, true>(nw, p, (uint32_t)grid, stream);
+    else launch_fwd<F32, false>(nw, p, (uint32_t)grid, stream);
+  }
   return check_launch(fn);
 }
 
@@ -337,14 +869,34 @@ extern "C" int gated_linear_recurrence_varlen_bwd(
   p.dgx_sc = ou[2].sc; p.dgx_st = ou[2].st; p.df_slot = df_stride_slot;
   p.di_slot = di_stride_slot; p.total_T = total_T; p.num_pairs = (int64_t)batch * dim;
   p.scale = decay_scale; p.batch = batch; p.dim = dim; p.pad_slot_id = pad_slot_id;
-  const int64_t grid = cdiv(p.num_pairs, 64);
-  if (batch > 0 && !valid_grid(grid, 64))
-    return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
-  if (batch > 0) {
-    if (dtype == SCONV_BF16)
-      hipLaunchKernelGGL(rec_bwd_simple<Bf16>, dim3((uint32_t)grid), dim3(64), 0, stream, p);
-    else
-      hipLaunchKernelGGL(rec_bwd_simple<F32>, dim3((uint32_t)grid), dim3(64), 0, stream, p);
+  const auto planes = {in[0], in[1], in[2], in[3], ou[0], ou[1], ou[2]};
+  if (batch > 0 && side_by_side(planes) && dim > 1) {
+    const bool two = row_lanes(planes, 2);
+    const int64_t grid = batch * cdiv(dim, two ? 128 : 64);
+    if (!valid_grid(grid, kRowBwdWaves * 64))
+      return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
+    const dim3 g((uint32_t)grid), th(kRowBwdWaves * 64);
+    if (dtype == SCONV_BF16) {
+      if (two) hipLaunchKernelGGL((rec_bwd_rows_kernel<Bf16, 2>), g, th, 0, stream, p);
+      else hipLaunchKernelGGL((rec_bwd_rows_kernel<Bf16, 1>), g, th, 0, stream, p);
+    } else {
+      if (two) hipLaunchKernelGGL((rec_bwd_rows_kernel<F32, 2>), g, th, 0, stream, p);
+      else hipLaunchKernelGGL((rec_bwd_rows_kernel<F32, 1>), g, th, 0, stream, p);
+    }
+    if (const int rc = check_launch(fn)) return rc;
+  } else if (batch > 0) {
+    const bool vec = token_lanes(planes);
+    const int nw = waves_per_pair(p.num_pairs, total_T, batch);
+    const int64_t grid = nw == 1 ? cdiv(p.num_pairs, 4) : p.num_pairs;
+    if (!valid_grid(grid, nw > 4 ? nw * 64 : 256))
+      return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
+    if (dtype == SCONV_BF16) {
+      if (vec) launch_bwd<Bf16, true>(nw, p, (uint32_t)grid, stream);
+      else launch_bwd<Bf16, false>(nw, p, (uint32_t)grid, stream);
+    } else {
+      if (vec) launch_bwd<F32, true>(nw, p, (uint32_t)grid, stream);
+      else launch_bwd<F32, false>(nw, p, (uint32_t)grid, stream);
+    }
     if (const int rc = check_launch(fn)) return rc;
   }
   hipLaunchKernelGGL(rec_ddecay_kernel, dim3((uint32_t)cdiv(dim, 64)), dim3(64), 0, stream,

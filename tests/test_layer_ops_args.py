@@ -89,7 +89,7 @@ def test_recurrence_backward_refusals(lib, kw, text):
 def test_recurrence_checkpoint_rows(lib):
     n = ctypes.c_int64()
     f = lib.gated_linear_recurrence_checkpoint_rows
-    for T, b, want in ((0, 0, 0), (0, 3, 3), (1, 1, 2), (128, 1, 2), (129, 2, 4)):
+    for T, b, want in ((0, 0, 0), (0, 3, 3), (1, 1, 2), (64, 1, 2), (65, 2, 4)):
         assert f(T, b, ctypes.byref(n)) == 0 and n.value == want
     assert f(-1, 1, ctypes.byref(n)) == 1 and f(1, -1, ctypes.byref(n)) == 1 and f(1, 1, None) == 1
 
