@@ -7,7 +7,7 @@
 //   du_i = sum_l w_{W-1-l} dz_{i+l}  (+ the final state's gradient)
 //   dw_k = sum_t dz_t u_{t-(W-1)+k},  dbias = sum_t dz_t
 // z is recomputed from the inputs, so the forward saves nothing.
-#include "sconv_device.h"
+#include "column_sum.h"
 #include "sconv_host.h"
 
 namespace sconv {
@@ -110,18 +110,14 @@ __global__ __launch_bounds__(64) void conv_grad_simple(const ConvGradParams p) {
   part[W] = db;
 }
 
-// dweight and dbias: the sequences' sums, added in their order.
-__global__ __launch_bounds__(64) void conv_grad_sum_kernel(const float* partial, float* dweight,
-                                                           float* dbias, int32_t batch,
-                                                           int32_t dim, int32_t W) {
-  const int64_t id = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  const int64_t n = (int64_t)dim * (W + 1);
-  if (id >= n) return;
-  float acc = 0.f;
-  for (int b = 0; b < batch; ++b) acc += partial[b * n + id];
-  const int c = (int)(id / (W + 1)), k = (int)(id - (int64_t)c * (W + 1));
-  if (k < W) dweight[(int64_t)c * W + k] = acc;
-  else if (dbias) dbias[c] = acc;
+__global__ __launch_bounds__(kSumCols * kSumGroups) void conv_grad_sum_kernel(
+    const float* partial, float* dweight, float* dbias, int32_t batch, int32_t dim, int32_t W) {
+  column_sum(partial, batch, (int64_t)dim * (W + 1), [&](int64_t id, float v) {
+    const int64_t c = id / (W + 1);
+    const int k = (int)(id - c * (W + 1));
+    if (k < W) dweight[c * W + k] = v;
+    else if (dbias) dbias[c] = v;
+  });
 }
 
 template <typename D>
@@ -215,15 +211,16 @@ extern "C" int causal_conv1d_varlen_bwd(
   p.df_k = df_stride_k; p.di_slot = di_stride_slot; p.di_c = di_stride_c; p.di_k = di_stride_k;
   p.total_T = total_T; p.num_pairs = (int64_t)batch * dim; p.batch = batch; p.dim = dim;
   p.silu = activation == SCONV_ACT_SILU; p.pad_slot_id = pad_slot_id;
-  const int64_t grid = cdiv(p.num_pairs, 64), sums = cdiv((int64_t)dim * (W + 1), 64);
-  if ((batch > 0 && !valid_grid(grid, 64)) || !valid_grid(sums, 64))
+  const int64_t grid = cdiv(p.num_pairs, 64), sums = cdiv((int64_t)dim * (W + 1), kSumCols);
+  if ((batch > 0 && !valid_grid(grid, 64)) || !valid_grid(sums, kSumCols * kSumGroups))
     return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
   if (batch > 0) {
     if (dtype == SCONV_BF16) launch_conv_grad<Bf16>(W, p, (uint32_t)grid, stream);
     else launch_conv_grad<F32>(W, p, (uint32_t)grid, stream);
     if (const int rc = check_launch(fn)) return rc;
   }
-  hipLaunchKernelGGL(conv_grad_sum_kernel, dim3((uint32_t)sums), dim3(64), 0, stream, workspace,
+  hipLaunchKernelGGL(conv_grad_sum_kernel, dim3((uint32_t)sums), dim3(kSumCols * kSumGroups), 0,
+                     stream, workspace,
                      dweight, dbias, batch, dim, W);
   return check_launch(fn);
 }

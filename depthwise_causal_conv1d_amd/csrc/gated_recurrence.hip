@@ -6,6 +6,7 @@
 // conv's packing (query_start_loc), state slots and layouts.
 #include <initializer_list>
 
+#include "column_sum.h"
 #include "recurrence_device.h"
 #include "sconv_host.h"
 
@@ -581,15 +582,12 @@ __global__ __launch_bounds__(kRowBwdWaves * 64) void rec_bwd_rows_kernel(const R
   }
 }
 
-// ddecay[c] = -scale sigmoid(decay[c]) * the sequences' sums, in their order.
-__global__ __launch_bounds__(64) void rec_ddecay_kernel(const float* partial, const float* decay,
-                                                        float* ddecay, int32_t batch, int32_t dim,
-                                                        float scale) {
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (c >= dim) return;
-  double acc = 0.0;
-  for (int b = 0; b < batch; ++b) acc += (double)partial[(int64_t)b * dim + c];
-  ddecay[c] = -scale * sigmoid(decay[c]) * (float)acc;
+// ddecay[c] = -scale sigmoid(decay[c]) * the sequences' sums.
+__global__ __launch_bounds__(kSumCols * kSumGroups) void rec_ddecay_kernel(
+    const float* partial, const float* decay, float* ddecay, int32_t batch, int32_t dim,
+    float scale) {
+  column_sum(partial, batch, dim,
+             [&](int64_t c, float v) { ddecay[c] = -scale * sigmoid(decay[c]) * v; });
 }
 
 struct RecUpdParams {
@@ -899,8 +897,8 @@ extern "C" int gated_linear_recurrence_varlen_bwd(
     }
     if (const int rc = check_launch(fn)) return rc;
   }
-  hipLaunchKernelGGL(rec_ddecay_kernel, dim3((uint32_t)cdiv(dim, 64)), dim3(64), 0, stream,
-                     workspace, decay, ddecay, batch, dim, decay_scale);
+  hipLaunchKernelGGL(rec_ddecay_kernel, dim3((uint32_t)cdiv(dim, kSumCols)),
+                     dim3(kSumCols * kSumGroups), 0, stream, workspace, decay, ddecay, batch, dim, decay_scale);
   return check_launch(fn);
 }
 

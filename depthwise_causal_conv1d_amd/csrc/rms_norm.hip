@@ -4,8 +4,11 @@
 //
 //   s = x + residual, out = s * rsqrt(mean(s^2) + eps) * weight
 //   8 bits: scale = max |out| over a group / 448, code = e4m3(out / scale)
-#include "sconv_device.h"
+#include "column_sum.h"
 #include "sconv_host.h"
+
+#include <initializer_list>
+#include <type_traits>
 
 namespace sconv {
 
@@ -30,15 +33,34 @@ __device__ __forceinline__ typename D::storage norm_round(float v) {
     return v;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+// v combined over groups of N consecutive lanes (a power of two); every lane
+// gets the result.  Up to 16 lanes by DPP moves inside a row.
+template <int N, typename T, typename F>
+__device__ __forceinline__ T lanes_reduce(T v, F&& f) {
+  auto step = [&](auto ctrl) {
+    constexpr int C = decltype(ctrl)::value;
+    const int m = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), C, 0xF, 0xF, true);
+    v = f(v, __builtin_bit_cast(T, m));
+  };
+  if constexpr (N >= 2) step(std::integral_constant<int, 0xB1>());   // lanes 1 0 3 2
+  if constexpr (N >= 4) step(std::integral_constant<int, 0x4E>());   // lanes 2 3 0 1
+  if constexpr (N >= 8) step(std::integral_constant<int, 0x141>());  // half rows mirrored
+  if constexpr (N >= 16) step(std::integral_constant<int, 0x140>()); // rows mirrored
+  if constexpr (N >= 32) v = f(v, __shfl_xor(v, 16, 64));
+  if constexpr (N >= 64) v = f(v, __shfl_xor(v, 32, 64));
   return v;
 }
 
+struct Add {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
+};
+
 // Sum over the workgroup; every thread gets it.
 __device__ __forceinline__ float block_sum(float v, float* lds) {
-  v = wave_sum(v);
+  v = lanes_reduce<64>(v, Add());
   const int wave = threadIdx.x >> 6, n = blockDim.x >> 6;
   if ((threadIdx.x & 63) == 0) lds[wave] = v;
   __syncthreads();
@@ -61,7 +83,24 @@ __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xFF);
 }
 
-// One workgroup per row, which it reads three times.
+// V codes of v * inv, one store.
+template <int V>
+__device__ __forceinline__ void store_codes(uint8_t* q, const float (&v)[V], float inv) {
+  if constexpr (V == 1) {
+    *q = to_e4m3(v[0] * inv);
+  } else {
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int e = 0; e < V; e += 4) {
+      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[e] * inv, v[e + 1] * inv, 0, false);
+      w[e / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[e + 2] * inv, v[e + 3] * inv, lo, true);
+    }
+    __builtin_memcpy(__builtin_assume_aligned(q, V), w, V);
+  }
+}
+
+// One workgroup per row, which it reads three times: rows too long for the
+// registers, and groups of channels at unaligned rows.
 template <typename D, bool Q>
 __global__ __launch_bounds__(kNormThreads) void norm_fwd_simple(const NormParams p) {
   using S = typename D::storage;
@@ -81,7 +120,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_simple(const NormParams
   const float mean = block_sum(sq, lds) / (float)p.dim;
   const float rstd = 1.0f / sqrtf(mean + p.eps);
   for (int g = 0; g < p.dim; g += p.group) {
-    float scale = 1.f;
+    float inv = 1.f;
     if constexpr (Q) {
       if (threadIdx.x == 0) amax = 0;
       __syncthreads();
@@ -90,7 +129,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_simple(const NormParams
         m = max(m, abs_bits(at(c) * rstd * load_as_float<D>(w + c)));
       atomicMax(&amax, m);
       __syncthreads();
-      scale = scale_of(amax);
+      const float scale = scale_of(amax);
+      inv = 1.0f / scale;
       if (threadIdx.x == 0) p.scales[row * p.sc_rs + g / p.group] = scale;
       __syncthreads();
     }
@@ -98,8 +138,111 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_simple(const NormParams
       const float v = at(c);
       const float y = v * rstd * load_as_float<D>(w + c);
       if (sum) sum[c] = norm_round<D>(v);
-      if constexpr (Q) static_cast<uint8_t*>(p.out)[row * p.o_rs + c] = to_e4m3(y / scale);
+      if constexpr (Q) static_cast<uint8_t*>(p.out)[row * p.o_rs + c] = to_e4m3(y * inv);
       else static_cast<S*>(p.out)[row * p.o_rs + c] = norm_round<D>(y);
+    }
+  }
+}
+
+// A row in registers, read once: T threads (one wave, or the workgroup's
+// four) hold NV vectors of V channels each.  Bound by the bytes of the rows;
+// weight comes from the caches.  G: lanes that share a scale (0: the row).
+template <typename D, int V, int NV, int T, bool Q, int G>
+__global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(const NormParams p) {
+  using S = typename D::storage;
+  using P = Pack<D, V>;
+  constexpr int kRows = kNormThreads / T, kWaves = T / 64;
+  __shared__ float lsum[kWaves];
+  __shared__ uint32_t lmax[kWaves];
+  const int t = threadIdx.x % T, wave = t >> 6;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
+  if (row >= p.rows) return;  // with a barrier below, a workgroup has one row
+  const S* x = static_cast<const S*>(p.x) + row * p.x_rs;
+  const S* res = static_cast<const S*>(p.res) + row * p.r_rs;
+  const S* w = static_cast<const S*>(p.w);
+  S* sum = static_cast<S*>(p.sum) + row * p.s_rs;
+  P xv[NV], rv[NV], wv[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * T + t) * V;
+    xv[j].zero();
+    rv[j].zero();
+    wv[j].zero();
+    if (c < p.dim) {
+      xv[j].load(x + c);
+      if (p.res) rv[j].load(res + c);
+      wv[j].load(w + c);
+    }
+  }
+  float s[NV][V], sq = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    float f[V];
+    xv[j].to_float(s[j]);
+    if (p.res) {
+      rv[j].to_float(f);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[j][e] += f[e];
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) sq = __builtin_fmaf(s[j][e], s[j][e], sq);
+  }
+  sq = lanes_reduce<64>(sq, Add());
+  if constexpr (kWaves > 1) {
+    if ((t & 63) == 0) lsum[wave] = sq;
+    __syncthreads();
+    sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) sq += lsum[i];
+  }
+  const float rstd = 1.0f / sqrtf(sq / (float)p.dim + p.eps);
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * T + t) * V;
+    if (p.sum && c < p.dim) {
+      P o;
+      o.from_float(s[j]);
+      o.store(sum + c);
+    }
+    float f[V];
+    wv[j].to_float(f);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      s[j][e] = s[j][e] * rstd * f[e];
+      if constexpr (Q && G == 0) amax = Max()(amax, c < p.dim ? abs_bits(s[j][e]) : 0u);
+    }
+  }
+  float inv = 0.f;
+  if constexpr (Q && G == 0) {
+    amax = lanes_reduce<64>(amax, Max());
+    if constexpr (kWaves > 1) {
+      if ((t & 63) == 0) lmax[wave] = amax;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) amax = Max()(amax, lmax[i]);
+    }
+    const float scale = scale_of(amax);
+    inv = 1.0f / scale;
+    if (t == 0) p.scales[row * p.sc_rs] = scale;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * T + t) * V;
+    if constexpr (Q) {
+      if constexpr (G > 0) {
+        amax = 0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) amax = Max()(amax, abs_bits(s[j][e]));
+        const float scale = scale_of(lanes_reduce<(G > 0 ? G : 1)>(amax, Max()));
+        inv = 1.0f / scale;
+        if (t % (G > 0 ? G : 1) == 0 && c < p.dim) p.scales[row * p.sc_rs + c / p.group] = scale;
+      }
+      if (c < p.dim) store_codes(static_cast<uint8_t*>(p.out) + row * p.o_rs + c, s[j], inv);
+    } else if (c < p.dim) {
+      P o;
+      o.from_float(s[j]);
+      o.store(static_cast<S*>(p.out) + row * p.o_rs + c);
     }
   }
 }
@@ -114,7 +257,7 @@ struct NormBwdParams {
 };
 
 // dx = rstd (w dout - x^ mean(w dout x^)) + dresidual, x^ = x rstd;
-// dweight's share of this workgroup's rows.
+// dweight's share of this workgroup's rows.  Rows too long for the registers.
 template <typename D>
 __global__ __launch_bounds__(kNormThreads) void norm_bwd_simple(const NormBwdParams p) {
   using S = typename D::storage;
@@ -146,18 +289,228 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_simple(const NormBwdPar
   }
 }
 
-// dweight: the workgroups' sums, added in their order.
-__global__ __launch_bounds__(64) void norm_dweight_kernel(const float* partial, float* dweight,
-                                                          int32_t dim, int32_t n) {
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (c >= dim) return;
-  float acc = 0.f;
-  for (int i = 0; i < n; ++i) acc += partial[(int64_t)i * dim + c];
-  dweight[c] = acc;
+// Rows in registers: T threads hold NV vectors of V channels of a row, walk
+// every kRows * gridDim-th row, and keep dweight's sums of their channels.
+// The next row's loads are issued before this row's sums are exchanged.
+template <typename D, int V, int NV, int T>
+__global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(const NormBwdParams p) {
+  using S = typename D::storage;
+  using P = Pack<D, V>;
+  constexpr int kRows = kNormThreads / T, kWaves = T / 64;
+  __shared__ float2 lsum[2][kWaves];
+  const int t = threadIdx.x % T, wave = t >> 6, mine = threadIdx.x / T;
+  const S* w = static_cast<const S*>(p.w);
+  P wv[NV], xv[NV], gv[NV], dv[NV];
+  float dw[NV][V];
+  auto fetch = [&](int64_t row) {
+    const S* x = static_cast<const S*>(p.x) + row * p.x_rs;
+    const S* g = static_cast<const S*>(p.dout) + row * p.do_rs;
+    const S* dr = static_cast<const S*>(p.dres) + row * p.dr_rs;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * T + t) * V;
+      if (c < p.dim) {
+        xv[j].load(x + c);
+        gv[j].load(g + c);
+        if (p.dres) dv[j].load(dr + c);
+      }
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * T + t) * V;
+    wv[j].zero();
+    xv[j].zero();
+    gv[j].zero();
+    dv[j].zero();
+    if (c < p.dim) wv[j].load(w + c);
+#pragma unroll
+    for (int e = 0; e < V; ++e) dw[j][e] = 0.f;
+  }
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + mine;
+  if (row < p.rows) fetch(row);
+  for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+    float x[NV][V], g[NV][V], d[NV][V], sq = 0.f, dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float f[V];
+      xv[j].to_float(x[j]);
+      gv[j].to_float(g[j]);
+      dv[j].to_float(d[j]);
+      wv[j].to_float(f);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        sq = __builtin_fmaf(x[j][e], x[j][e], sq);
+        dot = __builtin_fmaf(g[j][e] * f[e], x[j][e], dot);
+      }
+    }
+    if (row + step < p.rows) fetch(row + step);
+    sq = lanes_reduce<64>(sq, Add());
+    dot = lanes_reduce<64>(dot, Add());
+    if constexpr (kWaves > 1) {
+      if ((t & 63) == 0) lsum[turn][wave] = make_float2(sq, dot);
+      __syncthreads();
+      sq = dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) {
+        sq += lsum[turn][i].x;
+        dot += lsum[turn][i].y;
+      }
+    }
+    const float n = (float)p.dim;
+    const float rstd = 1.0f / sqrtf(sq / n + p.eps);
+    const float proj = dot * rstd / n;
+    S* dx = static_cast<S*>(p.dx) + row * p.dx_rs;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * T + t) * V;
+      float f[V], y[V];
+      wv[j].to_float(f);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float hat = x[j][e] * rstd;
+        dw[j][e] = __builtin_fmaf(g[j][e], hat, dw[j][e]);
+        y[e] = rstd * (g[j][e] * f[e] - hat * proj) + d[j][e];
+      }
+      if (c < p.dim) {
+        P o;
+        o.from_float(y);
+        o.store(dx + c);
+      }
+    }
+  }
+  // the rows' sums of one channel in the order of the workgroup's waves
+  if constexpr (kRows > 1) {
+    __shared__ float lds[kRows][T * V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < V; ++e) lds[mine][t * V + e] = dw[j][e];
+      __syncthreads();
+      if (mine == 0) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float a = 0.f;
+#pragma unroll
+          for (int q = 0; q < kRows; ++q) a += lds[q][t * V + e];
+          dw[j][e] = a;
+        }
+      }
+    }
+    if (mine != 0) return;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * T + t) * V;
+    if (c < p.dim) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) p.partial[(int64_t)blockIdx.x * p.dim + c + e] = dw[j][e];
+    }
+  }
+}
+
+__global__ __launch_bounds__(kSumCols * kSumGroups) void norm_dweight_kernel(const float* partial,
+                                                                             float* dweight,
+                                                                             int32_t dim,
+                                                                             int32_t n) {
+  column_sum(partial, n, dim, [&](int64_t c, float v) { dweight[c] = v; });
+}
+
+// How many vectors of a row T threads hold: the smallest instance that
+// covers dim, 0 if none does.
+static int norm_vectors(int32_t dim, int V, int T) {
+  const int64_t need = cdiv(dim, (int64_t)V * T);
+  if (V > 1) return need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : 0;
+  return need <= 4 ? 4 : need <= 16 ? 16 : need <= 32 ? 32 : 0;
+}
+
+// Threads of a row: a wave needs no barrier and gives every lane more loads
+// at once, four waves shorten a long row's chain when rows are few.
+static int norm_threads(int32_t dim, int V, int64_t rows) {
+  const int64_t per = cdiv(dim, (int64_t)V * 64);
+  if (per <= (V > 1 ? 2 : 16)) return 64;
+  return V > 1 && per <= 8 && rows >= 4096 ? 64 : 256;
+}
+
+template <typename D, int V, int NV, int T>
+static void launch_norm_fwd(bool quant, int lanes, const NormParams& p, hipStream_t s) {
+  const dim3 g((uint32_t)cdiv(p.rows, kNormThreads / T)), th(kNormThreads);
+  if (!quant) hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, false, 0>), g, th, 0, s, p);
+  else if (lanes == 0) hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 0>), g, th, 0, s, p);
+  else if constexpr (V > 1) {
+    switch (lanes) {
+      case 4: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 4>), g, th, 0, s, p); break;
+      case 8: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 8>), g, th, 0, s, p); break;
+      case 16: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 16>), g, th, 0, s, p); break;
+      case 32: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 32>), g, th, 0, s, p); break;
+      default: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 64>), g, th, 0, s, p); break;
+    }
+  }
+}
+
+template <typename D, int V>
+static void launch_norm_fwd_n(int nv, int T, bool quant, int lanes, const NormParams& p,
+                              hipStream_t s) {
+  if constexpr (V > 1) {
+    if (T == 64) {
+      if (nv == 1) launch_norm_fwd<D, V, 1, 64>(quant, lanes, p, s);
+      else if (nv == 2) launch_norm_fwd<D, V, 2, 64>(quant, lanes, p, s);
+      else if (nv == 4) launch_norm_fwd<D, V, 4, 64>(quant, lanes, p, s);
+      else launch_norm_fwd<D, V, 8, 64>(quant, lanes, p, s);
+    } else {
+      if (nv == 1) launch_norm_fwd<D, V, 1, 256>(quant, lanes, p, s);
+      else if (nv == 2) launch_norm_fwd<D, V, 2, 256>(quant, lanes, p, s);
+      else if (nv == 4) launch_norm_fwd<D, V, 4, 256>(quant, lanes, p, s);
+      else launch_norm_fwd<D, V, 8, 256>(quant, lanes, p, s);
+    }
+  } else {
+    if (T == 64) {
+      if (nv == 4) launch_norm_fwd<D, 1, 4, 64>(quant, 0, p, s);
+      else launch_norm_fwd<D, 1, 16, 64>(quant, 0, p, s);
+    } else {
+      if (nv <= 16) launch_norm_fwd<D, 1, 16, 256>(quant, 0, p, s);
+      else launch_norm_fwd<D, 1, 32, 256>(quant, 0, p, s);
+    }
+  }
+}
+
+template <typename D, int V>
+static void launch_norm_bwd_n(int nv, int T, const NormBwdParams& p, uint32_t grid, hipStream_t s) {
+  const dim3 g(grid), th(kNormThreads);
+  if constexpr (V > 1) {
+    if (T == 64) {
+      if (nv == 1) hipLaunchKernelGGL((norm_bwd_kernel<D, V, 1, 64>), g, th, 0, s, p);
+      else hipLaunchKernelGGL((norm_bwd_kernel<D, V, 2, 64>), g, th, 0, s, p);
+    } else {
+      if (nv == 1) hipLaunchKernelGGL((norm_bwd_kernel<D, V, 1, 256>), g, th, 0, s, p);
+      else if (nv == 2) hipLaunchKernelGGL((norm_bwd_kernel<D, V, 2, 256>), g, th, 0, s, p);
+      else if (nv == 4) hipLaunchKernelGGL((norm_bwd_kernel<D, V, 4, 256>), g, th, 0, s, p);
+      else hipLaunchKernelGGL((norm_bwd_kernel<D, V, 8, 256>), g, th, 0, s, p);
+    }
+  } else {
+    if (T == 64) {
+      if (nv == 4) hipLaunchKernelGGL((norm_bwd_kernel<D, 1, 4, 64>), g, th, 0, s, p);
+      else hipLaunchKernelGGL((norm_bwd_kernel<D, 1, 16, 64>), g, th, 0, s, p);
+    } else {
+      if (nv <= 16) hipLaunchKernelGGL((norm_bwd_kernel<D, 1, 16, 256>), g, th, 0, s, p);
+      else hipLaunchKernelGGL((norm_bwd_kernel<D, 1, 32, 256>), g, th, 0, s, p);
+    }
+  }
+}
+
+// Every row starts on a multiple of V elements, and holds whole vectors.
+static bool norm_vec(std::initializer_list<Plane> planes, int64_t V) {
+  for (const Plane& a : planes)
+    if (!a.empty() && (a.nc % V != 0 || (a.nt > 1 && a.st % V != 0) || !aligned_to(a.p, V * a.es)))
+      return false;
+  return true;
 }
 
 // Workgroups of the backward pass, and rows of its workspace.
-static int64_t norm_parts(int64_t rows) { return rows < 512 ? rows : 512; }
+// Four rows each at least, which is a row a wave where a wave holds one.
+static int64_t norm_parts(int64_t rows) { return rows < 4096 ? cdiv(rows, 4) : 1024; }
 
 }  // namespace sconv
 
@@ -214,6 +567,20 @@ extern "C" int rms_norm_fwd(const void* x, int64_t x_stride_r, const void* resid
   p.x_rs = px.st; p.r_rs = pr.st; p.s_rs = ps.st; p.o_rs = po.st; p.sc_rs = pc.st; p.rows = rows;
   p.dim = dim; p.group = group_size ? group_size : dim; p.eps = eps;
   if (!valid_grid(rows, kNormThreads)) return fail(SCONV_ERR_UNSUPPORTED, "%s: too many rows", fn);
+  const int vec16 = (int)(16 / es);
+  const bool vec = norm_vec({px, pr, ps, po}, vec16) && aligned16(weight);
+  const int V = vec ? vec16 : 1, T = norm_threads(dim, V, rows), nv = norm_vectors(dim, V, T);
+  const int lanes = group_size / V;
+  if (nv > 0 && (vec || group_size == 0)) {
+    if (dtype == SCONV_BF16) {
+      if (vec) launch_norm_fwd_n<Bf16, 8>(nv, T, quant, lanes, p, stream);
+      else launch_norm_fwd_n<Bf16, 1>(nv, T, quant, 0, p, stream);
+    } else {
+      if (vec) launch_norm_fwd_n<F32, 4>(nv, T, quant, lanes, p, stream);
+      else launch_norm_fwd_n<F32, 1>(nv, T, quant, 0, p, stream);
+    }
+    return check_launch(fn);
+  }
   const dim3 grid((uint32_t)rows), th(kNormThreads);
   if (dtype == SCONV_BF16) {
     if (quant) hipLaunchKernelGGL((norm_fwd_simple<Bf16, true>), grid, th, 0, stream, p);
@@ -279,12 +646,27 @@ extern "C" int rms_norm_bwd(const void* dout, int64_t dout_stride_r, const void*
   p.do_rs = in[0].st; p.x_rs = in[1].st; p.dr_rs = in[2].st; p.dx_rs = po.st; p.rows = rows;
   p.dim = dim; p.eps = eps;
   if (rows > 0) {
-    const dim3 grid((uint32_t)parts), th(kNormThreads);
-    if (dtype == SCONV_BF16) hipLaunchKernelGGL(norm_bwd_simple<Bf16>, grid, th, 0, stream, p);
-    else hipLaunchKernelGGL(norm_bwd_simple<F32>, grid, th, 0, stream, p);
+    const int vec16 = (int)(16 / es);
+    const bool vec = norm_vec({in[0], in[1], in[2], po}, vec16) && aligned16(weight);
+    const int V = vec ? vec16 : 1, T = norm_threads(dim, V, 0), nv = norm_vectors(dim, V, T);
+    const uint32_t grid = (uint32_t)parts;
+    if (nv > 0) {
+      if (dtype == SCONV_BF16) {
+        if (vec) launch_norm_bwd_n<Bf16, 8>(nv, T, p, grid, stream);
+        else launch_norm_bwd_n<Bf16, 1>(nv, T, p, grid, stream);
+      } else {
+        if (vec) launch_norm_bwd_n<F32, 4>(nv, T, p, grid, stream);
+        else launch_norm_bwd_n<F32, 1>(nv, T, p, grid, stream);
+      }
+    } else if (dtype == SCONV_BF16) {
+      hipLaunchKernelGGL(norm_bwd_simple<Bf16>, dim3(grid), dim3(kNormThreads), 0, stream, p);
+    } else {
+      hipLaunchKernelGGL(norm_bwd_simple<F32>, dim3(grid), dim3(kNormThreads), 0, stream, p);
+    }
     if (const int rc = check_launch(fn)) return rc;
   }
-  hipLaunchKernelGGL(norm_dweight_kernel, dim3((uint32_t)cdiv(dim, 64)), dim3(64), 0, stream,
-                     workspace, dweight, dim, (int32_t)parts);
+  hipLaunchKernelGGL(norm_dweight_kernel, dim3((uint32_t)cdiv(dim, kSumCols)),
+                     dim3(kSumCols * kSumGroups), 0, stream, workspace, dweight, dim,
+                     (int32_t)parts);
   return check_launch(fn);
 }
