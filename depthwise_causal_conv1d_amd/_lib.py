@@ -38,6 +38,7 @@ EXPORTS = (
     "gated_linear_recurrence_varlen_fwd",
     "gated_linear_recurrence_varlen_bwd",
     "gated_linear_recurrence_update",
+    "causal_conv1d_varlen_bwd_workspace",
     "causal_conv1d_varlen_bwd",
     "rms_norm_fwd",
     "rms_norm_bwd_workspace",
@@ -111,6 +112,7 @@ _SIGS = {
                                            I64, I32, I32, P],
     "gated_linear_recurrence_update": [P, I64, P, I64, P, I64, P, FLT, P, I64, I64, P, P, I64,
                                        I32, I32, I32, I32, P],
+    "causal_conv1d_varlen_bwd_workspace": [I64, I32, I32, I32, PI64],
     "causal_conv1d_varlen_bwd": [P, I64, I64, P, I64, I64, P, I64, I64, P, P, I64, I64, I64, I64,
                                  P, I32, P, P, P, I64, I64, I64, P, I64, I64, I64, P, I64, I64, P,
                                  P, P, I64, I32, I64, I32, I32, I32, I32, P],

@@ -8,6 +8,7 @@
 //   dw_k = sum_t dz_t u_{t-(W-1)+k},  dbias = sum_t dz_t
 // z is recomputed from the inputs, so the forward saves nothing.
 #include "column_sum.h"
+#include "lane_tokens.h"
 #include "sconv_host.h"
 
 namespace sconv {
@@ -19,20 +20,12 @@ struct ConvGradParams {
   const uint8_t* has_init;
   const void* dfinal;
   void *dinitial, *dx;
-  float* partial;  // [batch, dim, W + 1]: dw, dbias of one sequence
+  float* partial;  // [parts, dim, W + 1]: dw, dbias of one sequence or segment
   int64_t do_sc, do_st, x_sc, x_st, w_sc, w_sk, dx_sc, dx_st;
   int64_t is_slot, is_c, is_k, df_slot, df_c, df_k, di_slot, di_c, di_k;
-  int64_t total_T, num_pairs;
+  int64_t total_T, num_pairs, strip;
   int32_t batch, dim, silu, pad_slot_id;
 };
-
-template <typename D>
-__device__ __forceinline__ typename D::storage rounded(float v) {
-  if constexpr (sizeof(typename D::storage) == 2)
-    return __builtin_bit_cast(uint16_t, (__bf16)v);
-  else
-    return v;
-}
 
 // dout * d silu(z) / dz
 __device__ __forceinline__ float silu_grad(float z, float g) {
@@ -40,74 +33,374 @@ __device__ __forceinline__ float silu_grad(float z, float g) {
   return g * s * __builtin_fmaf(z, 1.0f - s, 1.0f);
 }
 
-// One thread per (sequence, channel), token by token: du_i is complete once
-// dz_{i+W-1} is known.
+// The three dz after a run of tokens, or before the first: dz of tokens
+// [t, t + W-1) of the sequence [start, end), from scalar loads.
 template <typename D, int W>
-__global__ __launch_bounds__(64) void conv_grad_simple(const ConvGradParams p) {
+struct Head {
   using S = typename D::storage;
-  constexpr int SL = W - 1;
-  const int64_t id = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (id >= p.num_pairs) return;
-  const int b = (int)(id / p.dim), c = (int)(id - (int64_t)b * p.dim);
-  const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
-  float* part = p.partial + id * (W + 1);
-  if (slot == p.pad_slot_id) {
+  const S *x, *g;
+  int64_t x_st, g_st, start, end;
+  float s0[W];  // initial state, oldest first (W-1 used)
+  float w[W], bias;
+  bool silu;
+
+  __device__ __forceinline__ float input(int64_t t) const {
+    if (t >= start) return load_as_float<D>(x + t * x_st);
+    return t >= start - (W - 1) ? pick(s0, (int)(t - start + W - 1)) : 0.f;
+  }
+  __device__ __forceinline__ void after(int64_t t, float (&dz)[W]) const {
+    float u[2 * W];
 #pragma unroll
-    for (int k = 0; k <= W; ++k) part[k] = 0.f;
+    for (int k = 0; k < 2 * W - 2; ++k) u[k] = t + k - (W - 1) < end ? input(t + k - (W - 1)) : 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      dz[j] = 0.f;
+      if (j < W - 1 && t + j < end) {
+        float z = bias;
+#pragma unroll
+        for (int k = 0; k < W; ++k) z = __builtin_fmaf(w[k], u[j + k], z);
+        const float gv = load_as_float<D>(g + (t + j) * g_st);
+        dz[j] = silu ? silu_grad(z, gv) : gv;
+      }
+    }
+  }
+};
+
+// Tokens in lanes: a wave takes chunks of 512 tokens of one channel from the
+// last to the first, lane l the tokens [8 l, 8 l + 8).  The inputs before a
+// lane's tokens come from the lane below, the dz after them from the lane
+// above, and across chunks from a load and from the chunk done before.
+// Every byte of x and dout is read once; bound by that.  NW waves share a
+// sequence, each with a run of its chunks (one dz past a run is recomputed).
+template <typename D, bool VEC, int W, int NW>
+__global__ __launch_bounds__(256) void conv_grad_kernel(const ConvGradParams p) {
+  using S = typename D::storage;
+  constexpr int SL = W - 1, N = kLaneTokens, kPairs = 4 / NW;
+  static_assert(NW == 1 || NW == 4, "a barrier is met by one pair only");
+  __shared__ float sums[NW][W + 1];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int sub = wave % NW;
+  const int64_t pair = (int64_t)xcd_contiguous(blockIdx.x, gridDim.x) * kPairs + wave / NW;
+  if (pair >= p.num_pairs) return;
+  const int b = (int)(pair / p.dim), c = (int)(pair - (int64_t)b * p.dim);
+  const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
+  float* part = p.partial + pair * (W + 1);
+  if (slot == p.pad_slot_id) {
+    if (sub == 0 && lane <= W) part[lane] = 0.f;
     return;
   }
-  const int64_t start = p.qsl[b], L = p.qsl[b + 1] - start;
+  const int64_t start = p.qsl[b], end = p.qsl[b + 1];
   const bool init = p.initial && p.has_init && p.has_init[b] != 0;
-  const S* x = static_cast<const S*>(p.x) + c * p.x_sc + start * p.x_st;
-  const S* g = static_cast<const S*>(p.dout) + c * p.do_sc + start * p.do_st;
-  S* dx = static_cast<S*>(p.dx) + c * p.dx_sc + start * p.dx_st;
-  const S* df = p.dfinal ? static_cast<const S*>(p.dfinal) + slot * p.df_slot + c * p.df_c : nullptr;
-  S* di = p.dinitial ? static_cast<S*>(p.dinitial) + slot * p.di_slot + c * p.di_c : nullptr;
-  float w[W], u[W], dz[W], dw[W], db = 0.f;
-  const float bias = p.bias ? load_as_float<D>(static_cast<const S*>(p.bias) + c) : 0.f;
+  Head<D, W> q;
+  q.x = static_cast<const S*>(p.x) + c * p.x_sc;
+  q.g = static_cast<const S*>(p.dout) + c * p.do_sc;
+  q.x_st = p.x_st;
+  q.g_st = p.do_st;
+  q.start = start;
+  q.end = end;
+  q.silu = p.silu;
+  q.bias = p.bias ? load_as_float<D>(static_cast<const S*>(p.bias) + c) : 0.f;
+  float dfv[W], acc[W + 1];
 #pragma unroll
   for (int k = 0; k < W; ++k) {
-    w[k] = load_as_float<D>(static_cast<const S*>(p.w) + c * p.w_sc + k * p.w_sk);
-    dw[k] = dz[k] = u[k] = 0.f;
+    q.w[k] = load_as_float<D>(static_cast<const S*>(p.w) + c * p.w_sc + k * p.w_sk);
+    q.s0[k] = k < SL && init ? load_as_float<D>(static_cast<const S*>(p.initial) + slot * p.is_slot +
+                                                c * p.is_c + k * p.is_k) : 0.f;
+    dfv[k] = k < SL && p.dfinal ? load_as_float<D>(static_cast<const S*>(p.dfinal) + slot * p.df_slot +
+                                                   c * p.df_c + k * p.df_k) : 0.f;
+    acc[k] = 0.f;
   }
-#pragma unroll
-  for (int m = 0; m < SL; ++m)  // u[W-1] is the current token's input
-    if (init) u[m + 1] = load_as_float<D>(static_cast<const S*>(p.initial) + slot * p.is_slot + c * p.is_c + m * p.is_k);
-  float dfv[W];
-#pragma unroll
-  for (int m = 0; m < SL; ++m) dfv[m] = df ? load_as_float<D>(df + m * p.df_k) : 0.f;
-  for (int64_t t = 0; t < L + SL; ++t) {
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-      u[k] = u[k + 1];
-      dz[k] = dz[k + 1];
-    }
-    u[W - 1] = 0.f;
-    dz[W - 1] = 0.f;
-    if (t < L) {
-      u[W - 1] = load_as_float<D>(x + t * p.x_st);
-      float z = bias;
-#pragma unroll
-      for (int k = 0; k < W; ++k) z = __builtin_fmaf(w[k], u[k], z);
-      const float gv = load_as_float<D>(g + t * p.do_st);
-      dz[W - 1] = p.silu ? silu_grad(z, gv) : gv;
-#pragma unroll
-      for (int k = 0; k < W; ++k) dw[k] = __builtin_fmaf(dz[W - 1], u[k], dw[k]);
-      db += dz[W - 1];
-    }
-    const int64_t i = t - SL;  // dz[l] = dz_{i+l}
-    float du = 0.f;
-#pragma unroll
-    for (int l = 0; l < W; ++l) du = __builtin_fmaf(w[W - 1 - l], dz[l], du);
+  acc[W] = 0.f;
+  S* dx = static_cast<S*>(p.dx) + c * p.dx_sc;
+
+  // this wave's run of chunks [c_lo, c_hi)
+  const int64_t c0 = start / kChunkTokens, c1 = end > start ? (end - 1) / kChunkTokens + 1 : c0;
+  const int64_t per = (c1 - c0 + NW - 1) / NW;
+  const int64_t c_lo = c0 + sub * per, c_hi = c_lo + per < c1 ? c_lo + per : c1;
+  Raw8<D> rx, rg;
+  S before[W];  // the inputs before the chunk (uniform)
+  auto fetch = [&](int64_t base) {
+    const int64_t t = base + lane * N;
+    rx.template load<VEC>(q.x, p.x_st, t, p.total_T);
+    rg.template load<VEC>(q.g, p.do_st, t, p.total_T);
 #pragma unroll
     for (int m = 0; m < SL; ++m)
-      if (i == L - SL + m) du += dfv[m];
-    if (i >= 0) dx[i * p.dx_st] = rounded<D>(du);
-    else if (di) di[(i + SL) * p.di_k] = init ? rounded<D>(du) : rounded<D>(0.f);
+      before[m] = base - SL + m >= start ? q.x[(base - SL + m) * p.x_st] : (S)0;
+  };
+  float next[W];  // dz of the tokens after the chunk
+  if (c_hi > c_lo) {
+    fetch((c_hi - 1) * kChunkTokens);
+    q.after(c_hi * kChunkTokens, next);
+  }
+  for (int64_t ch = c_hi - 1; ch >= c_lo; --ch) {
+    const int64_t base = ch * kChunkTokens, t = base + lane * N;
+    float u[SL + N], dz[N + SL];
+    {
+      float f[N];
+      rx.to_float(f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) u[SL + e] = f[e];
+      rg.to_float(f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) dz[e] = f[e];
+    }
+    float head[W];
+#pragma unroll
+    for (int m = 0; m < SL; ++m) {
+      head[m] = to_float<D>(before[m]);
+      if (base - SL + m < start) head[m] = q.input(base - SL + m);
+    }
+    if (ch > c_lo) fetch(base - kChunkTokens);
+    const bool edge = base < start || base + kChunkTokens > end;
+    if (edge) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int64_t i = t + e - start;
+        if (i < 0) u[SL + e] = i >= -SL ? pick(q.s0, (int)(i + SL)) : 0.f;
+        dz[e] = i >= 0 && t + e < end ? dz[e] : 0.f;
+        u[SL + e] = t + e < end ? u[SL + e] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < SL; ++m) u[m] = lane_move<0x138>(head[m], u[N + m]);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      float z = q.bias;
+#pragma unroll
+      for (int k = 0; k < W; ++k) z = __builtin_fmaf(q.w[k], u[e + k], z);
+      if (p.silu) dz[e] = silu_grad(z, dz[e]);
+#pragma unroll
+      for (int k = 0; k < W; ++k) acc[k] = __builtin_fmaf(dz[e], u[e + k], acc[k]);
+      acc[W] += dz[e];
+    }
+#pragma unroll
+    for (int m = 0; m < SL; ++m) {
+      dz[N + m] = lane_move<0x130>(next[m], dz[m]);  // from the lane above
+      next[m] = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(dz[m])));
+    }
+    float y[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      y[e] = 0.f;
+#pragma unroll
+      for (int l = 0; l < W; ++l) y[e] = __builtin_fmaf(q.w[W - 1 - l], dz[e + l], y[e]);
+    }
+    if (base + kChunkTokens > end - SL) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int64_t m = t + e - (end - SL);
+        if (m >= 0 && m < SL) y[e] += pick(dfv, (int)m);
+      }
+    }
+    Raw8<D> o;
+    o.from_float(y);
+    o.template store<VEC>(dx, p.dx_st, t, start, end);
   }
 #pragma unroll
-  for (int k = 0; k < W; ++k) part[k] = dw[k];
-  part[W] = db;
+  for (int k = 0; k <= W; ++k) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) acc[k] += __shfl_xor(acc[k], d, 64);
+  }
+  if constexpr (NW > 1) {
+    if (lane == 0) {
+#pragma unroll
+      for (int k = 0; k <= W; ++k) sums[sub][k] = acc[k];
+    }
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int k = 0; k <= W; ++k) {
+      acc[k] = 0.f;
+#pragma unroll
+      for (int s = 0; s < NW; ++s) acc[k] += sums[s][k];
+    }
+  }
+  if (sub != 0 || lane != 0) return;
+#pragma unroll
+  for (int k = 0; k <= W; ++k) part[k] = acc[k];
+  if (SL > 0 && p.dinitial) {
+    float dz[W];
+    q.after(start, dz);
+    S* di = static_cast<S*>(p.dinitial) + slot * p.di_slot + c * p.di_c;
+    const int64_t L = end - start;
+#pragma unroll
+    for (int j = 0; j < SL; ++j) {  // logical index j - SL
+      float du = 0.f;
+#pragma unroll
+      for (int l = SL - j; l < W; ++l) du = __builtin_fmaf(q.w[W - 1 - l], dz[j - SL + l], du);
+      if (j >= L) du += pick(dfv, (int)(j - L));
+      di[j * p.di_k] = init ? round_to<D>(du) : (S)0;
+    }
+  }
+}
+
+// Channels in lanes (rows of tokens): a wave walks a strip of rows forward
+// with the last W inputs and dz of its V channels in registers; du_i is
+// complete once dz_{i+W-1} is known, so a strip reads W-1 rows before it and
+// W-1 after it again.  Strips lie on the flat token axis, whatever the
+// sequences' lengths: a wave takes every sequence that its strip meets.
+constexpr int kStripWaves = 4, kStripGroup = 8;
+
+// The first sequence that does not end before row lo.
+__device__ __forceinline__ int first_sequence(const int32_t* qsl, int32_t batch, int64_t lo) {
+  int n = 0;
+  for (int i0 = 0; i0 < batch; i0 += 64) {
+    const int i = i0 + (threadIdx.x & 63);
+    const bool done = i < batch && qsl[i + 1] < lo;
+    const int k = __popcll(__ballot(done));
+    n += k;
+    if (k < 64) break;
+  }
+  return n;
+}
+
+template <typename D, int V, int W>
+__global__ __launch_bounds__(kStripWaves * 64) void conv_grad_rows_kernel(const ConvGradParams p) {
+  using S = typename D::storage;
+  using P = Pack<D, V>;
+  constexpr int SL = W - 1, G = kStripGroup;
+  __shared__ float sums[kStripWaves][W + 1][64 * V];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
+  const uint32_t wg = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int64_t seg = wg / slabs;
+  const int ch = ((int)(wg % slabs) * 64 + lane) * V;
+  const bool live = ch < p.dim;
+  const int c = live ? ch : p.dim - V;
+  const int64_t strip = seg * kStripWaves + wave;
+  const int64_t lo = strip * p.strip, hi = lo + p.strip;
+  // The strip of the last row (of none: the first strip) also takes the
+  // sequences that start at the end of the rows; strips past it are idle.
+  const bool used = lo < p.total_T || strip == 0, last = used && hi >= p.total_T;
+  float w[W][V], bias[V], acc[W + 1][V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    bias[v] = p.bias ? load_as_float<D>(static_cast<const S*>(p.bias) + c + v) : 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+      w[k][v] = load_as_float<D>(static_cast<const S*>(p.w) + (c + v) * p.w_sc + k * p.w_sk);
+#pragma unroll
+    for (int k = 0; k <= W; ++k) acc[k][v] = 0.f;
+  }
+  const S* x = static_cast<const S*>(p.x) + c;
+  const S* g = static_cast<const S*>(p.dout) + c;
+  S* dx = static_cast<S*>(p.dx) + c;
+  for (int b = used ? first_sequence(p.qsl, p.batch, lo) : p.batch; b < p.batch; ++b) {
+    const int64_t start = p.qsl[b], end = p.qsl[b + 1];
+    if (start >= hi && !last) break;
+    const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
+    const bool mine_first = start >= lo && (start < hi || last);
+    const int64_t from = start > lo ? start : lo, to = end < hi ? end : hi;
+    if (slot == p.pad_slot_id || (from >= to && !(start == end && mine_first))) continue;
+    const bool init = p.initial && p.has_init && p.has_init[b] != 0;
+    auto state = [&](int64_t i, int v) {  // initial state, logical index i in [-SL, 0)
+      return init && i >= -SL ? load_as_float<D>(static_cast<const S*>(p.initial) + slot * p.is_slot +
+                                                 (c + v) * p.is_c + (i + SL) * p.is_k) : 0.f;
+    };
+    float u[W][V], dz[W][V];
+#pragma unroll
+    for (int m = 0; m < W; ++m) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) u[m][v] = dz[m][v] = 0.f;
+      if (m >= 1) {  // u[1..SL]: the inputs before `from`
+        const int64_t t = from - W + m;
+        if (t >= start) {
+          P r;
+          r.load(x + t * p.x_st);
+          r.to_float(u[m]);
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) u[m][v] = state(t - start, v);
+        }
+      }
+    }
+    P rx[G], rg[G];
+    auto fetch = [&](int64_t t0) {
+#pragma unroll
+      for (int r = 0; r < G; ++r) {
+        const int64_t t = t0 + r < end ? t0 + r : end - 1;
+        if (end > start) {
+          rx[r].load(x + t * p.x_st);
+          rg[r].load(g + t * p.do_st);
+        } else {
+          rx[r].zero();
+          rg[r].zero();
+        }
+      }
+    };
+    fetch(from);
+    for (int64_t t0 = from; t0 < to + SL; t0 += G) {
+      P cx[G], cg[G];
+#pragma unroll
+      for (int r = 0; r < G; ++r) {
+        cx[r] = rx[r];
+        cg[r] = rg[r];
+      }
+      if (t0 + G < to + SL) fetch(t0 + G);
+#pragma unroll
+      for (int r = 0; r < G; ++r) {
+        const int64_t t = t0 + r, i = t - SL;
+        if (t >= to + SL) break;
+        const bool in = t < end;
+        float gf[V], xf[V], du[V];
+        cx[r].to_float(xf);
+        cg[r].to_float(gf);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+          for (int k = 0; k + 1 < W; ++k) {
+            u[k][v] = u[k + 1][v];
+            dz[k][v] = dz[k + 1][v];
+          }
+          u[SL][v] = in ? xf[v] : 0.f;
+          float z = bias[v];
+#pragma unroll
+          for (int k = 0; k < W; ++k) z = __builtin_fmaf(w[k][v], u[k][v], z);
+          const float d = p.silu ? silu_grad(z, gf[v]) : gf[v];
+          dz[SL][v] = in ? d : 0.f;
+          const float own = t < to ? dz[SL][v] : 0.f;  // the rows after the strip are another's
+#pragma unroll
+          for (int k = 0; k < W; ++k) acc[k][v] = __builtin_fmaf(own, u[k][v], acc[k][v]);
+          acc[W][v] += own;
+          du[v] = 0.f;
+#pragma unroll
+          for (int l = 0; l < W; ++l) du[v] = __builtin_fmaf(w[W - 1 - l][v], dz[l][v], du[v]);
+        }
+        if (p.dfinal && i >= end - SL) {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            du[v] += load_as_float<D>(static_cast<const S*>(p.dfinal) + slot * p.df_slot +
+                                      (c + v) * p.df_c + (i - (end - SL)) * p.df_k);
+        }
+        if (i >= from) {
+          P o;
+          o.from_float(du);
+          if (live) o.store(dx + i * p.dx_st);
+        } else if (i < start && mine_first && p.dinitial && live) {
+          S* di = static_cast<S*>(p.dinitial) + slot * p.di_slot + (i - start + SL) * p.di_k;
+#pragma unroll
+          for (int v = 0; v < V; ++v) di[(c + v) * p.di_c] = init ? round_to<D>(du[v]) : (S)0;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k <= W; ++k) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) sums[wave][k][lane * V + v] = acc[k][v];
+  }
+  __syncthreads();
+  if (wave != 0 || !live) return;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int k = 0; k <= W; ++k) {
+      float a = 0.f;
+#pragma unroll
+      for (int s = 0; s < kStripWaves; ++s) a += sums[s][k][lane * V + v];
+      p.partial[(seg * p.dim + c + v) * (W + 1) + k] = a;
+    }
+  }
 }
 
 __global__ __launch_bounds__(kSumCols * kSumGroups) void conv_grad_sum_kernel(
@@ -120,17 +413,58 @@ __global__ __launch_bounds__(kSumCols * kSumGroups) void conv_grad_sum_kernel(
   });
 }
 
-template <typename D>
-static void launch_conv_grad(int W, const ConvGradParams& p, uint32_t grid, hipStream_t s) {
+template <typename D, bool VEC, int NW>
+static void launch_grad(int W, const ConvGradParams& p, uint32_t grid, hipStream_t s) {
+  const dim3 g(grid), th(256);
   switch (W) {
-    case 1: hipLaunchKernelGGL((conv_grad_simple<D, 1>), dim3(grid), dim3(64), 0, s, p); break;
-    case 2: hipLaunchKernelGGL((conv_grad_simple<D, 2>), dim3(grid), dim3(64), 0, s, p); break;
-    case 3: hipLaunchKernelGGL((conv_grad_simple<D, 3>), dim3(grid), dim3(64), 0, s, p); break;
-    default: hipLaunchKernelGGL((conv_grad_simple<D, 4>), dim3(grid), dim3(64), 0, s, p); break;
+    case 1: hipLaunchKernelGGL((conv_grad_kernel<D, VEC, 1, NW>), g, th, 0, s, p); break;
+    case 2: hipLaunchKernelGGL((conv_grad_kernel<D, VEC, 2, NW>), g, th, 0, s, p); break;
+    case 3: hipLaunchKernelGGL((conv_grad_kernel<D, VEC, 3, NW>), g, th, 0, s, p); break;
+    default: hipLaunchKernelGGL((conv_grad_kernel<D, VEC, 4, NW>), g, th, 0, s, p); break;
   }
 }
 
+template <typename D, int V>
+static void launch_grad_rows(int W, const ConvGradParams& p, uint32_t grid, hipStream_t s) {
+  const dim3 g(grid), th(kStripWaves * 64);
+  switch (W) {
+    case 1: hipLaunchKernelGGL((conv_grad_rows_kernel<D, V, 1>), g, th, 0, s, p); break;
+    case 2: hipLaunchKernelGGL((conv_grad_rows_kernel<D, V, 2>), g, th, 0, s, p); break;
+    case 3: hipLaunchKernelGGL((conv_grad_rows_kernel<D, V, 3>), g, th, 0, s, p); break;
+    default: hipLaunchKernelGGL((conv_grad_rows_kernel<D, V, 4>), g, th, 0, s, p); break;
+  }
+}
+
+// Rows of a strip: long strips read fewer rows twice, short ones keep a
+// small batch's chain short.
+static int64_t strip_rows(int64_t total_T, int32_t dim) {
+  return total_T * dim >= (int64_t)1 << 22 ? 64 : 16;
+}
+
+static int64_t grad_segments(int64_t total_T, int32_t dim) {
+  const int64_t n = cdiv(total_T, strip_rows(total_T, dim) * kStripWaves);
+  return n > 0 ? n : 1;  // sequences without tokens still have state gradients
+}
+
+// Parts of the workspace: the larger of the two kernels' counts, so that its
+// size does not depend on strides.
+static int64_t grad_floats(int64_t total_T, int32_t batch, int32_t dim, int32_t W) {
+  const int64_t s = grad_segments(total_T, dim), parts = batch == 0 ? 0 : s > batch ? s : batch;
+  return parts * dim * (W + 1);
+}
+
 }  // namespace sconv
+
+extern "C" int causal_conv1d_varlen_bwd_workspace(int64_t total_T, int32_t batch, int32_t dim,
+                                                  int32_t W, int64_t* floats) {
+  using namespace sconv;
+  clear_error();
+  if (total_T < 0 || batch < 0 || dim < 0 || W < 1 || W > 4 || !floats)
+    return fail(SCONV_ERR_INVALID, "causal_conv1d_varlen_bwd_workspace: sizes must be >= 0, W in "
+                                   "[1, 4], floats not NULL");
+  *floats = grad_floats(total_T, batch, dim, W);
+  return SCONV_OK;
+}
 
 extern "C" int causal_conv1d_varlen_bwd(
     const void* dout, int64_t do_stride_c, int64_t do_stride_t, const void* x,
@@ -167,7 +501,7 @@ extern "C" int causal_conv1d_varlen_bwd(
       (dfinal_states && (df_stride_slot < 0 || df_stride_c < 0 || df_stride_k < 0)) ||
       (dinitial_states && (di_stride_slot < 1 || di_stride_c < 1 || di_stride_k < 1)))
     return fail(SCONV_ERR_INVALID, "%s: strides too small", fn);
-  const int64_t need = (int64_t)batch * dim * (W + 1);
+  const int64_t need = grad_floats(total_T, batch, dim, W);
   if (workspace_floats < need)
     return fail(SCONV_ERR_INVALID, "%s: workspace holds %lld floats, %lld needed", fn,
                 (long long)workspace_floats, (long long)need);
@@ -211,16 +545,53 @@ extern "C" int causal_conv1d_varlen_bwd(
   p.df_k = df_stride_k; p.di_slot = di_stride_slot; p.di_c = di_stride_c; p.di_k = di_stride_k;
   p.total_T = total_T; p.num_pairs = (int64_t)batch * dim; p.batch = batch; p.dim = dim;
   p.silu = activation == SCONV_ACT_SILU; p.pad_slot_id = pad_slot_id;
-  const int64_t grid = cdiv(p.num_pairs, 64), sums = cdiv((int64_t)dim * (W + 1), kSumCols);
-  if ((batch > 0 && !valid_grid(grid, 64)) || !valid_grid(sums, kSumCols * kSumGroups))
+  const bool rows = dim > 1 && pg.sc == 1 && px.sc == 1 && po.sc == 1;
+  int64_t parts = batch, grid = 0;
+  int NW = 1, V = 1;
+  bool vec = false;
+  if (rows) {
+    auto lanes = [&](const Plane& a) { return a.st % 2 == 0 && aligned_to(a.p, 2 * es); };
+    V = dim % 2 == 0 && lanes(pg) && lanes(px) && lanes(po) ? 2 : 1;
+    p.strip = strip_rows(total_T, dim);
+    parts = grad_segments(total_T, dim);
+    grid = parts * cdiv(dim, 64 * V);
+  } else {
+    auto lanes = [&](const Plane& a) {
+      return a.st == 1 && (a.sc * es) % 16 == 0 && aligned16(a.p);
+    };
+    vec = lanes(pg) && lanes(px) && lanes(po);
+    // few (sequence, channel) pairs of several chunks: four waves for each
+    NW = p.num_pairs < 8192 && total_T / (batch ? batch : 1) >= 2 * kChunkTokens ? 4 : 1;
+    grid = cdiv(p.num_pairs, 4 / NW);
+  }
+  const int64_t sums = cdiv((int64_t)dim * (W + 1), kSumCols);
+  if ((batch > 0 && !valid_grid(grid, 256)) || !valid_grid(sums, kSumCols * kSumGroups))
     return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
   if (batch > 0) {
-    if (dtype == SCONV_BF16) launch_conv_grad<Bf16>(W, p, (uint32_t)grid, stream);
-    else launch_conv_grad<F32>(W, p, (uint32_t)grid, stream);
+    const uint32_t g = (uint32_t)grid;
+    if (rows) {
+      if (dtype == SCONV_BF16) {
+        if (V == 2) launch_grad_rows<Bf16, 2>(W, p, g, stream);
+        else launch_grad_rows<Bf16, 1>(W, p, g, stream);
+      } else {
+        if (V == 2) launch_grad_rows<F32, 2>(W, p, g, stream);
+        else launch_grad_rows<F32, 1>(W, p, g, stream);
+      }
+    } else if (dtype == SCONV_BF16) {
+      if (vec && NW == 1) launch_grad<Bf16, true, 1>(W, p, g, stream);
+      else if (vec) launch_grad<Bf16, true, 4>(W, p, g, stream);
+      else if (NW == 1) launch_grad<Bf16, false, 1>(W, p, g, stream);
+      else launch_grad<Bf16, false, 4>(W, p, g, stream);
+    } else {
+      if (vec && NW == 1) launch_grad<F32, true, 1>(W, p, g, stream);
+      else if (vec) launch_grad<F32, true, 4>(W, p, g, stream);
+      else if (NW == 1) launch_grad<F32, false, 1>(W, p, g, stream);
+      else launch_grad<F32, false, 4>(W, p, g, stream);
+    }
     if (const int rc = check_launch(fn)) return rc;
   }
   hipLaunchKernelGGL(conv_grad_sum_kernel, dim3((uint32_t)sums), dim3(kSumCols * kSumGroups), 0,
                      stream, workspace,
-                     dweight, dbias, batch, dim, W);
+                     dweight, dbias, (int32_t)(batch > 0 ? parts : 0), dim, W);
   return check_launch(fn);
 }

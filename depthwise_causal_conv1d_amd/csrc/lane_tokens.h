@@ -1,0 +1,128 @@
+// lane_tokens.h -- eight consecutive tokens of one channel in a lane, and the
+// cross-lane moves between them: shared by the gated linear recurrence and
+// the conv's gradients.
+#pragma once
+
+#include "sconv_device.h"
+
+namespace sconv {
+
+template <typename D>
+__device__ __forceinline__ typename D::storage round_to(float v) {
+  if constexpr (sizeof(typename D::storage) == 2)
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
+  else
+    return v;
+}
+
+// ---------------------------------------------------------------- eight tokens of a lane
+
+constexpr int kLaneTokens = 8;                     // consecutive tokens of one lane
+constexpr int kChunkTokens = 64 * kLaneTokens;     // tokens of one wave
+
+// Raw bits of a lane's eight tokens of one channel.
+template <typename D>
+struct Raw8 {
+  using S = typename D::storage;
+  static constexpr int kPacks = kLaneTokens / D::kVec16;
+  using P = Pack<D, D::kVec16>;
+  struct Elems { S e[kLaneTokens]; };
+  P p[kPacks];
+
+  // Tokens [t, t + 8) of a row of `total` tokens.  VEC: tokens contiguous,
+  // rows 16-byte aligned, t a multiple of 8.  Tokens past the row's end read
+  // as zero bits; tokens of other sequences are read and not used.
+  template <bool VEC>
+  __device__ __forceinline__ void load(const S* row, int64_t stride, int64_t t, int64_t total) {
+    if (VEC && t + kLaneTokens <= total) {
+#pragma unroll
+      for (int q = 0; q < kPacks; ++q) p[q].load_nt(row + t + q * D::kVec16);
+    } else {
+      Elems v;
+#pragma unroll
+      for (int e = 0; e < kLaneTokens; ++e)
+        v.e[e] = t + e < total ? row[(t + e) * stride] : (S)0;
+      __builtin_memcpy(p, &v, sizeof v);
+    }
+  }
+
+  __device__ __forceinline__ void to_float(float (&f)[kLaneTokens]) const {
+#pragma unroll
+    for (int q = 0; q < kPacks; ++q) {
+      float g[D::kVec16];
+      p[q].to_float(g);
+#pragma unroll
+      for (int e = 0; e < D::kVec16; ++e) f[q * D::kVec16 + e] = g[e];
+    }
+  }
+
+  __device__ __forceinline__ void from_float(const float (&f)[kLaneTokens]) {
+#pragma unroll
+    for (int q = 0; q < kPacks; ++q) {
+      float g[D::kVec16];
+#pragma unroll
+      for (int e = 0; e < D::kVec16; ++e) g[e] = f[q * D::kVec16 + e];
+      p[q].from_float(g);
+    }
+  }
+
+  // Store the tokens of [t, t + 8) that lie in [start, end).
+  template <bool VEC>
+  __device__ __forceinline__ void store(S* row, int64_t stride, int64_t t, int64_t start,
+                                        int64_t end) const {
+    if (VEC && t >= start && t + kLaneTokens <= end) {
+#pragma unroll
+      for (int q = 0; q < kPacks; ++q) p[q].store_nt(row + t + q * D::kVec16);
+    } else {
+      Elems v;
+      __builtin_memcpy(&v, p, sizeof v);
+#pragma unroll
+      for (int e = 0; e < kLaneTokens; ++e)
+        if (t + e >= start && t + e < end) row[(t + e) * stride] = v.e[e];
+    }
+  }
+};
+
+// ---------------------------------------------------------------- scans of h -> P h + H
+
+// v of another lane by a DPP move; lanes that the move has no source for,
+// and rows outside ROWS, get `other`.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float lane_move(float other, float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(other), __float_as_int(v), CTRL,
+                                                    ROWS, 0xF, false));
+}
+
+// One step of an inclusive scan: this lane's map after the moved lane's.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ void compose(float& P, float& H) {
+  const float p = lane_move<CTRL, ROWS>(1.0f, P), h = lane_move<CTRL, ROWS>(0.0f, H);
+  H = __builtin_fmaf(P, h, H);
+  P *= p;
+}
+
+// Maps of lanes 0..l composed, in ascending lane order (row_shr 1, 2, 4, 8
+// inside rows of 16 lanes, then the last lane of a row to the next row, then
+// lane 31 to the upper half).
+__device__ __forceinline__ void scan_wave_up(float& P, float& H) {
+  compose<0x111>(P, H);
+  compose<0x112>(P, H);
+  compose<0x114>(P, H);
+  compose<0x118>(P, H);
+  compose<0x142, 0xA>(P, H);
+  compose<0x143, 0xC>(P, H);
+}
+
+// The same inside each row of 16 lanes, in descending lane order (row_shl).
+__device__ __forceinline__ void scan_row_down(float& P, float& H) {
+  compose<0x101>(P, H);
+  compose<0x102>(P, H);
+  compose<0x104>(P, H);
+  compose<0x108>(P, H);
+}
+
+__device__ __forceinline__ float last_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+}  // namespace sconv

@@ -764,7 +764,11 @@ def causal_conv1d_varlen_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.
     pl = _planes(x.shape, dout, x, dx)
     dweight = torch.empty(dim, W, dtype=torch.float32, device=x.device)
     dbias = torch.empty(dim, dtype=torch.float32, device=x.device) if bias is not None else None
-    ws = torch.empty(batch * dim * (W + 1), dtype=torch.float32, device=x.device)
+    need = ctypes.c_int64()
+    _lib.check(_lib.load().causal_conv1d_varlen_bwd_workspace(total_T, batch, dim, W,
+                                                              ctypes.byref(need)),
+               "causal_conv1d_varlen_bwd_workspace")
+    ws = torch.empty(need.value, dtype=torch.float32, device=x.device)
     _call("causal_conv1d_varlen_bwd", x, *pl[:6], weight.data_ptr(), weight.stride(0),
           weight.stride(1), _ptr(bias), *pool_args[0], slots, query_start_loc.data_ptr(), batch,
           _ptr(cache_indices), _ptr(hi), *pool_args[1], *pool_args[2], *pl[6:],

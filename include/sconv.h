@@ -656,6 +656,10 @@ int gated_linear_recurrence_update(
     void* out, int64_t out_stride_b, int32_t batch, int32_t dim, int32_t dtype,
     int32_t pad_slot_id, hipStream_t stream);
 
+/* Floats of workspace that causal_conv1d_varlen_bwd needs.  Host only. */
+int causal_conv1d_varlen_bwd_workspace(int64_t total_T, int32_t batch, int32_t dim, int32_t W,
+                                       int64_t* floats);
+
 /*
  * causal_conv1d_varlen_bwd -- gradients of causal_conv1d_varlen_fwd.  With u
  * a sequence's initial state (oldest first) followed by its inputs and
@@ -676,8 +680,8 @@ int gated_linear_recurrence_update(
  *            sequence's initial state (zeros without has_initial_state), or
  *            NULL; overlaps nothing
  *   dweight  fp32 [dim, W] dense, dbias fp32 [dim] or NULL (written)
- *   workspace  fp32 [batch * dim * (W + 1)], the call's own until it has
- *            finished; workspace_floats says how many it holds
+ *   workspace  fp32, causal_conv1d_varlen_bwd_workspace floats, the call's
+ *            own until it has finished; workspace_floats says how many it holds
  *   the other arguments as causal_conv1d_varlen_fwd's
  *
  * Rows of dx outside every sequence, or in a skipped one, are not written.

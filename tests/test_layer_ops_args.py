@@ -141,6 +141,16 @@ def test_conv_gradient_refusals(lib, kw, text):
     assert cgrad(lib, **kw) == 1 and text in err(lib), err(lib)
 
 
+def test_conv_gradient_workspace(lib):
+    n = ctypes.c_int64()
+    f = lib.causal_conv1d_varlen_bwd_workspace
+    assert f(64, 2, 16, 4, ctypes.byref(n)) == 0 and n.value >= 2 * 16 * 5
+    assert f(64, 0, 16, 4, ctypes.byref(n)) == 0 and n.value == 0
+    for bad in ((-1, 1, 1, 4), (1, -1, 1, 4), (1, 1, -1, 4), (1, 1, 1, 0), (1, 1, 1, 5)):
+        assert f(*bad, ctypes.byref(n)) == 1
+    assert f(1, 1, 1, 4, None) == 1
+
+
 def norm(lib, **kw):
     a = dict(x=X, xr=256, res=GA, rr=256, w=DEC, eps=1e-6, so=GX, sr=256, out=OUT, orr=256, sc=ST,
              scr=2, group=128, rows=4, dim=256, dt=1, odt=2)
