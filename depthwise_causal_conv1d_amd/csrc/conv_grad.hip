@@ -73,14 +73,14 @@ struct Head {
 // Every byte of x and dout is read once; bound by that.  NW waves share a
 // sequence, each with a run of its chunks (one dz past a run is recomputed).
 template <typename D, bool VEC, int W, int NW>
-__global__ __launch_bounds__(256) void conv_grad_kernel(const ConvGradParams p) {
+__global__ __launch_bounds__(256, 4) void conv_grad_kernel(const ConvGradParams p) {
   using S = typename D::storage;
   constexpr int SL = W - 1, N = kLaneTokens, kPairs = 4 / NW;
   static_assert(NW == 1 || NW == 4, "a barrier is met by one pair only");
   __shared__ float sums[NW][W + 1];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int sub = wave % NW;
-  const int64_t pair = (int64_t)xcd_contiguous(blockIdx.x, gridDim.x) * kPairs + wave / NW;
+  const int64_t pair = (int64_t)xcd_groups<8>(blockIdx.x, gridDim.x) * kPairs + wave / NW;
   if (pair >= p.num_pairs) return;
   const int b = (int)(pair / p.dim), c = (int)(pair - (int64_t)b * p.dim);
   const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
@@ -113,10 +113,10 @@ __global__ __launch_bounds__(256) void conv_grad_kernel(const ConvGradParams p) 
   acc[W] = 0.f;
   S* dx = static_cast<S*>(p.dx) + c * p.dx_sc;
 
-  // this wave's run of chunks [c_lo, c_hi)
-  const int64_t c0 = start / kChunkTokens, c1 = end > start ? (end - 1) / kChunkTokens + 1 : c0;
-  const int64_t per = (c1 - c0 + NW - 1) / NW;
-  const int64_t c_lo = c0 + sub * per, c_hi = c_lo + per < c1 ? c_lo + per : c1;
+  // this wave's run of chunks [c_lo, c_hi), counted from the start
+  const int64_t chunks = (end - start + kChunkTokens - 1) / kChunkTokens;
+  const int64_t per = (chunks + NW - 1) / NW;
+  const int64_t c_lo = sub * per, c_hi = c_lo + per < chunks ? c_lo + per : chunks;
   Raw8<D> rx, rg;
   S before[W];  // the inputs before the chunk (uniform)
   auto fetch = [&](int64_t base) {
@@ -129,11 +129,11 @@ __global__ __launch_bounds__(256) void conv_grad_kernel(const ConvGradParams p) 
   };
   float next[W];  // dz of the tokens after the chunk
   if (c_hi > c_lo) {
-    fetch((c_hi - 1) * kChunkTokens);
-    q.after(c_hi * kChunkTokens, next);
+    fetch(start + (c_hi - 1) * kChunkTokens);
+    q.after(start + c_hi * kChunkTokens, next);
   }
   for (int64_t ch = c_hi - 1; ch >= c_lo; --ch) {
-    const int64_t base = ch * kChunkTokens, t = base + lane * N;
+    const int64_t base = start + ch * kChunkTokens, t = base + lane * N;
     float u[SL + N], dz[N + SL];
     {
       float f[N];
@@ -151,13 +151,10 @@ __global__ __launch_bounds__(256) void conv_grad_kernel(const ConvGradParams p) 
       if (base - SL + m < start) head[m] = q.input(base - SL + m);
     }
     if (ch > c_lo) fetch(base - kChunkTokens);
-    const bool edge = base < start || base + kChunkTokens > end;
-    if (edge) {
+    if (base + kChunkTokens > end) {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const int64_t i = t + e - start;
-        if (i < 0) u[SL + e] = i >= -SL ? pick(q.s0, (int)(i + SL)) : 0.f;
-        dz[e] = i >= 0 && t + e < end ? dz[e] : 0.f;
+        dz[e] = t + e < end ? dz[e] : 0.f;
         u[SL + e] = t + e < end ? u[SL + e] : 0.f;
       }
     }
@@ -194,7 +191,7 @@ __global__ __launch_bounds__(256) void conv_grad_kernel(const ConvGradParams p) 
     }
     Raw8<D> o;
     o.from_float(y);
-    o.template store<VEC>(dx, p.dx_st, t, start, end);
+    o.template store<VEC>(dx, p.dx_st, t, end);
   }
 #pragma unroll
   for (int k = 0; k <= W; ++k) {
@@ -556,10 +553,7 @@ extern "C" int causal_conv1d_varlen_bwd(
     parts = grad_segments(total_T, dim);
     grid = parts * cdiv(dim, 64 * V);
   } else {
-    auto lanes = [&](const Plane& a) {
-      return a.st == 1 && (a.sc * es) % 16 == 0 && aligned16(a.p);
-    };
-    vec = lanes(pg) && lanes(px) && lanes(po);
+    vec = pg.st == 1 && px.st == 1 && po.st == 1;
     // few (sequence, channel) pairs of several chunks: four waves for each
     NW = p.num_pairs < 8192 && total_T / (batch ? batch : 1) >= 2 * kChunkTokens ? 4 : 1;
     grid = cdiv(p.num_pairs, 4 / NW);

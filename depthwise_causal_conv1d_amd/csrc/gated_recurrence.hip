@@ -26,10 +26,17 @@ struct RecFwdParams {
   int32_t batch, dim, pad_slot_id;
 };
 
+// The checkpoint row of sequence b's token start + rel (rel a multiple of
+// 64): rows of later sequences lie behind it, since a sequence of L tokens has
+// ceil(L / 64) of them and ends less than 64 ceil(L / 64) after its start.
+__device__ __forceinline__ int64_t mark_row(int64_t start, int b, int64_t rel) {
+  return start / kMarkTokens + b + rel / kMarkTokens;
+}
+
 // ---------------------------------------------------------------- tokens in lanes
 
-// A wave takes a chunk of 512 tokens of one channel, lane l the tokens
-// [8 l, 8 l + 8) of it, on the grid of absolute multiples of 512.  The
+// A wave takes a chunk of 512 tokens of one channel, counted from the
+// sequence's start, lane l the tokens [8 l, 8 l + 8) of it.  The
 // recurrence is a composition of maps h -> a h + u: a lane composes its
 // eight, the wave its lanes (six DPP steps), and NW waves that walk one
 // sequence together exchange their chunks' maps through LDS, so that no
@@ -44,7 +51,7 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_fwd_kernel(const R
   __shared__ float2 maps[2][kPairs][NW];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int sub = wave % NW, mine = wave / NW;
-  int64_t pair = (int64_t)xcd_contiguous(blockIdx.x, gridDim.x) * kPairs + mine;
+  const int64_t pair = (int64_t)xcd_groups<8>(blockIdx.x, gridDim.x) * kPairs + mine;
   if (pair >= p.num_pairs) return;  // NW waves of one pair leave together
   const int b = (int)(pair / p.dim), c = (int)(pair - (int64_t)b * p.dim);
   const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
@@ -66,7 +73,7 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_fwd_kernel(const R
       rg.template load<VEC>(gx, p.gx_st, t, p.total_T);
     }
   };
-  const int64_t first = start / kChunkTokens * kChunkTokens + sub * kChunkTokens;
+  const int64_t first = start + sub * kChunkTokens;
   if (end > start) fetch(first);
   int turn = 0;
   for (int64_t base = first; base - sub * kChunkTokens < end; base += NW * kChunkTokens, turn ^= 1) {
@@ -85,10 +92,10 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_fwd_kernel(const R
         a[e] = g.a;
         u[e] = g.m * (g.i * xf[e]);
       }
-      if (base < start || base + kChunkTokens > end) {
+      if (base + kChunkTokens > end) {
 #pragma unroll
         for (int e = 0; e < kLaneTokens; ++e) {
-          const bool in = t + e >= start && t + e < end;
+          const bool in = t + e < end;
           a[e] = in ? a[e] : 1.f;
           u[e] = in ? u[e] : 0.f;
         }
@@ -116,8 +123,8 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_fwd_kernel(const R
     }
     if (!any) continue;
     h = __builtin_fmaf(lane_move<0x138>(1.0f, P), h, lane_move<0x138>(0.0f, H));
-    if (p.marks && lane % (kMarkTokens / kLaneTokens) == 0 && t + kMarkTokens > start && t < end)
-      p.marks[(t / kMarkTokens + b) * p.dim + c] = h;
+    if (p.marks && lane % (kMarkTokens / kLaneTokens) == 0 && t < end)
+      p.marks[mark_row(start, b, t - start) * p.dim + c] = h;
 #pragma unroll
     for (int e = 0; e < kLaneTokens; ++e) {
       h = __builtin_fmaf(a[e], h, u[e]);
@@ -125,7 +132,7 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_fwd_kernel(const R
     }
     Raw8<D> o;
     o.from_float(u);
-    o.template store<VEC>(out, p.o_st, t, start, end);
+    o.template store<VEC>(out, p.o_st, t, end);
   }
   if (p.states && sub == 0 && lane == 0) p.states[slot * p.ss_slot + c] = carry;
 }
@@ -146,7 +153,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void rec_fwd_rows_kernel(const RecF
   __shared__ Map maps[2][NW][64];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
-  const uint32_t wg = xcd_contiguous(blockIdx.x, gridDim.x);
+  const uint32_t wg = blockIdx.x;
   const int b = (int)(wg / slabs), slab = (int)(wg % slabs);
   const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
   if (slot == p.pad_slot_id) return;
@@ -171,15 +178,14 @@ __global__ __launch_bounds__(kRowWaves * 64) void rec_fwd_rows_kernel(const RecF
   auto fetch = [&](int64_t row0) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      // outside the sequence: the nearest row inside it, unused
-      int64_t row = row0 + r < start ? start : row0 + r;
-      row = row < end ? row : end - 1;
+      // past the sequence: its last row, unused
+      const int64_t row = row0 + r < end ? row0 + r : end - 1;
       rx[r].load_nt(x + row * p.x_st);
       ra[r].load_nt(ga + row * p.ga_st);
       rg[r].load_nt(gx + row * p.gx_st);
     }
   };
-  int64_t base = start / kTile * kTile;
+  int64_t base = start;
   if (end > start) fetch(base + wave * R);
   for (int turn = 0; base < end; base += kTile, turn ^= 1) {
     const int64_t row0 = base + wave * R;
@@ -190,14 +196,13 @@ __global__ __launch_bounds__(kRowWaves * 64) void rec_fwd_rows_kernel(const RecF
       m.P[v] = 1.f;
       m.H[v] = 0.f;
     }
-    const bool whole = row0 >= start && row0 + R <= end;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float xf[V], af[V], gf[V];
       rx[r].to_float(xf);
       ra[r].to_float(af);
       rg[r].to_float(gf);
-      const bool in = whole || (row0 + r >= start && row0 + r < end);
+      const bool in = row0 + r < end;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Gates g = make_gates(af[v], gf[v], d[v]);
@@ -210,9 +215,9 @@ __global__ __launch_bounds__(kRowWaves * 64) void rec_fwd_rows_kernel(const RecF
     }
     if (base + kTile < end) fetch(row0 + kTile);
     maps[turn][wave][lane] = m;
-    if (p.marks && wave == 0 && live && base % kMarkTokens == 0) {
+    if (p.marks && wave == 0 && live) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) p.marks[(base / kMarkTokens + b) * p.dim + c + v] = carry[v];
+      for (int v = 0; v < V; ++v) p.marks[mark_row(start, b, base - start) * p.dim + c + v] = carry[v];
     }
     __syncthreads();
     float h[V];
@@ -232,7 +237,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void rec_fwd_rows_kernel(const RecF
       for (int v = 0; v < V; ++v) y[v] = __builtin_fmaf(pl[r][v], h[v], hl[r][v]);
       P_ o;
       o.from_float(y);
-      if (live && row0 + r >= start && row0 + r < end) o.store_nt(out + (row0 + r) * p.o_st);
+      if (live && row0 + r < end) o.store_nt(out + (row0 + r) * p.o_st);
     }
   }
   if (p.states && wave == 0 && live) {
@@ -274,7 +279,9 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_bwd_kernel(const R
   __shared__ float2 maps[2][kPairs][NW];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int sub = wave % NW, mine = wave / NW;
-  const int64_t pair = (int64_t)xcd_contiguous(blockIdx.x, gridDim.x) * kPairs + mine;
+  const int64_t pair = (int64_t)
+      xcd_groups<8>(blockIdx.x, gridDim.x)
+      * kPairs + mine;
   if (pair >= p.num_pairs) return;
   const int b = (int)(pair / p.dim), c = (int)(pair - (int64_t)b * p.dim);
   const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
@@ -292,33 +299,27 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_bwd_kernel(const R
   S* dx = static_cast<S*>(p.dx) + c * p.dx_sc;
   S* dga = static_cast<S*>(p.dga) + c * p.dga_sc;
   S* dgx = static_cast<S*>(p.dgx) + c * p.dgx_sc;
-  const int64_t first_mark = start / kMarkTokens;
-
   Raw8<D> rd, rx, ra, rg;
   float mark = 0.f;
   const int back = (63 - lane) * kLaneTokens;
   auto fetch = [&](int64_t base) {
     const int64_t t = base + back;
-    if (base >= 0 && base + kChunkTokens > start) {
+    if (base >= start) {
       rd.template load<VEC>(dout, p.do_st, t, p.total_T);
       rx.template load<VEC>(x, p.x_st, t, p.total_T);
       ra.template load<VEC>(ga, p.ga_st, t, p.total_T);
       rg.template load<VEC>(gx, p.gx_st, t, p.total_T);
-      // the row's first 64-token block that the sequence reaches
-      int64_t blk = t / 128 * (128 / kMarkTokens);
-      blk = blk < first_mark ? first_mark : blk;
-      const bool reached = t / 128 * 128 + 128 > start && blk * kMarkTokens < end;
-      mark = reached ? p.marks[(blk + b) * p.dim + c] : 0.f;
+      const int64_t row = (t - start) / 128 * 128;  // the first token of the row of lanes
+      mark = start + row < end ? p.marks[mark_row(start, b, row) * p.dim + c] : 0.f;
     }
   };
   float acc = 0.f;
-  const int64_t top = (end - 1) / kChunkTokens * kChunkTokens;  // the last chunk
+  const int64_t top = start + (end - 1 - start) / kChunkTokens * kChunkTokens;  // the last chunk
   if (end > start) fetch(top - sub * kChunkTokens);
   int turn = 0;
-  for (int64_t high = top; end > start && high + kChunkTokens > start;
-       high -= NW * kChunkTokens, turn ^= 1) {
+  for (int64_t high = top; end > start && high >= start; high -= NW * kChunkTokens, turn ^= 1) {
     const int64_t base = high - sub * kChunkTokens, t = base + back;
-    const bool any = base >= 0 && base + kChunkTokens > start;
+    const bool any = base >= start;
     float g[kLaneTokens], xf[kLaneTokens], a[kLaneTokens], r[kLaneTokens], i[kLaneTokens];
     float m[kLaneTokens], over[kLaneTokens];  // over: a i x / m
     float P = 1.f, H = 0.f, T = 0.f;
@@ -328,10 +329,10 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_bwd_kernel(const R
       ra.to_float(r);
       rg.to_float(i);
       const float h0 = mark;
-      if (base < start || base + kChunkTokens > end) {
+      if (base + kChunkTokens > end) {
 #pragma unroll
         for (int e = 0; e < kLaneTokens; ++e) {
-          const bool in = t + e >= start && t + e < end;
+          const bool in = t + e < end;
           g[e] = in ? g[e] : 0.f;
           xf[e] = in ? xf[e] : 0.f;
           r[e] = in ? r[e] : -INFINITY;  // r = 0: a = 1, u = 0, no part in a sum
@@ -395,11 +396,11 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_bwd_kernel(const R
     }
     Raw8<D> o;
     o.from_float(g);
-    o.template store<VEC>(dx, p.dx_st, t, start, end);
+    o.template store<VEC>(dx, p.dx_st, t, end);
     o.from_float(i);
-    o.template store<VEC>(dgx, p.dgx_st, t, start, end);
+    o.template store<VEC>(dgx, p.dgx_st, t, end);
     o.from_float(r);
-    o.template store<VEC>(dga, p.dga_st, t, start, end);
+    o.template store<VEC>(dga, p.dga_st, t, end);
   }
 #pragma unroll
   for (int w = 32; w > 0; w >>= 1) acc += __shfl_xor(acc, w, 64);
@@ -432,7 +433,7 @@ __global__ __launch_bounds__(kRowBwdWaves * 64) void rec_bwd_rows_kernel(const R
   __shared__ float mp[2][NW][V][64], mh[2][NW][V][64], mt[2][NW][V][64];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
-  const uint32_t wg = xcd_contiguous(blockIdx.x, gridDim.x);
+  const uint32_t wg = blockIdx.x;
   const int b = (int)(wg / slabs), slab = (int)(wg % slabs);
   const int ch = (slab * 64 + lane) * V;
   const bool live = ch < p.dim;
@@ -466,21 +467,19 @@ __global__ __launch_bounds__(kRowBwdWaves * 64) void rec_bwd_rows_kernel(const R
     const int64_t row0 = base + (NW - 1 - wave) * R;
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      int64_t row = row0 + q < start ? start : row0 + q;
-      row = row < end ? row : end - 1;
+      const int64_t row = row0 + q < end ? row0 + q : end - 1;
       rd[q].load_nt(dout + row * p.do_st);
       rx[q].load_nt(x + row * p.x_st);
       ra[q].load_nt(ga + row * p.ga_st);
       rg[q].load_nt(gx + row * p.gx_st);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) mark[v] = p.marks[(base / kMarkTokens + b) * p.dim + c + v];
+    for (int v = 0; v < V; ++v) mark[v] = p.marks[mark_row(start, b, base - start) * p.dim + c + v];
   };
-  int64_t base = (end - 1) / kTile * kTile;
+  int64_t base = start + (end - 1 - start) / kTile * kTile;
   if (end > start) fetch(base);
-  for (int turn = 0; end > start && base + kTile > start; base -= kTile, turn ^= 1) {
+  for (int turn = 0; end > start && base >= start; base -= kTile, turn ^= 1) {
     const int64_t row0 = base + (NW - 1 - wave) * R;
-    const bool whole = row0 >= start && row0 + R <= end;
     float g[R][V], xf[R][V], a[R][V], r[R][V], i[R][V], m[R][V], over[R][V];
     float P[V], H[V], T[V], h[V];
 #pragma unroll
@@ -495,7 +494,7 @@ __global__ __launch_bounds__(kRowBwdWaves * 64) void rec_bwd_rows_kernel(const R
       rx[q].to_float(xf[q]);
       ra[q].to_float(r[q]);
       rg[q].to_float(i[q]);
-      const bool in = whole || (row0 + q >= start && row0 + q < end);
+      const bool in = row0 + q < end;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         g[q][v] = in ? g[q][v] : 0.f;
@@ -553,7 +552,7 @@ __global__ __launch_bounds__(kRowBwdWaves * 64) void rec_bwd_rows_kernel(const R
         og[v] = ox[v] * xf[q][v] * (1.f - i[q][v]);
         oa[v] = -d[v].k * dlog * (r[q][v] * (1.f - r[q][v]));
       }
-      if (live && row0 + q >= start && row0 + q < end) {
+      if (live && row0 + q < end) {
         const int64_t row = row0 + q;
         P_ o;
         o.from_float(ox);
@@ -665,10 +664,10 @@ static bool row_lanes(std::initializer_list<Plane> planes, int64_t V) {
   return true;
 }
 
-// Vector lanes of eight tokens: tokens side by side, rows 16-byte aligned.
+// Vector lanes of eight tokens: tokens side by side, at any alignment.
 static bool token_lanes(std::initializer_list<Plane> planes) {
   for (const Plane& a : planes)
-    if (a.st != 1 || (a.sc * a.es) % 16 != 0 || !aligned16(a.p)) return false;
+    if (a.st != 1) return false;
   return true;
 }
 

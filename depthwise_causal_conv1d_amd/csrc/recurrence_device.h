@@ -24,9 +24,24 @@ struct Decay {
   float k_log2;  // the same in powers of two
 };
 
+// softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) <= 1, to a few ulp.
+// log1p(e) = 2 artanh(z), z = e / (2 + e) <= 1/3, by its power series.  The
+// product |v| log2 e is carried in two parts, or exp would lose |v| / 2 ulp.
 __device__ __forceinline__ Decay make_decay(float decay, float scale) {
-  // softplus; past 20 it equals its argument in fp32
-  const float sp = decay > 20.f ? decay : log1pf(expf(decay));
+  const float v = -__builtin_fabsf(decay);
+  const float t = v * kLog2e;
+  const float rest = __builtin_fmaf(v, kLog2e, -t) + v * 1.92596299e-8f;  // log2 e - kLog2e
+  float e = __builtin_amdgcn_exp2f(t);
+  e = __builtin_fmaf(e, rest * 0.693147181f, e);
+  const float z = e * __builtin_amdgcn_rcpf(2.0f + e), w = z * z;
+  float s = 1.0f / 13;
+  s = __builtin_fmaf(s, w, 1.0f / 11);
+  s = __builtin_fmaf(s, w, 1.0f / 9);
+  s = __builtin_fmaf(s, w, 1.0f / 7);
+  s = __builtin_fmaf(s, w, 1.0f / 5);
+  s = __builtin_fmaf(s, w, 1.0f / 3);
+  s = __builtin_fmaf(s, w, 1.0f);
+  const float sp = __builtin_fmaf(2.0f * z, s, decay > 0.f ? decay : 0.f);
   Decay d;
   d.k = scale * sp;
   d.k_log2 = d.k * kLog2e;
