@@ -35,6 +35,7 @@ EXPORTS = (
     "gather_intermediate_conv_window",
     "gather_intermediate_ssm_state",
     "gated_linear_recurrence_checkpoint_rows",
+    "gated_linear_recurrence_workspace",
     "gated_linear_recurrence_varlen_fwd",
     "gated_linear_recurrence_varlen_bwd",
     "gated_linear_recurrence_update",
@@ -103,9 +104,10 @@ _SIGS = {
     "gather_intermediate_conv_window": [P, I64, I32, I64, I64, P, P, I32, P, I64, I32, I32, P],
     "gather_intermediate_ssm_state": [P, I64, I64, I64, P, P, I32, P, I64, I32, P],
     "gated_linear_recurrence_checkpoint_rows": [I64, I32, PI64],
+    "gated_linear_recurrence_workspace": [I64, I32, I32, PI64, PI64],
     "gated_linear_recurrence_varlen_fwd": [P, I64, I64, P, I64, I64, P, I64, I64, P, FLT, P, I64,
-                                           I64, P, I32, P, P, P, I64, I64, P, I64, I32, I64, I32,
-                                           I32, P],
+                                           I64, P, I32, P, P, P, I64, I64, P, I64, P, I64, I32,
+                                           I64, I32, I32, P],
     "gated_linear_recurrence_varlen_bwd": [P, I64, I64, P, I64, I64, P, I64, I64, P, I64, I64, P,
                                            FLT, P, I64, P, I32, P, P, I64, P, I64, P, I64, P,
                                            I64, I64, P, I64, I64, P, I64, I64, P, P, I64, I32,

@@ -238,19 +238,6 @@ __global__ __launch_bounds__(256, 4) void conv_grad_kernel(const ConvGradParams 
 // sequences' lengths: a wave takes every sequence that its strip meets.
 constexpr int kStripWaves = 4, kStripGroup = 8;
 
-// The first sequence that does not end before row lo.
-__device__ __forceinline__ int first_sequence(const int32_t* qsl, int32_t batch, int64_t lo) {
-  int n = 0;
-  for (int i0 = 0; i0 < batch; i0 += 64) {
-    const int i = i0 + (threadIdx.x & 63);
-    const bool done = i < batch && qsl[i + 1] < lo;
-    const int k = __popcll(__ballot(done));
-    n += k;
-    if (k < 64) break;
-  }
-  return n;
-}
-
 template <typename D, int V, int W>
 __global__ __launch_bounds__(kStripWaves * 64) void conv_grad_rows_kernel(const ConvGradParams p) {
   using S = typename D::storage;

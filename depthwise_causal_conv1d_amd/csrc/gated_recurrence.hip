@@ -5,11 +5,11 @@
 // The recurrence is the layer step behind the short conv: it takes the
 // conv's packing (query_start_loc), state slots and layouts.
 #include <initializer_list>
+#include <type_traits>
 
 #include "column_sum.h"
 #include "recurrence_device.h"
 #include "sconv_host.h"
-
 namespace sconv {
 
 struct RecFwdParams {
@@ -21,7 +21,30 @@ struct RecFwdParams {
   const uint8_t* has_init;
   void* out;
   float* marks;
+  float *maps, *saved;  // segments: [segments, dim, 2] and [segments, dim]
   int64_t x_sc, x_st, ga_sc, ga_st, gx_sc, gx_st, o_sc, o_st, ss_slot, total_T, num_pairs;
+  int32_t seg_rows;  // rows of a segment
+  int32_t sorted;    // the longest sequences first
+  uint32_t pad_lds;  // unused LDS of a workgroup (host: fewer on a CU)
+  float scale;
+  int32_t batch, dim, pad_slot_id;
+};
+
+struct RecBwdParams {
+  const void *dout, *x, *ga, *gx;
+  const float *decay, *marks;
+  const int32_t* qsl;
+  const int32_t* cache_indices;
+  const uint8_t* has_init;
+  const float* dfinal;
+  float* dinitial;
+  void *dx, *dga, *dgx;
+  float* partial;  // [batch or segments, dim] sums over tokens of r * dlog a
+  float *maps, *saved;  // as the forward's
+  int64_t do_sc, do_st, x_sc, x_st, ga_sc, ga_st, gx_sc, gx_st;
+  int64_t dx_sc, dx_st, dga_sc, dga_st, dgx_sc, dgx_st;
+  int64_t df_slot, di_slot, total_T, num_pairs;
+  int32_t seg_rows, sorted;
   float scale;
   int32_t batch, dim, pad_slot_id;
 };
@@ -41,11 +64,11 @@ __device__ __forceinline__ int64_t mark_row(int64_t start, int b, int64_t rel) {
 // eight, the wave its lanes (six DPP steps), and NW waves that walk one
 // sequence together exchange their chunks' maps through LDS, so that no
 // state ever waits for another workgroup and every input is read once.
-// Tokens outside the sequence are the identity (a = 1, u = 0).
+// Tokens past the sequence are the identity (a = 1, u = 0).
 template <typename D, bool VEC, int NW>
 __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_fwd_kernel(const RecFwdParams p) {
   using S = typename D::storage;
-  constexpr int kWaves = NW > 4 ? NW : 4;
+  constexpr int N = kLaneTokens, kWaves = NW > 4 ? NW : 4;
   constexpr int kPairs = kWaves / NW;  // (sequence, channel) pairs of a workgroup
   static_assert(kPairs == 1 || NW == 1, "a barrier is met by one pair only");
   __shared__ float2 maps[2][kPairs][NW];
@@ -66,7 +89,7 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_fwd_kernel(const R
 
   Raw8<D> rx, ra, rg;
   auto fetch = [&](int64_t base) {
-    const int64_t t = base + lane * kLaneTokens;
+    const int64_t t = base + lane * N;
     if (base < end) {
       rx.template load<VEC>(x, p.x_st, t, p.total_T);
       ra.template load<VEC>(ga, p.ga_st, t, p.total_T);
@@ -77,35 +100,28 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_fwd_kernel(const R
   if (end > start) fetch(first);
   int turn = 0;
   for (int64_t base = first; base - sub * kChunkTokens < end; base += NW * kChunkTokens, turn ^= 1) {
-    const int64_t t = base + lane * kLaneTokens;
-    float a[kLaneTokens], u[kLaneTokens];
+    const int64_t t = base + lane * N;
+    float a[N], u[N];
     float P = 1.f, H = 0.f;
     const bool any = base < end;
     if (any) {
-      float xf[kLaneTokens], gf[kLaneTokens];
-      rx.to_float(xf);
-      ra.to_float(a);
-      rg.to_float(gf);
+      // the last chunk: this lane's tokens from `n` on are not the sequence's
+      const int n = t + N <= end ? N : t < end ? (int)(end - t) : 0;
+      auto gates = [&](auto edge) {
 #pragma unroll
-      for (int e = 0; e < kLaneTokens; ++e) {
-        const Gates g = make_gates(a[e], gf[e], d);
-        a[e] = g.a;
-        u[e] = g.m * (g.i * xf[e]);
-      }
-      if (base + kChunkTokens > end) {
-#pragma unroll
-        for (int e = 0; e < kLaneTokens; ++e) {
-          const bool in = t + e < end;
-          a[e] = in ? a[e] : 1.f;
-          u[e] = in ? u[e] : 0.f;
+        for (int e = 0; e < N; ++e) {
+          const Gates g = make_gates(ra.get(e), rg.get(e), d);
+          const bool in = !decltype(edge)::value || e < n;
+          a[e] = in ? g.a : 1.f;
+          u[e] = in ? g.m * (g.i * rx.get(e)) : 0.f;
+          H = __builtin_fmaf(a[e], H, u[e]);
+          P *= a[e];
         }
-      }
+      };
+      if (base + kChunkTokens <= end) gates(std::false_type());
+      else gates(std::true_type());
+      in_order();
       fetch(base + NW * kChunkTokens);
-#pragma unroll
-      for (int e = 0; e < kLaneTokens; ++e) {
-        H = __builtin_fmaf(a[e], H, u[e]);
-        P *= a[e];
-      }
       scan_wave_up(P, H);
     }
     float h = carry;
@@ -123,10 +139,10 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_fwd_kernel(const R
     }
     if (!any) continue;
     h = __builtin_fmaf(lane_move<0x138>(1.0f, P), h, lane_move<0x138>(0.0f, H));
-    if (p.marks && lane % (kMarkTokens / kLaneTokens) == 0 && t < end)
+    if (p.marks && lane % (kMarkTokens / N) == 0 && t < end)
       p.marks[mark_row(start, b, t - start) * p.dim + c] = h;
 #pragma unroll
-    for (int e = 0; e < kLaneTokens; ++e) {
+    for (int e = 0; e < N; ++e) {
       h = __builtin_fmaf(a[e], h, u[e]);
       u[e] = h;
     }
@@ -137,151 +153,22 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_fwd_kernel(const R
   if (p.states && sub == 0 && lane == 0) p.states[slot * p.ss_slot + c] = carry;
 }
 
-// ---------------------------------------------------------------- channels in lanes
-
-// For channels that lie side by side (rows of tokens): lane l takes V
-// channels, wave w of a workgroup the rows [R w, R w + R) of each tile of
-// NW * R tokens, and the tile's maps meet in LDS as above.
-constexpr int kRowWaves = 8, kRowTokens = 8;
-
-template <typename D, int V>
-__global__ __launch_bounds__(kRowWaves * 64) void rec_fwd_rows_kernel(const RecFwdParams p) {
-  using S = typename D::storage;
-  using P_ = Pack<D, V>;
-  constexpr int R = kRowTokens, NW = kRowWaves, kTile = R * NW;
-  struct alignas(8 * V) Map { float P[V], H[V]; };
-  __shared__ Map maps[2][NW][64];
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
-  const uint32_t wg = blockIdx.x;
-  const int b = (int)(wg / slabs), slab = (int)(wg % slabs);
-  const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
-  if (slot == p.pad_slot_id) return;
-  const int64_t start = p.qsl[b], end = p.qsl[b + 1];
-  // lanes past the last channel read it and write nothing
-  const int ch = (slab * 64 + lane) * V;
-  const bool live = ch < p.dim;
-  const int c = live ? ch : p.dim - V;
-  const S* x = static_cast<const S*>(p.x) + c;  // may be out
-  const S* ga = static_cast<const S*>(p.ga) + c;
-  const S* gx = static_cast<const S*>(p.gx) + c;
-  S* out = static_cast<S*>(p.out) + c;
-  Decay d[V];
-  float carry[V];
-  const bool init = p.has_init && p.has_init[b] != 0;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    d[v] = make_decay(p.decay[c + v], p.scale);
-    carry[v] = init ? p.states[slot * p.ss_slot + c + v] : 0.f;
-  }
-  P_ rx[R], ra[R], rg[R];
-  auto fetch = [&](int64_t row0) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      // past the sequence: its last row, unused
-      const int64_t row = row0 + r < end ? row0 + r : end - 1;
-      rx[r].load_nt(x + row * p.x_st);
-      ra[r].load_nt(ga + row * p.ga_st);
-      rg[r].load_nt(gx + row * p.gx_st);
-    }
-  };
-  int64_t base = start;
-  if (end > start) fetch(base + wave * R);
-  for (int turn = 0; base < end; base += kTile, turn ^= 1) {
-    const int64_t row0 = base + wave * R;
-    float pl[R][V], hl[R][V];
-    Map m;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      m.P[v] = 1.f;
-      m.H[v] = 0.f;
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float xf[V], af[V], gf[V];
-      rx[r].to_float(xf);
-      ra[r].to_float(af);
-      rg[r].to_float(gf);
-      const bool in = row0 + r < end;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Gates g = make_gates(af[v], gf[v], d[v]);
-        const float a = in ? g.a : 1.f, u = in ? g.m * (g.i * xf[v]) : 0.f;
-        m.H[v] = __builtin_fmaf(a, m.H[v], u);
-        m.P[v] *= a;
-        pl[r][v] = m.P[v];
-        hl[r][v] = m.H[v];
-      }
-    }
-    if (base + kTile < end) fetch(row0 + kTile);
-    maps[turn][wave][lane] = m;
-    if (p.marks && wave == 0 && live) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.marks[mark_row(start, b, base - start) * p.dim + c + v] = carry[v];
-    }
-    __syncthreads();
-    float h[V];
-#pragma unroll
-    for (int q = 0; q < NW; ++q) {
-      const Map f = maps[turn][q][lane];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (q == wave) h[v] = carry[v];
-        carry[v] = __builtin_fmaf(f.P[v], carry[v], f.H[v]);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float y[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) y[v] = __builtin_fmaf(pl[r][v], h[v], hl[r][v]);
-      P_ o;
-      o.from_float(y);
-      if (live && row0 + r < end) o.store_nt(out + (row0 + r) * p.o_st);
-    }
-  }
-  if (p.states && wave == 0 && live) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) p.states[slot * p.ss_slot + c + v] = carry[v];
-  }
-}
-
-// ---------------------------------------------------------------- gradients
-
-struct RecBwdParams {
-  const void *dout, *x, *ga, *gx;
-  const float *decay, *marks;
-  const int32_t* qsl;
-  const int32_t* cache_indices;
-  const uint8_t* has_init;
-  const float* dfinal;
-  float* dinitial;
-  void *dx, *dga, *dgx;
-  float* partial;  // [batch, dim] sums over tokens of r * dlog a
-  int64_t do_sc, do_st, x_sc, x_st, ga_sc, ga_st, gx_sc, gx_st;
-  int64_t dx_sc, dx_st, dga_sc, dga_st, dgx_sc, dgx_st;
-  int64_t df_slot, di_slot, total_T, num_pairs;
-  float scale;
-  int32_t batch, dim, pad_slot_id;
-};
-
-// Tokens in lanes, from the end of the sequence: lane l of a chunk takes
-// tokens [8 (63 - l), 8 (63 - l) + 8), so that the gradient of the state,
-// which runs against time, runs up the lanes.  The states come from the
-// checkpoints: each row of 16 lanes (128 tokens) starts from its own, and
-// only composes inside the row.  The gates are computed once per token.
+// The gradients, tokens in lanes, from the end of the sequence: lane l of a
+// chunk takes tokens [8 (63 - l), 8 (63 - l) + 8), so that the gradient of
+// the state, which runs against time, runs up the lanes.  The states come
+// from the checkpoints: each row of 16 lanes (128 tokens) starts from its
+// own, and only composes inside the row.  The gates are computed once.
 template <typename D, bool VEC, int NW>
-__global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_bwd_kernel(const RecBwdParams p) {
+__global__ __launch_bounds__(NW > 4 ? NW * 64 : 256, VEC && NW == 1 && sizeof(typename D::storage) == 2 ? 4 : 1)
+void rec_bwd_kernel(const RecBwdParams p) {
   using S = typename D::storage;
-  constexpr int kWaves = NW > 4 ? NW : 4;
+  constexpr int N = kLaneTokens, kWaves = NW > 4 ? NW : 4;
   constexpr int kPairs = kWaves / NW;
   static_assert(kPairs == 1 || NW == 1, "a barrier is met by one pair only");
   __shared__ float2 maps[2][kPairs][NW];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int sub = wave % NW, mine = wave / NW;
-  const int64_t pair = (int64_t)
-      xcd_groups<8>(blockIdx.x, gridDim.x)
-      * kPairs + mine;
+  const int64_t pair = (int64_t)xcd_groups<8>(blockIdx.x, gridDim.x) * kPairs + mine;
   if (pair >= p.num_pairs) return;
   const int b = (int)(pair / p.dim), c = (int)(pair - (int64_t)b * p.dim);
   const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
@@ -299,9 +186,10 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_bwd_kernel(const R
   S* dx = static_cast<S*>(p.dx) + c * p.dx_sc;
   S* dga = static_cast<S*>(p.dga) + c * p.dga_sc;
   S* dgx = static_cast<S*>(p.dgx) + c * p.dgx_sc;
+
   Raw8<D> rd, rx, ra, rg;
   float mark = 0.f;
-  const int back = (63 - lane) * kLaneTokens;
+  const int back = (63 - lane) * N;
   auto fetch = [&](int64_t base) {
     const int64_t t = base + back;
     if (base >= start) {
@@ -320,51 +208,46 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_bwd_kernel(const R
   for (int64_t high = top; end > start && high >= start; high -= NW * kChunkTokens, turn ^= 1) {
     const int64_t base = high - sub * kChunkTokens, t = base + back;
     const bool any = base >= start;
-    float g[kLaneTokens], xf[kLaneTokens], a[kLaneTokens], r[kLaneTokens], i[kLaneTokens];
-    float m[kLaneTokens], over[kLaneTokens];  // over: a i x / m
-    float P = 1.f, H = 0.f, T = 0.f;
+    float g[N], xf[N], a[N], r[N], i[N], m[N], over[N];  // over: a i x / m
+    float P = 1.f, H = 0.f, T = 0.f, h0 = 0.f;
     if (any) {
-      rd.to_float(g);
-      rx.to_float(xf);
-      ra.to_float(r);
-      rg.to_float(i);
-      const float h0 = mark;
-      if (base + kChunkTokens > end) {
+      const int n = t + N <= end ? N : t < end ? (int)(end - t) : 0;
+      h0 = mark;
+      auto gates = [&](auto edge) {
 #pragma unroll
-        for (int e = 0; e < kLaneTokens; ++e) {
-          const bool in = t + e < end;
-          g[e] = in ? g[e] : 0.f;
-          xf[e] = in ? xf[e] : 0.f;
-          r[e] = in ? r[e] : -INFINITY;  // r = 0: a = 1, u = 0, no part in a sum
-          i[e] = in ? i[e] : 0.f;
+        for (int e = 0; e < N; ++e) {
+          const bool in = !decltype(edge)::value || e < n;
+          g[e] = in ? rd.get(e) : 0.f;
+          xf[e] = in ? rx.get(e) : 0.f;
+          // r = 0 past the end: a = 1, u = 0, no part in a sum
+          const GatesInv q = make_gates_inv(in ? ra.get(e) : -INFINITY, in ? rg.get(e) : 0.f, d);
+          const float ix = q.i * xf[e];
+          r[e] = q.r;
+          i[e] = q.i;
+          a[e] = q.a;
+          m[e] = q.m;
+          over[e] = q.a * q.inv_m * ix;
+          H = __builtin_fmaf(q.a, H, q.m * ix);
+          P *= q.a;
         }
-      }
-#pragma unroll
-      for (int e = 0; e < kLaneTokens; ++e) {
-        const GatesInv q = make_gates_inv(r[e], i[e], d);
-        const float ix = q.i * xf[e];
-        r[e] = q.r;
-        i[e] = q.i;
-        a[e] = q.a;
-        m[e] = q.m;
-        over[e] = q.a * q.inv_m * ix;
-        H = __builtin_fmaf(q.a, H, q.m * ix);
-        P *= q.a;
-      }
+      };
+      if (base + kChunkTokens <= end) gates(std::false_type());
+      else gates(std::true_type());
+      in_order();
       fetch(base - NW * kChunkTokens);
       // states before each token, less a i x / m
-      float A = P;
+      const float A = P;
       scan_row_down(P, H);
       float h = __builtin_fmaf(lane_move<0x101>(1.0f, P), h0, lane_move<0x101>(0.0f, H));
 #pragma unroll
-      for (int e = 0; e < kLaneTokens; ++e) {
+      for (int e = 0; e < N; ++e) {
         const float next = __builtin_fmaf(a[e], h, m[e] * (i[e] * xf[e]));
         over[e] = h - over[e];
         h = next;
       }
       // s -> a (dout + s), from the last token to the first
 #pragma unroll
-      for (int e = kLaneTokens - 1; e >= 0; --e) T = a[e] * (T + g[e]);
+      for (int e = N - 1; e >= 0; --e) T = a[e] * (T + g[e]);
       P = A;
       scan_wave_up(P, T);
     }
@@ -384,7 +267,7 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_bwd_kernel(const R
     if (!any) continue;
     s = __builtin_fmaf(lane_move<0x138>(1.0f, P), s, lane_move<0x138>(0.0f, T));
 #pragma unroll
-    for (int e = kLaneTokens - 1; e >= 0; --e) {
+    for (int e = N - 1; e >= 0; --e) {
       const float dh = g[e] + s;
       s = a[e] * dh;
       const float vx = dh * (m[e] * i[e]);
@@ -419,165 +302,581 @@ __global__ __launch_bounds__(NW > 4 ? NW * 64 : 256) void rec_bwd_kernel(const R
   }
 }
 
-// Channels in lanes, from the end: wave w takes the rows of a tile of 64
-// tokens (one checkpoint) that are w * R from its end.  The forward maps and
-// the backward ones, which share their factor, meet in LDS together.
-constexpr int kRowBwdWaves = 16, kRowBwdTokens = 4;
+// ---------------------------------------------------------------- channels in lanes
 
-template <typename D, int V>
-__global__ __launch_bounds__(kRowBwdWaves * 64) void rec_bwd_rows_kernel(const RecBwdParams p) {
+// For channels that lie side by side (rows of tokens): lane l takes V
+// channels, wave w of a workgroup R rows of each tile of NW * R = 64 tokens
+// (counted from the sequence's start, so that a tile starts at a checkpoint),
+// and the tile's maps meet in LDS.
+//
+// A workgroup takes one sequence where they are many, and else (SEG) a
+// segment of rows of the flat token axis, whatever sequences it meets: the
+// tiles that start in it.  Then a launch before has composed each segment's
+// maps of the one sequence that goes on behind it, and a workgroup composes
+// the segments before its own; a sequence that starts in a segment has its
+// initial state folded into that map, so a composition starts from zero.
+// The inputs are read twice then (14 bytes an element in bf16, not 8).
+constexpr int kTile = kMarkTokens;
+
+// First token at or after row `at` that starts a tile of the sequence.
+__device__ __forceinline__ int tile_start(int start, int at) {
+  return at <= start ? start : start + (at - start + kTile - 1) / kTile * kTile;
+}
+
+// The part of a sequence whose tiles start in rows [lo, hi).
+struct Part {
+  int start, end, from, to;
+  __device__ __forceinline__ Part(const int32_t* qsl, int b, int lo, int hi) {
+    start = qsl[b];
+    end = qsl[b + 1];
+    from = tile_start(start, lo);
+    to = tile_start(start, hi);
+    to = to < end ? to : end;
+  }
+};
+
+// Composes the maps of segments [first, last) in steps of `by` (1 or -1)
+// from `first`, all waves of the workgroup together.
+template <int V, int NW, typename M>
+__device__ __forceinline__ void compose_segments(const float* seg_maps, int64_t dim, int c,
+                                                 int first, int count, int by, int lane,
+                                                 int wave, M (&maps)[NW][64], float (&h)[V]) {
+  const int per = (count + NW - 1) / NW;
+  const int j0 = wave * per, j1 = j0 + per < count ? j0 + per : count;
+  M m;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    m.P[v] = 1.f;
+    m.H[v] = 0.f;
+  }
+#pragma unroll 8
+  for (int j = j0; j < j1; ++j) {
+    const float* q = seg_maps + ((int64_t)(first + by * j) * dim + c) * 2;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      m.H[v] = __builtin_fmaf(q[2 * v], m.H[v], q[2 * v + 1]);
+      m.P[v] *= q[2 * v];
+    }
+  }
+  maps[wave][lane] = m;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const M f = maps[w][lane];
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(f.P[v], h[v], f.H[v]);
+  }
+  __syncthreads();
+}
+
+// A lane's vector of one row: a uniform row and a 32-bit byte offset, which
+// is what the addressing mode takes.
+template <typename S>
+__device__ __forceinline__ S* in_row(S* row, uint32_t bytes) {
+  typedef std::conditional_t<std::is_const_v<S>, const char, char> B;
+  return reinterpret_cast<S*>(reinterpret_cast<B*>(row) + bytes);
+}
+
+// Hides where a lane's byte offset comes from: a 64-bit copy made once ahead
+// of a loop would keep the addressing mode from taking the 32-bit one.
+__device__ __forceinline__ uint32_t lane_offset(uint32_t bytes) {
+  asm("" : "+v"(bytes));
+  return bytes;
+}
+
+// R rows [row0, row0 + R) of a plane, rows from `end` on read as row end - 1
+// (unused).  Ordinary loads: streaming ones cost 216 us where these take 154
+// (16 ragged sequences x 4096 bf16: 2-byte lanes), and read lines that two
+// workgroups share twice (8191 x 1001 fp32: 179 against 139 us).
+template <typename P, int R, typename S>
+__device__ __forceinline__ void load_rows(P (&v)[R], const S* plane, int64_t stride, int row0,
+                                          int end, uint32_t bytes) {
+  const int n = end - row0;
+  const S* q = plane + (n > 0 ? row0 : end - 1) * stride;
+  bytes = lane_offset(bytes);
+  // (No second path for whole tiles: a branch between a load and its use makes
+  // the loads wait where the paths meet, 217 against 154 us.)
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    v[r].load(in_row(q, bytes));
+    q += r + 1 < n ? stride : 0;
+  }
+}
+
+template <int V>
+struct alignas(8 * V) RowMap { float P[V], H[V]; };
+
+constexpr int kFwdWaves = 8;
+
+template <typename D, int V, bool SEG>
+__global__ __launch_bounds__(kFwdWaves * 64) void rec_fwd_rows_kernel(const RecFwdParams p) {
   using S = typename D::storage;
   using P_ = Pack<D, V>;
-  constexpr int R = kRowBwdTokens, NW = kRowBwdWaves, kTile = R * NW;
-  static_assert(kTile == kMarkTokens, "a tile starts at a checkpoint");
-  __shared__ float mp[2][NW][V][64], mh[2][NW][V][64], mt[2][NW][V][64];
+  constexpr int NW = kFwdWaves, R = kTile / NW;
+  __shared__ RowMap<V> maps[2][NW][64];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
-  const uint32_t wg = blockIdx.x;
-  const int b = (int)(wg / slabs), slab = (int)(wg % slabs);
-  const int ch = (slab * 64 + lane) * V;
+  const int unit = (int)(blockIdx.x / slabs);  // sequence or segment
+  // lanes past the last channel read it and write nothing
+  const int ch = (int)((blockIdx.x % slabs) * 64 + lane) * V;
   const bool live = ch < p.dim;
   const int c = live ? ch : p.dim - V;
-  const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
-  if (slot == p.pad_slot_id) {
-    if (wave == 0 && live) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.partial[(int64_t)b * p.dim + c + v] = 0.f;
-    }
-    return;
-  }
-  const int64_t start = p.qsl[b], end = p.qsl[b + 1];
-  const S* dout = static_cast<const S*>(p.dout) + c;
-  const S* x = static_cast<const S*>(p.x) + c;
-  const S* ga = static_cast<const S*>(p.ga) + c;
-  const S* gx = static_cast<const S*>(p.gx) + c;
-  S* dx = static_cast<S*>(p.dx) + c;
-  S* dga = static_cast<S*>(p.dga) + c;
-  S* dgx = static_cast<S*>(p.dgx) + c;
+  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(S);
+  const int total = (int)p.total_T, lo = SEG ? unit * p.seg_rows : 0;
+  const bool last = !SEG || total - lo <= p.seg_rows;
+  const int hi = last ? total : lo + p.seg_rows;
+  const S* x = static_cast<const S*>(p.x);  // may be out
+  const S* ga = static_cast<const S*>(p.ga);
+  const S* gx = static_cast<const S*>(p.gx);
+  S* out = static_cast<S*>(p.out);
   Decay d[V];
-  float carry[V], acc[V], mark[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) d[v] = make_decay(p.decay[c + v], p.scale);
+  int turn = 0;
+  const int b0 = SEG ? first_sequence(p.qsl, p.batch, lo) : p.sorted ? by_length(p.qsl, p.batch, (int)unit) : (int)unit;
+  const int b1 = SEG ? p.batch : b0 + 1;
+  for (int b = b0; b < b1; ++b) {
+    const Part s(p.qsl, b, lo, hi);
+    if (SEG && s.start >= hi && !last) break;
+    const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
+    const bool opens = s.start >= lo;  // its first token, or its place if it has none
+    if (slot == p.pad_slot_id || (s.from >= s.to && !(opens && s.start == s.end))) continue;
+    float carry[V];
+    if (!SEG || opens) {
+      const bool init = p.has_init && p.has_init[b] != 0;
+      // a sequence that goes on: its slot may hold its last state already
+      const float* from = SEG && s.to < s.end ? p.saved + (int64_t)unit * p.dim : p.states + slot * p.ss_slot;
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = init ? from[c + v] : 0.f;
+    } else {
+      const int first = s.start / p.seg_rows;
+      compose_segments<V, NW>(p.maps, p.dim, c, first, unit - first, 1, lane, wave, maps[turn], carry);
+    }
+    P_ rx[R], ra[R], rg[R];
+    auto fetch = [&](int row0) {
+      load_rows(rx, x, p.x_st, row0, s.end, off);
+      load_rows(ra, ga, p.ga_st, row0, s.end, off);
+      load_rows(rg, gx, p.gx_st, row0, s.end, off);
+    };
+    if (s.to > s.from) fetch(s.from + wave * R);
+    for (int base = s.from; base < s.to; base += kTile, turn ^= 1) {
+      const int row0 = base + wave * R;
+      float pl[R][V], hl[R][V];
+      RowMap<V> m;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        m.P[v] = 1.f;
+        m.H[v] = 0.f;
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float xf[V], af[V], gf[V];
+        rx[r].to_float(xf);
+        ra[r].to_float(af);
+        rg[r].to_float(gf);
+        const bool in = row0 + r < s.end;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const Gates g = make_gates(af[v], gf[v], d[v]);
+          const float a = in ? g.a : 1.f, u = in ? g.m * (g.i * xf[v]) : 0.f;
+          m.H[v] = __builtin_fmaf(a, m.H[v], u);
+          m.P[v] *= a;
+          pl[r][v] = m.P[v];
+          hl[r][v] = m.H[v];
+        }
+      }
+      maps[turn][wave][lane] = m;
+      if (base + kTile < s.to) fetch(row0 + kTile);
+      if (p.marks && wave == 0 && live) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          p.marks[mark_row(s.start, b, base - s.start) * p.dim + c + v] = carry[v];
+      }
+      __syncthreads();
+      float h[V];
+#pragma unroll
+      for (int q = 0; q < NW; ++q) {
+        const RowMap<V> f = maps[turn][q][lane];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (q == wave) h[v] = carry[v];
+          carry[v] = __builtin_fmaf(f.P[v], carry[v], f.H[v]);
+        }
+      }
+      const uint32_t at = lane_offset(off);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float y[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) y[v] = __builtin_fmaf(pl[r][v], h[v], hl[r][v]);
+        P_ o;
+        o.from_float(y);
+        if (live && row0 + r < s.end) o.store_nt(in_row(out + (int64_t)(row0 + r) * p.o_st, at));
+      }
+    }
+    if (p.states && s.to == s.end && wave == 0 && live) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.states[slot * p.ss_slot + c + v] = carry[v];
+    }
+  }
+}
+
+// Rows [from, to) cut into one run a wave, walked R rows at a time.
+constexpr int kMapWaves = 8, kMapRows = 8;
+
+// The map of the one sequence that goes on behind each segment, over its
+// tiles in the segment.
+template <typename D, int V>
+__global__ __launch_bounds__(kMapWaves * 64) void rec_fwd_map_kernel(const RecFwdParams p) {
+  using S = typename D::storage;
+  using P_ = Pack<D, V>;
+  constexpr int NW = kMapWaves, R = kMapRows;
+  __shared__ RowMap<V> maps[NW][64];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
+  const int unit = (int)(blockIdx.x / slabs), total = (int)p.total_T, lo = unit * p.seg_rows;
+  const int hi = total - lo <= p.seg_rows ? total : lo + p.seg_rows;
+  const int ch = (int)((blockIdx.x % slabs) * 64 + lane) * V;
+  const bool live = ch < p.dim;
+  const int c = live ? ch : p.dim - V;
+  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(S);
+  const int b = first_sequence(p.qsl, p.batch, hi + 1);  // the first that ends behind hi
+  if (b >= p.batch) return;
+  const Part s(p.qsl, b, lo, hi);
+  const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
+  if (s.start >= hi || s.to >= s.end || slot == p.pad_slot_id) return;
+  const S* x = static_cast<const S*>(p.x);
+  const S* ga = static_cast<const S*>(p.ga);
+  const S* gx = static_cast<const S*>(p.gx);
+  Decay d[V];
+  RowMap<V> m;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     d[v] = make_decay(p.decay[c + v], p.scale);
-    carry[v] = p.dfinal ? p.dfinal[slot * p.df_slot + c + v] : 0.f;
-    acc[v] = mark[v] = 0.f;
+    m.P[v] = 1.f;
+    m.H[v] = 0.f;
   }
-  P_ rd[R], rx[R], ra[R], rg[R];
-  auto fetch = [&](int64_t base) {
-    const int64_t row0 = base + (NW - 1 - wave) * R;
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const int64_t row = row0 + q < end ? row0 + q : end - 1;
-      rd[q].load_nt(dout + row * p.do_st);
-      rx[q].load_nt(x + row * p.x_st);
-      ra[q].load_nt(ga + row * p.ga_st);
-      rg[q].load_nt(gx + row * p.gx_st);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) mark[v] = p.marks[mark_row(start, b, base - start) * p.dim + c + v];
+  const int per = (s.to - s.from + NW - 1) / NW;
+  const int from = s.from + wave * per, to = from + per < s.to ? from + per : s.to;
+  P_ rx[R], ra[R], rg[R];
+  auto fetch = [&](int row0) {
+    load_rows(rx, x, p.x_st, row0, to, off);
+    load_rows(ra, ga, p.ga_st, row0, to, off);
+    load_rows(rg, gx, p.gx_st, row0, to, off);
   };
-  int64_t base = start + (end - 1 - start) / kTile * kTile;
-  if (end > start) fetch(base);
-  for (int turn = 0; end > start && base >= start; base -= kTile, turn ^= 1) {
-    const int64_t row0 = base + (NW - 1 - wave) * R;
-    float g[R][V], xf[R][V], a[R][V], r[R][V], i[R][V], m[R][V], over[R][V];
-    float P[V], H[V], T[V], h[V];
+  if (from < to) fetch(from);
+  for (int row0 = from; row0 < to; row0 += R) {
+    P_ cx[R], ca[R], cg[R];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      P[v] = 1.f;
-      H[v] = T[v] = 0.f;
-      h[v] = mark[v];
+    for (int r = 0; r < R; ++r) {
+      cx[r] = rx[r];
+      ca[r] = ra[r];
+      cg[r] = rg[r];
     }
+    if (row0 + R < to) fetch(row0 + R);
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      rd[q].to_float(g[q]);
-      rx[q].to_float(xf[q]);
-      ra[q].to_float(r[q]);
-      rg[q].to_float(i[q]);
-      const bool in = row0 + q < end;
+    for (int r = 0; r < R; ++r) {
+      float xf[V], af[V], gf[V];
+      cx[r].to_float(xf);
+      ca[r].to_float(af);
+      cg[r].to_float(gf);
+      const bool in = row0 + r < to;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        g[q][v] = in ? g[q][v] : 0.f;
-        xf[q][v] = in ? xf[q][v] : 0.f;
-        r[q][v] = in ? r[q][v] : -INFINITY;  // r = 0: a = 1, u = 0, no part in a sum
-        i[q][v] = in ? i[q][v] : 0.f;
-        const GatesInv f = make_gates_inv(r[q][v], i[q][v], d[v]);
-        const float ix = f.i * xf[q][v];
-        r[q][v] = f.r;
-        i[q][v] = f.i;
-        a[q][v] = f.a;
-        m[q][v] = f.m;
-        over[q][v] = f.a * f.inv_m * ix;
-        H[v] = __builtin_fmaf(f.a, H[v], f.m * ix);
-        P[v] *= f.a;
+        const Gates g = make_gates(af[v], gf[v], d[v]);
+        m.H[v] = __builtin_fmaf(in ? g.a : 1.f, m.H[v], in ? g.m * (g.i * xf[v]) : 0.f);
+        m.P[v] *= in ? g.a : 1.f;
       }
     }
-    if (base > start) fetch(base - kTile);
+  }
+  maps[wave][lane] = m;
+  __syncthreads();
+  if (wave != 0 || !live) return;
+  const bool opens = s.start >= lo, init = opens && p.has_init && p.has_init[b] != 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-#pragma unroll
-      for (int q = R - 1; q >= 0; --q) T[v] = a[q][v] * (T[v] + g[q][v]);
-      mp[turn][wave][v][lane] = P[v];
-      mh[turn][wave][v][lane] = H[v];
-      mt[turn][wave][v][lane] = T[v];
-    }
-    __syncthreads();
-    float s[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-#pragma unroll
-      for (int q = 0; q < NW; ++q) {
-        if (q == wave) s[v] = carry[v];
-        carry[v] = __builtin_fmaf(mp[turn][q][v][lane], carry[v], mt[turn][q][v][lane]);
-      }
-      for (int q = NW - 1; q > wave; --q)  // the rows before this wave's
-        h[v] = __builtin_fmaf(mp[turn][q][v][lane], h[v], mh[turn][q][v][lane]);
-#pragma unroll
-      for (int q = 0; q < R; ++q) {
-        const float next = __builtin_fmaf(a[q][v], h[v], m[q][v] * (i[q][v] * xf[q][v]));
-        over[q][v] = h[v] - over[q][v];
-        h[v] = next;
-      }
+  for (int v = 0; v < V; ++v) {
+    float P = 1.f, H = 0.f;
+    if (opens) {
+      P = 0.f;
+      H = init ? p.states[slot * p.ss_slot + c + v] : 0.f;
+      p.saved[(int64_t)unit * p.dim + c + v] = H;
     }
 #pragma unroll
-    for (int q = R - 1; q >= 0; --q) {
-      float ox[V], oa[V], og[V];
+    for (int w = 0; w < NW; ++w) {
+      H = __builtin_fmaf(maps[w][lane].P[v], H, maps[w][lane].H[v]);
+      P *= maps[w][lane].P[v];
+    }
+    p.maps[((int64_t)unit * p.dim + c + v) * 2] = P;
+    p.maps[((int64_t)unit * p.dim + c + v) * 2 + 1] = H;
+  }
+}
+
+// The gradients, from the end: wave w takes the R rows of a tile that are
+// w R from its end.  The forward maps and the backward ones, which share
+// their factor, meet in LDS together.
+constexpr int kBwdWaves = 8;
+
+template <typename D, int V, bool SEG>
+__global__ __launch_bounds__(kBwdWaves * 64) void rec_bwd_rows_kernel(const RecBwdParams p) {
+  using S = typename D::storage;
+  using P_ = Pack<D, V>;
+  constexpr int NW = kBwdWaves, R = kTile / NW;
+  __shared__ RowMap<V> maps[2][NW][64];  // s -> P s + H
+  __shared__ float mh[2][NW][V][64];     // h -> P h + mh
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
+  const int unit = (int)(blockIdx.x / slabs);
+  const int ch = (int)((blockIdx.x % slabs) * 64 + lane) * V;
+  const bool live = ch < p.dim;
+  const int c = live ? ch : p.dim - V;
+  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(S);
+  const int total = (int)p.total_T, lo = SEG ? unit * p.seg_rows : 0;
+  const bool last = !SEG || total - lo <= p.seg_rows;
+  const int hi = last ? total : lo + p.seg_rows;
+  const S* dout = static_cast<const S*>(p.dout);
+  const S* x = static_cast<const S*>(p.x);
+  const S* ga = static_cast<const S*>(p.ga);
+  const S* gx = static_cast<const S*>(p.gx);
+  S* dx = static_cast<S*>(p.dx);
+  S* dga = static_cast<S*>(p.dga);
+  S* dgx = static_cast<S*>(p.dgx);
+  Decay d[V];
+  float acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    d[v] = make_decay(p.decay[c + v], p.scale);
+    acc[v] = 0.f;
+  }
+  int turn = 0;
+  const int b0 = SEG ? first_sequence(p.qsl, p.batch, lo) : p.sorted ? by_length(p.qsl, p.batch, (int)unit) : (int)unit;
+  const int b1 = SEG ? p.batch : b0 + 1;
+  for (int b = b0; b < b1; ++b) {
+    const Part q(p.qsl, b, lo, hi);
+    if (SEG && q.start >= hi && !last) break;
+    const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
+    const bool opens = q.start >= lo;
+    if (slot == p.pad_slot_id || (q.from >= q.to && !(opens && q.start == q.end))) continue;
+    float carry[V];
+    if (!SEG || q.to == q.end) {
+      // a sequence that began before: dfinal's slot may hold its dinitial already
+      const float* from = SEG && !opens ? p.saved + (int64_t)unit * p.dim : p.dfinal + slot * p.df_slot;
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = p.dfinal ? from[c + v] : 0.f;
+    } else {
+      // from the segment of the last tile down to the next one
+      const int top = (q.start + (q.end - 1 - q.start) / kTile * kTile) / p.seg_rows;
+      compose_segments<V, NW>(p.maps, p.dim, c, top, top - unit, -1, lane, wave, maps[turn], carry);
+    }
+    P_ rd[R], rx[R], ra[R], rg[R];
+    float mark[V];
+    auto fetch = [&](int base) {
+      const int row0 = base + (NW - 1 - wave) * R;
+      load_rows(rd, dout, p.do_st, row0, q.end, off);
+      load_rows(rx, x, p.x_st, row0, q.end, off);
+      load_rows(ra, ga, p.ga_st, row0, q.end, off);
+      load_rows(rg, gx, p.gx_st, row0, q.end, off);
+#pragma unroll
+      for (int v = 0; v < V; ++v) mark[v] = p.marks[mark_row(q.start, b, base - q.start) * p.dim + c + v];
+    };
+    int base = q.start + (q.to - 1 - q.start) / kTile * kTile;
+    if (q.to > q.from) fetch(base);
+    for (; q.to > q.from && base >= q.from; base -= kTile, turn ^= 1) {
+      const int row0 = base + (NW - 1 - wave) * R;
+      float g[R][V], xf[R][V], a[R][V], r[R][V], i[R][V], m[R][V], over[R][V];
+      float P[V], H[V], T[V], h[V], s[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float dh = g[q][v] + s[v];
-        s[v] = a[q][v] * dh;
-        ox[v] = dh * (m[q][v] * i[q][v]);
-        const float dlog = s[v] * over[q][v];
-        acc[v] = __builtin_fmaf(dlog, r[q][v], acc[v]);
-        og[v] = ox[v] * xf[q][v] * (1.f - i[q][v]);
-        oa[v] = -d[v].k * dlog * (r[q][v] * (1.f - r[q][v]));
+        P[v] = 1.f;
+        H[v] = T[v] = 0.f;
+        h[v] = mark[v];
       }
-      if (live && row0 + q < end) {
-        const int64_t row = row0 + q;
-        P_ o;
-        o.from_float(ox);
-        o.store_nt(dx + row * p.dx_st);
-        o.from_float(og);
-        o.store_nt(dgx + row * p.dgx_st);
-        o.from_float(oa);
-        o.store_nt(dga + row * p.dga_st);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        rd[k].to_float(g[k]);
+        rx[k].to_float(xf[k]);
+        ra[k].to_float(r[k]);
+        rg[k].to_float(i[k]);
+        const bool in = row0 + k < q.end;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          g[k][v] = in ? g[k][v] : 0.f;
+          xf[k][v] = in ? xf[k][v] : 0.f;
+          // r = 0 past the end: a = 1, u = 0, no part in a sum
+          const GatesInv f = make_gates_inv(in ? r[k][v] : -INFINITY, in ? i[k][v] : 0.f, d[v]);
+          const float ix = f.i * xf[k][v];
+          r[k][v] = f.r;
+          i[k][v] = f.i;
+          a[k][v] = f.a;
+          m[k][v] = f.m;
+          over[k][v] = f.a * f.inv_m * ix;
+          H[v] = __builtin_fmaf(f.a, H[v], f.m * ix);
+          P[v] *= f.a;
+        }
       }
+      RowMap<V> f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int k = R - 1; k >= 0; --k) T[v] = a[k][v] * (T[v] + g[k][v]);
+        f.P[v] = P[v];
+        f.H[v] = T[v];
+        mh[turn][wave][v][lane] = H[v];
+      }
+      maps[turn][wave][lane] = f;
+      if (base > q.from) fetch(base - kTile);
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        f = maps[turn][w][lane];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (w == wave) s[v] = carry[v];
+          carry[v] = __builtin_fmaf(f.P[v], carry[v], f.H[v]);
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        for (int w = NW - 1; w > wave; --w)  // the rows before this wave's
+          h[v] = __builtin_fmaf(maps[turn][w][lane].P[v], h[v], mh[turn][w][v][lane]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          const float next = __builtin_fmaf(a[k][v], h[v], m[k][v] * (i[k][v] * xf[k][v]));
+          over[k][v] = h[v] - over[k][v];
+          h[v] = next;
+        }
+      }
+      const uint32_t at = lane_offset(off);
+#pragma unroll
+      for (int k = R - 1; k >= 0; --k) {
+        float ox[V], oa[V], og[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float dh = g[k][v] + s[v];
+          s[v] = a[k][v] * dh;
+          ox[v] = dh * (m[k][v] * i[k][v]);
+          const float dlog = s[v] * over[k][v];
+          acc[v] = __builtin_fmaf(dlog, r[k][v], acc[v]);
+          og[v] = ox[v] * xf[k][v] * (1.f - i[k][v]);
+          oa[v] = -d[v].k * dlog * (r[k][v] * (1.f - r[k][v]));
+        }
+        if (live && row0 + k < q.end) {
+          const int64_t row = row0 + k;
+          P_ o;
+          o.from_float(ox);
+          o.store_nt(in_row(dx + row * p.dx_st, at));
+          o.from_float(og);
+          o.store_nt(in_row(dgx + row * p.dgx_st, at));
+          o.from_float(oa);
+          o.store_nt(in_row(dga + row * p.dga_st, at));
+        }
+      }
+    }
+    if (p.dinitial && opens && wave == 0 && live) {
+      const bool init = p.has_init && p.has_init[b] != 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.dinitial[slot * p.di_slot + c + v] = init ? carry[v] : 0.f;
     }
   }
   // ddecay's sum over the waves, in their order
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < V; ++v) mp[0][wave][v][lane] = acc[v];
+  for (int v = 0; v < V; ++v) mh[0][wave][v][lane] = acc[v];
   __syncthreads();
   if (wave != 0 || !live) return;
-  const bool init = p.has_init && p.has_init[b] != 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     float sum = 0.f;
 #pragma unroll
-    for (int q = 0; q < NW; ++q) sum += mp[0][q][v][lane];
-    p.partial[(int64_t)b * p.dim + c + v] = sum;
-    if (p.dinitial) p.dinitial[slot * p.di_slot + c + v] = init ? carry[v] : 0.f;
+    for (int w = 0; w < NW; ++w) sum += mh[0][w][v][lane];
+    p.partial[(int64_t)unit * p.dim + c + v] = sum;  // in this launch's order of units
+  }
+}
+
+// The backward map of the one sequence that began before each segment, over
+// its tiles in the segment, from the last to the first: s -> a (dout + s).
+template <typename D, int V>
+__global__ __launch_bounds__(kMapWaves * 64) void rec_bwd_map_kernel(const RecBwdParams p) {
+  using S = typename D::storage;
+  using P_ = Pack<D, V>;
+  constexpr int NW = kMapWaves, R = kMapRows;
+  __shared__ RowMap<V> maps[NW][64];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
+  const int unit = (int)(blockIdx.x / slabs), total = (int)p.total_T, lo = unit * p.seg_rows;
+  const int hi = total - lo <= p.seg_rows ? total : lo + p.seg_rows;
+  const int ch = (int)((blockIdx.x % slabs) * 64 + lane) * V;
+  const bool live = ch < p.dim;
+  const int c = live ? ch : p.dim - V;
+  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(S);
+  const int b = first_sequence(p.qsl, p.batch, lo + 1);  // the first that ends behind lo
+  if (b >= p.batch) return;
+  const Part s(p.qsl, b, lo, hi);
+  const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
+  if (s.start >= lo || s.from >= s.to || slot == p.pad_slot_id) return;
+  const S* dout = static_cast<const S*>(p.dout);
+  const S* ga = static_cast<const S*>(p.ga);
+  Decay d[V];
+  RowMap<V> m;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    d[v] = make_decay(p.decay[c + v], p.scale);
+    m.P[v] = 1.f;
+    m.H[v] = 0.f;
+  }
+  // wave 0 has the last run
+  const int per = (s.to - s.from + NW - 1) / NW;
+  const int from = s.from + (NW - 1 - wave) * per, to = from + per < s.to ? from + per : s.to;
+  P_ rd[R], ra[R];
+  // groups of R rows, the last first; the group at `from` may reach behind `to`
+  auto fetch = [&](int row0) {
+    load_rows(rd, dout, p.do_st, row0, to, off);
+    load_rows(ra, ga, p.ga_st, row0, to, off);
+  };
+  const int top = from + (to - 1 - from) / R * R;
+  if (from < to) fetch(top);
+  for (int row0 = top; from < to && row0 >= from; row0 -= R) {
+    P_ cd[R], ca[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      cd[r] = rd[r];
+      ca[r] = ra[r];
+    }
+    if (row0 - R >= from) fetch(row0 - R);
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+      float df[V], af[V];
+      cd[r].to_float(df);
+      ca[r].to_float(af);
+      const bool in = row0 + r < to;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float a = __builtin_amdgcn_exp2f(-d[v].k_log2 * sigmoid(af[v]));
+        m.H[v] = in ? a * (m.H[v] + df[v]) : m.H[v];
+        m.P[v] *= in ? a : 1.f;
+      }
+    }
+  }
+  maps[wave][lane] = m;
+  __syncthreads();
+  if (wave != 0 || !live) return;
+  const bool ends = s.to == s.end;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float P = 1.f, H = 0.f;
+    if (ends) {
+      P = 0.f;
+      H = p.dfinal ? p.dfinal[slot * p.df_slot + c + v] : 0.f;
+      p.saved[(int64_t)unit * p.dim + c + v] = H;
+    }
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      H = __builtin_fmaf(maps[w][lane].P[v], H, maps[w][lane].H[v]);
+      P *= maps[w][lane].P[v];
+    }
+    p.maps[((int64_t)unit * p.dim + c + v) * 2] = P;
+    p.maps[((int64_t)unit * p.dim + c + v) * 2 + 1] = H;
   }
 }
 
@@ -618,12 +917,25 @@ __global__ __launch_bounds__(64) void rec_update_kernel(const RecUpdParams p) {
   static_cast<S*>(p.out)[b * p.o_rs + c] = round_to<D>(h);
 }
 
+// Unused LDS that leaves room for three workgroups of a CU (of eight) where
+// waves walk long sequences: more of them at once read from too many places
+// (8 x 4096 x 8192 bf16: 369 us with three, 402 with four, 466 with all;
+// 16 sequences of 1088 tokens: 128 us with all, 154 with three).
+constexpr uint32_t kLongPadLds = 53000;
+constexpr int64_t kLongTokens = 2048;
+// The same for a whole sequence in rows: two of three (16 ragged sequences x
+// 4096: 163 against 170 us, one alone 182).
+constexpr uint32_t kRowsPadLds = 60000;
+
 template <typename D, bool VEC>
 static void launch_fwd(int nw, const RecFwdParams& p, uint32_t grid, hipStream_t s) {
   switch (nw) {
-    case 1: hipLaunchKernelGGL((rec_fwd_kernel<D, VEC, 1>), dim3(grid), dim3(256), 0, s, p); break;
+    case 1: hipLaunchKernelGGL((rec_fwd_kernel<D, VEC, 1>), dim3(grid), dim3(256), p.pad_lds, s, p); break;
     case 4: hipLaunchKernelGGL((rec_fwd_kernel<D, VEC, 4>), dim3(grid), dim3(256), 0, s, p); break;
-    default: hipLaunchKernelGGL((rec_fwd_kernel<D, VEC, 16>), dim3(grid), dim3(1024), 0, s, p); break;
+    default:
+      if constexpr (VEC)
+        hipLaunchKernelGGL((rec_fwd_kernel<D, VEC, 16>), dim3(grid), dim3(1024), 0, s, p);
+      break;
   }
 }
 
@@ -632,7 +944,33 @@ static void launch_bwd(int nw, const RecBwdParams& p, uint32_t grid, hipStream_t
   switch (nw) {
     case 1: hipLaunchKernelGGL((rec_bwd_kernel<D, VEC, 1>), dim3(grid), dim3(256), 0, s, p); break;
     case 4: hipLaunchKernelGGL((rec_bwd_kernel<D, VEC, 4>), dim3(grid), dim3(256), 0, s, p); break;
-    default: hipLaunchKernelGGL((rec_bwd_kernel<D, VEC, 16>), dim3(grid), dim3(1024), 0, s, p); break;
+    default:
+      if constexpr (VEC)
+        hipLaunchKernelGGL((rec_bwd_kernel<D, VEC, 8>), dim3(grid), dim3(512), 0, s, p);
+      break;
+  }
+}
+
+template <typename D, int V>
+static void launch_fwd_rows(const RecFwdParams& p, uint32_t grid, hipStream_t s) {
+  const dim3 g(grid), th(kFwdWaves * 64), tm(kMapWaves * 64);
+  if (p.seg_rows) {
+    hipLaunchKernelGGL((rec_fwd_map_kernel<D, V>), g, tm, 0, s, p);
+    hipLaunchKernelGGL((rec_fwd_rows_kernel<D, V, true>), g, th, 0, s, p);
+  } else if constexpr (V == 1) {
+    hipLaunchKernelGGL((rec_fwd_rows_kernel<D, 1, false>), g, th, kRowsPadLds, s, p);
+  }
+}
+
+// One channel a lane: the rows of seven planes leave no registers for two.
+template <typename D>
+static void launch_bwd_rows(const RecBwdParams& p, uint32_t grid, hipStream_t s) {
+  const dim3 g(grid), th(kBwdWaves * 64), tm(kMapWaves * 64);
+  if (p.seg_rows) {
+    hipLaunchKernelGGL((rec_bwd_map_kernel<D, 1>), g, tm, 0, s, p);
+    hipLaunchKernelGGL((rec_bwd_rows_kernel<D, 1, true>), g, th, 0, s, p);
+  } else {
+    hipLaunchKernelGGL((rec_bwd_rows_kernel<D, 1, false>), g, th, 0, s, p);
   }
 }
 
@@ -643,6 +981,8 @@ static int rec_check(const char* fn, int32_t batch, int32_t dim, int64_t total_T
                      float scale) {
   if (batch < 0 || dim < 0 || total_T < 0)
     return fail(SCONV_ERR_INVALID, "%s: batch, dim and total_T must be >= 0", fn);
+  if (total_T > INT32_MAX - 4096)  // token numbers are int32, as the offsets
+    return fail(SCONV_ERR_UNSUPPORTED, "%s: total_T too large", fn);
   if (!valid_dtype(dtype)) return fail(SCONV_ERR_INVALID, "%s: unknown dtype %d", fn, dtype);
   if (!(scale > 0.f) || !(scale <= 3.0e38f))
     return fail(SCONV_ERR_INVALID, "%s: decay_scale must be positive and finite", fn);
@@ -655,6 +995,14 @@ static bool side_by_side(std::initializer_list<Plane> planes) {
   for (const Plane& a : planes)
     if (a.sc != 1) return false;
   return true;
+}
+
+// Whether workgroups take the longest sequences first: few sequences, of
+// more than a few tiles (the order costs a round trip: 113 against 122 us
+// for 33 sequences of 248 rows x 1001, forward and gradients; 16 of 1088 x
+// 4096 gain 233 -> 203 us).
+static bool longest_first(int64_t total_T, int32_t batch) {
+  return batch > 1 && batch <= 64 && total_T / batch >= 8 * kTile;
 }
 
 // Vector lanes of V channels: every row starts on a multiple of V elements.
@@ -671,12 +1019,36 @@ static bool token_lanes(std::initializer_list<Plane> planes) {
   return true;
 }
 
-// Waves that walk one sequence together.
-static int waves_per_pair(int64_t pairs, int64_t total_T, int32_t batch) {
+// Waves that walk one sequence together, at most `most`.
+static int waves_per_pair(int64_t pairs, int64_t total_T, int32_t batch, int most) {
   const int64_t mean = total_T / batch;
-  if (pairs < 512 && mean >= 8 * kChunkTokens) return 16;
+  if (most > 4 && pairs < 512 && mean >= 8 * kChunkTokens) return most;
   if (pairs < 8192 && mean >= 2 * kChunkTokens) return 4;
   return 1;
+}
+
+// Rows of a segment of the flat token axis for calls whose channels lie side
+// by side, or 0: a workgroup takes a whole sequence.
+// Segments cost a second read of the inputs, and pay where whole sequences
+// are too few workgroups, or too uneven ones: 8 ragged x 17409 x 4096 bf16
+// (512 workgroups) 209 us in segments, 239..383 without; 16 (1024) 201..209
+// and 138..163; 1 x 32768 x 1024 102 and 1727.  2048 workgroups instead of
+// 1024 were no faster (108 us for the last).
+static int64_t segment_rows(int64_t total_T, int32_t batch, int32_t dim) {
+  const int64_t slabs = cdiv(dim, 64);
+  if (batch == 0 || total_T / batch < 8 * kTile || batch * slabs > 768) return 0;
+  const int64_t segments = cdiv(1024, slabs);
+  const int64_t rows = cdiv(cdiv(total_T, segments), kTile) * kTile;
+  return rows < 2 * kTile ? 2 * kTile : rows;
+}
+
+// Floats of workspace: the segments' maps and saved states, and the parts of
+// ddecay (backward).
+static void rec_workspace(int64_t total_T, int32_t batch, int32_t dim, int64_t* fwd, int64_t* bwd) {
+  const int64_t rows = segment_rows(total_T, batch, dim);
+  const int64_t n = rows ? cdiv(total_T, rows) : 0;
+  *fwd = 3 * n * dim;
+  *bwd = 3 * n * dim + (n > batch ? n : batch) * dim;
 }
 
 static int64_t mark_rows(int64_t total_T, int32_t batch) {
@@ -696,6 +1068,17 @@ extern "C" int gated_linear_recurrence_checkpoint_rows(int64_t total_T, int32_t 
   return SCONV_OK;
 }
 
+extern "C" int gated_linear_recurrence_workspace(int64_t total_T, int32_t batch, int32_t dim,
+                                                 int64_t* fwd_floats, int64_t* bwd_floats) {
+  using namespace sconv;
+  clear_error();
+  const char* fn = "gated_linear_recurrence_workspace";
+  if (total_T < 0 || batch < 0 || dim < 0 || !fwd_floats || !bwd_floats)
+    return fail(SCONV_ERR_INVALID, "%s: sizes must be >= 0, results not NULL", fn);
+  rec_workspace(total_T, batch, dim, fwd_floats, bwd_floats);
+  return SCONV_OK;
+}
+
 extern "C" int gated_linear_recurrence_varlen_fwd(
     const void* x, int64_t x_stride_c, int64_t x_stride_t, const void* gate_a,
     int64_t ga_stride_c, int64_t ga_stride_t, const void* gate_x, int64_t gx_stride_c,
@@ -703,7 +1086,8 @@ extern "C" int gated_linear_recurrence_varlen_fwd(
     int64_t st_stride_slot, const int32_t* query_start_loc, int32_t batch,
     const int32_t* cache_indices, const uint8_t* has_initial_state, void* out,
     int64_t out_stride_c, int64_t out_stride_t, float* checkpoints, int64_t checkpoint_rows,
-    int32_t dim, int64_t total_T, int32_t dtype, int32_t pad_slot_id, hipStream_t stream) {
+    float* workspace, int64_t workspace_floats, int32_t dim, int64_t total_T, int32_t dtype,
+    int32_t pad_slot_id, hipStream_t stream) {
   using namespace sconv;
   clear_error();
   const char* fn = "gated_linear_recurrence_varlen_fwd";
@@ -740,6 +1124,16 @@ extern "C" int gated_linear_recurrence_varlen_fwd(
       overlap(checkpoints, mb, gate_x, pg.bytes()) || overlap(checkpoints, mb, out, po.bytes()) ||
       overlap(checkpoints, mb, states, sb))
     return fail(SCONV_ERR_INVALID, "%s: states or checkpoints overlap another buffer", fn);
+  int64_t need = 0, bwd_need = 0;
+  rec_workspace(total_T, batch, dim, &need, &bwd_need);
+  const int64_t wb = workspace ? need * 4 : 0;
+  if (workspace && workspace_floats < need)
+    return fail(SCONV_ERR_INVALID, "%s: workspace holds %lld floats, %lld needed", fn,
+                (long long)workspace_floats, (long long)need);
+  if (overlap(workspace, wb, x, px.bytes()) || overlap(workspace, wb, gate_a, pa.bytes()) ||
+      overlap(workspace, wb, gate_x, pg.bytes()) || overlap(workspace, wb, out, po.bytes()) ||
+      overlap(workspace, wb, states, sb) || overlap(workspace, wb, checkpoints, mb))
+    return fail(SCONV_ERR_INVALID, "%s: workspace overlaps another buffer", fn);
   RecFwdParams p = {};
   p.x = x; p.ga = gate_a; p.gx = gate_x; p.decay = decay; p.states = states;
   p.qsl = query_start_loc; p.cache_indices = cache_indices; p.has_init = has_initial_state;
@@ -750,22 +1144,30 @@ extern "C" int gated_linear_recurrence_varlen_fwd(
   p.batch = batch; p.dim = dim; p.pad_slot_id = pad_slot_id;
   const auto planes = {px, pa, pg, po};
   if (side_by_side(planes) && dim > 1) {
-    const bool two = row_lanes(planes, 2);
-    const int64_t grid = batch * cdiv(dim, two ? 128 : 64);
-    if (!valid_grid(grid, kRowWaves * 64))
+    p.seg_rows = workspace ? (int32_t)segment_rows(total_T, batch, dim) : 0;
+    // Two channels a lane halve the segments' instructions; a whole sequence
+    // is walked sooner by twice the workgroups (203 -> 154 us for the 16).
+    const bool two = p.seg_rows && row_lanes(planes, 2);
+    const int64_t slabs = cdiv(dim, two ? 128 : 64);
+    p.sorted = longest_first(total_T, batch);
+    const int64_t segments = p.seg_rows ? cdiv(total_T, p.seg_rows) : 0;
+    p.maps = workspace;
+    p.saved = workspace + 2 * segments * dim;
+    const int64_t grid = (segments ? segments : batch) * slabs;
+    if (!valid_grid(grid, kFwdWaves * 64))
       return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
-    const dim3 g((uint32_t)grid), th(kRowWaves * 64);
     if (dtype == SCONV_BF16) {
-      if (two) hipLaunchKernelGGL((rec_fwd_rows_kernel<Bf16, 2>), g, th, 0, stream, p);
-      else hipLaunchKernelGGL((rec_fwd_rows_kernel<Bf16, 1>), g, th, 0, stream, p);
+      if (two) launch_fwd_rows<Bf16, 2>(p, (uint32_t)grid, stream);
+      else launch_fwd_rows<Bf16, 1>(p, (uint32_t)grid, stream);
     } else {
-      if (two) hipLaunchKernelGGL((rec_fwd_rows_kernel<F32, 2>), g, th, 0, stream, p);
-      else hipLaunchKernelGGL((rec_fwd_rows_kernel<F32, 1>), g, th, 0, stream, p);
+      if (two) launch_fwd_rows<F32, 2>(p, (uint32_t)grid, stream);
+      else launch_fwd_rows<F32, 1>(p, (uint32_t)grid, stream);
     }
     return check_launch(fn);
   }
   const bool vec = token_lanes(planes);
-  const int nw = waves_per_pair(p.num_pairs, total_T, batch);
+  const int nw = waves_per_pair(p.num_pairs, total_T, batch, vec ? 16 : 4);
+  p.pad_lds = total_T / batch >= kLongTokens ? kLongPadLds : 0;
   const int64_t grid = nw == 1 ? cdiv(p.num_pairs, 4) : p.num_pairs;
   if (!valid_grid(grid, nw > 4 ? nw * 64 : 256))
     return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
@@ -810,9 +1212,11 @@ extern "C" int gated_linear_recurrence_varlen_bwd(
   if (batch > 0 && checkpoint_rows < mark_rows(total_T, batch))
     return fail(SCONV_ERR_INVALID, "%s: checkpoints hold %lld rows, %lld needed", fn,
                 (long long)checkpoint_rows, (long long)mark_rows(total_T, batch));
-  if (batch > 0 && workspace_floats < (int64_t)batch * dim)
+  int64_t fwd_need = 0, need = 0;
+  rec_workspace(total_T, batch, dim, &fwd_need, &need);
+  if (workspace_floats < need)
     return fail(SCONV_ERR_INVALID, "%s: workspace holds %lld floats, %lld needed", fn,
-                (long long)workspace_floats, (long long)batch * dim);
+                (long long)workspace_floats, (long long)need);
   const int64_t es = elem_size(dtype);
   const Plane in[4] = {plane(dout, do_stride_c, do_stride_t, dim, total_T, es),
                        plane(x, x_stride_c, x_stride_t, dim, total_T, es),
@@ -826,7 +1230,7 @@ extern "C" int gated_linear_recurrence_varlen_bwd(
   const int64_t dfb = dfinal_states ? ((num_slots - 1) * df_stride_slot + dim) * 4 : 0;
   const int64_t mb = batch > 0 ? mark_rows(total_T, batch) * dim * 4 : 0;
   const struct { const void* p; int64_t n; } wr[3] = {
-      {dinitial_states, dib}, {ddecay, (int64_t)dim * 4}, {workspace, (int64_t)batch * dim * 4}};
+      {dinitial_states, dib}, {ddecay, (int64_t)dim * 4}, {workspace, need * 4}};
   for (const Plane& a : in)
     if (!a.readable()) return fail(SCONV_ERR_INVALID, "%s: strides must be >= 0", fn);
   for (int i = 0; i < 3; ++i) {
@@ -867,23 +1271,24 @@ extern "C" int gated_linear_recurrence_varlen_bwd(
   p.di_slot = di_stride_slot; p.total_T = total_T; p.num_pairs = (int64_t)batch * dim;
   p.scale = decay_scale; p.batch = batch; p.dim = dim; p.pad_slot_id = pad_slot_id;
   const auto planes = {in[0], in[1], in[2], in[3], ou[0], ou[1], ou[2]};
+  int64_t parts = batch;
   if (batch > 0 && side_by_side(planes) && dim > 1) {
-    const bool two = row_lanes(planes, 2);
-    const int64_t grid = batch * cdiv(dim, two ? 128 : 64);
-    if (!valid_grid(grid, kRowBwdWaves * 64))
+    p.seg_rows = (int32_t)segment_rows(total_T, batch, dim);
+    p.sorted = longest_first(total_T, batch);
+    const int64_t segments = p.seg_rows ? cdiv(total_T, p.seg_rows) : 0;
+    parts = segments ? segments : batch;
+    p.maps = workspace;
+    p.saved = workspace + 2 * segments * dim;
+    p.partial = workspace + 3 * segments * dim;
+    const int64_t grid = parts * cdiv(dim, 64);
+    if (!valid_grid(grid, kBwdWaves * 64))
       return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
-    const dim3 g((uint32_t)grid), th(kRowBwdWaves * 64);
-    if (dtype == SCONV_BF16) {
-      if (two) hipLaunchKernelGGL((rec_bwd_rows_kernel<Bf16, 2>), g, th, 0, stream, p);
-      else hipLaunchKernelGGL((rec_bwd_rows_kernel<Bf16, 1>), g, th, 0, stream, p);
-    } else {
-      if (two) hipLaunchKernelGGL((rec_bwd_rows_kernel<F32, 2>), g, th, 0, stream, p);
-      else hipLaunchKernelGGL((rec_bwd_rows_kernel<F32, 1>), g, th, 0, stream, p);
-    }
+    if (dtype == SCONV_BF16) launch_bwd_rows<Bf16>(p, (uint32_t)grid, stream);
+    else launch_bwd_rows<F32>(p, (uint32_t)grid, stream);
     if (const int rc = check_launch(fn)) return rc;
   } else if (batch > 0) {
     const bool vec = token_lanes(planes);
-    const int nw = waves_per_pair(p.num_pairs, total_T, batch);
+    const int nw = waves_per_pair(p.num_pairs, total_T, batch, vec ? 8 : 4);
     const int64_t grid = nw == 1 ? cdiv(p.num_pairs, 4) : p.num_pairs;
     if (!valid_grid(grid, nw > 4 ? nw * 64 : 256))
       return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
@@ -897,7 +1302,8 @@ extern "C" int gated_linear_recurrence_varlen_bwd(
     if (const int rc = check_launch(fn)) return rc;
   }
   hipLaunchKernelGGL(rec_ddecay_kernel, dim3((uint32_t)cdiv(dim, kSumCols)),
-                     dim3(kSumCols * kSumGroups), 0, stream, workspace, decay, ddecay, batch, dim, decay_scale);
+                     dim3(kSumCols * kSumGroups), 0, stream, p.partial, decay, ddecay,
+                     (int32_t)parts, dim, decay_scale);
   return check_launch(fn);
 }
 

@@ -27,6 +27,11 @@ __device__ __forceinline__ uint32_t xcd_groups(uint32_t g, uint32_t G) {
   return (idx / N * 8 + xcd) * N + idx % N;
 }
 
+// Keeps the instructions before it and behind it apart.  Eight tokens' gates
+// have no order among them, and the compiler would start them all at once
+// and run out of registers: one or two at a time keep a lane busy.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 // ---------------------------------------------------------------- eight tokens of a lane
 
 constexpr int kLaneTokens = 8;                     // consecutive tokens of one lane
@@ -61,9 +66,21 @@ struct Raw8 {
     } else {
       Elems v;
 #pragma unroll
-      for (int e = 0; e < kLaneTokens; ++e)
-        v.e[e] = t + e < total ? row[(t + e) * stride] : (S)0;
+      for (int e = 0; e < kLaneTokens; ++e) {
+        v.e[e] = t + e < total ? row[(t + e) * (VEC ? 1 : stride)] : (S)0;
+        if (VEC) in_order();  // a row's end only: not worth eight addresses at once
+      }
       __builtin_memcpy(p, &v, sizeof v);
+    }
+  }
+
+  // Token e (a constant) as a float.
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(S) == 2) {
+      const uint32_t w = p[0].raw[e / 2];
+      return __uint_as_float(e % 2 ? w & 0xFFFF0000u : w << 16);
+    } else {
+      return __uint_as_float(p[e / 4].raw[e % 4]);
     }
   }
 
@@ -99,11 +116,41 @@ struct Raw8 {
       Elems v;
       __builtin_memcpy(&v, p, sizeof v);
 #pragma unroll
-      for (int e = 0; e < kLaneTokens; ++e)
-        if (t + e < end) row[(t + e) * stride] = v.e[e];
+      for (int e = 0; e < kLaneTokens; ++e) {
+        if (t + e < end) row[(t + e) * (VEC ? 1 : stride)] = v.e[e];
+        in_order();
+      }
     }
   }
 };
+
+// The sequence of the unit-th largest length (ties: the lower index first), so
+// that the longest start first and the shortest fill the end.  Up to 64
+// sequences, one a lane; more are taken as they come.
+__device__ __forceinline__ int by_length(const int32_t* qsl, int32_t batch, int unit) {
+  if (batch > 64 || batch == 1) return unit;
+  const int lane = threadIdx.x & 63;
+  const int n = lane < batch ? qsl[lane + 1] - qsl[lane] : -1;
+  int rank = 0;
+  for (int j = 0; j < batch; ++j) {
+    const int m = __builtin_amdgcn_readlane(n, j);
+    rank += m > n || (m == n && j < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < batch && rank == unit));
+}
+
+// The first of `batch` sequences that does not end before row lo (batch: none).
+__device__ __forceinline__ int first_sequence(const int32_t* qsl, int32_t batch, int64_t lo) {
+  int n = 0;
+  for (int i0 = 0; i0 < batch; i0 += 64) {
+    const int i = i0 + (threadIdx.x & 63);
+    const bool done = i < batch && qsl[i + 1] < lo;
+    const int k = __popcll(__ballot(done));
+    n += k;
+    if (k < 64) break;
+  }
+  return n;
+}
 
 // ---------------------------------------------------------------- scans of h -> P h + H
 

@@ -593,6 +593,16 @@ def gated_linear_recurrence_checkpoints(x: torch.Tensor, query_start_loc: torch.
     return torch.empty(rows.value, x.shape[0], dtype=torch.float32, device=x.device)
 
 
+def _recurrence_workspace(total_T: int, batch: int, dim: int, backward: bool, x: torch.Tensor):
+    """(tensor or None, floats) of workspace for one packed call."""
+    fwd, bwd = ctypes.c_int64(), ctypes.c_int64()
+    _lib.check(_lib.load().gated_linear_recurrence_workspace(
+        total_T, batch, dim, ctypes.byref(fwd), ctypes.byref(bwd)),
+        "gated_linear_recurrence_workspace")
+    n = bwd.value if backward else fwd.value
+    return (torch.empty(n, dtype=torch.float32, device=x.device) if n else None), n
+
+
 def gated_linear_recurrence_varlen_fwd(x: torch.Tensor, gate_a: torch.Tensor,
                                        gate_x: torch.Tensor, decay: torch.Tensor,
                                        states: Optional[torch.Tensor],
@@ -630,11 +640,13 @@ def gated_linear_recurrence_varlen_fwd(x: torch.Tensor, gate_a: torch.Tensor,
             raise ValueError("checkpoints must be a dense float32 [rows, dim] tensor")
         rows = checkpoints.shape[0]
     pl = _planes(x.shape, x, gate_a, gate_x, out)
+    ws, n = (_recurrence_workspace(total_T, batch, dim, False, x) if x.stride(0) == 1
+             else (None, 0))  # only rows of tokens use one
     _call("gated_linear_recurrence_varlen_fwd", x, *pl[:9], decay.data_ptr(), decay_scale,
           _ptr(states), states.shape[0] if states is not None else 0,
           states.stride(0) if states is not None else 0, query_start_loc.data_ptr(), batch,
-          _ptr(cache_indices), _ptr(hi), *pl[9:], _ptr(checkpoints), rows, dim, total_T, dt,
-          int(pad_slot_id))
+          _ptr(cache_indices), _ptr(hi), *pl[9:], _ptr(checkpoints), rows, _ptr(ws), n, dim,
+          total_T, dt, int(pad_slot_id))
     return out
 
 
@@ -680,13 +692,13 @@ def gated_linear_recurrence_varlen_bwd(dout: torch.Tensor, x: torch.Tensor, gate
         raise ValueError("checkpoints must be a dense float32 [rows, dim] tensor")
     pl = _planes(x.shape, dout, x, gate_a, gate_x, dx, dgate_a, dgate_x)
     ddecay = torch.empty(dim, dtype=torch.float32, device=x.device)
-    ws = torch.empty(batch * dim, dtype=torch.float32, device=x.device)
+    ws, n = _recurrence_workspace(total_T, batch, dim, True, x)
     _call("gated_linear_recurrence_varlen_bwd", x, *pl[:12], decay.data_ptr(), decay_scale,
           checkpoints.data_ptr(), checkpoints.shape[0], query_start_loc.data_ptr(), batch,
           _ptr(cache_indices), _ptr(hi), slots, _ptr(dfinal_states),
           dfinal_states.stride(0) if dfinal_states is not None else 0, _ptr(dinitial_states),
           dinitial_states.stride(0) if dinitial_states is not None else 0, *pl[12:],
-          ddecay.data_ptr(), ws.data_ptr(), ws.numel(), dim, total_T, dt, int(pad_slot_id))
+          ddecay.data_ptr(), _ptr(ws), n, dim, total_T, dt, int(pad_slot_id))
     return dx, dgate_a, dgate_x, ddecay
 
 

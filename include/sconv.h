@@ -10,8 +10,8 @@
  * - Every buffer is a caller-owned DEVICE pointer (hipMalloc / torch).  The
  *   library allocates nothing, never synchronizes and never reads device data
  *   on the host: each call enqueues one kernel on `stream` (NULL = the null
- *   stream; sconv_fused_insert_conv_gather and the gradient entry points may
- *   enqueue two) and returns.
+ *   stream; sconv_fused_insert_conv_gather and the entry points that take a
+ *   workspace may enqueue up to three) and returns.
  *   This makes every call capturable in a hipGraph; grids depend on host
  *   scalars only.
  * - Strides are in ELEMENTS.  Only host scalars are validated.  Properties of
@@ -562,6 +562,13 @@ int gather_intermediate_ssm_state(const void* states, int64_t num_chunks, int64_
 int gated_linear_recurrence_checkpoint_rows(int64_t total_T, int32_t batch, int64_t* rows);
 
 /*
+ * gated_linear_recurrence_workspace -- floats of workspace that a forward and
+ * a backward call over these sizes use.  Host only.
+ */
+int gated_linear_recurrence_workspace(int64_t total_T, int32_t batch, int32_t dim,
+                                      int64_t* fwd_floats, int64_t* bwd_floats);
+
+/*
  * gated_linear_recurrence_varlen_fwd -- the recurrence over packed sequences.
  *
  *   x, gate_a, gate_x, out  [dim, total_T] strides (stride_c, stride_t); out
@@ -575,6 +582,10 @@ int gated_linear_recurrence_checkpoint_rows(int64_t total_T, int32_t batch, int6
  *            causal_conv1d_varlen_fwd (a sequence of no tokens leaves its
  *            initial state, or zeros, in its slot)
  *   checkpoints  fp32 [checkpoint_rows, dim] for the backward call, or NULL
+ *   workspace  fp32 of gated_linear_recurrence_workspace's fwd_floats, the
+ *            call's own until it has finished, or NULL.  With it, few long
+ *            sequences in rows of tokens are cut over their tokens (two
+ *            launches); without, a workgroup walks each of them alone
  *
  * Rows of out outside every sequence, or in a skipped one, are not written.
  *
@@ -583,7 +594,7 @@ int gated_linear_recurrence_checkpoint_rows(int64_t total_T, int32_t batch, int6
  *
  * Host errors (SCONV_ERR_INVALID): negative sizes, decay_scale not positive
  * and finite, NULL required pointer, unknown dtype, has_initial_state without
- * states, too few slots or checkpoint rows, overlapping buffers.
+ * states, too few slots, checkpoint rows or workspace floats, overlapping buffers.
  * SCONV_ERR_UNSUPPORTED: batch * dim beyond one launch.
  * batch == 0 or dim == 0 is a successful no-op.
  */
@@ -594,7 +605,8 @@ int gated_linear_recurrence_varlen_fwd(
     int64_t st_stride_slot, const int32_t* query_start_loc, int32_t batch,
     const int32_t* cache_indices, const uint8_t* has_initial_state, void* out,
     int64_t out_stride_c, int64_t out_stride_t, float* checkpoints, int64_t checkpoint_rows,
-    int32_t dim, int64_t total_T, int32_t dtype, int32_t pad_slot_id, hipStream_t stream);
+    float* workspace, int64_t workspace_floats, int32_t dim, int64_t total_T, int32_t dtype,
+    int32_t pad_slot_id, hipStream_t stream);
 
 /*
  * gated_linear_recurrence_varlen_bwd -- its gradients.  With dh the gradient
@@ -618,8 +630,8 @@ int gated_linear_recurrence_varlen_fwd(
  *            sequence's initial state (zero without has_initial_state), or
  *            NULL; may be dfinal_states itself
  *   ddecay   fp32 [dim] (written)
- *   workspace  fp32 [batch * dim], the call's own until it has finished;
- *            workspace_floats says how many it holds
+ *   workspace  fp32 of gated_linear_recurrence_workspace's bwd_floats, the
+ *            call's own until it has finished
  *
  * The sums over tokens and sequences have a fixed order: equal inputs give
  * equal bits.  Errors as the forward's, and too small a workspace.  dim == 0

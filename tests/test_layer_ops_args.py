@@ -33,7 +33,7 @@ def err(lib):
 def fwd(lib, **kw):
     a = dict(x=X, xc=64, xt=1, ga=GA, gac=64, gat=1, gx=GX, gxc=64, gxt=1, decay=DEC, scale=8.0,
              st=ST, slots=4, ss=16, qsl=QSL, batch=2, idx=IDX, has=HAS, out=OUT, oc=64, ot=1,
-             mk=MK, rows=3, dim=16, T=64, dt=0, pad=-1)
+             mk=MK, rows=3, ws=None, wsn=0, dim=16, T=64, dt=0, pad=-1)
     a.update(kw)
     return lib.gated_linear_recurrence_varlen_fwd(*a.values(), None)
 
@@ -53,6 +53,21 @@ def fwd(lib, **kw):
 ])
 def test_recurrence_forward_refusals(lib, kw, text):
     assert fwd(lib, **kw) == 1 and text in err(lib), err(lib)
+
+
+def test_recurrence_forward_workspace_refusals(lib):
+    """One sequence of 65536 tokens in rows: cut over its tokens."""
+    fwd_n, bwd_n = ctypes.c_int64(), ctypes.c_int64()
+    f = lib.gated_linear_recurrence_workspace
+    assert f(65536, 1, 16, ctypes.byref(fwd_n), ctypes.byref(bwd_n)) == 0
+    assert fwd_n.value > 0 and bwd_n.value > fwd_n.value
+    kw = dict(xc=1, xt=16, gac=1, gat=16, gxc=1, gxt=16, oc=1, ot=16, batch=1, T=65536, rows=1025)
+    assert fwd(lib, **kw, ws=WS, wsn=fwd_n.value - 1) == 1 and "workspace holds" in err(lib)
+    assert fwd(lib, **kw, ws=X + 64, wsn=fwd_n.value) == 1 and "workspace overlaps" in err(lib)
+    assert fwd(lib, **kw, ws=MK, wsn=fwd_n.value) == 1 and "workspace overlaps" in err(lib)
+    for bad in ((-1, 1, 1), (1, -1, 1), (1, 1, -1)):
+        assert f(*bad, ctypes.byref(fwd_n), ctypes.byref(bwd_n)) == 1
+    assert f(1, 1, 1, None, ctypes.byref(bwd_n)) == 1 and f(1, 1, 1, ctypes.byref(fwd_n), None) == 1
 
 
 def test_recurrence_forward_no_ops_and_limits(lib):
