@@ -513,35 +513,72 @@ def gather_intermediate_ssm_state(states: torch.Tensor, chunk_indices: torch.Ten
 
 # ---------------------------------------------------------------- the layer around the conv
 
+# The host's share of a small call is most of its time (a decode step's kernel
+# takes 3 us): these helpers ask each tensor for little, and once.
+_getters = [getattr(torch._C, n, None)
+            for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice")]
+_functions = {}
+
+
+def _current_stream(index: int) -> int:
+    if _getters[0] is not None:
+        return _getters[0](index)
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def _current_device() -> int:
+    return _getters[1]() if _getters[1] is not None else torch.cuda.current_device()
+
+
 def _one_device(first: torch.Tensor, *ts):
     """Every tensor on the first one's GPU."""
-    if not first.is_cuda:
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("libsconv tensors must live on the GPU")
-    dev = first.device
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device} in one call")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device} in one call")
 
 
 def _call(name: str, on: torch.Tensor, *args):
     """One library call on the current stream of `on`'s device."""
-    fn = getattr(_lib.load(), name)
-    index = on.device.index
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, torch.cuda.current_stream(index).cuda_stream)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_lib.load(), name)
+    index = on.get_device()
+    if _current_device() == index:
+        rc = fn(*args, _current_stream(index))
     else:
         with torch.cuda.device(index):
-            rc = fn(*args, torch.cuda.current_stream(index).cuda_stream)
+            rc = fn(*args, _current_stream(index))
     if rc:
         _lib.check(rc, name)
 
 
+def _floats(name: str, *args) -> int:
+    """What a host query of the library writes to its last argument."""
+    n = ctypes.c_int64()
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_lib.load(), name)
+    rc = fn(*args, ctypes.byref(n))
+    if rc:
+        _lib.check(rc, name)
+    return n.value
+
+
 def _same_type(x: torch.Tensor, what: str, *ts) -> int:
-    dt = _dtype(x)
+    dtype = x.dtype
     for t in ts:
-        if t is not None and t.dtype != x.dtype:
+        if t is not None and t.dtype != dtype:
             raise TypeError(f"{what} must share one element type")
-    return dt
+    return _dtype(x)
+
+
+def _dense(t: torch.Tensor, dtype: torch.dtype, name: str, min_len: int = 0):
+    """t is a contiguous 1-D tensor of a type, of min_len entries at least."""
+    if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() or t.numel() < min_len:
+        _vec(t, dtype, name, min_len)
 
 
 def _planes(shape, *ts):
@@ -550,34 +587,60 @@ def _planes(shape, *ts):
     for t in ts:
         if t.shape != shape:
             raise ValueError("the [dim, total_T] tensors of a call must have one shape")
-        args += [t.data_ptr(), t.stride(0), t.stride(1)]
+        args.append(t.data_ptr())
+        args += t.stride()
     return args
 
 
 def _packing(query_start_loc, cache_indices, has_initial_state):
     """(batch, has_initial_state as uint8) after checks."""
     batch = query_start_loc.numel() - 1
-    _vec(query_start_loc, torch.int32, "query_start_loc", 1)
+    _dense(query_start_loc, torch.int32, "query_start_loc", 1)
     if cache_indices is not None:
-        _vec(cache_indices, torch.int32, "cache_indices", batch)
+        _dense(cache_indices, torch.int32, "cache_indices", batch)
     hi = has_initial_state
     if hi is not None:
         if hi.dtype == torch.bool:
             hi = hi.view(torch.uint8)
-        _vec(hi, torch.uint8, "has_initial_state", batch)
+        _dense(hi, torch.uint8, "has_initial_state", batch)
     return batch, hi
 
 
 def _pool(t: Optional[torch.Tensor], dim: int, name: str):
-    """Checks of an fp32 [num_slots, dim] state pool."""
+    """(ptr, slots, slot stride) of an fp32 [num_slots, dim] state pool."""
     if t is None:
-        return
+        return None, 0, 0
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be float32, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] != dim:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != dim:
         raise ValueError(f"{name} must be [num_slots, dim]")
-    if dim > 1 and t.stride(1) != 1:
+    stride = t.stride()
+    if dim > 1 and stride[1] != 1:
         raise ValueError(f"{name} needs contiguous channels")
+    return t.data_ptr(), shape[0], stride[0]
+
+
+def _rows(shape, *ts):
+    """[ptr, row stride] of each [rows, dim] tensor (None: NULL, 0)."""
+    args = []
+    wide = shape[1] > 1
+    for t in ts:
+        if t is None:
+            args += (None, 0)
+            continue
+        stride = t.stride()
+        if t.shape != shape or (wide and stride[1] != 1):
+            raise ValueError("the [rows, dim] tensors of a call need one shape and contiguous "
+                             "channels")
+        args += (t.data_ptr(), stride[0])
+    return args
+
+
+def _checkpoint_rows(t: torch.Tensor, dim: int) -> int:
+    if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != dim or not t.is_contiguous():
+        raise ValueError("checkpoints must be a dense float32 [rows, dim] tensor")
+    return t.shape[0]
 
 
 def gated_linear_recurrence_checkpoints(x: torch.Tensor, query_start_loc: torch.Tensor
@@ -586,20 +649,16 @@ def gated_linear_recurrence_checkpoints(x: torch.Tensor, query_start_loc: torch.
     backward call needs, for inputs like x [dim, total_T]."""
     if x.dim() != 2:
         raise ValueError("x [dim, total_T]")
-    rows = ctypes.c_int64()
-    _lib.check(_lib.load().gated_linear_recurrence_checkpoint_rows(
-        x.shape[1], query_start_loc.numel() - 1, ctypes.byref(rows)),
-        "gated_linear_recurrence_checkpoint_rows")
-    return torch.empty(rows.value, x.shape[0], dtype=torch.float32, device=x.device)
+    rows = _floats("gated_linear_recurrence_checkpoint_rows", x.shape[1],
+                   query_start_loc.numel() - 1)
+    return torch.empty(rows, x.shape[0], dtype=torch.float32, device=x.device)
 
 
 def _recurrence_workspace(total_T: int, batch: int, dim: int, backward: bool, x: torch.Tensor):
     """(tensor or None, floats) of workspace for one packed call."""
-    fwd, bwd = ctypes.c_int64(), ctypes.c_int64()
-    _lib.check(_lib.load().gated_linear_recurrence_workspace(
-        total_T, batch, dim, ctypes.byref(fwd), ctypes.byref(bwd)),
-        "gated_linear_recurrence_workspace")
-    n = bwd.value if backward else fwd.value
+    fwd = ctypes.c_int64()
+    bwd = _floats("gated_linear_recurrence_workspace", total_T, batch, dim, ctypes.byref(fwd))
+    n = bwd if backward else fwd.value
     return (torch.empty(n, dtype=torch.float32, device=x.device) if n else None), n
 
 
@@ -631,22 +690,15 @@ def gated_linear_recurrence_varlen_fwd(x: torch.Tensor, gate_a: torch.Tensor,
                 has_initial_state, out, checkpoints)
     dt = _same_type(x, "x, the gates and out", gate_a, gate_x, out)
     batch, hi = _packing(query_start_loc, cache_indices, has_initial_state)
-    _vec(decay, torch.float32, "decay", dim)
-    _pool(states, dim, "states")
-    rows = 0
-    if checkpoints is not None:
-        if checkpoints.dtype != torch.float32 or checkpoints.dim() != 2 or \
-                checkpoints.shape[1] != dim or not checkpoints.is_contiguous():
-            raise ValueError("checkpoints must be a dense float32 [rows, dim] tensor")
-        rows = checkpoints.shape[0]
+    _dense(decay, torch.float32, "decay", dim)
+    pool, slots, slot_stride = _pool(states, dim, "states")
+    rows = _checkpoint_rows(checkpoints, dim) if checkpoints is not None else 0
     pl = _planes(x.shape, x, gate_a, gate_x, out)
-    ws, n = (_recurrence_workspace(total_T, batch, dim, False, x) if x.stride(0) == 1
+    ws, n = (_recurrence_workspace(total_T, batch, dim, False, x) if pl[1] == 1
              else (None, 0))  # only rows of tokens use one
-    _call("gated_linear_recurrence_varlen_fwd", x, *pl[:9], decay.data_ptr(), decay_scale,
-          _ptr(states), states.shape[0] if states is not None else 0,
-          states.stride(0) if states is not None else 0, query_start_loc.data_ptr(), batch,
-          _ptr(cache_indices), _ptr(hi), *pl[9:], _ptr(checkpoints), rows, _ptr(ws), n, dim,
-          total_T, dt, int(pad_slot_id))
+    _call("gated_linear_recurrence_varlen_fwd", x, *pl[:9], decay.data_ptr(), decay_scale, pool,
+          slots, slot_stride, query_start_loc.data_ptr(), batch, _ptr(cache_indices), _ptr(hi),
+          *pl[9:], _ptr(checkpoints), rows, _ptr(ws), n, dim, total_T, dt, int(pad_slot_id))
     return out
 
 
@@ -678,26 +730,18 @@ def gated_linear_recurrence_varlen_bwd(dout: torch.Tensor, x: torch.Tensor, gate
     dt = _same_type(x, "dout, x, the gates and their gradients", dout, gate_a, gate_x, dx, dgate_a,
                     dgate_x)
     batch, hi = _packing(query_start_loc, cache_indices, has_initial_state)
-    _vec(decay, torch.float32, "decay", dim)
-    _pool(dfinal_states, dim, "dfinal_states")
-    _pool(dinitial_states, dim, "dinitial_states")
-    slots = 0
-    if dfinal_states is not None and dinitial_states is not None and \
-            dfinal_states.shape != dinitial_states.shape:
+    _dense(decay, torch.float32, "decay", dim)
+    dfinal, slots, df_stride = _pool(dfinal_states, dim, "dfinal_states")
+    dinitial, di_slots, di_stride = _pool(dinitial_states, dim, "dinitial_states")
+    if slots and di_slots and slots != di_slots:
         raise ValueError("dfinal_states and dinitial_states must have one shape")
-    for t in (dfinal_states, dinitial_states):
-        slots = t.shape[0] if t is not None else slots
-    if checkpoints.dtype != torch.float32 or checkpoints.dim() != 2 or \
-            checkpoints.shape[1] != dim or not checkpoints.is_contiguous():
-        raise ValueError("checkpoints must be a dense float32 [rows, dim] tensor")
+    rows = _checkpoint_rows(checkpoints, dim)
     pl = _planes(x.shape, dout, x, gate_a, gate_x, dx, dgate_a, dgate_x)
     ddecay = torch.empty(dim, dtype=torch.float32, device=x.device)
     ws, n = _recurrence_workspace(total_T, batch, dim, True, x)
     _call("gated_linear_recurrence_varlen_bwd", x, *pl[:12], decay.data_ptr(), decay_scale,
-          checkpoints.data_ptr(), checkpoints.shape[0], query_start_loc.data_ptr(), batch,
-          _ptr(cache_indices), _ptr(hi), slots, _ptr(dfinal_states),
-          dfinal_states.stride(0) if dfinal_states is not None else 0, _ptr(dinitial_states),
-          dinitial_states.stride(0) if dinitial_states is not None else 0, *pl[12:],
+          checkpoints.data_ptr(), rows, query_start_loc.data_ptr(), batch, _ptr(cache_indices),
+          _ptr(hi), slots or di_slots, dfinal, df_stride, dinitial, di_stride, *pl[12:],
           ddecay.data_ptr(), _ptr(ws), n, dim, total_T, dt, int(pad_slot_id))
     return dx, dgate_a, dgate_x, ddecay
 
@@ -717,18 +761,13 @@ def gated_linear_recurrence_update(x: torch.Tensor, gate_a: torch.Tensor, gate_x
     batch, dim = x.shape
     _one_device(x, gate_a, gate_x, decay, states, state_indices, out)
     dt = _same_type(x, "x, the gates and out", gate_a, gate_x, out)
-    rows = []
-    for t in (x, gate_a, gate_x, out):
-        if t.shape != x.shape or (dim > 1 and t.stride(1) != 1):
-            raise ValueError("x, the gates and out need one shape and contiguous channels")
-        rows += [t.data_ptr(), t.stride(0)]
-    _vec(decay, torch.float32, "decay", dim)
-    _pool(states, dim, "states")
+    rows = _rows(x.shape, x, gate_a, gate_x, out)
+    _dense(decay, torch.float32, "decay", dim)
+    pool, slots, slot_stride = _pool(states, dim, "states")
     if state_indices is not None:
-        _vec(state_indices, torch.int32, "state_indices", batch)
-    _call("gated_linear_recurrence_update", x, *rows[:6], decay.data_ptr(), decay_scale,
-          states.data_ptr(), states.shape[0], states.stride(0), _ptr(state_indices), *rows[6:],
-          batch, dim, dt, int(pad_slot_id))
+        _dense(state_indices, torch.int32, "state_indices", batch)
+    _call("gated_linear_recurrence_update", x, *rows[:6], decay.data_ptr(), decay_scale, pool,
+          slots, slot_stride, _ptr(state_indices), *rows[6:], batch, dim, dt, int(pad_slot_id))
     return out
 
 
@@ -760,47 +799,31 @@ def causal_conv1d_varlen_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.
     if weight.shape[0] != dim:
         raise ValueError("weight must be [dim, W]")
     if bias is not None:
-        _vec(bias, x.dtype, "bias", dim)
+        _dense(bias, x.dtype, "bias", dim)
     batch, hi = _packing(query_start_loc, cache_indices, has_initial_state)
     slots, pool_args = 0, []
     for t in pools:
         if t is None:
             pool_args.append((None, 0, 0, 0))
             continue
-        if t.dim() != 3 or t.shape[1] != dim or t.shape[2] != W - 1:
+        shape = t.shape
+        if len(shape) != 3 or shape[1] != dim or shape[2] != W - 1:
             raise ValueError("states and their gradients must be [num_slots, dim, W-1]")
-        if slots and t.shape[0] != slots:
+        if slots and shape[0] != slots:
             raise ValueError("states and their gradients must have one number of slots")
-        slots = t.shape[0]
-        pool_args.append((t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)))
+        slots = shape[0]
+        pool_args.append((t.data_ptr(), *t.stride()))
     pl = _planes(x.shape, dout, x, dx)
     dweight = torch.empty(dim, W, dtype=torch.float32, device=x.device)
     dbias = torch.empty(dim, dtype=torch.float32, device=x.device) if bias is not None else None
-    need = ctypes.c_int64()
-    _lib.check(_lib.load().causal_conv1d_varlen_bwd_workspace(total_T, batch, dim, W,
-                                                              ctypes.byref(need)),
-               "causal_conv1d_varlen_bwd_workspace")
-    ws = torch.empty(need.value, dtype=torch.float32, device=x.device)
+    n = _floats("causal_conv1d_varlen_bwd_workspace", total_T, batch, dim, W)
+    ws = torch.empty(n, dtype=torch.float32, device=x.device)
     _call("causal_conv1d_varlen_bwd", x, *pl[:6], weight.data_ptr(), weight.stride(0),
           weight.stride(1), _ptr(bias), *pool_args[0], slots, query_start_loc.data_ptr(), batch,
           _ptr(cache_indices), _ptr(hi), *pool_args[1], *pool_args[2], *pl[6:],
-          dweight.data_ptr(), _ptr(dbias), ws.data_ptr(), ws.numel(), dim, total_T, W, dt,
+          dweight.data_ptr(), _ptr(dbias), ws.data_ptr(), n, dim, total_T, W, dt,
           _lib.ACT_SILU if silu_activation else _lib.ACT_NONE, int(pad_slot_id))
     return dx, dweight, dbias
-
-
-def _rows(shape, *ts):
-    """[ptr, row stride] of each [rows, dim] tensor (None: NULL, 0)."""
-    args = []
-    for t in ts:
-        if t is None:
-            args += [None, 0]
-            continue
-        if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError("the [rows, dim] tensors of a call need one shape and contiguous "
-                             "channels")
-        args += [t.data_ptr(), t.stride(0)]
-    return args
 
 
 def _norm(x, weight, eps, residual, residual_out, out, scales, group_size, out_dt):
@@ -811,7 +834,7 @@ def _norm(x, weight, eps, residual, residual_out, out, scales, group_size, out_d
         residual_out = residual
     _one_device(x, weight, residual, residual_out, out, scales)
     dt = _same_type(x, "x, weight, residual and residual_out", weight, residual, residual_out)
-    _vec(weight, x.dtype, "weight", dim)
+    _dense(weight, x.dtype, "weight", dim)
     a = _rows(x.shape, x, residual, residual_out, out)
     _call("rms_norm_fwd", x, *a[:4], weight.data_ptr(), eps, *a[4:], _ptr(scales),
           scales.stride(0) if scales is not None else 0, group_size, rows, dim, dt,
@@ -872,13 +895,11 @@ def rms_norm_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, eps:
     dx = torch.empty_like(x) if dx is None else dx
     _one_device(x, dout, weight, dresidual, dx)
     dt = _same_type(x, "dout, x, weight, dresidual and dx", dout, weight, dresidual, dx)
-    _vec(weight, x.dtype, "weight", dim)
+    _dense(weight, x.dtype, "weight", dim)
     a = _rows(x.shape, dout, x, dresidual, dx)
-    need = ctypes.c_int64()
-    _lib.check(_lib.load().rms_norm_bwd_workspace(rows, dim, ctypes.byref(need)),
-               "rms_norm_bwd_workspace")
+    n = _floats("rms_norm_bwd_workspace", rows, dim)
     dweight = torch.empty(dim, dtype=torch.float32, device=x.device)
-    ws = torch.empty(need.value, dtype=torch.float32, device=x.device)
+    ws = torch.empty(n, dtype=torch.float32, device=x.device)
     _call("rms_norm_bwd", x, *a[:4], weight.data_ptr(), eps, *a[4:], dweight.data_ptr(),
-          ws.data_ptr(), ws.numel(), rows, dim, dt)
+          ws.data_ptr(), n, rows, dim, dt)
     return dx, dweight
