@@ -9,6 +9,7 @@
 // z is recomputed from the inputs, so the forward saves nothing.
 #include "column_sum.h"
 #include "lane_tokens.h"
+#include "row_lanes.h"
 #include "sconv_host.h"
 
 namespace sconv {
@@ -23,8 +24,8 @@ struct ConvGradParams {
   float* partial;  // [parts, dim, W + 1]: dw, dbias of one sequence or segment
   int64_t do_sc, do_st, x_sc, x_st, w_sc, w_sk, dx_sc, dx_st;
   int64_t is_slot, is_c, is_k, df_slot, df_c, df_k, di_slot, di_c, di_k;
-  int64_t total_T, num_pairs, strip;
-  int32_t batch, dim, silu, pad_slot_id;
+  int64_t total_T, num_pairs;
+  int32_t strip, batch, dim, silu, pad_slot_id;
 };
 
 // dout * d silu(z) / dz
@@ -247,15 +248,18 @@ __global__ __launch_bounds__(kStripWaves * 64) void conv_grad_rows_kernel(const 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
   const uint32_t wg = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int64_t seg = wg / slabs;
+  const int seg = (int)(wg / slabs), total = (int)p.total_T;
   const int ch = ((int)(wg % slabs) * 64 + lane) * V;
   const bool live = ch < p.dim;
   const int c = live ? ch : p.dim - V;
-  const int64_t strip = seg * kStripWaves + wave;
-  const int64_t lo = strip * p.strip, hi = lo + p.strip;
+  const int strip = seg * kStripWaves + wave;
   // The strip of the last row (of none: the first strip) also takes the
   // sequences that start at the end of the rows; strips past it are idle.
-  const bool used = lo < p.total_T || strip == 0, last = used && hi >= p.total_T;
+  const bool used = strip == 0 || (int64_t)strip * p.strip < total;
+  const int lo = used ? strip * p.strip : total;
+  const bool last = used && total - lo <= p.strip;
+  const int hi = last ? total : used ? lo + p.strip : lo;
+  const uint32_t off = (uint32_t)c * (uint32_t)sizeof(S);
   float w[W][V], bias[V], acc[W + 1][V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -266,18 +270,18 @@ __global__ __launch_bounds__(kStripWaves * 64) void conv_grad_rows_kernel(const 
 #pragma unroll
     for (int k = 0; k <= W; ++k) acc[k][v] = 0.f;
   }
-  const S* x = static_cast<const S*>(p.x) + c;
-  const S* g = static_cast<const S*>(p.dout) + c;
-  S* dx = static_cast<S*>(p.dx) + c;
+  const S* x = static_cast<const S*>(p.x);
+  const S* g = static_cast<const S*>(p.dout);
+  S* dx = static_cast<S*>(p.dx);
   for (int b = used ? first_sequence(p.qsl, p.batch, lo) : p.batch; b < p.batch; ++b) {
-    const int64_t start = p.qsl[b], end = p.qsl[b + 1];
+    const int start = p.qsl[b], end = p.qsl[b + 1];
     if (start >= hi && !last) break;
     const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
     const bool mine_first = start >= lo && (start < hi || last);
-    const int64_t from = start > lo ? start : lo, to = end < hi ? end : hi;
+    const int from = start > lo ? start : lo, to = end < hi ? end : hi;
     if (slot == p.pad_slot_id || (from >= to && !(start == end && mine_first))) continue;
     const bool init = p.initial && p.has_init && p.has_init[b] != 0;
-    auto state = [&](int64_t i, int v) {  // initial state, logical index i in [-SL, 0)
+    auto state = [&](int i, int v) {  // initial state, logical index i in [-SL, 0)
       return init && i >= -SL ? load_as_float<D>(static_cast<const S*>(p.initial) + slot * p.is_slot +
                                                  (c + v) * p.is_c + (i + SL) * p.is_k) : 0.f;
     };
@@ -287,10 +291,10 @@ __global__ __launch_bounds__(kStripWaves * 64) void conv_grad_rows_kernel(const 
 #pragma unroll
       for (int v = 0; v < V; ++v) u[m][v] = dz[m][v] = 0.f;
       if (m >= 1) {  // u[1..SL]: the inputs before `from`
-        const int64_t t = from - W + m;
+        const int t = from - W + m;
         if (t >= start) {
           P r;
-          r.load(x + t * p.x_st);
+          r.load(in_row(x + (int64_t)t * p.x_st, off));
           r.to_float(u[m]);
         } else {
 #pragma unroll
@@ -299,31 +303,30 @@ __global__ __launch_bounds__(kStripWaves * 64) void conv_grad_rows_kernel(const 
       }
     }
     P rx[G], rg[G];
-    auto fetch = [&](int64_t t0) {
+    auto fetch = [&](int t0) {
+      load_rows(rx, x, p.x_st, t0, end, off);
+      load_rows(rg, g, p.do_st, t0, end, off);
+    };
+    if (end > start) {
+      fetch(from);
+    } else {
 #pragma unroll
       for (int r = 0; r < G; ++r) {
-        const int64_t t = t0 + r < end ? t0 + r : end - 1;
-        if (end > start) {
-          rx[r].load(x + t * p.x_st);
-          rg[r].load(g + t * p.do_st);
-        } else {
-          rx[r].zero();
-          rg[r].zero();
-        }
+        rx[r].zero();
+        rg[r].zero();
       }
-    };
-    fetch(from);
-    for (int64_t t0 = from; t0 < to + SL; t0 += G) {
+    }
+    for (int t0 = from; t0 < to + SL; t0 += G) {
       P cx[G], cg[G];
 #pragma unroll
       for (int r = 0; r < G; ++r) {
         cx[r] = rx[r];
         cg[r] = rg[r];
       }
-      if (t0 + G < to + SL) fetch(t0 + G);
+      if (t0 + G < to + SL && end > start) fetch(t0 + G);
 #pragma unroll
       for (int r = 0; r < G; ++r) {
-        const int64_t t = t0 + r, i = t - SL;
+        const int t = t0 + r, i = t - SL;
         if (t >= to + SL) break;
         const bool in = t < end;
         float gf[V], xf[V], du[V];
@@ -359,7 +362,7 @@ __global__ __launch_bounds__(kStripWaves * 64) void conv_grad_rows_kernel(const 
         if (i >= from) {
           P o;
           o.from_float(du);
-          if (live) o.store(dx + i * p.dx_st);
+          if (live) o.store(in_row(dx + (int64_t)i * p.dx_st, off));
         } else if (i < start && mine_first && p.dinitial && live) {
           S* di = static_cast<S*>(p.dinitial) + slot * p.di_slot + (i - start + SL) * p.di_k;
 #pragma unroll
@@ -382,7 +385,7 @@ __global__ __launch_bounds__(kStripWaves * 64) void conv_grad_rows_kernel(const 
       float a = 0.f;
 #pragma unroll
       for (int s = 0; s < kStripWaves; ++s) a += sums[s][k][lane * V + v];
-      p.partial[(seg * p.dim + c + v) * (W + 1) + k] = a;
+      p.partial[((int64_t)seg * p.dim + c + v) * (W + 1) + k] = a;
     }
   }
 }
@@ -420,9 +423,10 @@ static void launch_grad_rows(int W, const ConvGradParams& p, uint32_t grid, hipS
 }
 
 // Rows of a strip: long strips read fewer rows twice, short ones keep a
-// small batch's chain short.
+// small batch's chain short (5003 x 1021 fp32: 16 rows 21 us, 32 22, 64 26,
+// 128 38; 17409 x 4096 bf16: 143, 117, 115, 127).
 static int64_t strip_rows(int64_t total_T, int32_t dim) {
-  return total_T * dim >= (int64_t)1 << 22 ? 64 : 16;
+  return total_T * dim >= (int64_t)1 << 23 ? 64 : 16;
 }
 
 static int64_t grad_segments(int64_t total_T, int32_t dim) {
@@ -466,6 +470,8 @@ extern "C" int causal_conv1d_varlen_bwd(
   const char* fn = "causal_conv1d_varlen_bwd";
   if (batch < 0 || dim < 0 || total_T < 0)
     return fail(SCONV_ERR_INVALID, "%s: batch, dim and total_T must be >= 0", fn);
+  if (total_T > INT32_MAX - 4096)  // token numbers are int32, as the offsets
+    return fail(SCONV_ERR_UNSUPPORTED, "%s: total_T too large", fn);
   if (W < 1 || W > 4) return fail(SCONV_ERR_INVALID, "%s: W=%d outside [1, 4]", fn, W);
   if (!valid_dtype(dtype)) return fail(SCONV_ERR_INVALID, "%s: unknown dtype %d", fn, dtype);
   if (!valid_act(activation))
@@ -536,7 +542,7 @@ extern "C" int causal_conv1d_varlen_bwd(
   if (rows) {
     auto lanes = [&](const Plane& a) { return a.st % 2 == 0 && aligned_to(a.p, 2 * es); };
     V = dim % 2 == 0 && lanes(pg) && lanes(px) && lanes(po) ? 2 : 1;
-    p.strip = strip_rows(total_T, dim);
+    p.strip = (int32_t)strip_rows(total_T, dim);
     parts = grad_segments(total_T, dim);
     grid = parts * cdiv(dim, 64 * V);
   } else {
