@@ -382,6 +382,10 @@ __global__ __launch_bounds__(kFwdWaves * 64) void rec_fwd_rows_kernel(const RecF
   using S = typename D::storage;
   using P_ = Pack<D, V>;
   constexpr int NW = kFwdWaves, R = kTile / NW;
+  // Tiles of loads in flight: a long sequence alone on its CUs waits for them
+  // (16 ragged x 4096: 154 against 163 us); where many segments share the
+  // CUs, the registers are worth more (1 x 32768 x 1024: 102, with two 112).
+  constexpr int kAhead = SEG ? 1 : 2;
   __shared__ RowMap<V> maps[2][NW][64];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const uint32_t slabs = (uint32_t)((p.dim + 64 * V - 1) / (64 * V));
@@ -421,14 +425,16 @@ __global__ __launch_bounds__(kFwdWaves * 64) void rec_fwd_rows_kernel(const RecF
       const int first = s.start / p.seg_rows;
       compose_segments<V, NW>(p.maps, p.dim, c, first, unit - first, 1, lane, wave, maps[turn], carry);
     }
-    P_ rx[R], ra[R], rg[R];
-    auto fetch = [&](int row0) {
-      load_rows(rx, x, p.x_st, row0, s.end, off);
-      load_rows(ra, ga, p.ga_st, row0, s.end, off);
-      load_rows(rg, gx, p.gx_st, row0, s.end, off);
+    P_ rx[kAhead][R], ra[kAhead][R], rg[kAhead][R];
+    auto fetch = [&](auto which, int base) {
+      constexpr int k = decltype(which)::value;
+      const int row0 = base + wave * R;
+      load_rows(rx[k], x, p.x_st, row0, s.end, off);
+      load_rows(ra[k], ga, p.ga_st, row0, s.end, off);
+      load_rows(rg[k], gx, p.gx_st, row0, s.end, off);
     };
-    if (s.to > s.from) fetch(s.from + wave * R);
-    for (int base = s.from; base < s.to; base += kTile, turn ^= 1) {
+    auto tile = [&](auto which, int base) {
+      constexpr int k = decltype(which)::value;
       const int row0 = base + wave * R;
       float pl[R][V], hl[R][V];
       RowMap<V> m;
@@ -440,9 +446,9 @@ __global__ __launch_bounds__(kFwdWaves * 64) void rec_fwd_rows_kernel(const RecF
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float xf[V], af[V], gf[V];
-        rx[r].to_float(xf);
-        ra[r].to_float(af);
-        rg[r].to_float(gf);
+        rx[k][r].to_float(xf);
+        ra[k][r].to_float(af);
+        rg[k][r].to_float(gf);
         const bool in = row0 + r < s.end;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -455,7 +461,7 @@ __global__ __launch_bounds__(kFwdWaves * 64) void rec_fwd_rows_kernel(const RecF
         }
       }
       maps[turn][wave][lane] = m;
-      if (base + kTile < s.to) fetch(row0 + kTile);
+      if (base + kAhead * kTile < s.to) fetch(which, base + kAhead * kTile);
       if (p.marks && wave == 0 && live) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -482,6 +488,15 @@ __global__ __launch_bounds__(kFwdWaves * 64) void rec_fwd_rows_kernel(const RecF
         o.from_float(y);
         if (live && row0 + r < s.end) o.store_nt(in_row(out + (int64_t)(row0 + r) * p.o_st, at));
       }
+      turn ^= 1;
+    };
+    const std::integral_constant<int, 0> even;
+    const std::integral_constant<int, kAhead - 1> odd;
+    if (s.from < s.to) fetch(even, s.from);
+    if (kAhead == 2 && s.from + kTile < s.to) fetch(odd, s.from + kTile);
+    for (int base = s.from; base < s.to; base += kAhead * kTile) {
+      tile(even, base);
+      if (kAhead == 2 && base + kTile < s.to) tile(odd, base + kTile);
     }
     if (p.states && s.to == s.end && wave == 0 && live) {
 #pragma unroll
@@ -925,7 +940,7 @@ static void launch_fwd_rows(const RecFwdParams& p, uint32_t grid, hipStream_t s)
     hipLaunchKernelGGL((rec_fwd_map_kernel<D, V>), g, tm, 0, s, p);
     hipLaunchKernelGGL((rec_fwd_rows_kernel<D, V, true>), g, th, 0, s, p);
   } else if constexpr (V == 1) {
-    hipLaunchKernelGGL((rec_fwd_rows_kernel<D, 1, false>), g, th, kRowsPadLds, s, p);
+    hipLaunchKernelGGL((rec_fwd_rows_kernel<D, 1, false>), g, th, p.sorted ? kRowsPadLds : 0, s, p);
   }
 }
 
@@ -1112,9 +1127,11 @@ extern "C" int gated_linear_recurrence_varlen_fwd(
   const auto planes = {px, pa, pg, po};
   if (side_by_side(planes) && dim > 1) {
     p.seg_rows = workspace ? (int32_t)segment_rows(total_T, batch, dim) : 0;
-    // Two channels a lane halve the segments' instructions; a whole sequence
-    // is walked sooner by twice the workgroups (203 -> 154 us for the 16).
-    const bool two = p.seg_rows && row_lanes(planes, 2);
+    // Two channels a lane halve the segments' instructions (bf16: 102 against
+    // 108 us for 1 x 32768 x 1024; fp32 loses a workgroup a CU to their
+    // registers, 34 us against 38 for 40000 x 100); a whole sequence is walked
+    // sooner by twice the workgroups (203 -> 154 us for the 16).
+    const bool two = p.seg_rows && dtype == SCONV_BF16 && row_lanes(planes, 2);
     const int64_t slabs = cdiv(dim, two ? 128 : 64);
     p.sorted = longest_first(total_T, batch);
     const int64_t segments = p.seg_rows ? cdiv(total_T, p.seg_rows) : 0;
@@ -1127,8 +1144,7 @@ extern "C" int gated_linear_recurrence_varlen_fwd(
       if (two) launch_fwd_rows<Bf16, 2>(p, (uint32_t)grid, stream);
       else launch_fwd_rows<Bf16, 1>(p, (uint32_t)grid, stream);
     } else {
-      if (two) launch_fwd_rows<F32, 2>(p, (uint32_t)grid, stream);
-      else launch_fwd_rows<F32, 1>(p, (uint32_t)grid, stream);
+      launch_fwd_rows<F32, 1>(p, (uint32_t)grid, stream);
     }
     return check_launch(fn);
   }

@@ -213,6 +213,69 @@ def test_recurrence_launch_shapes(layout, dim, batch):
     c.check_backward(got, di, layout)
 
 
+# Few long sequences in rows are cut into segments of 128 rows and more:
+# sequences that end at, before and after a cut, several cuts long, inside one
+# segment, empty at a cut and at both ends, skipped.
+SEGMENTED = [
+    ([128, 1280, 0, 128, 1800], (0, 1), ()),
+    ([0, 1000, 3, 0, 2000, 127, 1900, 0], (1, 2, 4, 7), (5,)),
+    ([2049], (), ()),
+    ([700, 0, 900, 1664, 1], (0, 2, 3), (2,)),
+]
+
+
+@pytest.mark.parametrize("layout", ["token", "token_odd", "channel"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("which", range(len(SEGMENTED)))
+def test_recurrence_segments(which, dtype, layout):
+    lens, inits, pads = SEGMENTED[which]
+    c = Rec(lens, [6, 130, 64, 65][which], dtype, seed=20 + which, inits=inits, pads=pads,
+            lead=[0, 5, 0, 64][which], trail=which % 2)
+    d = c.gpu(layout)
+    out, m = c.forward(d, layout)
+    c.check_forward(out, d["pool"], layout)
+    got, di = c.backward(d, m, layout)
+    c.check_backward(got, di, layout)
+    # state gradients in place, and the forward in place: the same bits
+    df = torch.full_like(d["pool"], NAN)
+    for b in range(len(lens)):
+        if c.live[b]:
+            df[int(c.slots[b])] = c.dfinal[b].cuda()
+    again = lib.gated_linear_recurrence_varlen_bwd(
+        d["dout"], d["x"], d["ga"], d["gx"], d["decay"], m, d["qsl"], d["slots"], d["has"],
+        decay_scale=c.scale, dfinal_states=df, dinitial_states=df)
+    live = [int(c.slots[b]) for b in range(len(lens)) if c.live[b]]
+    assert torch.equal(R.bits(df[live]), R.bits(di[live]))
+    for g, name in zip(again, ("dx", "dgate_a", "dgate_x")):
+        assert torch.equal(R.bits(g)[:, c.inside], R.bits(got[name])[:, c.inside])
+    assert torch.equal(R.bits(again[3]), R.bits(got["ddecay"]))
+    d["pool"] = c.pool.cuda()
+    x = d["x"]
+    lib.gated_linear_recurrence_varlen_fwd(x, d["ga"], d["gx"], d["decay"], d["pool"], d["qsl"],
+                                           d["slots"], d["has"], decay_scale=c.scale, out=x)
+    assert torch.equal(R.bits(x)[:, c.inside], R.bits(out)[:, c.inside])
+
+
+def test_recurrence_segments_equal_whole_sequences():
+    """The C entry without a workspace walks each sequence alone: the results of
+    both ways, held to one bound by the tests above, agree to a few units."""
+    c = Rec([1500, 900], 64, "f32", seed=31, inits=(0,))
+    d = c.gpu("token")
+    out, _ = c.forward(d, "token", marks=False)
+    from depthwise_causal_conv1d_amd import _lib
+    alone = torch.empty_like(d["x"])
+    pool = c.pool.cuda()
+    pl = lambda t: (t.data_ptr(), *t.stride())  # noqa: E731
+    rc = _lib.load().gated_linear_recurrence_varlen_fwd(
+        *pl(d["x"]), *pl(d["ga"]), *pl(d["gx"]), d["decay"].data_ptr(), 8.0, pool.data_ptr(),
+        pool.shape[0], pool.stride(0), d["qsl"].data_ptr(), 2, d["slots"].data_ptr(),
+        d["has"].view(torch.uint8).data_ptr(), *pl(alone), None, 0, None, 0, 64, c.T, 0, -1,
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    c.check_forward(alone, pool, "alone")
+    assert float((alone - out).abs().max()) <= float(2 * c.f["eh"].max())
+
+
 @pytest.mark.parametrize("layout", LAYOUTS)
 def test_recurrence_in_place_and_without_states(layout):
     c = Rec([300, 5, 600], 24, "bf16", seed=5)
@@ -379,6 +442,32 @@ def test_conv_gradients(W, silu, dtype, layout):
             R.check(d[int(slots[k])], ref["dinitial"][0][k], ref["dinitial"][1][k], f"dinitial {k}")
             d[int(slots[k])] = SENTINEL
     assert bool((d == SENTINEL).all()), "dinitial: wrote another slot"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[16, 0, 16, 48, 0], [0, 0, 3], [64, 64, 0, 128], [1] * 40, [0, 0],
+                                  [100, 2, 1, 0, 1, 1, 60]])
+def test_conv_gradients_at_strip_ends(lens, dtype):
+    """Rows cut into strips: sequences that end at a cut, are empty there, and
+    are shorter than the window; every initial state has a gradient."""
+    dim, n, dt = 34, len(lens), DT[dtype]
+    b = R.offsets(lens)
+    x, g = rand(1, dim, b[-1], dtype=dt), rand(2, dim, b[-1], dtype=dt)
+    w, bias = rand(3, dim, 4, dtype=dt, scale=0.5), rand(4, dim, dtype=dt)
+    first, end = rand(5, n, dim, 3, dtype=dt), rand(6, n, dim, 3, dtype=dt)
+    has = torch.tensor([k % 3 != 1 for k in range(n)])
+    ref = R.conv_grad(R.f64(g), R.f64(x), R.f64(w), R.f64(bias), b, True, R.f64(first), R.f64(end),
+                      R.f64(has.double()))
+    for layout in ("token", "channel"):
+        di = torch.empty(n, dim, 3, dtype=dt, device="cuda")
+        dx, dw, db = lib.causal_conv1d_varlen_bwd(
+            place(g, layout), place(x, layout), w.cuda(), bias.cuda(), first.cuda(),
+            torch.tensor(b, dtype=torch.int32, device="cuda"), None, has.cuda(), True,
+            dfinal_states=end.cuda(), dinitial_states=di)
+        R.check(dx, *ref["dx"], layout + " dx")
+        R.check(dw, *ref["dweight"], layout + " dweight")
+        R.check(db, *ref["dbias"], layout + " dbias")
+        R.check(di, *ref["dinitial"], layout + " dinitial")
 
 
 @pytest.mark.parametrize("layout", ["channel", "token"])
