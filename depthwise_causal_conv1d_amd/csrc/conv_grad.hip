@@ -10,7 +10,7 @@
 #include "column_sum.h"
 #include "lane_tokens.h"
 #include "row_lanes.h"
-#include "sconv_host.h"
+#include "plane_host.h"
 
 namespace sconv {
 
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(kStripWaves * 64) void conv_grad_rows_kernel(const 
   S* dx = static_cast<S*>(p.dx);
   for (int b = used ? first_sequence(p.qsl, p.batch, lo) : p.batch; b < p.batch; ++b) {
     const int start = p.qsl[b], end = p.qsl[b + 1];
-    if (start >= hi && !last) break;
+    if (start >= hi && !(last && p.dinitial)) break;  // an empty one has no other gradient
     const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
     const bool mine_first = start >= lo && (start < hi || last);
     const int from = start > lo ? start : lo, to = end < hi ? end : hi;
@@ -472,6 +472,8 @@ extern "C" int causal_conv1d_varlen_bwd(
     return fail(SCONV_ERR_INVALID, "%s: batch, dim and total_T must be >= 0", fn);
   if (total_T > INT32_MAX - 4096)  // token numbers are int32, as the offsets
     return fail(SCONV_ERR_UNSUPPORTED, "%s: total_T too large", fn);
+  if (dim > 1 << 28)  // a lane's byte offset in a row is 32 bits
+    return fail(SCONV_ERR_UNSUPPORTED, "%s: dim too large", fn);
   if (W < 1 || W > 4) return fail(SCONV_ERR_INVALID, "%s: W=%d outside [1, 4]", fn, W);
   if (!valid_dtype(dtype)) return fail(SCONV_ERR_INVALID, "%s: unknown dtype %d", fn, dtype);
   if (!valid_act(activation))

@@ -8,9 +8,10 @@
 #include <type_traits>
 
 #include "column_sum.h"
+#include "plane_host.h"
 #include "recurrence_device.h"
 #include "row_lanes.h"
-#include "sconv_host.h"
+
 namespace sconv {
 
 struct RecFwdParams {
@@ -406,11 +407,13 @@ __global__ __launch_bounds__(kFwdWaves * 64) void rec_fwd_rows_kernel(const RecF
 #pragma unroll
   for (int v = 0; v < V; ++v) d[v] = make_decay(p.decay[c + v], p.scale);
   int turn = 0;
-  const int b0 = SEG ? first_sequence(p.qsl, p.batch, lo) : p.sorted ? by_length(p.qsl, p.batch, (int)unit) : (int)unit;
+  const int b0 = SEG        ? first_sequence(p.qsl, p.batch, lo)
+                 : p.sorted ? by_length(p.qsl, p.batch, unit)
+                            : unit;
   const int b1 = SEG ? p.batch : b0 + 1;
   for (int b = b0; b < b1; ++b) {
     const Part s(p.qsl, b, lo, hi);
-    if (SEG && s.start >= hi && !last) break;
+    if (SEG && s.start >= hi && !(last && p.states)) break;  // nothing to keep of an empty one
     const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
     const bool opens = s.start >= lo;  // its first token, or its place if it has none
     if (slot == p.pad_slot_id || (s.from >= s.to && !(opens && s.start == s.end))) continue;
@@ -632,11 +635,13 @@ __global__ __launch_bounds__(kBwdWaves * 64) void rec_bwd_rows_kernel(const RecB
     acc[v] = 0.f;
   }
   int turn = 0;
-  const int b0 = SEG ? first_sequence(p.qsl, p.batch, lo) : p.sorted ? by_length(p.qsl, p.batch, (int)unit) : (int)unit;
+  const int b0 = SEG        ? first_sequence(p.qsl, p.batch, lo)
+                 : p.sorted ? by_length(p.qsl, p.batch, unit)
+                            : unit;
   const int b1 = SEG ? p.batch : b0 + 1;
   for (int b = b0; b < b1; ++b) {
     const Part q(p.qsl, b, lo, hi);
-    if (SEG && q.start >= hi && !last) break;
+    if (SEG && q.start >= hi && !(last && p.dinitial)) break;
     const int64_t slot = p.cache_indices ? (int64_t)p.cache_indices[b] : (int64_t)b;
     const bool opens = q.start >= lo;
     if (slot == p.pad_slot_id || (q.from >= q.to && !(opens && q.start == q.end))) continue;
@@ -965,6 +970,8 @@ static int rec_check(const char* fn, int32_t batch, int32_t dim, int64_t total_T
     return fail(SCONV_ERR_INVALID, "%s: batch, dim and total_T must be >= 0", fn);
   if (total_T > INT32_MAX - 4096)  // token numbers are int32, as the offsets
     return fail(SCONV_ERR_UNSUPPORTED, "%s: total_T too large", fn);
+  if (dim > 1 << 28)  // a lane's byte offset in a row is 32 bits
+    return fail(SCONV_ERR_UNSUPPORTED, "%s: dim too large", fn);
   if (!valid_dtype(dtype)) return fail(SCONV_ERR_INVALID, "%s: unknown dtype %d", fn, dtype);
   if (!(scale > 0.f) || !(scale <= 3.0e38f))
     return fail(SCONV_ERR_INVALID, "%s: decay_scale must be positive and finite", fn);
@@ -1012,13 +1019,15 @@ static int waves_per_pair(int64_t pairs, int64_t total_T, int32_t batch, int mos
 // Rows of a segment of the flat token axis for calls whose channels lie side
 // by side, or 0: a workgroup takes a whole sequence.
 // Segments cost a second read of the inputs, and pay where whole sequences
-// are too few workgroups, or too uneven ones: 8 ragged x 17409 x 4096 bf16
-// (512 workgroups) 209 us in segments, 239..383 without; 16 (1024) 201..209
-// and 138..163; 1 x 32768 x 1024 102 and 1727.  2048 workgroups instead of
-// 1024 were no faster (108 us for the last).
+// are too few workgroups, or too uneven ones, and long enough to be cut.
+// Measured, prefill, in segments and without: 8 ragged x 17409 x 4096 bf16 (512
+// workgroups) 209 and 239..383 us; 16 (1024) 201..209 and 138..163; 33 of 248
+// tokens x 1001 fp32 (528) 57 and 41..51; 16 of 256 x 1024 bf16 (256) 26 and
+// 36; 40 of 125 x 256 bf16 26..30 and 18..26; 1 x 32768 x 1024 102 and 1727.
+// 2048 segments' workgroups instead of 1024 were no faster (108 us for the last).
 static int64_t segment_rows(int64_t total_T, int32_t batch, int32_t dim) {
   const int64_t slabs = cdiv(dim, 64);
-  if (batch == 0 || total_T / batch < 8 * kTile || batch * slabs > 768) return 0;
+  if (batch == 0 || total_T / batch < 200 || batch * slabs > 512) return 0;
   const int64_t segments = cdiv(1024, slabs);
   const int64_t rows = cdiv(cdiv(total_T, segments), kTile) * kTile;
   return rows < 2 * kTile ? 2 * kTile : rows;

@@ -5,7 +5,7 @@
 //   s = x + residual, out = s * rsqrt(mean(s^2) + eps) * weight
 //   8 bits: scale = max |out| over a group / 448, code = e4m3(out / scale)
 #include "column_sum.h"
-#include "sconv_host.h"
+#include "plane_host.h"
 
 #include <initializer_list>
 #include <type_traits>

@@ -595,7 +595,8 @@ int gated_linear_recurrence_workspace(int64_t total_T, int32_t batch, int32_t di
  * Host errors (SCONV_ERR_INVALID): negative sizes, decay_scale not positive
  * and finite, NULL required pointer, unknown dtype, has_initial_state without
  * states, too few slots, checkpoint rows or workspace floats, overlapping buffers.
- * SCONV_ERR_UNSUPPORTED: batch * dim beyond one launch.
+ * SCONV_ERR_UNSUPPORTED: batch * dim beyond one launch, total_T above
+ * 2^31 - 4097, dim above 2^28.
  * batch == 0 or dim == 0 is a successful no-op.
  */
 int gated_linear_recurrence_varlen_fwd(
@@ -701,8 +702,8 @@ int causal_conv1d_varlen_bwd_workspace(int64_t total_T, int32_t batch, int32_t d
  *
  * Host errors (SCONV_ERR_INVALID): those of the forward, has_initial_state
  * without initial_states, too small a workspace, an output that overlaps
- * another buffer.  dim == 0 is a no-op; batch == 0 writes zeros to dweight
- * and dbias.
+ * another buffer.  SCONV_ERR_UNSUPPORTED: as gated_linear_recurrence_varlen_fwd.
+ * dim == 0 is a no-op; batch == 0 writes zeros to dweight and dbias.
  */
 int causal_conv1d_varlen_bwd(
     const void* dout, int64_t do_stride_c, int64_t do_stride_t, const void* x,

@@ -702,6 +702,108 @@ def test_layer_in_a_graph_and_on_another_stream():
             assert torch.equal(R.bits(side[k]), R.bits(eager[k])), (seed, k, "side stream")
 
 
+def test_strides_past_32_bits():
+    """Rows, channels and slots whose element offsets pass 2^31 and byte offsets
+    2^32: planes of one 9 GB buffer."""
+    step = (1 << 31) + 8  # elements between two rows (bf16)
+    big = torch.empty(2 * step + 4096, dtype=torch.bfloat16, device="cuda")
+
+    def far(shape, at, t=None):
+        v = big[at:].as_strided(shape, (step, 1))
+        return v if t is None else v.copy_(t)
+
+    bf = dict(dtype=torch.bfloat16)
+    x, w = rand(1, 3, 96, **bf), rand(2, 96, **bf)
+    y, ey = R.norm(R.f64(x), R.f64(w), 1e-6)
+    xd = far((3, 96), 0, x)
+    R.check(lib.rms_norm_fwd(xd, w.cuda(), 1e-6, out=far((3, 96), 256)), y, ey, "norm")
+    dx, _ = lib.rms_norm_bwd(xd, xd, w.cuda(), 1e-6, dx=far((3, 96), 512))
+    R.check(dx, *R.norm_grad(R.f64(x), R.f64(x), R.f64(w), 1e-6)["dx"], "norm dx")
+    # three tokens of rows of channels, three channels of tokens
+    for rows in (True, False):
+        turn = (lambda t: t.t()) if rows else (lambda t: t)
+        c = Rec([3] if rows else [100], 96 if rows else 3, "bf16", seed=3)
+        c.dfinal.zero_()
+        d = c.gpu("token" if rows else "channel")
+        shape = (3, 96) if rows else (3, 100)
+        d["x"] = turn(far(shape, 1024, turn(c.x)))
+        o, m = c.forward(d, None, out=turn(far(shape, 2048).fill_(SENTINEL)))
+        c.check_forward(o, d["pool"], "far")
+        dx, dga, _, _ = lib.gated_linear_recurrence_varlen_bwd(
+            d["dout"], d["x"], d["ga"], d["gx"], d["decay"], m, d["qsl"], d["slots"],
+            dx=turn(far(shape, 3072)))
+        ref = R.recurrence_grad(c.f, c.z(c.dout), c.z(c.x), c.decay, 8.0, c.bounds)
+        R.check(dx, *ref["dx"], "far dx")
+        R.check(dga, *ref["dgate_a"], "far dgate_a")
+        shape, T = ((3, 64), 3) if rows else ((3, 64), 64)
+        dim = 64 if rows else 3
+        g, x, w = rand(5, dim, T, **bf), rand(6, dim, T, **bf), rand(7, dim, 4, **bf)
+        ref = R.conv_grad(R.f64(g), R.f64(x), R.f64(w), torch.zeros(dim, dtype=torch.float64),
+                          [0, T], True)
+        q = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        dx, dw, _ = lib.causal_conv1d_varlen_bwd(
+            turn(far(shape, 0, turn(g))), turn(far(shape, 256, turn(x))), w.cuda(), None, None, q,
+            None, None, True, dx=turn(far(shape, 512)))
+        R.check(dx, *ref["dx"], "far conv dx")
+        R.check(dw, *ref["dweight"], "far conv dweight")
+    # far slots
+    c = Rec([1, 1], 96, "f32", seed=4, inits=(0, 1))
+    pool = big.view(torch.float32)[40:].as_strided((2, 96), ((1 << 31) - 64, 1)).copy_(c.h0)
+    row = lambda t: t.t().contiguous().cuda()  # noqa: E731
+    o = lib.gated_linear_recurrence_update(row(c.x), row(c.ga), row(c.gx), c.decay.cuda(), pool)
+    R.check(o.t(), c.f["h"], c.f["eh"], "far slots")
+    R.check(pool, c.f["last"], c.f["elast"], "far states")
+
+
+def test_two_streams_and_two_graphs_at_once():
+    """Calls in flight on two streams, and two captured graphs replayed in turn
+    and side by side, keep their own workspaces."""
+    _, d1, _ = layer_inputs(100, lens=(700, 600))
+    _, d2, _ = layer_inputs(110, lens=(700, 600))
+    want = [{k: v.clone() for k, v in layer_step({**d, "cstate": d["cstate"].clone()}).items()}
+            for d in (d1, d2)]
+    ins = [{**d, "sum": torch.empty_like(d["sum"]), "cstate": d["cstate"].clone()} for d in (d1, d2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [None, None]
+    for _ in range(5):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                got[k] = layer_step(ins[k])
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for n in want[k]:
+            assert torch.equal(R.bits(got[k][n]), R.bits(want[k][n])), (k, n, "streams")
+    graphs, held = [], []
+    for k in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(layer_step(ins[k]))
+        graphs.append(g)
+    for turn in range(4):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k if turn % 2 else 0]):
+                graphs[k].replay()
+        torch.cuda.synchronize()
+        for k in (0, 1):
+            for n in want[k]:
+                assert torch.equal(R.bits(held[k][n]), R.bits(want[k][n])), (turn, k, n, "graphs")
+
+
+def test_padded_batch_of_empty_sequences():
+    """A fixed batch whose tail has no tokens: states pass through, nothing else
+    is touched."""
+    for n in (1, 70):  # segments, whole sequences
+        lens = [900, 1300] + [0] * n
+        for layout in ("token", "channel"):
+            c = Rec(lens, 40, "f32", seed=50, inits=range(0, n + 2, 3), pads=range(n, n + 2), trail=9)
+            d = c.gpu(layout)
+            out, m = c.forward(d, layout)
+            c.check_forward(out, d["pool"], layout)
+            got, di = c.backward(d, m, layout)
+            c.check_backward(got, di, layout)
+
+
 def test_empty_calls():
     e = dict(dtype=torch.float32, device="cuda")
     q0 = torch.zeros(1, dtype=torch.int32, device="cuda")

@@ -74,6 +74,10 @@ def test_recurrence_forward_no_ops_and_limits(lib):
     assert fwd(lib, batch=0) == 0 and fwd(lib, dim=0) == 0
     # more threads than one launch takes, whatever the kernel
     assert fwd(lib, batch=1 << 30, dim=1 << 14, T=1, st=None, has=None, mk=None) == 2
+    # token numbers are int32, a channel's byte offset in a row 32 bits
+    assert fwd(lib, T=(1 << 31) - 4096) == 2 and bwd(lib, T=(1 << 31) - 4096) == 2
+    assert fwd(lib, dim=(1 << 28) + 1) == 2 and cgrad(lib, dim=(1 << 28) + 1) == 2
+    assert cgrad(lib, T=(1 << 31) - 4096) == 2
 
 
 def bwd(lib, **kw):
