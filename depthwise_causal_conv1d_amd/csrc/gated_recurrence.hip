@@ -839,7 +839,7 @@ __global__ __launch_bounds__(kMapWaves * 64) void rec_bwd_map_kernel(const RecBw
       const bool in = row0 + r < to;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float a = __builtin_amdgcn_exp2f(-d[v].k_log2 * sigmoid(af[v]));
+        const float a = __builtin_amdgcn_exp2f(d[v].k_log2 * sigmoid(af[v]));
         m.H[v] = in ? a * (m.H[v] + df[v]) : m.H[v];
         m.P[v] *= in ? a : 1.f;
       }

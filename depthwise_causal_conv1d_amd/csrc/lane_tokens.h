@@ -162,32 +162,48 @@ __device__ __forceinline__ float lane_move(float other, float v) {
                                                     ROWS, 0xF, false));
 }
 
-// One step of an inclusive scan: this lane's map after the moved lane's.
-template <int CTRL, int ROWS = 0xF>
-__device__ __forceinline__ void compose(float& P, float& H) {
-  const float p = lane_move<CTRL, ROWS>(1.0f, P), h = lane_move<CTRL, ROWS>(0.0f, H);
-  H = __builtin_fmaf(P, h, H);
-  P *= p;
-}
+// One step of an inclusive scan: this lane's map after that of the lane which
+// the DPP move names (lanes without one keep their own).  Two instructions
+// that take the move as an operand (the compiler made six: the identities,
+// the moves, the products); the wait is the one a DPP operand needs behind a
+// write.  P and H are written last by vector instructions, all lanes active.
+#define SCONV_COMPOSE(NAME, MOVE)                                      \
+  __device__ __forceinline__ void NAME(float& P, float& H) {           \
+    asm("s_nop 1\n\t"                                                  \
+        "v_fmac_f32_dpp %1, %1, %0 " MOVE " bank_mask:0xf\n\t"         \
+        "v_mul_f32_dpp %0, %0, %0 " MOVE " bank_mask:0xf"              \
+        : "+v"(P), "+v"(H));                                           \
+  }
+SCONV_COMPOSE(compose_shr1, "row_shr:1 row_mask:0xf")
+SCONV_COMPOSE(compose_shr2, "row_shr:2 row_mask:0xf")
+SCONV_COMPOSE(compose_shr4, "row_shr:4 row_mask:0xf")
+SCONV_COMPOSE(compose_shr8, "row_shr:8 row_mask:0xf")
+SCONV_COMPOSE(compose_bcast15, "row_bcast:15 row_mask:0xa")
+SCONV_COMPOSE(compose_bcast31, "row_bcast:31 row_mask:0xc")
+SCONV_COMPOSE(compose_shl1, "row_shl:1 row_mask:0xf")
+SCONV_COMPOSE(compose_shl2, "row_shl:2 row_mask:0xf")
+SCONV_COMPOSE(compose_shl4, "row_shl:4 row_mask:0xf")
+SCONV_COMPOSE(compose_shl8, "row_shl:8 row_mask:0xf")
+#undef SCONV_COMPOSE
 
 // Maps of lanes 0..l composed, in ascending lane order (row_shr 1, 2, 4, 8
 // inside rows of 16 lanes, then the last lane of a row to the next row, then
 // lane 31 to the upper half).
 __device__ __forceinline__ void scan_wave_up(float& P, float& H) {
-  compose<0x111>(P, H);
-  compose<0x112>(P, H);
-  compose<0x114>(P, H);
-  compose<0x118>(P, H);
-  compose<0x142, 0xA>(P, H);
-  compose<0x143, 0xC>(P, H);
+  compose_shr1(P, H);
+  compose_shr2(P, H);
+  compose_shr4(P, H);
+  compose_shr8(P, H);
+  compose_bcast15(P, H);
+  compose_bcast31(P, H);
 }
 
 // The same inside each row of 16 lanes, in descending lane order (row_shl).
 __device__ __forceinline__ void scan_row_down(float& P, float& H) {
-  compose<0x101>(P, H);
-  compose<0x102>(P, H);
-  compose<0x104>(P, H);
-  compose<0x108>(P, H);
+  compose_shl1(P, H);
+  compose_shl2(P, H);
+  compose_shl4(P, H);
+  compose_shl8(P, H);
 }
 
 __device__ __forceinline__ float last_lane(float v) {

@@ -21,7 +21,8 @@ constexpr int kMarkTokens = 64;  // tokens between two checkpoints of the state
 // Per-channel constants of the decay.
 struct Decay {
   float k;       // decay_scale * softplus(decay)
-  float k_log2;  // the same in powers of two
+  float k2;      // twice that
+  float k_log2;  // -k in powers of two
 };
 
 // softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) <= 1, to a few ulp.
@@ -44,7 +45,8 @@ __device__ __forceinline__ Decay make_decay(float decay, float scale) {
   const float sp = __builtin_fmaf(2.0f * z, s, decay > 0.f ? decay : 0.f);
   Decay d;
   d.k = scale * sp;
-  d.k_log2 = d.k * kLog2e;
+  d.k2 = 2.0f * d.k;
+  d.k_log2 = d.k * -kLog2e;
   return d;
 }
 
@@ -52,20 +54,18 @@ __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -kLog2e));
 }
 
-// 1 - a^2 from y = 2 log a <= 0 and a itself.  For y > -0.7 it is
-// -y (e^y - 1)/y with the quotient's Chebyshev interpolant of degree 5 on
-// [-0.7, 0] (relative error 1.1e-8, coefficients computed for this file);
-// below, 1 - a^2 >= 0.5 and the difference loses at most one bit.  A result
-// below the smallest normal number counts as zero.
-__device__ __forceinline__ float one_minus_square(float y, float a) {
-  float q = 1.0332433739677072e-3f;
-  q = __builtin_fmaf(q, y, 8.06795246899128e-3f);
-  q = __builtin_fmaf(q, y, 4.157276451587677e-2f);
-  q = __builtin_fmaf(q, y, 1.6665145754814148e-1f);
-  q = __builtin_fmaf(q, y, 4.9999910593032837e-1f);
-  q = __builtin_fmaf(q, y, 1.0f);
-  const float near = -y * q, far = __builtin_fmaf(-a, a, 1.0f);
-  return y > -0.7f ? near : far;
+// 1 - a^2 from w = -2 log a >= 0 and a itself.  For w < 0.35 it is
+// w (1 - e^-w)/w with the quotient's Chebyshev interpolant of degree 4
+// (relative error 1.4e-8, coefficients computed for this file); above,
+// 1 - a^2 >= 0.29 and the difference loses at most two bits.
+__device__ __forceinline__ float one_minus_square(float w, float a) {
+  float q = 7.211245596408844e-3f;
+  q = __builtin_fmaf(q, w, -4.133187234401703e-2f);
+  q = __builtin_fmaf(q, w, 1.6662530601024628e-1f);
+  q = __builtin_fmaf(q, w, -4.9999821186065674e-1f);
+  q = __builtin_fmaf(q, w, 1.0f);
+  const float near = w * q, far = __builtin_fmaf(-a, a, 1.0f);
+  return w < 0.35f ? near : far;
 }
 
 // One token's gates.
@@ -77,8 +77,8 @@ __device__ __forceinline__ Gates make_gates(float ga, float gx, const Decay& d) 
   Gates g;
   g.r = sigmoid(ga);
   g.i = sigmoid(gx);
-  g.a = __builtin_amdgcn_exp2f(-d.k_log2 * g.r);
-  g.m = __builtin_amdgcn_sqrtf(one_minus_square(-2.0f * d.k * g.r, g.a));
+  g.a = __builtin_amdgcn_exp2f(d.k_log2 * g.r);
+  g.m = __builtin_amdgcn_sqrtf(one_minus_square(d.k2 * g.r, g.a));
   return g;
 }
 
@@ -92,8 +92,8 @@ __device__ __forceinline__ GatesInv make_gates_inv(float ga, float gx, const Dec
   GatesInv g;
   g.r = sigmoid(ga);
   g.i = sigmoid(gx);
-  g.a = __builtin_amdgcn_exp2f(-d.k_log2 * g.r);
-  const float m2 = one_minus_square(-2.0f * d.k * g.r, g.a);
+  g.a = __builtin_amdgcn_exp2f(d.k_log2 * g.r);
+  const float m2 = one_minus_square(d.k2 * g.r, g.a);
   // Zero below the normal range, but a NaN stays one.
   const float inv = __builtin_amdgcn_rsqf(m2);
   g.inv_m = m2 < 1.17549435e-38f ? 0.0f : inv;
