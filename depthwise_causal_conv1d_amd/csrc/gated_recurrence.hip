@@ -52,8 +52,8 @@ struct RecBwdParams {
 };
 
 // The checkpoint row of sequence b's token start + rel (rel a multiple of
-// 64): rows of later sequences lie behind it, since a sequence of L tokens has
-// ceil(L / 64) of them and ends less than 64 ceil(L / 64) after its start.
+// 32): rows of later sequences lie behind it, since a sequence of L tokens has
+// ceil(L / 32) of them and ends less than 32 ceil(L / 32) after its start.
 __device__ __forceinline__ int64_t mark_row(int64_t start, int b, int64_t rel) {
   return start / kMarkTokens + b + rel / kMarkTokens;
 }
@@ -318,7 +318,7 @@ void rec_bwd_kernel(const RecBwdParams p) {
 // the segments before its own; a sequence that starts in a segment has its
 // initial state folded into that map, so a composition starts from zero.
 // The inputs are read twice then (14 bytes an element in bf16, not 8).
-constexpr int kTile = kMarkTokens;
+constexpr int kTile = 64;
 
 // First token at or after row `at` that starts a tile of the sequence.
 __device__ __forceinline__ int tile_start(int start, int at) {
@@ -465,11 +465,6 @@ __global__ __launch_bounds__(kFwdWaves * 64) void rec_fwd_rows_kernel(const RecF
       }
       maps[turn][wave][lane] = m;
       if (base + kAhead * kTile < s.to) fetch(which, base + kAhead * kTile);
-      if (p.marks && wave == 0 && live) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          p.marks[mark_row(s.start, b, base - s.start) * p.dim + c + v] = carry[v];
-      }
       __syncthreads();
       float h[V];
 #pragma unroll
@@ -482,6 +477,11 @@ __global__ __launch_bounds__(kFwdWaves * 64) void rec_fwd_rows_kernel(const RecF
         }
       }
       const uint32_t at = lane_offset(off);
+      if (p.marks && wave * R % kMarkTokens == 0 && live && row0 < s.end) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          p.marks[mark_row(s.start, b, row0 - s.start) * p.dim + c + v] = h[v];
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float y[V];
@@ -601,13 +601,19 @@ __global__ __launch_bounds__(kMapWaves * 64) void rec_fwd_map_kernel(const RecFw
 // The gradients, from the end: wave w takes the R rows of a tile that are
 // w R from its end.  The forward maps and the backward ones, which share
 // their factor, meet in LDS together.
-constexpr int kBwdWaves = 8;
+// Tiles of 64 tokens (eight waves) for whole sequences, whose chain of tiles
+// is what they wait for; of 32 (four waves) for segments, so that three
+// workgroups share a CU where eight waves leave room for one (8000 x 2048 bf16,
+// forward and gradients: 134 against 147 us; 33 ragged x 1001 fp32: 162 and 137).
+template <bool SEG>
+constexpr int kBwdWaves = SEG ? 4 : 8;
 
 template <typename D, int V, bool SEG>
-__global__ __launch_bounds__(kBwdWaves * 64) void rec_bwd_rows_kernel(const RecBwdParams p) {
+__global__ __launch_bounds__(kBwdWaves<SEG> * 64) void rec_bwd_rows_kernel(const RecBwdParams p) {
   using S = typename D::storage;
   using P_ = Pack<D, V>;
-  constexpr int NW = kBwdWaves, R = kTile / NW;
+  constexpr int NW = kBwdWaves<SEG>, R = 8, kBwdTile = NW * R;
+  static_assert(kBwdTile % kMarkTokens == 0, "a tile starts at a checkpoint");
   __shared__ RowMap<V> maps[2][NW][64];  // s -> P s + H
   __shared__ float mh[2][NW][V][64];     // h -> P h + mh
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -667,9 +673,9 @@ __global__ __launch_bounds__(kBwdWaves * 64) void rec_bwd_rows_kernel(const RecB
 #pragma unroll
       for (int v = 0; v < V; ++v) mark[v] = p.marks[mark_row(q.start, b, base - q.start) * p.dim + c + v];
     };
-    int base = q.start + (q.to - 1 - q.start) / kTile * kTile;
+    int base = q.start + (q.to - 1 - q.start) / kBwdTile * kBwdTile;
     if (q.to > q.from) fetch(base);
-    for (; q.to > q.from && base >= q.from; base -= kTile, turn ^= 1) {
+    for (; q.to > q.from && base >= q.from; base -= kBwdTile, turn ^= 1) {
       const int row0 = base + (NW - 1 - wave) * R;
       float g[R][V], xf[R][V], a[R][V], r[R][V], i[R][V], m[R][V], over[R][V];
       float P[V], H[V], T[V], h[V], s[V];
@@ -712,7 +718,7 @@ __global__ __launch_bounds__(kBwdWaves * 64) void rec_bwd_rows_kernel(const RecB
         mh[turn][wave][v][lane] = H[v];
       }
       maps[turn][wave][lane] = f;
-      if (base > q.from) fetch(base - kTile);
+      if (base > q.from) fetch(base - kBwdTile);
       __syncthreads();
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
@@ -952,12 +958,12 @@ static void launch_fwd_rows(const RecFwdParams& p, uint32_t grid, hipStream_t s)
 // One channel a lane: the rows of seven planes leave no registers for two.
 template <typename D>
 static void launch_bwd_rows(const RecBwdParams& p, uint32_t grid, hipStream_t s) {
-  const dim3 g(grid), th(kBwdWaves * 64), tm(kMapWaves * 64);
+  const dim3 g(grid), tm(kMapWaves * 64);
   if (p.seg_rows) {
     hipLaunchKernelGGL((rec_bwd_map_kernel<D, 1>), g, tm, 0, s, p);
-    hipLaunchKernelGGL((rec_bwd_rows_kernel<D, 1, true>), g, th, 0, s, p);
+    hipLaunchKernelGGL((rec_bwd_rows_kernel<D, 1, true>), g, dim3(kBwdWaves<true> * 64), 0, s, p);
   } else {
-    hipLaunchKernelGGL((rec_bwd_rows_kernel<D, 1, false>), g, th, 0, s, p);
+    hipLaunchKernelGGL((rec_bwd_rows_kernel<D, 1, false>), g, dim3(kBwdWaves<false> * 64), 0, s, p);
   }
 }
 
@@ -1273,7 +1279,7 @@ extern "C" int gated_linear_recurrence_varlen_bwd(
     p.saved = workspace + 2 * segments * dim;
     p.partial = workspace + 3 * segments * dim;
     const int64_t grid = parts * cdiv(dim, 64);
-    if (!valid_grid(grid, kBwdWaves * 64))
+    if (!valid_grid(grid, kMapWaves * 64))
       return fail(SCONV_ERR_UNSUPPORTED, "%s: batch * dim too large", fn);
     if (dtype == SCONV_BF16) launch_bwd_rows<Bf16>(p, (uint32_t)grid, stream);
     else launch_bwd_rows<F32>(p, (uint32_t)grid, stream);

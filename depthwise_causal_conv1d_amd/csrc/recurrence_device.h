@@ -16,7 +16,7 @@
 namespace sconv {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kMarkTokens = 64;  // tokens between two checkpoints of the state
+constexpr int kMarkTokens = 32;  // tokens between two checkpoints of the state
 
 // Per-channel constants of the decay.
 struct Decay {

@@ -554,9 +554,9 @@ int gather_intermediate_ssm_state(const void* states, int64_t num_chunks, int64_
  *
  * gated_linear_recurrence_checkpoint_rows -- rows of the checkpoint buffer
  * that a forward call leaves for its backward call:
- *     *rows = ceil(total_T / 64) + batch
+ *     *rows = ceil(total_T / 32) + batch
  * The buffer is fp32 [rows, dim], dense; row
- * start_b / 64 + b + i holds sequence b's state before its token 64 i.  Rows that
+ * start_b / 32 + b + i holds sequence b's state before its token 32 i.  Rows that
  * no sequence has are not written.  Host only; launches nothing.
  */
 int gated_linear_recurrence_checkpoint_rows(int64_t total_T, int32_t batch, int64_t* rows);

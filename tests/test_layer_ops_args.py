@@ -33,7 +33,7 @@ def err(lib):
 def fwd(lib, **kw):
     a = dict(x=X, xc=64, xt=1, ga=GA, gac=64, gat=1, gx=GX, gxc=64, gxt=1, decay=DEC, scale=8.0,
              st=ST, slots=4, ss=16, qsl=QSL, batch=2, idx=IDX, has=HAS, out=OUT, oc=64, ot=1,
-             mk=MK, rows=3, ws=None, wsn=0, dim=16, T=64, dt=0, pad=-1)
+             mk=MK, rows=4, ws=None, wsn=0, dim=16, T=64, dt=0, pad=-1)
     a.update(kw)
     return lib.gated_linear_recurrence_varlen_fwd(*a.values(), None)
 
@@ -45,7 +45,7 @@ def fwd(lib, **kw):
     (dict(x=None), "NULL"), (dict(ga=None), "NULL"), (dict(gx=None), "NULL"),
     (dict(out=None), "NULL"), (dict(decay=None), "NULL"), (dict(qsl=None), "NULL"),
     (dict(st=None), "without states"), (dict(slots=0), "slots"),
-    (dict(idx=None, slots=1), "slots"), (dict(ss=15), "slot stride"), (dict(rows=2), "checkpoints"),
+    (dict(idx=None, slots=1), "slots"), (dict(ss=15), "slot stride"), (dict(rows=3), "checkpoints"),
     (dict(xc=-1), "strides"), (dict(gat=-1), "strides"), (dict(oc=0), "each other"),
     (dict(oc=63), "each other"), (dict(out=X + 4), "overlaps x"), (dict(out=X, oc=65), "overlaps x"),
     (dict(out=GA), "gate"), (dict(out=GX), "gate"), (dict(st=OUT), "overlap"),
@@ -61,7 +61,7 @@ def test_recurrence_forward_workspace_refusals(lib):
     f = lib.gated_linear_recurrence_workspace
     assert f(65536, 1, 16, ctypes.byref(fwd_n), ctypes.byref(bwd_n)) == 0
     assert fwd_n.value > 0 and bwd_n.value > fwd_n.value
-    kw = dict(xc=1, xt=16, gac=1, gat=16, gxc=1, gxt=16, oc=1, ot=16, batch=1, T=65536, rows=1025)
+    kw = dict(xc=1, xt=16, gac=1, gat=16, gxc=1, gxt=16, oc=1, ot=16, batch=1, T=65536, rows=2049)
     assert fwd(lib, **kw, ws=WS, wsn=fwd_n.value - 1) == 1 and "workspace holds" in err(lib)
     assert fwd(lib, **kw, ws=X + 64, wsn=fwd_n.value) == 1 and "workspace overlaps" in err(lib)
     assert fwd(lib, **kw, ws=MK, wsn=fwd_n.value) == 1 and "workspace overlaps" in err(lib)
@@ -82,7 +82,7 @@ def test_recurrence_forward_no_ops_and_limits(lib):
 
 def bwd(lib, **kw):
     a = dict(do=DO, doc=64, dot=1, x=X, xc=64, xt=1, ga=GA, gac=64, gat=1, gx=GX, gxc=64, gxt=1,
-             decay=DEC, scale=8.0, mk=MK, rows=3, qsl=QSL, batch=2, idx=IDX, has=HAS, slots=4,
+             decay=DEC, scale=8.0, mk=MK, rows=4, qsl=QSL, batch=2, idx=IDX, has=HAS, slots=4,
              df=DF, dfs=16, di=DI, dis=16, dx=DX, dxc=64, dxt=1, dga=DGA, dgac=64, dgat=1, dgx=DGX,
              dgxc=64, dgxt=1, dd=DD, ws=WS, wsn=32, dim=16, T=64, dt=0, pad=-1)
     a.update(kw)
@@ -92,7 +92,7 @@ def bwd(lib, **kw):
 @pytest.mark.parametrize("kw,text", [
     (dict(batch=-1), ">= 0"), (dict(dt=5), "dtype"), (dict(scale=0.0), "decay_scale"),
     (dict(do=None), "NULL"), (dict(mk=None), "NULL"), (dict(dd=None), "NULL"),
-    (dict(ws=None), "NULL"), (dict(dga=None), "NULL"), (dict(rows=2), "checkpoints"),
+    (dict(ws=None), "NULL"), (dict(dga=None), "NULL"), (dict(rows=3), "checkpoints"),
     (dict(wsn=31), "workspace"), (dict(slots=0), "slots"), (dict(idx=None, slots=1), "slots"),
     (dict(dfs=8), "slot stride"), (dict(dis=8), "slot stride"), (dict(doc=-1), "strides"),
     (dict(dxt=0), "each other"), (dict(dx=X), "overlaps an input"), (dict(dx=DO), "overlaps an input"),
@@ -108,7 +108,7 @@ def test_recurrence_backward_refusals(lib, kw, text):
 def test_recurrence_checkpoint_rows(lib):
     n = ctypes.c_int64()
     f = lib.gated_linear_recurrence_checkpoint_rows
-    for T, b, want in ((0, 0, 0), (0, 3, 3), (1, 1, 2), (64, 1, 2), (65, 2, 4)):
+    for T, b, want in ((0, 0, 0), (0, 3, 3), (1, 1, 2), (32, 1, 2), (33, 2, 4)):
         assert f(T, b, ctypes.byref(n)) == 0 and n.value == want
     assert f(-1, 1, ctypes.byref(n)) == 1 and f(1, -1, ctypes.byref(n)) == 1 and f(1, 1, None) == 1
 
