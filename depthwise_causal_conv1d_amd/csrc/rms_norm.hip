@@ -380,33 +380,31 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(const NormBwdPar
       }
     }
   }
-  // the rows' sums of one channel in the order of the workgroup's waves
+  // the waves' sums of one channel, in the order of the waves
+  float* part = p.partial + (int64_t)blockIdx.x * p.dim;
   if constexpr (kRows > 1) {
-    __shared__ float lds[kRows][T * V];
+    constexpr int kWide = NV * T * V;
+    __shared__ float lds[kRows][kWide];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      __syncthreads();
 #pragma unroll
-      for (int e = 0; e < V; ++e) lds[mine][t * V + e] = dw[j][e];
-      __syncthreads();
-      if (mine == 0) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float a = 0.f;
-#pragma unroll
-          for (int q = 0; q < kRows; ++q) a += lds[q][t * V + e];
-          dw[j][e] = a;
-        }
-      }
+      for (int e = 0; e < V; ++e) lds[mine][(j * T + t) * V + e] = dw[j][e];
     }
-    if (mine != 0) return;
-  }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.dim; c += kNormThreads) {
+      float a = 0.f;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * T + t) * V;
-    if (c < p.dim) {
+      for (int q = 0; q < kRows; ++q) a += lds[q][c];
+      part[c] = a;
+    }
+  } else {
 #pragma unroll
-      for (int e = 0; e < V; ++e) p.partial[(int64_t)blockIdx.x * p.dim + c + e] = dw[j][e];
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * T + t) * V;
+      if (c < p.dim) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) part[c + e] = dw[j][e];
+      }
     }
   }
 }
