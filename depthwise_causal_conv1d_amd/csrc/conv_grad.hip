@@ -34,7 +34,7 @@ __device__ __forceinline__ float silu_grad(float z, float g) {
   return g * s * __builtin_fmaf(z, 1.0f - s, 1.0f);
 }
 
-// The three dz after a run of tokens, or before the first: dz of tokens
+// The W - 1 dz after a run of tokens, or before the first: dz of tokens
 // [t, t + W-1) of the sequence [start, end), from scalar loads.
 template <typename D, int W>
 struct Head {
@@ -73,6 +73,7 @@ struct Head {
 // above, and across chunks from a load and from the chunk done before.
 // Every byte of x and dout is read once; bound by that.  NW waves share a
 // sequence, each with a run of its chunks (one dz past a run is recomputed).
+// 8 x 4096 x 8192 bf16: 300 us with the sums' launch, 5.4 TB/s of 6 bytes an element.
 template <typename D, bool VEC, int W, int NW>
 __global__ __launch_bounds__(256, 4) void conv_grad_kernel(const ConvGradParams p) {
   using S = typename D::storage;
@@ -237,6 +238,8 @@ __global__ __launch_bounds__(256, 4) void conv_grad_kernel(const ConvGradParams 
 // complete once dz_{i+W-1} is known, so a strip reads W-1 rows before it and
 // W-1 after it again.  Strips lie on the flat token axis, whatever the
 // sequences' lengths: a wave takes every sequence that its strip meets.
+// 17409 x 4096 bf16: 115 us (83 at a copy's rate); 5003 x 1021 fp32: 19 us,
+// the latency of a strip's chain of loads.
 constexpr int kStripWaves = 4, kStripGroup = 8;
 
 template <typename D, int V, int W>

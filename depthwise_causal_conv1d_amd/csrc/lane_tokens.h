@@ -27,9 +27,8 @@ __device__ __forceinline__ uint32_t xcd_groups(uint32_t g, uint32_t G) {
   return (idx / N * 8 + xcd) * N + idx % N;
 }
 
-// Keeps the instructions before it and behind it apart.  Eight tokens' gates
-// have no order among them, and the compiler would start them all at once
-// and run out of registers: one or two at a time keep a lane busy.
+// Keeps the instructions before it and behind it apart, where the compiler
+// would start them all at once and hold more registers than it gains.
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // ---------------------------------------------------------------- eight tokens of a lane

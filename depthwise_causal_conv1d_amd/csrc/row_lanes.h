@@ -24,9 +24,10 @@ __device__ __forceinline__ uint32_t lane_offset(uint32_t bytes) {
 }
 
 // R rows [row0, row0 + R) of a plane, rows from `end` on read as row end - 1
-// (unused).  Ordinary loads: streaming ones cost 216 us where these take 154
-// (16 ragged sequences x 4096 bf16: 2-byte lanes), and read lines that two
-// workgroups share twice (8191 x 1001 fp32: 179 against 139 us).
+// (unused).  Ordinary loads: streaming ones read lines that two workgroups
+// share twice (8191 x 1001 fp32, forward and gradients: 176 against 134 us);
+// where rows are whole lines they gain 2% (16 ragged sequences x 4096 bf16,
+// prefill: 148 against 152 us).
 template <typename P, int R, typename S>
 __device__ __forceinline__ void load_rows(P (&v)[R], const S* plane, int64_t stride, int row0,
                                           int end, uint32_t bytes) {
@@ -34,7 +35,7 @@ __device__ __forceinline__ void load_rows(P (&v)[R], const S* plane, int64_t str
   const S* q = plane + (n > 0 ? row0 : end - 1) * stride;
   bytes = lane_offset(bytes);
   // (No second path for whole tiles: a branch between a load and its use makes
-  // the loads wait where the paths meet, 217 against 154 us.)
+  // the loads wait where the paths meet, 220 against 152 us.)
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     v[r].load(in_row(q, bytes));

@@ -19,7 +19,8 @@
  *   caller's contract and are stated per function; breaking them is
  *   undefined behaviour.
  * - Floating tensors of one call share one element type (sconv_dtype_t):
- *   x, weight, bias, cache / state pool and out.  Arithmetic is fp32.
+ *   x, weight, bias, cache / state pool and out, unless a function says that
+ *   one of them is fp32.  Arithmetic is fp32.
  * - SCONV_ERR_HIP reports a launch error taken from hipGetLastError().
  */
 #ifndef SCONV_H
