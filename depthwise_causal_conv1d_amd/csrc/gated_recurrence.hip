@@ -1133,6 +1133,10 @@ extern "C" int gated_linear_recurrence_varlen_fwd(
   if (workspace && workspace_floats < need)
     return fail(SCONV_ERR_INVALID, "%s: workspace holds %lld floats, %lld needed", fn,
                 (long long)workspace_floats, (long long)need);
+  const int64_t db = (int64_t)dim * 4;
+  if (overlap(decay, db, out, po.bytes()) || overlap(decay, db, states, sb) ||
+      overlap(decay, db, checkpoints, mb) || overlap(decay, db, workspace, wb))
+    return fail(SCONV_ERR_INVALID, "%s: an output overlaps decay", fn);
   if (overlap(workspace, wb, x, px.bytes()) || overlap(workspace, wb, gate_a, pa.bytes()) ||
       overlap(workspace, wb, gate_x, pg.bytes()) || overlap(workspace, wb, out, po.bytes()) ||
       overlap(workspace, wb, states, sb) || overlap(workspace, wb, checkpoints, mb))
@@ -1247,6 +1251,7 @@ extern "C" int gated_linear_recurrence_varlen_bwd(
       if (planes_overlap(ou[i], ou[j]))
         return fail(SCONV_ERR_INVALID, "%s: two gradients overlap", fn);
     if (overlap(ou[i].p, ou[i].bytes(), checkpoints, mb) ||
+        overlap(ou[i].p, ou[i].bytes(), decay, (int64_t)dim * 4) ||
         overlap(ou[i].p, ou[i].bytes(), dfinal_states, dfb))
       return fail(SCONV_ERR_INVALID, "%s: a gradient overlaps an input", fn);
   }
@@ -1344,6 +1349,9 @@ extern "C" int gated_linear_recurrence_update(
   if (overlap(states, sb, x, px.bytes()) || overlap(states, sb, gate_a, pa.bytes()) ||
       overlap(states, sb, gate_x, pg.bytes()) || overlap(states, sb, out, po.bytes()))
     return fail(SCONV_ERR_INVALID, "%s: states overlap another buffer", fn);
+  if (overlap(decay, (int64_t)dim * 4, out, po.bytes()) ||
+      overlap(decay, (int64_t)dim * 4, states, sb))
+    return fail(SCONV_ERR_INVALID, "%s: an output overlaps decay", fn);
   RecUpdParams p = {};
   p.x = x; p.ga = gate_a; p.gx = gate_x; p.decay = decay; p.states = states;
   p.idx = state_indices; p.out = out; p.x_rs = px.st; p.ga_rs = pa.st; p.gx_rs = pg.st;

@@ -243,3 +243,17 @@ def test_binding_wants_gpu_tensors_of_one_type_and_shape():
         sc.rms_norm_quant(x, torch.zeros(8), group_size=3)
     with pytest.raises(TypeError):
         sc.rms_norm_fwd(x, torch.zeros(8), out=torch.zeros(4, 8, dtype=torch.bfloat16))
+
+
+def test_recurrence_outputs_do_not_overlap_decay(lib):
+    """Every channel of every workgroup reads decay while others write."""
+    rows = dict(xc=1, xt=16, gac=1, gat=16, gxc=1, gxt=16, oc=1, ot=16, batch=1, T=65536, rows=2049)
+    fwd_n, bwd_n = ctypes.c_int64(), ctypes.c_int64()
+    assert lib.gated_linear_recurrence_workspace(65536, 1, 16, ctypes.byref(fwd_n),
+                                                 ctypes.byref(bwd_n)) == 0
+    calls = [lambda: fwd(lib, decay=OUT), lambda: fwd(lib, decay=ST + 60), lambda: fwd(lib, decay=MK),
+             lambda: fwd(lib, **rows, decay=WS, ws=WS, wsn=fwd_n.value),
+             lambda: upd(lib, decay=OUT + 16), lambda: upd(lib, decay=ST)]
+    calls += [lambda k=k: bwd(lib, decay=k) for k in (DX, DGA + 4, DGX, DI, DD, WS)]
+    for k, call in enumerate(calls):
+        assert call() == 1 and "overlap" in err(lib), (k, err(lib))
