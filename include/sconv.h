@@ -549,9 +549,9 @@ int gather_intermediate_ssm_state(const void* states, int64_t num_chunks, int64_
  * checkpoints and every gradient of them are fp32, and so is the arithmetic.
  * Packing, state slots, PAD and has_initial_state are those of
  * causal_conv1d_varlen_fwd.  Planes are [dim, total_T] at any strides >= 0
- * (out and gradients: no two elements in one place): tokens contiguous
- * (channel-major) and channels contiguous (rows of tokens) with 16-byte
- * aligned rows run with vector lanes.
+ * (out and gradients: no two elements in one place): the fast forms are tokens
+ * contiguous (channel-major) and channels contiguous (rows of tokens), both at
+ * any alignment; other strides load one element at a time.
  *
  * gated_linear_recurrence_checkpoint_rows -- rows of the checkpoint buffer
  * that a forward call leaves for its backward call:
