@@ -1039,7 +1039,7 @@ static int waves_per_pair(int64_t pairs, int64_t total_T, int32_t batch, int mos
 // 2048 segments' workgroups instead of 1024 were no faster (108 us for the last).
 static int64_t segment_rows(int64_t total_T, int32_t batch, int32_t dim) {
   const int64_t slabs = cdiv(dim, 64);
-  if (batch == 0 || total_T / batch < 200 || batch * slabs > 512) return 0;
+  if (batch == 0 || dim == 0 || total_T / batch < 200 || batch * slabs > 512) return 0;
   const int64_t segments = cdiv(1024, slabs);
   const int64_t rows = cdiv(cdiv(total_T, segments), kTile) * kTile;
   return rows < 2 * kTile ? 2 * kTile : rows;
