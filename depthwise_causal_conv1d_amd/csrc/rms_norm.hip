@@ -83,17 +83,36 @@ __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xFF);
 }
 
-// V codes of v * inv, one store.
+// V codes of v / scale, one store.  The quotient is the nearest fp32 one: the
+// product with 1 / scale alone falls on the other side of a border between
+// two codes now and then.  The product's remainder mends it (exact, since
+// it is a multiple of the last place of v) where no place is lost below fp32's
+// range; there, and at an infinite or NaN scale, the division itself
+// (everywhere: 103 against 101 us for 17408 x 4096 bf16, 11.6 against 11.0 for
+// 4096 x 1001 fp32).
+constexpr float kFp8NearScale = 8.0779357e-28f;  // 2^-90
 template <int V>
-__device__ __forceinline__ void store_codes(uint8_t* q, const float (&v)[V], float inv) {
+__device__ __forceinline__ void store_codes(uint8_t* q, const float (&v)[V], float scale) {
+  float y[V];
+  if (scale >= kFp8NearScale && scale < INFINITY) {
+    const float inv = 1.0f / scale;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float near = v[e] * inv;
+      y[e] = __builtin_fmaf(__builtin_fmaf(-scale, near, v[e]), inv, near);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[e] = v[e] / scale;
+  }
   if constexpr (V == 1) {
-    *q = to_e4m3(v[0] * inv);
+    *q = to_e4m3(y[0]);
   } else {
     uint32_t w[V / 4];
 #pragma unroll
     for (int e = 0; e < V; e += 4) {
-      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[e] * inv, v[e + 1] * inv, 0, false);
-      w[e / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[e + 2] * inv, v[e + 3] * inv, lo, true);
+      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[e], y[e + 1], 0, false);
+      w[e / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[e + 2], y[e + 3], lo, true);
     }
     __builtin_memcpy(__builtin_assume_aligned(q, V), w, V);
   }
@@ -120,7 +139,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_simple(const NormParams
   const float mean = block_sum(sq, lds) / (float)p.dim;
   const float rstd = 1.0f / sqrtf(mean + p.eps);
   for (int g = 0; g < p.dim; g += p.group) {
-    float inv = 1.f;
+    float scale = 1.f;
     if constexpr (Q) {
       if (threadIdx.x == 0) amax = 0;
       __syncthreads();
@@ -129,8 +148,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_simple(const NormParams
         m = max(m, abs_bits(at(c) * rstd * load_as_float<D>(w + c)));
       atomicMax(&amax, m);
       __syncthreads();
-      const float scale = scale_of(amax);
-      inv = 1.0f / scale;
+      scale = scale_of(amax);
       if (threadIdx.x == 0) p.scales[row * p.sc_rs + g / p.group] = scale;
       __syncthreads();
     }
@@ -138,7 +156,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_simple(const NormParams
       const float v = at(c);
       const float y = v * rstd * load_as_float<D>(w + c);
       if (sum) sum[c] = norm_round<D>(v);
-      if constexpr (Q) static_cast<uint8_t*>(p.out)[row * p.o_rs + c] = to_e4m3(y * inv);
+      if constexpr (Q) static_cast<uint8_t*>(p.out)[row * p.o_rs + c] = to_e4m3(y / scale);
       else static_cast<S*>(p.out)[row * p.o_rs + c] = norm_round<D>(y);
     }
   }
@@ -215,7 +233,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(const NormParams
       if constexpr (Q && G == 0) amax = Max()(amax, c < p.dim ? abs_bits(s[j][e]) : 0u);
     }
   }
-  float inv = 0.f;
+  float scale = 1.f;
   if constexpr (Q && G == 0) {
     amax = lanes_reduce<64>(amax, Max());
     if constexpr (kWaves > 1) {
@@ -224,8 +242,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(const NormParams
 #pragma unroll
       for (int i = 0; i < kWaves; ++i) amax = Max()(amax, lmax[i]);
     }
-    const float scale = scale_of(amax);
-    inv = 1.0f / scale;
+    scale = scale_of(amax);
     if (t == 0) p.scales[row * p.sc_rs] = scale;
   }
 #pragma unroll
@@ -236,11 +253,10 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(const NormParams
         amax = 0;
 #pragma unroll
         for (int e = 0; e < V; ++e) amax = Max()(amax, abs_bits(s[j][e]));
-        const float scale = scale_of(lanes_reduce<(G > 0 ? G : 1)>(amax, Max()));
-        inv = 1.0f / scale;
+        scale = scale_of(lanes_reduce<(G > 0 ? G : 1)>(amax, Max()));
         if (t % (G > 0 ? G : 1) == 0 && c < p.dim) p.scales[row * p.sc_rs + c / p.group] = scale;
       }
-      if (c < p.dim) store_codes(static_cast<uint8_t*>(p.out) + row * p.o_rs + c, s[j], inv);
+      if (c < p.dim) store_codes(static_cast<uint8_t*>(p.out) + row * p.o_rs + c, s[j], scale);
     } else if (c < p.dim) {
       P o;
       o.from_float(s[j]);

@@ -725,9 +725,10 @@ int causal_conv1d_varlen_bwd(
  *     y = s / sqrt(mean(s^2) + eps) * weight
  *   out_dtype == dtype:       out = y
  *   out_dtype == SCONV_E4M3:  per group of group_size channels (0: the whole
- *     row) scale = max(max |y| / 448, 2^-126), out = y / scale in e4m3, and
- *     scales[row, group] = scale; y is not rounded before.  A NaN in a group
- *     makes its scale and all its codes NaN.
+ *     row) scale = max(max |y| / 448, 2^-126) to a step of fp32, and
+ *     scales[row, group] = scale; out = y / scale, the nearest fp32 quotient by
+ *     the scale as it is stored, in e4m3 (to nearest even); y is not rounded
+ *     before.  A NaN in a group makes its scale and all its codes NaN.
  *
  *   x, residual, residual_out, out  [rows, dim] rows of their strides,
  *            channels contiguous; weight [dim]; x, residual, weight and
