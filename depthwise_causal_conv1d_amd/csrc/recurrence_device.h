@@ -28,8 +28,13 @@ struct Decay {
 // softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) <= 1, to a few ulp.
 // log1p(e) = 2 artanh(z), z = e / (2 + e) <= 1/3, by its power series.  The
 // product |v| log2 e is carried in two parts, or exp would lose |v| / 2 ulp.
+// |v| ends at 200, where e is zero already: the parts of an infinite product
+// would be inf - inf.  k ends at 2^126, where a is zero at every gate above
+// -80: times a closed gate's r = 0 it is zero, which an infinity is not.
+// (Both comparisons leave a NaN as it is.)
+constexpr float kMaxDecay = 8.50705917e37f;  // 2^126
 __device__ __forceinline__ Decay make_decay(float decay, float scale) {
-  const float v = -__builtin_fabsf(decay);
+  const float least = -__builtin_fabsf(decay), v = least < -200.0f ? -200.0f : least;
   const float t = v * kLog2e;
   const float rest = __builtin_fmaf(v, kLog2e, -t) + v * 1.92596299e-8f;  // log2 e - kLog2e
   float e = __builtin_amdgcn_exp2f(t);
@@ -44,7 +49,7 @@ __device__ __forceinline__ Decay make_decay(float decay, float scale) {
   s = __builtin_fmaf(s, w, 1.0f);
   const float sp = __builtin_fmaf(2.0f * z, s, decay > 0.f ? decay : 0.f);
   Decay d;
-  d.k = scale * sp;
+  d.k = scale * sp > kMaxDecay ? kMaxDecay : scale * sp;
   d.k2 = 2.0f * d.k;
   d.k_log2 = d.k * -kLog2e;
   return d;

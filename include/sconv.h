@@ -547,6 +547,8 @@ int gather_intermediate_ssm_state(const void* states, int64_t num_chunks, int64_
  *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x[c, t],   out[c, t] = h_t
  * x, the gates and out share one element type; decay, the states, the
  * checkpoints and every gradient of them are fp32, and so is the arithmetic.
+ * decay = -inf gives a = 1 (the state is kept, no input enters), +inf gives a = 0
+ * (at a gate_a below -80, whose sigmoid ends fp32's range, a value up to one).
  * Packing, state slots, PAD and has_initial_state are those of
  * causal_conv1d_varlen_fwd.  Planes are [dim, total_T] at any strides >= 0
  * (out and gradients: no two elements in one place): the fast forms are tokens

@@ -7,6 +7,8 @@ import pytest
 import torch
 
 import depthwise_causal_conv1d_amd as lib
+from tests import layer_ref as R
+from tests.test_gpu_layer_ops import NAN, Rec
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +67,41 @@ def test_codes_are_the_quotient_rounded_once(dim, group, odd):
     codes = (y / sc[:, :, None]).to(torch.float8_e4m3fn).view(3, dim)
     got, want = q.cpu().view(torch.uint8), codes.view(torch.uint8)
     assert torch.equal(got, want), f"{int((got != want).sum())} of {got.numel()} codes"
+
+
+# ---------------------------------------------------------------- ends of decay's range
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["channel", "token", "strided"])
+@pytest.mark.parametrize("lens", [[300, 5], [700, 900]])
+def test_recurrence_at_the_ends_of_decay(lens, layout, dtype):
+    """decay = -inf keeps the state and takes no input in (a = 1), +inf keeps
+    nothing (a = 0); so do finite values past the range in which softplus
+    differs from those.  A NaN stays in its channel."""
+    ends = [float("-inf"), -3.0e38, -200.0, float("inf"), 3.0e38, 1.0e6, NAN]
+    near = [-800.0, -800.0, -800.0, 1.0e6, 1.0e6, 1.0e6, 0.0]  # the same a and m in 64 bits
+    c = Rec(lens, 9, dtype, seed=60, inits=(0, 1), gate_scale=1.0)
+    c.decay[:7] = torch.tensor(near)
+    c.f = R.recurrence(c.z(c.x), c.z(c.ga), c.z(c.gx), c.decay, c.scale, c.bounds, R.f64(c.h0))
+    ref = R.recurrence_grad(c.f, c.z(c.dout), c.z(c.x), c.decay, c.scale, c.bounds, R.f64(c.dfinal),
+                            R.f64(c.has.double()))
+    d = c.gpu(layout)
+    d["decay"][:7] = torch.tensor(ends, device="cuda")
+    out, m = c.forward(d, layout)
+    got, di = c.backward(d, m, layout)
+    live = [0, 1, 2, 3, 4, 5, 7, 8]
+    o = out.cpu()
+    R.check(o[live], c.f["h"][live], c.f["eh"][live], "out")
+    slots = c.slots.long()
+    R.check(d["pool"].cpu()[slots][:, live], c.f["last"][:, live], c.f["elast"][:, live], "states")
+    R.check(di.cpu()[slots][:, live], *(t[:, live] for t in ref["dinitial"]), "dinitial")
+    for n in ("dx", "dgate_a", "dgate_x"):
+        R.check(got[n].cpu()[live], *(t[live] for t in ref[n]), n)
+    R.check(got["ddecay"].cpu()[live], *(t[live] for t in ref["ddecay"]), "ddecay")
+    assert bool(o[6].isnan().all()) and bool(got["ddecay"][6].isnan())
+    # one token
+    pool, slots = c.pool.cuda(), c.slots.cuda()
+    first = [d[k].t()[[c.bounds[0], c.bounds[1]]].contiguous() for k in ("x", "ga", "gx")]
+    one = lib.gated_linear_recurrence_update(*first, d["decay"], pool, slots)
+    R.check(one.t()[live], c.f["h"][live][:, c.bounds[:2]], c.f["eh"][live][:, c.bounds[:2]], "update")
+    assert bool(one[:, 6].isnan().all())
