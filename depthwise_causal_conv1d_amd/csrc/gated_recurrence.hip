@@ -744,6 +744,11 @@ __global__ __launch_bounds__(kBwdWaves<SEG> * 64) void rec_bwd_rows_kernel(const
         }
       }
       const uint32_t at = lane_offset(off);
+      // ddecay's terms of a tile first, then the tiles: T / 64 + 8 additions
+      // behind one another, not T / 8
+      float part[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) part[v] = 0.f;
 #pragma unroll
       for (int k = R - 1; k >= 0; --k) {
         float ox[V], oa[V], og[V];
@@ -753,7 +758,7 @@ __global__ __launch_bounds__(kBwdWaves<SEG> * 64) void rec_bwd_rows_kernel(const
           s[v] = a[k][v] * dh;
           ox[v] = dh * (m[k][v] * i[k][v]);
           const float dlog = s[v] * over[k][v];
-          acc[v] = __builtin_fmaf(dlog, r[k][v], acc[v]);
+          part[v] = __builtin_fmaf(dlog, r[k][v], part[v]);
           og[v] = ox[v] * xf[k][v] * (1.f - i[k][v]);
           oa[v] = -d[v].k * dlog * (r[k][v] * (1.f - r[k][v]));
         }
@@ -768,6 +773,8 @@ __global__ __launch_bounds__(kBwdWaves<SEG> * 64) void rec_bwd_rows_kernel(const
           o.store_nt(in_row(dga + row * p.dga_st, at));
         }
       }
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += part[v];
     }
     if (p.dinitial && opens && wave == 0 && live) {
       const bool init = p.has_init && p.has_init[b] != 0;

@@ -8,7 +8,7 @@ import torch
 
 import depthwise_causal_conv1d_amd as lib
 from tests import layer_ref as R
-from tests.test_gpu_layer_ops import NAN, Rec
+from tests.test_gpu_layer_ops import NAN, Rec, place
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +105,37 @@ def test_recurrence_at_the_ends_of_decay(lens, layout, dtype):
     one = lib.gated_linear_recurrence_update(*first, d["decay"], pool, slots)
     R.check(one.t()[live], c.f["h"][live][:, c.bounds[:2]], c.f["eh"][live][:, c.bounds[:2]], "update")
     assert bool(one[:, 6].isnan().all())
+
+
+# ---------------------------------------------------------------- long sums
+
+def test_recurrence_ddecay_of_a_long_sequence():
+    """Equal terms whose roundings do not cancel, over one sequence of 60000 rows
+    among empty ones (a mean too short for segments): within the bound of T / 64 + 64 +
+    batch additions behind one another."""
+    T, batch = 60000, 301
+    k = 8.0 * torch.nn.functional.softplus(torch.tensor(-1.0))
+    r, i = torch.sigmoid(torch.tensor(0.5)), torch.sigmoid(torch.tensor(0.25))
+    a = torch.exp(-k * r)
+    m = torch.sqrt(-torch.expm1(-2 * k * r))
+    # gradients whose term of the sum, added to itself T / 8 times, is furthest off
+    grid = 1.0 + torch.arange(4096) / 4096
+    term = a * grid / (1 - a) * (m * i * 0.75 / (1 - a) - a * i * 0.75 / m) * r
+    acc = torch.zeros(4096)
+    for _ in range(T // 8):
+        acc += term
+    worst = (acc.double() / term.double() - T // 8).abs().topk(16).indices
+    dim = 16
+    one = torch.ones(dim, T)
+    x, ga, gx, dout = one * 0.75, one * 0.5, one * 0.25, one * grid[worst][:, None]
+    decay = torch.full((dim,), -1.0)
+    bounds = [0] + [T] * batch
+    f = R.recurrence(R.f64(x), R.f64(ga), R.f64(gx), decay, 8.0, bounds)
+    ref = R.recurrence_grad(f, R.f64(dout), R.f64(x), decay, 8.0, bounds)["ddecay"]
+    q = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    for layout in ("token", "channel"):
+        d = [place(t, layout) for t in (dout, x, ga, gx)]
+        marks = lib.gated_linear_recurrence_checkpoints(d[1], q)
+        lib.gated_linear_recurrence_varlen_fwd(*d[1:], decay.cuda(), None, q, checkpoints=marks)
+        dd = lib.gated_linear_recurrence_varlen_bwd(*d, decay.cuda(), marks, q)[3]
+        R.check(dd, *ref, layout)
