@@ -549,6 +549,9 @@ int gather_intermediate_ssm_state(const void* states, int64_t num_chunks, int64_
  * checkpoints and every gradient of them are fp32, and so is the arithmetic.
  * decay = -inf gives a = 1 (the state is kept, no input enters), +inf gives a = 0
  * (at a gate_a below -80, whose sigmoid ends fp32's range, a value up to one).
+ * From an infinite x, or from the start at an infinite initial state, the rest
+ * of that channel's sequence is not finite: infinite, or NaN where the product of
+ * the decays between has become zero in fp32 (which depends on the layout).
  * Packing, state slots, PAD and has_initial_state are those of
  * causal_conv1d_varlen_fwd.  Planes are [dim, total_T] at any strides >= 0
  * (out and gradients: no two elements in one place): the fast forms are tokens

@@ -107,6 +107,33 @@ def test_recurrence_at_the_ends_of_decay(lens, layout, dtype):
     assert bool(one[:, 6].isnan().all())
 
 
+@pytest.mark.parametrize("layout", ["channel", "token", "strided"])
+@pytest.mark.parametrize("lens", [[700, 40], [1400, 600]])
+def test_recurrence_infinite_input_and_state(lens, layout):
+    """From an infinite input, or from the start where the initial state is
+    infinite, the rest of its sequence in that channel is not finite (infinite or
+    NaN); everything else is as without it, to the bit."""
+    c = Rec(lens, 8, "f32", seed=61, inits=(0, 1))
+    d = c.gpu(layout)
+    base, _ = c.forward(d, layout, marks=False)
+    base_pool, d["pool"] = d["pool"], c.pool.cuda()
+    d["x"][3, 100] = float("inf")
+    d["x"][4, lens[0] + 7] = float("-inf")
+    d["pool"][int(c.slots[1]), 5] = float("inf")
+    out, _ = c.forward(d, layout, marks=False)
+    hit = torch.zeros(8, c.T, dtype=torch.bool)
+    hit[3, 100:lens[0]] = hit[4, lens[0] + 7:] = hit[5, lens[0]:] = True
+    o = out.cpu()
+    assert not bool(o[hit].isfinite().any())
+    assert torch.equal(R.bits(o)[~hit], R.bits(base)[~hit])
+    p, want = d["pool"].cpu(), base_pool.cpu()
+    for b, ch in ((0, 3), (1, 4), (1, 5)):
+        s = int(c.slots[b])
+        assert not bool(p[s, ch].isfinite())
+        p[s, ch] = want[s, ch] = 0
+    assert torch.equal(R.bits(p), R.bits(want))
+
+
 # ---------------------------------------------------------------- long sums
 
 def test_recurrence_ddecay_of_a_long_sequence():
