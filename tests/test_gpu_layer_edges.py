@@ -8,7 +8,7 @@ import torch
 
 import depthwise_causal_conv1d_amd as lib
 from tests import layer_ref as R
-from tests.test_gpu_layer_ops import NAN, Rec, place
+from tests.test_gpu_layer_ops import DT, NAN, Rec, check_codes, place, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +166,113 @@ def test_recurrence_ddecay_of_a_long_sequence():
         lib.gated_linear_recurrence_varlen_fwd(*d[1:], decay.cuda(), None, q, checkpoints=marks)
         dd = lib.gated_linear_recurrence_varlen_bwd(*d, decay.cuda(), marks, q)[3]
         R.check(dd, *ref, layout)
+
+
+# ---------------------------------------------------------------- variants of large calls
+
+def some_channels(dim, n=8):
+    """The first and last channels and some between: each is computed for itself."""
+    return torch.unique(torch.cat([torch.arange(min(n, dim)), torch.arange(max(0, dim - n), dim),
+                                   torch.randint(0, dim, (n,), generator=torch.Generator().manual_seed(dim))]))
+
+
+# Whole sequences in rows, the longest first, in both passes (more than 512
+# workgroups, 512 tokens a sequence and more); a wave for each channel of long
+# sequences, with the launch held to three workgroups a CU (8192 channels in all
+# and more, 2048 tokens a sequence); four and sixteen waves for one.
+LARGE = [
+    ("token", [512, 700, 3, 900, 0, 640, 1100, 64, 800], 4096),
+    ("token_odd", [512, 700, 3, 900, 0, 640, 1100, 64, 800], 4001),
+    ("channel", [3000, 1, 4000, 1500], 2048),
+    ("channel_odd", [3000, 1, 4000, 1500], 2049),
+    ("channel", [2000, 1, 1500], 1024),
+    ("channel", [4500], 300),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("which", range(len(LARGE)))
+def test_recurrence_in_large_calls(which, dtype):
+    layout, lens, dim = LARGE[which]
+    dt, n = DT[dtype], len(lens)
+    b = R.offsets(lens)
+    T = b[-1]
+    x, ga, gx, dout = (rand(70 + k, dim, T, dtype=dt) for k in range(4))
+    decay = rand(75, dim) * 0.5 - 4
+    h0, end = rand(76, n, dim), rand(77, n, dim)
+    has = torch.tensor([k % 2 == 0 for k in range(n)])
+    d = [place(t, layout) for t in (dout, x, ga, gx)]
+    q, states = torch.tensor(b, dtype=torch.int32, device="cuda"), h0.cuda()
+    marks = lib.gated_linear_recurrence_checkpoints(d[1], q)
+    out = place(torch.full_like(x, NAN), layout)
+    lib.gated_linear_recurrence_varlen_fwd(*d[1:], decay.cuda(), states, q, None, has.cuda(),
+                                           checkpoints=marks, out=out)
+    grads = {k: place(torch.full_like(x, NAN), layout) for k in ("dx", "dgate_a", "dgate_x")}
+    di = torch.empty_like(states)
+    dd = lib.gated_linear_recurrence_varlen_bwd(
+        *d, decay.cuda(), marks, q, None, has.cuda(), dfinal_states=end.cuda(), dinitial_states=di,
+        **grads)[3]
+    ch = some_channels(dim)
+    z = lambda t: R.f64(t[ch])  # noqa: E731
+    f = R.recurrence(z(x), z(ga), z(gx), decay[ch], 8.0, b, R.f64(h0[:, ch]) * has[:, None])
+    ref = R.recurrence_grad(f, z(dout), z(x), decay[ch], 8.0, b, R.f64(end[:, ch]), R.f64(has.double()))
+    R.check(out.cpu()[ch], f["h"], f["eh"], "out")
+    R.check(states.cpu()[:, ch], f["last"], f["elast"], "states")
+    for k in grads:
+        R.check(grads[k].cpu()[ch], *ref[k], k)
+    R.check(dd.cpu()[ch], *ref["ddecay"], "ddecay")
+    R.check(di.cpu()[:, ch], *ref["dinitial"], "dinitial")
+    for t in (out, states, di, dd, *grads.values()):  # every element has been written
+        assert bool(torch.isfinite(t).all())
+
+
+@pytest.mark.parametrize("layout", ["token", "token_odd"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_conv_gradients_in_long_strips(dtype, layout):
+    """2^23 elements and more in rows: strips of 64 rows, cut and ended anywhere."""
+    dim, lens, dt = 1030, [64, 1, 0, 127, 3000, 2, 64, 4943, 0], DT[dtype]
+    b, n = R.offsets(lens), len(lens)
+    assert b[-1] * dim >= 1 << 23
+    x, g = rand(1, dim, b[-1], dtype=dt), rand(2, dim, b[-1], dtype=dt)
+    w, bias = rand(3, dim, 4, dtype=dt, scale=0.5), rand(4, dim, dtype=dt)
+    first, end = rand(5, n, dim, 3, dtype=dt), rand(6, n, dim, 3, dtype=dt)
+    has = torch.tensor([k % 3 != 1 for k in range(n)])
+    di = torch.full((n, dim, 3), NAN, dtype=dt, device="cuda")
+    dx = place(torch.full_like(x, NAN), layout)
+    _, dw, db = lib.causal_conv1d_varlen_bwd(
+        place(g, layout), place(x, layout), w.cuda(), bias.cuda(), first.cuda(),
+        torch.tensor(b, dtype=torch.int32, device="cuda"), None, has.cuda(), True,
+        dfinal_states=end.cuda(), dinitial_states=di, dx=dx)
+    c = some_channels(dim)
+    ref = R.conv_grad(R.f64(g[c]), R.f64(x[c]), R.f64(w[c]), R.f64(bias[c]), b, True,
+                      R.f64(first[:, c]), R.f64(end[:, c]), R.f64(has.double()))
+    R.check(dx.cpu()[c], *ref["dx"], "dx")
+    R.check(dw.cpu()[c], *ref["dweight"], "dweight")
+    R.check(db.cpu()[c], *ref["dbias"], "dbias")
+    R.check(di.cpu()[:, c], *ref["dinitial"], "dinitial")
+    for t in (dx, dw, db, di):
+        assert bool(torch.isfinite(t).all())
+
+
+@pytest.mark.parametrize("dim,group", [(136, 0), (1001, 0), (1024, 64), (2048, 128), (4096, 256)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_of_many_rows(dim, group, dtype):
+    """4096 rows and more: a wave holds a row of up to eight vectors a lane, and a
+    workgroup of the gradients walks several rows."""
+    rows, dt = 9001 if dim <= 1024 else 4099, DT[dtype]
+    x, res, g, dres = (rand(80 + k, rows, dim, dtype=dt).cuda() for k in range(4))
+    w = (rand(84, dim) * 0.5 + 1).to(dt).cuda()
+    total = torch.empty_like(x)
+    out = lib.rms_norm_fwd(x, w, 1e-5, residual=res, residual_out=total)
+    s = x.double() + res.double()
+    y, ey = R.norm(s, w.double(), 1e-5)
+    ey = ey + 3 * R.EPS * y.abs()  # s itself is rounded to fp32 before it is used
+    near = lambda t, v, e, what: R.check(t, v.cpu(), e.cpu(), what)  # noqa: E731
+    near(out, y, ey, "out")
+    near(total, s, R.EPS * s.abs(), "sum")
+    q, scales = lib.rms_norm_quant(x, w, 1e-5, group_size=group, residual=res, residual_out=total)
+    check_codes(q, scales, y.cpu(), ey.cpu(), group or dim)
+    dx, dw = lib.rms_norm_bwd(g, total, w, 1e-5, dresidual=dres)
+    ref = R.norm_grad(g.double(), total.double(), w.double(), 1e-5, dres.double())
+    near(dx, *ref["dx"], "dx")
+    near(dw, *ref["dweight"], "dweight")
