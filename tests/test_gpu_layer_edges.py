@@ -3,10 +3,13 @@ the parameters' range, values next to a rounding's border, the variants that
 large calls take, and a layer's calls in flight together."""
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 import torch
 
 import depthwise_causal_conv1d_amd as lib
+from depthwise_causal_conv1d_amd import _lib
 from tests import layer_ref as R
 from tests.test_gpu_layer_ops import DT, NAN, Rec, check_codes, place, rand
 
@@ -276,3 +279,136 @@ def test_norm_of_many_rows(dim, group, dtype):
     ref = R.norm_grad(g.double(), total.double(), w.double(), 1e-5, dres.double())
     near(dx, *ref["dx"], "dx")
     near(dw, *ref["dweight"], "dweight")
+
+
+# ---------------------------------------------------------------- a layer's calls together
+
+def layer_inputs(seed, layout, lens):
+    """One layer's tensors, every plane in the same layout: rows of tokens (few
+    long sequences: segments, whose two launches hand over through a workspace) or
+    channel-major."""
+    dim, b = 96, R.offsets(lens)
+    T = b[-1]
+    plane = (lambda k: rand(k, T, dim).cuda().t()) if layout == "token" else (
+        lambda k: rand(k, dim, T).cuda())
+    return dict(x=rand(seed, T, dim).cuda(), res=rand(seed + 1, T, dim).cuda(),
+                nw=(rand(seed + 2, dim) * 0.1 + 1).cuda(), cw=rand(seed + 3, dim, 4, scale=0.5).cuda(),
+                cb=rand(seed + 4, dim, scale=0.1).cuda(), ga=plane(seed + 5), gx=plane(seed + 6),
+                dout=plane(seed + 7), decay=(rand(seed + 8, dim) * 0.3 - 4).cuda(),
+                cstate=torch.zeros(len(lens), dim, 3, device="cuda"),
+                qsl=torch.tensor(b, dtype=torch.int32, device="cuda"), rows=layout == "token")
+
+
+def layer_step(t):
+    """norm -> conv -> recurrence and back, on the library's calls; every value that
+    passes from one to the next."""
+    k = dict(total=torch.empty_like(t["x"]))
+    k["y"] = lib.rms_norm_fwd(t["x"], t["nw"], 1e-6, residual=t["res"], residual_out=k["total"])
+    k["v"] = k["y"].t() if t["rows"] else k["y"].t().contiguous()
+    k["u"] = k["v"].clone()
+    lib.causal_conv1d_varlen_fwd(k["u"], t["cw"], t["cb"], t["cstate"], t["qsl"], None, None, True)
+    marks = lib.gated_linear_recurrence_checkpoints(k["u"], t["qsl"])
+    k["h"] = lib.gated_linear_recurrence_varlen_fwd(k["u"], t["ga"], t["gx"], t["decay"], None, t["qsl"],
+                                                    checkpoints=marks)
+    k["du"], k["dga"], k["dgx"], k["dd"] = lib.gated_linear_recurrence_varlen_bwd(
+        t["dout"], k["u"], t["ga"], t["gx"], t["decay"], marks, t["qsl"])
+    k["dv"], k["dcw"], k["dcb"] = lib.causal_conv1d_varlen_bwd(
+        k["du"], k["v"], t["cw"], t["cb"], None, t["qsl"], None, None, True)
+    k["dy"] = k["dv"].t() if t["rows"] else k["dv"].t().contiguous()
+    k["dx"], k["dnw"] = lib.rms_norm_bwd(k["dy"], k["total"], t["nw"], 1e-6)
+    k["q"], k["scales"] = lib.rms_norm_quant(k["h"].t().contiguous(), t["nw"], 1e-6, group_size=32)
+    return k
+
+
+LAYERS = [("token", (700, 600)), ("channel", (2500, 1700))]
+
+
+def assert_forms(t, k, lens):
+    """The planes are what the fast forms take, and rows of them are cut into segments."""
+    planes = [t["ga"], t["gx"], t["dout"], k["u"], k["h"], k["v"], k["dv"]] + [
+        k[n] for n in ("du", "dga", "dgx")]
+    fwd, bwd = ctypes.c_int64(), ctypes.c_int64()
+    assert _lib.load().gated_linear_recurrence_workspace(
+        sum(lens), len(lens), 96, ctypes.byref(fwd), ctypes.byref(bwd)) == 0
+    if t["rows"]:
+        assert fwd.value > 0 and all(p.stride(0) == 1 for p in planes)
+    else:
+        assert all(p.stride(1) == 1 for p in planes)
+
+
+@pytest.mark.parametrize("layout,lens", LAYERS)
+def test_each_call_of_a_layer_against_its_reference(layout, lens):
+    """Every call's results within its own derived bound, at the values that the
+    call before left."""
+    t = layer_inputs(200, layout, lens)
+    k = layer_step(t)
+    assert_forms(t, k, lens)
+    b, c = R.offsets(lens), {n: R.f64(v) for n, v in {**t, **k}.items()
+                             if n not in ("qsl", "rows", "q")}
+    s = c["x"] + c["res"]
+    y, ey = R.norm(s, c["nw"], 1e-6)
+    R.check(k["y"], y, ey + 3 * R.EPS * y.abs(), "norm")
+    u = R.conv(c["v"], c["cw"], c["cb"], b, True)
+    # four products and sums, then |silu'| < 1.1 and the sigmoid's |z| + 16 units
+    z = R.conv(c["v"], c["cw"], c["cb"], b, False)
+    az = R.conv(c["v"].abs(), c["cw"].abs(), c["cb"].abs(), b, False)
+    R.check(k["u"], u, R.EPS * (6 * 1.1 * az + (16 + z.abs()) * u.abs()), "conv")
+    f = R.recurrence(c["u"], c["ga"], c["gx"], t["decay"].cpu(), 8.0, b)
+    R.check(k["h"], f["h"], f["eh"], "recurrence")
+    ref = R.recurrence_grad(f, c["dout"], c["u"], t["decay"].cpu(), 8.0, b)
+    for n, r in (("du", "dx"), ("dga", "dgate_a"), ("dgx", "dgate_x"), ("dd", "ddecay")):
+        R.check(k[n], *ref[r], n)
+    ref = R.conv_grad(c["du"], c["v"], c["cw"], c["cb"], b, True)
+    for n, r in (("dv", "dx"), ("dcw", "dweight"), ("dcb", "dbias")):
+        R.check(k[n], *ref[r], n)
+    ref = R.norm_grad(c["dy"], c["total"], c["nw"], 1e-6)
+    R.check(k["dx"], *ref["dx"], "dx")
+    R.check(k["dnw"], *ref["dweight"], "dnw")
+    y, ey = R.norm(c["h"].t(), c["nw"], 1e-6)
+    check_codes(k["q"], k["scales"], y, ey, 32)
+
+
+@pytest.mark.parametrize("layout,lens", LAYERS)
+def test_layers_in_flight_on_streams_and_in_graphs(layout, lens):
+    """Two layers on two streams at once, then two captured graphs replayed one
+    after another and side by side, with eager work of a third layer between:
+    the bits of each layer alone."""
+    lib.sconv_init()
+    ins = [layer_inputs(seed, layout, lens) for seed in (300, 310, 320)]
+    want = [{n: v.clone() for n, v in layer_step(t).items()} for t in ins]
+    assert_forms(ins[0], want[0], lens)
+
+    def same(got, k, what):
+        for n in want[k]:
+            assert torch.equal(R.bits(got[n]), R.bits(want[k][n])), (k, n, what)
+
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for turn in range(4):
+        got = [None, None]
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                for _ in range(3):
+                    got[k] = layer_step(ins[k])
+        torch.cuda.synchronize()
+        for k in (0, 1):
+            same(got[k], k, f"streams, turn {turn}")
+    graphs, held = [], []
+    for k in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(layer_step(ins[k]))
+        graphs.append(g)
+    for turn in range(4):
+        for k in (0, 1):
+            for v in held[k].values():  # what an earlier replay left
+                v.zero_()
+        torch.cuda.synchronize()
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k if turn % 2 else 0]):
+                graphs[k].replay()
+        eager = layer_step(ins[2])
+        torch.cuda.synchronize()
+        for k in (0, 1):
+            same(held[k], k, f"graphs, turn {turn}")
+        same(eager, 2, f"eager, turn {turn}")
