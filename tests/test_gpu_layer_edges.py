@@ -137,6 +137,39 @@ def test_recurrence_infinite_input_and_state(lens, layout):
     assert torch.equal(R.bits(p), R.bits(want))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["channel", "token", "strided"])
+@pytest.mark.parametrize("lens", [[260], [420, 500]])
+def test_recurrence_gates_at_their_ends(lens, layout, dtype):
+    """Closed, open and infinite gates within the derived bounds.  Below a gate of
+    -88 the sigmoid is zero here, so r < 2^-126 counts as zero: that moves m = sqrt(2 k r)
+    by `least` at most, a state by as much for each token, and the gradients
+    (products of such an m, or of its square over itself, with dh) likewise."""
+    c = Rec(lens, 8, dtype, seed=62, inits=range(len(lens)))
+    ends = [-float("inf"), float("inf"), -200.0, 200.0, -90.0, 60.0, -30.0]
+    for ch, v in enumerate(ends):
+        c.ga[ch + 1, 40:60] = v
+        c.gx[ch + 1, 50:70] = -v
+    c.ga[3, 100:] = -90.0  # closed to the end
+    c.decay[5], c.decay[6], c.decay[7] = 60.0, -60.0, 3.0
+    start, has = R.f64(c.h0), R.f64(c.has.double())
+    c.f = f = R.recurrence(R.f64(c.x), R.f64(c.ga), R.f64(c.gx), c.decay, 8.0, c.bounds, start)
+    ref = R.recurrence_grad(f, R.f64(c.dout), R.f64(c.x), c.decay, 8.0, c.bounds, R.f64(c.dfinal), has)
+    least = (2 * float(f["k"].max()) * 2.0 ** -126) ** 0.5 * float(c.x.abs().max())
+    dh = float(c.dout.abs().sum(1).max() + c.dfinal.abs().max())  # a <= 1
+    f["eh"] += c.T * least
+    f["elast"] += c.T * least
+    for v, e in ref.values():
+        e += c.T * least * dh
+    d = c.gpu(layout)
+    out, m = c.forward(d, layout)
+    c.check_forward(out, d["pool"], layout)
+    got, di = c.backward(d, m, layout)
+    for n in ("dx", "dgate_a", "dgate_x", "ddecay"):
+        R.check(got[n].cpu(), *ref[n], n)
+    R.check(di.cpu()[c.slots.long()], *ref["dinitial"], "dinitial")
+
+
 # ---------------------------------------------------------------- long sums
 
 def test_recurrence_ddecay_of_a_long_sequence():
