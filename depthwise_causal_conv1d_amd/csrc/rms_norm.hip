@@ -5,6 +5,7 @@
 //   s = x + residual, out = s * rsqrt(mean(s^2) + eps) * weight
 //   8 bits: scale = max |out| over a group / 448, code = e4m3(out / scale)
 #include "column_sum.h"
+#include "lane_tokens.h"
 #include "plane_host.h"
 
 #include <initializer_list>
@@ -24,14 +25,6 @@ struct NormParams {
   int32_t dim, group;  // group: channels that share a scale
   float eps;
 };
-
-template <typename D>
-__device__ __forceinline__ typename D::storage norm_round(float v) {
-  if constexpr (sizeof(typename D::storage) == 2)
-    return __builtin_bit_cast(uint16_t, (__bf16)v);
-  else
-    return v;
-}
 
 // v combined over groups of N consecutive lanes (a power of two); every lane
 // gets the result.  Up to 16 lanes by DPP moves inside a row.
@@ -155,9 +148,9 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_simple(const NormParams
     for (int c = g + threadIdx.x; c < g + p.group; c += kNormThreads) {
       const float v = at(c);
       const float y = v * rstd * load_as_float<D>(w + c);
-      if (sum) sum[c] = norm_round<D>(v);
+      if (sum) sum[c] = round_to<D>(v);
       if constexpr (Q) static_cast<uint8_t*>(p.out)[row * p.o_rs + c] = to_e4m3(y / scale);
-      else static_cast<S*>(p.out)[row * p.o_rs + c] = norm_round<D>(y);
+      else static_cast<S*>(p.out)[row * p.o_rs + c] = round_to<D>(y);
     }
   }
 }
@@ -302,7 +295,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_simple(const NormBwdPar
       float v = rstd * (gv * load_as_float<D>(w + c) - hat * proj);
       if (dr) v += load_as_float<D>(dr + c);
       part[c] = __builtin_fmaf(gv, hat, part[c]);
-      dx[c] = norm_round<D>(v);
+      dx[c] = round_to<D>(v);
     }
   }
 }
@@ -451,36 +444,36 @@ static int norm_threads(int32_t dim, int V, int64_t rows) {
   return V > 1 && per <= 8 && rows >= 4096 ? 64 : 256;
 }
 
+// group: channels that share a scale, 0 for the row.
 template <typename D, int V, int NV, int T>
-static void launch_norm_fwd(bool quant, int lanes, const NormParams& p, hipStream_t s) {
+static void launch_norm_fwd(bool quant, int group, const NormParams& p, hipStream_t s) {
   const dim3 g((uint32_t)cdiv(p.rows, kNormThreads / T)), th(kNormThreads);
   if (!quant) hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, false, 0>), g, th, 0, s, p);
-  else if (lanes == 0) hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 0>), g, th, 0, s, p);
+  else if (group == 0) hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 0>), g, th, 0, s, p);
   else if constexpr (V > 1) {
-    switch (lanes) {
-      case 4: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 4>), g, th, 0, s, p); break;
-      case 8: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 8>), g, th, 0, s, p); break;
-      case 16: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 16>), g, th, 0, s, p); break;
-      case 32: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 32>), g, th, 0, s, p); break;
-      default: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 64>), g, th, 0, s, p); break;
+    switch (group) {
+      case 32: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 32 / V>), g, th, 0, s, p); break;
+      case 64: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 64 / V>), g, th, 0, s, p); break;
+      case 128: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 128 / V>), g, th, 0, s, p); break;
+      default: hipLaunchKernelGGL((norm_fwd_kernel<D, V, NV, T, true, 256 / V>), g, th, 0, s, p); break;
     }
   }
 }
 
 template <typename D, int V>
-static void launch_norm_fwd_n(int nv, int T, bool quant, int lanes, const NormParams& p,
+static void launch_norm_fwd_n(int nv, int T, bool quant, int group, const NormParams& p,
                               hipStream_t s) {
   if constexpr (V > 1) {
     if (T == 64) {
-      if (nv == 1) launch_norm_fwd<D, V, 1, 64>(quant, lanes, p, s);
-      else if (nv == 2) launch_norm_fwd<D, V, 2, 64>(quant, lanes, p, s);
-      else if (nv == 4) launch_norm_fwd<D, V, 4, 64>(quant, lanes, p, s);
-      else launch_norm_fwd<D, V, 8, 64>(quant, lanes, p, s);
+      if (nv == 1) launch_norm_fwd<D, V, 1, 64>(quant, group, p, s);
+      else if (nv == 2) launch_norm_fwd<D, V, 2, 64>(quant, group, p, s);
+      else if (nv == 4) launch_norm_fwd<D, V, 4, 64>(quant, group, p, s);
+      else launch_norm_fwd<D, V, 8, 64>(quant, group, p, s);
     } else {
-      if (nv == 1) launch_norm_fwd<D, V, 1, 256>(quant, lanes, p, s);
-      else if (nv == 2) launch_norm_fwd<D, V, 2, 256>(quant, lanes, p, s);
-      else if (nv == 4) launch_norm_fwd<D, V, 4, 256>(quant, lanes, p, s);
-      else launch_norm_fwd<D, V, 8, 256>(quant, lanes, p, s);
+      if (nv == 1) launch_norm_fwd<D, V, 1, 256>(quant, group, p, s);
+      else if (nv == 2) launch_norm_fwd<D, V, 2, 256>(quant, group, p, s);
+      else if (nv == 4) launch_norm_fwd<D, V, 4, 256>(quant, group, p, s);
+      else launch_norm_fwd<D, V, 8, 256>(quant, group, p, s);
     }
   } else {
     if (T == 64) {
@@ -587,13 +580,12 @@ extern "C" int rms_norm_fwd(const void* x, int64_t x_stride_r, const void* resid
   const int vec16 = (int)(16 / es);
   const bool vec = norm_vec({px, pr, ps, po}, vec16) && aligned16(weight);
   const int V = vec ? vec16 : 1, T = norm_threads(dim, V, rows), nv = norm_vectors(dim, V, T);
-  const int lanes = group_size / V;
   if (nv > 0 && (vec || group_size == 0)) {
     if (dtype == SCONV_BF16) {
-      if (vec) launch_norm_fwd_n<Bf16, 8>(nv, T, quant, lanes, p, stream);
+      if (vec) launch_norm_fwd_n<Bf16, 8>(nv, T, quant, group_size, p, stream);
       else launch_norm_fwd_n<Bf16, 1>(nv, T, quant, 0, p, stream);
     } else {
-      if (vec) launch_norm_fwd_n<F32, 4>(nv, T, quant, lanes, p, stream);
+      if (vec) launch_norm_fwd_n<F32, 4>(nv, T, quant, group_size, p, stream);
       else launch_norm_fwd_n<F32, 1>(nv, T, quant, 0, p, stream);
     }
     return check_launch(fn);
