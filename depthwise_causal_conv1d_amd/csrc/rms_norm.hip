@@ -158,8 +158,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_simple(const NormParams
 // A row in registers, read once: T threads (one wave, or the workgroup's
 // four) hold NV vectors of V channels each.  Bound by the bytes of the rows;
 // weight comes from the caches.  G: lanes that share a scale (0: the row).
-// 32768 x 4096 bf16: 199 us (5.4 TB/s); 17408 x 4096 bf16 to 8 bits with
-// the residual, groups of 128: 100 us (5.0 TB/s).
+// 17408 x 4096 bf16 to 8 bits with the residual, groups of 128: 90 us
+// (5.5 TB/s).
 template <typename D, int V, int NV, int T, bool Q, int G>
 __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(const NormParams p) {
   using S = typename D::storage;
@@ -436,12 +436,12 @@ static int norm_vectors(int32_t dim, int V, int T) {
   return need <= 4 ? 4 : need <= 16 ? 16 : need <= 32 ? 32 : 0;
 }
 
-// Threads of a row: a wave needs no barrier and gives every lane more loads
-// at once, four waves shorten a long row's chain when rows are few.
-static int norm_threads(int32_t dim, int V, int64_t rows) {
-  const int64_t per = cdiv(dim, (int64_t)V * 64);
-  if (per <= (V > 1 ? 2 : 16)) return 64;
-  return V > 1 && per <= 8 && rows >= 4096 ? 64 : 256;
+// Threads of a row: a wave where it holds the row in two vectors a lane (16
+// single elements), which spares the barriers; else four waves, however many
+// the rows: with a wave for rows of four and eight vectors, 17408 x 4096 bf16 to
+// 8 bits takes 102 us (four waves 90), 4096 x 4096 30 (24), 17408 x 2048 fp32 97 (83).
+static int norm_threads(int32_t dim, int V) {
+  return cdiv(dim, (int64_t)V * 64) <= (V > 1 ? 2 : 16) ? 64 : 256;
 }
 
 // group: channels that share a scale, 0 for the row.
@@ -466,9 +466,7 @@ static void launch_norm_fwd_n(int nv, int T, bool quant, int group, const NormPa
   if constexpr (V > 1) {
     if (T == 64) {
       if (nv == 1) launch_norm_fwd<D, V, 1, 64>(quant, group, p, s);
-      else if (nv == 2) launch_norm_fwd<D, V, 2, 64>(quant, group, p, s);
-      else if (nv == 4) launch_norm_fwd<D, V, 4, 64>(quant, group, p, s);
-      else launch_norm_fwd<D, V, 8, 64>(quant, group, p, s);
+      else launch_norm_fwd<D, V, 2, 64>(quant, group, p, s);
     } else {
       if (nv == 1) launch_norm_fwd<D, V, 1, 256>(quant, group, p, s);
       else if (nv == 2) launch_norm_fwd<D, V, 2, 256>(quant, group, p, s);
@@ -579,7 +577,7 @@ extern "C" int rms_norm_fwd(const void* x, int64_t x_stride_r, const void* resid
   if (!valid_grid(rows, kNormThreads)) return fail(SCONV_ERR_UNSUPPORTED, "%s: too many rows", fn);
   const int vec16 = (int)(16 / es);
   const bool vec = norm_vec({px, pr, ps, po}, vec16) && aligned16(weight);
-  const int V = vec ? vec16 : 1, T = norm_threads(dim, V, rows), nv = norm_vectors(dim, V, T);
+  const int V = vec ? vec16 : 1, T = norm_threads(dim, V), nv = norm_vectors(dim, V, T);
   if (nv > 0 && (vec || group_size == 0)) {
     if (dtype == SCONV_BF16) {
       if (vec) launch_norm_fwd_n<Bf16, 8>(nv, T, quant, group_size, p, stream);
@@ -657,7 +655,7 @@ extern "C" int rms_norm_bwd(const void* dout, int64_t dout_stride_r, const void*
   if (rows > 0) {
     const int vec16 = (int)(16 / es);
     const bool vec = norm_vec({in[0], in[1], in[2], po}, vec16) && aligned16(weight);
-    const int V = vec ? vec16 : 1, T = norm_threads(dim, V, 0), nv = norm_vectors(dim, V, T);
+    const int V = vec ? vec16 : 1, T = norm_threads(dim, V), nv = norm_vectors(dim, V, T);
     const uint32_t grid = (uint32_t)parts;
     if (nv > 0) {
       if (dtype == SCONV_BF16) {

@@ -293,8 +293,8 @@ def test_conv_gradients_in_long_strips(dtype, layout):
 @pytest.mark.parametrize("dim,group", [(136, 0), (1001, 0), (1024, 64), (2048, 128), (4096, 256)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_norm_of_many_rows(dim, group, dtype):
-    """4096 rows and more: a wave holds a row of up to eight vectors a lane, and a
-    workgroup of the gradients walks several rows."""
+    """4096 rows and more: many workgroups of one row or four, and in the gradients
+    each walks several."""
     rows, dt = 9001 if dim <= 1024 else 4099, DT[dtype]
     x, res, g, dres = (rand(80 + k, rows, dim, dtype=dt).cuda() for k in range(4))
     w = (rand(84, dim) * 0.5 + 1).to(dt).cuda()
