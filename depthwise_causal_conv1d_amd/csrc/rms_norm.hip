@@ -516,9 +516,19 @@ static bool norm_vec(std::initializer_list<Plane> planes, int64_t V) {
   return true;
 }
 
-// Workgroups of the backward pass, and rows of its workspace.
-// Four rows each at least, which is a row a wave where a wave holds one.
-static int64_t norm_parts(int64_t rows) { return rows < 4096 ? cdiv(rows, 4) : 1024; }
+// Workgroups of the backward pass, and rows of its workspace: four rows each at
+// least (a row a wave where a wave holds one; single rows were no faster, 1023 x
+// 8192 fp32 forward and gradients 52 us both).  At most one a CU where registers
+// hold the rows, since each walks them with the next one's loads in flight and
+// leaves a row of partial sums (forward and gradients with 1024 and with 256:
+// 32768 x 4096 bf16 401 and 373 us, 8192 x 4096 106 and 96, 8192 x 1001 fp32 68 and
+// 60); four a CU for wider rows, which are read twice (4096 x 20000 bf16: 977 and
+// 1995).  The width tells them apart whatever the type and alignment, which a
+// workspace's size does not know.
+static int64_t norm_parts(int64_t rows, int32_t dim) {
+  const int64_t most = dim <= 8192 ? 256 : 1024;
+  return rows < 4 * most ? cdiv(rows, 4) : most;
+}
 
 }  // namespace sconv
 
@@ -604,7 +614,7 @@ extern "C" int rms_norm_bwd_workspace(int64_t rows, int32_t dim, int64_t* floats
   clear_error();
   if (rows < 0 || dim < 0 || !floats)
     return fail(SCONV_ERR_INVALID, "rms_norm_bwd_workspace: rows and dim must be >= 0, floats not NULL");
-  *floats = norm_parts(rows) * dim;
+  *floats = norm_parts(rows, dim) * dim;
   return SCONV_OK;
 }
 
@@ -624,7 +634,7 @@ extern "C" int rms_norm_bwd(const void* dout, int64_t dout_stride_r, const void*
   if (dim == 0) return SCONV_OK;
   if (!dweight || (rows > 0 && (!dout || !x || !weight || !dx || !workspace)))
     return fail(SCONV_ERR_INVALID, "%s: NULL pointer", fn);
-  const int64_t parts = norm_parts(rows), need = parts * dim;
+  const int64_t parts = norm_parts(rows, dim), need = parts * dim;
   if (workspace_floats < need)
     return fail(SCONV_ERR_INVALID, "%s: workspace holds %lld floats, %lld needed", fn,
                 (long long)workspace_floats, (long long)need);
