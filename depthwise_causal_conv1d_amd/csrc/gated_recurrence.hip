@@ -1027,11 +1027,19 @@ static bool token_lanes(std::initializer_list<Plane> planes) {
   return true;
 }
 
-// Waves that walk one sequence together, at most `most`.
+// Waves that walk one sequence together, at most `most`: more of them where
+// few (sequence, channel) pairs have chunks enough.  Measured, prefill and
+// forward + gradients in us, bf16: sixteen (eight) waves and four: 1 x 65536 x 256 30,
+// 76 and 38, 94; x 512 53, 145 and 53, 158; x 700 81, 215 and 81, 207; 1 x 4096 x 400 the
+// same.  Four waves and one: 1 x 8192 x 512 10, 30 and 19, 47; 2 x 1024 x 1024 8.8, 29.7
+// and 9.5, 31.9; 8 x 600 x 512 12.3, 39 and 9.7, 33; 4096 pairs of 1024 tokens 11.9,
+// 36 and 9.9, 30 (fp32 13.6, 40 and 14.0, 39), of 1500 14.5, 45 and 13.7, 33 (18.9, 60 and
+// 19.7, 61), of 2048 14.5, 43 and 15.6, 39 (26.5, 72 and 28.3, 79), of 8192 57, 143 and 65,
+// 153; 8192 pairs of 4096 tokens 52, 142 and 45, 134.
 static int waves_per_pair(int64_t pairs, int64_t total_T, int32_t batch, int most) {
   const int64_t mean = total_T / batch;
   if (most > 4 && pairs < 512 && mean >= 8 * kChunkTokens) return most;
-  if (pairs < 8192 && mean >= 2 * kChunkTokens) return 4;
+  if (pairs < 8192 && mean >= (pairs < 4096 ? 2 : 4) * kChunkTokens) return 4;
   return 1;
 }
 
