@@ -239,7 +239,10 @@ __global__ __launch_bounds__(256, 4) void conv_grad_kernel(const ConvGradParams 
 // W-1 after it again.  Strips lie on the flat token axis, whatever the
 // sequences' lengths: a wave takes every sequence that its strip meets.
 // 17409 x 4096 bf16: 115 us (83 at a copy's rate); 5003 x 1021 fp32: 19 us,
-// the latency of a strip's chain of loads.
+// the latency of a strip's chain of loads.  Ordinary stores: what reads dx next
+// finds a small plane in the caches (with a copy of dx after it, ordinary and
+// streaming: 5003 x 1021 fp32 27.6 and 29.2 us, 2048 x 4096 bf16 37.9 and 39.1; past
+// the caches streaming wins, 17408 x 4096 175.7 and 171.8).
 constexpr int kStripWaves = 4, kStripGroup = 8;
 
 template <typename D, int V, int W>
@@ -552,8 +555,12 @@ extern "C" int causal_conv1d_varlen_bwd(
     grid = parts * cdiv(dim, 64 * V);
   } else {
     vec = pg.st == 1 && px.st == 1 && po.st == 1;
-    // few (sequence, channel) pairs of several chunks: four waves for each
-    NW = p.num_pairs < 8192 && total_T / (batch ? batch : 1) >= 2 * kChunkTokens ? 4 : 1;
+    // Few (sequence, channel) pairs of several chunks: four waves for each.  With
+    // four and with one, us: 1 x 65536 x 512 bf16 49 and 119, 1 x 8192 x 1024 18.5 and
+    // 22.0, 2 x 4096 x 1024 21 and 18 (fp32 24 and 25), 2 x 8192 x 1024 27.5 and 28.2,
+    // 3 x 4096 x 1024 25 and 21 (38 and 35), 6 x 1024 x 1024 27 and 18 (26 and 19),
+    // 6 x 4096 x 1024 53 and 34 (69 both).
+    NW = p.num_pairs < 2048 && total_T / (batch ? batch : 1) >= 2 * kChunkTokens ? 4 : 1;
     grid = cdiv(p.num_pairs, 4 / NW);
   }
   const int64_t sums = cdiv((int64_t)dim * (W + 1), kSumCols);
