@@ -1005,12 +1005,15 @@ static bool side_by_side(std::initializer_list<Plane> planes) {
   return true;
 }
 
-// Whether workgroups take the longest sequences first: few sequences, of
-// more than a few tiles (the order costs a round trip: 113 against 122 us
-// for 33 sequences of 248 rows x 1001, forward and gradients; 16 of 1088 x
-// 4096 gain 233 -> 203 us).
+// Whether workgroups of whole sequences in rows take the longest ones first (and
+// leave each CU two of them): few sequences, of a few tiles and more, since the
+// order costs a round trip.  Forward + gradients, us, in order of length and as
+// they come, three draws of lengths each: 33 of 248 tokens x 1001 fp32 128, 117, 152 and
+// 113, 111, 155 (equal lengths: 120 and 116); 40 of 200 x 1024 bf16 86, 141, 102 and 107,
+// 140, 99; 33 of 300 x 1001 fp32 182, 132, 123 and 199, 151, 141; 60 of 300 x 2048 bf16
+// 258, 256, 258 and 263, 284, 271; 40 of 400 x 2048 bf16 323, 204, 235 and 389, 241, 325.
 static bool longest_first(int64_t total_T, int32_t batch) {
-  return batch > 1 && batch <= 64 && total_T / batch >= 8 * kTile;
+  return batch > 1 && batch <= 64 && total_T / batch >= 4 * kTile;
 }
 
 // Vector lanes of V channels: every row starts on a multiple of V elements.
@@ -1047,11 +1050,12 @@ static int waves_per_pair(int64_t pairs, int64_t total_T, int32_t batch, int mos
 // by side, or 0: a workgroup takes a whole sequence.
 // Segments cost a second read of the inputs, and pay where whole sequences
 // are too few workgroups, or too uneven ones, and long enough to be cut.
-// Measured, prefill, in segments and without: 8 ragged x 17409 x 4096 bf16 (512
-// workgroups) 209 and 239..383 us; 16 (1024) 201..209 and 138..163; 33 of 248
-// tokens x 1001 fp32 (528) 57 and 41..51; 16 of 256 x 1024 bf16 (256) 26 and
-// 36; 40 of 125 x 256 bf16 26..30 and 18..26; 1 x 32768 x 1024 102 and 1727.
-// 2048 segments' workgroups instead of 1024 were no faster (108 us for the last).
+// Measured, prefill, in segments and without, by the lengths drawn: 8 ragged x
+// 17409 x 4096 bf16 (512 workgroups) 203..216 and 150..383 us, of equal lengths 189 and
+// 130; 9 (576) 204..214 and 150..200; 11 to 16 (704 to 1024) 202..216 and 131..194; 16 of equal
+// lengths 123 and 130; 33 of 248 tokens x 1001 fp32 (528) 57 and 41..61; 16 of 256 x 1024
+// bf16 (256) 26 and 36; 40 of 125 x 256 bf16 26..30 and 18..26; 1 x 32768 x 1024 102 and
+// 1727.  2048 segments' workgroups instead of 1024 were no faster (108 us for the last).
 static int64_t segment_rows(int64_t total_T, int32_t batch, int32_t dim) {
   const int64_t slabs = cdiv(dim, 64);
   if (batch == 0 || dim == 0 || total_T / batch < 200 || batch * slabs > 512) return 0;
