@@ -112,7 +112,9 @@ __device__ __forceinline__ void store_codes(uint8_t* q, const float (&v)[V], flo
 }
 
 // One workgroup per row, which it reads three times: rows too long for the
-// registers, and groups of channels at unaligned rows.
+// registers (8192 x 8196 fp32 332 us, 8192 x 8192 in registers 202), and groups of
+// channels at unaligned rows, a few threads and four barriers a group (8192 x
+// 4096 bf16 in groups of 128 and 32: 701 and 2634 us, aligned 44).
 template <typename D, bool Q>
 __global__ __launch_bounds__(kNormThreads) void norm_fwd_simple(const NormParams p) {
   using S = typename D::storage;
@@ -305,7 +307,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_simple(const NormBwdPar
 // Rows in registers: T threads hold NV vectors of V channels of a row, walk
 // every kRows * gridDim-th row, and keep dweight's sums of their channels.
 // The next row's loads are issued before this row's sums are exchanged.
-// 32768 x 4096 bf16: 223 us (4.8 TB/s); 1023 x 1001 fp32: 12 us, latency.
+// 32768 x 4096 bf16: 199 us (5.4 TB/s); 1023 x 1001 fp32: 11 us, latency.
 template <typename D, int V, int NV, int T>
 __global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(const NormBwdParams p) {
   using S = typename D::storage;

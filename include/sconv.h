@@ -556,7 +556,8 @@ int gather_intermediate_ssm_state(const void* states, int64_t num_chunks, int64_
  * causal_conv1d_varlen_fwd.  Planes are [dim, total_T] at any strides >= 0
  * (out and gradients: no two elements in one place): the fast forms are tokens
  * contiguous (channel-major) and channels contiguous (rows of tokens), both at
- * any alignment; other strides load one element at a time.
+ * any alignment, all planes of a call alike; other strides, and planes of both
+ * kinds in one call, load one element at a time (3 to 15 times the time).
  *
  * gated_linear_recurrence_checkpoint_rows -- rows of the checkpoint buffer
  * that a forward call leaves for its backward call:
@@ -591,7 +592,10 @@ int gated_linear_recurrence_workspace(int64_t total_T, int32_t batch, int32_t di
  *   workspace  fp32 of gated_linear_recurrence_workspace's fwd_floats, the
  *            call's own until it has finished, or NULL.  With it, few long
  *            sequences in rows of tokens are cut over their tokens (two
- *            launches); without, a workgroup walks each of them alone
+ *            launches); without, a workgroup walks each of them alone.  The
+ *            choice goes by batch and total_T / batch: empty and skipped entries
+ *            count, and one long sequence among many of them is walked alone
+ *            (32768 tokens of 1024 channels: 0.1 ms by itself, 1.1 ms among 64)
  *
  * Rows of out outside every sequence, or in a skipped one, are not written.
  *
@@ -688,7 +692,8 @@ int causal_conv1d_varlen_bwd_workspace(int64_t total_T, int32_t batch, int32_t d
  *             W-1 entries of u; dx and dinitial_states are its two parts
  *     dweight[k] = sum_t dz_t u[t - (W-1) + k],   dbias = sum_t dz_t
  *
- *   dout, x, dx   [dim, total_T] at any strides (dx overlaps neither)
+ *   dout, x, dx   [dim, total_T] at any strides (dx overlaps neither); fast
+ *            where all three have tokens, or all three channels, contiguous
  *   weight [dim, W], bias [dim] or NULL: as the forward's
  *   initial_states [num_slots, dim, W-1]: the state pool as it was BEFORE the
  *            forward call (which overwrites it), read where
@@ -742,6 +747,10 @@ int causal_conv1d_varlen_bwd(
  *            and may be residual or x itself; so may out
  *   scales   fp32 [rows, dim / group_size] row stride scales_stride_r
  *            (row groups: [rows, 1]); NULL unless 8 bits
+ *
+ * A row is read once up to 16384 bf16 or 8192 fp32 channels where rows start
+ * and end on 16 bytes, up to 8192 elsewhere; wider rows, and groups at rows
+ * that do not, take a plain kernel (2 to 60 times the time).
  *
  * Host errors (SCONV_ERR_INVALID): negative sizes, eps negative or not
  * finite, NULL required pointer, unknown types, group_size that does not
