@@ -14,6 +14,10 @@ from .ops import (
     causal_conv1d_update_tokens,
     causal_conv1d_varlen_bwd,
     causal_conv1d_varlen_fwd,
+    gated_delta_rule_checkpoints,
+    gated_delta_rule_update,
+    gated_delta_rule_varlen_bwd,
+    gated_delta_rule_varlen_fwd,
     gated_linear_recurrence_checkpoints,
     gated_linear_recurrence_update,
     gated_linear_recurrence_varlen_bwd,
@@ -39,6 +43,10 @@ __all__ = [
     "causal_conv1d_update_tokens",
     "causal_conv1d_varlen_bwd",
     "causal_conv1d_varlen_fwd",
+    "gated_delta_rule_checkpoints",
+    "gated_delta_rule_update",
+    "gated_delta_rule_varlen_bwd",
+    "gated_delta_rule_varlen_fwd",
     "gated_linear_recurrence_checkpoints",
     "gated_linear_recurrence_update",
     "gated_linear_recurrence_varlen_bwd",

@@ -44,6 +44,11 @@ EXPORTS = (
     "rms_norm_fwd",
     "rms_norm_bwd_workspace",
     "rms_norm_bwd",
+    "gated_delta_rule_checkpoint_rows",
+    "gated_delta_rule_workspace",
+    "gated_delta_rule_varlen_fwd",
+    "gated_delta_rule_varlen_bwd",
+    "gated_delta_rule_update",
 )
 
 P = ctypes.c_void_p
@@ -121,6 +126,15 @@ _SIGS = {
     "rms_norm_fwd": [P, I64, P, I64, P, FLT, P, I64, P, I64, P, I64, I32, I64, I32, I32, I32, P],
     "rms_norm_bwd_workspace": [I64, I32, PI64],
     "rms_norm_bwd": [P, I64, P, I64, P, FLT, P, I64, P, I64, P, P, I64, I64, I32, I32, P],
+    "gated_delta_rule_checkpoint_rows": [I64, I32, I32, PI64],
+    "gated_delta_rule_workspace": [I64, I32, I32, I32, I32, I32, PI64, PI64],
+    "gated_delta_rule_varlen_fwd": [*[P, I64, I64] * 5, FLT, P, I64, I64, P, I32, P, P, P, I64, I64,
+                                    P, I64, P, I64, I64, I32, I32, I32, I32, I32, I32, I32, P],
+    "gated_delta_rule_varlen_bwd": [*[P, I64, I64] * 6, FLT, P, I64, P, I32, P, P, I64, P, I64, P,
+                                    I64, *[P, I64, I64] * 5, P, I64, I64, I32, I32, I32, I32, I32,
+                                    I32, I32, P],
+    "gated_delta_rule_update": [*[P, I64, I64] * 5, FLT, P, I64, I64, P, P, I64, I64, I32, I32, I32,
+                                I32, I32, I32, I32, I32, P],
 }
 
 

@@ -1,0 +1,167 @@
+// delta_host.h -- host-side checks shared by the gated delta rule's entry
+// points.
+#pragma once
+
+#include <initializer_list>
+
+#include "delta_rule.h"
+
+namespace sconv {
+
+struct DeltaCall {
+  const char* what;
+  int64_t tokens;
+  int32_t batch, key_heads, heads, K, V, dtype, gate_dtype;
+};
+
+// Workspace in floats: vectors first, then frags (16-byte pieces), then the
+// gradients' states.
+struct DeltaSpace {
+  int64_t vectors, fwd, bwd, bwd_states;
+};
+
+inline DeltaSpace delta_space(int64_t total_T, int32_t batch, int32_t heads, int32_t K, int32_t V,
+                              int32_t dtype) {
+  const int C = delta_chunk(dtype), nf = C == 64 ? kDeltaFrags<64> : kDeltaFrags<32>;
+  const int64_t n = delta_rows(total_T, batch, C) * heads;
+  DeltaSpace s;
+  s.vectors = n * 5 * C;
+  s.fwd = s.vectors + n * 2 * nf * (kFragBytes / 4);
+  s.bwd_states = s.vectors + n * 3 * nf * (kFragBytes / 4);
+  s.bwd = s.bwd_states + n * K * V;
+  return s;
+}
+
+inline int delta_sizes(const DeltaCall& c) {
+  if (c.tokens < 0 || c.batch < 0 || c.key_heads < 0 || c.heads < 0 || c.K < 0 || c.V < 0)
+    return fail(SCONV_ERR_INVALID, "%s: negative size", c.what);
+  if (!valid_dtype(c.dtype)) return fail(SCONV_ERR_INVALID, "%s: unknown dtype", c.what);
+  if (c.gate_dtype != SCONV_F32 && c.gate_dtype != c.dtype)
+    return fail(SCONV_ERR_INVALID, "%s: g and beta are fp32 or of the inputs' type", c.what);
+  if (c.heads > 0 && (c.key_heads < 1 || c.heads % c.key_heads))
+    return fail(SCONV_ERR_INVALID, "%s: %d value heads do not share %d key heads evenly", c.what,
+                c.heads, c.key_heads);
+  if (c.K < 1 && c.heads > 0 && c.V > 0)
+    return fail(SCONV_ERR_INVALID, "%s: K must be positive", c.what);
+  if (c.K > kDeltaMaxK)
+    return fail(SCONV_ERR_UNSUPPORTED, "%s: key heads of %d channels (at most %d)", c.what, c.K,
+                kDeltaMaxK);
+  // chunks, heads and sequences are grid dimensions of one workgroup each at least
+  if (c.tokens > INT32_MAX - 4097 || c.V > (1 << 20) || c.heads > 65535 || c.batch > 65535 ||
+      !valid_grid(delta_rows(c.tokens, c.batch, 32) + 1, 256))
+    return fail(SCONV_ERR_UNSUPPORTED, "%s: too many tokens, sequences, heads or channels", c.what);
+  return SCONV_OK;
+}
+
+// Memory that a call touches: `bytes` from p on, in runs `step` bytes apart
+// (step 0: one run).
+struct DeltaBuffer {
+  const void* p;
+  int64_t bytes, run, step;
+};
+
+inline DeltaBuffer delta_block(const void* p, int64_t bytes) { return {p, bytes, bytes, 0}; }
+
+// A [tokens, heads, width] tensor, channels contiguous.
+inline DeltaBuffer delta_tensor(const void* p, int64_t st, int64_t sh, int64_t tokens,
+                                int64_t heads, int64_t width, int64_t es) {
+  if (!tokens || !heads || !width) return delta_block(p, 0);
+  const int64_t row = (heads - 1) * sh + width, all = (tokens - 1) * st + row;
+  if (tokens > 1 && st >= row) return {p, all * es, row * es, st * es};
+  return delta_block(p, all * es);
+}
+
+// Tensors whose rows lie between each other's (columns of one wider matrix) do not overlap.
+inline bool delta_overlap(const DeltaBuffer& a, const DeltaBuffer& b) {
+  if (!overlap(a.p, a.bytes, b.p, b.bytes)) return false;
+  if (!a.step || a.step != b.step) return true;
+  int64_t d = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p) % a.step;
+  if (d < 0) d += a.step;
+  return d < a.run || a.step - d < b.run;
+}
+
+inline int delta_inputs(const DeltaCall& c, DeltaParams& p, const void* q, int64_t q_t, int64_t q_h,
+                        const void* k, int64_t k_t, int64_t k_h, const void* v, int64_t v_t,
+                        int64_t v_h, const void* g, int64_t g_t, int64_t g_h, const void* beta,
+                        int64_t b_t, int64_t b_h, float scale) {
+  if (!(scale - scale == 0.f)) return fail(SCONV_ERR_INVALID, "%s: scale is not finite", c.what);
+  if (c.tokens > 0 && (!q || !k || !v || !g || !beta))
+    return fail(SCONV_ERR_INVALID, "%s: NULL input", c.what);
+  for (int64_t s : {q_t, q_h, k_t, k_h, v_t, v_h, g_t, g_h, b_t, b_h})
+    if (s < 0) return fail(SCONV_ERR_INVALID, "%s: negative stride", c.what);
+  p.q = q, p.k = k, p.v = v, p.g = g, p.beta = beta;
+  p.q_t = q_t, p.q_h = q_h, p.k_t = k_t, p.k_h = k_h, p.v_t = v_t, p.v_h = v_h;
+  p.g_t = g_t, p.g_h = g_h, p.b_t = b_t, p.b_h = b_h;
+  p.batch = c.batch, p.heads = c.heads, p.K = c.K, p.V = c.V;
+  p.group = c.heads / c.key_heads;
+  p.scale = scale;
+  p.gates_f32 = c.gate_dtype == SCONV_F32;
+  // rows that start and end on 16 bytes load as vectors
+  const int64_t n = 16 / elem_size(c.dtype);
+  auto vec = [&](const void* t, int64_t st, int64_t sh) {
+    return aligned16(t) && st % n == 0 && sh % n == 0 && c.K % n == 0;
+  };
+  p.q_vec = vec(q, q_t, q_h), p.k_vec = vec(k, k_t, k_h);
+  return SCONV_OK;
+}
+
+inline void delta_packing(const DeltaCall&, DeltaParams& p, const int32_t* qsl, const int32_t* slots,
+                          const uint8_t* has, int32_t pad) {
+  p.qsl = qsl, p.slots = slots, p.has = has, p.pad = pad;
+}
+
+// An fp32 [num_slots, heads, K, V] pool, dense but for the slots.
+inline int delta_pool(const DeltaCall& c, const void* pool, int64_t slots, int64_t stride,
+                      bool indexed, const char* name, DeltaBuffer* out) {
+  *out = delta_block(pool, 0);
+  if (!pool) return SCONV_OK;
+  const int64_t one = (int64_t)c.heads * c.K * c.V;
+  if (slots < 0 || (slots > 1 && stride < one))
+    return fail(SCONV_ERR_INVALID, "%s: %s: slots overlap", c.what, name);
+  if (!indexed && slots < c.batch)
+    return fail(SCONV_ERR_INVALID, "%s: %s has %lld slots, needs %d", c.what, name,
+                (long long)slots, c.batch);
+  *out = delta_block(pool, slots ? ((slots - 1) * stride + one) * 4 : 0);
+  return SCONV_OK;
+}
+
+// An output [tokens, heads, width]: no two elements in one place.
+inline int delta_output(const DeltaCall& c, const void* t, int64_t st, int64_t sh, int64_t heads,
+                        int64_t width, const char* name, DeltaBuffer* out, int64_t es = 0) {
+  es = es ? es : elem_size(c.dtype);
+  *out = delta_block(t, 0);
+  if (c.tokens == 0) return SCONV_OK;
+  if (!t) return fail(SCONV_ERR_INVALID, "%s: NULL %s", c.what, name);
+  if (st < 0 || sh < 0) return fail(SCONV_ERR_INVALID, "%s: negative stride", c.what);
+  const bool rows = heads == 1 || (sh >= width && (c.tokens == 1 || st >= (heads - 1) * sh + width));
+  const bool planes = c.tokens == 1 || (st >= width && (heads == 1 || sh >= (c.tokens - 1) * st + width));
+  if (heads == 1 ? !planes : !(rows || planes))
+    return fail(SCONV_ERR_INVALID, "%s: elements of %s share memory", c.what, name);
+  *out = delta_tensor(t, st, sh, c.tokens, heads, width, es);
+  return SCONV_OK;
+}
+
+// Outputs overlap neither each other nor an input (the first may be v itself).
+inline int delta_disjoint(const DeltaCall& c, const DeltaParams& p,
+                          std::initializer_list<DeltaBuffer> outs, bool first_is_v = false) {
+  const int64_t es = elem_size(c.dtype), gs = elem_size(c.gate_dtype);
+  const DeltaBuffer ins[] = {delta_tensor(p.v, p.v_t, p.v_h, c.tokens, c.heads, c.V, es),
+                             delta_tensor(p.q, p.q_t, p.q_h, c.tokens, c.key_heads, c.K, es),
+                             delta_tensor(p.k, p.k_t, p.k_h, c.tokens, c.key_heads, c.K, es),
+                             delta_tensor(p.g, p.g_t, p.g_h, c.tokens, c.heads, 1, gs),
+                             delta_tensor(p.beta, p.b_t, p.b_h, c.tokens, c.heads, 1, gs)};
+  const DeltaBuffer* o = outs.begin();
+  for (size_t i = 0; i < outs.size(); ++i) {
+    for (size_t j = 0; j < i; ++j)
+      if (delta_overlap(o[i], o[j]))
+        return fail(SCONV_ERR_INVALID, "%s: outputs, states or workspace overlap", c.what);
+    for (int j = 0; j < 5; ++j) {
+      if (i == 0 && j == 0 && first_is_v) continue;
+      if (delta_overlap(o[i], ins[j]))
+        return fail(SCONV_ERR_INVALID, "%s: an output overlaps an input", c.what);
+    }
+  }
+  return SCONV_OK;
+}
+
+}  // namespace sconv

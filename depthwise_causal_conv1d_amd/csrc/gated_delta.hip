@@ -1,0 +1,457 @@
+// gated_delta.hip -- the gated delta rule over packed sequences and its
+// one-token update, for gfx950.  The mathematics is in delta_rule.h.
+#include "delta_prep.h"
+#include "delta_host.h"
+
+namespace sconv {
+
+struct DeltaFwd {
+  DeltaParams p;
+  float* states;
+  int64_t st_slot;
+  void* out;
+  int64_t o_t, o_h;
+  float* marks;
+};
+
+constexpr int kWalkWaves = 4;
+
+// One workgroup walks a sequence's chunks for one value head and 16 NC columns
+// a wave.
+template <typename D, int KP, int NC>
+__global__ __launch_bounds__(64 * kWalkWaves, 2) void delta_walk_kernel(DeltaFwd a) {
+  using T = Tile<D>;
+  using S = typename D::storage;
+  constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32;
+  constexpr int NF = kDeltaFrags<C>, THREADS = 64 * kWalkWaves;
+  using Rows = LdsRows<D, KP>;
+  __shared__ __attribute__((aligned(16))) S lk[C * Rows::LD];
+  __shared__ __attribute__((aligned(16))) S lq[C * Rows::LD];
+  __shared__ __attribute__((aligned(16))) char lf[2 * NF * kFragBytes];
+  __shared__ __attribute__((aligned(16))) float lv[3 * C];
+
+  const DeltaParams& p = a.p;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int32_t h = blockIdx.y, b = blockIdx.z, kh = h / p.group;
+  const int32_t slot = p.slots ? p.slots[b] : b;
+  if (p.slots && slot == p.pad) return;
+  const int32_t start = p.qsl[b], end = p.qsl[b + 1];
+  const int32_t col0 = (blockIdx.x * kWalkWaves + wave) * 16 * NC + r * NC;  // columns col0 + 0 .. NC - 1
+  const int64_t KV = (int64_t)p.K * p.V;
+
+  f32x4 s[KT][NC];
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int n = 0; n < NC; ++n) s[t][n] = zero4();
+  float* state = a.states ? a.states + slot * a.st_slot + h * KV : nullptr;
+  auto each_state = [&](auto&& f) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = 16 * t + 4 * g + e;
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+          if (k < p.K && col0 + n < p.V) s[t][n][e] = f((int64_t)k * p.V + col0 + n, s[t][n][e]);
+      }
+  };
+  if (p.has && p.has[b]) each_state([&](int64_t i, float) { return state[i]; });
+
+  // a thread's share of a chunk's K, Q, frags and vectors on its way to LDS
+  constexpr int O8 = C * KP / 8 / THREADS;                    // octets of K, and of Q
+  constexpr int F16 = 2 * NF * kFragBytes / 16 / THREADS;     // 16-byte pieces of the frags
+  typename T::Exact nk[O8], nq[O8];
+  u32x4 nf[F16];
+  float nv = 0.f;
+  const S* q = static_cast<const S*>(p.q) + kh * p.q_h;
+  const S* k = static_cast<const S*>(p.k) + kh * p.k_h;
+  const int32_t row0 = start / C + b;
+  auto fetch = [&](int32_t i) {
+    const int32_t t0 = start + i * C;
+    const int64_t at = (int64_t)(row0 + i) * p.heads + h;
+#pragma unroll
+    for (int o = 0; o < O8; ++o) {
+      const int x = threadIdx.x + o * THREADS, t = x / (KP / 8), k0 = x % (KP / 8) * 8;
+      nk[o] = zero8<D>(), nq[o] = zero8<D>();
+      if (t0 + t < end) {
+        nk[o] = row8<D>(k + (int64_t)(t0 + t) * p.k_t, k0, p.K, p.k_vec);
+        nq[o] = row8<D>(q + (int64_t)(t0 + t) * p.q_t, k0, p.K, p.q_vec);
+      }
+    }
+    const u32x4* f = reinterpret_cast<const u32x4*>(p.frags + at * (2 * NF) * kFragBytes);
+#pragma unroll
+    for (int o = 0; o < F16; ++o) nf[o] = f[threadIdx.x + o * THREADS];
+    if (threadIdx.x < 3 * C) nv = p.vectors[at * kDeltaVectors<C> + threadIdx.x];
+  };
+  auto stage = [&]() {
+#pragma unroll
+    for (int o = 0; o < O8; ++o) {
+      const int x = threadIdx.x + o * THREADS, t = x / (KP / 8), k0 = x % (KP / 8) * 8;
+      Rows::put8(lk, t, k0, nk[o]);
+      Rows::put8(lq, t, k0, nq[o]);
+    }
+#pragma unroll
+    for (int o = 0; o < F16; ++o) reinterpret_cast<u32x4*>(lf)[threadIdx.x + o * THREADS] = nf[o];
+    if (threadIdx.x < 3 * C) lv[threadIdx.x] = nv;
+  };
+
+  const S* v = static_cast<const S*>(p.v) + h * p.v_h;
+  S* out = static_cast<S*>(a.out) + h * a.o_h;
+  const int32_t chunks = (end - start + C - 1) / C;
+  if (chunks > 0) fetch(0);
+  for (int32_t i = 0; i < chunks; ++i) {
+    const int32_t t0 = start + i * C, len = end - t0;
+    __syncthreads();
+    stage();
+    __syncthreads();
+    if (i + 1 < chunks) fetch(i + 1);
+    if (a.marks) {
+      float* mark = a.marks + ((int64_t)(row0 + i) * p.heads + h) * KV;
+      each_state([&](int64_t x, float w) { return mark[x] = w; });
+    }
+    f32x4 u[NT][NC];  // V, then R, then U
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int x = 16 * t + 4 * g + e;
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+          u[t][n][e] = x < len && col0 + n < p.V
+                           ? to_float<D>(v[(int64_t)(t0 + x) * p.v_t + col0 + n]) : 0.f;
+      }
+    f32x4 xs[NT][NC], ys[NT][NC];  // K S, Q S
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int n = 0; n < NC; ++n) xs[t][n] = zero4(), ys[t][n] = zero4();
+#pragma unroll
+    for (int c = 0; c < KS; ++c) {
+      typename T::Split sp[NC];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) sp[n] = T::split(s[2 * c][n], s[2 * c + 1][n]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const auto kf = Rows::rows(lk, 16 * t, 32 * c, lane);
+        const auto qf = Rows::rows(lq, 16 * t, 32 * c, lane);
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          xs[t][n] = T::mul(kf, sp[n], xs[t][n]);
+          ys[t][n] = T::mul(qf, sp[n], ys[t][n]);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const f32x4 gam = lds4(lv + 16 * t + 4 * g), bt = lds4(lv + 2 * C + 16 * t + 4 * g);
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          u[t][n][e] = bt[e] * (u[t][n][e] - gam[e] * xs[t][n][e]);
+          ys[t][n][e] *= p.scale * gam[e];
+        }
+    }
+    {
+      typename T::Split rs[CS][NC];
+#pragma unroll
+      for (int c = 0; c < CS; ++c)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) rs[c][n] = T::split(u[2 * c][n], u[2 * c + 1][n]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c <= t / 2; ++c) {
+          const auto nf2 = T::get(lf + lower_frag<C>(t, c) * kFragBytes, lane);
+#pragma unroll
+          for (int n = 0; n < NC; ++n) u[t][n] = T::mul(nf2, rs[c][n], u[t][n]);
+        }
+    }
+    {
+      typename T::Split us[CS][NC];
+#pragma unroll
+      for (int c = 0; c < CS; ++c)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) us[c][n] = T::split(u[2 * c][n], u[2 * c + 1][n]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c <= t / 2; ++c) {
+          const auto pf = T::get(lf + (NF + lower_frag<C>(t, c)) * kFragBytes, lane);
+#pragma unroll
+          for (int n = 0; n < NC; ++n) ys[t][n] = T::mul(pf, us[c][n], ys[t][n]);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int x = 16 * t + 4 * g + e;
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+          if (x < len && col0 + n < p.V)
+            out[(int64_t)(t0 + x) * a.o_t + col0 + n] = delta_round<D>(ys[t][n][e]);
+      }
+    const float whole = lv[C - 1];
+    typename T::Fine us[CS][NC];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const f32x4 left = lds4(lv + C + 16 * t + 4 * g);
+#pragma unroll
+      for (int n = 0; n < NC; ++n) u[t][n] *= left;
+    }
+#pragma unroll
+    for (int c = 0; c < CS; ++c)
+#pragma unroll
+      for (int n = 0; n < NC; ++n) us[c][n] = T::fine(u[2 * c][n], u[2 * c + 1][n]);
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+#pragma unroll
+      for (int n = 0; n < NC; ++n) s[t][n] *= whole;
+#pragma unroll
+      for (int c = 0; c < CS; ++c) {
+        const auto kf = Rows::cols(lk, 32 * c, 16 * t, lane);
+#pragma unroll
+        for (int n = 0; n < NC; ++n) s[t][n] = T::mul(kf, us[c][n], s[t][n]);
+      }
+    }
+  }
+  if (state) each_state([&](int64_t i, float w) { return state[i] = w; });
+}
+
+// ---------------------------------------------------------------- one token
+
+struct DeltaUpdate {
+  DeltaParams p;  // rows instead of tokens
+  float* states;
+  int64_t st_slot;
+  void* out;
+  int64_t o_t, o_h;
+};
+
+constexpr int kUpdateThreads = 256;
+
+// One workgroup a row, value head and CL * VEC columns of the state, which it
+// reads and writes once.  Both products with the old state are summed in one
+// pass, since S^T q = S'^T q + (k.q) u: one meeting of the row groups.
+template <typename D, int CL, int VEC>
+__global__ __launch_bounds__(kUpdateThreads) void delta_update_kernel(DeltaUpdate a) {
+  using S = typename D::storage;
+  typedef float vf __attribute__((ext_vector_type(VEC)));
+  constexpr int RG = kUpdateThreads / CL, RPG = kDeltaMaxK / RG;
+  __shared__ float lk[kDeltaMaxK], lq[kDeltaMaxK];
+  __shared__ float part[2][RG][CL * VEC];
+  const DeltaParams& p = a.p;
+  const int32_t b = blockIdx.z, h = blockIdx.y, kh = h / p.group;
+  const int32_t slot = p.slots ? p.slots[b] : b;
+  if (p.slots && slot == p.pad) return;
+  const int cl = threadIdx.x % CL, rg = threadIdx.x / CL;
+  const int32_t col = (blockIdx.x * CL + cl) * VEC;
+  const bool on = col < p.V;
+  float* state = a.states + slot * a.st_slot + (int64_t)h * p.K * p.V + col;
+  vf s[RPG];
+#pragma unroll
+  for (int j = 0; j < RPG; ++j) {
+    const int k = rg + RG * j;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s[j][e] = 0.f;
+    if (on && k < p.K) s[j] = *reinterpret_cast<const vf*>(state + (int64_t)k * p.V);
+  }
+  if (threadIdx.x < kDeltaMaxK) {
+    const int k = threadIdx.x;
+    lk[k] = k < p.K ? load_as_float<D>(static_cast<const S*>(p.k) + b * p.k_t + kh * p.k_h + k) : 0.f;
+    lq[k] = k < p.K ? load_as_float<D>(static_cast<const S*>(p.q) + b * p.q_t + kh * p.q_h + k) : 0.f;
+  }
+  const float decay = expf(delta_bound(delta_gate(p, p.g, b * p.g_t + h * p.g_h)));
+  const float beta = delta_gate(p, p.beta, b * p.b_t + h * p.b_h);
+  float v[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e)
+    v[e] = on ? load_as_float<D>(static_cast<const S*>(p.v) + b * p.v_t + h * p.v_h + col + e) : 0.f;
+  __syncthreads();
+  vf x = s[0] * 0.f, y = x;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) x[e] = 0.f, y[e] = 0.f;
+#pragma unroll
+  for (int j = 0; j < RPG; ++j) {
+    s[j] *= decay;
+    x += s[j] * lk[rg + RG * j];
+    y += s[j] * lq[rg + RG * j];
+  }
+  *reinterpret_cast<vf*>(&part[0][rg][cl * VEC]) = x;
+  *reinterpret_cast<vf*>(&part[1][rg][cl * VEC]) = y;
+  float kq = 0.f;
+  {
+    const int l = threadIdx.x & 63;
+    kq = lk[l] * lq[l] + lk[l + 64] * lq[l + 64];
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) kq += __shfl_xor(kq, d, 64);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) x[e] = 0.f, y[e] = 0.f;
+#pragma unroll
+  for (int w = 0; w < RG; ++w) {
+    x += *reinterpret_cast<const vf*>(&part[0][w][cl * VEC]);
+    y += *reinterpret_cast<const vf*>(&part[1][w][cl * VEC]);
+  }
+  vf u;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) u[e] = beta * (v[e] - x[e]);
+  if (!on) return;
+#pragma unroll
+  for (int j = 0; j < RPG; ++j) {
+    const int k = rg + RG * j;
+    if (k < p.K) *reinterpret_cast<vf*>(state + (int64_t)k * p.V) = s[j] + u * lk[k];
+  }
+  if (rg == 0) {
+    S* out = static_cast<S*>(a.out) + b * a.o_t + h * a.o_h + col;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = delta_round<D>(p.scale * (y[e] + kq * u[e]));
+  }
+}
+
+template <typename D, int KP>
+static int delta_forward(const DeltaFwd& a, int64_t rows, hipStream_t stream) {
+  const DeltaParams& p = a.p;
+  hipLaunchKernelGGL((delta_prep_kernel<D, KP, false>), dim3((uint32_t)rows, p.heads), dim3(64), 0,
+                     stream, p);
+  if (int rc = check_launch("gated_delta_rule_varlen_fwd")) return rc;
+  const int cols = 16 * kWalkWaves;
+  hipLaunchKernelGGL((delta_walk_kernel<D, KP, 1>), dim3((p.V + cols - 1) / cols, p.heads, p.batch),
+                     dim3(64 * kWalkWaves), 0, stream, a);
+  return check_launch("gated_delta_rule_varlen_fwd");
+}
+
+template <typename D, int CL, int VEC>
+static void delta_update_launch(const DeltaUpdate& a, hipStream_t stream) {
+  const int cols = CL * VEC;
+  hipLaunchKernelGGL((delta_update_kernel<D, CL, VEC>),
+                     dim3((a.p.V + cols - 1) / cols, a.p.heads, a.p.batch), dim3(kUpdateThreads), 0,
+                     stream, a);
+}
+
+template <typename D> static void delta_update_pick(const DeltaUpdate& a, hipStream_t stream) {
+  const DeltaParams& p = a.p;
+  const bool vec = p.V % 4 == 0 && aligned16(a.states) && a.st_slot % 4 == 0;
+  if (!vec) delta_update_launch<D, 64, 1>(a, stream);
+  else if (p.V <= 64) delta_update_launch<D, 16, 4>(a, stream);
+  else delta_update_launch<D, 32, 4>(a, stream);
+}
+
+}  // namespace sconv
+
+extern "C" int gated_delta_rule_checkpoint_rows(int64_t total_T, int32_t batch, int32_t dtype,
+                                                int64_t* rows) {
+  using namespace sconv;
+  clear_error();
+  if (total_T < 0 || batch < 0 || !valid_dtype(dtype) || !rows)
+    return fail(SCONV_ERR_INVALID, "gated_delta_rule_checkpoint_rows: bad argument");
+  *rows = delta_rows(total_T, batch, delta_chunk(dtype));
+  return SCONV_OK;
+}
+
+extern "C" int gated_delta_rule_workspace(int64_t total_T, int32_t batch, int32_t heads, int32_t K,
+                                          int32_t V, int32_t dtype, int64_t* fwd_floats,
+                                          int64_t* bwd_floats) {
+  using namespace sconv;
+  clear_error();
+  if (total_T < 0 || batch < 0 || heads < 0 || K < 0 || V < 0 || !valid_dtype(dtype) ||
+      !fwd_floats || !bwd_floats)
+    return fail(SCONV_ERR_INVALID, "gated_delta_rule_workspace: bad argument");
+  const DeltaSpace s = delta_space(total_T, batch, heads, K, V, dtype);
+  *fwd_floats = s.fwd;
+  *bwd_floats = s.bwd;
+  return SCONV_OK;
+}
+
+extern "C" int gated_delta_rule_varlen_fwd(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k, int64_t k_stride_t,
+    int64_t k_stride_h, const void* v, int64_t v_stride_t, int64_t v_stride_h, const void* g,
+    int64_t g_stride_t, int64_t g_stride_h, const void* beta, int64_t b_stride_t,
+    int64_t b_stride_h, float scale, float* states, int64_t num_slots, int64_t st_stride_slot,
+    const int32_t* query_start_loc, int32_t batch, const int32_t* cache_indices,
+    const uint8_t* has_initial_state, void* out, int64_t out_stride_t, int64_t out_stride_h,
+    float* checkpoints, int64_t checkpoint_rows, float* workspace, int64_t workspace_floats,
+    int64_t total_T, int32_t key_heads, int32_t value_heads, int32_t K, int32_t V, int32_t dtype,
+    int32_t gate_dtype, int32_t pad_slot_id, hipStream_t stream) {
+  using namespace sconv;
+  clear_error();
+  const char* what = "gated_delta_rule_varlen_fwd";
+  DeltaFwd a = {};
+  DeltaCall c = {what, total_T, batch, key_heads, value_heads, K, V, dtype, gate_dtype};
+  if (int rc = delta_sizes(c)) return rc;
+  if (batch == 0 || value_heads == 0 || V == 0) return SCONV_OK;
+  if (!query_start_loc) return fail(SCONV_ERR_INVALID, "%s: NULL query_start_loc", what);
+  if (int rc = delta_inputs(c, a.p, q, q_stride_t, q_stride_h, k, k_stride_t, k_stride_h, v,
+                            v_stride_t, v_stride_h, g, g_stride_t, g_stride_h, beta, b_stride_t,
+                            b_stride_h, scale))
+    return rc;
+  delta_packing(c, a.p, query_start_loc, cache_indices, has_initial_state, pad_slot_id);
+  if (has_initial_state && !states)
+    return fail(SCONV_ERR_INVALID, "%s: has_initial_state without states", what);
+  DeltaBuffer pool, o;
+  if (int rc = delta_pool(c, states, num_slots, st_stride_slot, cache_indices != nullptr, "states",
+                          &pool))
+    return rc;
+  if (int rc = delta_output(c, out, out_stride_t, out_stride_h, value_heads, V, "out", &o)) return rc;
+  const int64_t rows = delta_rows(total_T, batch, delta_chunk(dtype));
+  const int64_t KV = (int64_t)K * V;
+  if (checkpoints && checkpoint_rows < rows)
+    return fail(SCONV_ERR_INVALID, "%s: %lld checkpoint rows, needs %lld", what,
+                (long long)checkpoint_rows, (long long)rows);
+  const DeltaSpace s = delta_space(total_T, batch, value_heads, K, V, dtype);
+  if (!workspace || workspace_floats < s.fwd || !aligned16(workspace))
+    return fail(SCONV_ERR_INVALID, "%s: workspace needs %lld floats at 16 bytes", what,
+                (long long)s.fwd);
+  const DeltaBuffer marks = delta_block(checkpoints, checkpoints ? rows * value_heads * KV * 4 : 0);
+  const DeltaBuffer work = delta_block(workspace, s.fwd * 4);
+  if (int rc = delta_disjoint(c, a.p, {o, pool, marks, work}, /*out may be v=*/out == v &&
+                              out_stride_t == v_stride_t && out_stride_h == v_stride_h))
+    return rc;
+  a.p.vectors = workspace;
+  a.p.frags = reinterpret_cast<char*>(workspace + s.vectors);
+  a.states = states, a.st_slot = st_stride_slot;
+  a.out = out, a.o_t = out_stride_t, a.o_h = out_stride_h;
+  a.marks = checkpoints;
+  if (dtype == SCONV_BF16)
+    return K <= 64 ? delta_forward<Bf16, 64>(a, rows, stream) : delta_forward<Bf16, 128>(a, rows, stream);
+  return K <= 64 ? delta_forward<F32, 64>(a, rows, stream) : delta_forward<F32, 128>(a, rows, stream);
+}
+
+extern "C" int gated_delta_rule_update(
+    const void* q, int64_t q_stride_b, int64_t q_stride_h, const void* k, int64_t k_stride_b,
+    int64_t k_stride_h, const void* v, int64_t v_stride_b, int64_t v_stride_h, const void* g,
+    int64_t g_stride_b, int64_t g_stride_h, const void* beta, int64_t b_stride_b,
+    int64_t b_stride_h, float scale, float* states, int64_t num_slots, int64_t st_stride_slot,
+    const int32_t* state_indices, void* out, int64_t out_stride_b, int64_t out_stride_h,
+    int32_t batch, int32_t key_heads, int32_t value_heads, int32_t K, int32_t V, int32_t dtype,
+    int32_t gate_dtype, int32_t pad_slot_id, hipStream_t stream) {
+  using namespace sconv;
+  clear_error();
+  const char* what = "gated_delta_rule_update";
+  DeltaUpdate a = {};
+  DeltaCall c = {what, batch, batch, key_heads, value_heads, K, V, dtype, gate_dtype};
+  if (int rc = delta_sizes(c)) return rc;
+  if (batch == 0 || value_heads == 0 || V == 0) return SCONV_OK;
+  if (int rc = delta_inputs(c, a.p, q, q_stride_b, q_stride_h, k, k_stride_b, k_stride_h, v,
+                            v_stride_b, v_stride_h, g, g_stride_b, g_stride_h, beta, b_stride_b,
+                            b_stride_h, scale))
+    return rc;
+  delta_packing(c, a.p, nullptr, state_indices, nullptr, pad_slot_id);
+  if (!states) return fail(SCONV_ERR_INVALID, "%s: NULL states", what);
+  DeltaBuffer pool, o;
+  if (int rc = delta_pool(c, states, num_slots, st_stride_slot, state_indices != nullptr, "states",
+                          &pool))
+    return rc;
+  if (int rc = delta_output(c, out, out_stride_b, out_stride_h, value_heads, V, "out", &o)) return rc;
+  if (int rc = delta_disjoint(c, a.p, {o, pool}, out == v && out_stride_b == v_stride_b &&
+                              out_stride_h == v_stride_h))
+    return rc;
+  a.states = states, a.st_slot = st_stride_slot;
+  a.out = out, a.o_t = out_stride_b, a.o_h = out_stride_h;
+  if (dtype == SCONV_BF16) delta_update_pick<Bf16>(a, stream);
+  else delta_update_pick<F32>(a, stream);
+  return check_launch(what);
+}

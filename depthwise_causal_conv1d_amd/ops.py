@@ -903,3 +903,187 @@ def rms_norm_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, eps:
     _call("rms_norm_bwd", x, *a[:4], weight.data_ptr(), eps, *a[4:], dweight.data_ptr(),
           ws.data_ptr(), n, rows, dim, dt)
     return dx, dweight
+
+
+# ---------------------------------------------------------------- gated delta rule
+
+def _heads(shape, what: str, *ts):
+    """[ptr, stride_t, stride_h] of each [tokens, heads, channels] tensor."""
+    args = []
+    wide = shape[2] > 1
+    for t in ts:
+        stride = t.stride()
+        if t.shape != shape or (wide and stride[2] != 1):
+            raise ValueError(f"{what} must be {list(shape)} with contiguous channels")
+        args += (t.data_ptr(), stride[0], stride[1])
+    return args
+
+
+def _delta(q, k, v, g, beta):
+    """(pointers and strides of the inputs, sizes, types) after checks."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k [tokens, key_heads, K], v [tokens, value_heads, V]")
+    tokens, key_heads, K = q.shape
+    _, value_heads, V = v.shape
+    dt = _same_type(q, "q, k, v and out", k, v)
+    if g.dtype != beta.dtype or g.dtype not in (torch.float32, q.dtype):
+        raise TypeError("g and beta must both be float32 or of the inputs' type")
+    if g.shape != (tokens, value_heads) or beta.shape != g.shape or v.shape[0] != tokens:
+        raise ValueError("g and beta must be [tokens, value_heads], as v is")
+    args = _heads(q.shape, "q and k", q, k) + _heads(v.shape, "v", v)
+    for t in (g, beta):
+        args += (t.data_ptr(), *t.stride())
+    return args, (key_heads, value_heads, K, V, dt, _DT[g.dtype])
+
+
+def _matrix_pool(t: Optional[torch.Tensor], heads: int, K: int, V: int, name: str):
+    """(ptr, slots, slot stride) of an fp32 [num_slots, heads, K, V] state pool."""
+    if t is None:
+        return None, 0, 0
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    if t.dim() != 4 or t.shape[1:] != (heads, K, V):
+        raise ValueError(f"{name} must be [num_slots, value_heads, K, V]")
+    if t.shape[0] and not t[0].is_contiguous():
+        raise ValueError(f"{name} needs dense slots")
+    return t.data_ptr(), t.shape[0], t.stride(0)
+
+
+def _delta_marks(t: Optional[torch.Tensor], heads: int, K: int, V: int):
+    if t is None:
+        return 0
+    if t.dtype != torch.float32 or t.dim() != 4 or t.shape[1:] != (heads, K, V) \
+            or not t.is_contiguous():
+        raise ValueError("checkpoints must be a dense float32 [rows, value_heads, K, V] tensor")
+    return t.shape[0]
+
+
+def _delta_workspace(tokens: int, batch: int, sizes, backward: bool, x: torch.Tensor):
+    """(tensor, floats) of workspace for one packed call."""
+    fwd = ctypes.c_int64()
+    bwd = _floats("gated_delta_rule_workspace", tokens, batch, *sizes[1:5], ctypes.byref(fwd))
+    n = bwd if backward else fwd.value
+    return torch.empty(n, dtype=torch.float32, device=x.device), n
+
+
+def _delta_scale(scale: Optional[float], K: int) -> float:
+    return (K ** -0.5 if K else 1.0) if scale is None else float(scale)
+
+
+def gated_delta_rule_checkpoints(k: torch.Tensor, v: torch.Tensor, query_start_loc: torch.Tensor
+                                 ) -> torch.Tensor:
+    """The buffer in which gated_delta_rule_varlen_fwd leaves what its backward
+    call needs, for inputs like k [total_T, key_heads, K] and v [total_T,
+    value_heads, V]."""
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k [total_T, key_heads, K], v [total_T, value_heads, V]")
+    rows = _floats("gated_delta_rule_checkpoint_rows", v.shape[0], query_start_loc.numel() - 1,
+                   _dtype(v))
+    return torch.empty(rows, v.shape[1], k.shape[2], v.shape[2], dtype=torch.float32,
+                       device=v.device)
+
+
+def gated_delta_rule_varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                g: torch.Tensor, beta: torch.Tensor,
+                                states: Optional[torch.Tensor], query_start_loc: torch.Tensor,
+                                cache_indices: Optional[torch.Tensor] = None,
+                                has_initial_state: Optional[torch.Tensor] = None,
+                                scale: Optional[float] = None, pad_slot_id: int = -1,
+                                out: Optional[torch.Tensor] = None,
+                                checkpoints: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """S' = exp(g) S, u = beta (v - S'^T k), S = S' + k u^T, out = scale S^T q
+    over packed sequences, a K x V state for each value head.
+
+    q, k [total_T, key_heads, K], v [total_T, value_heads, V], g, beta
+    [total_T, value_heads] (float32 or the inputs' type); key head kh serves
+    value_heads / key_heads value heads.  states float32 [num_slots,
+    value_heads, K, V] is updated in place (None: start at zero, keep nothing).
+    scale: None is K ** -0.5.  ``checkpoints`` (gated_delta_rule_checkpoints)
+    is filled for the backward call.  With ``out`` None a new tensor is
+    returned, whose rows outside the sequences (or in skipped ones) are
+    undefined."""
+    _one_device(q, k, v, g, beta, states, query_start_loc, cache_indices, has_initial_state, out,
+                checkpoints)
+    args, sizes = _delta(q, k, v, g, beta)
+    _, heads, K, V, _, _ = sizes
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    _same_type(v, "q, k, v and out", out)
+    batch, hi = _packing(query_start_loc, cache_indices, has_initial_state)
+    pool = _matrix_pool(states, heads, K, V, "states")
+    rows = _delta_marks(checkpoints, heads, K, V)
+    tokens = v.shape[0]
+    ws, n = _delta_workspace(tokens, batch, sizes, False, v)
+    _call("gated_delta_rule_varlen_fwd", v, *args, _delta_scale(scale, K), *pool,
+          query_start_loc.data_ptr(), batch, _ptr(cache_indices), _ptr(hi),
+          *_heads(v.shape, "out", out), _ptr(checkpoints), rows, ws.data_ptr(), n, tokens, *sizes,
+          int(pad_slot_id))
+    return out
+
+
+def gated_delta_rule_varlen_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                                v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                                checkpoints: torch.Tensor, query_start_loc: torch.Tensor,
+                                cache_indices: Optional[torch.Tensor] = None,
+                                has_initial_state: Optional[torch.Tensor] = None,
+                                scale: Optional[float] = None, pad_slot_id: int = -1,
+                                dfinal_states: Optional[torch.Tensor] = None,
+                                dinitial_states: Optional[torch.Tensor] = None,
+                                dq: Optional[torch.Tensor] = None,
+                                dk: Optional[torch.Tensor] = None,
+                                dv: Optional[torch.Tensor] = None):
+    """Gradients of gated_delta_rule_varlen_fwd: (dq, dk, dv, dg, dbeta), dq
+    and dk summed over the value heads of a key head.  ``checkpoints`` is what
+    the forward call left; the other inputs are the forward's.  dfinal_states /
+    dinitial_states float32 [num_slots, value_heads, K, V]: gradient of each
+    sequence's last state (read) and of its initial state (written).  Gradients
+    made here are undefined at tokens outside the sequences (or in skipped
+    ones)."""
+    _one_device(v, dout, q, k, g, beta, checkpoints, query_start_loc, cache_indices,
+                has_initial_state, dfinal_states, dinitial_states, dq, dk, dv)
+    args, sizes = _delta(q, k, v, g, beta)
+    _, heads, K, V, _, _ = sizes
+    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    dq = new(q) if dq is None else dq
+    dk = new(k) if dk is None else dk
+    dv = new(v) if dv is None else dv
+    dg, dbeta = new(g), new(beta)
+    _same_type(v, "q, k, v, dout and their gradients", dout, dq, dk, dv)
+    batch, hi = _packing(query_start_loc, cache_indices, has_initial_state)
+    dfinal, slots, df_stride = _matrix_pool(dfinal_states, heads, K, V, "dfinal_states")
+    dinitial, di_slots, di_stride = _matrix_pool(dinitial_states, heads, K, V, "dinitial_states")
+    if slots and di_slots and slots != di_slots:
+        raise ValueError("dfinal_states and dinitial_states must have one shape")
+    rows = _delta_marks(checkpoints, heads, K, V)
+    tokens = v.shape[0]
+    ws, n = _delta_workspace(tokens, batch, sizes, True, v)
+    _call("gated_delta_rule_varlen_bwd", v, *_heads(v.shape, "dout", dout), *args,
+          _delta_scale(scale, K), checkpoints.data_ptr(), rows, query_start_loc.data_ptr(), batch,
+          _ptr(cache_indices), _ptr(hi), slots or di_slots, dfinal, df_stride, dinitial, di_stride,
+          *_heads(q.shape, "dq and dk", dq, dk), *_heads(v.shape, "dv", dv), dg.data_ptr(),
+          *dg.stride(), dbeta.data_ptr(), *dbeta.stride(), ws.data_ptr(), n, tokens, *sizes,
+          int(pad_slot_id))
+    return dq, dk, dv, dg, dbeta
+
+
+def gated_delta_rule_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                            beta: torch.Tensor, states: torch.Tensor,
+                            state_indices: Optional[torch.Tensor] = None,
+                            scale: Optional[float] = None, pad_slot_id: int = -1,
+                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One decode token per row: q, k [batch, key_heads, K], v [batch,
+    value_heads, V], g, beta [batch, value_heads]; states float32 [num_slots,
+    value_heads, K, V] updated in place.  scale: None is K ** -0.5.  With
+    ``out`` None a new tensor is returned, whose skipped rows are undefined."""
+    _one_device(q, k, v, g, beta, states, state_indices, out)
+    args, sizes = _delta(q, k, v, g, beta)
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    _same_type(v, "q, k, v and out", out)
+    pool = _matrix_pool(states, *sizes[1:4], "states")
+    batch = v.shape[0]
+    if state_indices is not None:
+        _dense(state_indices, torch.int32, "state_indices", batch)
+    _call("gated_delta_rule_update", v, *args, _delta_scale(scale, sizes[2]), *pool,
+          _ptr(state_indices), *_heads(v.shape, "out", out), batch, *sizes, int(pad_slot_id))
+    return out

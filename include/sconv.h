@@ -789,6 +789,144 @@ int rms_norm_bwd(const void* dout, int64_t dout_stride_r, const void* x, int64_t
                  float* workspace, int64_t workspace_floats, int64_t rows, int32_t dim,
                  int32_t dtype, hipStream_t stream);
 
+/*
+ * Gated delta rule
+ * ----------------
+ * The recurrent step of a layer whose short conv feeds a matrix state.  Per
+ * value head and token of one sequence, with S a K x V matrix in fp32:
+ *     S' = exp(g_t) S_{t-1},  u_t = beta_t (v_t - S'^T k_t)
+ *     S_t = S' + k_t u_t^T,   out_t = scale S_t^T q_t
+ * Key head kh serves the value heads kh * group .. + group - 1, group =
+ * value_heads / key_heads.  A caller normalises q and k beforehand where its
+ * model does (rms_norm_fwd with a weight of 1 / sqrt(K) gives unit length);
+ * the step is a contraction where exp(g) <= 1 and 0 <= beta |k|^2 <= 2.
+ *
+ * q, k, v and out share one element type; g and beta are of that type or fp32
+ * (gate_dtype); states, checkpoints and their gradients are fp32.  All sums
+ * are fp32.  bf16 inputs: values computed in fp32 enter the matrix products as
+ * the sum of two bf16 parts (16 bits of them), fp32 inputs as they are.
+ * A g below -200 counts as -200, whose exponential is zero (-inf closes the
+ * state).  An infinite or NaN input makes the rest of its sequence, and the
+ * chunk of 64 tokens (fp32: 32) that it lies in, NaN or infinite for all value
+ * heads that read it (an infinite v: for its column).
+ *
+ * Tensors are [total_T, heads, channels] at strides (t, h) >= 0, channels
+ * contiguous (g, beta: [total_T, value_heads]); q and k load fastest where
+ * rows start and end on 16 bytes.  Packing, state slots, PAD and
+ * has_initial_state are those of causal_conv1d_varlen_fwd.
+ *
+ * gated_delta_rule_checkpoint_rows -- rows of the checkpoint buffer that a
+ * forward call leaves for its backward call:
+ *     *rows = ceil(total_T / C) + batch,   C = 64 (bf16), 32 (fp32)
+ * The buffer is fp32 [rows, value_heads, K, V], dense; row start_b / C + b + i
+ * holds sequence b's states before its token C i.  Rows that no sequence has
+ * are not written.  Host only.
+ */
+int gated_delta_rule_checkpoint_rows(int64_t total_T, int32_t batch, int32_t dtype, int64_t* rows);
+
+/* Floats of workspace that a forward and a backward call over these sizes need.  Host only. */
+int gated_delta_rule_workspace(int64_t total_T, int32_t batch, int32_t value_heads, int32_t K,
+                               int32_t V, int32_t dtype, int64_t* fwd_floats, int64_t* bwd_floats);
+
+/*
+ * gated_delta_rule_varlen_fwd -- the rule over packed sequences.
+ *
+ *   q, k     [total_T, key_heads, K], 1 <= K <= 128;  v, out [total_T,
+ *            value_heads, V]; out may be v itself
+ *   g, beta  [total_T, value_heads], of gate_dtype
+ *   states   fp32 [num_slots, value_heads, K, V], dense but for the slot
+ *            stride (read where has_initial_state, then written with the state
+ *            after the sequence's last token); NULL: every sequence starts at
+ *            zero and its last state is dropped
+ *   query_start_loc, cache_indices, has_initial_state, pad_slot_id: as
+ *            causal_conv1d_varlen_fwd (a sequence of no tokens leaves its
+ *            initial state, or zeros, in its slot)
+ *   checkpoints  fp32, for the backward call, or NULL
+ *   workspace  fp32 at 16 bytes, gated_delta_rule_workspace's fwd_floats, the
+ *            call's own until it has finished
+ *
+ * Rows of out outside every sequence, or in a skipped one, are not written.
+ *
+ * Device-data contract: offsets non-decreasing within [0, total_T]; non-PAD
+ * slots distinct and in [0, num_slots).
+ *
+ * Host errors (SCONV_ERR_INVALID): negative sizes or strides, a scale that is
+ * not finite, NULL required pointer, unknown types, value heads that key heads
+ * do not divide, has_initial_state without states, too few slots, checkpoint
+ * rows or workspace floats, overlapping buffers.  SCONV_ERR_UNSUPPORTED: K
+ * above 128, more than 65535 heads or sequences, total_T above 2^31 - 4097, a
+ * grid beyond one launch.  batch, value_heads or V of 0 is a successful no-op.
+ */
+int gated_delta_rule_varlen_fwd(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k, int64_t k_stride_t,
+    int64_t k_stride_h, const void* v, int64_t v_stride_t, int64_t v_stride_h, const void* g,
+    int64_t g_stride_t, int64_t g_stride_h, const void* beta, int64_t b_stride_t,
+    int64_t b_stride_h, float scale, float* states, int64_t num_slots, int64_t st_stride_slot,
+    const int32_t* query_start_loc, int32_t batch, const int32_t* cache_indices,
+    const uint8_t* has_initial_state, void* out, int64_t out_stride_t, int64_t out_stride_h,
+    float* checkpoints, int64_t checkpoint_rows, float* workspace, int64_t workspace_floats,
+    int64_t total_T, int32_t key_heads, int32_t value_heads, int32_t K, int32_t V, int32_t dtype,
+    int32_t gate_dtype, int32_t pad_slot_id, hipStream_t stream);
+
+/*
+ * gated_delta_rule_varlen_bwd -- its gradients.  With dS the gradient of a
+ * state (the last one's is dfinal_states), token by token from the end:
+ *     dS += scale q dout^T,  dq = scale S dout,   du = dS^T k,  e = v - S'^T k
+ *     dbeta = du.e,  dv = beta du,   dk = beta dS e - S' dv
+ *     dS -= k dv^T,  dg = <dS, S'>,  dS = exp(g) dS
+ * dq and dk are summed over the value heads of a key head.
+ *
+ *   dout     [total_T, value_heads, V]; the inputs and checkpoints as the
+ *            forward call had and left them
+ *   dfinal_states  fp32 [num_slots, value_heads, K, V] gradient of each
+ *            sequence's last state, by its slot, or NULL (zeros)
+ *   dinitial_states  the same shape, written with the gradient of each
+ *            sequence's initial state (zero without has_initial_state), or
+ *            NULL; may be dfinal_states itself
+ *   dq, dk [total_T, key_heads, K], dv [total_T, value_heads, V] of the
+ *            inputs' type, dg, dbeta [total_T, value_heads] of gate_dtype,
+ *            which overlap nothing (columns of one wider matrix are fine);
+ *            written inside the sequences that are not skipped
+ *   workspace  fp32 at 16 bytes, gated_delta_rule_workspace's bwd_floats
+ *
+ * Sums have a fixed order: equal inputs give equal bits.  Errors as the
+ * forward's.
+ */
+int gated_delta_rule_varlen_bwd(
+    const void* dout, int64_t do_stride_t, int64_t do_stride_h, const void* q, int64_t q_stride_t,
+    int64_t q_stride_h, const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v,
+    int64_t v_stride_t, int64_t v_stride_h, const void* g, int64_t g_stride_t, int64_t g_stride_h,
+    const void* beta, int64_t b_stride_t, int64_t b_stride_h, float scale,
+    const float* checkpoints, int64_t checkpoint_rows, const int32_t* query_start_loc,
+    int32_t batch, const int32_t* cache_indices, const uint8_t* has_initial_state,
+    int64_t num_slots, const float* dfinal_states, int64_t df_stride_slot, float* dinitial_states,
+    int64_t di_stride_slot, void* dq, int64_t dq_stride_t, int64_t dq_stride_h, void* dk,
+    int64_t dk_stride_t, int64_t dk_stride_h, void* dv, int64_t dv_stride_t, int64_t dv_stride_h,
+    void* dg, int64_t dg_stride_t, int64_t dg_stride_h, void* dbeta, int64_t db_stride_t,
+    int64_t db_stride_h, float* workspace, int64_t workspace_floats, int64_t total_T,
+    int32_t key_heads, int32_t value_heads, int32_t K, int32_t V, int32_t dtype,
+    int32_t gate_dtype, int32_t pad_slot_id, hipStream_t stream);
+
+/*
+ * gated_delta_rule_update -- one decode token per row against the state pool:
+ * q, k [batch, key_heads, K], v, out [batch, value_heads, V], g, beta [batch,
+ * value_heads] (out may be v itself); states fp32 [num_slots, value_heads, K,
+ * V] (read and written); state_indices int32 [batch] (NULL: the row's own
+ * number), a row whose slot equals pad_slot_id is skipped.
+ *
+ * Device-data contract: slots of non-PAD rows distinct and in [0, num_slots).
+ *
+ * Host errors as gated_delta_rule_varlen_fwd.
+ */
+int gated_delta_rule_update(
+    const void* q, int64_t q_stride_b, int64_t q_stride_h, const void* k, int64_t k_stride_b,
+    int64_t k_stride_h, const void* v, int64_t v_stride_b, int64_t v_stride_h, const void* g,
+    int64_t g_stride_b, int64_t g_stride_h, const void* beta, int64_t b_stride_b,
+    int64_t b_stride_h, float scale, float* states, int64_t num_slots, int64_t st_stride_slot,
+    const int32_t* state_indices, void* out, int64_t out_stride_b, int64_t out_stride_h,
+    int32_t batch, int32_t key_heads, int32_t value_heads, int32_t K, int32_t V, int32_t dtype,
+    int32_t gate_dtype, int32_t pad_slot_id, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
