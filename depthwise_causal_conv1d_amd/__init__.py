@@ -24,6 +24,8 @@ from .ops import (
     gated_linear_recurrence_varlen_fwd,
     gather_intermediate_conv_window,
     gather_intermediate_ssm_state,
+    layer_norm_bwd,
+    layer_norm_fwd,
     rms_norm_bwd,
     rms_norm_fwd,
     rms_norm_quant,
@@ -33,6 +35,7 @@ from .ops import (
     sconv_fused_insert_conv_streams,
     sconv_fused_plan,
     sconv_init,
+    sconv_paged_metadata,
     sconv_seq_metadata,
 )
 
@@ -53,6 +56,8 @@ __all__ = [
     "gated_linear_recurrence_varlen_fwd",
     "gather_intermediate_conv_window",
     "gather_intermediate_ssm_state",
+    "layer_norm_bwd",
+    "layer_norm_fwd",
     "rms_norm_bwd",
     "rms_norm_fwd",
     "rms_norm_quant",
@@ -62,5 +67,6 @@ __all__ = [
     "sconv_fused_insert_conv_streams",
     "sconv_fused_plan",
     "sconv_init",
+    "sconv_paged_metadata",
     "sconv_seq_metadata",
 ]

@@ -49,6 +49,10 @@ EXPORTS = (
     "gated_delta_rule_varlen_fwd",
     "gated_delta_rule_varlen_bwd",
     "gated_delta_rule_update",
+    "layer_norm_fwd",
+    "layer_norm_bwd_workspace",
+    "layer_norm_bwd",
+    "sconv_paged_metadata",
 )
 
 P = ctypes.c_void_p
@@ -135,6 +139,10 @@ _SIGS = {
                                     I32, I32, P],
     "gated_delta_rule_update": [*[P, I64, I64] * 5, FLT, P, I64, I64, P, P, I64, I64, I32, I32, I32,
                                 I32, I32, I32, I32, I32, P],
+    "layer_norm_fwd": [P, I64, P, I64, P, P, FLT, P, I64, P, I64, I64, I32, I32, P],
+    "layer_norm_bwd_workspace": [I64, I32, PI64],
+    "layer_norm_bwd": [P, I64, P, I64, P, FLT, P, I64, P, I64, P, P, P, I64, I64, I32, I32, P],
+    "sconv_paged_metadata": [P, P, I32, P, I64, P, I64, I32, I32, P, I64, P, P, P, P, P, P],
 }
 
 

@@ -6,14 +6,10 @@
 //   8 bits: scale = max |out| over a group / 448, code = e4m3(out / scale)
 #include "column_sum.h"
 #include "lane_tokens.h"
-#include "plane_host.h"
-
-#include <initializer_list>
-#include <type_traits>
+#include "norm_rows.h"
 
 namespace sconv {
 
-constexpr int kNormThreads = 256;
 constexpr float kFp8Max = 448.f;               // largest e4m3 value
 constexpr float kFp8MinScale = 1.17549435e-38f;  // keeps a row of zeros finite
 
@@ -26,42 +22,9 @@ struct NormParams {
   float eps;
 };
 
-// v combined over groups of N consecutive lanes (a power of two); every lane
-// gets the result.  Up to 16 lanes by DPP moves inside a row.
-template <int N, typename T, typename F>
-__device__ __forceinline__ T lanes_reduce(T v, F&& f) {
-  auto step = [&](auto ctrl) {
-    constexpr int C = decltype(ctrl)::value;
-    const int m = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), C, 0xF, 0xF, true);
-    v = f(v, __builtin_bit_cast(T, m));
-  };
-  if constexpr (N >= 2) step(std::integral_constant<int, 0xB1>());   // lanes 1 0 3 2
-  if constexpr (N >= 4) step(std::integral_constant<int, 0x4E>());   // lanes 2 3 0 1
-  if constexpr (N >= 8) step(std::integral_constant<int, 0x141>());  // half rows mirrored
-  if constexpr (N >= 16) step(std::integral_constant<int, 0x140>()); // rows mirrored
-  if constexpr (N >= 32) v = f(v, __shfl_xor(v, 16, 64));
-  if constexpr (N >= 64) v = f(v, __shfl_xor(v, 32, 64));
-  return v;
-}
-
-struct Add {
-  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
 struct Max {
   __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
 };
-
-// Sum over the workgroup; every thread gets it.
-__device__ __forceinline__ float block_sum(float v, float* lds) {
-  v = lanes_reduce<64>(v, Add());
-  const int wave = threadIdx.x >> 6, n = blockDim.x >> 6;
-  if ((threadIdx.x & 63) == 0) lds[wave] = v;
-  __syncthreads();
-  float t = 0.f;
-  for (int i = 0; i < n; ++i) t += lds[i];
-  __syncthreads();
-  return t;
-}
 
 // |v| as bits: the order of the bits is that of the values, and a NaN is
 // above every number, so that a NaN reaches the scale.
@@ -432,22 +395,6 @@ __global__ __launch_bounds__(kSumCols * kSumGroups) void norm_dweight_kernel(con
   column_sum(partial, n, dim, [&](int64_t c, float v) { dweight[c] = v; });
 }
 
-// How many vectors of a row T threads hold: the smallest instance that
-// covers dim, 0 if none does.
-static int norm_vectors(int32_t dim, int V, int T) {
-  const int64_t need = cdiv(dim, (int64_t)V * T);
-  if (V > 1) return need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : 0;
-  return need <= 4 ? 4 : need <= 16 ? 16 : need <= 32 ? 32 : 0;
-}
-
-// Threads of a row: a wave where it holds the row in two vectors a lane (16
-// single elements), which spares the barriers; else four waves, however many
-// the rows: with a wave for rows of four and eight vectors, 17408 x 4096 bf16 to
-// 8 bits takes 102 us (four waves 90), 4096 x 4096 30 (24), 17408 x 2048 fp32 97 (83).
-static int norm_threads(int32_t dim, int V) {
-  return cdiv(dim, (int64_t)V * 64) <= (V > 1 ? 2 : 16) ? 64 : 256;
-}
-
 // group: channels that share a scale, 0 for the row.
 template <typename D, int V, int NV, int T>
 static void launch_norm_fwd(bool quant, int group, const NormParams& p, hipStream_t s) {
@@ -510,14 +457,6 @@ static void launch_norm_bwd_n(int nv, int T, const NormBwdParams& p, uint32_t gr
       else hipLaunchKernelGGL((norm_bwd_kernel<D, 1, 32, 256>), g, th, 0, s, p);
     }
   }
-}
-
-// Every row starts on a multiple of V elements, and holds whole vectors.
-static bool norm_vec(std::initializer_list<Plane> planes, int64_t V) {
-  for (const Plane& a : planes)
-    if (!a.empty() && (a.nc % V != 0 || (a.nt > 1 && a.st % V != 0) || !aligned_to(a.p, V * a.es)))
-      return false;
-  return true;
 }
 
 // Workgroups of the backward pass, and rows of its workspace: four rows each at

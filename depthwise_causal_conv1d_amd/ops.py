@@ -1087,3 +1087,102 @@ def gated_delta_rule_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
     _call("gated_delta_rule_update", v, *args, _delta_scale(scale, sizes[2]), *pool,
           _ptr(state_indices), *_heads(v.shape, "out", out), batch, *sizes, int(pad_slot_id))
     return out
+
+
+# ---------------------------------------------------------------- layer norm
+
+def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                   eps: float = 1e-5, residual: Optional[torch.Tensor] = None,
+                   residual_out: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """(s - mean(s)) / sqrt(var(s) + eps) * weight + bias over rows, s = x +
+    residual.
+
+    x, residual [rows, dim], weight, bias [dim].  The sum goes to
+    ``residual_out``, or back to residual if that is None (in place, as a
+    layer's stream does).
+    """
+    if x.dim() != 2 or weight.dim() != 1:
+        raise ValueError("x [rows, dim], weight, bias [dim]")
+    rows, dim = x.shape
+    if out is None:
+        out = torch.empty_like(x)
+    if residual is not None and residual_out is None:
+        residual_out = residual
+    _one_device(x, weight, bias, residual, residual_out, out)
+    dt = _same_type(x, "x, weight, bias, residual, residual_out and out", weight, bias, residual,
+                    residual_out, out)
+    _dense(weight, x.dtype, "weight", dim)
+    if bias is not None:
+        _dense(bias, x.dtype, "bias", dim)
+    a = _rows(x.shape, x, residual, residual_out, out)
+    _call("layer_norm_fwd", x, *a[:4], weight.data_ptr(), _ptr(bias), eps, *a[4:], rows, dim, dt)
+    return out
+
+
+def layer_norm_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                   dresidual: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None):
+    """Gradients of layer_norm_fwd at the rows x that it normalised (its
+    residual_out, or its x): (dx, dweight float32 [dim], dbias float32 [dim]).
+    ``dresidual``, the gradient that reaches residual_out from elsewhere, is
+    added to dx, which is then the gradient of x and of residual."""
+    if x.dim() != 2 or weight.dim() != 1:
+        raise ValueError("dout, x [rows, dim], weight [dim]")
+    rows, dim = x.shape
+    dx = torch.empty_like(x) if dx is None else dx
+    _one_device(x, dout, weight, dresidual, dx)
+    dt = _same_type(x, "dout, x, weight, dresidual and dx", dout, weight, dresidual, dx)
+    _dense(weight, x.dtype, "weight", dim)
+    a = _rows(x.shape, dout, x, dresidual, dx)
+    n = _floats("layer_norm_bwd_workspace", rows, dim)
+    dweight, dbias = (torch.empty(dim, dtype=torch.float32, device=x.device) for _ in range(2))
+    ws = torch.empty(n, dtype=torch.float32, device=x.device)
+    _call("layer_norm_bwd", x, *a[:4], weight.data_ptr(), eps, *a[4:], dweight.data_ptr(),
+          dbias.data_ptr(), ws.data_ptr(), n, rows, dim, dt)
+    return dx, dweight, dbias
+
+
+# ---------------------------------------------------------------- a step's paged metadata
+
+def sconv_paged_metadata(query_lens: torch.Tensor, context_lens: torch.Tensor,
+                         free_blocks: torch.Tensor, block_table: torch.Tensor, block_size: int,
+                         query_start_loc: torch.Tensor, seq_idx_out: Optional[torch.Tensor],
+                         query_start_out: Optional[torch.Tensor], positions_out: torch.Tensor,
+                         slot_mapping_out: torch.Tensor,
+                         blocks_used: Optional[torch.Tensor] = None) -> None:
+    """Fill a step's static metadata buffers from its requests' lengths.
+
+    query_lens, context_lens int32 [num_reqs]: tokens of this step, and tokens
+    before it.  Blocks that a request's row of block_table (int32 [num_reqs,
+    max_blocks], updated in place) lacks come from free_blocks (int32), in the
+    order of the requests; blocks_used int32 [1] says how many they need.
+    query_start_loc int32 [num_reqs + 1], seq_idx_out, query_start_out int32
+    and positions_out, slot_mapping_out int64, all of one length (the padded
+    token count), are written; seq_idx_out and query_start_out may be None.
+    Rows behind the last token have slot -1 and zeros elsewhere; where
+    free_blocks or a table's row ends, slots are -1."""
+    _one_device(query_lens, context_lens, free_blocks, block_table, query_start_loc, seq_idx_out,
+                query_start_out, positions_out, slot_mapping_out, blocks_used)
+    reqs, padded = query_lens.numel(), slot_mapping_out.numel()
+    _dense(query_lens, torch.int32, "query_lens")
+    _dense(context_lens, torch.int32, "context_lens", reqs)
+    _dense(free_blocks, torch.int32, "free_blocks")
+    _dense(query_start_loc, torch.int32, "query_start_loc", reqs + 1)
+    _dense(positions_out, torch.int64, "positions_out", padded)
+    _dense(slot_mapping_out, torch.int64, "slot_mapping_out", padded)
+    for t, name, n in ((seq_idx_out, "seq_idx_out", padded),
+                       (query_start_out, "query_start_out", padded),
+                       (blocks_used, "blocks_used", 1)):
+        if t is not None:
+            _dense(t, torch.int32, name, n)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise TypeError("block_table must be int32 [num_reqs, max_blocks]")
+    max_blocks = block_table.shape[1]
+    if max_blocks > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table needs contiguous entries within a row")
+    _table_rows(block_table, reqs)
+    _call("sconv_paged_metadata", slot_mapping_out, query_lens.data_ptr(), context_lens.data_ptr(),
+          reqs, free_blocks.data_ptr(), free_blocks.numel(), block_table.data_ptr(),
+          block_table.stride(0), max_blocks, int(block_size), query_start_loc.data_ptr(), padded,
+          _ptr(seq_idx_out), _ptr(query_start_out), positions_out.data_ptr(),
+          slot_mapping_out.data_ptr(), _ptr(blocks_used))

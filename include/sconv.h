@@ -927,6 +927,104 @@ int gated_delta_rule_update(
     int32_t batch, int32_t key_heads, int32_t value_heads, int32_t K, int32_t V, int32_t dtype,
     int32_t gate_dtype, int32_t pad_slot_id, hipStream_t stream);
 
+/*
+ * layer_norm_fwd -- layer norm of rows, with the residual's addition:
+ *     s = x + residual (s = x without one; fp32, not rounded)
+ *     out = (s - mean(s)) / sqrt(mean((s - mean(s))^2) + eps) * weight + bias
+ *
+ *   x, residual, residual_out, out  [rows, dim] rows of their strides,
+ *            channels contiguous; weight, bias [dim] (bias may be NULL: zeros);
+ *            all of one dtype.  residual may be NULL; residual_out (needs
+ *            residual; NULL: not kept) receives s rounded to dtype, and may be
+ *            residual or x itself; so may out
+ *
+ * The variance is summed over differences from the mean.  A row is read once
+ * up to 16384 bf16 or 8192 fp32 channels where rows start and end on 16 bytes,
+ * up to 8192 elsewhere; wider rows are read three times.
+ *
+ * Host errors (SCONV_ERR_INVALID): negative sizes, eps negative or not
+ * finite, NULL required pointer, unknown dtype, partially overlapping buffers.
+ * SCONV_ERR_UNSUPPORTED: rows beyond one launch.  rows == 0 or dim == 0 is a
+ * successful no-op.
+ */
+int layer_norm_fwd(const void* x, int64_t x_stride_r, const void* residual,
+                   int64_t residual_stride_r, const void* weight, const void* bias, float eps,
+                   void* residual_out, int64_t residual_out_stride_r, void* out,
+                   int64_t out_stride_r, int64_t rows, int32_t dim, int32_t dtype,
+                   hipStream_t stream);
+
+/* Floats of workspace that layer_norm_bwd needs.  Host only. */
+int layer_norm_bwd_workspace(int64_t rows, int32_t dim, int64_t* floats);
+
+/*
+ * layer_norm_bwd -- gradients of layer_norm_fwd at the rows x it normalised
+ * (the forward's residual_out, or its x without a residual).  With n the
+ * normalised rows and rstd their factor:
+ *     dx = rstd (weight dout - mean(weight dout) - n mean(weight dout n)) + dresidual
+ *     dweight = sum over rows of dout n,   dbias = sum over rows of dout
+ *   dresidual [rows, dim] or NULL: the gradient that reaches residual_out
+ *            from elsewhere; dx is then the gradient of x and of residual
+ *   dx       may be dout, x or dresidual itself
+ *   dweight  fp32 [dim], dbias fp32 [dim] or NULL (written)
+ *   workspace  fp32, layer_norm_bwd_workspace floats, the call's own until it
+ *            has finished
+ * The sums have a fixed order: equal inputs give equal bits.  Errors as
+ * layer_norm_fwd's, and too small a workspace; SCONV_ERR_UNSUPPORTED: dim
+ * above 2^28.  dim == 0 is a no-op; rows == 0 writes zeros to dweight and dbias.
+ */
+int layer_norm_bwd(const void* dout, int64_t dout_stride_r, const void* x, int64_t x_stride_r,
+                   const void* weight, float eps, const void* dresidual,
+                   int64_t dresidual_stride_r, void* dx, int64_t dx_stride_r, float* dweight,
+                   float* dbias, float* workspace, int64_t workspace_floats, int64_t rows,
+                   int32_t dim, int32_t dtype, hipStream_t stream);
+
+/*
+ * sconv_paged_metadata -- block tables, slots and per-token metadata of a
+ * step, from its requests' lengths: what the fused insert + conv takes.
+ *
+ * Request r brings query_lens[r] tokens after context_lens[r] earlier ones
+ * (negative counts as zero).  Its table has ceil(context / block_size) blocks;
+ * the ceil((context + query) / block_size) that it needs are filled up from
+ * free_blocks, in the order of the requests:
+ *     block_table[r, have .. need - 1] = the next need - have of free_blocks
+ * Rows are the requests' tokens in order; for row t of request r:
+ *     seq_idx_out[t] = r,  query_start_out[t] = query_start_loc[r]
+ *     positions_out[t] = context_lens[r] + t - query_start_loc[r]
+ *     slot_mapping_out[t] = block_table[r, position / block_size] * block_size
+ *                           + position % block_size
+ * query_start_loc [num_reqs + 1] holds the running sum of the lengths,
+ * blocks_used[0] the blocks that the requests need from free_blocks.  Rows
+ * behind the last request up to num_padded_tokens have slot -1 and zeros
+ * elsewhere; rows beyond num_padded_tokens are not written.
+ *
+ * Where free_blocks ends (blocks_used > num_free), the entries are -1 and the
+ * tokens' slots -1; so are the slots of tokens behind max_blocks blocks (for
+ * which nothing is written to the table) and of tokens whose entry is negative.
+ * The other entries of the table stay as they are.
+ *
+ *   query_lens, context_lens  int32 [num_reqs];  free_blocks  int32 [num_free]
+ *   block_table  int32 [num_reqs, max_blocks] row stride bt_row_stride
+ *            (read and written)
+ *   seq_idx_out, query_start_out  int32 [num_padded_tokens], each may be NULL;
+ *   positions_out, slot_mapping_out  int64 [num_padded_tokens]
+ *   blocks_used  int32 [1] or NULL
+ *
+ * Device-data contract: the sum of the lengths, and each request's context +
+ * query, stay below 2^31.
+ *
+ * One launch up to 4096 requests, two beyond.
+ *
+ * Host errors (SCONV_ERR_INVALID): negative sizes, block_size < 1, table rows
+ * that overlap, NULL required pointer, an output that overlaps another buffer.
+ * SCONV_ERR_UNSUPPORTED: tokens beyond one launch (2^32).
+ */
+int sconv_paged_metadata(const int32_t* query_lens, const int32_t* context_lens, int32_t num_reqs,
+                         const int32_t* free_blocks, int64_t num_free, int32_t* block_table,
+                         int64_t bt_row_stride, int32_t max_blocks, int32_t block_size,
+                         int32_t* query_start_loc, int64_t num_padded_tokens, int32_t* seq_idx_out,
+                         int32_t* query_start_out, int64_t* positions_out,
+                         int64_t* slot_mapping_out, int32_t* blocks_used, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
