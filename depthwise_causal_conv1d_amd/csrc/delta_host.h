@@ -67,7 +67,9 @@ inline DeltaBuffer delta_tensor(const void* p, int64_t st, int64_t sh, int64_t t
                                 int64_t heads, int64_t width, int64_t es) {
   if (!tokens || !heads || !width) return delta_block(p, 0);
   const int64_t row = (heads - 1) * sh + width, all = (tokens - 1) * st + row;
+  const int64_t head = (tokens - 1) * st + width;
   if (tokens > 1 && st >= row) return {p, all * es, row * es, st * es};
+  if (heads > 1 && sh >= head) return {p, all * es, head * es, sh * es};
   return delta_block(p, all * es);
 }
 

@@ -540,7 +540,11 @@ __global__ __launch_bounds__(4 * KP, KP == 128 ? 2 : 1) void delta_grad_kernel(D
         if (lane + d < 64) after += y2;
       }
       if (t < ch.len) {
-        const float dg = (float)(after + (before - km) + (double)lv[C - 1] * all), db = sv - sz;
+        float dg = (float)(after + (before - km) + (double)lv[C - 1] * all);
+        const float db = sv - sz;
+        // behind a closed gate the parts cancel but for their roundings
+        const float gt = lv[3 * C + t] + lv[4 * C + t] - (t ? lv[3 * C + t - 1] + lv[4 * C + t - 1] : 0.f);
+        if (gt < -104.f) dg = 0.f;  // e^g is zero in fp32
         const int64_t tok = ch.t0 + t;
         if (p.gates_f32) {
           static_cast<float*>(a.dg)[tok * a.dg_t + h * a.dg_h] = dg;
