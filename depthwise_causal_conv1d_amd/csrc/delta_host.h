@@ -82,6 +82,11 @@ inline bool delta_overlap(const DeltaBuffer& a, const DeltaBuffer& b) {
   return d < a.run || a.step - d < b.run;
 }
 
+// Rows of whole 16-byte vectors of n elements.
+inline bool delta_vec(const void* t, int64_t st, int64_t sh, int64_t width, int64_t n) {
+  return aligned16(t) && st % n == 0 && sh % n == 0 && width % n == 0;
+}
+
 inline int delta_inputs(const DeltaCall& c, DeltaParams& p, const void* q, int64_t q_t, int64_t q_h,
                         const void* k, int64_t k_t, int64_t k_h, const void* v, int64_t v_t,
                         int64_t v_h, const void* g, int64_t g_t, int64_t g_h, const void* beta,
@@ -100,10 +105,8 @@ inline int delta_inputs(const DeltaCall& c, DeltaParams& p, const void* q, int64
   p.gates_f32 = c.gate_dtype == SCONV_F32;
   // rows that start and end on 16 bytes load as vectors
   const int64_t n = 16 / elem_size(c.dtype);
-  auto vec = [&](const void* t, int64_t st, int64_t sh) {
-    return aligned16(t) && st % n == 0 && sh % n == 0 && c.K % n == 0;
-  };
-  p.q_vec = vec(q, q_t, q_h), p.k_vec = vec(k, k_t, k_h);
+  p.qk_vec = delta_vec(q, q_t, q_h, c.K, n) && delta_vec(k, k_t, k_h, c.K, n);
+  p.v_vec = delta_vec(v, v_t, v_h, c.V, n);
   return SCONV_OK;
 }
 

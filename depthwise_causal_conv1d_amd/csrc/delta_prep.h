@@ -10,6 +10,8 @@
 // floats: e_ij is the exponential of a difference of sums.
 #pragma once
 
+#include <type_traits>
+
 #include "delta_rule.h"
 
 namespace sconv {
@@ -136,19 +138,24 @@ __global__ __launch_bounds__(64) void delta_prep_kernel(DeltaParams p) {
   const S* q = static_cast<const S*>(p.q) + (int64_t)c.t0 * p.q_t + kh * p.q_h;
   const S* k = static_cast<const S*>(p.k) + (int64_t)c.t0 * p.k_t + kh * p.k_h;
   typename T::Exact kf[NT][KS], qf[NT][KS];
+  auto load = [&](auto v) {
 #pragma unroll
-  for (int I = 0; I < NT; ++I) {
-    const int t = 16 * I + r;
+    for (int I = 0; I < NT; ++I)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        kf[I][s] = load8<D, decltype(v)::value>(k, p.k_t, 16 * I + r, c.len, 32 * s + 8 * g, p.K);
+        qf[I][s] = load8<D, decltype(v)::value>(q, p.q_t, 16 * I + r, c.len, 32 * s + 8 * g, p.K);
+      }
+  };
+  if (p.qk_vec) load(std::true_type()); else load(std::false_type());
+#pragma unroll
+  for (int I = 0; I < NT; ++I)
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      const int k0 = 32 * s + 8 * g;
-      kf[I][s] = zero8<D>(), qf[I][s] = zero8<D>();
-      if (t < c.len) {
-        kf[I][s] = row8<D>(k + (int64_t)t * p.k_t, k0, p.K, p.k_vec);
-        qf[I][s] = row8<D>(q + (int64_t)t * p.q_t, k0, p.K, p.q_vec);
-      }
+      const int n = 16 * I + r < c.len ? p.K - (32 * s + 8 * g) : 0;
+      kf[I][s] = mask8<D>(kf[I][s], n);
+      qf[I][s] = mask8<D>(qf[I][s], n);
     }
-  }
   // A into LDS
 #pragma unroll
   for (int I = 0; I < NT; ++I)

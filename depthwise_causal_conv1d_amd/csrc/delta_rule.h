@@ -55,7 +55,7 @@ struct DeltaParams {
   const uint8_t* has;
   int32_t batch, pad, heads, group, K, V;  // heads: value heads; group: of one key head
   float scale;
-  int32_t gates_f32, q_vec, k_vec;
+  int32_t gates_f32, qk_vec, v_vec;
   // operands of every chunk: frags (2 KB each), then vectors
   char* frags;
   float* vectors;
@@ -162,7 +162,15 @@ template <> struct Tile<Bf16> {
     c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.hi, b.lo, c, 0, 0, 0);
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.hi, b.hi, c, 0, 0, 0);
   }
-  static __device__ __forceinline__ float value(const Exact& a, int e) { return (float)a.v[e]; }
+  // by whole words: entries taken from the bf16 vector itself under a condition
+  // have all come out as the first one
+  static __device__ __forceinline__ float value(const Exact& a, int e) {
+    const uint32_t w = __builtin_bit_cast(u32x4, a.v)[e / 2];
+    return __uint_as_float(e % 2 ? w & 0xFFFF0000u : w << 16);
+  }
+  static __device__ __forceinline__ uint16_t raw(const Exact& a, int e) {
+    return (uint16_t)(__builtin_bit_cast(u32x4, a.v)[e / 2] >> (16 * (e % 2)));
+  }
   static __device__ __forceinline__ Exact join(const uint16_t (&a)[8]) {
     struct W { uint16_t e[8]; } w;
 #pragma unroll
@@ -198,6 +206,7 @@ template <> struct Tile<F32> {
   static __device__ __forceinline__ float value(const Exact& a, int e) {
     return e < 4 ? a.a[e] : a.b[e - 4];
   }
+  static __device__ __forceinline__ float raw(const Exact& a, int e) { return value(a, e); }
   static __device__ __forceinline__ Exact join(const float (&a)[8]) {
     return {{a[0], a[1], a[2], a[3]}, {a[4], a[5], a[6], a[7]}};
   }
@@ -211,35 +220,61 @@ template <> struct Tile<F32> {
   }
 };
 
-// 8 consecutive entries of a row from k0 on, zeros from K on; vec: rows of 16-byte vectors.
-template <typename D>
-__device__ __forceinline__ typename Tile<D>::Exact row8(const typename D::storage* row, int k0,
-                                                        int K, bool vec) {
-  using T = Tile<D>;
-  if (vec) {
-    if constexpr (sizeof(typename D::storage) == 2) {
-      u32x4 w = {0, 0, 0, 0};
-      if (k0 < K) w = *reinterpret_cast<const u32x4*>(row + k0);
-      return {__builtin_bit_cast(bf16x8, w)};
-    } else {
-      f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-      if (k0 < K) a = *reinterpret_cast<const f32x4*>(row + k0);
-      if (k0 + 4 < K) b = *reinterpret_cast<const f32x4*>(row + k0 + 4);
-      return {a, b};
-    }
-  }
-  typename D::storage w[8];
+// 8 consecutive entries of row t from c0 on; VEC: rows of 16-byte vectors.
+// Every lane loads from some place inside rows 0 .. T - 1 (T > 0) and columns
+// 0 .. W - 1, and drops by mask8 what it should not see when it uses it: a load
+// under a condition, or a select behind it, waits for the data there (a chunk
+// of the walk took 14 and 10 us so).
+template <typename D, bool VEC>
+__device__ __forceinline__ typename Tile<D>::Exact load8(const typename D::storage* m, int64_t ld, int t,
+                                                         int T, int c0, int W) {
+  const typename D::storage* row = m + (t < T ? t : T - 1) * ld;
+  if constexpr (VEC) {
+    const typename D::storage* at = row + (c0 < W ? c0 : 0);
+    if constexpr (sizeof(typename D::storage) == 2)
+      return {__builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(at))};
+    else
+      return {*reinterpret_cast<const f32x4*>(at),
+              *reinterpret_cast<const f32x4*>(row + (c0 + 4 < W ? c0 + 4 : 0))};
+  } else {
+    typename D::storage w[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = k0 + e < K ? row[k0 + e] : (typename D::storage)0;
-  return T::join(w);
+    for (int e = 0; e < 8; ++e) w[e] = row[c0 + e < W ? c0 + e : W - 1];
+    return Tile<D>::join(w);
+  }
 }
 
+// The first n entries, zeros behind them.
 template <typename D>
-__device__ __forceinline__ typename Tile<D>::Exact zero8() {
-  if constexpr (sizeof(typename D::storage) == 2)
-    return {__builtin_bit_cast(bf16x8, (u32x4){0, 0, 0, 0})};
-  else
-    return {{0, 0, 0, 0}, {0, 0, 0, 0}};
+__device__ __forceinline__ typename Tile<D>::Exact mask8(typename Tile<D>::Exact x, int n) {
+  if constexpr (sizeof(typename D::storage) == 2) {
+    u32x4 w = __builtin_bit_cast(u32x4, x.v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = n > 2 * e + 1 ? w[e] : n > 2 * e ? w[e] & 0xFFFFu : 0u;
+    return {__builtin_bit_cast(bf16x8, w)};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x.a[e] = n > e ? x.a[e] : 0.f, x.b[e] = n > e + 4 ? x.b[e] : 0.f;
+    return x;
+  }
+}
+
+// 8 entries to columns c0.. of a row, those before W.
+template <typename D>
+__device__ __forceinline__ void put_row8(typename D::storage* row, int c0, int W, bool vec,
+                                         const typename Tile<D>::Exact& x) {
+  if (vec) {
+    if constexpr (sizeof(typename D::storage) == 2) {
+      if (c0 < W) *reinterpret_cast<u32x4*>(row + c0) = __builtin_bit_cast(u32x4, x.v);
+    } else {
+      if (c0 < W) *reinterpret_cast<f32x4*>(row + c0) = x.a;
+      if (c0 + 4 < W) *reinterpret_cast<f32x4*>(row + c0 + 4) = x.b;
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c0 + e < W) row[c0 + e] = Tile<D>::raw(x, e);
 }
 
 // A matrix of W columns (a multiple of 32) in LDS, one row a token.  bf16 rows
@@ -266,6 +301,15 @@ template <typename D, int W> struct LdsRows {
     } else {
       *reinterpret_cast<f32x4*>(m + t * LD + c0) = x.a;
       *reinterpret_cast<f32x4*>(m + t * LD + c0 + 4) = x.b;
+    }
+  }
+  static __device__ __forceinline__ typename Tile<D>::Exact get8(const S* m, int t, int c0) {
+    const S* at = m + t * LD + pos(c0);
+    if constexpr (sizeof(S) == 2) {
+      const u32x2 x = *reinterpret_cast<const u32x2*>(at), y = *reinterpret_cast<const u32x2*>(at + 8);
+      return {__builtin_bit_cast(bf16x8, (u32x4){x[0], x[1], y[0], y[1]})};
+    } else {
+      return {*reinterpret_cast<const f32x4*>(at), *reinterpret_cast<const f32x4*>(at + 4)};
     }
   }
   // operand whose rows are tokens t0 + lane % 16, summed over columns c0 .. c0 + 31

@@ -2,6 +2,7 @@
 // one-token update, for gfx950.  The mathematics is in delta_rule.h.
 #include "delta_prep.h"
 #include "delta_host.h"
+#include "delta_walk.h"
 
 namespace sconv {
 
@@ -12,23 +13,21 @@ struct DeltaFwd {
   void* out;
   int64_t o_t, o_h;
   float* marks;
+  int32_t o_vec;
 };
 
-constexpr int kWalkWaves = 4;
-
-// One workgroup walks a sequence's chunks for one value head and 16 NC columns
-// a wave.
-template <typename D, int KP, int NC>
-__global__ __launch_bounds__(64 * kWalkWaves, 2) void delta_walk_kernel(DeltaFwd a) {
+// One workgroup walks a sequence's chunks for one value head, 16 columns a
+// wave.  An output chunk waits in LDS, in V's place, for the next one's staging.
+template <typename D, int KP, int NW>
+__global__ __launch_bounds__(64 * NW, 8 / NW) void delta_walk_kernel(DeltaFwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
   constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32;
-  constexpr int NF = kDeltaFrags<C>, THREADS = 64 * kWalkWaves;
-  using Rows = LdsRows<D, KP>;
-  __shared__ __attribute__((aligned(16))) S lk[C * Rows::LD];
-  __shared__ __attribute__((aligned(16))) S lq[C * Rows::LD];
-  __shared__ __attribute__((aligned(16))) char lf[2 * NF * kFragBytes];
-  __shared__ __attribute__((aligned(16))) float lv[3 * C];
+  constexpr int NF = kDeltaFrags<C>;
+  using Stage = WalkStage<D, KP, NW>;
+  using Rows = typename Stage::L::Rows;
+  using Cols = typename Stage::L::Cols;
+  __shared__ typename Stage::L l;
 
   const DeltaParams& p = a.p;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -36,188 +35,115 @@ __global__ __launch_bounds__(64 * kWalkWaves, 2) void delta_walk_kernel(DeltaFwd
   const int32_t slot = p.slots ? p.slots[b] : b;
   if (p.slots && slot == p.pad) return;
   const int32_t start = p.qsl[b], end = p.qsl[b + 1];
-  const int32_t col0 = (blockIdx.x * kWalkWaves + wave) * 16 * NC + r * NC;  // columns col0 + 0 .. NC - 1
+  const int32_t cols0 = blockIdx.x * 16 * NW, c16 = 16 * wave, col = cols0 + c16 + r;
   const int64_t KV = (int64_t)p.K * p.V;
 
-  f32x4 s[KT][NC];
+  f32x4 s[KT];
 #pragma unroll
-  for (int t = 0; t < KT; ++t)
-#pragma unroll
-    for (int n = 0; n < NC; ++n) s[t][n] = zero4();
+  for (int t = 0; t < KT; ++t) s[t] = zero4();
   float* state = a.states ? a.states + slot * a.st_slot + h * KV : nullptr;
-  auto each_state = [&](auto&& f) {
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int k = 16 * t + 4 * g + e;
-#pragma unroll
-        for (int n = 0; n < NC; ++n)
-          if (k < p.K && col0 + n < p.V) s[t][n][e] = f((int64_t)k * p.V + col0 + n, s[t][n][e]);
-      }
-  };
-  if (p.has && p.has[b]) each_state([&](int64_t i, float) { return state[i]; });
+  auto each = [&](auto&& f) { each_entry(s, p.K, p.V, col, cols0 + c16 + 16, f); };
+  if (p.has && p.has[b]) each([&](int64_t i, float) { return state[i]; });
 
-  // a thread's share of a chunk's K, Q, frags and vectors on its way to LDS
-  constexpr int O8 = C * KP / 8 / THREADS;                    // octets of K, and of Q
-  constexpr int F16 = 2 * NF * kFragBytes / 16 / THREADS;     // 16-byte pieces of the frags
-  typename T::Exact nk[O8], nq[O8];
-  u32x4 nf[F16];
-  float nv = 0.f;
   const S* q = static_cast<const S*>(p.q) + kh * p.q_h;
   const S* k = static_cast<const S*>(p.k) + kh * p.k_h;
-  const int32_t row0 = start / C + b;
-  auto fetch = [&](int32_t i) {
-    const int32_t t0 = start + i * C;
-    const int64_t at = (int64_t)(row0 + i) * p.heads + h;
-#pragma unroll
-    for (int o = 0; o < O8; ++o) {
-      const int x = threadIdx.x + o * THREADS, t = x / (KP / 8), k0 = x % (KP / 8) * 8;
-      nk[o] = zero8<D>(), nq[o] = zero8<D>();
-      if (t0 + t < end) {
-        nk[o] = row8<D>(k + (int64_t)(t0 + t) * p.k_t, k0, p.K, p.k_vec);
-        nq[o] = row8<D>(q + (int64_t)(t0 + t) * p.q_t, k0, p.K, p.q_vec);
-      }
-    }
-    const u32x4* f = reinterpret_cast<const u32x4*>(p.frags + at * (2 * NF) * kFragBytes);
-#pragma unroll
-    for (int o = 0; o < F16; ++o) nf[o] = f[threadIdx.x + o * THREADS];
-    if (threadIdx.x < 3 * C) nv = p.vectors[at * kDeltaVectors<C> + threadIdx.x];
-  };
-  auto stage = [&]() {
-#pragma unroll
-    for (int o = 0; o < O8; ++o) {
-      const int x = threadIdx.x + o * THREADS, t = x / (KP / 8), k0 = x % (KP / 8) * 8;
-      Rows::put8(lk, t, k0, nk[o]);
-      Rows::put8(lq, t, k0, nq[o]);
-    }
-#pragma unroll
-    for (int o = 0; o < F16; ++o) reinterpret_cast<u32x4*>(lf)[threadIdx.x + o * THREADS] = nf[o];
-    if (threadIdx.x < 3 * C) lv[threadIdx.x] = nv;
-  };
-
   const S* v = static_cast<const S*>(p.v) + h * p.v_h;
   S* out = static_cast<S*>(a.out) + h * a.o_h;
+  const int32_t row0 = start / C + b;
+  Stage next;
+  auto fetch = [&](int32_t i) {
+    const int64_t at = (int64_t)(row0 + i) * p.heads + h;
+    next.fetch(p, k, q, v, p.v_t, p.qk_vec && p.v_vec, cols0, start + i * C, end,
+               p.frags + at * (2 * NF) * kFragBytes, p.vectors + at * kDeltaVectors<C>);
+  };
+  auto put_out = [&](int32_t i) {
+    const int32_t t0 = start + i * C;
+#pragma unroll
+    for (int o = 0; o < Stage::XO; ++o) {
+      const int x = threadIdx.x + o * Stage::THREADS, t = x / (2 * NW), c0 = x % (2 * NW) * 8;
+      if (t < end - t0)
+        put_row8<D>(out + (int64_t)(t0 + t) * a.o_t, cols0 + c0, p.V, a.o_vec, Cols::get8(l.x, t, c0));
+    }
+  };
   const int32_t chunks = (end - start + C - 1) / C;
   if (chunks > 0) fetch(0);
   for (int32_t i = 0; i < chunks; ++i) {
-    const int32_t t0 = start + i * C, len = end - t0;
     __syncthreads();
-    stage();
+    if (i > 0) put_out(i - 1);
+    next.stage(l, p, cols0, end - (start + i * C));
     __syncthreads();
     if (i + 1 < chunks) fetch(i + 1);
     if (a.marks) {
       float* mark = a.marks + ((int64_t)(row0 + i) * p.heads + h) * KV;
-      each_state([&](int64_t x, float w) { return mark[x] = w; });
+      each([&](int64_t x, float w) { return mark[x] = w; });
     }
-    f32x4 u[NT][NC];  // V, then R, then U
+    f32x4 xs[NT], ys[NT];  // K S, Q S
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int x = 16 * t + 4 * g + e;
-#pragma unroll
-        for (int n = 0; n < NC; ++n)
-          u[t][n][e] = x < len && col0 + n < p.V
-                           ? to_float<D>(v[(int64_t)(t0 + x) * p.v_t + col0 + n]) : 0.f;
-      }
-    f32x4 xs[NT][NC], ys[NT][NC];  // K S, Q S
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int n = 0; n < NC; ++n) xs[t][n] = zero4(), ys[t][n] = zero4();
+    for (int t = 0; t < NT; ++t) xs[t] = zero4(), ys[t] = zero4();
 #pragma unroll
     for (int c = 0; c < KS; ++c) {
-      typename T::Split sp[NC];
-#pragma unroll
-      for (int n = 0; n < NC; ++n) sp[n] = T::split(s[2 * c][n], s[2 * c + 1][n]);
+      const auto sp = T::split(s[2 * c], s[2 * c + 1]);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const auto kf = Rows::rows(lk, 16 * t, 32 * c, lane);
-        const auto qf = Rows::rows(lq, 16 * t, 32 * c, lane);
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          xs[t][n] = T::mul(kf, sp[n], xs[t][n]);
-          ys[t][n] = T::mul(qf, sp[n], ys[t][n]);
-        }
+        xs[t] = T::mul(Rows::rows(l.k, 16 * t, 32 * c, lane), sp, xs[t]);
+        ys[t] = T::mul(Rows::rows(l.q, 16 * t, 32 * c, lane), sp, ys[t]);
       }
     }
+    f32x4 u[NT];  // R, then U
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const f32x4 gam = lds4(lv + 16 * t + 4 * g), bt = lds4(lv + 2 * C + 16 * t + 4 * g);
+    for (int c = 0; c < CS; ++c) {
+      const auto vv = Cols::cols(l.x, 32 * c, c16, lane);
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
+      for (int o = 0; o < 2; ++o) {
+        const int t = 2 * c + o;
+        const f32x4 gam = lds4(l.v + 16 * t + 4 * g), bt = lds4(l.v + 2 * C + 16 * t + 4 * g);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          u[t][n][e] = bt[e] * (u[t][n][e] - gam[e] * xs[t][n][e]);
-          ys[t][n][e] *= p.scale * gam[e];
+          u[t][e] = bt[e] * (T::value(vv, 4 * o + e) - gam[e] * xs[t][e]);
+          ys[t][e] *= p.scale * gam[e];
         }
-    }
-    {
-      typename T::Split rs[CS][NC];
-#pragma unroll
-      for (int c = 0; c < CS; ++c)
-#pragma unroll
-        for (int n = 0; n < NC; ++n) rs[c][n] = T::split(u[2 * c][n], u[2 * c + 1][n]);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int c = 0; c <= t / 2; ++c) {
-          const auto nf2 = T::get(lf + lower_frag<C>(t, c) * kFragBytes, lane);
-#pragma unroll
-          for (int n = 0; n < NC; ++n) u[t][n] = T::mul(nf2, rs[c][n], u[t][n]);
-        }
-    }
-    {
-      typename T::Split us[CS][NC];
-#pragma unroll
-      for (int c = 0; c < CS; ++c)
-#pragma unroll
-        for (int n = 0; n < NC; ++n) us[c][n] = T::split(u[2 * c][n], u[2 * c + 1][n]);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int c = 0; c <= t / 2; ++c) {
-          const auto pf = T::get(lf + (NF + lower_frag<C>(t, c)) * kFragBytes, lane);
-#pragma unroll
-          for (int n = 0; n < NC; ++n) ys[t][n] = T::mul(pf, us[c][n], ys[t][n]);
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int x = 16 * t + 4 * g + e;
-#pragma unroll
-        for (int n = 0; n < NC; ++n)
-          if (x < len && col0 + n < p.V)
-            out[(int64_t)(t0 + x) * a.o_t + col0 + n] = delta_round<D>(ys[t][n][e]);
       }
-    const float whole = lv[C - 1];
-    typename T::Fine us[CS][NC];
+    }
+    {
+      typename T::Split rs[CS];
+#pragma unroll
+      for (int c = 0; c < CS; ++c) rs[c] = T::split(u[2 * c], u[2 * c + 1]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c <= t / 2; ++c)
+          u[t] = T::mul(T::get(l.f + lower_frag<C>(t, c) * kFragBytes, lane), rs[c], u[t]);
+    }
+    {
+      typename T::Split us[CS];
+#pragma unroll
+      for (int c = 0; c < CS; ++c) us[c] = T::split(u[2 * c], u[2 * c + 1]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c <= t / 2; ++c)
+          ys[t] = T::mul(T::get(l.f + (NF + lower_frag<C>(t, c)) * kFragBytes, lane), us[c], ys[t]);
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const f32x4 left = lds4(lv + C + 16 * t + 4 * g);
 #pragma unroll
-      for (int n = 0; n < NC; ++n) u[t][n] *= left;
+      for (int e = 0; e < 4; ++e)
+        l.x[(16 * t + 4 * g + e) * Cols::LD + Cols::pos(c16 + r)] = delta_round<D>(ys[t][e]);
+      u[t] *= lds4(l.v + C + 16 * t + 4 * g);
     }
+    const float whole = l.v[C - 1];
 #pragma unroll
-    for (int c = 0; c < CS; ++c)
+    for (int t = 0; t < KT; ++t) s[t] *= whole;
 #pragma unroll
-      for (int n = 0; n < NC; ++n) us[c][n] = T::fine(u[2 * c][n], u[2 * c + 1][n]);
+    for (int c = 0; c < CS; ++c) {
+      const auto us = T::fine(u[2 * c], u[2 * c + 1]);
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-#pragma unroll
-      for (int n = 0; n < NC; ++n) s[t][n] *= whole;
-#pragma unroll
-      for (int c = 0; c < CS; ++c) {
-        const auto kf = Rows::cols(lk, 32 * c, 16 * t, lane);
-#pragma unroll
-        for (int n = 0; n < NC; ++n) s[t][n] = T::mul(kf, us[c][n], s[t][n]);
-      }
+      for (int t = 0; t < KT; ++t) s[t] = T::mul(Rows::cols(l.k, 32 * c, 16 * t, lane), us, s[t]);
     }
   }
-  if (state) each_state([&](int64_t i, float w) { return state[i] = w; });
+  __syncthreads();
+  if (chunks > 0) put_out(chunks - 1);
+  if (state) each([&](int64_t i, float w) { return state[i] = w; });
 }
 
 // ---------------------------------------------------------------- one token
@@ -318,9 +244,11 @@ static int delta_forward(const DeltaFwd& a, int64_t rows, hipStream_t stream) {
   hipLaunchKernelGGL((delta_prep_kernel<D, KP, false>), dim3((uint32_t)rows, p.heads), dim3(64), 0,
                      stream, p);
   if (int rc = check_launch("gated_delta_rule_varlen_fwd")) return rc;
-  const int cols = 16 * kWalkWaves;
-  hipLaunchKernelGGL((delta_walk_kernel<D, KP, 1>), dim3((p.V + cols - 1) / cols, p.heads, p.batch),
-                     dim3(64 * kWalkWaves), 0, stream, a);
+  const dim3 grid((p.V + 127) / 128, p.heads, p.batch);
+  if (p.V > 64)
+    hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8>), grid, dim3(512), 0, stream, a);
+  else
+    hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4>), grid, dim3(256), 0, stream, a);
   return check_launch("gated_delta_rule_varlen_fwd");
 }
 
@@ -414,6 +342,7 @@ extern "C" int gated_delta_rule_varlen_fwd(
   a.p.frags = reinterpret_cast<char*>(workspace + s.vectors);
   a.states = states, a.st_slot = st_stride_slot;
   a.out = out, a.o_t = out_stride_t, a.o_h = out_stride_h;
+  a.o_vec = delta_vec(out, out_stride_t, out_stride_h, V, 16 / elem_size(dtype));
   a.marks = checkpoints;
   if (dtype == SCONV_BF16)
     return K <= 64 ? delta_forward<Bf16, 64>(a, rows, stream) : delta_forward<Bf16, 128>(a, rows, stream);

@@ -20,6 +20,7 @@
 // in which the parts that would cancel are left out.
 #include "delta_host.h"
 #include "delta_prep.h"
+#include "delta_walk.h"
 
 namespace sconv {
 
@@ -32,24 +33,21 @@ struct DeltaBwd {
   int64_t df_slot, di_slot;
   void *dq, *dk, *dv, *dg, *db;
   int64_t dq_t, dq_h, dk_t, dk_h, dv_t, dv_h, dg_t, dg_h, db_t, db_h;
-  int32_t do_vec, v_vec;
+  int32_t do_vec;
 };
-
-constexpr int kBackWaves = 4;
 
 // One workgroup walks a sequence's chunks from the last, for one value head
 // and 16 columns a wave.
-template <typename D, int KP>
-__global__ __launch_bounds__(64 * kBackWaves, 2) void delta_back_kernel(DeltaBwd a) {
+template <typename D, int KP, int NW>
+__global__ __launch_bounds__(64 * NW, 8 / NW) void delta_back_kernel(DeltaBwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
   constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32;
-  constexpr int NF = kDeltaFrags<C>, THREADS = 64 * kBackWaves;
-  using Rows = LdsRows<D, KP>;
-  __shared__ __attribute__((aligned(16))) S lk[C * Rows::LD];
-  __shared__ __attribute__((aligned(16))) S lq[C * Rows::LD];
-  __shared__ __attribute__((aligned(16))) char lf[2 * NF * kFragBytes];
-  __shared__ __attribute__((aligned(16))) float lv[3 * C];
+  constexpr int NF = kDeltaFrags<C>;
+  using Stage = WalkStage<D, KP, NW>;
+  using Rows = typename Stage::L::Rows;
+  using Cols = typename Stage::L::Cols;
+  __shared__ typename Stage::L l;
 
   const DeltaParams& p = a.p;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -57,85 +55,36 @@ __global__ __launch_bounds__(64 * kBackWaves, 2) void delta_back_kernel(DeltaBwd
   const int32_t slot = p.slots ? p.slots[b] : b;
   if (p.slots && slot == p.pad) return;
   const int32_t start = p.qsl[b], end = p.qsl[b + 1];
-  const int32_t col = (blockIdx.x * kBackWaves + wave) * 16 + r;
+  const int32_t cols0 = blockIdx.x * 16 * NW, c16 = 16 * wave, col = cols0 + c16 + r;
   const int64_t KV = (int64_t)p.K * p.V;
 
   f32x4 s[KT];
-  auto each_state = [&](auto&& f) {
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int k = 16 * t + 4 * g + e;
-        if (k < p.K && col < p.V) s[t][e] = f((int64_t)k * p.V + col, s[t][e]);
-      }
-  };
 #pragma unroll
   for (int t = 0; t < KT; ++t) s[t] = zero4();
+  auto each = [&](auto&& f) { each_entry(s, p.K, p.V, col, cols0 + c16 + 16, f); };
   if (a.dfinal) {
     const float* from = a.dfinal + slot * a.df_slot + h * KV;
-    each_state([&](int64_t i, float) { return from[i]; });
+    each([&](int64_t i, float) { return from[i]; });
   }
-
-  constexpr int O8 = C * KP / 8 / THREADS;
-  constexpr int F16 = 2 * NF * kFragBytes / 16 / THREADS;
-  typename T::Exact nk[O8], nq[O8];
-  u32x4 nf[F16];
-  float nv = 0.f;
   const S* q = static_cast<const S*>(p.q) + kh * p.q_h;
   const S* k = static_cast<const S*>(p.k) + kh * p.k_h;
-  const int32_t row0 = start / C + b;
-  auto fetch = [&](int32_t i) {
-    const int32_t t0 = start + i * C;
-    const int64_t at = (int64_t)(row0 + i) * p.heads + h;
-#pragma unroll
-    for (int o = 0; o < O8; ++o) {
-      const int x = threadIdx.x + o * THREADS, t = x / (KP / 8), k0 = x % (KP / 8) * 8;
-      nk[o] = zero8<D>(), nq[o] = zero8<D>();
-      if (t0 + t < end) {
-        nk[o] = row8<D>(k + (int64_t)(t0 + t) * p.k_t, k0, p.K, p.k_vec);
-        nq[o] = row8<D>(q + (int64_t)(t0 + t) * p.q_t, k0, p.K, p.q_vec);
-      }
-    }
-    const u32x4* f = reinterpret_cast<const u32x4*>(p.frags + (at * (3 * NF) + NF) * kFragBytes);
-#pragma unroll
-    for (int o = 0; o < F16; ++o) nf[o] = f[threadIdx.x + o * THREADS];
-    if (threadIdx.x < 3 * C) nv = p.vectors[at * kDeltaVectors<C> + threadIdx.x];
-  };
-  auto stage = [&]() {
-#pragma unroll
-    for (int o = 0; o < O8; ++o) {
-      const int x = threadIdx.x + o * THREADS, t = x / (KP / 8), k0 = x % (KP / 8) * 8;
-      Rows::put8(lk, t, k0, nk[o]);
-      Rows::put8(lq, t, k0, nq[o]);
-    }
-#pragma unroll
-    for (int o = 0; o < F16; ++o) reinterpret_cast<u32x4*>(lf)[threadIdx.x + o * THREADS] = nf[o];
-    if (threadIdx.x < 3 * C) lv[threadIdx.x] = nv;
-  };
-
   const S* dout = static_cast<const S*>(a.dout) + h * a.do_h;
+  const int32_t row0 = start / C + b;
+  Stage next;
+  auto fetch = [&](int32_t i) {
+    const int64_t at = (int64_t)(row0 + i) * p.heads + h;
+    next.fetch(p, k, q, dout, a.do_t, p.qk_vec && a.do_vec, cols0, start + i * C, end,
+               p.frags + (at * (3 * NF) + NF) * kFragBytes, p.vectors + at * kDeltaVectors<C>);
+  };
   const int32_t chunks = (end - start + C - 1) / C;
   if (chunks > 0) fetch(chunks - 1);
   for (int32_t i = chunks - 1; i >= 0; --i) {
-    const int32_t t0 = start + i * C, len = end - t0;
     __syncthreads();
-    stage();
+    next.stage(l, p, cols0, end - (start + i * C));
     __syncthreads();
     if (i > 0) fetch(i - 1);
     float* mark = a.dstates + ((int64_t)(row0 + i) * p.heads + h) * KV;
-    each_state([&](int64_t x, float w) { return mark[x] = w; });
-    typename T::Exact go[CS];  // dO
-#pragma unroll
-    for (int c = 0; c < CS; ++c) {
-      S w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int x = 32 * c + 16 * (e / 4) + 4 * g + e % 4;
-        w[e] = x < len && col < p.V ? dout[(int64_t)(t0 + x) * a.do_t + col] : (S)0;
-      }
-      go[c] = T::join(w);
-    }
+    each([&](int64_t x, float w) { return mark[x] = w; });
     f32x4 u[NT];  // K dS, then dU, then dR
 #pragma unroll
     for (int t = 0; t < NT; ++t) u[t] = zero4();
@@ -143,14 +92,17 @@ __global__ __launch_bounds__(64 * kBackWaves, 2) void delta_back_kernel(DeltaBwd
     for (int c = 0; c < KS; ++c) {
       const auto sp = T::split(s[2 * c], s[2 * c + 1]);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) u[t] = T::mul(Rows::rows(lk, 16 * t, 32 * c, lane), sp, u[t]);
+      for (int t = 0; t < NT; ++t) u[t] = T::mul(Rows::rows(l.k, 16 * t, 32 * c, lane), sp, u[t]);
     }
+    typename T::Exact go[CS];  // dO
+#pragma unroll
+    for (int c = 0; c < CS; ++c) go[c] = Cols::cols(l.x, 32 * c, c16, lane);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      u[t] *= lds4(lv + C + 16 * t + 4 * g);
+      u[t] *= lds4(l.v + C + 16 * t + 4 * g);
 #pragma unroll
       for (int c = t / 2; c < CS; ++c)
-        u[t] = T::mul(T::get(lf + (NF + upper_frag<C>(t, c)) * kFragBytes, lane), go[c], u[t]);
+        u[t] = T::mul(T::get(l.f + (NF + upper_frag<C>(t, c)) * kFragBytes, lane), go[c], u[t]);
     }
     {
       typename T::Split us[CS];
@@ -160,9 +112,9 @@ __global__ __launch_bounds__(64 * kBackWaves, 2) void delta_back_kernel(DeltaBwd
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int c = t / 2; c < CS; ++c)
-          u[t] = T::mul(T::get(lf + upper_frag<C>(t, c) * kFragBytes, lane), us[c], u[t]);
+          u[t] = T::mul(T::get(l.f + upper_frag<C>(t, c) * kFragBytes, lane), us[c], u[t]);
     }
-    const float whole = lv[C - 1];
+    const float whole = l.v[C - 1];
 #pragma unroll
     for (int t = 0; t < KT; ++t) s[t] *= whole;
 #pragma unroll
@@ -171,7 +123,7 @@ __global__ __launch_bounds__(64 * kBackWaves, 2) void delta_back_kernel(DeltaBwd
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
         const int t = 2 * c + o;
-        const f32x4 gam = lds4(lv + 16 * t + 4 * g), bt = lds4(lv + 2 * C + 16 * t + 4 * g);
+        const f32x4 gam = lds4(l.v + 16 * t + 4 * g), bt = lds4(l.v + 2 * C + 16 * t + 4 * g);
         x[o] = -(gam * bt) * u[t];
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[o][e] = p.scale * gam[e] * T::value(go[c], 4 * o + e);
@@ -179,15 +131,15 @@ __global__ __launch_bounds__(64 * kBackWaves, 2) void delta_back_kernel(DeltaBwd
       const auto fx = T::fine(x[0], x[1]), fy = T::fine(y[0], y[1]);
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
-        s[t] = T::mul(Rows::cols(lk, 32 * c, 16 * t, lane), fx, s[t]);
-        s[t] = T::mul(Rows::cols(lq, 32 * c, 16 * t, lane), fy, s[t]);
+        s[t] = T::mul(Rows::cols(l.k, 32 * c, 16 * t, lane), fx, s[t]);
+        s[t] = T::mul(Rows::cols(l.q, 32 * c, 16 * t, lane), fy, s[t]);
       }
     }
   }
   if (a.dinitial) {
     float* to = a.dinitial + slot * a.di_slot + h * KV;
     const bool keep = p.has && p.has[b];
-    each_state([&](int64_t i, float w) { return to[i] = keep ? w : 0.f; });
+    each([&](int64_t i, float w) { return to[i] = keep ? w : 0.f; });
   }
 }
 
@@ -272,20 +224,34 @@ __global__ __launch_bounds__(4 * KP, KP == 128 ? 2 : 1) void delta_grad_kernel(D
       return Tri::cols(m, t0, c0, lane);
   };
 
+  // columns w0 .. of the chunk's rows of two tensors
+  auto stage2 = [&](S* l1, S* l2, const S* m1, int64_t ld1, const S* m2, int64_t ld2, int w0, int W,
+                    bool vec) {
+    constexpr int N = C * KP / 8 / THREADS;
+    static_assert(C * KP / 8 % THREADS == 0);
+    typename T::Exact x1[N], x2[N];
+    auto load = [&](auto v) {
+#pragma unroll
+      for (int o = 0; o < N; ++o) {
+        const int i = threadIdx.x + o * THREADS, t = i / (KP / 8), c0 = w0 + i % (KP / 8) * 8;
+        x1[o] = load8<D, decltype(v)::value>(m1, ld1, t, ch.len, c0, W);
+        x2[o] = load8<D, decltype(v)::value>(m2, ld2, t, ch.len, c0, W);
+      }
+    };
+    if (vec) load(std::true_type()); else load(std::false_type());
+#pragma unroll
+    for (int o = 0; o < N; ++o) {
+      const int i = threadIdx.x + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
+      const int n = t < ch.len ? W - w0 - c0 : 0;
+      Rows::put8(l1, t, c0, mask8<D>(x1[o], n));
+      Rows::put8(l2, t, c0, mask8<D>(x2[o], n));
+    }
+  };
   // K and Q of the chunk
   {
     const S* q = static_cast<const S*>(p.q) + (int64_t)ch.t0 * p.q_t + kh * p.q_h;
     const S* k = static_cast<const S*>(p.k) + (int64_t)ch.t0 * p.k_t + kh * p.k_h;
-    for (int x = threadIdx.x; x < C * KP / 8; x += THREADS) {
-      const int t = x / (KP / 8), k0 = x % (KP / 8) * 8;
-      auto xk = zero8<D>(), xq = zero8<D>();
-      if (t < ch.len) {
-        xk = row8<D>(k + (int64_t)t * p.k_t, k0, p.K, p.k_vec);
-        xq = row8<D>(q + (int64_t)t * p.q_t, k0, p.K, p.q_vec);
-      }
-      Rows::put8(lk, t, k0, xk);
-      Rows::put8(lq, t, k0, xq);
-    }
+    stage2(lk, lq, k, p.k_t, q, p.q_t, 0, p.K, p.qk_vec);
   }
 
   f32x4 dq[NT], dk[NT];
@@ -313,16 +279,8 @@ __global__ __launch_bounds__(4 * KP, KP == 128 ? 2 : 1) void delta_grad_kernel(D
 
     for (int32_t v0 = 0; v0 < p.V; v0 += KP) {
       __syncthreads();  // the last reads of dO, U, dR and the triangles
-      for (int x = threadIdx.x; x < C * KP / 8; x += THREADS) {
-        const int t = x / (KP / 8), c0 = x % (KP / 8) * 8;
-        auto xo = zero8<D>(), xv = zero8<D>();
-        if (t < ch.len) {
-          xo = row8<D>(dout + (int64_t)t * a.do_t, v0 + c0, p.V, a.do_vec);
-          xv = row8<D>(v + (int64_t)t * p.v_t, v0 + c0, p.V, a.v_vec);
-        }
-        Rows::put8(ldo, t, c0, xo);
-        Rows::put8(lu, t, c0, xv);  // V until U replaces it
-      }
+      // V lies in U's place until U replaces it
+      stage2(ldo, lu, dout, a.do_t, v, p.v_t, v0, p.V, a.do_vec && p.v_vec);
       if (v0 == 0)
         for (int x = threadIdx.x; x < kDeltaVectors<C>; x += THREADS)
           lv[x] = p.vectors[at * kDeltaVectors<C> + x];
@@ -577,9 +535,11 @@ static int delta_backward(const DeltaBwd& a, int64_t rows, hipStream_t stream) {
   hipLaunchKernelGGL((delta_prep_kernel<D, KP, true>), dim3((uint32_t)rows, p.heads), dim3(64), 0,
                      stream, p);
   if (int rc = check_launch(what)) return rc;
-  const int cols = 16 * kBackWaves;
-  hipLaunchKernelGGL((delta_back_kernel<D, KP>), dim3((p.V + cols - 1) / cols, p.heads, p.batch),
-                     dim3(64 * kBackWaves), 0, stream, a);
+  const dim3 grid((p.V + 127) / 128, p.heads, p.batch);
+  if (p.V > 64)
+    hipLaunchKernelGGL((delta_back_kernel<D, KP, 8>), grid, dim3(512), 0, stream, a);
+  else
+    hipLaunchKernelGGL((delta_back_kernel<D, KP, 4>), grid, dim3(256), 0, stream, a);
   if (int rc = check_launch(what)) return rc;
   hipLaunchKernelGGL((delta_grad_kernel<D, KP>), dim3((uint32_t)rows, p.heads / p.group),
                      dim3(4 * KP), 0, stream, a);
@@ -662,9 +622,7 @@ extern "C" int gated_delta_rule_varlen_bwd(
   a.dv = dv, a.dv_t = dv_stride_t, a.dv_h = dv_stride_h;
   a.dg = dg, a.dg_t = dg_stride_t, a.dg_h = dg_stride_h;
   a.db = dbeta, a.db_t = db_stride_t, a.db_h = db_stride_h;
-  const int64_t n = 16 / elem_size(dtype);
-  a.do_vec = aligned16(dout) && do_stride_t % n == 0 && do_stride_h % n == 0 && V % n == 0;
-  a.v_vec = aligned16(v) && v_stride_t % n == 0 && v_stride_h % n == 0 && V % n == 0;
+  a.do_vec = delta_vec(dout, do_stride_t, do_stride_h, V, 16 / elem_size(dtype));
   if (dtype == SCONV_BF16)
     return K <= 64 ? delta_backward<Bf16, 64>(a, rows, stream) : delta_backward<Bf16, 128>(a, rows, stream);
   return K <= 64 ? delta_backward<F32, 64>(a, rows, stream) : delta_backward<F32, 128>(a, rows, stream);
