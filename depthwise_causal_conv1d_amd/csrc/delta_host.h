@@ -110,6 +110,12 @@ inline int delta_inputs(const DeltaCall& c, DeltaParams& p, const void* q, int64
   return SCONV_OK;
 }
 
+// Whether a wave of a walk takes 32 columns (else 16): it reads half as much
+// LDS a product, on half as many CUs.
+inline bool delta_wide(const DeltaParams& p) {
+  return p.V > 64 && (int64_t)p.batch * p.heads * ((p.V + 63) / 64) > 256;
+}
+
 inline void delta_packing(const DeltaCall&, DeltaParams& p, const int32_t* qsl, const int32_t* slots,
                           const uint8_t* has, int32_t pad) {
   p.qsl = qsl, p.slots = slots, p.has = has, p.pad = pad;

@@ -29,6 +29,8 @@
 // matrix instructions, nothing is split.
 #pragma once
 
+#include <type_traits>
+
 #include "plane_host.h"
 #include "sconv_device.h"
 
@@ -140,6 +142,25 @@ template <> struct Tile<Bf16> {
     }
     return o;
   }
+  // A product's instructions one by one, the small parts first, so that a
+  // caller can let those of several tiles alternate: one that waits for the
+  // last one's sum leaves the matrix core idle.
+  static constexpr int kExactSplit = 2, kSplitSplit = 3, kExactFine = 3, kSplitExact = 2, kExactExact = 1;
+  template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Exact& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
+  }
+  template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Split& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, P == 0 ? b.lo : b.hi, c, 0, 0, 0);
+  }
+  template <int P> static __device__ __forceinline__ f32x4 part(const Split& a, const Exact& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(P == 0 ? a.lo : a.hi, b.v, c, 0, 0, 0);
+  }
+  template <int P> static __device__ __forceinline__ f32x4 part(const Split& a, const Split& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(P == 0 ? a.lo : a.hi, P == 1 ? b.lo : b.hi, c, 0, 0, 0);
+  }
+  template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Fine& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, P == 0 ? b.lo : P == 1 ? b.mid : b.hi, c, 0, 0, 0);
+  }
   static __device__ __forceinline__ f32x4 mul(const Exact& a, const Exact& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
   }
@@ -194,6 +215,11 @@ template <> struct Tile<F32> {
   using Split = Exact;
   using Fine = Exact;
 
+  static constexpr int kExactSplit = 8, kSplitSplit = 8, kExactFine = 8, kSplitExact = 8, kExactExact = 8;
+  template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Exact& b, f32x4 c) {
+    if constexpr (P < 4) return __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[P], b.a[P], c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_16x16x4f32(a.b[P - 4], b.b[P - 4], c, 0, 0, 0);
+  }
   static __device__ __forceinline__ Split split(const f32x4& a, const f32x4& b) { return {a, b}; }
   static __device__ __forceinline__ Fine fine(const f32x4& a, const f32x4& b) { return {a, b}; }
   static __device__ __forceinline__ f32x4 mul(const Exact& a, const Exact& b, f32x4 c) {
@@ -339,6 +365,20 @@ template <typename D, int W> struct LdsRows {
     }
   }
 };
+
+// f(0), .. f(N - 1) with constants.
+template <int N, int I = 0, typename F> __device__ __forceinline__ void each_part(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    each_part<N, I + 1>(f);
+  }
+}
+
+// What is above stays above in the instruction stream: loads ahead of the
+// products that cover their latency.  Left to itself the compiler puts each
+// load right before its use, to save registers (a chunk of the walk took 20000
+// cycles so, with 2400 of matrix instructions).
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
 __device__ __forceinline__ float delta_gate(const DeltaParams& p, const void* t, int64_t at) {
   return p.gates_f32 ? static_cast<const float*>(t)[at]

@@ -5,6 +5,7 @@
 #pragma once
 
 #include "delta_rule.h"
+#include "row_lanes.h"
 
 namespace sconv {
 
@@ -25,7 +26,8 @@ template <typename D, int KP, int NW> struct WalkStage {
   using S = typename D::storage;
   using E = typename Tile<D>::Exact;
   static constexpr int C = L::C, THREADS = 64 * NW;
-  static constexpr int KN = C * KP / 8, XN = C * 2 * NW, FN = 2 * kDeltaFrags<C> * kFragBytes / 16;
+  static constexpr int XW = 2 * NW;  // octets of a row of x
+  static constexpr int KN = C * KP / 8, XN = C * XW, FN = 2 * kDeltaFrags<C> * kFragBytes / 16;
   static constexpr int KO = (KN + THREADS - 1) / THREADS, XO = XN / THREADS, FO = FN / THREADS;
   static_assert(XN % THREADS == 0 && FN % THREADS == 0 && 3 * C <= THREADS);
   E k[KO], q[KO], x[XO];
@@ -46,7 +48,7 @@ template <typename D, int KP, int NW> struct WalkStage {
     }
 #pragma unroll
     for (int o = 0; o < XO; ++o) {
-      const int i = threadIdx.x + o * THREADS, t = i / (2 * NW), c0 = i % (2 * NW) * 8;
+      const int i = threadIdx.x + o * THREADS, t = i / XW, c0 = i % XW * 8;
       x[o] = load8<D, VEC>(tx + t0 * x_t, x_t, t, end - t0, col0 + c0, p.V);
     }
   }
@@ -73,7 +75,7 @@ template <typename D, int KP, int NW> struct WalkStage {
     }
 #pragma unroll
     for (int o = 0; o < XO; ++o) {
-      const int i = threadIdx.x + o * THREADS, t = i / (2 * NW), c0 = i % (2 * NW) * 8;
+      const int i = threadIdx.x + o * THREADS, t = i / XW, c0 = i % XW * 8;
       L::Cols::put8(l.x, t, c0, mask8<D>(x[o], t < len ? p.V - col0 - c0 : 0));
     }
 #pragma unroll
@@ -82,25 +84,126 @@ template <typename D, int KP, int NW> struct WalkStage {
   }
 };
 
-// A wave's 16 columns of a K x V matrix in accumulator tiles: f(index, value)
-// for every entry it has, and the values that f returns in their place.
-template <int KT, typename F>
-__device__ __forceinline__ void each_entry(f32x4 (&s)[KT], int K, int V, int col, int col_end, F&& f) {
+// A wave's 16 columns of a K x V matrix in memory and in accumulator tiles.  A
+// row is a uniform address and a lane's 32-bit offset: 64-bit addresses for
+// every lane and row, made once ahead of the loop, would take 64 registers.
+template <bool STORE, int KT>
+__device__ __forceinline__ void state_columns(f32x4 (&s)[KT], std::conditional_t<STORE, float, const float>* m,
+                                              int K, int V, int col, int col_end) {
   const int g = (threadIdx.x & 63) >> 4;
-  if (K == 16 * KT && col_end <= V) {  // of the whole wave
+  const uint32_t off = lane_offset((uint32_t)(4 * g * V + col) * 4u);
+  auto all = [&](auto in) {
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] = f((int64_t)(16 * t + 4 * g + e) * V + col, s[t][e]);
-    return;
-  }
+      for (int e = 0; e < 4; ++e) {
+        if (!in(16 * t + 4 * g + e)) continue;
+        auto* at = in_row(m + (int64_t)(16 * t + e) * V, off);
+        if constexpr (STORE) *at = s[t][e];
+        else s[t][e] = *at;
+      }
+  };
+  if (K == 16 * KT && col_end <= V) all([](int) { return true; });  // of the whole wave
+  else all([&](int k) { return k < K && col < V; });
+}
+
+// The products of a chunk's K (and Q) with 16 columns of a state: x = K S, y =
+// Q S.  K's and Q's operands alternate, each loaded while the other's products
+// run; `last` loads what comes next, behind the last of Q's.
+template <typename D, typename Rows, int KS, int NT, bool BOTH, typename F>
+__device__ __forceinline__ void rows_times_state(const typename D::storage* lk, const typename D::storage* lq,
+                                                 const f32x4 (&s)[2 * KS], f32x4 (&x)[NT], f32x4 (&y)[NT],
+                                                 int lane, F&& last) {
+  using T = Tile<D>;
+  typename T::Exact kf[2][NT], qf[NT];
+  typename T::Split sp[2];
+  auto load = [&](const typename D::storage* m, int c, typename T::Exact (&to)[NT]) {
 #pragma unroll
-  for (int t = 0; t < KT; ++t)
+    for (int t = 0; t < NT; ++t) to[t] = Rows::rows(m, 16 * t, 32 * c, lane);
+  };
+  load(lk, 0, kf[0]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int k = 16 * t + 4 * g + e;
-      if (k < K && col < V) s[t][e] = f((int64_t)k * V + col, s[t][e]);
+  for (int t = 0; t < NT; ++t) x[t] = y[t] = zero4();
+  sp[0] = T::split(s[0], s[1]);
+#pragma unroll
+  for (int c = 0; c < KS; ++c) {
+    constexpr int B = BOTH ? 0 : 1;  // K alone: its own operands alternate
+    if constexpr (BOTH) {
+      load(lq, c, qf);
+    } else {
+      if (c + 1 < KS) load(lk, c + 1, kf[(c + 1) & B]);
+      else last();
     }
+    keep_order();
+    if (!BOTH && c + 1 < KS) sp[(c + 1) & 1] = T::split(s[2 * c + 2], s[2 * c + 3]);
+    each_part<T::kExactSplit>([&](auto P) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) x[t] = T::template part<P>(kf[c & B][t], sp[c & 1], x[t]);
+    });
+    keep_order();
+    if constexpr (BOTH) {
+      if (c + 1 < KS) load(lk, c + 1, kf[0]);
+      else last();
+      keep_order();
+      if (c + 1 < KS) sp[(c + 1) & 1] = T::split(s[2 * c + 2], s[2 * c + 3]);
+      each_part<T::kExactSplit>([&](auto P) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) y[t] = T::template part<P>(qf[t], sp[c & 1], y[t]);
+      });
+      keep_order();
+    }
+  }
+}
+
+// x += (the triangle's frags) y: lower rows meet columns of steps c <= t / 2,
+// upper ones c >= t / 2.
+template <typename D, bool LOWER, int NF, typename Y, int NT>
+__device__ __forceinline__ void triangle_times(const typename Tile<D>::Split (&tri)[NF],
+                                               const Y (&y)[NT / 2], f32x4 (&x)[NT]) {
+  using T = Tile<D>;
+  constexpr int C = 16 * NT, CS = NT / 2;
+  constexpr int N = std::is_same<Y, typename T::Split>::value ? T::kSplitSplit : T::kSplitExact;
+  each_part<CS * N>([&](auto P) {
+    constexpr int c = P / N;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (LOWER ? c <= t / 2 : c >= t / 2)
+        x[t] = T::template part<P % N>(tri[LOWER ? lower_frag<C>(t, c) : upper_frag<C>(t, c)], y[c], x[t]);
+  });
+}
+
+template <typename D, int NF>
+__device__ __forceinline__ void load_triangle(typename Tile<D>::Split (&tri)[NF], const char* f, int lane) {
+#pragma unroll
+  for (int x = 0; x < NF; ++x) tri[x] = Tile<D>::get(f + x * kFragBytes, lane);
+}
+
+// s += M^T u for M's rows in LDS, 16 columns of u; half of M's operands are
+// loaded while the other half's products run.
+template <typename D, typename Rows, int KT, int CS>
+__device__ __forceinline__ void cols_times(const typename D::storage* m,
+                                           const typename Tile<D>::Fine (&u)[CS], f32x4 (&s)[KT], int lane) {
+  using T = Tile<D>;
+  constexpr int H = KT / 2;
+  typename T::Exact f[2][H];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int t = 0; t < H; ++t) f[i & 1][t] = Rows::cols(m, 32 * (i / 2), 16 * (H * (i & 1) + t), lane);
+  };
+  load(0);
+#pragma unroll
+  for (int i = 0; i < 2 * CS; ++i) {
+    if (i + 1 < 2 * CS) load(i + 1);
+    keep_order();
+    each_part<T::kExactFine>([&](auto P) {
+#pragma unroll
+      for (int t = 0; t < H; ++t) {
+        f32x4& to = s[H * (i & 1) + t];
+        to = T::template part<P>(f[i & 1][t], u[i / 2], to);
+      }
+    });
+    keep_order();
+  }
 }
 
 }  // namespace sconv

@@ -19,7 +19,7 @@ struct DeltaFwd {
 // One workgroup walks a sequence's chunks for one value head, 16 columns a
 // wave.  An output chunk waits in LDS, in V's place, for the next one's staging.
 template <typename D, int KP, int NW>
-__global__ __launch_bounds__(64 * NW, 8 / NW) void delta_walk_kernel(DeltaFwd a) {
+__global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
   constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32;
@@ -42,8 +42,8 @@ __global__ __launch_bounds__(64 * NW, 8 / NW) void delta_walk_kernel(DeltaFwd a)
 #pragma unroll
   for (int t = 0; t < KT; ++t) s[t] = zero4();
   float* state = a.states ? a.states + slot * a.st_slot + h * KV : nullptr;
-  auto each = [&](auto&& f) { each_entry(s, p.K, p.V, col, cols0 + c16 + 16, f); };
-  if (p.has && p.has[b]) each([&](int64_t i, float) { return state[i]; });
+  const int32_t ends = cols0 + c16 + 16;
+  if (p.has && p.has[b]) state_columns<false>(s, state, p.K, p.V, col, ends);
 
   const S* q = static_cast<const S*>(p.q) + kh * p.q_h;
   const S* k = static_cast<const S*>(p.k) + kh * p.k_h;
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(64 * NW, 8 / NW) void delta_walk_kernel(DeltaFwd a)
     const int32_t t0 = start + i * C;
 #pragma unroll
     for (int o = 0; o < Stage::XO; ++o) {
-      const int x = threadIdx.x + o * Stage::THREADS, t = x / (2 * NW), c0 = x % (2 * NW) * 8;
+      const int x = threadIdx.x + o * Stage::THREADS, t = x / Stage::XW, c0 = x % Stage::XW * 8;
       if (t < end - t0)
         put_row8<D>(out + (int64_t)(t0 + t) * a.o_t, cols0 + c0, p.V, a.o_vec, Cols::get8(l.x, t, c0));
     }
@@ -73,77 +73,53 @@ __global__ __launch_bounds__(64 * NW, 8 / NW) void delta_walk_kernel(DeltaFwd a)
     next.stage(l, p, cols0, end - (start + i * C));
     __syncthreads();
     if (i + 1 < chunks) fetch(i + 1);
-    if (a.marks) {
-      float* mark = a.marks + ((int64_t)(row0 + i) * p.heads + h) * KV;
-      each([&](int64_t x, float w) { return mark[x] = w; });
-    }
-    f32x4 xs[NT], ys[NT];  // K S, Q S
+    if (a.marks)
+      state_columns<true>(s, a.marks + ((int64_t)(row0 + i) * p.heads + h) * KV, p.K, p.V, col, ends);
+    f32x4 u[NT], y[NT];  // K S, then R, then U; Q S, then O
+    typename T::Exact vv[CS];
+    typename T::Split tri[NF], us[CS];
+    rows_times_state<D, Rows, KS, NT, true>(l.k, l.q, s, u, y, lane, [&] {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) xs[t] = zero4(), ys[t] = zero4();
-#pragma unroll
-    for (int c = 0; c < KS; ++c) {
-      const auto sp = T::split(s[2 * c], s[2 * c + 1]);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        xs[t] = T::mul(Rows::rows(l.k, 16 * t, 32 * c, lane), sp, xs[t]);
-        ys[t] = T::mul(Rows::rows(l.q, 16 * t, 32 * c, lane), sp, ys[t]);
-      }
-    }
-    f32x4 u[NT];  // R, then U
-#pragma unroll
-    for (int c = 0; c < CS; ++c) {
-      const auto vv = Cols::cols(l.x, 32 * c, c16, lane);
-#pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const int t = 2 * c + o;
-        const f32x4 gam = lds4(l.v + 16 * t + 4 * g), bt = lds4(l.v + 2 * C + 16 * t + 4 * g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          u[t][e] = bt[e] * (T::value(vv, 4 * o + e) - gam[e] * xs[t][e]);
-          ys[t][e] *= p.scale * gam[e];
-        }
-      }
-    }
-    {
-      typename T::Split rs[CS];
-#pragma unroll
-      for (int c = 0; c < CS; ++c) rs[c] = T::split(u[2 * c], u[2 * c + 1]);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int c = 0; c <= t / 2; ++c)
-          u[t] = T::mul(T::get(l.f + lower_frag<C>(t, c) * kFragBytes, lane), rs[c], u[t]);
-    }
-    {
-      typename T::Split us[CS];
-#pragma unroll
-      for (int c = 0; c < CS; ++c) us[c] = T::split(u[2 * c], u[2 * c + 1]);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int c = 0; c <= t / 2; ++c)
-          ys[t] = T::mul(T::get(l.f + (NF + lower_frag<C>(t, c)) * kFragBytes, lane), us[c], ys[t]);
-    }
+      for (int c = 0; c < CS; ++c) vv[c] = Cols::cols(l.x, 32 * c, c16, lane);
+      load_triangle<D>(tri, l.f, lane);
+    });
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+      const f32x4 gam = lds4(l.v + 16 * t + 4 * g), bt = lds4(l.v + 2 * C + 16 * t + 4 * g);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        l.x[(16 * t + 4 * g + e) * Cols::LD + Cols::pos(c16 + r)] = delta_round<D>(ys[t][e]);
-      u[t] *= lds4(l.v + C + 16 * t + 4 * g);
+      for (int e = 0; e < 4; ++e) {
+        u[t][e] = bt[e] * (T::value(vv[t / 2], 4 * (t & 1) + e) - gam[e] * u[t][e]);
+        y[t][e] *= p.scale * gam[e];
+      }
     }
+#pragma unroll
+    for (int c = 0; c < CS; ++c) us[c] = T::split(u[2 * c], u[2 * c + 1]);
+    triangle_times<D, true>(tri, us, u);
+    keep_order();
+    load_triangle<D>(tri, l.f + NF * kFragBytes, lane);
+    keep_order();
+#pragma unroll
+    for (int c = 0; c < CS; ++c) us[c] = T::split(u[2 * c], u[2 * c + 1]);
     const float whole = l.v[C - 1];
+    typename T::Fine fine[CS];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) u[t] *= lds4(l.v + C + 16 * t + 4 * g);
+#pragma unroll
+    for (int c = 0; c < CS; ++c) fine[c] = T::fine(u[2 * c], u[2 * c + 1]);
 #pragma unroll
     for (int t = 0; t < KT; ++t) s[t] *= whole;
+    triangle_times<D, true>(tri, us, y);
+    keep_order();
+    cols_times<D, Rows>(l.k, fine, s, lane);
 #pragma unroll
-    for (int c = 0; c < CS; ++c) {
-      const auto us = T::fine(u[2 * c], u[2 * c + 1]);
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < KT; ++t) s[t] = T::mul(Rows::cols(l.k, 32 * c, 16 * t, lane), us, s[t]);
-    }
+      for (int e = 0; e < 4; ++e)
+        l.x[(16 * t + 4 * g + e) * Cols::LD + Cols::pos(c16 + r)] = delta_round<D>(y[t][e]);
   }
   __syncthreads();
   if (chunks > 0) put_out(chunks - 1);
-  if (state) each([&](int64_t i, float w) { return state[i] = w; });
+  if (state) state_columns<true>(s, state, p.K, p.V, col, ends);
 }
 
 // ---------------------------------------------------------------- one token
@@ -244,11 +220,12 @@ static int delta_forward(const DeltaFwd& a, int64_t rows, hipStream_t stream) {
   hipLaunchKernelGGL((delta_prep_kernel<D, KP, false>), dim3((uint32_t)rows, p.heads), dim3(64), 0,
                      stream, p);
   if (int rc = check_launch("gated_delta_rule_varlen_fwd")) return rc;
-  const dim3 grid((p.V + 127) / 128, p.heads, p.batch);
-  if (p.V > 64)
-    hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8>), grid, dim3(512), 0, stream, a);
+  if (delta_wide(p))
+    hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8>), dim3((p.V + 127) / 128, p.heads, p.batch),
+                       dim3(512), 0, stream, a);
   else
-    hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4>), grid, dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4>), dim3((p.V + 63) / 64, p.heads, p.batch),
+                       dim3(256), 0, stream, a);
   return check_launch("gated_delta_rule_varlen_fwd");
 }
 

@@ -39,7 +39,7 @@ struct DeltaBwd {
 // One workgroup walks a sequence's chunks from the last, for one value head
 // and 16 columns a wave.
 template <typename D, int KP, int NW>
-__global__ __launch_bounds__(64 * NW, 8 / NW) void delta_back_kernel(DeltaBwd a) {
+__global__ __launch_bounds__(64 * NW, NW / 4) void delta_back_kernel(DeltaBwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
   constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32;
@@ -61,11 +61,8 @@ __global__ __launch_bounds__(64 * NW, 8 / NW) void delta_back_kernel(DeltaBwd a)
   f32x4 s[KT];
 #pragma unroll
   for (int t = 0; t < KT; ++t) s[t] = zero4();
-  auto each = [&](auto&& f) { each_entry(s, p.K, p.V, col, cols0 + c16 + 16, f); };
-  if (a.dfinal) {
-    const float* from = a.dfinal + slot * a.df_slot + h * KV;
-    each([&](int64_t i, float) { return from[i]; });
-  }
+  const int32_t ends = cols0 + c16 + 16;
+  if (a.dfinal) state_columns<false>(s, a.dfinal + slot * a.df_slot + h * KV, p.K, p.V, col, ends);
   const S* q = static_cast<const S*>(p.q) + kh * p.q_h;
   const S* k = static_cast<const S*>(p.k) + kh * p.k_h;
   const S* dout = static_cast<const S*>(a.dout) + h * a.do_h;
@@ -83,63 +80,54 @@ __global__ __launch_bounds__(64 * NW, 8 / NW) void delta_back_kernel(DeltaBwd a)
     next.stage(l, p, cols0, end - (start + i * C));
     __syncthreads();
     if (i > 0) fetch(i - 1);
-    float* mark = a.dstates + ((int64_t)(row0 + i) * p.heads + h) * KV;
-    each([&](int64_t x, float w) { return mark[x] = w; });
-    f32x4 u[NT];  // K dS, then dU, then dR
-#pragma unroll
-    for (int t = 0; t < NT; ++t) u[t] = zero4();
-#pragma unroll
-    for (int c = 0; c < KS; ++c) {
-      const auto sp = T::split(s[2 * c], s[2 * c + 1]);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) u[t] = T::mul(Rows::rows(l.k, 16 * t, 32 * c, lane), sp, u[t]);
-    }
+    state_columns<true>(s, a.dstates + ((int64_t)(row0 + i) * p.heads + h) * KV, p.K, p.V, col, ends);
+    f32x4 u[NT], none[NT];     // K dS, then dU, then dR
     typename T::Exact go[CS];  // dO
+    typename T::Split tri[NF], us[CS];
+    rows_times_state<D, Rows, KS, NT, false>(l.k, l.q, s, u, none, lane, [&] {
 #pragma unroll
-    for (int c = 0; c < CS; ++c) go[c] = Cols::cols(l.x, 32 * c, c16, lane);
+      for (int c = 0; c < CS; ++c) go[c] = Cols::cols(l.x, 32 * c, c16, lane);
+      load_triangle<D>(tri, l.f + NF * kFragBytes, lane);
+    });
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      u[t] *= lds4(l.v + C + 16 * t + 4 * g);
+    for (int t = 0; t < NT; ++t) u[t] *= lds4(l.v + C + 16 * t + 4 * g);
+    triangle_times<D, false>(tri, go, u);
+    keep_order();
+    load_triangle<D>(tri, l.f, lane);
+    keep_order();
 #pragma unroll
-      for (int c = t / 2; c < CS; ++c)
-        u[t] = T::mul(T::get(l.f + (NF + upper_frag<C>(t, c)) * kFragBytes, lane), go[c], u[t]);
-    }
-    {
-      typename T::Split us[CS];
-#pragma unroll
-      for (int c = 0; c < CS; ++c) us[c] = T::split(u[2 * c], u[2 * c + 1]);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int c = t / 2; c < CS; ++c)
-          u[t] = T::mul(T::get(l.f + upper_frag<C>(t, c) * kFragBytes, lane), us[c], u[t]);
-    }
+    for (int c = 0; c < CS; ++c) us[c] = T::split(u[2 * c], u[2 * c + 1]);
     const float whole = l.v[C - 1];
 #pragma unroll
     for (int t = 0; t < KT; ++t) s[t] *= whole;
+    typename T::Fine fine[CS];
 #pragma unroll
     for (int c = 0; c < CS; ++c) {
-      f32x4 x[2], y[2];
+      f32x4 y[2];
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
-        const int t = 2 * c + o;
-        const f32x4 gam = lds4(l.v + 16 * t + 4 * g), bt = lds4(l.v + 2 * C + 16 * t + 4 * g);
-        x[o] = -(gam * bt) * u[t];
+        const f32x4 gam = lds4(l.v + 32 * c + 16 * o + 4 * g) * p.scale;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[o][e] = p.scale * gam[e] * T::value(go[c], 4 * o + e);
+        for (int e = 0; e < 4; ++e) y[o][e] = gam[e] * T::value(go[c], 4 * o + e);
       }
-      const auto fx = T::fine(x[0], x[1]), fy = T::fine(y[0], y[1]);
-#pragma unroll
-      for (int t = 0; t < KT; ++t) {
-        s[t] = T::mul(Rows::cols(l.k, 32 * c, 16 * t, lane), fx, s[t]);
-        s[t] = T::mul(Rows::cols(l.q, 32 * c, 16 * t, lane), fy, s[t]);
-      }
+      fine[c] = T::fine(y[0], y[1]);
     }
+    triangle_times<D, false>(tri, us, u);
+    keep_order();
+    cols_times<D, Rows>(l.q, fine, s, lane);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      u[t] *= -(lds4(l.v + 16 * t + 4 * g) * lds4(l.v + 2 * C + 16 * t + 4 * g));
+#pragma unroll
+    for (int c = 0; c < CS; ++c) fine[c] = T::fine(u[2 * c], u[2 * c + 1]);
+    cols_times<D, Rows>(l.k, fine, s, lane);
   }
   if (a.dinitial) {
-    float* to = a.dinitial + slot * a.di_slot + h * KV;
-    const bool keep = p.has && p.has[b];
-    each([&](int64_t i, float w) { return to[i] = keep ? w : 0.f; });
+    if (!(p.has && p.has[b])) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t) s[t] = zero4();
+    }
+    state_columns<true>(s, a.dinitial + slot * a.di_slot + h * KV, p.K, p.V, col, ends);
   }
 }
 
@@ -535,11 +523,12 @@ static int delta_backward(const DeltaBwd& a, int64_t rows, hipStream_t stream) {
   hipLaunchKernelGGL((delta_prep_kernel<D, KP, true>), dim3((uint32_t)rows, p.heads), dim3(64), 0,
                      stream, p);
   if (int rc = check_launch(what)) return rc;
-  const dim3 grid((p.V + 127) / 128, p.heads, p.batch);
-  if (p.V > 64)
-    hipLaunchKernelGGL((delta_back_kernel<D, KP, 8>), grid, dim3(512), 0, stream, a);
+  if (delta_wide(p))
+    hipLaunchKernelGGL((delta_back_kernel<D, KP, 8>), dim3((p.V + 127) / 128, p.heads, p.batch),
+                       dim3(512), 0, stream, a);
   else
-    hipLaunchKernelGGL((delta_back_kernel<D, KP, 4>), grid, dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((delta_back_kernel<D, KP, 4>), dim3((p.V + 63) / 64, p.heads, p.batch),
+                       dim3(256), 0, stream, a);
   if (int rc = check_launch(what)) return rc;
   hipLaunchKernelGGL((delta_grad_kernel<D, KP>), dim3((uint32_t)rows, p.heads / p.group),
                      dim3(4 * KP), 0, stream, a);
