@@ -14,10 +14,10 @@ struct DeltaCall {
   int32_t batch, key_heads, heads, K, V, dtype, gate_dtype;
 };
 
-// Workspace in floats: vectors first, then frags (16-byte pieces), then the
-// gradients' states.
+// Workspace in floats: vectors first, then frags (16-byte pieces), then for
+// gradients dR's tiles and the states' gradients.
 struct DeltaSpace {
-  int64_t vectors, fwd, bwd, bwd_states;
+  int64_t vectors, fwd, bwd, bwd_rows, bwd_states;
 };
 
 inline DeltaSpace delta_space(int64_t total_T, int32_t batch, int32_t heads, int32_t K, int32_t V,
@@ -27,7 +27,8 @@ inline DeltaSpace delta_space(int64_t total_T, int32_t batch, int32_t heads, int
   DeltaSpace s;
   s.vectors = n * 5 * C;
   s.fwd = s.vectors + n * 2 * nf * (kFragBytes / 4);
-  s.bwd_states = s.vectors + n * 3 * nf * (kFragBytes / 4);
+  s.bwd_rows = s.vectors + n * 3 * nf * (kFragBytes / 4);
+  s.bwd_states = s.bwd_rows + n * C * cdiv(V, 16) * 16;
   s.bwd = s.bwd_states + n * K * V;
   return s;
 }

@@ -5,7 +5,7 @@
 //   dU = P^T dO + e^(G_C - G) (K dS1),  dR = T^T dU = dU + N^T dU
 //   dS0 = e^(G_C) dS1 + scale Q^T (e^G dO) - K^T (e^G beta dR)
 // One kernel walks the chunks from the end with dS in registers, as the
-// forward walks them, and leaves dS1 of every chunk; then every chunk's
+// forward walks them, and leaves dS1 and dR of every chunk; then every chunk's
 // gradients are independent.  With E_P = scale e (dO U^T) (i >= j), E_A =
 // e (dR U^T) (i > j):
 //   dV = beta dR,  dQ = scale e^G (dO S0^T) + E_P K
@@ -21,6 +21,7 @@
 #include "delta_host.h"
 #include "delta_prep.h"
 #include "delta_walk.h"
+#include "norm_rows.h"
 
 namespace sconv {
 
@@ -29,12 +30,18 @@ struct DeltaBwd {
   const void* dout;
   int64_t do_t, do_h;
   const float *marks, *dfinal;
-  float *dinitial, *dstates;
+  float *dinitial, *dstates, *drows;  // drows: dR's accumulator tiles
   int64_t df_slot, di_slot;
   void *dq, *dk, *dv, *dg, *db;
   int64_t dq_t, dq_h, dk_t, dk_h, dv_t, dv_h, dg_t, dg_h, db_t, db_h;
-  int32_t do_vec;
+  int32_t do_vec, dqk_vec, dv_vec;
 };
+
+// Where a lane's part of dR's tiles of 16 columns lies: 1 KB a tile of 16 tokens.
+template <int C>
+__device__ __forceinline__ f32x4* delta_row_tiles(float* drows, int64_t at, int32_t V, int32_t tile, int lane) {
+  return reinterpret_cast<f32x4*>(drows + (at * ((V + 15) / 16) + tile) * 16 * C) + lane;
+}
 
 // One workgroup walks a sequence's chunks from the last, for one value head
 // and 16 columns a wave.
@@ -115,6 +122,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_back_kernel(DeltaBwd a)
     triangle_times<D, false>(tri, us, u);
     keep_order();
     cols_times<D, Rows>(l.q, fine, s, lane);
+    if (cols0 + c16 < p.V) {
+      f32x4* to = delta_row_tiles<C>(a.drows, (int64_t)(row0 + i) * p.heads + h, p.V, (cols0 + c16) / 16, lane);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) to[64 * t] = u[t];
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       u[t] *= -(lds4(l.v + 16 * t + 4 * g) * lds4(l.v + 2 * C + 16 * t + 4 * g));
@@ -131,54 +143,53 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_back_kernel(DeltaBwd a)
   }
 }
 
-// v summed over the 16 lanes of a group; all of them get it.
-__device__ __forceinline__ float sum16(float v) {
-#pragma unroll
-  for (int d = 1; d < 16; d *= 2) v += __shfl_xor(v, d, 64);
-  return v;
-}
+// Row of tile n of a lower triangle of 4 x 4 tiles, counted row by row.
+__device__ __forceinline__ int tile_row(int n) { return n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0; }
 
 // LDS of a workgroup below: K, Q, dO, the parts of U and dR (later of three
 // triangles), vectors, sums of the waves.
-template <typename D, int KP>
-constexpr int kGradParts = sizeof(typename D::storage) == 2 ? 2 : 1;
-template <typename D, int KP> constexpr int kGradBig = kDeltaChunk<D> * LdsRows<D, KP>::LD;
-template <typename D, int KP>
-constexpr int kGradSmall = kDeltaChunk<D> * LdsRows<D, kDeltaChunk<D>>::LD;
-template <typename D, int KP>
-constexpr int kGradShared = kGradParts<D, KP> * (3 * kGradSmall<D, KP> > 2 * kGradBig<D, KP>
-                                                     ? 3 * kGradSmall<D, KP> : 2 * kGradBig<D, KP>);
-template <typename D, int KP>
-constexpr int kGradLds = (3 * kGradBig<D, KP> + kGradShared<D, KP>) * (int)sizeof(typename D::storage) +
-                         4 * (kDeltaVectors<kDeltaChunk<D>> + KP / 16 * (4 * kDeltaChunk<D> + 1));
+template <typename D, int KP> struct GradLds {
+  using S = typename D::storage;
+  static constexpr int C = kDeltaChunk<D>, NW = KP / 16, PARTS = sizeof(S) == 2 ? 2 : 1;
+  static constexpr int BIG = C * LdsRows<D, KP>::LD, SMALL = C * LdsRows<D, C>::LD;
+  __attribute__((aligned(16))) S k[BIG];
+  __attribute__((aligned(16))) S q[BIG];
+  __attribute__((aligned(16))) S dout[BIG];
+  union {
+    struct { S u[PARTS * BIG], r[PARTS * BIG]; };
+    S e[3 * PARTS * SMALL];  // E_P, E_A, beta E_A
+    __attribute__((aligned(16))) char align_;
+  };
+  __attribute__((aligned(16))) char f[kDeltaFrags<C> * kFragBytes];  // N
+  __attribute__((aligned(16))) float v[kDeltaVectors<C>];
+  float part[NW][4][C], dots[NW];
+};
 
 // One workgroup: all gradients of a chunk's tokens for one key head, its value
 // heads one after another (dq and dk add up in registers, in that order).
 // Columns come in blocks of KP, 16 a wave; then a wave owns 16 of K.
-template <typename D, int KP>
-__global__ __launch_bounds__(4 * KP, KP == 128 ? 2 : 1) void delta_grad_kernel(DeltaBwd a) {
+template <typename D, int KP, bool GROUPED>
+__global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
-  constexpr bool kB = sizeof(S) == 2;
-  constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, CS = C / 32, NW = KP / 16;
-  constexpr int NF = kDeltaFrags<C>, THREADS = 64 * NW, PARTS = kGradParts<D, KP>;
-  constexpr int TILES = NT * (NT + 1) / 2, MINE = (TILES + NW - 1) / NW;
+  using L = GradLds<D, KP>;
   using Rows = LdsRows<D, KP>;
+  constexpr bool kB = sizeof(S) == 2;
+  constexpr int C = L::C, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32, NW = L::NW;
+  constexpr int NF = kDeltaFrags<C>, THREADS = 64 * NW, PARTS = L::PARTS, BIG = L::BIG, SMALL = L::SMALL;
+  constexpr int TILES = NT * (NT + 1) / 2, MINE = (TILES + NW - 1) / NW;
   using Tri = LdsRows<D, C>;
-  constexpr int BIG = kGradBig<D, KP>, SMALL = kGradSmall<D, KP>;
-  __shared__ __attribute__((aligned(16))) char lds[kGradLds<D, KP>];
-  S* lk = reinterpret_cast<S*>(lds);
-  S* lq = lk + BIG;
-  S* ldo = lq + BIG;
-  S* lu = ldo + BIG;           // PARTS planes each
-  S* lr = lu + PARTS * BIG;
-  S* le = lu;                  // E_P, E_A, beta E_A over U and dR once those are read
-  float* lv = reinterpret_cast<float*>(lu + kGradShared<D, KP>);  // the chunk's vectors
-  float* part = lv + kDeltaVectors<C>;                     // [NW][4][C]
-  float* dots = part + NW * 4 * C;                         // [NW]
+  __shared__ L l;
 
   const DeltaParams& p = a.p;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  // Hidden anew in every loop below: all that is computed from them would
+  // otherwise be computed once ahead of the loops and spilled there.
+  int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int wave = uniform(tid >> 6);
+  auto hide = [&] {
+    tid = (int)lane_offset((uint32_t)tid);
+    lane = tid & 63, r = lane & 15, g = lane >> 4;
+  };
   const int32_t row = blockIdx.x, kh = blockIdx.y;
   const DeltaChunk ch = delta_find<C>(p, row);
   if (ch.len == 0) return;
@@ -211,271 +222,332 @@ __global__ __launch_bounds__(4 * KP, KP == 128 ? 2 : 1) void delta_grad_kernel(D
     else
       return Tri::cols(m, t0, c0, lane);
   };
-
-  // columns w0 .. of the chunk's rows of two tensors
-  auto stage2 = [&](S* l1, S* l2, const S* m1, int64_t ld1, const S* m2, int64_t ld2, int w0, int W,
-                    bool vec) {
-    constexpr int N = C * KP / 8 / THREADS;
-    static_assert(C * KP / 8 % THREADS == 0);
-    typename T::Exact x1[N], x2[N];
+  // columns w0 .. of the chunk's rows of two tensors, to registers and on to LDS
+  constexpr int N8 = C * KP / 8 / THREADS;
+  static_assert(C * KP / 8 % THREADS == 0);
+  typedef typename T::Exact Octets[N8];
+  auto load2 = [&](Octets& x1, Octets& x2, const S* m1, int64_t ld1, const S* m2, int64_t ld2, int w0,
+                   int W, bool vec) {
     auto load = [&](auto v) {
 #pragma unroll
-      for (int o = 0; o < N; ++o) {
-        const int i = threadIdx.x + o * THREADS, t = i / (KP / 8), c0 = w0 + i % (KP / 8) * 8;
+      for (int o = 0; o < N8; ++o) {
+        const int i = tid + o * THREADS, t = i / (KP / 8), c0 = w0 + i % (KP / 8) * 8;
         x1[o] = load8<D, decltype(v)::value>(m1, ld1, t, ch.len, c0, W);
         x2[o] = load8<D, decltype(v)::value>(m2, ld2, t, ch.len, c0, W);
       }
     };
     if (vec) load(std::true_type()); else load(std::false_type());
+  };
+  auto stage2 = [&](S* l1, S* l2, const Octets& x1, const Octets& x2, int w0, int W) {
 #pragma unroll
-    for (int o = 0; o < N; ++o) {
-      const int i = threadIdx.x + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
+    for (int o = 0; o < N8; ++o) {
+      const int i = tid + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
       const int n = t < ch.len ? W - w0 - c0 : 0;
       Rows::put8(l1, t, c0, mask8<D>(x1[o], n));
       Rows::put8(l2, t, c0, mask8<D>(x2[o], n));
     }
   };
-  // K and Q of the chunk
-  {
-    const S* q = static_cast<const S*>(p.q) + (int64_t)ch.t0 * p.q_t + kh * p.q_h;
-    const S* k = static_cast<const S*>(p.k) + (int64_t)ch.t0 * p.k_t + kh * p.k_h;
-    stage2(lk, lq, k, p.k_t, q, p.q_t, 0, p.K, p.qk_vec);
-  }
-
-  f32x4 dq[NT], dk[NT];
+  // a tile back to memory, 16 bytes a lane where rows are of such vectors
+  auto put_tile = [&](S* m, int64_t ld, int w0, int W, bool vec, auto&& octet) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) dq[t] = zero4(), dk[t] = zero4();
-  const int kidx = 16 * wave + r;  // this lane's channel of K
+    for (int o = 0; o < N8; ++o) {
+      const int i = tid + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
+      if (t < ch.len) put_row8<D>(m + t * ld, w0 + c0, W, vec, octet(t, c0));
+    }
+  };
 
-  for (int32_t gh = 0; gh < p.group; ++gh) {
+  Octets x1, x2;
+  load2(x1, x2, static_cast<const S*>(p.k) + ch.t0 * p.k_t + kh * p.k_h, p.k_t,
+        static_cast<const S*>(p.q) + ch.t0 * p.q_t + kh * p.q_h, p.q_t, 0, p.K, p.qk_vec);
+  f32x4 dq[NT], dk[NT];
+  if constexpr (GROUPED) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) dq[t] = dk[t] = zero4();
+  }
+  const bool rows4 = p.V % 4 == 0;
+
+  for (int32_t gh = 0; gh < (GROUPED ? p.group : 1); ++gh) {
+    hide();
     const int32_t h = kh * p.group + gh;
     const int64_t at = (int64_t)row * p.heads + h;
-    const char* frags = p.frags + at * (3 * NF) * kFragBytes;
     const float *s0 = a.marks + at * KV, *ds = a.dstates + at * KV;
-    const S* v = static_cast<const S*>(p.v) + (int64_t)ch.t0 * p.v_t + h * p.v_h;
-    const S* dout = static_cast<const S*>(a.dout) + (int64_t)ch.t0 * a.do_t + h * a.do_h;
-    S* dv = static_cast<S*>(a.dv) + (int64_t)ch.t0 * a.dv_t + h * a.dv_h;
+    const S* v = static_cast<const S*>(p.v) + ch.t0 * p.v_t + h * p.v_h;
+    const S* dout = static_cast<const S*>(a.dout) + ch.t0 * a.do_t + h * a.do_h;
 
     f32x4 mq[NT], mz[NT], mw[NT];  // dO S0^T, dR S0^T, U dS1^T
     f32x4 ep[MINE], ea[MINE];      // tiles of dO U^T and dR U^T
-    f32x4 rv[NT];                  // rowsum(dR V), this lane's columns
     float dot = 0.f;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) mq[t] = mz[t] = mw[t] = rv[t] = zero4();
+    for (int t = 0; t < NT; ++t) mq[t] = mz[t] = mw[t] = zero4();
 #pragma unroll
     for (int m = 0; m < MINE; ++m) ep[m] = ea[m] = zero4();
 
     for (int32_t v0 = 0; v0 < p.V; v0 += KP) {
-      __syncthreads();  // the last reads of dO, U, dR and the triangles
-      // V lies in U's place until U replaces it
-      stage2(ldo, lu, dout, a.do_t, v, p.v_t, v0, p.V, a.do_vec && p.v_vec);
-      if (v0 == 0)
-        for (int x = threadIdx.x; x < kDeltaVectors<C>; x += THREADS)
-          lv[x] = p.vectors[at * kDeltaVectors<C> + x];
-      __syncthreads();
+      hide();
       const int c16 = 16 * wave, col = v0 + c16 + r;
-      f32x4 u[NT], y[NT];
+      // everything that the block needs from memory, before anything waits
+      Octets xo, xv;
+      load2(xo, xv, dout, a.do_t, v, p.v_t, v0, p.V, a.do_vec && p.v_vec);
+      const bool first = v0 == 0;
+      float vec = 0.f;
+      if (first) vec = p.vectors[at * kDeltaVectors<C> + min(tid, kDeltaVectors<C> - 1)];
+      static_assert(kDeltaVectors<C> <= THREADS || KP == 64, "a vector entry a thread");
+      f32x4 st[KT], y[NT];  // S0's columns, dR
+#pragma unroll
+      for (int t = 0; t < KT; ++t) st[t] = zero4();
+#pragma unroll
+      for (int t = 0; t < NT; ++t) y[t] = zero4();
+      state_columns<false>(st, s0, p.K, p.V, col, v0 + c16 + 16);
+      if (v0 + c16 < p.V) {
+        const f32x4* from = delta_row_tiles<C>(a.drows, at, p.V, (v0 + c16) / 16, lane);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) y[t] = from[64 * t];
+      }
+      constexpr int F16 = NF * kFragBytes / 16, FO = (F16 + THREADS - 1) / THREADS;
+      u32x4 nf[FO];
+      if (first) {
+        const u32x4* from = reinterpret_cast<const u32x4*>(p.frags + at * (3 * NF) * kFragBytes);
+#pragma unroll
+        for (int o = 0; o < FO; ++o) nf[o] = from[min(tid + o * THREADS, F16 - 1)];
+      }
+      __syncthreads();  // the last reads of dO, U, dR and the triangles
+      if (gh == 0 && first) stage2(l.k, l.q, x1, x2, 0, p.K);
+      stage2(l.dout, l.u, xo, xv, v0, p.V);  // V lies in U's place until U replaces it
+      if (first) {
+#pragma unroll
+        for (int o = 0; o < FO; ++o)
+          if (F16 % THREADS == 0 || tid + o * THREADS < F16)
+            reinterpret_cast<u32x4*>(l.f)[tid + o * THREADS] = nf[o];
+        for (int x = tid; x < kDeltaVectors<C>; x += THREADS)
+          l.v[x] = x == tid ? vec : p.vectors[at * kDeltaVectors<C> + x];
+      }
+      __syncthreads();
+      f32x4 u[NT], none[NT];
+      typename T::Exact vv[CS];
+      typename T::Split tri[NF];
+      rows_times_state<D, Rows, KS, NT, false>(l.k, l.q, st, u, none, lane, [&] {
+#pragma unroll
+        for (int c = 0; c < CS; ++c) vv[c] = Rows::cols(l.u, 32 * c, c16, lane);
+        load_triangle<D>(tri, l.f, lane);
+      });
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const f32x4 gam = lds4(l.v + 16 * t + 4 * g), bt = lds4(l.v + 2 * C + 16 * t + 4 * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = T::value(vv[t / 2], 4 * (t & 1) + e);
+          u[t][e] = bt[e] * (x - gam[e] * u[t][e]);
+          // rowsum(dR V), this wave's columns
+          const float sv = lanes_reduce<16>(y[t][e] * x, Add());
+          float* to = &l.part[wave][3][16 * t + 4 * g + e];
+          if (r == 0) *to = first ? sv : *to + sv;
+        }
+      }
       {
-        f32x4 x[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) x[t] = y[t] = zero4();
-#pragma unroll
-        for (int c = 0; c < KS; ++c) {
-          f32x4 w[2], z[2];
-#pragma unroll
-          for (int o = 0; o < 2; ++o)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = 32 * c + 16 * o + 4 * g + e;
-              const bool in = k < p.K && col < p.V;
-              w[o][e] = in ? s0[(int64_t)k * p.V + col] : 0.f;
-              z[o][e] = in ? ds[(int64_t)k * p.V + col] : 0.f;
-            }
-          const auto sw = T::split(w[0], w[1]), sz = T::split(z[0], z[1]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const auto kf = Rows::rows(lk, 16 * t, 32 * c, lane);
-            x[t] = T::mul(kf, sw, x[t]);
-            y[t] = T::mul(kf, sz, y[t]);
-          }
-        }
-        f32x4 vv[NT];
-#pragma unroll
-        for (int c = 0; c < CS; ++c) {
-          const auto w = Rows::cols(lu, 32 * c, c16, lane);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) vv[2 * c + e / 4][e % 4] = T::value(w, e);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          u[t] = lds4(lv + 2 * C + 16 * t + 4 * g) * (vv[t] - lds4(lv + 16 * t + 4 * g) * x[t]);
         typename T::Split us[CS];
 #pragma unroll
         for (int c = 0; c < CS; ++c) us[c] = T::split(u[2 * c], u[2 * c + 1]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int c = 0; c <= t / 2; ++c)
-            u[t] = T::mul(T::get(frags + lower_frag<C>(t, c) * kFragBytes, lane), us[c], u[t]);
-        // dU
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          y[t] *= lds4(lv + C + 16 * t + 4 * g);
-#pragma unroll
-          for (int c = t / 2; c < CS; ++c)
-            y[t] = T::mul(T::get(frags + (2 * NF + upper_frag<C>(t, c)) * kFragBytes, lane),
-                          Rows::cols(ldo, 32 * c, c16, lane), y[t]);
-        }
-#pragma unroll
-        for (int c = 0; c < CS; ++c) us[c] = T::split(y[2 * c], y[2 * c + 1]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-          for (int c = t / 2; c < CS; ++c)
-            y[t] = T::mul(T::get(frags + (NF + upper_frag<C>(t, c)) * kFragBytes, lane), us[c], y[t]);
-          rv[t] += y[t] * vv[t];
-        }
+        triangle_times<D, true>(tri, us, u);
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const f32x4 bt = lds4(lv + 2 * C + 16 * t + 4 * g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int x = 16 * t + 4 * g + e;
-          put_split(lu, BIG, x * Rows::LD + Rows::pos(c16 + r), u[t][e]);
-          put_split(lr, BIG, x * Rows::LD + Rows::pos(c16 + r), y[t][e]);
-          if (x < ch.len && col < p.V) dv[(int64_t)x * a.dv_t + col] = delta_round<D>(bt[e] * y[t][e]);
-        }
-      }
-      __syncthreads();
-      // products over this block's columns
+      // the first step's rows of S0 and dS1 are on their way over the barrier
       const int steps = (min(KP, p.V - v0) + 31) / 32;
-      for (int c = 0; c < steps; ++c) {
-        f32x4 w[2], z[2];
+      f32x4 w[2][2], z[2][2];
+      const int kidx = 16 * wave + r;  // this lane's channel of K
+      auto load_states = [&](int c) {
+        const int64_t base = (int64_t)min(kidx, p.K - 1) * p.V;
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
           const int vc = v0 + 32 * c + 16 * o + 4 * g;
-          w[o] = z[o] = zero4();
-          if (kidx < p.K) {
-            const int64_t i = (int64_t)kidx * p.V + vc;
-            if (p.V % 4 == 0) {
-              if (vc < p.V) w[o] = lds4(s0 + i), z[o] = lds4(ds + i);
-            } else {
+          if (rows4) {
+            const int64_t i = base + min(vc, p.V - 4);
+            w[c & 1][o] = lds4(s0 + i), z[c & 1][o] = lds4(ds + i);
+          } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (vc + e < p.V) w[o][e] = s0[i + e], z[o][e] = ds[i + e];
+            for (int e = 0; e < 4; ++e) {
+              const int64_t i = base + min(vc + e, p.V - 1);
+              w[c & 1][o][e] = s0[i], z[c & 1][o][e] = ds[i];
             }
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dot = fmaf(w[o][e], z[o][e], dot);
         }
-        const auto sw = T::split(w[0], w[1]), sz = T::split(z[0], z[1]);
+      };
+      load_states(0);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = (16 * t + 4 * g + e) * Rows::LD + Rows::pos(c16 + r);
+          put_split(l.u, BIG, i, u[t][e]);
+          put_split(l.r, BIG, i, y[t][e]);
+        }
+      __syncthreads();
+      put_tile(static_cast<S*>(a.dv) + ch.t0 * a.dv_t + h * a.dv_h, a.dv_t, v0, p.V, a.dv_vec,
+               [&](int t, int c0) {
+                 const float bt = l.v[2 * C + t];
+                 S o[8];
+                 const auto hi = Rows::get8(l.r, t, c0);
+                 if constexpr (kB) {
+                   const auto lo = Rows::get8(l.r + BIG, t, c0);
+#pragma unroll
+                   for (int e = 0; e < 8; ++e) o[e] = delta_round<D>(bt * (T::value(hi, e) + T::value(lo, e)));
+                 } else {
+#pragma unroll
+                   for (int e = 0; e < 8; ++e) o[e] = bt * T::value(hi, e);
+                 }
+                 return T::join(o);
+               });
+      // products over this block's columns
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        if (c >= steps) break;
+        if (c + 1 < steps) load_states(c + 1);
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool in = kidx < p.K && v0 + 32 * c + 16 * o + 4 * g + e < p.V;
+            const float x = in ? w[c & 1][o][e] : 0.f, x2 = in ? z[c & 1][o][e] : 0.f;
+            dot = fmaf(x, x2, dot);
+            w[c & 1][o][e] = x, z[c & 1][o][e] = x2;
+          }
+        const auto sw = T::split(w[c & 1][0], w[c & 1][1]), sz = T::split(z[c & 1][0], z[c & 1][1]);
+        typename T::Exact fo[2];
+        typename T::Split fr[2], fu[2];
+        auto load_rows = [&](int t) {
+          fo[t & 1] = Rows::rows(l.dout, 16 * t, 32 * c, lane);
+          fr[t & 1] = rows2(l.r, 16 * t, 32 * c);
+          fu[t & 1] = rows2(l.u, 16 * t, 32 * c);
+        };
+        load_rows(0);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          mq[t] = T::mul(Rows::rows(ldo, 16 * t, 32 * c, lane), sw, mq[t]);
-          mz[t] = T::mul(rows2(lr, 16 * t, 32 * c), sw, mz[t]);
-          mw[t] = T::mul(rows2(lu, 16 * t, 32 * c), sz, mw[t]);
+          if (t + 1 < NT) load_rows(t + 1);
+          keep_order();
+          each_part<T::kSplitSplit>([&](auto P) {
+            if constexpr (P < T::kExactSplit) mq[t] = T::template part<P>(fo[t & 1], sw, mq[t]);
+            mz[t] = T::template part<P>(fr[t & 1], sw, mz[t]);
+            mw[t] = T::template part<P>(fu[t & 1], sz, mw[t]);
+          });
+          keep_order();
         }
       }
-      int I = 0, J = 0, n = 0;
 #pragma unroll
       for (int m = 0; m < MINE; ++m) {
         const int want = wave + m * NW;
         if (want >= TILES) break;
-        for (; n < want; ++n) J == I ? (++I, J = 0) : ++J;
+        const int I = tile_row(want), J = want - I * (I + 1) / 2;
         for (int c = 0; c < steps; ++c) {
-          const auto uf = rows2(lu, 16 * J, 32 * c);
-          ep[m] = T::mul(Rows::rows(ldo, 16 * I, 32 * c, lane), uf, ep[m]);
-          ea[m] = T::mul(rows2(lr, 16 * I, 32 * c), uf, ea[m]);
+          const auto uf = rows2(l.u, 16 * J, 32 * c), rf = rows2(l.r, 16 * I, 32 * c);
+          const auto of = Rows::rows(l.dout, 16 * I, 32 * c, lane);
+          each_part<T::kSplitSplit>([&](auto P) {
+            if constexpr (P < T::kExactSplit) ep[m] = T::template part<P>(of, uf, ep[m]);
+            ea[m] = T::template part<P>(rf, uf, ea[m]);
+          });
         }
       }
     }
     __syncthreads();
+    hide();
     // the triangles, with zeros above the diagonal of every 32 columns
     {
-      int I = 0, J = 0, n = 0;
 #pragma unroll
       for (int m = 0; m < MINE; ++m) {
         const int want = wave + m * NW;
         if (want >= TILES) break;
-        for (; n < want; ++n) J == I ? (++I, J = 0) : ++J;
+        const int I = tile_row(want), J = want - I * (I + 1) / 2;
         const int j = 16 * J + r;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = 16 * I + 4 * g + e, x = i * Tri::LD + Tri::pos(j);
           float dec = 0.f;
-          if (i >= j) dec = expf((lv[3 * C + i] - lv[3 * C + j]) + (lv[4 * C + i] - lv[4 * C + j]));
+          if (i >= j) dec = expf((l.v[3 * C + i] - l.v[3 * C + j]) + (l.v[4 * C + i] - l.v[4 * C + j]));
           const float pv = i >= j ? p.scale * dec * ep[m][e] : 0.f;
           const float av = i > j ? dec * ea[m][e] : 0.f;
-          put_split(le, SMALL, x, pv);
-          put_split(le + PARTS * SMALL, SMALL, x, av);
-          put_split(le + 2 * PARTS * SMALL, SMALL, x, lv[2 * C + i] * av);
+          put_split(l.e, SMALL, x, pv);
+          put_split(l.e + PARTS * SMALL, SMALL, x, av);
+          put_split(l.e + 2 * PARTS * SMALL, SMALL, x, l.v[2 * C + i] * av);
         }
         if (I == J && I % 2 == 0) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int x = (16 * I + 4 * g + e) * Tri::LD + Tri::pos(j + 16);
 #pragma unroll
-            for (int o = 0; o < 3; ++o) put_split(le + o * PARTS * SMALL, SMALL, x, 0.f);
+            for (int o = 0; o < 3; ++o) put_split(l.e + o * PARTS * SMALL, SMALL, x, 0.f);
           }
         }
       }
     }
-    __syncthreads();
-    f32x4 w[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const f32x4 gam = lds4(lv + 16 * t + 4 * g);
+      const f32x4 gam = lds4(l.v + 16 * t + 4 * g);
       mq[t] *= p.scale * gam;
       mz[t] *= gam;
-      mw[t] *= lds4(lv + C + 16 * t + 4 * g);
-      w[t] = zero4();
+      mw[t] *= lds4(l.v + C + 16 * t + 4 * g);
     }
+    __syncthreads();
+    f32x4 w[NT], neg[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) w[t] = neg[t] = zero4();
 #pragma unroll
     for (int c = 0; c < CS; ++c) {
-      const auto kf = Rows::cols(lk, 32 * c, 16 * wave, lane), qf = Rows::cols(lq, 32 * c, 16 * wave, lane);
+      const auto kf = Rows::cols(l.k, 32 * c, 16 * wave, lane), qf = Rows::cols(l.q, 32 * c, 16 * wave, lane);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         if (c <= t / 2) {
-          mq[t] = T::mul(tri_rows(le, 16 * t, 32 * c), kf, mq[t]);
-          mz[t] = T::mul(tri_rows(le + PARTS * SMALL, 16 * t, 32 * c), kf, mz[t]);
+          const auto x = tri_rows(l.e, 16 * t, 32 * c), y = tri_rows(l.e + PARTS * SMALL, 16 * t, 32 * c);
+          each_part<T::kSplitExact>([&](auto P) {
+            mq[t] = T::template part<P>(x, kf, mq[t]);
+            mz[t] = T::template part<P>(y, kf, mz[t]);
+          });
         }
         if (c >= t / 2) {
-          f32x4 neg = T::mul(tri_cols(le + 2 * PARTS * SMALL, 32 * c, 16 * t), kf, zero4());
-          w[t] = T::mul(tri_cols(le, 32 * c, 16 * t), qf, w[t] - neg);
+          const auto x = tri_cols(l.e, 32 * c, 16 * t), y = tri_cols(l.e + 2 * PARTS * SMALL, 32 * c, 16 * t);
+          each_part<T::kSplitExact>([&](auto P) {
+            w[t] = T::template part<P>(x, qf, w[t]);
+            neg[t] = T::template part<P>(y, kf, neg[t]);
+          });
         }
       }
     }
     // rows' sums over this wave's channels, and the sums over value heads
+    const bool last = gh + 1 == p.group;
+    const int kidx = 16 * wave + r;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const f32x4 bt = lds4(lv + 2 * C + 16 * t + 4 * g);
+      const f32x4 bt = lds4(l.v + 2 * C + 16 * t + 4 * g);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int x = 16 * t + 4 * g + e, i = x * Rows::LD + Rows::pos(kidx);
-        const float kv = to_float<D>(lk[i]), qv = to_float<D>(lq[i]);
-        const float kz = kv * mz[t][e];
-        const float own = sum16(qv * mq[t][e] - bt[e] * kz - kv * w[t][e]);
-        const float km = sum16(kv * mw[t][e]), sz = sum16(kz), sv = sum16(rv[t][e]);
-        if (r == 0) {
-          float* to = part + wave * 4 * C + x;
-          to[0] = own, to[C] = km, to[2 * C] = sz, to[3 * C] = sv;
+        const float kv = to_float<D>(l.k[i]), qv = to_float<D>(l.q[i]);
+        const float kz = kv * mz[t][e], wv = w[t][e] - neg[t][e];
+        const float own = lanes_reduce<16>(qv * mq[t][e] - bt[e] * kz - kv * wv, Add());
+        const float km = lanes_reduce<16>(kv * mw[t][e], Add()), sz = lanes_reduce<16>(kz, Add());
+        if (r == 0) l.part[wave][0][x] = own, l.part[wave][1][x] = km, l.part[wave][2][x] = sz;
+        const float gk = mw[t][e] + wv - bt[e] * mz[t][e];
+        if constexpr (GROUPED) {
+          dq[t][e] += mq[t][e];
+          dk[t][e] += gk;
+        } else {
+          // this wave's channels of K and Q have been read for the last time
+          l.q[i] = delta_round<D>(mq[t][e]);
+          l.k[i] = delta_round<D>(gk);
         }
-        dq[t][e] += mq[t][e];
-        dk[t][e] += mw[t][e] + w[t][e] - bt[e] * mz[t][e];
+        if (GROUPED && last) {
+          l.q[i] = delta_round<D>(dq[t][e]);
+          l.k[i] = delta_round<D>(dk[t][e]);
+        }
       }
     }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d, 64);
-    if (lane == 0) dots[wave] = dot;
+    dot = lanes_reduce<64>(dot, Add());
+    if (lane == 0) l.dots[wave] = dot;
     __syncthreads();
     if (wave == 0) {
       const int t = lane;
       float own = 0.f, km = 0.f, sz = 0.f, sv = 0.f, all = 0.f;
+#pragma unroll
       for (int n = 0; n < NW; ++n) {
-        const float* from = part + n * 4 * C + (t < C ? t : 0);
-        own += from[0], km += from[C], sz += from[2 * C], sv += from[3 * C];
-        all += dots[n];
+        const int x = t < C ? t : 0;
+        own += l.part[n][0][x], km += l.part[n][1][x], sz += l.part[n][2][x], sv += l.part[n][3][x];
+        all += l.dots[n];
       }
       if (t >= C) own = km = 0.f;
       double before = km, after = own;
@@ -486,10 +558,10 @@ __global__ __launch_bounds__(4 * KP, KP == 128 ? 2 : 1) void delta_grad_kernel(D
         if (lane + d < 64) after += y2;
       }
       if (t < ch.len) {
-        float dg = (float)(after + (before - km) + (double)lv[C - 1] * all);
+        float dg = (float)(after + (before - km) + (double)l.v[C - 1] * all);
         const float db = sv - sz;
         // behind a closed gate the parts cancel but for their roundings
-        const float gt = lv[3 * C + t] + lv[4 * C + t] - (t ? lv[3 * C + t - 1] + lv[4 * C + t - 1] : 0.f);
+        const float gt = l.v[3 * C + t] + l.v[4 * C + t] - (t ? l.v[3 * C + t - 1] + l.v[4 * C + t - 1] : 0.f);
         if (gt < -104.f) dg = 0.f;  // e^g is zero in fp32
         const int64_t tok = ch.t0 + t;
         if (p.gates_f32) {
@@ -502,18 +574,11 @@ __global__ __launch_bounds__(4 * KP, KP == 128 ? 2 : 1) void delta_grad_kernel(D
       }
     }
   }
-  S* oq = static_cast<S*>(a.dq) + (int64_t)ch.t0 * a.dq_t + kh * a.dq_h + kidx;
-  S* ok = static_cast<S*>(a.dk) + (int64_t)ch.t0 * a.dk_t + kh * a.dk_h + kidx;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int x = 16 * t + 4 * g + e;
-      if (x < ch.len && kidx < p.K) {
-        oq[(int64_t)x * a.dq_t] = delta_round<D>(dq[t][e]);
-        ok[(int64_t)x * a.dk_t] = delta_round<D>(dk[t][e]);
-      }
-    }
+  // the barrier above also ends the writes of the tiles below
+  put_tile(static_cast<S*>(a.dq) + ch.t0 * a.dq_t + kh * a.dq_h, a.dq_t, 0, p.K, a.dqk_vec,
+           [&](int t, int c0) { return Rows::get8(l.q, t, c0); });
+  put_tile(static_cast<S*>(a.dk) + ch.t0 * a.dk_t + kh * a.dk_h, a.dk_t, 0, p.K, a.dqk_vec,
+           [&](int t, int c0) { return Rows::get8(l.k, t, c0); });
 }
 
 template <typename D, int KP>
@@ -530,8 +595,11 @@ static int delta_backward(const DeltaBwd& a, int64_t rows, hipStream_t stream) {
     hipLaunchKernelGGL((delta_back_kernel<D, KP, 4>), dim3((p.V + 63) / 64, p.heads, p.batch),
                        dim3(256), 0, stream, a);
   if (int rc = check_launch(what)) return rc;
-  hipLaunchKernelGGL((delta_grad_kernel<D, KP>), dim3((uint32_t)rows, p.heads / p.group),
-                     dim3(4 * KP), 0, stream, a);
+  const dim3 chunks((uint32_t)rows, p.heads / p.group), threads(4 * KP);
+  if (p.group > 1)
+    hipLaunchKernelGGL((delta_grad_kernel<D, KP, true>), chunks, threads, 0, stream, a);
+  else
+    hipLaunchKernelGGL((delta_grad_kernel<D, KP, false>), chunks, threads, 0, stream, a);
   return check_launch(what);
 }
 
@@ -602,6 +670,7 @@ extern "C" int gated_delta_rule_varlen_bwd(
   if (int rc = delta_disjoint(c, a.p, {oq, ok, ov, og, ob, di, work})) return rc;
   a.p.vectors = workspace;
   a.p.frags = reinterpret_cast<char*>(workspace + s.vectors);
+  a.drows = workspace + s.bwd_rows;
   a.dstates = workspace + s.bwd_states;
   a.dout = dout, a.do_t = do_stride_t, a.do_h = do_stride_h;
   a.marks = checkpoints, a.dfinal = dfinal_states, a.df_slot = df_stride_slot;
@@ -611,7 +680,10 @@ extern "C" int gated_delta_rule_varlen_bwd(
   a.dv = dv, a.dv_t = dv_stride_t, a.dv_h = dv_stride_h;
   a.dg = dg, a.dg_t = dg_stride_t, a.dg_h = dg_stride_h;
   a.db = dbeta, a.db_t = db_stride_t, a.db_h = db_stride_h;
-  a.do_vec = delta_vec(dout, do_stride_t, do_stride_h, V, 16 / elem_size(dtype));
+  const int64_t n = 16 / elem_size(dtype);
+  a.do_vec = delta_vec(dout, do_stride_t, do_stride_h, V, n);
+  a.dv_vec = delta_vec(dv, dv_stride_t, dv_stride_h, V, n);
+  a.dqk_vec = delta_vec(dq, dq_stride_t, dq_stride_h, K, n) && delta_vec(dk, dk_stride_t, dk_stride_h, K, n);
   if (dtype == SCONV_BF16)
     return K <= 64 ? delta_backward<Bf16, 64>(a, rows, stream) : delta_backward<Bf16, 128>(a, rows, stream);
   return K <= 64 ? delta_backward<F32, 64>(a, rows, stream) : delta_backward<F32, 128>(a, rows, stream);
