@@ -83,9 +83,9 @@ inline bool delta_overlap(const DeltaBuffer& a, const DeltaBuffer& b) {
   return d < a.run || a.step - d < b.run;
 }
 
-// Rows of whole 16-byte vectors of n elements.
+// Rows of whole 16-byte vectors of n elements, a chunk's rows within 2^31 bytes.
 inline bool delta_vec(const void* t, int64_t st, int64_t sh, int64_t width, int64_t n) {
-  return aligned16(t) && st % n == 0 && sh % n == 0 && width % n == 0;
+  return aligned16(t) && st % n == 0 && sh % n == 0 && width % n == 0 && st < (1 << 22);
 }
 
 inline int delta_inputs(const DeltaCall& c, DeltaParams& p, const void* q, int64_t q_t, int64_t q_h,

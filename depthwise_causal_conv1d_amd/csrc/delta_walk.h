@@ -34,50 +34,90 @@ template <typename D, int KP, int NW> struct WalkStage {
   u32x4 f[FO];
   float v;
 
-  // tk, tq, tx: the heads' first rows; the chunk's rows are t0 .. end - 1.
-  // vec: K's, Q's and x's rows are of 16-byte vectors.
+  // Whole chunks of whole rows: a row is a uniform address and a lane's 32-bit
+  // offset, and nothing is masked (a third of the walk's vector instructions
+  // were addresses and masks).
+  uint32_t k_off, q_off, x_off;
+  static constexpr int KR = THREADS / (KP / 8), XR = THREADS / XW;  // rows of one piece a thread
+
+  const S *tk, *tq, *tx;  // the heads' first rows
+  int64_t x_t;
+  int32_t col0;
+  bool vec, whole;  // rows of 16-byte vectors; no row ends inside the tiles
+
+  __device__ __forceinline__ void init(const DeltaParams& p, const S* k_, const S* q_, const S* x_,
+                                       int64_t x_t_, bool vec_, int32_t col0_) {
+    tk = k_, tq = q_, tx = x_, x_t = x_t_, vec = vec_, col0 = col0_;
+    whole = vec && p.K == KP && col0 + 16 * NW <= p.V && KN % THREADS == 0;
+    const int t = threadIdx.x / (KP / 8), c0 = threadIdx.x % (KP / 8) * 8, es = sizeof(S);
+    k_off = (uint32_t)(t * p.k_t + c0) * es;
+    q_off = (uint32_t)(t * p.q_t + c0) * es;
+    x_off = (uint32_t)(threadIdx.x / XW * x_t + threadIdx.x % XW * 8 + col0) * es;
+  }
+  // The other chunks.  Where the thread's number comes from is hidden, or all
+  // these addresses would be made ahead of the loop and held there.
   template <bool VEC>
-  __device__ __forceinline__ void fetch_rows(const DeltaParams& p, const S* tk, const S* tq,
-                                             const S* tx, int64_t x_t, int32_t col0, int32_t t0,
-                                             int32_t end) {
+  __device__ __forceinline__ void fetch_rows(const DeltaParams& p, int32_t t0, int32_t end) {
+    const int tid = (int)lane_offset(threadIdx.x);
 #pragma unroll
     for (int o = 0; o < KO; ++o) {
-      const int i = threadIdx.x + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
+      const int i = tid + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
       k[o] = load8<D, VEC>(tk + t0 * p.k_t, p.k_t, t, end - t0, c0, p.K);
       q[o] = load8<D, VEC>(tq + t0 * p.q_t, p.q_t, t, end - t0, c0, p.K);
     }
 #pragma unroll
     for (int o = 0; o < XO; ++o) {
-      const int i = threadIdx.x + o * THREADS, t = i / XW, c0 = i % XW * 8;
+      const int i = tid + o * THREADS, t = i / XW, c0 = i % XW * 8;
       x[o] = load8<D, VEC>(tx + t0 * x_t, x_t, t, end - t0, col0 + c0, p.V);
     }
   }
-  __device__ __forceinline__ void fetch(const DeltaParams& p, const S* tk, const S* tq, const S* tx,
-                                        int64_t x_t, bool vec, int32_t col0, int32_t t0,
-                                        int32_t end, const char* frags, const float* vectors) {
-    if (vec) fetch_rows<true>(p, tk, tq, tx, x_t, col0, t0, end);
-    else fetch_rows<false>(p, tk, tq, tx, x_t, col0, t0, end);
-    const u32x4* from = reinterpret_cast<const u32x4*>(frags);
+  static __device__ __forceinline__ E at(const S* row, uint32_t off) {
+    const S* m = in_row(row, off);
+    if constexpr (sizeof(S) == 2) return {__builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(m))};
+    else return {*reinterpret_cast<const f32x4*>(m), *reinterpret_cast<const f32x4*>(m + 4)};
+  }
+  // The chunk's rows are t0 .. end - 1.
+  __device__ __forceinline__ void fetch(const DeltaParams& p, int32_t t0, int32_t end,
+                                        const char* frags, const float* vectors) {
+    if (whole && t0 + C <= end) {
 #pragma unroll
-    for (int o = 0; o < FO; ++o) f[o] = from[threadIdx.x + o * THREADS];
-    v = vectors[threadIdx.x < 3 * C ? threadIdx.x : 0];
+      for (int o = 0; o < KO; ++o) {
+        k[o] = at(tk + (t0 + o * KR) * p.k_t, k_off);
+        q[o] = at(tq + (t0 + o * KR) * p.q_t, q_off);
+      }
+#pragma unroll
+      for (int o = 0; o < XO; ++o) x[o] = at(tx + (t0 + o * XR) * x_t, x_off);
+    } else if (vec) {
+      fetch_rows<true>(p, t0, end);
+    } else {
+      fetch_rows<false>(p, t0, end);
+    }
+#pragma unroll
+    for (int o = 0; o < FO; ++o)
+      f[o] = *reinterpret_cast<const u32x4*>(in_row(frags + o * THREADS * 16, threadIdx.x * 16u));
+    v = *in_row(vectors, (threadIdx.x < 3 * C ? threadIdx.x : 0) * 4u);
   }
   // len: tokens of the chunk
-  __device__ __forceinline__ void stage(L& l, const DeltaParams& p, int32_t col0, int32_t len) const {
+  template <bool MASK> __device__ __forceinline__ void stage_rows(L& l, const DeltaParams& p, int32_t len) const {
+    const int tid = MASK ? (int)lane_offset(threadIdx.x) : threadIdx.x;
 #pragma unroll
     for (int o = 0; o < KO; ++o) {
-      const int i = threadIdx.x + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
+      const int i = tid + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
       const int n = t < len ? p.K - c0 : 0;
       if (KN % THREADS == 0 || i < KN) {
-        L::Rows::put8(l.k, t, c0, mask8<D>(k[o], n));
-        L::Rows::put8(l.q, t, c0, mask8<D>(q[o], n));
+        L::Rows::put8(l.k, t, c0, MASK ? mask8<D>(k[o], n) : k[o]);
+        L::Rows::put8(l.q, t, c0, MASK ? mask8<D>(q[o], n) : q[o]);
       }
     }
 #pragma unroll
     for (int o = 0; o < XO; ++o) {
-      const int i = threadIdx.x + o * THREADS, t = i / XW, c0 = i % XW * 8;
-      L::Cols::put8(l.x, t, c0, mask8<D>(x[o], t < len ? p.V - col0 - c0 : 0));
+      const int i = tid + o * THREADS, t = i / XW, c0 = i % XW * 8;
+      L::Cols::put8(l.x, t, c0, MASK ? mask8<D>(x[o], t < len ? p.V - col0 - c0 : 0) : x[o]);
     }
+  }
+  __device__ __forceinline__ void stage(L& l, const DeltaParams& p, int32_t len) const {
+    if (whole && len >= C) stage_rows<false>(l, p, len);
+    else stage_rows<true>(l, p, len);
 #pragma unroll
     for (int o = 0; o < FO; ++o) reinterpret_cast<u32x4*>(l.f)[threadIdx.x + o * THREADS] = f[o];
     if (threadIdx.x < 3 * C) l.v[threadIdx.x] = v;

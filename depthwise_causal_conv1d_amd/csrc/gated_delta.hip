@@ -51,18 +51,26 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a)
   S* out = static_cast<S*>(a.out) + h * a.o_h;
   const int32_t row0 = start / C + b;
   Stage next;
+  next.init(p, k, q, v, p.v_t, p.qk_vec && p.v_vec, cols0);
   auto fetch = [&](int32_t i) {
     const int64_t at = (int64_t)(row0 + i) * p.heads + h;
-    next.fetch(p, k, q, v, p.v_t, p.qk_vec && p.v_vec, cols0, start + i * C, end,
-               p.frags + at * (2 * NF) * kFragBytes, p.vectors + at * kDeltaVectors<C>);
+    next.fetch(p, start + i * C, end, p.frags + at * (2 * NF) * kFragBytes,
+               p.vectors + at * kDeltaVectors<C>);
   };
+  const uint32_t o_off = (uint32_t)(threadIdx.x / Stage::XW * a.o_t + threadIdx.x % Stage::XW * 8 + cols0) * sizeof(S);
   auto put_out = [&](int32_t i) {
     const int32_t t0 = start + i * C;
+    const bool whole = next.whole && a.o_vec && t0 + C <= end;
 #pragma unroll
     for (int o = 0; o < Stage::XO; ++o) {
-      const int x = threadIdx.x + o * Stage::THREADS, t = x / Stage::XW, c0 = x % Stage::XW * 8;
-      if (t < end - t0)
-        put_row8<D>(out + (int64_t)(t0 + t) * a.o_t, cols0 + c0, p.V, a.o_vec, Cols::get8(l.x, t, c0));
+      const int x = threadIdx.x + o * Stage::THREADS;
+      const auto y = Cols::get8(l.x, x / Stage::XW, x % Stage::XW * 8);
+      if (whole) {
+        put_row8<D>(in_row(out + (t0 + o * Stage::XR) * a.o_t, o_off), 0, 8, true, y);
+      } else {
+        const int z = (int)lane_offset(x), t = z / Stage::XW, c0 = z % Stage::XW * 8;
+        if (t < end - t0) put_row8<D>(out + (int64_t)(t0 + t) * a.o_t, cols0 + c0, p.V, a.o_vec, y);
+      }
     }
   };
   const int32_t chunks = (end - start + C - 1) / C;
@@ -70,7 +78,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a)
   for (int32_t i = 0; i < chunks; ++i) {
     __syncthreads();
     if (i > 0) put_out(i - 1);
-    next.stage(l, p, cols0, end - (start + i * C));
+    next.stage(l, p, end - (start + i * C));
     __syncthreads();
     if (i + 1 < chunks) fetch(i + 1);
     if (a.marks)

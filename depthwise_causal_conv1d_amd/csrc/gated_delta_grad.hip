@@ -75,16 +75,17 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_back_kernel(DeltaBwd a)
   const S* dout = static_cast<const S*>(a.dout) + h * a.do_h;
   const int32_t row0 = start / C + b;
   Stage next;
+  next.init(p, k, q, dout, a.do_t, p.qk_vec && a.do_vec, cols0);
   auto fetch = [&](int32_t i) {
     const int64_t at = (int64_t)(row0 + i) * p.heads + h;
-    next.fetch(p, k, q, dout, a.do_t, p.qk_vec && a.do_vec, cols0, start + i * C, end,
-               p.frags + (at * (3 * NF) + NF) * kFragBytes, p.vectors + at * kDeltaVectors<C>);
+    next.fetch(p, start + i * C, end, p.frags + (at * (3 * NF) + NF) * kFragBytes,
+               p.vectors + at * kDeltaVectors<C>);
   };
   const int32_t chunks = (end - start + C - 1) / C;
   if (chunks > 0) fetch(chunks - 1);
   for (int32_t i = chunks - 1; i >= 0; --i) {
     __syncthreads();
-    next.stage(l, p, cols0, end - (start + i * C));
+    next.stage(l, p, end - (start + i * C));
     __syncthreads();
     if (i > 0) fetch(i - 1);
     state_columns<true>(s, a.dstates + ((int64_t)(row0 + i) * p.heads + h) * KV, p.K, p.V, col, ends);
