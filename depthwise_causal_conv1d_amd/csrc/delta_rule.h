@@ -305,11 +305,12 @@ __device__ __forceinline__ void put_row8(typename D::storage* row, int c0, int W
 
 // A matrix of W columns (a multiple of 32) in LDS, one row a token.  bf16 rows
 // keep, inside every 32 columns, the order of an operand (16 h + 4 g + e at
-// 8 g + 4 h + e), so that a lane's 8 entries are one 16-byte read; the pad
-// spreads 16 rows over all banks.
+// 8 g + 4 h + e), so that a lane's 8 entries are one 16-byte read.  The pad
+// of 32 bytes was the best of 0 to 128 for 16-byte and transposed reads together
+// (timed alone; at 16 bytes half the LDS time of a walk was conflicts).
 template <typename D, int W> struct LdsRows {
   using S = typename D::storage;
-  static constexpr int kPad = sizeof(S) == 2 ? 8 : 4;
+  static constexpr int kPad = sizeof(S) == 2 ? 16 : 4;
   static constexpr int LD = W + kPad;
 
   // where column c lies in a row
