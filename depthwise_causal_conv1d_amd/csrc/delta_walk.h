@@ -21,7 +21,7 @@ template <typename D, int KP, int NW> struct WalkLds {
   __attribute__((aligned(16))) float v[3 * C];
 };
 
-template <typename D, int KP, int NW> struct WalkStage {
+template <typename D, int KP, int NW, bool VEC> struct WalkStage {
   using L = WalkLds<D, KP, NW>;
   using S = typename D::storage;
   using E = typename Tile<D>::Exact;
@@ -34,63 +34,66 @@ template <typename D, int KP, int NW> struct WalkStage {
   u32x4 f[FO];
   float v;
 
-  // Whole chunks of whole rows: a row is a uniform address and a lane's 32-bit
-  // offset, and nothing is masked (a third of the walk's vector instructions
-  // were addresses and masks).
-  uint32_t k_off, q_off, x_off;
-  static constexpr int KR = THREADS / (KP / 8), XR = THREADS / XW;  // rows of one piece a thread
-
+  // A thread's column of each tensor in bytes (fp32: of its second half too),
+  // made once; a chunk's rows end at `end`, and lanes behind it load its last.
+  uint32_t k_c[2], x_c[2];
   const S *tk, *tq, *tx;  // the heads' first rows
   int64_t x_t;
   int32_t col0;
-  bool vec, whole;  // rows of 16-byte vectors; no row ends inside the tiles
+  bool whole;  // no row ends inside the tiles
 
+  static __device__ __forceinline__ void columns(uint32_t (&c)[2], int c0, int W) {
+    c[0] = (uint32_t)(c0 < W ? c0 : 0) * (uint32_t)sizeof(S);
+    c[1] = (uint32_t)(c0 + 4 < W ? c0 + 4 : 0) * (uint32_t)sizeof(S);
+  }
   __device__ __forceinline__ void init(const DeltaParams& p, const S* k_, const S* q_, const S* x_,
-                                       int64_t x_t_, bool vec_, int32_t col0_) {
-    tk = k_, tq = q_, tx = x_, x_t = x_t_, vec = vec_, col0 = col0_;
-    whole = vec && p.K == KP && col0 + 16 * NW <= p.V && KN % THREADS == 0;
-    const int t = threadIdx.x / (KP / 8), c0 = threadIdx.x % (KP / 8) * 8, es = sizeof(S);
-    k_off = (uint32_t)(t * p.k_t + c0) * es;
-    q_off = (uint32_t)(t * p.q_t + c0) * es;
-    x_off = (uint32_t)(threadIdx.x / XW * x_t + threadIdx.x % XW * 8 + col0) * es;
+                                       int64_t x_t_, int32_t col0_) {
+    tk = k_, tq = q_, tx = x_, x_t = x_t_, col0 = col0_;
+    whole = p.K == KP && col0 + 16 * NW <= p.V;
+    columns(k_c, threadIdx.x % (KP / 8) * 8, p.K);
+    columns(x_c, col0 + threadIdx.x % XW * 8, p.V);
   }
-  // The other chunks.  Where the thread's number comes from is hidden, or all
-  // these addresses would be made ahead of the loop and held there.
-  template <bool VEC>
-  __device__ __forceinline__ void fetch_rows(const DeltaParams& p, int32_t t0, int32_t end) {
-    const int tid = (int)lane_offset(threadIdx.x);
-#pragma unroll
-    for (int o = 0; o < KO; ++o) {
-      const int i = tid + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
-      k[o] = load8<D, VEC>(tk + t0 * p.k_t, p.k_t, t, end - t0, c0, p.K);
-      q[o] = load8<D, VEC>(tq + t0 * p.q_t, p.q_t, t, end - t0, c0, p.K);
-    }
-#pragma unroll
-    for (int o = 0; o < XO; ++o) {
-      const int i = tid + o * THREADS, t = i / XW, c0 = i % XW * 8;
-      x[o] = load8<D, VEC>(tx + t0 * x_t, x_t, t, end - t0, col0 + c0, p.V);
-    }
+  static __device__ __forceinline__ E at(const S* rows, uint32_t row, const uint32_t (&c)[2]) {
+    if constexpr (sizeof(S) == 2)
+      return {__builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(in_row(rows, row + c[0])))};
+    else
+      return {*reinterpret_cast<const f32x4*>(in_row(rows, row + c[0])),
+              *reinterpret_cast<const f32x4*>(in_row(rows, row + c[1]))};
   }
-  static __device__ __forceinline__ E at(const S* row, uint32_t off) {
-    const S* m = in_row(row, off);
-    if constexpr (sizeof(S) == 2) return {__builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(m))};
-    else return {*reinterpret_cast<const f32x4*>(m), *reinterpret_cast<const f32x4*>(m + 4)};
-  }
-  // The chunk's rows are t0 .. end - 1.
+  // The chunk's rows are t0 .. end - 1.  One path of loads: where paths with
+  // loads meet, the compiler waits for those of either, and on this machine a
+  // wait for loads is one for stores as well (4000 of a chunk's 13000 cycles).
   __device__ __forceinline__ void fetch(const DeltaParams& p, int32_t t0, int32_t end,
                                         const char* frags, const float* vectors) {
-    if (whole && t0 + C <= end) {
+    const S *rk = tk + t0 * p.k_t, *rq = tq + t0 * p.q_t, *rx = tx + t0 * x_t;
+    const int32_t last = end - t0 - 1;
+    if constexpr (VEC) {
+      const uint32_t es = sizeof(S);
 #pragma unroll
       for (int o = 0; o < KO; ++o) {
-        k[o] = at(tk + (t0 + o * KR) * p.k_t, k_off);
-        q[o] = at(tq + (t0 + o * KR) * p.q_t, q_off);
+        const uint32_t t = min((int)(threadIdx.x + o * THREADS) / (KP / 8), last);
+        k[o] = at(rk, t * (uint32_t)p.k_t * es, k_c);
+        q[o] = at(rq, t * (uint32_t)p.q_t * es, k_c);
       }
 #pragma unroll
-      for (int o = 0; o < XO; ++o) x[o] = at(tx + (t0 + o * XR) * x_t, x_off);
-    } else if (vec) {
-      fetch_rows<true>(p, t0, end);
+      for (int o = 0; o < XO; ++o) {
+        const uint32_t t = min((int)(threadIdx.x + o * THREADS) / XW, last);
+        x[o] = at(rx, t * (uint32_t)x_t * es, x_c);
+      }
     } else {
-      fetch_rows<false>(p, t0, end);
+      // hidden, or all these addresses would be made ahead of the loop and held
+      const int tid = (int)lane_offset(threadIdx.x);
+#pragma unroll
+      for (int o = 0; o < KO; ++o) {
+        const int i = tid + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
+        k[o] = load8<D, false>(rk, p.k_t, t, last + 1, c0, p.K);
+        q[o] = load8<D, false>(rq, p.q_t, t, last + 1, c0, p.K);
+      }
+#pragma unroll
+      for (int o = 0; o < XO; ++o) {
+        const int i = tid + o * THREADS, t = i / XW, c0 = i % XW * 8;
+        x[o] = load8<D, false>(rx, x_t, t, last + 1, col0 + c0, p.V);
+      }
     }
 #pragma unroll
     for (int o = 0; o < FO; ++o)
@@ -123,6 +126,10 @@ template <typename D, int KP, int NW> struct WalkStage {
     if (threadIdx.x < 3 * C) l.v[threadIdx.x] = v;
   }
 };
+
+// Ends what is in flight: loads ahead of a loop would make their registers'
+// first use inside it a wait for the loop's own.
+__device__ __forceinline__ void wait_for_all() { __builtin_amdgcn_s_waitcnt(0); }
 
 // A wave's 16 columns of a K x V matrix in memory and in accumulator tiles.  A
 // row is a uniform address and a lane's 32-bit offset: 64-bit addresses for

@@ -18,13 +18,13 @@ struct DeltaFwd {
 
 // One workgroup walks a sequence's chunks for one value head, 16 columns a
 // wave.  An output chunk waits in LDS, in V's place, for the next one's staging.
-template <typename D, int KP, int NW>
+template <typename D, int KP, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
   constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32;
   constexpr int NF = kDeltaFrags<C>;
-  using Stage = WalkStage<D, KP, NW>;
+  using Stage = WalkStage<D, KP, NW, VEC>;
   using Rows = typename Stage::L::Rows;
   using Cols = typename Stage::L::Cols;
   __shared__ typename Stage::L l;
@@ -51,29 +51,29 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a)
   S* out = static_cast<S*>(a.out) + h * a.o_h;
   const int32_t row0 = start / C + b;
   Stage next;
-  next.init(p, k, q, v, p.v_t, p.qk_vec && p.v_vec, cols0);
+  next.init(p, k, q, v, p.v_t, cols0);
   auto fetch = [&](int32_t i) {
     const int64_t at = (int64_t)(row0 + i) * p.heads + h;
     next.fetch(p, start + i * C, end, p.frags + at * (2 * NF) * kFragBytes,
                p.vectors + at * kDeltaVectors<C>);
   };
-  const uint32_t o_off = (uint32_t)(threadIdx.x / Stage::XW * a.o_t + threadIdx.x % Stage::XW * 8 + cols0) * sizeof(S);
   auto put_out = [&](int32_t i) {
     const int32_t t0 = start + i * C;
-    const bool whole = next.whole && a.o_vec && t0 + C <= end;
 #pragma unroll
     for (int o = 0; o < Stage::XO; ++o) {
-      const int x = threadIdx.x + o * Stage::THREADS;
-      const auto y = Cols::get8(l.x, x / Stage::XW, x % Stage::XW * 8);
-      if (whole) {
-        put_row8<D>(in_row(out + (t0 + o * Stage::XR) * a.o_t, o_off), 0, 8, true, y);
-      } else {
-        const int z = (int)lane_offset(x), t = z / Stage::XW, c0 = z % Stage::XW * 8;
-        if (t < end - t0) put_row8<D>(out + (int64_t)(t0 + t) * a.o_t, cols0 + c0, p.V, a.o_vec, y);
+      const int x = threadIdx.x + o * Stage::THREADS, t = x / Stage::XW, c0 = x % Stage::XW * 8;
+      if (t < end - t0) {
+        const auto y = Cols::get8(l.x, t, c0);
+        if constexpr (VEC)
+          put_row8<D>(in_row(out + t0 * a.o_t, (uint32_t)t * (uint32_t)a.o_t * (uint32_t)sizeof(S)),
+                      cols0 + c0, p.V, true, y);
+        else
+          put_row8<D>(out + (int64_t)(t0 + t) * a.o_t, cols0 + c0, p.V, false, y);
       }
     }
   };
   const int32_t chunks = (end - start + C - 1) / C;
+  wait_for_all();
   if (chunks > 0) fetch(0);
   for (int32_t i = 0; i < chunks; ++i) {
     __syncthreads();
@@ -228,12 +228,16 @@ static int delta_forward(const DeltaFwd& a, int64_t rows, hipStream_t stream) {
   hipLaunchKernelGGL((delta_prep_kernel<D, KP, false>), dim3((uint32_t)rows, p.heads), dim3(64), 0,
                      stream, p);
   if (int rc = check_launch("gated_delta_rule_varlen_fwd")) return rc;
-  if (delta_wide(p))
-    hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8>), dim3((p.V + 127) / 128, p.heads, p.batch),
-                       dim3(512), 0, stream, a);
-  else
-    hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4>), dim3((p.V + 63) / 64, p.heads, p.batch),
-                       dim3(256), 0, stream, a);
+  const bool vec = p.qk_vec && p.v_vec && a.o_vec;
+  if (delta_wide(p)) {
+    const dim3 grid((p.V + 127) / 128, p.heads, p.batch), threads(512);
+    if (vec) hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8, true>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8, false>), grid, threads, 0, stream, a);
+  } else {
+    const dim3 grid((p.V + 63) / 64, p.heads, p.batch), threads(256);
+    if (vec) hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4, true>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4, false>), grid, threads, 0, stream, a);
+  }
   return check_launch("gated_delta_rule_varlen_fwd");
 }
 

@@ -34,7 +34,7 @@ struct DeltaBwd {
   int64_t df_slot, di_slot;
   void *dq, *dk, *dv, *dg, *db;
   int64_t dq_t, dq_h, dk_t, dk_h, dv_t, dv_h, dg_t, dg_h, db_t, db_h;
-  int32_t do_vec, dqk_vec, dv_vec;
+  int32_t do_vec, grads_vec;
 };
 
 // Where a lane's part of dR's tiles of 16 columns lies: 1 KB a tile of 16 tokens.
@@ -45,13 +45,13 @@ __device__ __forceinline__ f32x4* delta_row_tiles(float* drows, int64_t at, int3
 
 // One workgroup walks a sequence's chunks from the last, for one value head
 // and 16 columns a wave.
-template <typename D, int KP, int NW>
+template <typename D, int KP, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, NW / 4) void delta_back_kernel(DeltaBwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
   constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32;
   constexpr int NF = kDeltaFrags<C>;
-  using Stage = WalkStage<D, KP, NW>;
+  using Stage = WalkStage<D, KP, NW, VEC>;
   using Rows = typename Stage::L::Rows;
   using Cols = typename Stage::L::Cols;
   __shared__ typename Stage::L l;
@@ -75,13 +75,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_back_kernel(DeltaBwd a)
   const S* dout = static_cast<const S*>(a.dout) + h * a.do_h;
   const int32_t row0 = start / C + b;
   Stage next;
-  next.init(p, k, q, dout, a.do_t, p.qk_vec && a.do_vec, cols0);
+  next.init(p, k, q, dout, a.do_t, cols0);
   auto fetch = [&](int32_t i) {
     const int64_t at = (int64_t)(row0 + i) * p.heads + h;
     next.fetch(p, start + i * C, end, p.frags + (at * (3 * NF) + NF) * kFragBytes,
                p.vectors + at * kDeltaVectors<C>);
   };
   const int32_t chunks = (end - start + C - 1) / C;
+  wait_for_all();
   if (chunks > 0) fetch(chunks - 1);
   for (int32_t i = chunks - 1; i >= 0; --i) {
     __syncthreads();
@@ -169,7 +170,7 @@ template <typename D, int KP> struct GradLds {
 // One workgroup: all gradients of a chunk's tokens for one key head, its value
 // heads one after another (dq and dk add up in registers, in that order).
 // Columns come in blocks of KP, 16 a wave; then a wave owns 16 of K.
-template <typename D, int KP, bool GROUPED>
+template <typename D, int KP, bool GROUPED, bool VEC>
 __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
@@ -228,16 +229,13 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
   static_assert(C * KP / 8 % THREADS == 0);
   typedef typename T::Exact Octets[N8];
   auto load2 = [&](Octets& x1, Octets& x2, const S* m1, int64_t ld1, const S* m2, int64_t ld2, int w0,
-                   int W, bool vec) {
-    auto load = [&](auto v) {
+                   int W) {
 #pragma unroll
-      for (int o = 0; o < N8; ++o) {
-        const int i = tid + o * THREADS, t = i / (KP / 8), c0 = w0 + i % (KP / 8) * 8;
-        x1[o] = load8<D, decltype(v)::value>(m1, ld1, t, ch.len, c0, W);
-        x2[o] = load8<D, decltype(v)::value>(m2, ld2, t, ch.len, c0, W);
-      }
-    };
-    if (vec) load(std::true_type()); else load(std::false_type());
+    for (int o = 0; o < N8; ++o) {
+      const int i = tid + o * THREADS, t = i / (KP / 8), c0 = w0 + i % (KP / 8) * 8;
+      x1[o] = load8<D, VEC>(m1, ld1, t, ch.len, c0, W);
+      x2[o] = load8<D, VEC>(m2, ld2, t, ch.len, c0, W);
+    }
   };
   auto stage2 = [&](S* l1, S* l2, const Octets& x1, const Octets& x2, int w0, int W) {
 #pragma unroll
@@ -249,17 +247,17 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
     }
   };
   // a tile back to memory, 16 bytes a lane where rows are of such vectors
-  auto put_tile = [&](S* m, int64_t ld, int w0, int W, bool vec, auto&& octet) {
+  auto put_tile = [&](S* m, int64_t ld, int w0, int W, auto&& octet) {
 #pragma unroll
     for (int o = 0; o < N8; ++o) {
       const int i = tid + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
-      if (t < ch.len) put_row8<D>(m + t * ld, w0 + c0, W, vec, octet(t, c0));
+      if (t < ch.len) put_row8<D>(m + t * ld, w0 + c0, W, VEC, octet(t, c0));
     }
   };
 
   Octets x1, x2;
   load2(x1, x2, static_cast<const S*>(p.k) + ch.t0 * p.k_t + kh * p.k_h, p.k_t,
-        static_cast<const S*>(p.q) + ch.t0 * p.q_t + kh * p.q_h, p.q_t, 0, p.K, p.qk_vec);
+        static_cast<const S*>(p.q) + ch.t0 * p.q_t + kh * p.q_h, p.q_t, 0, p.K);
   f32x4 dq[NT], dk[NT];
   if constexpr (GROUPED) {
 #pragma unroll
@@ -288,7 +286,7 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
       const int c16 = 16 * wave, col = v0 + c16 + r;
       // everything that the block needs from memory, before anything waits
       Octets xo, xv;
-      load2(xo, xv, dout, a.do_t, v, p.v_t, v0, p.V, a.do_vec && p.v_vec);
+      load2(xo, xv, dout, a.do_t, v, p.v_t, v0, p.V);
       const bool first = v0 == 0;
       float vec = 0.f;
       if (first) vec = p.vectors[at * kDeltaVectors<C> + min(tid, kDeltaVectors<C> - 1)];
@@ -381,7 +379,7 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
           put_split(l.r, BIG, i, y[t][e]);
         }
       __syncthreads();
-      put_tile(static_cast<S*>(a.dv) + ch.t0 * a.dv_t + h * a.dv_h, a.dv_t, v0, p.V, a.dv_vec,
+      put_tile(static_cast<S*>(a.dv) + ch.t0 * a.dv_t + h * a.dv_h, a.dv_t, v0, p.V,
                [&](int t, int c0) {
                  const float bt = l.v[2 * C + t];
                  S o[8];
@@ -576,9 +574,9 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
     }
   }
   // the barrier above also ends the writes of the tiles below
-  put_tile(static_cast<S*>(a.dq) + ch.t0 * a.dq_t + kh * a.dq_h, a.dq_t, 0, p.K, a.dqk_vec,
+  put_tile(static_cast<S*>(a.dq) + ch.t0 * a.dq_t + kh * a.dq_h, a.dq_t, 0, p.K,
            [&](int t, int c0) { return Rows::get8(l.q, t, c0); });
-  put_tile(static_cast<S*>(a.dk) + ch.t0 * a.dk_t + kh * a.dk_h, a.dk_t, 0, p.K, a.dqk_vec,
+  put_tile(static_cast<S*>(a.dk) + ch.t0 * a.dk_t + kh * a.dk_h, a.dk_t, 0, p.K,
            [&](int t, int c0) { return Rows::get8(l.k, t, c0); });
 }
 
@@ -589,18 +587,24 @@ static int delta_backward(const DeltaBwd& a, int64_t rows, hipStream_t stream) {
   hipLaunchKernelGGL((delta_prep_kernel<D, KP, true>), dim3((uint32_t)rows, p.heads), dim3(64), 0,
                      stream, p);
   if (int rc = check_launch(what)) return rc;
-  if (delta_wide(p))
-    hipLaunchKernelGGL((delta_back_kernel<D, KP, 8>), dim3((p.V + 127) / 128, p.heads, p.batch),
-                       dim3(512), 0, stream, a);
-  else
-    hipLaunchKernelGGL((delta_back_kernel<D, KP, 4>), dim3((p.V + 63) / 64, p.heads, p.batch),
-                       dim3(256), 0, stream, a);
+  const bool vec = p.qk_vec && a.do_vec;
+  if (delta_wide(p)) {
+    const dim3 grid((p.V + 127) / 128, p.heads, p.batch), threads(512);
+    if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, true>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false>), grid, threads, 0, stream, a);
+  } else {
+    const dim3 grid((p.V + 63) / 64, p.heads, p.batch), threads(256);
+    if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, true>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, false>), grid, threads, 0, stream, a);
+  }
   if (int rc = check_launch(what)) return rc;
   const dim3 chunks((uint32_t)rows, p.heads / p.group), threads(4 * KP);
-  if (p.group > 1)
-    hipLaunchKernelGGL((delta_grad_kernel<D, KP, true>), chunks, threads, 0, stream, a);
+  if (!(vec && p.v_vec && a.grads_vec))
+    hipLaunchKernelGGL((delta_grad_kernel<D, KP, true, false>), chunks, threads, 0, stream, a);
+  else if (p.group > 1)
+    hipLaunchKernelGGL((delta_grad_kernel<D, KP, true, true>), chunks, threads, 0, stream, a);
   else
-    hipLaunchKernelGGL((delta_grad_kernel<D, KP, false>), chunks, threads, 0, stream, a);
+    hipLaunchKernelGGL((delta_grad_kernel<D, KP, false, true>), chunks, threads, 0, stream, a);
   return check_launch(what);
 }
 
@@ -683,8 +687,8 @@ extern "C" int gated_delta_rule_varlen_bwd(
   a.db = dbeta, a.db_t = db_stride_t, a.db_h = db_stride_h;
   const int64_t n = 16 / elem_size(dtype);
   a.do_vec = delta_vec(dout, do_stride_t, do_stride_h, V, n);
-  a.dv_vec = delta_vec(dv, dv_stride_t, dv_stride_h, V, n);
-  a.dqk_vec = delta_vec(dq, dq_stride_t, dq_stride_h, K, n) && delta_vec(dk, dk_stride_t, dk_stride_h, K, n);
+  a.grads_vec = delta_vec(dv, dv_stride_t, dv_stride_h, V, n) && delta_vec(dq, dq_stride_t, dq_stride_h, K, n) &&
+                delta_vec(dk, dk_stride_t, dk_stride_h, K, n);
   if (dtype == SCONV_BF16)
     return K <= 64 ? delta_backward<Bf16, 64>(a, rows, stream) : delta_backward<Bf16, 128>(a, rows, stream);
   return K <= 64 ? delta_backward<F32, 64>(a, rows, stream) : delta_backward<F32, 128>(a, rows, stream);
