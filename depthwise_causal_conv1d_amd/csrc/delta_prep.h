@@ -24,19 +24,24 @@ __device__ __forceinline__ f32x4 mul16(const f32x4& x, const f32x4& y, f32x4 c) 
   return c;
 }
 
-// T = (I + A)^-1 in place: m [C][LD] holds A strictly below the diagonal.
-template <int C, int LD>
+// A lower triangle of 16 x 16 tiles in LDS, tile after tile; a row of 20 floats
+// lets 16 rows be read 16 bytes each without bank conflicts.
+constexpr int kTileLd = 20, kTileFloats = 16 * kTileLd;
+__host__ __device__ constexpr int tile_at(int I, int J) { return (I * (I + 1) / 2 + J) * kTileFloats; }
+
+// T = (I + A)^-1 in place: m holds A strictly below the diagonal (anything above).
+template <int C>
 __device__ __forceinline__ void unit_lower_inverse(float* m, int lane) {
   const int r = lane & 15, g = lane >> 4;
   if (lane < C) {
-    float* d = m + (16 * g) * LD + 16 * g;
+    float* d = m + (g * (g + 3) / 2) * kTileFloats;  // tile (g, g)
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float s = i == r ? 1.f : 0.f;
 #pragma unroll
       for (int j = 0; j < i; j += 4) {
-        const f32x4 a = lds4(d + i * LD + j);
+        const f32x4 a = lds4(d + i * kTileLd + j);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (j + e < i) s = fmaf(-a[e], x[j + e], s);
@@ -45,25 +50,24 @@ __device__ __forceinline__ void unit_lower_inverse(float* m, int lane) {
     }
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) d[i * LD + r] = x[i];
+    for (int i = 0; i < 16; ++i) d[i * kTileLd + r] = x[i];
   }
   __syncthreads();
-  auto rows = [&](int I, int J) { return lds4(m + (16 * I + r) * LD + 16 * J + 4 * g); };
+  auto rows = [&](int I, int J) { return lds4(m + tile_at(I, J) + r * kTileLd + 4 * g); };
   auto cols = [&](int I, int J) {
-    const float* at = m + (16 * I + 4 * g) * LD + 16 * J + r;
-    return (f32x4){at[0], at[LD], at[2 * LD], at[3 * LD]};
+    const float* at = m + tile_at(I, J) + 4 * g * kTileLd + r;
+    return (f32x4){at[0], at[kTileLd], at[2 * kTileLd], at[3 * kTileLd]};
   };
   auto store = [&](int I, int J, const f32x4& t) {
-    float* at = m + (16 * I + 4 * g) * LD + 16 * J + r;
+    float* at = m + tile_at(I, J) + 4 * g * kTileLd + r;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) at[e * LD] = -t[e];
+    for (int e = 0; e < 4; ++e) at[e * kTileLd] = -t[e];
   };
   f32x4 pair[C / 32];
 #pragma unroll
-  for (int P = 0; P < C / 32; ++P) {
-    const f32x4 w = mul16(rows(2 * P + 1, 2 * P), cols(2 * P, 2 * P), zero4());
-    pair[P] = mul16(rows(2 * P + 1, 2 * P + 1), w, zero4());
-  }
+  for (int P = 0; P < C / 32; ++P) pair[P] = mul16(rows(2 * P + 1, 2 * P), cols(2 * P, 2 * P), zero4());
+#pragma unroll
+  for (int P = 0; P < C / 32; ++P) pair[P] = mul16(rows(2 * P + 1, 2 * P + 1), pair[P], zero4());
   __syncthreads();
 #pragma unroll
   for (int P = 0; P < C / 32; ++P) store(2 * P + 1, 2 * P, pair[P]);
@@ -94,26 +98,48 @@ __device__ __forceinline__ void unit_lower_inverse(float* m, int lane) {
 // FWD: frags N (lower), P (lower).  Gradients: N (lower), N^T (upper), P^T (upper).
 template <int C, bool GRAD> constexpr int kPrepFrags = (GRAD ? 3 : 2) * kDeltaFrags<C>;
 
-template <typename D, int KP, bool GRAD>
-__global__ __launch_bounds__(64) void delta_prep_kernel(DeltaParams p) {
+// One wave a chunk and value head.  Bound by latency: three waves a SIMD are
+// what the LDS of a triangle leaves room for.
+template <typename D, int KP, bool GRAD, bool VEC>
+__global__ __launch_bounds__(64, 3) void delta_prep_kernel(DeltaParams p) {
   using T = Tile<D>;
   using S = typename D::storage;
-  constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, LD = C + 4, NF = kDeltaFrags<C>;
-  __shared__ float m[C * LD];
-  __shared__ float gh[C], gl[C], bt[C];
+  constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, NF = kDeltaFrags<C>;
+  __shared__ __attribute__((aligned(16))) float m[NT * (NT + 1) / 2 * kTileFloats];
+  __shared__ __attribute__((aligned(16))) float gh[C], gl[C], bt[C];
   const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
   const int32_t row = blockIdx.x, h = blockIdx.y;
   const DeltaChunk c = delta_find<C>(p, row);
   if (c.len == 0) return;
 
+  const int32_t kh = h / p.group;
+  const S* q = static_cast<const S*>(p.q) + (int64_t)c.t0 * p.q_t + kh * p.q_h;
+  const S* k = static_cast<const S*>(p.k) + (int64_t)c.t0 * p.k_t + kh * p.k_h;
+  typename T::Exact kf[NT][KS], qf[2][KS];
+  auto load = [&](const S* m, int64_t ld, int I, typename T::Exact (&to)[KS]) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      to[s] = load8<D, VEC>(m, ld, 16 * I + r, c.len, 32 * s + 8 * g, p.K);
+  };
+  auto mask = [&](int I, typename T::Exact (&x)[KS]) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      x[s] = mask8<D>(x[s], 16 * I + r < c.len ? p.K - (32 * s + 8 * g) : 0);
+  };
+#pragma unroll
+  for (int I = 0; I < NT; ++I) load(k, p.k_t, I, kf[I]);
+  load(q, p.q_t, 0, qf[0]);
+
   const int64_t at = (int64_t)row * p.heads + h;
   char* frags = p.frags + at * kPrepFrags<C, GRAD> * kFragBytes;
   float* vec = p.vectors + at * kDeltaVectors<C>;
   {
-    const int64_t t = c.t0 + lane;
+    const int64_t t = c.t0 + min(lane, c.len - 1);
     const bool live = lane < c.len;
-    double sum = live ? (double)delta_bound(delta_gate(p, p.g, t * p.g_t + h * p.g_h)) : 0.0;
-    const float b = live ? delta_gate(p, p.beta, t * p.b_t + h * p.b_h) : 0.f;
+    const float gv = delta_bound(delta_gate(p, p.g, t * p.g_t + h * p.g_h));
+    const float bv = delta_gate(p, p.beta, t * p.b_t + h * p.b_h);
+    double sum = live ? (double)gv : 0.0;
+    const float b = live ? bv : 0.f;
 #pragma unroll
     for (int d = 1; d < C; d *= 2) {
       const double o = __shfl_up(sum, d, 64);
@@ -132,81 +158,57 @@ __global__ __launch_bounds__(64) void delta_prep_kernel(DeltaParams p) {
     }
   }
   __syncthreads();
-  auto decay = [&](int i, int j) { return expf((gh[i] - gh[j]) + (gl[i] - gl[j])); };
-
-  const int32_t kh = h / p.group;
-  const S* q = static_cast<const S*>(p.q) + (int64_t)c.t0 * p.q_t + kh * p.q_h;
-  const S* k = static_cast<const S*>(p.k) + (int64_t)c.t0 * p.k_t + kh * p.k_h;
-  typename T::Exact kf[NT][KS], qf[NT][KS];
-  auto load = [&](auto v) {
 #pragma unroll
-    for (int I = 0; I < NT; ++I)
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        kf[I][s] = load8<D, decltype(v)::value>(k, p.k_t, 16 * I + r, c.len, 32 * s + 8 * g, p.K);
-        qf[I][s] = load8<D, decltype(v)::value>(q, p.q_t, 16 * I + r, c.len, 32 * s + 8 * g, p.K);
-      }
-  };
-  if (p.qk_vec) load(std::true_type()); else load(std::false_type());
-#pragma unroll
-  for (int I = 0; I < NT; ++I)
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int n = 16 * I + r < c.len ? p.K - (32 * s + 8 * g) : 0;
-      kf[I][s] = mask8<D>(kf[I][s], n);
-      qf[I][s] = mask8<D>(qf[I][s], n);
-    }
-  // A into LDS
-#pragma unroll
-  for (int I = 0; I < NT; ++I)
-#pragma unroll
-    for (int J = 0; J < NT; ++J) {
-      f32x4 a = zero4();
-      if (J <= I) {
-#pragma unroll
-        for (int s = 0; s < KS; ++s) a = T::mul(kf[I][s], kf[J][s], a);
-      }
-      const int j = 16 * J + r;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 16 * I + 4 * g + e;
-        m[i * LD + j] = i > j ? bt[i] * decay(i, j) * a[e] : 0.f;
-      }
-    }
-  // P or P^T from registers
+  for (int I = 0; I < NT; ++I) mask(I, kf[I]);
+  // Tiles of A and P, e_ij once for both.  An accumulator is then a piece of a
+  // frag as it lies: rows j and columns i for P's, rows i and columns j for P^T's.
+  constexpr float kLog2e = 1.44269504088896340736f;
   f32x4 pt[NT][NT];
 #pragma unroll
-  for (int I = 0; I < NT; ++I)
+  for (int I = 0; I < NT; ++I) {
+    if (I + 1 < NT) load(q, p.q_t, I + 1, qf[(I + 1) & 1]);
+    mask(I, qf[I & 1]);
 #pragma unroll
-    for (int J = 0; J < NT; ++J) {
-      pt[I][J] = zero4();
-      if (J > I) continue;
-      f32x4 a = zero4();
+    for (int J = 0; J <= I; ++J) {
+      f32x4 a = zero4(), w = zero4();
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
-        a = GRAD ? T::mul(qf[I][s], kf[J][s], a) : T::mul(kf[J][s], qf[I][s], a);
+      for (int s = 0; s < KS; ++s) {
+        a = GRAD ? T::mul(kf[I][s], kf[J][s], a) : T::mul(kf[J][s], kf[I][s], a);
+        w = GRAD ? T::mul(qf[I & 1][s], kf[J][s], w) : T::mul(kf[J][s], qf[I & 1][s], w);
+      }
+      const int lane_t = 16 * (GRAD ? J : I) + r, four = 16 * (GRAD ? I : J) + 4 * g;
+      const float h1 = gh[lane_t], l1 = gl[lane_t], b1 = bt[lane_t];
+      const f32x4 h4 = lds4(gh + four), l4 = lds4(gl + four), b4 = lds4(bt + four);
+      f32x4 x;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = 16 * I + (GRAD ? 4 * g + e : r), j = 16 * J + (GRAD ? r : 4 * g + e);
-        pt[I][J][e] = i >= j ? p.scale * decay(i, j) * a[e] : 0.f;
+        const int i = GRAD ? four + e : lane_t, j = GRAD ? lane_t : four + e;
+        const float d = GRAD ? (h4[e] - h1) + (l4[e] - l1) : (h1 - h4[e]) + (l1 - l4[e]);
+        const float dec = __builtin_amdgcn_exp2f(i >= j ? d * kLog2e : 0.f);
+        x[e] = (GRAD ? b4[e] : b1) * dec * a[e];
+        pt[I][J][e] = i >= j ? p.scale * dec * w[e] : 0.f;
       }
-    }
-#pragma unroll
-  for (int R = 0; R < NT; ++R)
-#pragma unroll
-    for (int s = 0; s < C / 32; ++s) {
       if constexpr (GRAD) {
-        if (s >= R / 2)
-          T::put(frags + (2 * NF + upper_frag<C>(R, s)) * kFragBytes, lane,
-                 T::split(pt[2 * s][R], pt[2 * s + 1][R]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[tile_at(I, J) + (4 * g + e) * kTileLd + r] = x[e];
       } else {
-        if (s <= R / 2)
-          T::put(frags + (NF + lower_frag<C>(R, s)) * kFragBytes, lane,
-                 T::split(pt[R][2 * s], pt[R][2 * s + 1]));
+        *reinterpret_cast<f32x4*>(m + tile_at(I, J) + r * kTileLd + 4 * g) = x;
       }
     }
+    if constexpr (!GRAD) {
+#pragma unroll
+      for (int s = 0; s <= I / 2; ++s)
+        T::put(frags + (NF + lower_frag<C>(I, s)) * kFragBytes, lane,
+               T::split(pt[I][2 * s], 2 * s + 1 <= I ? pt[I][2 * s + 1] : zero4()));
+    } else if (I % 2 == 1) {
+#pragma unroll
+      for (int J = 0; J <= I; ++J)
+        T::put(frags + (2 * NF + upper_frag<C>(J, I / 2)) * kFragBytes, lane,
+               T::split(J <= I - 1 ? pt[I - 1][J] : zero4(), pt[I][J]));
+    }
+  }
   __syncthreads();
-  unit_lower_inverse<C, LD>(m, lane);
+  unit_lower_inverse<C>(m, lane);
   // N = T - I; what lies above the diagonal of a frag's 32 columns is zero
 #pragma unroll
   for (int R = 0; R < NT; ++R)
@@ -214,12 +216,13 @@ __global__ __launch_bounds__(64) void delta_prep_kernel(DeltaParams p) {
     for (int s = 0; s <= R / 2; ++s) {
       f32x4 x[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) {
+        const int J = 2 * s + u;
+        x[u] = J <= R ? lds4(m + tile_at(R, J <= R ? J : 0) + r * kTileLd + 4 * g) : zero4();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 16 * R + r, j = 32 * s + 16 * u + 4 * g + e;
-          x[u][e] = j < i ? m[i * LD + j] : 0.f;
-        }
+        for (int e = 0; e < 4; ++e)
+          if (J == R) x[u][e] = 4 * g + e < r ? x[u][e] : 0.f;
+      }
       T::put(frags + lower_frag<C>(R, s) * kFragBytes, lane, T::split(x[0], x[1]));
     }
   if constexpr (GRAD) {
@@ -229,15 +232,26 @@ __global__ __launch_bounds__(64) void delta_prep_kernel(DeltaParams p) {
       for (int s = R / 2; s < C / 32; ++s) {
         f32x4 x[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+          const int I = 2 * s + u;
+          const float* at = m + tile_at(I >= R ? I : R, R) + 4 * g * kTileLd + r;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int j = 16 * R + r, i = 32 * s + 16 * u + 4 * g + e;
-            x[u][e] = j < i ? m[i * LD + j] : 0.f;
+            x[u][e] = I >= R ? at[e * kTileLd] : 0.f;
+            if (I == R) x[u][e] = r < 4 * g + e ? x[u][e] : 0.f;
           }
+        }
         T::put(frags + (NF + upper_frag<C>(R, s)) * kFragBytes, lane, T::split(x[0], x[1]));
       }
   }
+}
+
+template <typename D, int KP, bool GRAD>
+static int delta_prepare(const char* what, const DeltaParams& p, int64_t rows, hipStream_t stream) {
+  const dim3 grid((uint32_t)rows, p.heads), wave(64);
+  if (p.qk_vec) hipLaunchKernelGGL((delta_prep_kernel<D, KP, GRAD, true>), grid, wave, 0, stream, p);
+  else hipLaunchKernelGGL((delta_prep_kernel<D, KP, GRAD, false>), grid, wave, 0, stream, p);
+  return check_launch(what);
 }
 
 }  // namespace sconv

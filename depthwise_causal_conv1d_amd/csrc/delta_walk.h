@@ -9,11 +9,11 @@
 
 namespace sconv {
 
-template <typename D, int KP, int NW> struct WalkLds {
+template <typename D, int KP, int NW, int NC> struct WalkLds {
   using S = typename D::storage;
   static constexpr int C = kDeltaChunk<D>;
   using Rows = LdsRows<D, KP>;
-  using Cols = LdsRows<D, 16 * NW>;
+  using Cols = LdsRows<D, 16 * NW * NC>;
   __attribute__((aligned(16))) S k[C * Rows::LD];
   __attribute__((aligned(16))) S q[C * Rows::LD];
   __attribute__((aligned(16))) S x[C * Cols::LD];
@@ -21,12 +21,12 @@ template <typename D, int KP, int NW> struct WalkLds {
   __attribute__((aligned(16))) float v[3 * C];
 };
 
-template <typename D, int KP, int NW, bool VEC> struct WalkStage {
-  using L = WalkLds<D, KP, NW>;
+template <typename D, int KP, int NW, int NC, bool VEC> struct WalkStage {
+  using L = WalkLds<D, KP, NW, NC>;
   using S = typename D::storage;
   using E = typename Tile<D>::Exact;
   static constexpr int C = L::C, THREADS = 64 * NW;
-  static constexpr int XW = 2 * NW;  // octets of a row of x
+  static constexpr int XW = 2 * NW * NC;  // octets of a row of x
   static constexpr int KN = C * KP / 8, XN = C * XW, FN = 2 * kDeltaFrags<C> * kFragBytes / 16;
   static constexpr int KO = (KN + THREADS - 1) / THREADS, XO = XN / THREADS, FO = FN / THREADS;
   static_assert(XN % THREADS == 0 && FN % THREADS == 0 && 3 * C <= THREADS);
@@ -49,7 +49,7 @@ template <typename D, int KP, int NW, bool VEC> struct WalkStage {
   __device__ __forceinline__ void init(const DeltaParams& p, const S* k_, const S* q_, const S* x_,
                                        int64_t x_t_, int32_t col0_) {
     tk = k_, tq = q_, tx = x_, x_t = x_t_, col0 = col0_;
-    whole = p.K == KP && col0 + 16 * NW <= p.V;
+    whole = p.K == KP && col0 + 16 * NW * NC <= p.V;
     columns(k_c, threadIdx.x % (KP / 8) * 8, p.K);
     columns(x_c, col0 + threadIdx.x % XW * 8, p.V);
   }
@@ -63,42 +63,36 @@ template <typename D, int KP, int NW, bool VEC> struct WalkStage {
   // The chunk's rows are t0 .. end - 1.  One path of loads: where paths with
   // loads meet, the compiler waits for those of either, and on this machine a
   // wait for loads is one for stores as well (4000 of a chunk's 13000 cycles).
+  // Piece P of N of it: a wave stands still while the memory pipes are full, so
+  // a chunk's loads go out between the products of the one ahead of it.
+  template <int P, int N>
   __device__ __forceinline__ void fetch(const DeltaParams& p, int32_t t0, int32_t end,
                                         const char* frags, const float* vectors) {
     const S *rk = tk + t0 * p.k_t, *rq = tq + t0 * p.q_t, *rx = tx + t0 * x_t;
     const int32_t last = end - t0 - 1;
-    if constexpr (VEC) {
-      const uint32_t es = sizeof(S);
+    constexpr int ALL = 2 * KO + XO + FO + 1, LO = ALL * P / N, HI = ALL * (P + 1) / N;
+    // hidden, or all these addresses would be made ahead of the loop and held
+    const int tid = VEC ? (int)threadIdx.x : (int)lane_offset(threadIdx.x);
+    auto rows = [&](const S* m, int64_t ld, int i, int wide, const uint32_t (&c)[2], int c0, int W) {
+      const int t = i / wide;
+      if constexpr (VEC) return at(m, (uint32_t)min(t, last) * (uint32_t)ld * (uint32_t)sizeof(S), c);
+      else return load8<D, false>(m, ld, t, last + 1, c0 + i % wide * 8, W);
+    };
 #pragma unroll
-      for (int o = 0; o < KO; ++o) {
-        const uint32_t t = min((int)(threadIdx.x + o * THREADS) / (KP / 8), last);
-        k[o] = at(rk, t * (uint32_t)p.k_t * es, k_c);
-        q[o] = at(rq, t * (uint32_t)p.q_t * es, k_c);
-      }
-#pragma unroll
-      for (int o = 0; o < XO; ++o) {
-        const uint32_t t = min((int)(threadIdx.x + o * THREADS) / XW, last);
-        x[o] = at(rx, t * (uint32_t)x_t * es, x_c);
-      }
-    } else {
-      // hidden, or all these addresses would be made ahead of the loop and held
-      const int tid = (int)lane_offset(threadIdx.x);
-#pragma unroll
-      for (int o = 0; o < KO; ++o) {
-        const int i = tid + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
-        k[o] = load8<D, false>(rk, p.k_t, t, last + 1, c0, p.K);
-        q[o] = load8<D, false>(rq, p.q_t, t, last + 1, c0, p.K);
-      }
-#pragma unroll
-      for (int o = 0; o < XO; ++o) {
-        const int i = tid + o * THREADS, t = i / XW, c0 = i % XW * 8;
-        x[o] = load8<D, false>(rx, x_t, t, last + 1, col0 + c0, p.V);
+    for (int n = LO; n < HI; ++n) {
+      if (n < KO) {
+        k[n] = rows(rk, p.k_t, tid + n * THREADS, KP / 8, k_c, 0, p.K);
+      } else if (n < 2 * KO) {
+        q[n - KO] = rows(rq, p.q_t, tid + (n - KO) * THREADS, KP / 8, k_c, 0, p.K);
+      } else if (n < 2 * KO + XO) {
+        x[n - 2 * KO] = rows(rx, x_t, tid + (n - 2 * KO) * THREADS, XW, x_c, col0, p.V);
+      } else if (n < 2 * KO + XO + FO) {
+        const int o = n - 2 * KO - XO;
+        f[o] = *reinterpret_cast<const u32x4*>(in_row(frags + o * THREADS * 16, threadIdx.x * 16u));
+      } else {
+        v = *in_row(vectors, (threadIdx.x < 3 * C ? threadIdx.x : 0) * 4u);
       }
     }
-#pragma unroll
-    for (int o = 0; o < FO; ++o)
-      f[o] = *reinterpret_cast<const u32x4*>(in_row(frags + o * THREADS * 16, threadIdx.x * 16u));
-    v = *in_row(vectors, (threadIdx.x < 3 * C ? threadIdx.x : 0) * 4u);
   }
   // len: tokens of the chunk
   template <bool MASK> __device__ __forceinline__ void stage_rows(L& l, const DeltaParams& p, int32_t len) const {
@@ -131,17 +125,18 @@ template <typename D, int KP, int NW, bool VEC> struct WalkStage {
 // first use inside it a wait for the loop's own.
 __device__ __forceinline__ void wait_for_all() { __builtin_amdgcn_s_waitcnt(0); }
 
-// A wave's 16 columns of a K x V matrix in memory and in accumulator tiles.  A
-// row is a uniform address and a lane's 32-bit offset: 64-bit addresses for
-// every lane and row, made once ahead of the loop, would take 64 registers.
-template <bool STORE, int KT>
+// A wave's 16 columns of a K x V matrix in memory and in accumulator tiles (P of
+// N: a piece of the tiles).  A row is a uniform address and a lane's 32-bit
+// offset: 64-bit addresses for every lane and row, made once ahead of the loop,
+// would take 64 registers.
+template <bool STORE, int P, int N, int KT>
 __device__ __forceinline__ void state_columns(f32x4 (&s)[KT], std::conditional_t<STORE, float, const float>* m,
                                               int K, int V, int col, int col_end) {
   const int g = (threadIdx.x & 63) >> 4;
   const uint32_t off = lane_offset((uint32_t)(4 * g * V + col) * 4u);
   auto all = [&](auto in) {
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+    for (int t = KT * P / N; t < KT * (P + 1) / N; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (!in(16 * t + 4 * g + e)) continue;
@@ -154,59 +149,72 @@ __device__ __forceinline__ void state_columns(f32x4 (&s)[KT], std::conditional_t
   else all([&](int k) { return k < K && col < V; });
 }
 
-// The products of a chunk's K (and Q) with 16 columns of a state: x = K S, y =
-// Q S.  K's and Q's operands alternate, each loaded while the other's products
-// run; `last` loads what comes next, behind the last of Q's.
-template <typename D, typename Rows, int KS, int NT, bool BOTH, typename F>
+// The products of a chunk's K (and Q) with 16 NC columns of a state: x = K S, y
+// = Q S.  K's and Q's operands alternate, each loaded while the other's products
+// run; `last` loads what comes next, behind the last of them.  piece(j) issues
+// what else there is for memory, j of kGroups.
+template <int KS, bool BOTH> constexpr int kGroups = BOTH ? 2 * KS : KS;
+template <typename D, typename Rows, int KS, int NT, int NC, bool BOTH, typename F, typename G>
 __device__ __forceinline__ void rows_times_state(const typename D::storage* lk, const typename D::storage* lq,
-                                                 const f32x4 (&s)[2 * KS], f32x4 (&x)[NT], f32x4 (&y)[NT],
-                                                 int lane, F&& last) {
+                                                 const f32x4 (&s)[NC][2 * KS], f32x4 (&x)[NC][NT],
+                                                 f32x4 (&y)[NC][NT], int lane, F&& last, G&& piece) {
   using T = Tile<D>;
   typename T::Exact kf[2][NT], qf[NT];
-  typename T::Split sp[2];
+  typename T::Split sp[2][NC];
   auto load = [&](const typename D::storage* m, int c, typename T::Exact (&to)[NT]) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) to[t] = Rows::rows(m, 16 * t, 32 * c, lane);
   };
+  auto split = [&](int c) {
+#pragma unroll
+    for (int n = 0; n < NC; ++n) sp[c & 1][n] = T::split(s[n][2 * c], s[n][2 * c + 1]);
+  };
   load(lk, 0, kf[0]);
 #pragma unroll
-  for (int t = 0; t < NT; ++t) x[t] = y[t] = zero4();
-  sp[0] = T::split(s[0], s[1]);
+  for (int n = 0; n < NC; ++n)
 #pragma unroll
-  for (int c = 0; c < KS; ++c) {
+    for (int t = 0; t < NT; ++t) x[n][t] = y[n][t] = zero4();
+  split(0);
+  each_part<KS>([&](auto c) {
     constexpr int B = BOTH ? 0 : 1;  // K alone: its own operands alternate
     if constexpr (BOTH) {
       load(lq, c, qf);
     } else {
-      if (c + 1 < KS) load(lk, c + 1, kf[(c + 1) & B]);
+      if constexpr (c + 1 < KS) load(lk, c + 1, kf[(c + 1) & B]);
       else last();
     }
+    piece(std::integral_constant<int, BOTH ? 2 * c : c>());
     keep_order();
-    if (!BOTH && c + 1 < KS) sp[(c + 1) & 1] = T::split(s[2 * c + 2], s[2 * c + 3]);
+    if constexpr (!BOTH && c + 1 < KS) split(c + 1);
     each_part<T::kExactSplit>([&](auto P) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) x[t] = T::template part<P>(kf[c & B][t], sp[c & 1], x[t]);
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) x[n][t] = T::template part<P>(kf[c & B][t], sp[c & 1][n], x[n][t]);
     });
     keep_order();
     if constexpr (BOTH) {
-      if (c + 1 < KS) load(lk, c + 1, kf[0]);
+      if constexpr (c + 1 < KS) load(lk, c + 1, kf[0]);
       else last();
+      piece(std::integral_constant<int, 2 * c + 1>());
       keep_order();
-      if (c + 1 < KS) sp[(c + 1) & 1] = T::split(s[2 * c + 2], s[2 * c + 3]);
+      if constexpr (c + 1 < KS) split(c + 1);
       each_part<T::kExactSplit>([&](auto P) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) y[t] = T::template part<P>(qf[t], sp[c & 1], y[t]);
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int n = 0; n < NC; ++n) y[n][t] = T::template part<P>(qf[t], sp[c & 1][n], y[n][t]);
       });
       keep_order();
     }
-  }
+  });
 }
 
 // x += (the triangle's frags) y: lower rows meet columns of steps c <= t / 2,
 // upper ones c >= t / 2.
-template <typename D, bool LOWER, int NF, typename Y, int NT>
+template <typename D, bool LOWER, int NF, typename Y, int NT, int NC>
 __device__ __forceinline__ void triangle_times(const typename Tile<D>::Split (&tri)[NF],
-                                               const Y (&y)[NT / 2], f32x4 (&x)[NT]) {
+                                               const Y (&y)[NC][NT / 2], f32x4 (&x)[NC][NT]) {
   using T = Tile<D>;
   constexpr int C = 16 * NT, CS = NT / 2;
   constexpr int N = std::is_same<Y, typename T::Split>::value ? T::kSplitSplit : T::kSplitExact;
@@ -214,8 +222,10 @@ __device__ __forceinline__ void triangle_times(const typename Tile<D>::Split (&t
     constexpr int c = P / N;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-      if (LOWER ? c <= t / 2 : c >= t / 2)
-        x[t] = T::template part<P % N>(tri[LOWER ? lower_frag<C>(t, c) : upper_frag<C>(t, c)], y[c], x[t]);
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+        if (LOWER ? c <= t / 2 : c >= t / 2)
+          x[n][t] = T::template part<P % N>(tri[LOWER ? lower_frag<C>(t, c) : upper_frag<C>(t, c)], y[n][c], x[n][t]);
   });
 }
 
@@ -225,11 +235,20 @@ __device__ __forceinline__ void load_triangle(typename Tile<D>::Split (&tri)[NF]
   for (int x = 0; x < NF; ++x) tri[x] = Tile<D>::get(f + x * kFragBytes, lane);
 }
 
-// s += M^T u for M's rows in LDS, 16 columns of u; half of M's operands are
+template <typename D, int NT, int NC>
+__device__ __forceinline__ void split_tiles(const f32x4 (&u)[NC][NT], typename Tile<D>::Split (&o)[NC][NT / 2]) {
+#pragma unroll
+  for (int n = 0; n < NC; ++n)
+#pragma unroll
+    for (int c = 0; c < NT / 2; ++c) o[n][c] = Tile<D>::split(u[n][2 * c], u[n][2 * c + 1]);
+}
+
+// s += M^T u for M's rows in LDS, 16 NC columns of u; half of M's operands are
 // loaded while the other half's products run.
-template <typename D, typename Rows, int KT, int CS>
+template <typename D, typename Rows, int KT, int CS, int NC>
 __device__ __forceinline__ void cols_times(const typename D::storage* m,
-                                           const typename Tile<D>::Fine (&u)[CS], f32x4 (&s)[KT], int lane) {
+                                           const typename Tile<D>::Fine (&u)[NC][CS], f32x4 (&s)[NC][KT],
+                                           int lane) {
   using T = Tile<D>;
   constexpr int H = KT / 2;
   typename T::Exact f[2][H];
@@ -244,10 +263,12 @@ __device__ __forceinline__ void cols_times(const typename D::storage* m,
     keep_order();
     each_part<T::kExactFine>([&](auto P) {
 #pragma unroll
-      for (int t = 0; t < H; ++t) {
-        f32x4& to = s[H * (i & 1) + t];
-        to = T::template part<P>(f[i & 1][t], u[i / 2], to);
-      }
+      for (int t = 0; t < H; ++t)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          f32x4& to = s[n][H * (i & 1) + t];
+          to = T::template part<P>(f[i & 1][t], u[n][i / 2], to);
+        }
     });
     keep_order();
   }

@@ -16,15 +16,15 @@ struct DeltaFwd {
   int32_t o_vec;
 };
 
-// One workgroup walks a sequence's chunks for one value head, 16 columns a
+// One workgroup walks a sequence's chunks for one value head, 16 NC columns a
 // wave.  An output chunk waits in LDS, in V's place, for the next one's staging.
 template <typename D, int KP, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
   constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32;
-  constexpr int NF = kDeltaFrags<C>;
-  using Stage = WalkStage<D, KP, NW, VEC>;
+  constexpr int NC = 1, NF = kDeltaFrags<C>, PIECES = kGroups<KS, true>;
+  using Stage = WalkStage<D, KP, NW, NC, VEC>;
   using Rows = typename Stage::L::Rows;
   using Cols = typename Stage::L::Cols;
   __shared__ typename Stage::L l;
@@ -35,15 +35,21 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a)
   const int32_t slot = p.slots ? p.slots[b] : b;
   if (p.slots && slot == p.pad) return;
   const int32_t start = p.qsl[b], end = p.qsl[b + 1];
-  const int32_t cols0 = blockIdx.x * 16 * NW, c16 = 16 * wave, col = cols0 + c16 + r;
+  const int32_t cols0 = blockIdx.x * 16 * NW * NC, c16 = 16 * NC * wave;
   const int64_t KV = (int64_t)p.K * p.V;
 
-  f32x4 s[KT];
+  f32x4 s[NC][KT];
 #pragma unroll
-  for (int t = 0; t < KT; ++t) s[t] = zero4();
+  for (int n = 0; n < NC; ++n)
+#pragma unroll
+    for (int t = 0; t < KT; ++t) s[n][t] = zero4();
+  auto col = [&](int n) { return cols0 + c16 + 16 * n + r; };
+  auto ends = [&](int n) { return cols0 + c16 + 16 * n + 16; };
   float* state = a.states ? a.states + slot * a.st_slot + h * KV : nullptr;
-  const int32_t ends = cols0 + c16 + 16;
-  if (p.has && p.has[b]) state_columns<false>(s, state, p.K, p.V, col, ends);
+  if (p.has && p.has[b]) {
+#pragma unroll
+    for (int n = 0; n < NC; ++n) state_columns<false, 0, 1>(s[n], state, p.K, p.V, col(n), ends(n));
+  }
 
   const S* q = static_cast<const S*>(p.q) + kh * p.q_h;
   const S* k = static_cast<const S*>(p.k) + kh * p.k_h;
@@ -52,10 +58,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a)
   const int32_t row0 = start / C + b;
   Stage next;
   next.init(p, k, q, v, p.v_t, cols0);
-  auto fetch = [&](int32_t i) {
+  auto fetch = [&](int32_t i, auto P, auto N) {
     const int64_t at = (int64_t)(row0 + i) * p.heads + h;
-    next.fetch(p, start + i * C, end, p.frags + at * (2 * NF) * kFragBytes,
-               p.vectors + at * kDeltaVectors<C>);
+    next.template fetch<decltype(P)::value, decltype(N)::value>(
+        p, start + i * C, end, p.frags + at * (2 * NF) * kFragBytes, p.vectors + at * kDeltaVectors<C>);
   };
   auto put_out = [&](int32_t i) {
     const int32_t t0 = start + i * C;
@@ -74,60 +80,84 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a)
   };
   const int32_t chunks = (end - start + C - 1) / C;
   wait_for_all();
-  if (chunks > 0) fetch(0);
+  if (chunks > 0) fetch(0, std::integral_constant<int, 0>(), std::integral_constant<int, 1>());
   for (int32_t i = 0; i < chunks; ++i) {
     __syncthreads();
     if (i > 0) put_out(i - 1);
     next.stage(l, p, end - (start + i * C));
     __syncthreads();
-    if (i + 1 < chunks) fetch(i + 1);
-    if (a.marks)
-      state_columns<true>(s, a.marks + ((int64_t)(row0 + i) * p.heads + h) * KV, p.K, p.V, col, ends);
-    f32x4 u[NT], y[NT];  // K S, then R, then U; Q S, then O
-    typename T::Exact vv[CS];
-    typename T::Split tri[NF], us[CS];
-    rows_times_state<D, Rows, KS, NT, true>(l.k, l.q, s, u, y, lane, [&] {
+    float* mark = a.marks ? a.marks + ((int64_t)(row0 + i) * p.heads + h) * KV : nullptr;
+    f32x4 u[NC][NT], y[NC][NT];  // K S, then R, then U; Q S, then O
+    typename T::Exact vv[NC][CS];
+    typename T::Split tri[NF], us[NC][CS];
+    rows_times_state<D, Rows, KS, NT, NC, true>(
+        l.k, l.q, s, u, y, lane,
+        [&] {
 #pragma unroll
-      for (int c = 0; c < CS; ++c) vv[c] = Cols::cols(l.x, 32 * c, c16, lane);
-      load_triangle<D>(tri, l.f, lane);
-    });
+          for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int c = 0; c < CS; ++c) vv[n][c] = Cols::cols(l.x, 32 * c, c16 + 16 * n, lane);
+          load_triangle<D>(tri, l.f, lane);
+        },
+        [&](auto P) {
+          // the last chunk fetches itself again: a branch here would make loads wait
+          fetch(min(i + 1, chunks - 1), P, std::integral_constant<int, PIECES>());
+          if (mark) {
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+              state_columns<true, decltype(P)::value, PIECES>(s[n], mark, p.K, p.V, col(n), ends(n));
+          }
+        });
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const f32x4 gam = lds4(l.v + 16 * t + 4 * g), bt = lds4(l.v + 2 * C + 16 * t + 4 * g);
+      const f32x4 sg = gam * p.scale;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        u[t][e] = bt[e] * (T::value(vv[t / 2], 4 * (t & 1) + e) - gam[e] * u[t][e]);
-        y[t][e] *= p.scale * gam[e];
-      }
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          u[n][t][e] = bt[e] * (T::value(vv[n][t / 2], 4 * (t & 1) + e) - gam[e] * u[n][t][e]);
+          y[n][t][e] *= sg[e];
+        }
     }
-#pragma unroll
-    for (int c = 0; c < CS; ++c) us[c] = T::split(u[2 * c], u[2 * c + 1]);
+    split_tiles<D>(u, us);
     triangle_times<D, true>(tri, us, u);
     keep_order();
     load_triangle<D>(tri, l.f + NF * kFragBytes, lane);
     keep_order();
-#pragma unroll
-    for (int c = 0; c < CS; ++c) us[c] = T::split(u[2 * c], u[2 * c + 1]);
+    split_tiles<D>(u, us);
     const float whole = l.v[C - 1];
-    typename T::Fine fine[CS];
+    typename T::Fine fine[NC][CS];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) u[t] *= lds4(l.v + C + 16 * t + 4 * g);
+    for (int t = 0; t < NT; ++t) {
+      const f32x4 left = lds4(l.v + C + 16 * t + 4 * g);
 #pragma unroll
-    for (int c = 0; c < CS; ++c) fine[c] = T::fine(u[2 * c], u[2 * c + 1]);
+      for (int n = 0; n < NC; ++n) u[n][t] *= left;
+    }
 #pragma unroll
-    for (int t = 0; t < KT; ++t) s[t] *= whole;
+    for (int n = 0; n < NC; ++n) {
+#pragma unroll
+      for (int c = 0; c < CS; ++c) fine[n][c] = T::fine(u[n][2 * c], u[n][2 * c + 1]);
+#pragma unroll
+      for (int t = 0; t < KT; ++t) s[n][t] *= whole;
+    }
     triangle_times<D, true>(tri, us, y);
     keep_order();
     cols_times<D, Rows>(l.k, fine, s, lane);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int n = 0; n < NC; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        l.x[(16 * t + 4 * g + e) * Cols::LD + Cols::pos(c16 + r)] = delta_round<D>(y[t][e]);
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          l.x[(16 * t + 4 * g + e) * Cols::LD + Cols::pos(c16 + 16 * n + r)] = delta_round<D>(y[n][t][e]);
   }
   __syncthreads();
   if (chunks > 0) put_out(chunks - 1);
-  if (state) state_columns<true>(s, state, p.K, p.V, col, ends);
+  if (state) {
+#pragma unroll
+    for (int n = 0; n < NC; ++n) state_columns<true, 0, 1>(s[n], state, p.K, p.V, col(n), ends(n));
+  }
 }
 
 // ---------------------------------------------------------------- one token
@@ -225,9 +255,7 @@ __global__ __launch_bounds__(kUpdateThreads) void delta_update_kernel(DeltaUpdat
 template <typename D, int KP>
 static int delta_forward(const DeltaFwd& a, int64_t rows, hipStream_t stream) {
   const DeltaParams& p = a.p;
-  hipLaunchKernelGGL((delta_prep_kernel<D, KP, false>), dim3((uint32_t)rows, p.heads), dim3(64), 0,
-                     stream, p);
-  if (int rc = check_launch("gated_delta_rule_varlen_fwd")) return rc;
+  if (int rc = delta_prepare<D, KP, false>("gated_delta_rule_varlen_fwd", p, rows, stream)) return rc;
   const bool vec = p.qk_vec && p.v_vec && a.o_vec;
   if (delta_wide(p)) {
     const dim3 grid((p.V + 127) / 128, p.heads, p.batch), threads(512);

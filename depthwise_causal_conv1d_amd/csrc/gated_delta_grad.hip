@@ -44,14 +44,14 @@ __device__ __forceinline__ f32x4* delta_row_tiles(float* drows, int64_t at, int3
 }
 
 // One workgroup walks a sequence's chunks from the last, for one value head
-// and 16 columns a wave.
+// and 16 NC columns a wave.
 template <typename D, int KP, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, NW / 4) void delta_back_kernel(DeltaBwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
   constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32;
-  constexpr int NF = kDeltaFrags<C>;
-  using Stage = WalkStage<D, KP, NW, VEC>;
+  constexpr int NC = 1, NF = kDeltaFrags<C>, PIECES = kGroups<KS, false>;
+  using Stage = WalkStage<D, KP, NW, NC, VEC>;
   using Rows = typename Stage::L::Rows;
   using Cols = typename Stage::L::Cols;
   __shared__ typename Stage::L l;
@@ -62,86 +62,122 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_back_kernel(DeltaBwd a)
   const int32_t slot = p.slots ? p.slots[b] : b;
   if (p.slots && slot == p.pad) return;
   const int32_t start = p.qsl[b], end = p.qsl[b + 1];
-  const int32_t cols0 = blockIdx.x * 16 * NW, c16 = 16 * wave, col = cols0 + c16 + r;
+  const int32_t cols0 = blockIdx.x * 16 * NW * NC, c16 = 16 * NC * wave;
   const int64_t KV = (int64_t)p.K * p.V;
 
-  f32x4 s[KT];
+  f32x4 s[NC][KT];
 #pragma unroll
-  for (int t = 0; t < KT; ++t) s[t] = zero4();
-  const int32_t ends = cols0 + c16 + 16;
-  if (a.dfinal) state_columns<false>(s, a.dfinal + slot * a.df_slot + h * KV, p.K, p.V, col, ends);
+  for (int n = 0; n < NC; ++n)
+#pragma unroll
+    for (int t = 0; t < KT; ++t) s[n][t] = zero4();
+  auto col = [&](int n) { return cols0 + c16 + 16 * n + r; };
+  auto ends = [&](int n) { return cols0 + c16 + 16 * n + 16; };
+  if (a.dfinal) {
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+      state_columns<false, 0, 1>(s[n], a.dfinal + slot * a.df_slot + h * KV, p.K, p.V, col(n), ends(n));
+  }
   const S* q = static_cast<const S*>(p.q) + kh * p.q_h;
   const S* k = static_cast<const S*>(p.k) + kh * p.k_h;
   const S* dout = static_cast<const S*>(a.dout) + h * a.do_h;
   const int32_t row0 = start / C + b;
   Stage next;
   next.init(p, k, q, dout, a.do_t, cols0);
-  auto fetch = [&](int32_t i) {
+  auto fetch = [&](int32_t i, auto P, auto N) {
     const int64_t at = (int64_t)(row0 + i) * p.heads + h;
-    next.fetch(p, start + i * C, end, p.frags + (at * (3 * NF) + NF) * kFragBytes,
-               p.vectors + at * kDeltaVectors<C>);
+    next.template fetch<decltype(P)::value, decltype(N)::value>(
+        p, start + i * C, end, p.frags + (at * (3 * NF) + NF) * kFragBytes, p.vectors + at * kDeltaVectors<C>);
   };
   const int32_t chunks = (end - start + C - 1) / C;
   wait_for_all();
-  if (chunks > 0) fetch(chunks - 1);
+  if (chunks > 0) fetch(chunks - 1, std::integral_constant<int, 0>(), std::integral_constant<int, 1>());
   for (int32_t i = chunks - 1; i >= 0; --i) {
     __syncthreads();
     next.stage(l, p, end - (start + i * C));
     __syncthreads();
-    if (i > 0) fetch(i - 1);
-    state_columns<true>(s, a.dstates + ((int64_t)(row0 + i) * p.heads + h) * KV, p.K, p.V, col, ends);
-    f32x4 u[NT], none[NT];     // K dS, then dU, then dR
-    typename T::Exact go[CS];  // dO
-    typename T::Split tri[NF], us[CS];
-    rows_times_state<D, Rows, KS, NT, false>(l.k, l.q, s, u, none, lane, [&] {
+    const int64_t at = (int64_t)(row0 + i) * p.heads + h;
+    float* mark = a.dstates + at * KV;
+    f32x4 u[NC][NT], none[NC][NT];  // K dS, then dU, then dR
+    typename T::Exact go[NC][CS];   // dO
+    typename T::Split tri[NF], us[NC][CS];
+    rows_times_state<D, Rows, KS, NT, NC, false>(
+        l.k, l.q, s, u, none, lane,
+        [&] {
 #pragma unroll
-      for (int c = 0; c < CS; ++c) go[c] = Cols::cols(l.x, 32 * c, c16, lane);
-      load_triangle<D>(tri, l.f + NF * kFragBytes, lane);
-    });
+          for (int n = 0; n < NC; ++n)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) u[t] *= lds4(l.v + C + 16 * t + 4 * g);
+            for (int c = 0; c < CS; ++c) go[n][c] = Cols::cols(l.x, 32 * c, c16 + 16 * n, lane);
+          load_triangle<D>(tri, l.f + NF * kFragBytes, lane);
+        },
+        [&](auto P) {
+          // the first chunk fetches itself again: a branch here would make loads wait
+          fetch(max(i - 1, 0), P, std::integral_constant<int, PIECES>());
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
+            state_columns<true, decltype(P)::value, PIECES>(s[n], mark, p.K, p.V, col(n), ends(n));
+        });
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const f32x4 left = lds4(l.v + C + 16 * t + 4 * g);
+#pragma unroll
+      for (int n = 0; n < NC; ++n) u[n][t] *= left;
+    }
     triangle_times<D, false>(tri, go, u);
     keep_order();
     load_triangle<D>(tri, l.f, lane);
     keep_order();
-#pragma unroll
-    for (int c = 0; c < CS; ++c) us[c] = T::split(u[2 * c], u[2 * c + 1]);
+    split_tiles<D>(u, us);
     const float whole = l.v[C - 1];
+    typename T::Fine fine[NC][CS];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) s[t] *= whole;
-    typename T::Fine fine[CS];
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int t = 0; t < KT; ++t) s[n][t] *= whole;
 #pragma unroll
     for (int c = 0; c < CS; ++c) {
-      f32x4 y[2];
+      f32x4 gam[2];
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const f32x4 gam = lds4(l.v + 32 * c + 16 * o + 4 * g) * p.scale;
+      for (int o = 0; o < 2; ++o) gam[o] = lds4(l.v + 32 * c + 16 * o + 4 * g) * p.scale;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[o][e] = gam[e] * T::value(go[c], 4 * o + e);
+      for (int n = 0; n < NC; ++n) {
+        f32x4 y[2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e / 4][e % 4] = gam[e / 4][e % 4] * T::value(go[n][c], e);
+        fine[n][c] = T::fine(y[0], y[1]);
       }
-      fine[c] = T::fine(y[0], y[1]);
     }
     triangle_times<D, false>(tri, us, u);
     keep_order();
     cols_times<D, Rows>(l.q, fine, s, lane);
-    if (cols0 + c16 < p.V) {
-      f32x4* to = delta_row_tiles<C>(a.drows, (int64_t)(row0 + i) * p.heads + h, p.V, (cols0 + c16) / 16, lane);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) to[64 * t] = u[t];
+    for (int n = 0; n < NC; ++n) {
+      if (ends(n) - 16 >= p.V) continue;
+      f32x4* to = delta_row_tiles<C>(a.drows, at, p.V, ends(n) / 16 - 1, lane);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) to[64 * t] = u[n][t];
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-      u[t] *= -(lds4(l.v + 16 * t + 4 * g) * lds4(l.v + 2 * C + 16 * t + 4 * g));
+    for (int t = 0; t < NT; ++t) {
+      const f32x4 gb = lds4(l.v + 16 * t + 4 * g) * lds4(l.v + 2 * C + 16 * t + 4 * g);
 #pragma unroll
-    for (int c = 0; c < CS; ++c) fine[c] = T::fine(u[2 * c], u[2 * c + 1]);
+      for (int n = 0; n < NC; ++n) u[n][t] *= -gb;
+    }
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int c = 0; c < CS; ++c) fine[n][c] = T::fine(u[n][2 * c], u[n][2 * c + 1]);
     cols_times<D, Rows>(l.k, fine, s, lane);
   }
   if (a.dinitial) {
     if (!(p.has && p.has[b])) {
 #pragma unroll
-      for (int t = 0; t < KT; ++t) s[t] = zero4();
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int t = 0; t < KT; ++t) s[n][t] = zero4();
     }
-    state_columns<true>(s, a.dinitial + slot * a.di_slot + h * KV, p.K, p.V, col, ends);
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+      state_columns<true, 0, 1>(s[n], a.dinitial + slot * a.di_slot + h * KV, p.K, p.V, col(n), ends(n));
   }
 }
 
@@ -291,12 +327,12 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
       float vec = 0.f;
       if (first) vec = p.vectors[at * kDeltaVectors<C> + min(tid, kDeltaVectors<C> - 1)];
       static_assert(kDeltaVectors<C> <= THREADS || KP == 64, "a vector entry a thread");
-      f32x4 st[KT], y[NT];  // S0's columns, dR
+      f32x4 st[1][KT], y[NT];  // S0's columns, dR
 #pragma unroll
-      for (int t = 0; t < KT; ++t) st[t] = zero4();
+      for (int t = 0; t < KT; ++t) st[0][t] = zero4();
 #pragma unroll
       for (int t = 0; t < NT; ++t) y[t] = zero4();
-      state_columns<false>(st, s0, p.K, p.V, col, v0 + c16 + 16);
+      state_columns<false, 0, 1>(st[0], s0, p.K, p.V, col, v0 + c16 + 16);
       if (v0 + c16 < p.V) {
         const f32x4* from = delta_row_tiles<C>(a.drows, at, p.V, (v0 + c16) / 16, lane);
 #pragma unroll
@@ -321,14 +357,15 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
           l.v[x] = x == tid ? vec : p.vectors[at * kDeltaVectors<C> + x];
       }
       __syncthreads();
-      f32x4 u[NT], none[NT];
+      f32x4 u1[1][NT], none[1][NT];
+      f32x4(&u)[NT] = u1[0];
       typename T::Exact vv[CS];
       typename T::Split tri[NF];
-      rows_times_state<D, Rows, KS, NT, false>(l.k, l.q, st, u, none, lane, [&] {
+      rows_times_state<D, Rows, KS, NT, 1, false>(l.k, l.q, st, u1, none, lane, [&] {
 #pragma unroll
         for (int c = 0; c < CS; ++c) vv[c] = Rows::cols(l.u, 32 * c, c16, lane);
         load_triangle<D>(tri, l.f, lane);
-      });
+      }, [](auto) {});
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const f32x4 gam = lds4(l.v + 16 * t + 4 * g), bt = lds4(l.v + 2 * C + 16 * t + 4 * g);
@@ -343,10 +380,9 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         }
       }
       {
-        typename T::Split us[CS];
-#pragma unroll
-        for (int c = 0; c < CS; ++c) us[c] = T::split(u[2 * c], u[2 * c + 1]);
-        triangle_times<D, true>(tri, us, u);
+        typename T::Split us[1][CS];
+        split_tiles<D>(u1, us);
+        triangle_times<D, true>(tri, us, u1);
       }
       // the first step's rows of S0 and dS1 are on their way over the barrier
       const int steps = (min(KP, p.V - v0) + 31) / 32;
@@ -584,18 +620,16 @@ template <typename D, int KP>
 static int delta_backward(const DeltaBwd& a, int64_t rows, hipStream_t stream) {
   const char* what = "gated_delta_rule_varlen_bwd";
   const DeltaParams& p = a.p;
-  hipLaunchKernelGGL((delta_prep_kernel<D, KP, true>), dim3((uint32_t)rows, p.heads), dim3(64), 0,
-                     stream, p);
-  if (int rc = check_launch(what)) return rc;
+  if (int rc = delta_prepare<D, KP, true>(what, p, rows, stream)) return rc;
   const bool vec = p.qk_vec && a.do_vec;
   if (delta_wide(p)) {
-    const dim3 grid((p.V + 127) / 128, p.heads, p.batch), threads(512);
-    if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, true>), grid, threads, 0, stream, a);
-    else hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false>), grid, threads, 0, stream, a);
+    const dim3 grid((p.V + 127) / 128, p.heads, p.batch), walk(512);
+    if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, true>), grid, walk, 0, stream, a);
+    else hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false>), grid, walk, 0, stream, a);
   } else {
-    const dim3 grid((p.V + 63) / 64, p.heads, p.batch), threads(256);
-    if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, true>), grid, threads, 0, stream, a);
-    else hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, false>), grid, threads, 0, stream, a);
+    const dim3 grid((p.V + 63) / 64, p.heads, p.batch), walk(256);
+    if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, true>), grid, walk, 0, stream, a);
+    else hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, false>), grid, walk, 0, stream, a);
   }
   if (int rc = check_launch(what)) return rc;
   const dim3 chunks((uint32_t)rows, p.heads / p.group), threads(4 * KP);
