@@ -101,7 +101,7 @@ template <int C, bool GRAD> constexpr int kPrepFrags = (GRAD ? 3 : 2) * kDeltaFr
 // One wave a chunk and value head.  Bound by latency: three waves a SIMD are
 // what the LDS of a triangle leaves room for.
 template <typename D, int KP, bool GRAD, bool VEC>
-__global__ __launch_bounds__(64, 3) void delta_prep_kernel(DeltaParams p) {
+__global__ __launch_bounds__(64, VEC ? 3 : 2) void delta_prep_kernel(DeltaParams p) {
   using T = Tile<D>;
   using S = typename D::storage;
   constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, NF = kDeltaFrags<C>;

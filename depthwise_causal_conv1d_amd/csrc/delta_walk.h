@@ -1,7 +1,13 @@
 // delta_walk.h -- how the kernels that walk a sequence's chunks bring a chunk
 // into LDS: K, Q, two sets of frags, three vectors and the workgroup's columns
-// of one more tensor.  A chunk's loads are issued before the chunk ahead of it
-// is worked on and wait in registers meanwhile.
+// of one more tensor.
+//
+// Where the walks fill the chip (eight waves a workgroup), a chunk's loads go
+// out between the products of the chunk ahead of it and wait in registers.
+// Where they do not, a chain of chunks is what takes the time: four waves
+// compute and four more load, stage into a second buffer and store outputs
+// meanwhile (2 x 8192 tokens of 16 heads bf16, forward and backward walk: 597 and
+// 640 us without them).
 #pragma once
 
 #include "delta_rule.h"
@@ -9,11 +15,11 @@
 
 namespace sconv {
 
-template <typename D, int KP, int NW, int NC> struct WalkLds {
+template <typename D, int KP, int NW> struct WalkLds {
   using S = typename D::storage;
   static constexpr int C = kDeltaChunk<D>;
   using Rows = LdsRows<D, KP>;
-  using Cols = LdsRows<D, 16 * NW * NC>;
+  using Cols = LdsRows<D, 16 * NW>;
   __attribute__((aligned(16))) S k[C * Rows::LD];
   __attribute__((aligned(16))) S q[C * Rows::LD];
   __attribute__((aligned(16))) S x[C * Cols::LD];
@@ -21,12 +27,12 @@ template <typename D, int KP, int NW, int NC> struct WalkLds {
   __attribute__((aligned(16))) float v[3 * C];
 };
 
-template <typename D, int KP, int NW, int NC, bool VEC> struct WalkStage {
-  using L = WalkLds<D, KP, NW, NC>;
+template <typename D, int KP, int NW, bool VEC> struct WalkStage {
+  using L = WalkLds<D, KP, NW>;
   using S = typename D::storage;
   using E = typename Tile<D>::Exact;
   static constexpr int C = L::C, THREADS = 64 * NW;
-  static constexpr int XW = 2 * NW * NC;  // octets of a row of x
+  static constexpr int XW = 2 * NW;  // octets of a row of x
   static constexpr int KN = C * KP / 8, XN = C * XW, FN = 2 * kDeltaFrags<C> * kFragBytes / 16;
   static constexpr int KO = (KN + THREADS - 1) / THREADS, XO = XN / THREADS, FO = FN / THREADS;
   static_assert(XN % THREADS == 0 && FN % THREADS == 0 && 3 * C <= THREADS);
@@ -40,6 +46,7 @@ template <typename D, int KP, int NW, int NC, bool VEC> struct WalkStage {
   const S *tk, *tq, *tx;  // the heads' first rows
   int64_t x_t;
   int32_t col0;
+  int id;      // of THREADS
   bool whole;  // no row ends inside the tiles
 
   static __device__ __forceinline__ void columns(uint32_t (&c)[2], int c0, int W) {
@@ -47,11 +54,12 @@ template <typename D, int KP, int NW, int NC, bool VEC> struct WalkStage {
     c[1] = (uint32_t)(c0 + 4 < W ? c0 + 4 : 0) * (uint32_t)sizeof(S);
   }
   __device__ __forceinline__ void init(const DeltaParams& p, const S* k_, const S* q_, const S* x_,
-                                       int64_t x_t_, int32_t col0_) {
+                                       int64_t x_t_, int32_t col0_, int id_) {
+    id = id_;
     tk = k_, tq = q_, tx = x_, x_t = x_t_, col0 = col0_;
-    whole = p.K == KP && col0 + 16 * NW * NC <= p.V;
-    columns(k_c, threadIdx.x % (KP / 8) * 8, p.K);
-    columns(x_c, col0 + threadIdx.x % XW * 8, p.V);
+    whole = p.K == KP && col0 + 16 * NW <= p.V;
+    columns(k_c, id % (KP / 8) * 8, p.K);
+    columns(x_c, col0 + id % XW * 8, p.V);
   }
   static __device__ __forceinline__ E at(const S* rows, uint32_t row, const uint32_t (&c)[2]) {
     if constexpr (sizeof(S) == 2)
@@ -72,7 +80,7 @@ template <typename D, int KP, int NW, int NC, bool VEC> struct WalkStage {
     const int32_t last = end - t0 - 1;
     constexpr int ALL = 2 * KO + XO + FO + 1, LO = ALL * P / N, HI = ALL * (P + 1) / N;
     // hidden, or all these addresses would be made ahead of the loop and held
-    const int tid = VEC ? (int)threadIdx.x : (int)lane_offset(threadIdx.x);
+    const int tid = VEC ? id : (int)lane_offset(id);
     auto rows = [&](const S* m, int64_t ld, int i, int wide, const uint32_t (&c)[2], int c0, int W) {
       const int t = i / wide;
       if constexpr (VEC) return at(m, (uint32_t)min(t, last) * (uint32_t)ld * (uint32_t)sizeof(S), c);
@@ -88,15 +96,15 @@ template <typename D, int KP, int NW, int NC, bool VEC> struct WalkStage {
         x[n - 2 * KO] = rows(rx, x_t, tid + (n - 2 * KO) * THREADS, XW, x_c, col0, p.V);
       } else if (n < 2 * KO + XO + FO) {
         const int o = n - 2 * KO - XO;
-        f[o] = *reinterpret_cast<const u32x4*>(in_row(frags + o * THREADS * 16, threadIdx.x * 16u));
+        f[o] = *reinterpret_cast<const u32x4*>(in_row(frags + o * THREADS * 16, id * 16u));
       } else {
-        v = *in_row(vectors, (threadIdx.x < 3 * C ? threadIdx.x : 0) * 4u);
+        v = *in_row(vectors, (id < 3 * C ? id : 0) * 4u);
       }
     }
   }
   // len: tokens of the chunk
   template <bool MASK> __device__ __forceinline__ void stage_rows(L& l, const DeltaParams& p, int32_t len) const {
-    const int tid = MASK ? (int)lane_offset(threadIdx.x) : threadIdx.x;
+    const int tid = MASK ? (int)lane_offset(id) : id;
 #pragma unroll
     for (int o = 0; o < KO; ++o) {
       const int i = tid + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
@@ -116,10 +124,28 @@ template <typename D, int KP, int NW, int NC, bool VEC> struct WalkStage {
     if (whole && len >= C) stage_rows<false>(l, p, len);
     else stage_rows<true>(l, p, len);
 #pragma unroll
-    for (int o = 0; o < FO; ++o) reinterpret_cast<u32x4*>(l.f)[threadIdx.x + o * THREADS] = f[o];
-    if (threadIdx.x < 3 * C) l.v[threadIdx.x] = v;
+    for (int o = 0; o < FO; ++o) reinterpret_cast<u32x4*>(l.f)[id + o * THREADS] = f[o];
+    if (id < 3 * C) l.v[id] = v;
   }
 };
+
+// Rows t0 .. end - 1 of an output that waits in x, to memory.
+template <typename Stage, typename D, bool VEC>
+__device__ __forceinline__ void put_rows(const typename Stage::L& l, typename D::storage* out, int64_t ld, int32_t V,
+                                         int32_t cols0, int32_t t0, int32_t end, int id) {
+  using S = typename D::storage;
+#pragma unroll
+  for (int o = 0; o < Stage::XO; ++o) {
+    const int x = id + o * Stage::THREADS, t = x / Stage::XW, c0 = x % Stage::XW * 8;
+    if (t < end - t0) {
+      const auto y = Stage::L::Cols::get8(l.x, t, c0);
+      if constexpr (VEC)
+        put_row8<D>(in_row(out + t0 * ld, (uint32_t)t * (uint32_t)ld * (uint32_t)sizeof(S)), cols0 + c0, V, true, y);
+      else
+        put_row8<D>(out + (int64_t)(t0 + t) * ld, cols0 + c0, V, false, y);
+    }
+  }
+}
 
 // Ends what is in flight: loads ahead of a loop would make their registers'
 // first use inside it a wait for the loop's own.
@@ -149,31 +175,26 @@ __device__ __forceinline__ void state_columns(f32x4 (&s)[KT], std::conditional_t
   else all([&](int k) { return k < K && col < V; });
 }
 
-// The products of a chunk's K (and Q) with 16 NC columns of a state: x = K S, y
+// The products of a chunk's K (and Q) with 16 columns of a state: x = K S, y
 // = Q S.  K's and Q's operands alternate, each loaded while the other's products
 // run; `last` loads what comes next, behind the last of them.  piece(j) issues
 // what else there is for memory, j of kGroups.
 template <int KS, bool BOTH> constexpr int kGroups = BOTH ? 2 * KS : KS;
-template <typename D, typename Rows, int KS, int NT, int NC, bool BOTH, typename F, typename G>
+template <typename D, typename Rows, int KS, int NT, bool BOTH, typename F, typename G>
 __device__ __forceinline__ void rows_times_state(const typename D::storage* lk, const typename D::storage* lq,
-                                                 const f32x4 (&s)[NC][2 * KS], f32x4 (&x)[NC][NT],
-                                                 f32x4 (&y)[NC][NT], int lane, F&& last, G&& piece) {
+                                                 const f32x4 (&s)[2 * KS], f32x4 (&x)[NT],
+                                                 f32x4 (&y)[NT], int lane, F&& last, G&& piece) {
   using T = Tile<D>;
   typename T::Exact kf[2][NT], qf[NT];
-  typename T::Split sp[2][NC];
+  typename T::Split sp[2];
   auto load = [&](const typename D::storage* m, int c, typename T::Exact (&to)[NT]) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) to[t] = Rows::rows(m, 16 * t, 32 * c, lane);
   };
-  auto split = [&](int c) {
-#pragma unroll
-    for (int n = 0; n < NC; ++n) sp[c & 1][n] = T::split(s[n][2 * c], s[n][2 * c + 1]);
-  };
+  auto split = [&](int c) { sp[c & 1] = T::split(s[2 * c], s[2 * c + 1]); };
   load(lk, 0, kf[0]);
 #pragma unroll
-  for (int n = 0; n < NC; ++n)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) x[n][t] = y[n][t] = zero4();
+  for (int t = 0; t < NT; ++t) x[t] = y[t] = zero4();
   split(0);
   each_part<KS>([&](auto c) {
     constexpr int B = BOTH ? 0 : 1;  // K alone: its own operands alternate
@@ -188,9 +209,7 @@ __device__ __forceinline__ void rows_times_state(const typename D::storage* lk, 
     if constexpr (!BOTH && c + 1 < KS) split(c + 1);
     each_part<T::kExactSplit>([&](auto P) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int n = 0; n < NC; ++n) x[n][t] = T::template part<P>(kf[c & B][t], sp[c & 1][n], x[n][t]);
+      for (int t = 0; t < NT; ++t) x[t] = T::template part<P>(kf[c & B][t], sp[c & 1], x[t]);
     });
     keep_order();
     if constexpr (BOTH) {
@@ -201,9 +220,7 @@ __device__ __forceinline__ void rows_times_state(const typename D::storage* lk, 
       if constexpr (c + 1 < KS) split(c + 1);
       each_part<T::kExactSplit>([&](auto P) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int n = 0; n < NC; ++n) y[n][t] = T::template part<P>(qf[t], sp[c & 1][n], y[n][t]);
+        for (int t = 0; t < NT; ++t) y[t] = T::template part<P>(qf[t], sp[c & 1], y[t]);
       });
       keep_order();
     }
@@ -212,9 +229,9 @@ __device__ __forceinline__ void rows_times_state(const typename D::storage* lk, 
 
 // x += (the triangle's frags) y: lower rows meet columns of steps c <= t / 2,
 // upper ones c >= t / 2.
-template <typename D, bool LOWER, int NF, typename Y, int NT, int NC>
+template <typename D, bool LOWER, int NF, typename Y, int NT>
 __device__ __forceinline__ void triangle_times(const typename Tile<D>::Split (&tri)[NF],
-                                               const Y (&y)[NC][NT / 2], f32x4 (&x)[NC][NT]) {
+                                               const Y (&y)[NT / 2], f32x4 (&x)[NT]) {
   using T = Tile<D>;
   constexpr int C = 16 * NT, CS = NT / 2;
   constexpr int N = std::is_same<Y, typename T::Split>::value ? T::kSplitSplit : T::kSplitExact;
@@ -222,10 +239,8 @@ __device__ __forceinline__ void triangle_times(const typename Tile<D>::Split (&t
     constexpr int c = P / N;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int n = 0; n < NC; ++n)
-        if (LOWER ? c <= t / 2 : c >= t / 2)
-          x[n][t] = T::template part<P % N>(tri[LOWER ? lower_frag<C>(t, c) : upper_frag<C>(t, c)], y[n][c], x[n][t]);
+      if (LOWER ? c <= t / 2 : c >= t / 2)
+        x[t] = T::template part<P % N>(tri[LOWER ? lower_frag<C>(t, c) : upper_frag<C>(t, c)], y[c], x[t]);
   });
 }
 
@@ -235,19 +250,23 @@ __device__ __forceinline__ void load_triangle(typename Tile<D>::Split (&tri)[NF]
   for (int x = 0; x < NF; ++x) tri[x] = Tile<D>::get(f + x * kFragBytes, lane);
 }
 
-template <typename D, int NT, int NC>
-__device__ __forceinline__ void split_tiles(const f32x4 (&u)[NC][NT], typename Tile<D>::Split (&o)[NC][NT / 2]) {
+template <typename D, int NT>
+__device__ __forceinline__ void split_tiles(const f32x4 (&u)[NT], typename Tile<D>::Split (&o)[NT / 2]) {
 #pragma unroll
-  for (int n = 0; n < NC; ++n)
-#pragma unroll
-    for (int c = 0; c < NT / 2; ++c) o[n][c] = Tile<D>::split(u[n][2 * c], u[n][2 * c + 1]);
+  for (int c = 0; c < NT / 2; ++c) o[c] = Tile<D>::split(u[2 * c], u[2 * c + 1]);
 }
 
-// s += M^T u for M's rows in LDS, 16 NC columns of u; half of M's operands are
+template <typename D, int NT>
+__device__ __forceinline__ void fine_tiles(const f32x4 (&u)[NT], typename Tile<D>::Fine (&o)[NT / 2]) {
+#pragma unroll
+  for (int c = 0; c < NT / 2; ++c) o[c] = Tile<D>::fine(u[2 * c], u[2 * c + 1]);
+}
+
+// s += M^T u for M's rows in LDS, 16 columns of u; half of M's operands are
 // loaded while the other half's products run.
-template <typename D, typename Rows, int KT, int CS, int NC>
+template <typename D, typename Rows, int KT, int CS>
 __device__ __forceinline__ void cols_times(const typename D::storage* m,
-                                           const typename Tile<D>::Fine (&u)[NC][CS], f32x4 (&s)[NC][KT],
+                                           const typename Tile<D>::Fine (&u)[CS], f32x4 (&s)[KT],
                                            int lane) {
   using T = Tile<D>;
   constexpr int H = KT / 2;
@@ -263,12 +282,10 @@ __device__ __forceinline__ void cols_times(const typename D::storage* m,
     keep_order();
     each_part<T::kExactFine>([&](auto P) {
 #pragma unroll
-      for (int t = 0; t < H; ++t)
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          f32x4& to = s[n][H * (i & 1) + t];
-          to = T::template part<P>(f[i & 1][t], u[n][i / 2], to);
-        }
+      for (int t = 0; t < H; ++t) {
+        f32x4& to = s[H * (i & 1) + t];
+        to = T::template part<P>(f[i & 1][t], u[i / 2], to);
+      }
     });
     keep_order();
   }

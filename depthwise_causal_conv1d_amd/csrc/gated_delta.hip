@@ -16,18 +16,19 @@ struct DeltaFwd {
   int32_t o_vec;
 };
 
-// One workgroup walks a sequence's chunks for one value head, 16 NC columns a
-// wave.  An output chunk waits in LDS, in V's place, for the next one's staging.
-template <typename D, int KP, int NW, bool VEC>
-__global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a) {
+// One workgroup walks a sequence's chunks for one value head, 16 columns a
+// wave of NW; LOAD: as many waves more load and store.  An output chunk waits in
+// LDS, in V's place, for the next one's staging.
+template <typename D, int KP, int NW, bool LOAD, bool VEC>
+__global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kernel(DeltaFwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
   constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32;
-  constexpr int NC = 1, NF = kDeltaFrags<C>, PIECES = kGroups<KS, true>;
-  using Stage = WalkStage<D, KP, NW, NC, VEC>;
+  constexpr int NF = kDeltaFrags<C>, PIECES = kGroups<KS, true>;
+  using Stage = WalkStage<D, KP, NW, VEC>;
   using Rows = typename Stage::L::Rows;
   using Cols = typename Stage::L::Cols;
-  __shared__ typename Stage::L l;
+  __shared__ typename Stage::L lds[LOAD ? 2 : 1];
 
   const DeltaParams& p = a.p;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -35,90 +36,85 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a)
   const int32_t slot = p.slots ? p.slots[b] : b;
   if (p.slots && slot == p.pad) return;
   const int32_t start = p.qsl[b], end = p.qsl[b + 1];
-  const int32_t cols0 = blockIdx.x * 16 * NW * NC, c16 = 16 * NC * wave;
+  const int32_t cols0 = blockIdx.x * 16 * NW;
+  const int32_t chunks = (end - start + C - 1) / C, row0 = start / C + b;
   const int64_t KV = (int64_t)p.K * p.V;
-
-  f32x4 s[NC][KT];
-#pragma unroll
-  for (int n = 0; n < NC; ++n)
-#pragma unroll
-    for (int t = 0; t < KT; ++t) s[n][t] = zero4();
-  auto col = [&](int n) { return cols0 + c16 + 16 * n + r; };
-  auto ends = [&](int n) { return cols0 + c16 + 16 * n + 16; };
-  float* state = a.states ? a.states + slot * a.st_slot + h * KV : nullptr;
-  if (p.has && p.has[b]) {
-#pragma unroll
-    for (int n = 0; n < NC; ++n) state_columns<false, 0, 1>(s[n], state, p.K, p.V, col(n), ends(n));
-  }
-
   const S* q = static_cast<const S*>(p.q) + kh * p.q_h;
   const S* k = static_cast<const S*>(p.k) + kh * p.k_h;
   const S* v = static_cast<const S*>(p.v) + h * p.v_h;
   S* out = static_cast<S*>(a.out) + h * a.o_h;
-  const int32_t row0 = start / C + b;
   Stage next;
-  next.init(p, k, q, v, p.v_t, cols0);
+  const int id = threadIdx.x % Stage::THREADS;
+  next.init(p, k, q, v, p.v_t, cols0, id);
   auto fetch = [&](int32_t i, auto P, auto N) {
     const int64_t at = (int64_t)(row0 + i) * p.heads + h;
     next.template fetch<decltype(P)::value, decltype(N)::value>(
         p, start + i * C, end, p.frags + at * (2 * NF) * kFragBytes, p.vectors + at * kDeltaVectors<C>);
   };
-  auto put_out = [&](int32_t i) {
-    const int32_t t0 = start + i * C;
-#pragma unroll
-    for (int o = 0; o < Stage::XO; ++o) {
-      const int x = threadIdx.x + o * Stage::THREADS, t = x / Stage::XW, c0 = x % Stage::XW * 8;
-      if (t < end - t0) {
-        const auto y = Cols::get8(l.x, t, c0);
-        if constexpr (VEC)
-          put_row8<D>(in_row(out + t0 * a.o_t, (uint32_t)t * (uint32_t)a.o_t * (uint32_t)sizeof(S)),
-                      cols0 + c0, p.V, true, y);
-        else
-          put_row8<D>(out + (int64_t)(t0 + t) * a.o_t, cols0 + c0, p.V, false, y);
-      }
-    }
+  constexpr std::integral_constant<int, 0> kFirst;
+  constexpr std::integral_constant<int, 1> kWhole;
+  auto put_out = [&](int32_t i, const typename Stage::L& l) {
+    put_rows<Stage, D, VEC>(l, out, a.o_t, p.V, cols0, start + i * C, end, id);
   };
-  const int32_t chunks = (end - start + C - 1) / C;
+
+  if (LOAD && wave >= NW) {
+    if (chunks > 0) {
+      fetch(0, kFirst, kWhole);
+      next.stage(lds[0], p, end - start);
+    }
+    __syncthreads();
+    for (int32_t i = 0; i < chunks; ++i) {
+      // behind the last chunk it is fetched again: a branch here would make loads wait
+      fetch(min(i + 1, chunks - 1), kFirst, kWhole);
+      keep_order();
+      if (i > 0) put_out(i - 1, lds[(i + 1) & 1]);
+      if (i + 1 < chunks) next.stage(lds[(i + 1) & 1], p, end - (start + (i + 1) * C));
+      __syncthreads();
+    }
+    if (chunks > 0) put_out(chunks - 1, lds[(chunks - 1) & 1]);
+    return;
+  }
+
+  const int32_t c16 = 16 * wave, col = cols0 + c16 + r, ends = cols0 + c16 + 16;
+  f32x4 s[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t) s[t] = zero4();
+  float* state = a.states ? a.states + slot * a.st_slot + h * KV : nullptr;
+  if (p.has && p.has[b]) state_columns<false, 0, 1>(s, state, p.K, p.V, col, ends);
   wait_for_all();
-  if (chunks > 0) fetch(0, std::integral_constant<int, 0>(), std::integral_constant<int, 1>());
+  if (!LOAD && chunks > 0) fetch(0, kFirst, kWhole);
+  if (LOAD) __syncthreads();
   for (int32_t i = 0; i < chunks; ++i) {
-    __syncthreads();
-    if (i > 0) put_out(i - 1);
-    next.stage(l, p, end - (start + i * C));
-    __syncthreads();
+    typename Stage::L& l = lds[LOAD ? i & 1 : 0];
+    if constexpr (!LOAD) {
+      __syncthreads();
+      if (i > 0) put_out(i - 1, l);
+      next.stage(l, p, end - (start + i * C));
+      __syncthreads();
+    }
     float* mark = a.marks ? a.marks + ((int64_t)(row0 + i) * p.heads + h) * KV : nullptr;
-    f32x4 u[NC][NT], y[NC][NT];  // K S, then R, then U; Q S, then O
-    typename T::Exact vv[NC][CS];
-    typename T::Split tri[NF], us[NC][CS];
-    rows_times_state<D, Rows, KS, NT, NC, true>(
+    f32x4 u[NT], y[NT];  // K S, then R, then U; Q S, then O
+    typename T::Exact vv[CS];
+    typename T::Split tri[NF], us[CS];
+    rows_times_state<D, Rows, KS, NT, true>(
         l.k, l.q, s, u, y, lane,
         [&] {
 #pragma unroll
-          for (int n = 0; n < NC; ++n)
-#pragma unroll
-            for (int c = 0; c < CS; ++c) vv[n][c] = Cols::cols(l.x, 32 * c, c16 + 16 * n, lane);
+          for (int c = 0; c < CS; ++c) vv[c] = Cols::cols(l.x, 32 * c, c16, lane);
           load_triangle<D>(tri, l.f, lane);
         },
         [&](auto P) {
-          // the last chunk fetches itself again: a branch here would make loads wait
-          fetch(min(i + 1, chunks - 1), P, std::integral_constant<int, PIECES>());
-          if (mark) {
-#pragma unroll
-            for (int n = 0; n < NC; ++n)
-              state_columns<true, decltype(P)::value, PIECES>(s[n], mark, p.K, p.V, col(n), ends(n));
-          }
+          if constexpr (!LOAD) fetch(min(i + 1, chunks - 1), P, std::integral_constant<int, PIECES>());
+          if (mark) state_columns<true, decltype(P)::value, PIECES>(s, mark, p.K, p.V, col, ends);
         });
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const f32x4 gam = lds4(l.v + 16 * t + 4 * g), bt = lds4(l.v + 2 * C + 16 * t + 4 * g);
-      const f32x4 sg = gam * p.scale;
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          u[n][t][e] = bt[e] * (T::value(vv[n][t / 2], 4 * (t & 1) + e) - gam[e] * u[n][t][e]);
-          y[n][t][e] *= sg[e];
-        }
+      for (int e = 0; e < 4; ++e) {
+        u[t][e] = bt[e] * (T::value(vv[t / 2], 4 * (t & 1) + e) - gam[e] * u[t][e]);
+        y[t][e] *= p.scale * gam[e];
+      }
     }
     split_tiles<D>(u, us);
     triangle_times<D, true>(tri, us, u);
@@ -127,37 +123,27 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_walk_kernel(DeltaFwd a)
     keep_order();
     split_tiles<D>(u, us);
     const float whole = l.v[C - 1];
-    typename T::Fine fine[NC][CS];
+    typename T::Fine fine[CS];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const f32x4 left = lds4(l.v + C + 16 * t + 4 * g);
+    for (int t = 0; t < NT; ++t) u[t] *= lds4(l.v + C + 16 * t + 4 * g);
+    fine_tiles<D>(u, fine);
 #pragma unroll
-      for (int n = 0; n < NC; ++n) u[n][t] *= left;
-    }
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-#pragma unroll
-      for (int c = 0; c < CS; ++c) fine[n][c] = T::fine(u[n][2 * c], u[n][2 * c + 1]);
-#pragma unroll
-      for (int t = 0; t < KT; ++t) s[n][t] *= whole;
-    }
+    for (int t = 0; t < KT; ++t) s[t] *= whole;
     triangle_times<D, true>(tri, us, y);
     keep_order();
     cols_times<D, Rows>(l.k, fine, s, lane);
 #pragma unroll
-    for (int n = 0; n < NC; ++n)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          l.x[(16 * t + 4 * g + e) * Cols::LD + Cols::pos(c16 + 16 * n + r)] = delta_round<D>(y[n][t][e]);
+      for (int e = 0; e < 4; ++e)
+        l.x[(16 * t + 4 * g + e) * Cols::LD + Cols::pos(c16 + r)] = delta_round<D>(y[t][e]);
+    if (LOAD) __syncthreads();
   }
-  __syncthreads();
-  if (chunks > 0) put_out(chunks - 1);
-  if (state) {
-#pragma unroll
-    for (int n = 0; n < NC; ++n) state_columns<true, 0, 1>(s[n], state, p.K, p.V, col(n), ends(n));
+  if constexpr (!LOAD) {
+    __syncthreads();
+    if (chunks > 0) put_out(chunks - 1, lds[0]);
   }
+  if (state) state_columns<true, 0, 1>(s, state, p.K, p.V, col, ends);
 }
 
 // ---------------------------------------------------------------- one token
@@ -257,14 +243,15 @@ static int delta_forward(const DeltaFwd& a, int64_t rows, hipStream_t stream) {
   const DeltaParams& p = a.p;
   if (int rc = delta_prepare<D, KP, false>("gated_delta_rule_varlen_fwd", p, rows, stream)) return rc;
   const bool vec = p.qk_vec && p.v_vec && a.o_vec;
+  const dim3 threads(512);
   if (delta_wide(p)) {
-    const dim3 grid((p.V + 127) / 128, p.heads, p.batch), threads(512);
-    if (vec) hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8, true>), grid, threads, 0, stream, a);
-    else hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8, false>), grid, threads, 0, stream, a);
+    const dim3 grid((p.V + 127) / 128, p.heads, p.batch);
+    if (vec) hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8, false, true>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8, false, false>), grid, threads, 0, stream, a);
   } else {
-    const dim3 grid((p.V + 63) / 64, p.heads, p.batch), threads(256);
-    if (vec) hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4, true>), grid, threads, 0, stream, a);
-    else hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4, false>), grid, threads, 0, stream, a);
+    const dim3 grid((p.V + 63) / 64, p.heads, p.batch);
+    if (vec) hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4, true, true>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4, true, false>), grid, threads, 0, stream, a);
   }
   return check_launch("gated_delta_rule_varlen_fwd");
 }

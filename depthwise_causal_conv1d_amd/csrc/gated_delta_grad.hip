@@ -44,17 +44,17 @@ __device__ __forceinline__ f32x4* delta_row_tiles(float* drows, int64_t at, int3
 }
 
 // One workgroup walks a sequence's chunks from the last, for one value head
-// and 16 NC columns a wave.
-template <typename D, int KP, int NW, bool VEC>
-__global__ __launch_bounds__(64 * NW, NW / 4) void delta_back_kernel(DeltaBwd a) {
+// and 16 columns a wave of NW; LOAD: as many waves more load.
+template <typename D, int KP, int NW, bool LOAD, bool VEC>
+__global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kernel(DeltaBwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
   constexpr int C = kDeltaChunk<D>, NT = C / 16, KS = KP / 32, KT = KP / 16, CS = C / 32;
-  constexpr int NC = 1, NF = kDeltaFrags<C>, PIECES = kGroups<KS, false>;
-  using Stage = WalkStage<D, KP, NW, NC, VEC>;
+  constexpr int NF = kDeltaFrags<C>, PIECES = kGroups<KS, false>;
+  using Stage = WalkStage<D, KP, NW, VEC>;
   using Rows = typename Stage::L::Rows;
   using Cols = typename Stage::L::Cols;
-  __shared__ typename Stage::L l;
+  __shared__ typename Stage::L lds[LOAD ? 2 : 1];
 
   const DeltaParams& p = a.p;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -62,122 +62,112 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void delta_back_kernel(DeltaBwd a)
   const int32_t slot = p.slots ? p.slots[b] : b;
   if (p.slots && slot == p.pad) return;
   const int32_t start = p.qsl[b], end = p.qsl[b + 1];
-  const int32_t cols0 = blockIdx.x * 16 * NW * NC, c16 = 16 * NC * wave;
+  const int32_t cols0 = blockIdx.x * 16 * NW;
+  const int32_t chunks = (end - start + C - 1) / C, row0 = start / C + b;
   const int64_t KV = (int64_t)p.K * p.V;
-
-  f32x4 s[NC][KT];
-#pragma unroll
-  for (int n = 0; n < NC; ++n)
-#pragma unroll
-    for (int t = 0; t < KT; ++t) s[n][t] = zero4();
-  auto col = [&](int n) { return cols0 + c16 + 16 * n + r; };
-  auto ends = [&](int n) { return cols0 + c16 + 16 * n + 16; };
-  if (a.dfinal) {
-#pragma unroll
-    for (int n = 0; n < NC; ++n)
-      state_columns<false, 0, 1>(s[n], a.dfinal + slot * a.df_slot + h * KV, p.K, p.V, col(n), ends(n));
-  }
   const S* q = static_cast<const S*>(p.q) + kh * p.q_h;
   const S* k = static_cast<const S*>(p.k) + kh * p.k_h;
   const S* dout = static_cast<const S*>(a.dout) + h * a.do_h;
-  const int32_t row0 = start / C + b;
   Stage next;
-  next.init(p, k, q, dout, a.do_t, cols0);
+  next.init(p, k, q, dout, a.do_t, cols0, threadIdx.x % Stage::THREADS);
   auto fetch = [&](int32_t i, auto P, auto N) {
     const int64_t at = (int64_t)(row0 + i) * p.heads + h;
     next.template fetch<decltype(P)::value, decltype(N)::value>(
         p, start + i * C, end, p.frags + (at * (3 * NF) + NF) * kFragBytes, p.vectors + at * kDeltaVectors<C>);
   };
-  const int32_t chunks = (end - start + C - 1) / C;
+  auto stage = [&](int32_t i, typename Stage::L& l) { next.stage(l, p, end - (start + i * C)); };
+  constexpr std::integral_constant<int, 0> kFirst;
+  constexpr std::integral_constant<int, 1> kWhole;
+
+  if (LOAD && wave >= NW) {
+    if (chunks > 0) {
+      fetch(chunks - 1, kFirst, kWhole);
+      stage(chunks - 1, lds[(chunks - 1) & 1]);
+    }
+    __syncthreads();
+    for (int32_t i = chunks - 1; i >= 0; --i) {
+      // ahead of the first chunk it is fetched again: a branch here would make loads wait
+      fetch(max(i - 1, 0), kFirst, kWhole);
+      if (i > 0) stage(i - 1, lds[(i - 1) & 1]);
+      __syncthreads();
+    }
+    return;
+  }
+
+  const int32_t c16 = 16 * wave, col = cols0 + c16 + r, ends = cols0 + c16 + 16;
+  f32x4 s[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t) s[t] = zero4();
+  if (a.dfinal) state_columns<false, 0, 1>(s, a.dfinal + slot * a.df_slot + h * KV, p.K, p.V, col, ends);
   wait_for_all();
-  if (chunks > 0) fetch(chunks - 1, std::integral_constant<int, 0>(), std::integral_constant<int, 1>());
+  if (!LOAD && chunks > 0) fetch(chunks - 1, kFirst, kWhole);
+  if (LOAD) __syncthreads();
   for (int32_t i = chunks - 1; i >= 0; --i) {
-    __syncthreads();
-    next.stage(l, p, end - (start + i * C));
-    __syncthreads();
+    typename Stage::L& l = lds[LOAD ? i & 1 : 0];
+    if constexpr (!LOAD) {
+      __syncthreads();
+      stage(i, l);
+      __syncthreads();
+    }
     const int64_t at = (int64_t)(row0 + i) * p.heads + h;
     float* mark = a.dstates + at * KV;
-    f32x4 u[NC][NT], none[NC][NT];  // K dS, then dU, then dR
-    typename T::Exact go[NC][CS];   // dO
-    typename T::Split tri[NF], us[NC][CS];
-    rows_times_state<D, Rows, KS, NT, NC, false>(
+    f32x4 u[NT], none[NT];    // K dS, then dU, then dR
+    typename T::Exact go[CS]; // dO
+    typename T::Split tri[NF], us[CS];
+    rows_times_state<D, Rows, KS, NT, false>(
         l.k, l.q, s, u, none, lane,
         [&] {
 #pragma unroll
-          for (int n = 0; n < NC; ++n)
-#pragma unroll
-            for (int c = 0; c < CS; ++c) go[n][c] = Cols::cols(l.x, 32 * c, c16 + 16 * n, lane);
+          for (int c = 0; c < CS; ++c) go[c] = Cols::cols(l.x, 32 * c, c16, lane);
           load_triangle<D>(tri, l.f + NF * kFragBytes, lane);
         },
         [&](auto P) {
-          // the first chunk fetches itself again: a branch here would make loads wait
-          fetch(max(i - 1, 0), P, std::integral_constant<int, PIECES>());
-#pragma unroll
-          for (int n = 0; n < NC; ++n)
-            state_columns<true, decltype(P)::value, PIECES>(s[n], mark, p.K, p.V, col(n), ends(n));
+          if constexpr (!LOAD) fetch(max(i - 1, 0), P, std::integral_constant<int, PIECES>());
+          state_columns<true, decltype(P)::value, PIECES>(s, mark, p.K, p.V, col, ends);
         });
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const f32x4 left = lds4(l.v + C + 16 * t + 4 * g);
-#pragma unroll
-      for (int n = 0; n < NC; ++n) u[n][t] *= left;
-    }
+    for (int t = 0; t < NT; ++t) u[t] *= lds4(l.v + C + 16 * t + 4 * g);
     triangle_times<D, false>(tri, go, u);
     keep_order();
     load_triangle<D>(tri, l.f, lane);
     keep_order();
     split_tiles<D>(u, us);
     const float whole = l.v[C - 1];
-    typename T::Fine fine[NC][CS];
+    typename T::Fine fine[CS];
 #pragma unroll
-    for (int n = 0; n < NC; ++n)
-#pragma unroll
-      for (int t = 0; t < KT; ++t) s[n][t] *= whole;
+    for (int t = 0; t < KT; ++t) s[t] *= whole;
 #pragma unroll
     for (int c = 0; c < CS; ++c) {
-      f32x4 gam[2];
+      f32x4 y[2];
 #pragma unroll
-      for (int o = 0; o < 2; ++o) gam[o] = lds4(l.v + 32 * c + 16 * o + 4 * g) * p.scale;
+      for (int o = 0; o < 2; ++o) {
+        const f32x4 gam = lds4(l.v + 32 * c + 16 * o + 4 * g) * p.scale;
 #pragma unroll
-      for (int n = 0; n < NC; ++n) {
-        f32x4 y[2];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e / 4][e % 4] = gam[e / 4][e % 4] * T::value(go[n][c], e);
-        fine[n][c] = T::fine(y[0], y[1]);
+        for (int e = 0; e < 4; ++e) y[o][e] = gam[e] * T::value(go[c], 4 * o + e);
       }
+      fine[c] = T::fine(y[0], y[1]);
     }
     triangle_times<D, false>(tri, us, u);
     keep_order();
     cols_times<D, Rows>(l.q, fine, s, lane);
+    if (ends - 16 < p.V) {
+      f32x4* to = delta_row_tiles<C>(a.drows, at, p.V, ends / 16 - 1, lane);
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      if (ends(n) - 16 >= p.V) continue;
-      f32x4* to = delta_row_tiles<C>(a.drows, at, p.V, ends(n) / 16 - 1, lane);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) to[64 * t] = u[n][t];
+      for (int t = 0; t < NT; ++t) to[64 * t] = u[t];
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const f32x4 gb = lds4(l.v + 16 * t + 4 * g) * lds4(l.v + 2 * C + 16 * t + 4 * g);
-#pragma unroll
-      for (int n = 0; n < NC; ++n) u[n][t] *= -gb;
-    }
-#pragma unroll
-    for (int n = 0; n < NC; ++n)
-#pragma unroll
-      for (int c = 0; c < CS; ++c) fine[n][c] = T::fine(u[n][2 * c], u[n][2 * c + 1]);
+    for (int t = 0; t < NT; ++t)
+      u[t] *= -(lds4(l.v + 16 * t + 4 * g) * lds4(l.v + 2 * C + 16 * t + 4 * g));
+    fine_tiles<D>(u, fine);
     cols_times<D, Rows>(l.k, fine, s, lane);
+    if (LOAD) __syncthreads();
   }
   if (a.dinitial) {
     if (!(p.has && p.has[b])) {
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
-#pragma unroll
-        for (int t = 0; t < KT; ++t) s[n][t] = zero4();
+      for (int t = 0; t < KT; ++t) s[t] = zero4();
     }
-#pragma unroll
-    for (int n = 0; n < NC; ++n)
-      state_columns<true, 0, 1>(s[n], a.dinitial + slot * a.di_slot + h * KV, p.K, p.V, col(n), ends(n));
+    state_columns<true, 0, 1>(s, a.dinitial + slot * a.di_slot + h * KV, p.K, p.V, col, ends);
   }
 }
 
@@ -327,12 +317,12 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
       float vec = 0.f;
       if (first) vec = p.vectors[at * kDeltaVectors<C> + min(tid, kDeltaVectors<C> - 1)];
       static_assert(kDeltaVectors<C> <= THREADS || KP == 64, "a vector entry a thread");
-      f32x4 st[1][KT], y[NT];  // S0's columns, dR
+      f32x4 st[KT], y[NT];  // S0's columns, dR
 #pragma unroll
-      for (int t = 0; t < KT; ++t) st[0][t] = zero4();
+      for (int t = 0; t < KT; ++t) st[t] = zero4();
 #pragma unroll
       for (int t = 0; t < NT; ++t) y[t] = zero4();
-      state_columns<false, 0, 1>(st[0], s0, p.K, p.V, col, v0 + c16 + 16);
+      state_columns<false, 0, 1>(st, s0, p.K, p.V, col, v0 + c16 + 16);
       if (v0 + c16 < p.V) {
         const f32x4* from = delta_row_tiles<C>(a.drows, at, p.V, (v0 + c16) / 16, lane);
 #pragma unroll
@@ -357,11 +347,10 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
           l.v[x] = x == tid ? vec : p.vectors[at * kDeltaVectors<C> + x];
       }
       __syncthreads();
-      f32x4 u1[1][NT], none[1][NT];
-      f32x4(&u)[NT] = u1[0];
+      f32x4 u[NT], none[NT];
       typename T::Exact vv[CS];
       typename T::Split tri[NF];
-      rows_times_state<D, Rows, KS, NT, 1, false>(l.k, l.q, st, u1, none, lane, [&] {
+      rows_times_state<D, Rows, KS, NT, false>(l.k, l.q, st, u, none, lane, [&] {
 #pragma unroll
         for (int c = 0; c < CS; ++c) vv[c] = Rows::cols(l.u, 32 * c, c16, lane);
         load_triangle<D>(tri, l.f, lane);
@@ -380,9 +369,9 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         }
       }
       {
-        typename T::Split us[1][CS];
-        split_tiles<D>(u1, us);
-        triangle_times<D, true>(tri, us, u1);
+        typename T::Split us[CS];
+        split_tiles<D>(u, us);
+        triangle_times<D, true>(tri, us, u);
       }
       // the first step's rows of S0 and dS1 are on their way over the barrier
       const int steps = (min(KP, p.V - v0) + 31) / 32;
@@ -622,14 +611,15 @@ static int delta_backward(const DeltaBwd& a, int64_t rows, hipStream_t stream) {
   const DeltaParams& p = a.p;
   if (int rc = delta_prepare<D, KP, true>(what, p, rows, stream)) return rc;
   const bool vec = p.qk_vec && a.do_vec;
+  const dim3 walk(512);
   if (delta_wide(p)) {
-    const dim3 grid((p.V + 127) / 128, p.heads, p.batch), walk(512);
-    if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, true>), grid, walk, 0, stream, a);
-    else hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false>), grid, walk, 0, stream, a);
+    const dim3 grid((p.V + 127) / 128, p.heads, p.batch);
+    if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false, true>), grid, walk, 0, stream, a);
+    else hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false, false>), grid, walk, 0, stream, a);
   } else {
-    const dim3 grid((p.V + 63) / 64, p.heads, p.batch), walk(256);
-    if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, true>), grid, walk, 0, stream, a);
-    else hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, false>), grid, walk, 0, stream, a);
+    const dim3 grid((p.V + 63) / 64, p.heads, p.batch);
+    if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, true, true>), grid, walk, 0, stream, a);
+    else hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, true, false>), grid, walk, 0, stream, a);
   }
   if (int rc = check_launch(what)) return rc;
   const dim3 chunks((uint32_t)rows, p.heads / p.group), threads(4 * KP);
