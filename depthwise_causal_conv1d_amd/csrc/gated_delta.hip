@@ -28,7 +28,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
   using Stage = WalkStage<D, KP, NW, VEC>;
   using Rows = typename Stage::L::Rows;
   using Cols = typename Stage::L::Cols;
-  __shared__ typename Stage::L lds[LOAD ? 2 : 1];
+  __shared__ typename Stage::L lds[2];
 
   const DeltaParams& p = a.p;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -82,16 +82,14 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
   float* state = a.states ? a.states + slot * a.st_slot + h * KV : nullptr;
   if (p.has && p.has[b]) state_columns<false, 0, 1>(s, state, p.K, p.V, col, ends);
   wait_for_all();
-  if (!LOAD && chunks > 0) fetch(0, kFirst, kWhole);
-  if (LOAD) __syncthreads();
+  if (!LOAD && chunks > 0) {
+    fetch(0, kFirst, kWhole);
+    next.stage(lds[0], p, end - start);
+  }
+  __syncthreads();
   for (int32_t i = 0; i < chunks; ++i) {
-    typename Stage::L& l = lds[LOAD ? i & 1 : 0];
-    if constexpr (!LOAD) {
-      __syncthreads();
-      if (i > 0) put_out(i - 1, l);
-      next.stage(l, p, end - (start + i * C));
-      __syncthreads();
-    }
+    typename Stage::L& l = lds[i & 1];
+    if (!LOAD && i > 0) put_out(i - 1, lds[(i + 1) & 1]);
     float* mark = a.marks ? a.marks + ((int64_t)(row0 + i) * p.heads + h) * KV : nullptr;
     f32x4 u[NT], y[NT];  // K S, then R, then U; Q S, then O
     typename T::Exact vv[CS];
@@ -137,12 +135,10 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         l.x[(16 * t + 4 * g + e) * Cols::LD + Cols::pos(c16 + r)] = delta_round<D>(y[t][e]);
-    if (LOAD) __syncthreads();
-  }
-  if constexpr (!LOAD) {
+    if (!LOAD && i + 1 < chunks) next.stage(lds[(i + 1) & 1], p, end - (start + (i + 1) * C));
     __syncthreads();
-    if (chunks > 0) put_out(chunks - 1, lds[0]);
   }
+  if (!LOAD && chunks > 0) put_out(chunks - 1, lds[(chunks - 1) & 1]);
   if (state) state_columns<true, 0, 1>(s, state, p.K, p.V, col, ends);
 }
 

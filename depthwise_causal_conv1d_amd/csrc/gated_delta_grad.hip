@@ -54,7 +54,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
   using Stage = WalkStage<D, KP, NW, VEC>;
   using Rows = typename Stage::L::Rows;
   using Cols = typename Stage::L::Cols;
-  __shared__ typename Stage::L lds[LOAD ? 2 : 1];
+  __shared__ typename Stage::L lds[2];
 
   const DeltaParams& p = a.p;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -100,15 +100,13 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
   for (int t = 0; t < KT; ++t) s[t] = zero4();
   if (a.dfinal) state_columns<false, 0, 1>(s, a.dfinal + slot * a.df_slot + h * KV, p.K, p.V, col, ends);
   wait_for_all();
-  if (!LOAD && chunks > 0) fetch(chunks - 1, kFirst, kWhole);
-  if (LOAD) __syncthreads();
+  if (!LOAD && chunks > 0) {
+    fetch(chunks - 1, kFirst, kWhole);
+    stage(chunks - 1, lds[(chunks - 1) & 1]);
+  }
+  __syncthreads();
   for (int32_t i = chunks - 1; i >= 0; --i) {
-    typename Stage::L& l = lds[LOAD ? i & 1 : 0];
-    if constexpr (!LOAD) {
-      __syncthreads();
-      stage(i, l);
-      __syncthreads();
-    }
+    const typename Stage::L& l = lds[i & 1];
     const int64_t at = (int64_t)(row0 + i) * p.heads + h;
     float* mark = a.dstates + at * KV;
     f32x4 u[NT], none[NT];    // K dS, then dU, then dR
@@ -160,7 +158,8 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
       u[t] *= -(lds4(l.v + 16 * t + 4 * g) * lds4(l.v + 2 * C + 16 * t + 4 * g));
     fine_tiles<D>(u, fine);
     cols_times<D, Rows>(l.k, fine, s, lane);
-    if (LOAD) __syncthreads();
+    if (!LOAD && i > 0) stage(i - 1, lds[(i - 1) & 1]);
+    __syncthreads();
   }
   if (a.dinitial) {
     if (!(p.has && p.has[b])) {
@@ -169,6 +168,37 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
     }
     state_columns<true, 0, 1>(s, a.dinitial + slot * a.di_slot + h * KV, p.K, p.V, col, ends);
   }
+}
+
+template <int CTRL> __device__ __forceinline__ float lanes_moved(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
+// N values (16 or 8) of every lane summed over the 16 lanes of its group; lane
+// r gets the sum of value r % N.  A step halves the values: a lane keeps one half
+// and gives its partner the other (15 additions where 16 sums over 16 lanes
+// take 64, and one store).
+template <int N> __device__ __forceinline__ float sums16(float (&v)[N], int r) {
+  static_assert(N == 16 || N == 8);
+  auto step = [&](auto ctrl, auto half, bool upper) {
+    constexpr int H = decltype(half)::value;
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+      const float keep = upper ? v[H + j] : v[j], give = upper ? v[j] : v[H + j];
+      v[j] = keep + lanes_moved<decltype(ctrl)::value>(give);
+    }
+  };
+  using std::integral_constant;
+  if constexpr (N == 16) {
+    step(integral_constant<int, 0x140>(), integral_constant<int, 8>(), (r & 8) != 0);  // mirrored
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] += lanes_moved<0x140>(v[j]);
+  }
+  step(integral_constant<int, 0x141>(), integral_constant<int, 4>(), (r & 4) != 0);  // halves mirrored
+  step(integral_constant<int, 0x1B>(), integral_constant<int, 2>(), (r & 2) != 0);   // lanes 3 2 1 0
+  step(integral_constant<int, 0xB1>(), integral_constant<int, 1>(), (r & 1) != 0);   // lanes 1 0 3 2
+  return v[0];
 }
 
 // Row of tile n of a lower triangle of 4 x 4 tiles, counted row by row.
@@ -348,6 +378,7 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
       }
       __syncthreads();
       f32x4 u[NT], none[NT];
+      float rv[4 * NT];
       typename T::Exact vv[CS];
       typename T::Split tri[NF];
       rows_times_state<D, Rows, KS, NT, false>(l.k, l.q, st, u, none, lane, [&] {
@@ -362,11 +393,13 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         for (int e = 0; e < 4; ++e) {
           const float x = T::value(vv[t / 2], 4 * (t & 1) + e);
           u[t][e] = bt[e] * (x - gam[e] * u[t][e]);
-          // rowsum(dR V), this wave's columns
-          const float sv = lanes_reduce<16>(y[t][e] * x, Add());
-          float* to = &l.part[wave][3][16 * t + 4 * g + e];
-          if (r == 0) *to = first ? sv : *to + sv;
+          rv[4 * t + e] = y[t][e] * x;
         }
+      }
+      {  // rowsum(dR V), this wave's columns
+        const float sv = sums16(rv, r);
+        float* to = &l.part[wave][3][16 * (r >> 2) + 4 * g + (r & 3)];
+        if (r < 4 * NT) *to = first ? sv : *to + sv;
       }
       {
         typename T::Split us[CS];
@@ -482,8 +515,9 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = 16 * I + 4 * g + e, x = i * Tri::LD + Tri::pos(j);
-          float dec = 0.f;
-          if (i >= j) dec = expf((l.v[3 * C + i] - l.v[3 * C + j]) + (l.v[4 * C + i] - l.v[4 * C + j]));
+          constexpr float kLog2e = 1.44269504088896340736f;
+          const float d = (l.v[3 * C + i] - l.v[3 * C + j]) + (l.v[4 * C + i] - l.v[4 * C + j]);
+          const float dec = __builtin_amdgcn_exp2f(i >= j ? d * kLog2e : 0.f);
           const float pv = i >= j ? p.scale * dec * ep[m][e] : 0.f;
           const float av = i > j ? dec * ea[m][e] : 0.f;
           put_split(l.e, SMALL, x, pv);
@@ -532,32 +566,38 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         }
       }
     }
-    // rows' sums over this wave's channels, and the sums over value heads
+    // rows' sums over this wave's channels, one quantity after the other
     const bool last = gh + 1 == p.group;
-    const int kidx = 16 * wave + r;
+    const int kidx = 16 * wave + r, mine = 16 * (r >> 2) + 4 * g + (r & 3);
+    auto row_sums = [&](float* to, auto&& f) {
+      float v[4 * NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * t + e] = f(t, e, (16 * t + 4 * g + e) * Rows::LD + Rows::pos(kidx));
+      const float sum = sums16(v, r);
+      if (r < 4 * NT) to[mine] = sum;
+    };
+#pragma unroll
+    for (int t = 0; t < NT; ++t) w[t] -= neg[t];
+    row_sums(l.part[wave][1], [&](int t, int e, int i) { return to_float<D>(l.k[i]) * mw[t][e]; });
+    row_sums(l.part[wave][2], [&](int t, int e, int i) { return to_float<D>(l.k[i]) * mz[t][e]; });
+    row_sums(l.part[wave][0], [&](int t, int e, int i) {
+      const float bt = l.v[2 * C + 16 * t + 4 * g + e];
+      return to_float<D>(l.q[i]) * mq[t][e] - to_float<D>(l.k[i]) * (bt * mz[t][e] + w[t][e]);
+    });
+    // dq and dk, over the value heads; this wave's channels of Q and K have
+    // been read for the last time
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const f32x4 bt = lds4(l.v + 2 * C + 16 * t + 4 * g);
+      f32x4 gk = mw[t] + w[t] - lds4(l.v + 2 * C + 16 * t + 4 * g) * mz[t], gq = mq[t];
+      if constexpr (GROUPED) gq = dq[t] += gq, gk = dk[t] += gk;
+      if (!GROUPED || last) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int x = 16 * t + 4 * g + e, i = x * Rows::LD + Rows::pos(kidx);
-        const float kv = to_float<D>(l.k[i]), qv = to_float<D>(l.q[i]);
-        const float kz = kv * mz[t][e], wv = w[t][e] - neg[t][e];
-        const float own = lanes_reduce<16>(qv * mq[t][e] - bt[e] * kz - kv * wv, Add());
-        const float km = lanes_reduce<16>(kv * mw[t][e], Add()), sz = lanes_reduce<16>(kz, Add());
-        if (r == 0) l.part[wave][0][x] = own, l.part[wave][1][x] = km, l.part[wave][2][x] = sz;
-        const float gk = mw[t][e] + wv - bt[e] * mz[t][e];
-        if constexpr (GROUPED) {
-          dq[t][e] += mq[t][e];
-          dk[t][e] += gk;
-        } else {
-          // this wave's channels of K and Q have been read for the last time
-          l.q[i] = delta_round<D>(mq[t][e]);
-          l.k[i] = delta_round<D>(gk);
-        }
-        if (GROUPED && last) {
-          l.q[i] = delta_round<D>(dq[t][e]);
-          l.k[i] = delta_round<D>(dk[t][e]);
+        for (int e = 0; e < 4; ++e) {
+          const int i = (16 * t + 4 * g + e) * Rows::LD + Rows::pos(kidx);
+          l.q[i] = delta_round<D>(gq[e]);
+          l.k[i] = delta_round<D>(gk[e]);
         }
       }
     }
@@ -574,15 +614,15 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         all += l.dots[n];
       }
       if (t >= C) own = km = 0.f;
-      double before = km, after = own;
+      float before = km, after = own;
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
-        const double x = __shfl_up(before, d, 64), y2 = __shfl_down(after, d, 64);
+        const float x = __shfl_up(before, d, 64), y = __shfl_down(after, d, 64);
         if (lane >= d) before += x;
-        if (lane + d < 64) after += y2;
+        if (lane + d < 64) after += y;
       }
       if (t < ch.len) {
-        float dg = (float)(after + (before - km) + (double)l.v[C - 1] * all);
+        float dg = after + (before - km) + l.v[C - 1] * all;
         const float db = sv - sz;
         // behind a closed gate the parts cancel but for their roundings
         const float gt = l.v[3 * C + t] + l.v[4 * C + t] - (t ? l.v[3 * C + t - 1] + l.v[4 * C + t - 1] : 0.f);
