@@ -34,7 +34,7 @@ struct DeltaBwd {
   int64_t df_slot, di_slot;
   void *dq, *dk, *dv, *dg, *db;
   int64_t dq_t, dq_h, dk_t, dk_h, dv_t, dv_h, dg_t, dg_h, db_t, db_h;
-  int32_t do_vec, grads_vec;
+  int32_t do_vec, grads_vec, rows4;
 };
 
 // Where a lane's part of dR's tiles of 16 columns lies: 1 KB a tile of 16 tokens.
@@ -319,7 +319,6 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
 #pragma unroll
     for (int t = 0; t < NT; ++t) dq[t] = dk[t] = zero4();
   }
-  const bool rows4 = p.V % 4 == 0;
 
   for (int32_t gh = 0; gh < (GROUPED ? p.group : 1); ++gh) {
     hide();
@@ -415,7 +414,7 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
           const int vc = v0 + 32 * c + 16 * o + 4 * g;
-          if (rows4) {
+          if (a.rows4) {
             const int64_t i = base + min(vc, p.V - 4);
             w[c & 1][o] = lds4(s0 + i), z[c & 1][o] = lds4(ds + i);
           } else {
@@ -751,6 +750,7 @@ extern "C" int gated_delta_rule_varlen_bwd(
   a.db = dbeta, a.db_t = db_stride_t, a.db_h = db_stride_h;
   const int64_t n = 16 / elem_size(dtype);
   a.do_vec = delta_vec(dout, do_stride_t, do_stride_h, V, n);
+  a.rows4 = V % 4 == 0 && aligned16(checkpoints);
   a.grads_vec = delta_vec(dv, dv_stride_t, dv_stride_h, V, n) && delta_vec(dq, dq_stride_t, dq_stride_h, K, n) &&
                 delta_vec(dk, dk_stride_t, dk_stride_h, K, n);
   if (dtype == SCONV_BF16)

@@ -10,8 +10,8 @@
  * - Every buffer is a caller-owned DEVICE pointer (hipMalloc / torch).  The
  *   library allocates nothing, never synchronizes and never reads device data
  *   on the host: each call enqueues one kernel on `stream` (NULL = the null
- *   stream; sconv_fused_insert_conv_gather and the entry points that take a
- *   workspace may enqueue up to three) and returns.
+ *   stream; sconv_fused_insert_conv_gather, sconv_paged_metadata and the entry
+ *   points that take a workspace may enqueue up to three) and returns.
  *   This makes every call capturable in a hipGraph; grids depend on host
  *   scalars only.
  * - Strides are in ELEMENTS.  Only host scalars are validated.  Properties of

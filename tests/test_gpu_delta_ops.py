@@ -227,6 +227,75 @@ def test_long_sequences_among_many():
         assert torch.equal(R.bits(a), R.bits(b))
 
 
+@pytest.mark.parametrize("lead", [0, 5])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_inputs_and_gradients_as_columns_of_one_matrix(dtype, lead):
+    """q, k, v as columns of a conv's output and their gradients as columns of
+    another matrix (aligned rows, and rows from an odd element on); gates and
+    betas as columns too, checkpoints at an odd element."""
+    c = Case([70, 3, 64], 2, 4, 32, 48, dtype, gates=dtype, seed=12, inits=(1,))
+    wide = [2 * 32, 2 * 32, 4 * 48]
+
+    def columns(*ts):
+        T, n = ts[0].shape[0], sum(t[0].numel() for t in ts)
+        row = n + lead
+        m = torch.full((T * row + lead,), NAN, dtype=ts[0].dtype, device="cuda")[lead:].as_strided(
+            (T, n), (row, 1), lead)
+        return [p.view(t.shape).copy_(t) for p, t in zip(m.split([t[0].numel() for t in ts], 1), ts)]
+
+    assert wide == [t[0].numel() for t in (c.q, c.k, c.v)]
+    d = c.gpu()
+    d["q"], d["k"], d["v"] = columns(c.q, c.k, c.v)
+    d["g"], d["beta"] = (t[..., 0] for t in columns(c.g[..., None], c.beta[..., None]))
+    out = place(torch.full_like(c.v, SENTINEL), "dense")
+    m = lib.gated_delta_rule_checkpoints(d["k"], d["v"], d["qsl"])
+    m = torch.empty(m.numel() + 1, device="cuda")[1:].view(m.shape)
+    args = d["q"], d["k"], d["v"], d["g"], d["beta"]
+    lib.gated_delta_rule_varlen_fwd(*args, d["pool"], d["qsl"], d["slots"], d["has"], scale=c.scale,
+                                    out=out, checkpoints=m)
+    new = columns(*(torch.full_like(t, SENTINEL) for t in (c.q, c.k, c.v)))
+    got = dict(zip(NAMES, lib.gated_delta_rule_varlen_bwd(
+        d["dout"], *args, m, d["qsl"], d["slots"], d["has"], scale=c.scale,
+        dq=new[0], dk=new[1], dv=new[2])))
+    c.check(out, d["pool"], got, None, "columns", dfinal=False)
+
+
+@pytest.mark.parametrize("heads,batch", [(40, 9), (3, 2)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_workgroups_of_both_widths(dtype, heads, batch):
+    """Enough heads and sequences for eight computing waves a workgroup, and too
+    few; more columns than one workgroup takes; equal bits in both where the
+    sequence is the same."""
+    lens = [40, 65] + [1] * (batch - 2)
+    c = Case(lens, 1, heads, 32, 136, dtype, seed=13, inits=(1,))
+    d = c.gpu()
+    out, m = c.forward(d)
+    got, di = c.backward(d, m)
+    o, state = out.clone(), d["pool"].clone()
+    # the first two sequences and three heads alone
+    few = {n: d[n][:105, :3] for n in ("v", "g", "beta")}
+    st = torch.full((2, 3, 32, 136), NAN, device="cuda")
+    st[1] = c.h0[1, :3].cuda()
+    alone = lib.gated_delta_rule_varlen_fwd(d["q"][:105], d["k"][:105], few["v"], few["g"], few["beta"], st,
+                                            d["qsl"][:3].clone(), None, d["has"][:2].clone(), scale=c.scale)
+    assert torch.equal(R.bits(alone), R.bits(o[:105, :3]))
+    for b in (0, 1):
+        assert torch.equal(R.bits(st[b]), R.bits(state[int(c.slots[b]), :3]))
+    if heads == 3:
+        c.check(out, d["pool"], got, di, "narrow")
+    else:  # a few heads of the gradients: the reference of all takes minutes
+        few = Case.__new__(Case)
+        few.__dict__.update(c.__dict__)
+        few.vh = 2
+        few.v, few.dout, few.g, few.beta = (t[:, :2] for t in (c.v, c.dout, c.g, c.beta))
+        few.h0, few.dfinal, few.pool = (t[:, :2] for t in (c.h0, c.dfinal, c.pool))
+        part = {n: got[n][:, :2] for n in ("dv", "dg", "dbeta")}
+        for b, s, v, e in few.ref():
+            R.check(out[s, :2], v["out"], e["out"], f"wide out {b}")
+            for n, t in part.items():
+                R.check(t[s], v[n], e[n], f"wide {n} {b}")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_closed_open_and_strong_gates(dtype):
     """g of 0, -inf and far below -200, beta of 0, 1 and 2: closed gates forget
