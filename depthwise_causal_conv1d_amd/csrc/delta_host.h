@@ -28,8 +28,8 @@ inline DeltaSpace delta_space(int64_t total_T, int32_t batch, int32_t heads, int
   s.vectors = n * 5 * C;
   s.fwd = s.vectors + n * 2 * nf * (kFragBytes / 4);
   s.bwd_rows = s.vectors + n * 3 * nf * (kFragBytes / 4);
-  s.bwd_states = s.bwd_rows + n * C * cdiv(V, 16) * 16;
-  s.bwd = s.bwd_states + n * K * V;
+  s.bwd_states = s.bwd_rows + n * C * tiles16(V) * 16;
+  s.bwd = s.bwd_states + n * delta_state_floats(K, V);
   return s;
 }
 

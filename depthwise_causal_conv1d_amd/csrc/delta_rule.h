@@ -100,6 +100,14 @@ template <int C> __host__ __device__ constexpr int upper_frag(int r, int s) {
 // Per chunk: e^G, e^(G_C - G), beta, and G as a sum of two floats.
 template <int C> constexpr int kDeltaVectors = 5 * C;
 
+// States of a chunk (checkpoints, and their gradients) lie as accumulator
+// tiles: per row and value head ceil(V / 16) x ceil(K / 16) tiles of 1 KB, a
+// lane's four rows of its column in 16 bytes, zeros behind K and V.
+__host__ __device__ constexpr int32_t tiles16(int32_t n) { return (n + 15) / 16; }
+__host__ __device__ constexpr int64_t delta_state_floats(int32_t K, int32_t V) {
+  return (int64_t)tiles16(K) * tiles16(V) * 256;
+}
+
 // ---------------------------------------------------------------- operands
 
 template <typename D> struct Tile;

@@ -151,18 +151,16 @@ __device__ __forceinline__ void put_rows(const typename Stage::L& l, typename D:
 // first use inside it a wait for the loop's own.
 __device__ __forceinline__ void wait_for_all() { __builtin_amdgcn_s_waitcnt(0); }
 
-// A wave's 16 columns of a K x V matrix in memory and in accumulator tiles (P of
-// N: a piece of the tiles).  A row is a uniform address and a lane's 32-bit
-// offset: 64-bit addresses for every lane and row, made once ahead of the loop,
-// would take 64 registers.
-template <bool STORE, int P, int N, int KT>
+// A wave's 16 columns of a K x V state in its slot and in accumulator tiles.  A
+// row is a uniform address and a lane's 32-bit offset.
+template <bool STORE, int KT>
 __device__ __forceinline__ void state_columns(f32x4 (&s)[KT], std::conditional_t<STORE, float, const float>* m,
                                               int K, int V, int col, int col_end) {
   const int g = (threadIdx.x & 63) >> 4;
   const uint32_t off = lane_offset((uint32_t)(4 * g * V + col) * 4u);
   auto all = [&](auto in) {
 #pragma unroll
-    for (int t = KT * P / N; t < KT * (P + 1) / N; ++t)
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (!in(16 * t + 4 * g + e)) continue;
@@ -173,6 +171,16 @@ __device__ __forceinline__ void state_columns(f32x4 (&s)[KT], std::conditional_t
   };
   if (K == 16 * KT && col_end <= V) all([](int) { return true; });  // of the whole wave
   else all([&](int k) { return k < K && col < V; });
+}
+
+// Piece P of N of the same columns to a chunk's tiles: one store of 1 KB a
+// tile.  (As rows of V floats a walk's chunk took 3000 of 9500 cycles for its
+// 32 stores of 64-byte pieces.)
+template <int P, int N, int KT>
+__device__ __forceinline__ void put_tiles(const f32x4 (&s)[KT], float* m, int K, int lane) {
+#pragma unroll
+  for (int t = KT * P / N; t < KT * (P + 1) / N; ++t)
+    if (16 * t < K) *reinterpret_cast<f32x4*>(in_row(m + t * 256, lane * 16u)) = s[t];
 }
 
 // The products of a chunk's K (and Q) with 16 columns of a state: x = K S, y

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
 #pragma unroll
   for (int t = 0; t < KT; ++t) s[t] = zero4();
   float* state = a.states ? a.states + slot * a.st_slot + h * KV : nullptr;
-  if (p.has && p.has[b]) state_columns<false, 0, 1>(s, state, p.K, p.V, col, ends);
+  if (p.has && p.has[b]) state_columns<false>(s, state, p.K, p.V, col, ends);
   wait_for_all();
   if (!LOAD && chunks > 0) {
     fetch(0, kFirst, kWhole);
@@ -90,7 +90,10 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
   for (int32_t i = 0; i < chunks; ++i) {
     typename Stage::L& l = lds[i & 1];
     if (!LOAD && i > 0) put_out(i - 1, lds[(i + 1) & 1]);
-    float* mark = a.marks ? a.marks + ((int64_t)(row0 + i) * p.heads + h) * KV : nullptr;
+    float* mark = nullptr;
+    if (a.marks && ends - 16 < p.V)
+      mark = a.marks + ((int64_t)(row0 + i) * p.heads + h) * delta_state_floats(p.K, p.V) +
+             (ends / 16 - 1) * tiles16(p.K) * 256;
     f32x4 u[NT], y[NT];  // K S, then R, then U; Q S, then O
     typename T::Exact vv[CS];
     typename T::Split tri[NF], us[CS];
@@ -103,7 +106,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
         },
         [&](auto P) {
           if constexpr (!LOAD) fetch(min(i + 1, chunks - 1), P, std::integral_constant<int, PIECES>());
-          if (mark) state_columns<true, decltype(P)::value, PIECES>(s, mark, p.K, p.V, col, ends);
+          if (mark) put_tiles<decltype(P)::value, PIECES>(s, mark, p.K, lane);
         });
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -139,7 +142,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
     __syncthreads();
   }
   if (!LOAD && chunks > 0) put_out(chunks - 1, lds[(chunks - 1) & 1]);
-  if (state) state_columns<true, 0, 1>(s, state, p.K, p.V, col, ends);
+  if (state) state_columns<true>(s, state, p.K, p.V, col, ends);
 }
 
 // ---------------------------------------------------------------- one token
@@ -325,15 +328,14 @@ extern "C" int gated_delta_rule_varlen_fwd(
     return rc;
   if (int rc = delta_output(c, out, out_stride_t, out_stride_h, value_heads, V, "out", &o)) return rc;
   const int64_t rows = delta_rows(total_T, batch, delta_chunk(dtype));
-  const int64_t KV = (int64_t)K * V;
-  if (checkpoints && checkpoint_rows < rows)
-    return fail(SCONV_ERR_INVALID, "%s: %lld checkpoint rows, needs %lld", what,
+  if (checkpoints && (checkpoint_rows < rows || !aligned16(checkpoints)))
+    return fail(SCONV_ERR_INVALID, "%s: %lld checkpoint rows, needs %lld at 16 bytes", what,
                 (long long)checkpoint_rows, (long long)rows);
   const DeltaSpace s = delta_space(total_T, batch, value_heads, K, V, dtype);
   if (!workspace || workspace_floats < s.fwd || !aligned16(workspace))
     return fail(SCONV_ERR_INVALID, "%s: workspace needs %lld floats at 16 bytes", what,
                 (long long)s.fwd);
-  const DeltaBuffer marks = delta_block(checkpoints, checkpoints ? rows * value_heads * KV * 4 : 0);
+  const DeltaBuffer marks = delta_block(checkpoints, checkpoints ? rows * value_heads * delta_state_floats(K, V) * 4 : 0);
   const DeltaBuffer work = delta_block(workspace, s.fwd * 4);
   if (int rc = delta_disjoint(c, a.p, {o, pool, marks, work}, /*out may be v=*/out == v &&
                               out_stride_t == v_stride_t && out_stride_h == v_stride_h))

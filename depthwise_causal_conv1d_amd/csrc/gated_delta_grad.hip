@@ -34,13 +34,13 @@ struct DeltaBwd {
   int64_t df_slot, di_slot;
   void *dq, *dk, *dv, *dg, *db;
   int64_t dq_t, dq_h, dk_t, dk_h, dv_t, dv_h, dg_t, dg_h, db_t, db_h;
-  int32_t do_vec, grads_vec, rows4;
+  int32_t do_vec, grads_vec;
 };
 
 // Where a lane's part of dR's tiles of 16 columns lies: 1 KB a tile of 16 tokens.
 template <int C>
 __device__ __forceinline__ f32x4* delta_row_tiles(float* drows, int64_t at, int32_t V, int32_t tile, int lane) {
-  return reinterpret_cast<f32x4*>(drows + (at * ((V + 15) / 16) + tile) * 16 * C) + lane;
+  return reinterpret_cast<f32x4*>(drows + (at * tiles16(V) + tile) * 16 * C) + lane;
 }
 
 // One workgroup walks a sequence's chunks from the last, for one value head
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
   f32x4 s[KT];
 #pragma unroll
   for (int t = 0; t < KT; ++t) s[t] = zero4();
-  if (a.dfinal) state_columns<false, 0, 1>(s, a.dfinal + slot * a.df_slot + h * KV, p.K, p.V, col, ends);
+  if (a.dfinal) state_columns<false>(s, a.dfinal + slot * a.df_slot + h * KV, p.K, p.V, col, ends);
   wait_for_all();
   if (!LOAD && chunks > 0) {
     fetch(chunks - 1, kFirst, kWhole);
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
   for (int32_t i = chunks - 1; i >= 0; --i) {
     const typename Stage::L& l = lds[i & 1];
     const int64_t at = (int64_t)(row0 + i) * p.heads + h;
-    float* mark = a.dstates + at * KV;
+    float* mark = a.dstates + at * delta_state_floats(p.K, p.V) + (ends / 16 - 1) * tiles16(p.K) * 256;
     f32x4 u[NT], none[NT];    // K dS, then dU, then dR
     typename T::Exact go[CS]; // dO
     typename T::Split tri[NF], us[CS];
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
         },
         [&](auto P) {
           if constexpr (!LOAD) fetch(max(i - 1, 0), P, std::integral_constant<int, PIECES>());
-          state_columns<true, decltype(P)::value, PIECES>(s, mark, p.K, p.V, col, ends);
+          if (ends - 16 < p.V) put_tiles<decltype(P)::value, PIECES>(s, mark, p.K, lane);
         });
 #pragma unroll
     for (int t = 0; t < NT; ++t) u[t] *= lds4(l.v + C + 16 * t + 4 * g);
@@ -166,12 +166,31 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
 #pragma unroll
       for (int t = 0; t < KT; ++t) s[t] = zero4();
     }
-    state_columns<true, 0, 1>(s, a.dinitial + slot * a.di_slot + h * KV, p.K, p.V, col, ends);
+    state_columns<true>(s, a.dinitial + slot * a.di_slot + h * KV, p.K, p.V, col, ends);
   }
 }
 
 template <int CTRL> __device__ __forceinline__ float lanes_moved(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
+// Four lanes' four values transposed: entry j of lane q of a quad is entry q of
+// its lane j.
+__device__ __forceinline__ f32x4 quad_transposed(const f32x4& a, int r) {
+  const bool odd = r & 1, high = r & 2;
+  f32x4 m;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const float keep = odd ? a[i + 1] : a[i], other = lanes_moved<0xB1>(odd ? a[i] : a[i + 1]);
+    m[i] = odd ? other : keep, m[i + 1] = odd ? keep : other;
+  }
+  f32x4 o;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float keep = high ? m[2 + i] : m[i], other = lanes_moved<0x4E>(high ? m[i] : m[2 + i]);
+    o[i] = high ? other : keep, o[2 + i] = high ? keep : other;
+  }
+  return o;
 }
 
 // N values (16 or 8) of every lane summed over the 16 lanes of its group; lane
@@ -251,7 +270,7 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
   const int32_t row = blockIdx.x, kh = blockIdx.y;
   const DeltaChunk ch = delta_find<C>(p, row);
   if (ch.len == 0) return;
-  const int64_t KV = (int64_t)p.K * p.V;
+  const int kt16 = tiles16(p.K);
 
   auto put_split = [&](S* m, int planes, int at, float v) {
     if constexpr (kB) {
@@ -324,7 +343,8 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
     hide();
     const int32_t h = kh * p.group + gh;
     const int64_t at = (int64_t)row * p.heads + h;
-    const float *s0 = a.marks + at * KV, *ds = a.dstates + at * KV;
+    const int64_t state = at * delta_state_floats(p.K, p.V);
+    const float *s0 = a.marks + state, *ds = a.dstates + state;
     const S* v = static_cast<const S*>(p.v) + ch.t0 * p.v_t + h * p.v_h;
     const S* dout = static_cast<const S*>(a.dout) + ch.t0 * a.do_t + h * a.do_h;
 
@@ -338,7 +358,7 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
 
     for (int32_t v0 = 0; v0 < p.V; v0 += KP) {
       hide();
-      const int c16 = 16 * wave, col = v0 + c16 + r;
+      const int c16 = 16 * wave;
       // everything that the block needs from memory, before anything waits
       Octets xo, xv;
       load2(xo, xv, dout, a.do_t, v, p.v_t, v0, p.V);
@@ -351,7 +371,12 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
       for (int t = 0; t < KT; ++t) st[t] = zero4();
 #pragma unroll
       for (int t = 0; t < NT; ++t) y[t] = zero4();
-      state_columns<false, 0, 1>(st, s0, p.K, p.V, col, v0 + c16 + 16);
+      const int tile0 = (v0 + c16) / 16 * kt16;
+      if (v0 + c16 < p.V) {
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+          if (t < kt16) st[t] = lds4(in_row(s0 + (tile0 + t) * 256, lane * 16u));
+      }
       if (v0 + c16 < p.V) {
         const f32x4* from = delta_row_tiles<C>(a.drows, at, p.V, (v0 + c16) / 16, lane);
 #pragma unroll
@@ -408,22 +433,15 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
       // the first step's rows of S0 and dS1 are on their way over the barrier
       const int steps = (min(KP, p.V - v0) + 31) / 32;
       f32x4 w[2][2], z[2][2];
-      const int kidx = 16 * wave + r;  // this lane's channel of K
+      // A tile's lane has four rows of K and one column; this lane's channel of
+      // K is one row and four columns of it: quads of lanes trade them.
       auto load_states = [&](int c) {
-        const int64_t base = (int64_t)min(kidx, p.K - 1) * p.V;
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
-          const int vc = v0 + 32 * c + 16 * o + 4 * g;
-          if (a.rows4) {
-            const int64_t i = base + min(vc, p.V - 4);
-            w[c & 1][o] = lds4(s0 + i), z[c & 1][o] = lds4(ds + i);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int64_t i = base + min(vc + e, p.V - 1);
-              w[c & 1][o][e] = s0[i], z[c & 1][o][e] = ds[i];
-            }
-          }
+          const int tile = min(v0 / 16 + 2 * c + o, tiles16(p.V) - 1) * kt16 + min(wave, kt16 - 1);
+          const uint32_t from = (uint32_t)(16 * (r >> 2) + 4 * g + (r & 3)) * 16u;
+          w[c & 1][o] = lds4(in_row(s0 + tile * 256, from));
+          z[c & 1][o] = lds4(in_row(ds + tile * 256, from));
         }
       };
       load_states(0);
@@ -457,14 +475,16 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         if (c >= steps) break;
         if (c + 1 < steps) load_states(c + 1);
 #pragma unroll
-        for (int o = 0; o < 2; ++o)
+        for (int o = 0; o < 2; ++o) {
+          const bool in = wave < kt16 && v0 / 16 + 2 * c + o < tiles16(p.V);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const bool in = kidx < p.K && v0 + 32 * c + 16 * o + 4 * g + e < p.V;
-            const float x = in ? w[c & 1][o][e] : 0.f, x2 = in ? z[c & 1][o][e] : 0.f;
-            dot = fmaf(x, x2, dot);
-            w[c & 1][o][e] = x, z[c & 1][o][e] = x2;
+            w[c & 1][o][e] = in ? w[c & 1][o][e] : 0.f, z[c & 1][o][e] = in ? z[c & 1][o][e] : 0.f;
+            dot = fmaf(w[c & 1][o][e], z[c & 1][o][e], dot);
           }
+          w[c & 1][o] = quad_transposed(w[c & 1][o], r);
+          z[c & 1][o] = quad_transposed(z[c & 1][o], r);
+        }
         const auto sw = T::split(w[c & 1][0], w[c & 1][1]), sz = T::split(z[c & 1][0], z[c & 1][1]);
         typename T::Exact fo[2];
         typename T::Split fr[2], fu[2];
@@ -703,9 +723,8 @@ extern "C" int gated_delta_rule_varlen_bwd(
   if (do_stride_t < 0 || do_stride_h < 0) return fail(SCONV_ERR_INVALID, "%s: negative stride", what);
   delta_packing(c, a.p, query_start_loc, cache_indices, has_initial_state, pad_slot_id);
   const int64_t rows = delta_rows(total_T, batch, delta_chunk(dtype));
-  const int64_t KV = (int64_t)K * V;
-  if (checkpoint_rows < rows)
-    return fail(SCONV_ERR_INVALID, "%s: %lld checkpoint rows, needs %lld", what,
+  if (checkpoint_rows < rows || !aligned16(checkpoints))
+    return fail(SCONV_ERR_INVALID, "%s: %lld checkpoint rows, needs %lld at 16 bytes", what,
                 (long long)checkpoint_rows, (long long)rows);
   const bool indexed = cache_indices != nullptr;
   DeltaBuffer df, di, oq, ok, ov, og, ob;
@@ -728,7 +747,7 @@ extern "C" int gated_delta_rule_varlen_bwd(
   const bool same = dfinal_states && dinitial_states == dfinal_states && di_stride_slot == df_stride_slot;
   if (!same && delta_overlap(df, di))
     return fail(SCONV_ERR_INVALID, "%s: dfinal_states and dinitial_states overlap", what);
-  const DeltaBuffer marks = delta_block(checkpoints, rows * value_heads * KV * 4);
+  const DeltaBuffer marks = delta_block(checkpoints, rows * value_heads * delta_state_floats(K, V) * 4);
   const DeltaBuffer work = delta_block(workspace, s.bwd * 4);
   const DeltaBuffer od = delta_tensor(dout, do_stride_t, do_stride_h, total_T, value_heads, V,
                                       elem_size(dtype));
@@ -750,7 +769,6 @@ extern "C" int gated_delta_rule_varlen_bwd(
   a.db = dbeta, a.db_t = db_stride_t, a.db_h = db_stride_h;
   const int64_t n = 16 / elem_size(dtype);
   a.do_vec = delta_vec(dout, do_stride_t, do_stride_h, V, n);
-  a.rows4 = V % 4 == 0 && aligned16(checkpoints);
   a.grads_vec = delta_vec(dv, dv_stride_t, dv_stride_h, V, n) && delta_vec(dq, dq_stride_t, dq_stride_h, K, n) &&
                 delta_vec(dk, dk_stride_t, dk_stride_h, K, n);
   if (dtype == SCONV_BF16)

@@ -949,12 +949,16 @@ def _matrix_pool(t: Optional[torch.Tensor], heads: int, K: int, V: int, name: st
     return t.data_ptr(), t.shape[0], t.stride(0)
 
 
+def _sixteens(n: int) -> int:
+    return -(-n // 16) * 16
+
+
 def _delta_marks(t: Optional[torch.Tensor], heads: int, K: int, V: int):
     if t is None:
         return 0
-    if t.dtype != torch.float32 or t.dim() != 4 or t.shape[1:] != (heads, K, V) \
-            or not t.is_contiguous():
-        raise ValueError("checkpoints must be a dense float32 [rows, value_heads, K, V] tensor")
+    if t.dtype != torch.float32 or t.dim() != 4 or not t.is_contiguous() \
+            or t.shape[1:] != (heads, _sixteens(K), _sixteens(V)):
+        raise ValueError("checkpoints must be what gated_delta_rule_checkpoints makes")
     return t.shape[0]
 
 
@@ -979,8 +983,8 @@ def gated_delta_rule_checkpoints(k: torch.Tensor, v: torch.Tensor, query_start_l
         raise ValueError("k [total_T, key_heads, K], v [total_T, value_heads, V]")
     rows = _floats("gated_delta_rule_checkpoint_rows", v.shape[0], query_start_loc.numel() - 1,
                    _dtype(v))
-    return torch.empty(rows, v.shape[1], k.shape[2], v.shape[2], dtype=torch.float32,
-                       device=v.device)
+    return torch.empty(rows, v.shape[1], _sixteens(k.shape[2]), _sixteens(v.shape[2]),
+                       dtype=torch.float32, device=v.device)
 
 
 def gated_delta_rule_varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,

@@ -818,8 +818,9 @@ int rms_norm_bwd(const void* dout, int64_t dout_stride_r, const void* x, int64_t
  * gated_delta_rule_checkpoint_rows -- rows of the checkpoint buffer that a
  * forward call leaves for its backward call:
  *     *rows = ceil(total_T / C) + batch,   C = 64 (bf16), 32 (fp32)
- * The buffer is fp32 [rows, value_heads, K, V], dense; row start_b / C + b + i
- * holds sequence b's states before its token C i.  Rows that no sequence has
+ * The buffer is fp32 [rows, value_heads, 16 ceil(K / 16), 16 ceil(V / 16)],
+ * dense, at 16 bytes; row start_b / C + b + i holds sequence b's states before
+ * its token C i, in an order of the library's own.  Rows that no sequence has
  * are not written.  Host only.
  */
 int gated_delta_rule_checkpoint_rows(int64_t total_T, int32_t batch, int32_t dtype, int64_t* rows);
@@ -841,7 +842,7 @@ int gated_delta_rule_workspace(int64_t total_T, int32_t batch, int32_t value_hea
  *   query_start_loc, cache_indices, has_initial_state, pad_slot_id: as
  *            causal_conv1d_varlen_fwd (a sequence of no tokens leaves its
  *            initial state, or zeros, in its slot)
- *   checkpoints  fp32, for the backward call, or NULL
+ *   checkpoints  fp32 at 16 bytes, for the backward call, or NULL
  *   workspace  fp32 at 16 bytes, gated_delta_rule_workspace's fwd_floats, the
  *            call's own until it has finished
  *

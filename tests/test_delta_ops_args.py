@@ -62,7 +62,7 @@ SHARED = [
 @pytest.mark.parametrize("kw,text", SHARED + [
     (dict(qsl=None), "NULL"), (dict(out=None), "NULL"), (dict(st=None), "without states"),
     (dict(ss=ONE - 1), "slots overlap"), (dict(idx=None, slots=1), "slots"), (dict(rows=3), "checkpoint"),
-    (dict(ws=None), "workspace"), (dict(wsn=100), "workspace"), (dict(ws=WS + 4), "workspace"),
+    (dict(mk=MK + 4), "16 bytes"), (dict(ws=None), "workspace"), (dict(wsn=100), "workspace"), (dict(ws=WS + 4), "workspace"),
     (dict(ot=15), "share memory"), (dict(oh=7), "share memory"), (dict(ot=0), "share memory"),
     (dict(ot=-1), "stride"), (dict(out=V + 4), "overlaps an input"), (dict(out=V, ot=17), "overlaps an input"),
     (dict(out=Q), "overlaps an input"), (dict(out=K + 64), "overlaps an input"), (dict(out=G), "overlaps an input"),
@@ -96,7 +96,7 @@ def bwd(lib, **kw):
 
 @pytest.mark.parametrize("kw,text", SHARED + [
     (dict(qsl=None), "NULL"), (dict(do=None), "NULL"), (dict(mk=None), "NULL"), (dict(dot=-1), "stride"),
-    (dict(rows=3), "checkpoint"), (dict(dfs=ONE - 1), "slots overlap"), (dict(dis=ONE - 1), "slots overlap"),
+    (dict(rows=3), "checkpoint"), (dict(mk=MK + 8), "16 bytes"), (dict(dfs=ONE - 1), "slots overlap"), (dict(dis=ONE - 1), "slots overlap"),
     (dict(idx=None, slots=1), "slots"), (dict(dq=None), "NULL"), (dict(dk=None), "NULL"), (dict(dv=None), "NULL"),
     (dict(dg=None), "NULL"), (dict(db=None), "NULL"), (dict(dqt=15), "share memory"), (dict(dvh=7), "share memory"),
     (dict(dgt=1), "share memory"), (dict(dbh=0), "share memory"), (dict(ws=None), "workspace"),
