@@ -111,8 +111,13 @@ inline int delta_inputs(const DeltaCall& c, DeltaParams& p, const void* q, int64
   return SCONV_OK;
 }
 
-// Whether a wave of a walk takes 32 columns (else 16): it reads half as much
-// LDS a product, on half as many CUs.
+// Whether a workgroup of a walk has eight waves on 128 columns and no loaders
+// (else four on 64, and four loaders): it reads half as much LDS a product, on
+// half as many CUs.  Where the narrow ones all have a CU of 256 at once they win
+// (4 x 2048 tokens, 32 heads of 128 x 128 bf16: 156 us, wide 207), beyond that
+// the wide ones (5 x 2048: 219 us, narrow 246; 8 x 4096: 590 and 636).  Products
+// of 32-bit tiles take the same time either way (320 narrow workgroups: 329 us,
+// wide 359; 512: 339 and 336), so they have the narrow form only.
 inline bool delta_wide(const DeltaParams& p) {
   return p.V > 64 && (int64_t)p.batch * p.heads * ((p.V + 63) / 64) > 256;
 }

@@ -155,16 +155,14 @@ struct DeltaUpdate {
   int64_t o_t, o_h;
 };
 
-constexpr int kUpdateThreads = 256;
-
 // One workgroup a row, value head and CL * VEC columns of the state, which it
 // reads and writes once.  Both products with the old state are summed in one
 // pass, since S^T q = S'^T q + (k.q) u: one meeting of the row groups.
-template <typename D, int CL, int VEC>
-__global__ __launch_bounds__(kUpdateThreads) void delta_update_kernel(DeltaUpdate a) {
+template <typename D, int CL, int VEC, int THREADS>
+__global__ __launch_bounds__(THREADS) void delta_update_kernel(DeltaUpdate a) {
   using S = typename D::storage;
   typedef float vf __attribute__((ext_vector_type(VEC)));
-  constexpr int RG = kUpdateThreads / CL, RPG = kDeltaMaxK / RG;
+  constexpr int RG = THREADS / CL, RPG = kDeltaMaxK / RG;
   __shared__ float lk[kDeltaMaxK], lq[kDeltaMaxK];
   __shared__ float part[2][RG][CL * VEC];
   const DeltaParams& p = a.p;
@@ -183,8 +181,7 @@ __global__ __launch_bounds__(kUpdateThreads) void delta_update_kernel(DeltaUpdat
     for (int e = 0; e < VEC; ++e) s[j][e] = 0.f;
     if (on && k < p.K) s[j] = *reinterpret_cast<const vf*>(state + (int64_t)k * p.V);
   }
-  if (threadIdx.x < kDeltaMaxK) {
-    const int k = threadIdx.x;
+  for (int k = threadIdx.x; k < kDeltaMaxK; k += THREADS) {
     lk[k] = k < p.K ? load_as_float<D>(static_cast<const S*>(p.k) + b * p.k_t + kh * p.k_h + k) : 0.f;
     lq[k] = k < p.K ? load_as_float<D>(static_cast<const S*>(p.q) + b * p.q_t + kh * p.q_h + k) : 0.f;
   }
@@ -243,11 +240,16 @@ static int delta_forward(const DeltaFwd& a, int64_t rows, hipStream_t stream) {
   if (int rc = delta_prepare<D, KP, false>("gated_delta_rule_varlen_fwd", p, rows, stream)) return rc;
   const bool vec = p.qk_vec && p.v_vec && a.o_vec;
   const dim3 threads(512);
-  if (delta_wide(p)) {
-    const dim3 grid((p.V + 127) / 128, p.heads, p.batch);
-    if (vec) hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8, false, true>), grid, threads, 0, stream, a);
-    else hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8, false, false>), grid, threads, 0, stream, a);
-  } else {
+  bool wide = false;
+  if constexpr (sizeof(typename D::storage) == 2) {
+    wide = delta_wide(p);
+    if (wide) {
+      const dim3 grid((p.V + 127) / 128, p.heads, p.batch);
+      if (vec) hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8, false, true>), grid, threads, 0, stream, a);
+      else hipLaunchKernelGGL((delta_walk_kernel<D, KP, 8, false, false>), grid, threads, 0, stream, a);
+    }
+  }
+  if (!wide) {
     const dim3 grid((p.V + 63) / 64, p.heads, p.batch);
     if (vec) hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4, true, true>), grid, threads, 0, stream, a);
     else hipLaunchKernelGGL((delta_walk_kernel<D, KP, 4, true, false>), grid, threads, 0, stream, a);
@@ -255,20 +257,25 @@ static int delta_forward(const DeltaFwd& a, int64_t rows, hipStream_t stream) {
   return check_launch("gated_delta_rule_varlen_fwd");
 }
 
-template <typename D, int CL, int VEC>
+template <typename D, int CL, int VEC, int THREADS>
 static void delta_update_launch(const DeltaUpdate& a, hipStream_t stream) {
   const int cols = CL * VEC;
-  hipLaunchKernelGGL((delta_update_kernel<D, CL, VEC>),
-                     dim3((a.p.V + cols - 1) / cols, a.p.heads, a.p.batch), dim3(kUpdateThreads), 0,
+  hipLaunchKernelGGL((delta_update_kernel<D, CL, VEC, THREADS>),
+                     dim3((a.p.V + cols - 1) / cols, a.p.heads, a.p.batch), dim3(THREADS), 0,
                      stream, a);
 }
 
+// Eight groups of rows, so that a thread has up to 16 loads under way (256
+// rows x 32 heads of 64 x 64: 57 us with eight groups, 62 with four, 103 with
+// sixteen; 128 x 128: 218, 350 with two, 308 with sixteen); half the columns a
+// workgroup where the head has no more.  States whose rows do not start on 16 bytes go by
+// single elements (64 x 63: 60 us; 66 with four groups, 118 of 128 columns).
 template <typename D> static void delta_update_pick(const DeltaUpdate& a, hipStream_t stream) {
   const DeltaParams& p = a.p;
   const bool vec = p.V % 4 == 0 && aligned16(a.states) && a.st_slot % 4 == 0;
-  if (!vec) delta_update_launch<D, 64, 1>(a, stream);
-  else if (p.V <= 64) delta_update_launch<D, 16, 4>(a, stream);
-  else delta_update_launch<D, 32, 4>(a, stream);
+  if (!vec) delta_update_launch<D, 64, 1, 512>(a, stream);
+  else if (p.V <= 64) delta_update_launch<D, 16, 4, 128>(a, stream);
+  else delta_update_launch<D, 32, 4, 256>(a, stream);
 }
 
 }  // namespace sconv

@@ -671,11 +671,16 @@ static int delta_backward(const DeltaBwd& a, int64_t rows, hipStream_t stream) {
   if (int rc = delta_prepare<D, KP, true>(what, p, rows, stream)) return rc;
   const bool vec = p.qk_vec && a.do_vec;
   const dim3 walk(512);
-  if (delta_wide(p)) {
-    const dim3 grid((p.V + 127) / 128, p.heads, p.batch);
-    if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false, true>), grid, walk, 0, stream, a);
-    else hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false, false>), grid, walk, 0, stream, a);
-  } else {
+  bool wide = false;
+  if constexpr (sizeof(typename D::storage) == 2) {
+    wide = delta_wide(p);
+    if (wide) {
+      const dim3 grid((p.V + 127) / 128, p.heads, p.batch);
+      if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false, true>), grid, walk, 0, stream, a);
+      else hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false, false>), grid, walk, 0, stream, a);
+    }
+  }
+  if (!wide) {
     const dim3 grid((p.V + 63) / 64, p.heads, p.batch);
     if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, true, true>), grid, walk, 0, stream, a);
     else hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, true, false>), grid, walk, 0, stream, a);

@@ -362,12 +362,23 @@ template <typename D, int V, typename... A> static void launch_layer_n(int nv, i
   }
 }
 
-// Workgroups of the backward pass, and rows of its workspace: four rows each
-// at least, at most one workgroup a CU where registers hold the rows, four
-// where they are read twice.
-static int64_t layer_parts(int64_t rows, int32_t dim) {
-  const int64_t most = dim <= 8192 ? 256 : 1024;
-  return rows < 4 * most ? cdiv(rows, 4) : most;
+// Workgroups of the backward pass; each writes its share of 2 dim sums, which
+// costs more than a workgroup gains below four rows (1000 x 4096 bf16: 20.0 us,
+// 25.9 with two rows each).  Where registers hold the rows one workgroup a CU
+// keeps memory busy (8192 x 8192 bf16: 87 us, two 100), but for short rows from
+// eight a workgroup on (2048 x 4096: 23 us, two 27): those of 8 KB (32768 x 4096
+// bf16: 161 us, one 184, four 188; 16384 x 4096 fp32: 150, two 156), or with a
+// fourth stream, dresidual, in vectors of 4 KB (8192 x 2048 bf16: 37, one 44;
+// 32768 x 4096: 189, two 207).  Rows read twice are latency: four a CU (4096 x
+// 12001: 463 us, one 1195) from two rows on (1024 x 12001: 192 us, from four 290).
+static int64_t layer_parts(int64_t rows, bool is_short, bool held) {
+  if (!held) return rows < 2048 ? cdiv(rows, 2) : 1024;
+  if (rows < 4096) return rows < 1024 ? cdiv(rows, 4) : 256;
+  return is_short ? 512 : 256;
+}
+// No fewer for either type, at any alignment: 8192 channels are always held.
+static int64_t layer_parts_most(int64_t rows, int32_t dim) {
+  return layer_parts(rows, dim <= 4096, dim <= 8192);
 }
 
 }  // namespace sconv
@@ -434,7 +445,7 @@ extern "C" int layer_norm_bwd_workspace(int64_t rows, int32_t dim, int64_t* floa
   clear_error();
   if (rows < 0 || dim < 0 || !floats)
     return fail(SCONV_ERR_INVALID, "layer_norm_bwd_workspace: rows and dim must be >= 0, floats not NULL");
-  *floats = layer_parts(rows, dim) * 2 * dim;
+  *floats = layer_parts_most(rows, dim) * 2 * dim;
   return SCONV_OK;
 }
 
@@ -455,7 +466,7 @@ extern "C" int layer_norm_bwd(const void* dout, int64_t dout_stride_r, const voi
   if (dim == 0) return SCONV_OK;
   if (!dweight || (rows > 0 && (!dout || !x || !weight || !dx || !workspace)))
     return fail(SCONV_ERR_INVALID, "%s: NULL pointer", fn);
-  const int64_t parts = layer_parts(rows, dim), need = parts * 2 * dim;
+  const int64_t need = layer_parts_most(rows, dim) * 2 * dim;
   if (workspace_floats < need)
     return fail(SCONV_ERR_INVALID, "%s: workspace holds %lld floats, %lld needed", fn,
                 (long long)workspace_floats, (long long)need);
@@ -484,11 +495,11 @@ extern "C" int layer_norm_bwd(const void* dout, int64_t dout_stride_r, const voi
   p.dout = dout; p.x = x; p.w = weight; p.dres = dresidual; p.dx = dx; p.partial = workspace;
   p.do_rs = in[0].st; p.x_rs = in[1].st; p.dr_rs = in[2].st; p.dx_rs = po.st; p.rows = rows;
   p.dim = dim; p.eps = eps;
+  const int vec16 = (int)(16 / es);
+  const bool vec = norm_vec({in[0], in[1], in[2], po}, vec16) && aligned16(weight);
+  const int V = vec ? vec16 : 1, T = norm_threads(dim, V), nv = norm_vectors(dim, V, T);
+  const uint32_t grid = (uint32_t)layer_parts(rows, dim * es <= (dresidual && vec ? 4096 : 8192), nv > 0);
   if (rows > 0) {
-    const int vec16 = (int)(16 / es);
-    const bool vec = norm_vec({in[0], in[1], in[2], po}, vec16) && aligned16(weight);
-    const int V = vec ? vec16 : 1, T = norm_threads(dim, V), nv = norm_vectors(dim, V, T);
-    const uint32_t grid = (uint32_t)parts;
     if (nv > 0) {
       if (dtype == SCONV_BF16) {
         if (vec) launch_layer_n<Bf16, 8>(nv, T, p, grid, stream);
@@ -506,6 +517,6 @@ extern "C" int layer_norm_bwd(const void* dout, int64_t dout_stride_r, const voi
   }
   hipLaunchKernelGGL(layer_dweight_kernel, dim3((uint32_t)cdiv(2 * (int64_t)dim, kSumCols)),
                      dim3(kSumCols * kSumGroups), 0, stream, workspace, dweight, dbias, dim,
-                     (int32_t)parts);
+                     (int32_t)grid);
   return check_launch(fn);
 }

@@ -944,9 +944,10 @@ def _matrix_pool(t: Optional[torch.Tensor], heads: int, K: int, V: int, name: st
         raise TypeError(f"{name} must be float32, got {t.dtype}")
     if t.dim() != 4 or t.shape[1:] != (heads, K, V):
         raise ValueError(f"{name} must be [num_slots, value_heads, K, V]")
-    if t.shape[0] and not t[0].is_contiguous():
+    stride = t.stride()
+    if stride[1:] != (K * V, V, 1) and t.shape[0] and not t[0].is_contiguous():
         raise ValueError(f"{name} needs dense slots")
-    return t.data_ptr(), t.shape[0], t.stride(0)
+    return t.data_ptr(), t.shape[0], stride[0]
 
 
 def _sixteens(n: int) -> int:

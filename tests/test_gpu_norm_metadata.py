@@ -98,6 +98,18 @@ def test_norm_and_gradients(dim, dtype):
     check_norm(x, None, w, None, 1e-3, False)
 
 
+@pytest.mark.parametrize("rows,dim", [(4100, 136), (4100, 2056), (2051, 8193)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_of_many_rows(rows, dim, dtype):
+    """The counts of workgroups that share a call's rows, one row left over."""
+    dt = DT[dtype]
+    x, g = rand(1, rows, dim, dtype=dt), rand(2, rows, dim, dtype=dt)
+    w = (rand(3, dim) * 0.2 + 1).to(dt)
+    ref = grads(R.f64(g), R.f64(x), R.f64(w), 1e-5, None)
+    for n, t in zip(ref, lib.layer_norm_bwd(g.cuda(), x.cuda(), w.cuda(), 1e-5)):
+        R.check(t, *ref[n], n)
+
+
 @pytest.mark.parametrize("rows", [0, 1, 2, 513, 1500])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_norm_row_counts(rows, dtype):
