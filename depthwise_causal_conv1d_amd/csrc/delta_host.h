@@ -47,9 +47,9 @@ inline int delta_sizes(const DeltaCall& c) {
   if (c.K > kDeltaMaxK)
     return fail(SCONV_ERR_UNSUPPORTED, "%s: key heads of %d channels (at most %d)", c.what, c.K,
                 kDeltaMaxK);
-  // chunks, heads and sequences are grid dimensions of one workgroup each at least
+  // chunks, heads and sequences are grid dimensions, of at most 512 threads each
   if (c.tokens > INT32_MAX - 4097 || c.V > (1 << 20) || c.heads > 65535 || c.batch > 65535 ||
-      !valid_grid(delta_rows(c.tokens, c.batch, 32) + 1, 256))
+      !valid_grid(delta_rows(c.tokens, c.batch, 32) + 1, 512))
     return fail(SCONV_ERR_UNSUPPORTED, "%s: too many tokens, sequences, heads or channels", c.what);
   return SCONV_OK;
 }

@@ -82,6 +82,7 @@ def test_no_ops_and_limits(lib):
         assert f(lib, V=(1 << 20) + 1) == 2
     assert fwd(lib, T=(1 << 31) - 4096) == 2 and bwd(lib, T=(1 << 31) - 4096) == 2
     assert fwd(lib, T=1 << 30) == 2  # more chunks than one launch takes
+    assert fwd(lib, T=3 << 27) == 2 and bwd(lib, T=3 << 27) == 2
     assert bwd(lib, batch=0) == 0 and bwd(lib, V=0) == 0 and upd(lib, batch=0) == 0
 
 
