@@ -122,6 +122,29 @@ inline bool delta_wide(const DeltaParams& p) {
   return p.V > 64 && (int64_t)p.batch * p.heads * ((p.V + 63) / 64) > 256;
 }
 
+// Workgroups of a walk with `cols` blocks of columns.  Those of one sequence
+// and key head read the same K and Q, so they take one XCD's cache: numbers 8
+// apart, as long as that leaves no XCD with more than its share (the call of 8 x
+// 4096 tokens, two value heads a key head: 537 us, in plain order 550; 3 x 4096
+// of 128 x 256: 380 and 393; with few workgroups nothing is gained, 1 x 8192 x 16
+// heads: 356 and 351).
+inline dim3 delta_walk_grid(DeltaParams& p, int32_t cols) {
+  const int64_t pairs = (int64_t)p.batch * (p.heads / p.group), n = (int64_t)p.group * cols;
+  const int64_t each = cdiv(pairs, 8);
+  p.spread = each * n <= 32 || 8 * each <= pairs + pairs / 4 ? 8 : 1;
+  return dim3((uint32_t)(cdiv(pairs, p.spread) * p.spread * n));
+}
+
+// Whether the walks' and the preparation's grids are one launch each.
+inline int delta_grids(const DeltaCall& c) {
+  if (c.heads == 0) return SCONV_OK;
+  const int64_t group = c.heads / c.key_heads, pairs = ((int64_t)c.batch * c.key_heads + 7) / 8 * 8;
+  const int64_t rows = (delta_rows(c.tokens, c.batch, 32) + 7) / 8 * 8;
+  if (pairs * group * cdiv(c.V, 64) * 512 >= (int64_t)1 << 32 || rows * group * 64 >= (int64_t)1 << 32)
+    return fail(SCONV_ERR_UNSUPPORTED, "%s: too many tokens, sequences, heads or channels", c.what);
+  return SCONV_OK;
+}
+
 inline void delta_packing(const DeltaCall&, DeltaParams& p, const int32_t* qsl, const int32_t* slots,
                           const uint8_t* has, int32_t pad) {
   p.qsl = qsl, p.slots = slots, p.has = has, p.pad = pad;

@@ -99,7 +99,8 @@ __device__ __forceinline__ void unit_lower_inverse(float* m, int lane) {
 template <int C, bool GRAD> constexpr int kPrepFrags = (GRAD ? 3 : 2) * kDeltaFrags<C>;
 
 // One wave a chunk and value head.  Bound by latency: three waves a SIMD are
-// what the LDS of a triangle leaves room for.
+// what the LDS of a triangle leaves room for.  The value heads of a key head
+// read the same rows, so they come 8 workgroups apart: on one XCD, soon after.
 template <typename D, int KP, bool GRAD, bool VEC>
 __global__ __launch_bounds__(64, VEC ? 3 : 2) void delta_prep_kernel(DeltaParams p) {
   using T = Tile<D>;
@@ -108,7 +109,8 @@ __global__ __launch_bounds__(64, VEC ? 3 : 2) void delta_prep_kernel(DeltaParams
   __shared__ __attribute__((aligned(16))) float m[NT * (NT + 1) / 2 * kTileFloats];
   __shared__ __attribute__((aligned(16))) float gh[C], gl[C], bt[C];
   const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
-  const int32_t row = blockIdx.x, h = blockIdx.y;
+  const int32_t x = blockIdx.x >> 3, row = x / p.group * 8 + (blockIdx.x & 7);
+  const int32_t h = blockIdx.y * p.group + x % p.group;
   const DeltaChunk c = delta_find<C>(p, row);
   if (c.len == 0) return;
 
@@ -248,7 +250,7 @@ __global__ __launch_bounds__(64, VEC ? 3 : 2) void delta_prep_kernel(DeltaParams
 
 template <typename D, int KP, bool GRAD>
 static int delta_prepare(const char* what, const DeltaParams& p, int64_t rows, hipStream_t stream) {
-  const dim3 grid((uint32_t)rows, p.heads), wave(64);
+  const dim3 grid((uint32_t)(cdiv(rows, 8) * 8 * p.group), p.heads / p.group), wave(64);
   if (p.qk_vec) hipLaunchKernelGGL((delta_prep_kernel<D, KP, GRAD, true>), grid, wave, 0, stream, p);
   else hipLaunchKernelGGL((delta_prep_kernel<D, KP, GRAD, false>), grid, wave, 0, stream, p);
   return check_launch(what);

@@ -58,6 +58,7 @@ struct DeltaParams {
   int32_t batch, pad, heads, group, K, V;  // heads: value heads; group: of one key head
   float scale;
   int32_t gates_f32, qk_vec, v_vec;
+  int32_t spread;  // of a walk's workgroups, by delta_walk_grid
   // operands of every chunk: frags (2 KB each), then vectors
   char* frags;
   float* vectors;

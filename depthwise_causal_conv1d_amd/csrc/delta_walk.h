@@ -15,6 +15,18 @@
 
 namespace sconv {
 
+// A workgroup's sequence, value head and block of columns; see delta_walk_grid.
+struct WalkPlace {
+  int32_t b, h, kh, block;
+  __device__ __forceinline__ WalkPlace(const DeltaParams& p, int32_t cols) {
+    const uint32_t L = blockIdx.x, m = L / (uint32_t)p.spread, n = (uint32_t)(p.group * cols);
+    const uint32_t pair = m / n * (uint32_t)p.spread + L % (uint32_t)p.spread, i = m % n;
+    const uint32_t key_heads = p.heads / p.group;
+    b = (int32_t)(pair / key_heads), kh = (int32_t)(pair % key_heads);
+    h = kh * p.group + (int32_t)i / cols, block = (int32_t)i % cols;
+  }
+};
+
 template <typename D, int KP, int NW> struct WalkLds {
   using S = typename D::storage;
   static constexpr int C = kDeltaChunk<D>;

@@ -58,11 +58,13 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
 
   const DeltaParams& p = a.p;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-  const int32_t h = blockIdx.y, b = blockIdx.z, kh = h / p.group;
+  const WalkPlace place(p, (p.V + 16 * NW - 1) / (16 * NW));
+  const int32_t b = place.b, h = place.h, kh = place.kh;
+  if (b >= p.batch) return;
   const int32_t slot = p.slots ? p.slots[b] : b;
   if (p.slots && slot == p.pad) return;
   const int32_t start = p.qsl[b], end = p.qsl[b + 1];
-  const int32_t cols0 = blockIdx.x * 16 * NW;
+  const int32_t cols0 = place.block * 16 * NW;
   const int32_t chunks = (end - start + C - 1) / C, row0 = start / C + b;
   const int64_t KV = (int64_t)p.K * p.V;
   const S* q = static_cast<const S*>(p.q) + kh * p.q_h;
@@ -665,7 +667,7 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
 }
 
 template <typename D, int KP>
-static int delta_backward(const DeltaBwd& a, int64_t rows, hipStream_t stream) {
+static int delta_backward(DeltaBwd a, int64_t rows, hipStream_t stream) {
   const char* what = "gated_delta_rule_varlen_bwd";
   const DeltaParams& p = a.p;
   if (int rc = delta_prepare<D, KP, true>(what, p, rows, stream)) return rc;
@@ -675,13 +677,13 @@ static int delta_backward(const DeltaBwd& a, int64_t rows, hipStream_t stream) {
   if constexpr (sizeof(typename D::storage) == 2) {
     wide = delta_wide(p);
     if (wide) {
-      const dim3 grid((p.V + 127) / 128, p.heads, p.batch);
+      const dim3 grid = delta_walk_grid(a.p, (p.V + 127) / 128);
       if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false, true>), grid, walk, 0, stream, a);
       else hipLaunchKernelGGL((delta_back_kernel<D, KP, 8, false, false>), grid, walk, 0, stream, a);
     }
   }
   if (!wide) {
-    const dim3 grid((p.V + 63) / 64, p.heads, p.batch);
+    const dim3 grid = delta_walk_grid(a.p, (p.V + 63) / 64);
     if (vec) hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, true, true>), grid, walk, 0, stream, a);
     else hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, true, false>), grid, walk, 0, stream, a);
   }
@@ -719,6 +721,7 @@ extern "C" int gated_delta_rule_varlen_bwd(
   DeltaCall c = {what, total_T, batch, key_heads, value_heads, K, V, dtype, gate_dtype};
   if (int rc = delta_sizes(c)) return rc;
   if (batch == 0 || value_heads == 0 || V == 0) return SCONV_OK;
+  if (int rc = delta_grids(c)) return rc;
   if (!query_start_loc) return fail(SCONV_ERR_INVALID, "%s: NULL query_start_loc", what);
   if (int rc = delta_inputs(c, a.p, q, q_stride_t, q_stride_h, k, k_stride_t, k_stride_h, v,
                             v_stride_t, v_stride_h, g, g_stride_t, g_stride_h, beta, b_stride_t,
