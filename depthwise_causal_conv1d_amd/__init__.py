@@ -1,5 +1,6 @@
 """libsconv: paged depthwise causal short convolution for AMD MI355X (gfx950),
-with the recurrence, the norm and the gradients of the layer around it.
+with the recurrences (gated diagonal, gated delta rule), the norms, the
+metadata and the gradients of the layer around it.
 
 The compute lives in hand-written HIP kernels behind a C ABI
 (``include/sconv.h``, built into ``libsconv.so``); this package is the thin

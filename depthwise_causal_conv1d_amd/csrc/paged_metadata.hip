@@ -4,7 +4,10 @@
 // Two running sums over the requests (tokens, and blocks that a table lacks)
 // decide everything; the rest is a search per token.  Up to kMetaReqs
 // requests every workgroup makes both sums for itself in LDS: a few loads a
-// thread, against a second launch that would wait for the first.
+// thread, against a second launch that would wait for the first.  Launches one
+// after another in a graph, one (two): 256 requests of one token 4.0 us (5.9), 64
+// of 256 tokens 3.9 (6.6), 1000 of 65 6.0 (11.7), 4096 of 16 13.7 (18.5), 4096 of 64
+// 33 (31).  Latency bounds all: 1000 requests' tokens are 2 MB, 0.4 us.
 #include "sconv_device.h"
 #include "sconv_host.h"
 

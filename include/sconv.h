@@ -811,8 +811,8 @@ int rms_norm_bwd(const void* dout, int64_t dout_stride_r, const void* x, int64_t
  * heads that read it (an infinite v: for its column).
  *
  * Tensors are [total_T, heads, channels] at strides (t, h) >= 0, channels
- * contiguous (g, beta: [total_T, value_heads]); q and k load fastest where
- * rows start and end on 16 bytes.  Packing, state slots, PAD and
+ * contiguous (g, beta: [total_T, value_heads]); calls are fastest where rows
+ * of all of them start and end on 16 bytes.  Packing, state slots, PAD and
  * has_initial_state are those of causal_conv1d_varlen_fwd.
  *
  * gated_delta_rule_checkpoint_rows -- rows of the checkpoint buffer that a
