@@ -227,6 +227,18 @@ def test_long_sequences_among_many():
         assert torch.equal(R.bits(a), R.bits(b))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kh,vh,lens", [(1, 40, [70, 5]), (3, 9, [65, 0, 33])])
+def test_heads_that_share_a_key_head(kh, vh, lens, dtype):
+    """More workgroups of one sequence and key head than an XCD has CUs, and
+    sequences and key heads that the XCDs do not divide evenly."""
+    c = Case(lens, kh, vh, 24, 72 if kh > 1 else 20, dtype, seed=21, inits=(0,))
+    d = c.gpu()
+    out, m = c.forward(d)
+    got, di = c.backward(d, m)
+    c.check(out, d["pool"], got, di, "shared")
+
+
 @pytest.mark.parametrize("lead", [0, 5])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_inputs_and_gradients_as_columns_of_one_matrix(dtype, lead):
