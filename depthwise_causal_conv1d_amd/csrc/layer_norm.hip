@@ -3,8 +3,12 @@
 //
 //   s = x + residual, n = (s - mean(s)) * rsqrt(mean((s - mean)^2) + eps),
 //   out = n * weight + bias
-// The variance is a sum over differences from the mean, so a row far from
-// zero loses nothing; it costs a second exchange between the waves of a row.
+// The variance is a sum over differences from the mean, and the mean's own
+// rounding is taken out of it: the same exchange sums the differences, whose mean
+// r is what the first mean was off by, so that n = (d - r) * rsqrt(mean(d^2) - r^2
+// + eps).  A row far from zero keeps its digits (4096 channels of 4321.1: outputs of
+// 1e-8 where a mean that is left as it is gives 0.15); it costs a second exchange
+// between the waves of a row.
 #include "column_sum.h"
 #include "lane_tokens.h"
 #include "norm_rows.h"
@@ -19,16 +23,36 @@ struct LayerParams {
   float eps;
 };
 
-// The sums of the waves of a row; one LDS row an exchange, so one barrier.
+template <int CTRL> __device__ __forceinline__ float moved(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
+// The sums of the waves of a row, N = 1, 2 or 4 of them; one LDS row an exchange,
+// so one barrier.  A lane keeps one half of several sums and gives its neighbour the
+// other, so that lane i % N ends with sum i: 7 moves for four sums (24 one by one;
+// 32768 x 4096 bf16 gradients with dresidual, four sums a row: 189 us, one by one 201).
 template <int N, int kWaves>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (*lds)[N], int t) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lanes_reduce<64>(v[i], Add());
-  if constexpr (kWaves > 1) {
-    if ((t & 63) == 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) lds[t >> 6][i] = v[i];
+  static_assert(N == 1 || N == 2 || N == 4);
+  float x;
+  if constexpr (N == 1) {
+    x = lanes_reduce<64>(v[0], Add());
+  } else {
+    const bool odd = t & 1, high = t & 2;
+    x = (odd ? v[1] : v[0]) + moved<0xB1>(odd ? v[0] : v[1]);  // lanes 1 0 3 2
+    if constexpr (N == 4) {
+      const float y = (odd ? v[3] : v[2]) + moved<0xB1>(odd ? v[2] : v[3]);
+      x = (high ? y : x) + moved<0x4E>(high ? x : y);  // lanes 2 3 0 1
+    } else {
+      x += moved<0x4E>(x);
     }
+    x += moved<0x124>(x);  // four lanes on, of sixteen
+    x += moved<0x128>(x);  // eight
+    x += __shfl_xor(x, 16, 64);
+    x += __shfl_xor(x, 32, 64);
+  }
+  if constexpr (kWaves > 1) {
+    if ((t & 63) < N) lds[t >> 6][t & 63] = x;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -36,8 +60,24 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*lds)[N], int t) 
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) v[i] += lds[w][i];
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      v[i] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), i));
   }
 }
+
+// Of a row, from the sums of the differences d from its rounded mean: their own
+// mean, and 1 / the standard deviation around it.
+struct RowScale {
+  float rest, rstd;
+  __device__ __forceinline__ RowScale(float sum, float squares, float n, float eps) {
+    rest = sum / n;
+    const float var = squares / n - rest * rest;
+    rstd = 1.0f / sqrtf((var < 0.f ? 0.f : var) + eps);  // a NaN stays one
+  }
+  __device__ __forceinline__ float operator()(float d) const { return __builtin_fmaf(d, rstd, -(rest * rstd)); }
+};
 
 // One workgroup a row, which it reads three times: rows too long for the registers.
 template <typename D>
@@ -50,19 +90,21 @@ __global__ __launch_bounds__(kNormThreads) void layer_fwd_simple(const LayerPara
   const S *w = static_cast<const S*>(p.w), *b = static_cast<const S*>(p.b);
   S* sum = p.sum ? static_cast<S*>(p.sum) + row * p.s_rs : nullptr;
   auto at = [&](int c) { return load_as_float<D>(x + c) + (res ? load_as_float<D>(res + c) : 0.f); };
-  float m = 0.f, sq = 0.f;
+  float m = 0.f, sum1 = 0.f, sq = 0.f;
   for (int c = threadIdx.x; c < p.dim; c += kNormThreads) m += at(c);
   const float mean = block_sum(m, lds) / (float)p.dim;
   for (int c = threadIdx.x; c < p.dim; c += kNormThreads) {
     const float d = at(c) - mean;
+    sum1 += d;
     sq = __builtin_fmaf(d, d, sq);
   }
-  const float rstd = 1.0f / sqrtf(block_sum(sq, lds) / (float)p.dim + p.eps);
+  const float all = block_sum(sum1, lds);
+  const RowScale norm(all, block_sum(sq, lds), (float)p.dim, p.eps);
   for (int c = threadIdx.x; c < p.dim; c += kNormThreads) {
     const float v = at(c);
     if (sum) sum[c] = round_to<D>(v);
     static_cast<S*>(p.out)[row * p.o_rs + c] = round_to<D>(
-        (v - mean) * rstd * load_as_float<D>(w + c) + (b ? load_as_float<D>(b + c) : 0.f));
+        norm(v - mean) * load_as_float<D>(w + c) + (b ? load_as_float<D>(b + c) : 0.f));
   }
 }
 
@@ -75,7 +117,7 @@ __global__ __launch_bounds__(kNormThreads) void layer_fwd_kernel(const LayerPara
   using S = typename D::storage;
   using P = Pack<D, V>;
   constexpr int kRows = kNormThreads / T, kWaves = T / 64;
-  __shared__ float lds[2][kWaves][1];
+  __shared__ float lmean[kWaves][1], lsum[kWaves][2];
   const int t = threadIdx.x % T;
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
   if (row >= p.rows) return;  // with a barrier below, a workgroup has one row
@@ -97,7 +139,7 @@ __global__ __launch_bounds__(kNormThreads) void layer_fwd_kernel(const LayerPara
       if (p.b) bv[j].load(b + c);
     }
   }
-  float s[NV][V], m[1] = {0.f}, sq[1] = {0.f};
+  float s[NV][V], m[1] = {0.f}, sums[2] = {0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     float f[V];
@@ -109,7 +151,7 @@ __global__ __launch_bounds__(kNormThreads) void layer_fwd_kernel(const LayerPara
       m[0] += s[j][e];
     }
   }
-  row_sums<1, kWaves>(m, lds[0], t);
+  row_sums<1, kWaves>(m, lmean, t);
   const float mean = m[0] / (float)p.dim;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -122,11 +164,12 @@ __global__ __launch_bounds__(kNormThreads) void layer_fwd_kernel(const LayerPara
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       s[j][e] = c < p.dim ? s[j][e] - mean : 0.f;
-      sq[0] = __builtin_fmaf(s[j][e], s[j][e], sq[0]);
+      sums[0] += s[j][e];
+      sums[1] = __builtin_fmaf(s[j][e], s[j][e], sums[1]);
     }
   }
-  row_sums<1, kWaves>(sq, lds[1], t);
-  const float rstd = 1.0f / sqrtf(sq[0] / (float)p.dim + p.eps);
+  row_sums<2, kWaves>(sums, lsum, t);
+  const RowScale norm(sums[0], sums[1], (float)p.dim, p.eps);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (j * T + t) * V;
@@ -134,7 +177,7 @@ __global__ __launch_bounds__(kNormThreads) void layer_fwd_kernel(const LayerPara
     wv[j].to_float(f);
     bv[j].to_float(h);
 #pragma unroll
-    for (int e = 0; e < V; ++e) s[j][e] = __builtin_fmaf(s[j][e] * rstd, f[e], h[e]);
+    for (int e = 0; e < V; ++e) s[j][e] = __builtin_fmaf(norm(s[j][e]), f[e], h[e]);
     if (c < p.dim) {
       P o;
       o.from_float(s[j]);
@@ -170,20 +213,23 @@ __global__ __launch_bounds__(kNormThreads) void layer_bwd_simple(const LayerBwdP
     const S* dr = p.dres ? static_cast<const S*>(p.dres) + row * p.dr_rs : nullptr;
     S* dx = static_cast<S*>(p.dx) + row * p.dx_rs;
     const float n = (float)p.dim;
-    float m = 0.f, sq = 0.f, one = 0.f, dot = 0.f;
+    float m = 0.f, sum1 = 0.f, sq = 0.f, one = 0.f, dot = 0.f;
     for (int c = threadIdx.x; c < p.dim; c += kNormThreads) m += load_as_float<D>(x + c);
     const float mean = block_sum(m, lds) / n;
     for (int c = threadIdx.x; c < p.dim; c += kNormThreads) {
       const float d = load_as_float<D>(x + c) - mean;
       const float wg = load_as_float<D>(g + c) * load_as_float<D>(w + c);
+      sum1 += d;
       sq = __builtin_fmaf(d, d, sq);
       one += wg;
       dot = __builtin_fmaf(wg, d, dot);
     }
-    const float rstd = 1.0f / sqrtf(block_sum(sq, lds) / n + p.eps);
-    const float flat = block_sum(one, lds) / n, proj = block_sum(dot, lds) * rstd / n;
+    const float all = block_sum(sum1, lds);
+    const RowScale norm(all, block_sum(sq, lds), n, p.eps);
+    const float ones = block_sum(one, lds), rstd = norm.rstd;
+    const float flat = ones / n, proj = (block_sum(dot, lds) - norm.rest * ones) * rstd / n;
     for (int c = threadIdx.x; c < p.dim; c += kNormThreads) {
-      const float hat = (load_as_float<D>(x + c) - mean) * rstd, gv = load_as_float<D>(g + c);
+      const float hat = norm(load_as_float<D>(x + c) - mean), gv = load_as_float<D>(g + c);
       float v = rstd * (gv * load_as_float<D>(w + c) - flat - hat * proj);
       if (dr) v += load_as_float<D>(dr + c);
       dw[c] = __builtin_fmaf(gv, hat, dw[c]);
@@ -198,7 +244,7 @@ __global__ __launch_bounds__(kNormThreads) void layer_bwd_simple(const LayerBwdP
 // The next row's loads are issued before this row's sums are exchanged, so a
 // workgroup always has a row under way: bytes bound it (32768 x 4096 bf16 161 us,
 // 5.0 TB/s; with dresidual 189, 5.7 TB/s), and for few rows two launches' latency
-// (1023 x 1001 fp32: 13 + 4 us).  16384 bf16 channels spill 44 registers of 512,
+// (1023 x 1001 fp32: 13 + 4 us).  16384 bf16 channels spill 45 registers of 512,
 // and are still faster than the two-pass kernel (4096 x 16384: 244 us; 4096 x
 // 12001, which that one takes, 463).
 template <typename D, int V, int NV, int T>
@@ -207,7 +253,7 @@ __global__ __launch_bounds__(kNormThreads) void layer_bwd_kernel(const LayerBwdP
   using P = Pack<D, V>;
   constexpr int kRows = kNormThreads / T, kWaves = T / 64;
   // each is written behind the other's barrier
-  __shared__ float lmean[kWaves][1], lsum[kWaves][3];
+  __shared__ float lmean[kWaves][1], lsum[kWaves][4];
   const int t = threadIdx.x % T, mine = threadIdx.x / T;
   const S* w = static_cast<const S*>(p.w);
   P wv[NV], xv[NV], gv[NV], dv[NV];
@@ -242,7 +288,7 @@ __global__ __launch_bounds__(kNormThreads) void layer_bwd_kernel(const LayerBwdP
   if (row < p.rows) fetch(row);
   const float n = (float)p.dim;
   for (; row < p.rows; row += step) {
-    float x[NV][V], g[NV][V], d[NV][V], m[1] = {0.f}, sums[3] = {0.f, 0.f, 0.f};
+    float x[NV][V], g[NV][V], d[NV][V], m[1] = {0.f}, sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       xv[j].to_float(x[j]);
@@ -266,11 +312,13 @@ __global__ __launch_bounds__(kNormThreads) void layer_bwd_kernel(const LayerBwdP
         sums[0] = __builtin_fmaf(x[j][e], x[j][e], sums[0]);
         sums[1] += wg;
         sums[2] = __builtin_fmaf(wg, x[j][e], sums[2]);
+        sums[3] += x[j][e];
       }
     }
-    row_sums<3, kWaves>(sums, lsum, t);
-    const float rstd = 1.0f / sqrtf(sums[0] / n + p.eps);
-    const float flat = sums[1] / n, proj = sums[2] * rstd / n;
+    row_sums<4, kWaves>(sums, lsum, t);
+    const RowScale norm(sums[3], sums[0], n, p.eps);
+    const float rstd = norm.rstd;
+    const float flat = sums[1] / n, proj = (sums[2] - norm.rest * sums[1]) * rstd / n;
     S* dx = static_cast<S*>(p.dx) + row * p.dx_rs;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -279,7 +327,7 @@ __global__ __launch_bounds__(kNormThreads) void layer_bwd_kernel(const LayerBwdP
       wv[j].to_float(f);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float hat = x[j][e] * rstd;
+        const float hat = norm(x[j][e]);
         dw[j][e] = __builtin_fmaf(g[j][e], hat, dw[j][e]);
         db[j][e] += g[j][e];
         y[e] = rstd * (g[j][e] * f[e] - flat - hat * proj) + d[j][e];

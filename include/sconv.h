@@ -939,7 +939,8 @@ int gated_delta_rule_update(
  *            residual; NULL: not kept) receives s rounded to dtype, and may be
  *            residual or x itself; so may out
  *
- * The variance is summed over differences from the mean.  A row is read once
+ * The variance is summed over differences from the mean, and the mean's rounding
+ * is taken out of both: a row far from zero keeps its digits.  A row is read once
  * up to 16384 bf16 or 8192 fp32 channels where rows start and end on 16 bytes,
  * up to 8192 elsewhere; wider rows are read three times.
  *
