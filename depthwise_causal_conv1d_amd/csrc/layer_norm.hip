@@ -432,9 +432,17 @@ static int64_t layer_parts(int64_t rows, bool is_short, bool held) {
   if (rows < 4096) return rows < 1024 ? cdiv(rows, 4) : 256;
   return is_short ? 512 : 256;
 }
-// No fewer for either type, at any alignment: 8192 channels are always held.
+// A workgroup's share of the weights' gradients is fp32 chains of its rows, then 64
+// bits add the shares.  So that no chain is longer than kChain rows, a call whose
+// workgroups would have more (in_hand rows at a time each) is several launches of
+// as many (2^20 equal terms: 4e-6 off, in chains of 2048 3e-5).
+constexpr int64_t kChain = 256;
+static int64_t layer_launches(int64_t rows, int64_t parts, int in_hand) {
+  return rows > 0 ? cdiv(rows, parts * in_hand * kChain) : 1;
+}
+// No fewer shares for either type, at any alignment: 8192 channels are always held.
 static int64_t layer_parts_most(int64_t rows, int32_t dim) {
-  return layer_parts(rows, dim <= 4096, dim <= 8192);
+  return layer_parts(rows, dim <= 4096, dim <= 8192) + (rows > 256 * kChain ? rows / kChain : 0);
 }
 
 }  // namespace sconv
@@ -555,7 +563,11 @@ extern "C" int layer_norm_bwd(const void* dout, int64_t dout_stride_r, const voi
   const bool vec = norm_vec({in[0], in[1], in[2], po}, vec16) && aligned16(weight);
   const int V = vec ? vec16 : 1, T = norm_threads(dim, V), nv = norm_vectors(dim, V, T);
   const uint32_t grid = (uint32_t)layer_parts(rows, dim * es <= (dresidual && vec ? 4096 : 8192), nv > 0);
-  if (rows > 0) {
+  // even parts of the rows, each with shares of its own
+  const int64_t launches = layer_launches(rows, grid, nv > 0 ? kNormThreads / T : 1);
+  const int64_t each = rows > 0 ? cdiv(rows, launches) : 1;
+  for (int64_t at = 0; at < rows; at += each) {
+    p.rows = rows - at < each ? rows - at : each;
     if (nv > 0) {
       if (dtype == SCONV_BF16) {
         if (vec) launch_layer_n<Bf16, 8>(nv, T, p, grid, stream);
@@ -570,9 +582,14 @@ extern "C" int layer_norm_bwd(const void* dout, int64_t dout_stride_r, const voi
       hipLaunchKernelGGL(layer_bwd_simple<F32>, dim3(grid), dim3(kNormThreads), 0, stream, p);
     }
     if (const int rc = check_launch(fn)) return rc;
+    p.dout = static_cast<const char*>(p.dout) + each * p.do_rs * es;
+    p.x = static_cast<const char*>(p.x) + each * p.x_rs * es;
+    if (p.dres) p.dres = static_cast<const char*>(p.dres) + each * p.dr_rs * es;
+    p.dx = static_cast<char*>(p.dx) + each * p.dx_rs * es;
+    p.partial += (int64_t)grid * 2 * dim;
   }
   hipLaunchKernelGGL(layer_dweight_kernel, dim3((uint32_t)cdiv(2 * (int64_t)dim, kSumCols)),
                      dim3(kSumCols * kSumGroups), 0, stream, workspace, dweight, dbias, dim,
-                     (int32_t)grid);
+                     (int32_t)(rows > 0 ? cdiv(rows, each) * grid : 0));
   return check_launch(fn);
 }

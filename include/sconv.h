@@ -11,7 +11,8 @@
  *   library allocates nothing, never synchronizes and never reads device data
  *   on the host: each call enqueues one kernel on `stream` (NULL = the null
  *   stream; sconv_fused_insert_conv_gather, sconv_paged_metadata and the entry
- *   points that take a workspace may enqueue up to three) and returns.
+ *   points that take a workspace may enqueue up to three, layer_norm_bwd one
+ *   more for every 65536 rows) and returns.
  *   This makes every call capturable in a hipGraph; grids depend on host
  *   scalars only.
  * - Strides are in ELEMENTS.  Only host scalars are validated.  Properties of
@@ -970,9 +971,10 @@ int layer_norm_bwd_workspace(int64_t rows, int32_t dim, int64_t* floats);
  *   dweight  fp32 [dim], dbias fp32 [dim] or NULL (written)
  *   workspace  fp32, layer_norm_bwd_workspace floats, the call's own until it
  *            has finished
- * The sums have a fixed order: equal inputs give equal bits.  Errors as
- * layer_norm_fwd's, and too small a workspace; SCONV_ERR_UNSUPPORTED: dim
- * above 2^28.  dim == 0 is a no-op; rows == 0 writes zeros to dweight and dbias.
+ * The sums have a fixed order: equal inputs give equal bits; no fp32 chain in
+ * them is longer than 256 rows.  Errors as layer_norm_fwd's, and too small a
+ * workspace; SCONV_ERR_UNSUPPORTED: dim above 2^28.  dim == 0 is a no-op; rows
+ * == 0 writes zeros to dweight and dbias.
  */
 int layer_norm_bwd(const void* dout, int64_t dout_stride_r, const void* x, int64_t x_stride_r,
                    const void* weight, float eps, const void* dresidual,

@@ -99,3 +99,20 @@ def test_a_nan_stays_one():
     x[1, 5] = float("nan")
     out = lib.layer_norm_fwd(x.cuda(), torch.ones(700, device="cuda"), None, 0.0)
     assert bool(out[1].isnan().all())
+
+
+@pytest.mark.parametrize("rows,dim", [(1 << 20, 1028), (1 << 18, 8196), ((1 << 20) + 77, 20)])
+def test_weights_gradients_of_a_million_equal_rows(rows, dim):
+    """Every row the same (strides of zero): a sum of equal terms, whose roundings
+    do not cancel.  No fp32 chain is longer than 256 rows: 256 EPS and a few."""
+    row, g = rand(1, dim), rand(2, dim).abs() + 0.5
+    w = torch.ones(dim)
+    hat, rstd, ed, er = statistics(R.f64(row)[None], 1e-5)
+    hat = (hat * rstd)[0]
+    ehat = (ed * rstd)[0] + hat.abs() * er[0] + 2 * R.EPS * hat.abs()
+    wide = lambda t: t.cuda()[None].expand(rows, dim)  # noqa: E731
+    dx = torch.empty(rows, dim, device="cuda")
+    _, dw, db = lib.layer_norm_bwd(wide(g), wide(row), w.cuda(), 1e-5, dx=dx)
+    G, chain = R.f64(g) * rows, 256 * R.EPS
+    R.check(db, G, (chain + 8 * R.EPS) * G.abs(), "dbias")
+    R.check(dw, G * hat, (chain + 8 * R.EPS) * (G * hat).abs() + G * ehat, "dweight")
