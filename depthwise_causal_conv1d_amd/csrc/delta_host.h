@@ -124,14 +124,15 @@ inline bool delta_wide(const DeltaParams& p) {
 
 // Workgroups of a walk with `cols` blocks of columns.  Those of one sequence
 // and key head read the same K and Q, so they take one XCD's cache: numbers 8
-// apart, as long as that leaves no XCD with more than its share (the call of 8 x
-// 4096 tokens, two value heads a key head: 537 us, in plain order 550; 3 x 4096
-// of 128 x 256: 380 and 393; with few workgroups nothing is gained, 1 x 8192 x 16
-// heads: 356 and 351).
+// apart, where that gives the XCDs even shares and they have 16 workgroups each (the
+// call of 8 x 4096 tokens, two value heads a key head: 512 us, in plain order 518; 3 x
+// 4096 of 128 x 256: 215 and 218).  With fewer nothing is gained (1 x 8192 x 16 heads:
+// 356 and 354), and with fewer pairs than XCDs the others idle (1 x 4096, 16 value
+// heads of one key head: 194 and 186; 4 of 8 x 256 columns: 184 and 181).
 inline dim3 delta_walk_grid(DeltaParams& p, int32_t cols) {
   const int64_t pairs = (int64_t)p.batch * (p.heads / p.group), n = (int64_t)p.group * cols;
   const int64_t each = cdiv(pairs, 8);
-  p.spread = each * n <= 32 || 8 * each <= pairs + pairs / 4 ? 8 : 1;
+  p.spread = pairs * n >= 128 && 8 * each <= pairs + pairs / 4 ? 8 : 1;
   return dim3((uint32_t)(cdiv(pairs, p.spread) * p.spread * n));
 }
 
