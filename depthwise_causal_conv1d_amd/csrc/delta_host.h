@@ -146,8 +146,8 @@ inline int delta_grids(const DeltaCall& c) {
   return SCONV_OK;
 }
 
-inline void delta_packing(const DeltaCall&, DeltaParams& p, const int32_t* qsl, const int32_t* slots,
-                          const uint8_t* has, int32_t pad) {
+inline void delta_packing(DeltaParams& p, const int32_t* qsl, const int32_t* slots, const uint8_t* has,
+                          int32_t pad) {
   p.qsl = qsl, p.slots = slots, p.has = has, p.pad = pad;
 }
 

@@ -90,7 +90,6 @@ __device__ __forceinline__ DeltaChunk delta_find(const DeltaParams& p, int32_t r
 // Operand pieces (frags) of a C x C triangle: 16 rows x 32 columns each.
 // Lower triangle: rows of tile r meet columns of step s <= r / 2; upper: s >= r / 2.
 template <int C> constexpr int kDeltaFrags = C == 64 ? 6 : 2;
-template <int C> constexpr int kDeltaSteps = C / 32;
 constexpr int kFragBytes = 2048;
 template <int C> __host__ __device__ constexpr int lower_frag(int r, int s) {
   return r < 2 ? r : 2 * (r - 1) + s;
@@ -154,16 +153,14 @@ template <> struct Tile<Bf16> {
   // A product's instructions one by one, the small parts first, so that a
   // caller can let those of several tiles alternate: one that waits for the
   // last one's sum leaves the matrix core idle.
-  static constexpr int kExactSplit = 2, kSplitSplit = 3, kExactFine = 3, kSplitExact = 2, kExactExact = 1;
-  template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Exact& b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
-  }
+  static constexpr int kExactSplit = 2, kSplitSplit = 3, kExactFine = 3, kSplitExact = 2;
   template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Split& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, P == 0 ? b.lo : b.hi, c, 0, 0, 0);
   }
   template <int P> static __device__ __forceinline__ f32x4 part(const Split& a, const Exact& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(P == 0 ? a.lo : a.hi, b.v, c, 0, 0, 0);
   }
+  // the product of the two small parts is below what the parts leave out
   template <int P> static __device__ __forceinline__ f32x4 part(const Split& a, const Split& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(P == 0 ? a.lo : a.hi, P == 1 ? b.lo : b.hi, c, 0, 0, 0);
   }
@@ -172,25 +169,6 @@ template <> struct Tile<Bf16> {
   }
   static __device__ __forceinline__ f32x4 mul(const Exact& a, const Exact& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ f32x4 mul(const Exact& a, const Split& b, f32x4 c) {
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.lo, c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.hi, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ f32x4 mul(const Exact& a, const Fine& b, f32x4 c) {
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.lo, c, 0, 0, 0);
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.mid, c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.hi, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ f32x4 mul(const Split& a, const Exact& b, f32x4 c) {
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.lo, b.v, c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.hi, b.v, c, 0, 0, 0);
-  }
-  // the product of the two small parts is below what the parts leave out
-  static __device__ __forceinline__ f32x4 mul(const Split& a, const Split& b, f32x4 c) {
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.lo, b.hi, c, 0, 0, 0);
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.hi, b.lo, c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.hi, b.hi, c, 0, 0, 0);
   }
   // by whole words: entries taken from the bf16 vector itself under a condition
   // have all come out as the first one
@@ -224,7 +202,7 @@ template <> struct Tile<F32> {
   using Split = Exact;
   using Fine = Exact;
 
-  static constexpr int kExactSplit = 8, kSplitSplit = 8, kExactFine = 8, kSplitExact = 8, kExactExact = 8;
+  static constexpr int kExactSplit = 8, kSplitSplit = 8, kExactFine = 8, kSplitExact = 8;
   template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Exact& b, f32x4 c) {
     if constexpr (P < 4) return __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[P], b.a[P], c, 0, 0, 0);
     else return __builtin_amdgcn_mfma_f32_16x16x4f32(a.b[P - 4], b.b[P - 4], c, 0, 0, 0);

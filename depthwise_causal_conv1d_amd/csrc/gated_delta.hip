@@ -205,7 +205,7 @@ __global__ __launch_bounds__(THREADS) void delta_update_kernel(DeltaUpdate a) {
   for (int e = 0; e < VEC; ++e)
     v[e] = on ? load_as_float<D>(static_cast<const S*>(p.v) + b * p.v_t + h * p.v_h + col + e) : 0.f;
   __syncthreads();
-  vf x = s[0] * 0.f, y = x;
+  vf x, y;
 #pragma unroll
   for (int e = 0; e < VEC; ++e) x[e] = 0.f, y[e] = 0.f;
 #pragma unroll
@@ -340,7 +340,7 @@ extern "C" int gated_delta_rule_varlen_fwd(
                             v_stride_t, v_stride_h, g, g_stride_t, g_stride_h, beta, b_stride_t,
                             b_stride_h, scale))
     return rc;
-  delta_packing(c, a.p, query_start_loc, cache_indices, has_initial_state, pad_slot_id);
+  delta_packing(a.p, query_start_loc, cache_indices, has_initial_state, pad_slot_id);
   if (has_initial_state && !states)
     return fail(SCONV_ERR_INVALID, "%s: has_initial_state without states", what);
   DeltaBuffer pool, o;
@@ -391,7 +391,7 @@ extern "C" int gated_delta_rule_update(
                             v_stride_b, v_stride_h, g, g_stride_b, g_stride_h, beta, b_stride_b,
                             b_stride_h, scale))
     return rc;
-  delta_packing(c, a.p, nullptr, state_indices, nullptr, pad_slot_id);
+  delta_packing(a.p, nullptr, state_indices, nullptr, pad_slot_id);
   if (!states) return fail(SCONV_ERR_INVALID, "%s: NULL states", what);
   DeltaBuffer pool, o;
   if (int rc = delta_pool(c, states, num_slots, st_stride_slot, state_indices != nullptr, "states",

@@ -737,7 +737,7 @@ extern "C" int gated_delta_rule_varlen_bwd(
     return rc;
   if ((total_T > 0 && !dout) || !checkpoints) return fail(SCONV_ERR_INVALID, "%s: NULL input", what);
   if (do_stride_t < 0 || do_stride_h < 0) return fail(SCONV_ERR_INVALID, "%s: negative stride", what);
-  delta_packing(c, a.p, query_start_loc, cache_indices, has_initial_state, pad_slot_id);
+  delta_packing(a.p, query_start_loc, cache_indices, has_initial_state, pad_slot_id);
   const int64_t rows = delta_rows(total_T, batch, delta_chunk(dtype));
   if (checkpoint_rows < rows || !aligned16(checkpoints))
     return fail(SCONV_ERR_INVALID, "%s: %lld checkpoint rows, needs %lld at 16 bytes", what,
