@@ -13,11 +13,13 @@
 //   M = e^(G_C - G) (U dS1^T)             (dk as written into S1)
 //   W = E_P^T Q - (beta E_A)^T K          (dk as written for later tokens)
 //   dK = M + W - beta Z,  dbeta = rowsum(dR V) - k.Z
-// The gradient of a running sum G_i is q.dq - beta k.Z - k.W - k.M, that of
-// G_C adds <dS1, S1> = e^(G_C) <dS1, S0> + sum k.M; so
-//   dg_t = sum_(i >= t) (q.dq - beta k.Z - k.W)_i + sum_(j < t) (k.M)_j
+// A gate g_t closes between the tokens j < t and i >= t, and only what passes
+// it enters its gradient.  With z_ij = E_P k_j.q_i - beta_i E_A k_i.k_j (i > j) and
+// s_i = e^G (scale q.(dO S0^T) - beta k.(dR S0^T))_i, what token i reads of S0:
+//   dg_t = sum_(i >= t) s_i + sum_(j < t) (k.M)_j + sum_(i >= t > j) z_ij
 //          + e^(G_C) <dS1, S0>
-// in which the parts that would cancel are left out.
+// Every term has the factor e^(g_t), and none is a difference of larger ones: the
+// gradient of a gate that is nearly closed keeps its digits.
 #include "delta_host.h"
 #include "delta_prep.h"
 #include "delta_walk.h"
@@ -224,6 +226,26 @@ template <int N> __device__ __forceinline__ float sums16(float (&v)[N], int r) {
   return v[0];
 }
 
+// Sums of the values of the 16 lanes of a group that come before a lane (without
+// its own), and of those from it on.
+__device__ __forceinline__ float sum_before(float v) {
+  v = lanes_moved<0x111>(v);  // shifted up by one, zero at the start
+  v += lanes_moved<0x111>(v);
+  v += lanes_moved<0x112>(v);
+  v += lanes_moved<0x114>(v);
+  return v + lanes_moved<0x118>(v);
+}
+__device__ __forceinline__ float sum_from(float v) {
+  v += lanes_moved<0x101>(v);
+  v += lanes_moved<0x102>(v);
+  v += lanes_moved<0x104>(v);
+  return v + lanes_moved<0x108>(v);
+}
+__device__ __forceinline__ float sum_groups(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
 // Row of tile n of a lower triangle of 4 x 4 tiles, counted row by row.
 __device__ __forceinline__ int tile_row(int n) { return n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0; }
 
@@ -244,6 +266,9 @@ template <typename D, int KP> struct GradLds {
   __attribute__((aligned(16))) char f[kDeltaFrags<C> * kFragBytes];  // N
   __attribute__((aligned(16))) float v[kDeltaVectors<C>];
   float part[NW][4][C], dots[NW];
+  // of a tile of z: its rows' and columns' sums (of one on the diagonal, in place
+  // of the latter, what passes each of its gates)
+  __attribute__((aligned(16))) float z[2][C / 16 * (C / 16 + 1) / 2][16];
 };
 
 // One workgroup: all gradients of a chunk's tokens for one key head, its value
@@ -541,6 +566,13 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         if (want >= TILES) break;
         const int I = tile_row(want), J = want - I * (I + 1) / 2;
         const int j = 16 * J + r;
+        f32x4 qk = zero4(), kk = zero4(), z;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const auto kj = Rows::rows(l.k, 16 * J, 32 * s, lane);
+          qk = T::mul(Rows::rows(l.q, 16 * I, 32 * s, lane), kj, qk);
+          kk = T::mul(Rows::rows(l.k, 16 * I, 32 * s, lane), kj, kk);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = 16 * I + 4 * g + e, x = i * Tri::LD + Tri::pos(j);
@@ -552,6 +584,23 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
           put_split(l.e, SMALL, x, pv);
           put_split(l.e + PARTS * SMALL, SMALL, x, av);
           put_split(l.e + 2 * PARTS * SMALL, SMALL, x, l.v[2 * C + i] * av);
+          z[e] = i > j ? pv * qk[e] - l.v[2 * C + i] * av * kk[e] : 0.f;
+        }
+        if (I == J) {  // the tile's rows i >= t and columns j < t, lane r's t
+          float passes = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float before = sum_before(z[e]);
+            passes += 4 * g + e >= r ? before : 0.f;
+          }
+          passes = sum_groups(passes);
+          if (g == 0) l.z[1][want][r] = passes;
+        } else {
+          const float cols = sum_groups((z[0] + z[1]) + (z[2] + z[3]));
+          if (g == 0) l.z[1][want][r] = cols;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[e] = lanes_reduce<16>(z[e], Add());
+          if (r == 0) *reinterpret_cast<f32x4*>(&l.z[0][want][4 * g]) = z;
         }
         if (I == J && I % 2 == 0) {
 #pragma unroll
@@ -570,6 +619,23 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
       mz[t] *= gam;
       mw[t] *= lds4(l.v + C + 16 * t + 4 * g);
     }
+    // rows' sums over this wave's channels, one quantity after the other
+    const bool last = gh + 1 == p.group;
+    const int kidx = 16 * wave + r, mine = 16 * (r >> 2) + 4 * g + (r & 3);
+    auto row_sums = [&](float* to, auto&& f) {
+      float v[4 * NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * t + e] = f(t, e, (16 * t + 4 * g + e) * Rows::LD + Rows::pos(kidx));
+      const float sum = sums16(v, r);
+      if (r < 4 * NT) to[mine] = sum;
+    };
+    row_sums(l.part[wave][0], [&](int t, int e, int i) {
+      const float bt = l.v[2 * C + 16 * t + 4 * g + e];
+      return to_float<D>(l.q[i]) * mq[t][e] - bt * (to_float<D>(l.k[i]) * mz[t][e]);
+    });
+    row_sums(l.part[wave][1], [&](int t, int e, int i) { return to_float<D>(l.k[i]) * mw[t][e]; });
     __syncthreads();
     f32x4 w[NT], neg[NT];
 #pragma unroll
@@ -595,26 +661,9 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         }
       }
     }
-    // rows' sums over this wave's channels, one quantity after the other
-    const bool last = gh + 1 == p.group;
-    const int kidx = 16 * wave + r, mine = 16 * (r >> 2) + 4 * g + (r & 3);
-    auto row_sums = [&](float* to, auto&& f) {
-      float v[4 * NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * t + e] = f(t, e, (16 * t + 4 * g + e) * Rows::LD + Rows::pos(kidx));
-      const float sum = sums16(v, r);
-      if (r < 4 * NT) to[mine] = sum;
-    };
 #pragma unroll
     for (int t = 0; t < NT; ++t) w[t] -= neg[t];
-    row_sums(l.part[wave][1], [&](int t, int e, int i) { return to_float<D>(l.k[i]) * mw[t][e]; });
     row_sums(l.part[wave][2], [&](int t, int e, int i) { return to_float<D>(l.k[i]) * mz[t][e]; });
-    row_sums(l.part[wave][0], [&](int t, int e, int i) {
-      const float bt = l.v[2 * C + 16 * t + 4 * g + e];
-      return to_float<D>(l.q[i]) * mq[t][e] - to_float<D>(l.k[i]) * (bt * mz[t][e] + w[t][e]);
-    });
     // dq and dk, over the value heads; this wave's channels of Q and K have
     // been read for the last time
 #pragma unroll
@@ -643,7 +692,24 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         all += l.dots[n];
       }
       if (t >= C) own = km = 0.f;
-      float before = km, after = own;
+      // what passes gate t, of z's tiles: those below and left of its own whole,
+      // those below it up to its column, those left of it from its row on
+      const int I = t < C ? t / 16 : 0, at16 = t % 16;
+      float whole = 0.f, below = 0.f, left = 0.f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < i; ++j) {
+          const int n = i * (i + 1) / 2 + j;
+          const float rs = l.z[0][n][at16], cs = l.z[1][n][at16];
+          whole += i > I && j < I ? rs : 0.f;
+          below += j == I ? cs : 0.f;
+          left += i == I ? rs : 0.f;
+        }
+      const float pairs = lanes_reduce<16>(whole, Add()) + sum_before(below) + sum_from(left) +
+                          l.z[1][I * (I + 3) / 2][at16];
+      float before = __shfl_up(km, 1, 64), after = own;
+      before = lane > 0 ? before : 0.f;
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const float x = __shfl_up(before, d, 64), y = __shfl_down(after, d, 64);
@@ -651,11 +717,8 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         if (lane + d < 64) after += y;
       }
       if (t < ch.len) {
-        float dg = after + (before - km) + l.v[C - 1] * all;
+        const float dg = (after + before) + (pairs + l.v[C - 1] * all);
         const float db = sv - sz;
-        // behind a closed gate the parts cancel but for their roundings
-        const float gt = l.v[3 * C + t] + l.v[4 * C + t] - (t ? l.v[3 * C + t - 1] + l.v[4 * C + t - 1] : 0.f);
-        if (gt < -104.f) dg = 0.f;  // e^g is zero in fp32
         const int64_t tok = ch.t0 + t;
         if (p.gates_f32) {
           static_cast<float*>(a.dg)[tok * a.dg_t + h * a.dg_h] = dg;
