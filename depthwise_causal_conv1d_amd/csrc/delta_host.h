@@ -25,7 +25,7 @@ inline DeltaSpace delta_space(int64_t total_T, int32_t batch, int32_t heads, int
   const int C = delta_chunk(dtype), nf = C == 64 ? kDeltaFrags<64> : kDeltaFrags<32>;
   const int64_t n = delta_rows(total_T, batch, C) * heads;
   DeltaSpace s;
-  s.vectors = n * 5 * C;
+  s.vectors = n * (5 * C + 16);
   s.fwd = s.vectors + n * 2 * nf * (kFragBytes / 4);
   s.bwd_rows = s.vectors + n * 3 * nf * (kFragBytes / 4);
   s.bwd_states = s.bwd_rows + n * C * tiles16(V) * 16;

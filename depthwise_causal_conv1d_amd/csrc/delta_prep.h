@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "delta_rule.h"
+#include "norm_rows.h"
 
 namespace sconv {
 
@@ -23,6 +24,10 @@ __device__ __forceinline__ f32x4 mul16(const f32x4& x, const f32x4& y, f32x4 c) 
   for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], c, 0, 0, 0);
   return c;
 }
+
+struct Larger {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
 
 // A lower triangle of 16 x 16 tiles in LDS, tile after tile; a row of 20 floats
 // lets 16 rows be read 16 bytes each without bank conflicts.
@@ -157,13 +162,23 @@ __global__ __launch_bounds__(64, VEC ? 3 : 2) void delta_prep_kernel(DeltaParams
       vec[lane] = expf((float)sum);
       vec[C + lane] = expf((float)(whole - sum));
       vec[2 * C + lane] = b;
-      vec[3 * C + lane] = gh[lane];
-      vec[4 * C + lane] = gl[lane];
+      if constexpr (GRAD) {
+        vec[kDeltaSums<C> + lane] = gh[lane];
+        vec[kDeltaSums<C> + C + lane] = gl[lane];
+      }
     }
   }
   __syncthreads();
 #pragma unroll
   for (int I = 0; I < NT; ++I) mask(I, kf[I]);
+  // A factor for entries of which a lane has none above `most`; its inverse goes to
+  // the vectors.
+  auto factor = [&](float most, int at) {
+    if constexpr (!T::kScaled) return 1.f;
+    const Pow2 by(groups_max(lanes_reduce<16>(most, Larger())));
+    if (lane == 0) vec[kDeltaFactors<C> + at] = by.down;
+    return by.up;
+  };
   // Tiles of A and P, e_ij once for both.  An accumulator is then a piece of a
   // frag as it lies: rows j and columns i for P's, rows i and columns j for P^T's.
   constexpr float kLog2e = 1.44269504088896340736f;
@@ -200,53 +215,74 @@ __global__ __launch_bounds__(64, VEC ? 3 : 2) void delta_prep_kernel(DeltaParams
       }
     }
     if constexpr (!GRAD) {
+      float most = 0.f;
+#pragma unroll
+      for (int J = 0; J <= I; ++J) most = max4(pt[I][J], most);
+      const float up = factor(most, 4 + I);
 #pragma unroll
       for (int s = 0; s <= I / 2; ++s)
         T::put(frags + (NF + lower_frag<C>(I, s)) * kFragBytes, lane,
-               T::split(pt[I][2 * s], 2 * s + 1 <= I ? pt[I][2 * s + 1] : zero4()));
-    } else if (I % 2 == 1) {
+               T::pair(pt[I][2 * s], 2 * s + 1 <= I ? pt[I][2 * s + 1] : zero4(), up));
+    } else if (I % 2 == 1) {  // P^T's columns of this step are complete, its rows are not
+      float most = 0.f;
+#pragma unroll
+      for (int J = 0; J <= I; ++J) {
+        most = max4(pt[I][J], most);
+        if (J < I) most = max4(pt[I - 1][J], most);
+      }
+      const float up = factor(most, 4 + I / 2);
 #pragma unroll
       for (int J = 0; J <= I; ++J)
         T::put(frags + (2 * NF + upper_frag<C>(J, I / 2)) * kFragBytes, lane,
-               T::split(J <= I - 1 ? pt[I - 1][J] : zero4(), pt[I][J]));
+               T::pair(J <= I - 1 ? pt[I - 1][J] : zero4(), pt[I][J], up));
     }
   }
   __syncthreads();
   unit_lower_inverse<C>(m, lane);
   // N = T - I; what lies above the diagonal of a frag's 32 columns is zero
 #pragma unroll
-  for (int R = 0; R < NT; ++R)
+  for (int R = 0; R < NT; ++R) {
+    f32x4 x[C / 32][2];
+    float most = 0.f;
 #pragma unroll
-    for (int s = 0; s <= R / 2; ++s) {
-      f32x4 x[2];
+    for (int s = 0; s <= R / 2; ++s)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int J = 2 * s + u;
-        x[u] = J <= R ? lds4(m + tile_at(R, J <= R ? J : 0) + r * kTileLd + 4 * g) : zero4();
+        x[s][u] = J <= R ? lds4(m + tile_at(R, J <= R ? J : 0) + r * kTileLd + 4 * g) : zero4();
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (J == R) x[u][e] = 4 * g + e < r ? x[u][e] : 0.f;
+          if (J == R) x[s][u][e] = 4 * g + e < r ? x[s][u][e] : 0.f;
+        most = max4(x[s][u], most);
       }
-      T::put(frags + lower_frag<C>(R, s) * kFragBytes, lane, T::split(x[0], x[1]));
-    }
+    const float up = factor(most, (GRAD ? kFactorsN : 0) + R);
+#pragma unroll
+    for (int s = 0; s <= R / 2; ++s)
+      T::put(frags + lower_frag<C>(R, s) * kFragBytes, lane, T::pair(x[s][0], x[s][1], up));
+  }
   if constexpr (GRAD) {
 #pragma unroll
-    for (int R = 0; R < NT; ++R)
+    for (int R = 0; R < NT; ++R) {
+      f32x4 x[C / 32][2];
+      float most = 0.f;
 #pragma unroll
-      for (int s = R / 2; s < C / 32; ++s) {
-        f32x4 x[2];
+      for (int s = R / 2; s < C / 32; ++s)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int I = 2 * s + u;
           const float* at = m + tile_at(I >= R ? I : R, R) + 4 * g * kTileLd + r;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[u][e] = I >= R ? at[e * kTileLd] : 0.f;
-            if (I == R) x[u][e] = r < 4 * g + e ? x[u][e] : 0.f;
+            x[s][u][e] = I >= R ? at[e * kTileLd] : 0.f;
+            if (I == R) x[s][u][e] = r < 4 * g + e ? x[s][u][e] : 0.f;
           }
+          most = max4(x[s][u], most);
         }
-        T::put(frags + (NF + upper_frag<C>(R, s)) * kFragBytes, lane, T::split(x[0], x[1]));
-      }
+      const float up = factor(most, R);
+#pragma unroll
+      for (int s = R / 2; s < C / 32; ++s)
+        T::put(frags + (NF + upper_frag<C>(R, s)) * kFragBytes, lane, T::pair(x[s][0], x[s][1], up));
+    }
   }
 }
 

@@ -21,12 +21,13 @@
 // 16 h + 4 g + e.  What R, U and S need as operands therefore never leaves
 // the registers; K and Q are laid out in LDS in that order.
 //
-// bf16 inputs: q, k, v are exact operands.  What is computed in fp32 (S, R,
-// U, N, P) enters as the sum of two bf16 parts, which leave out 2^-16 of the
-// value at most; what is added to a state as the sum of three, all 24 bits.
-// Sums are fp32.  (2048 tokens of one head, decays of 0.99: states are 9e-7
-// off so, 2.9e-6 with two parts everywhere, 4e-3 with one.)  fp32 inputs: fp32
-// matrix instructions, nothing is split.
+// bf16 inputs: q, k, v are exact operands.  What is computed in fp32 enters
+// beside them as the sum of three bf16 parts, all 24 bits (S, what is added to a
+// state), and beside each other (R, U, N, P) as the sum of two fp16 parts of the
+// value times a power of two that brings the largest of its tile or column to 2^14:
+// 22 bits, down to 2^-17 of that largest.  Three products of such parts take what
+// three of two bf16 parts do, which hold 16 bits.  Sums are fp32.  fp32 inputs:
+// fp32 matrix instructions, nothing is split.
 #pragma once
 
 #include <type_traits>
@@ -39,6 +40,8 @@ namespace sconv {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -97,8 +100,16 @@ template <int C> __host__ __device__ constexpr int lower_frag(int r, int s) {
 template <int C> __host__ __device__ constexpr int upper_frag(int r, int s) {
   return C == 32 ? r : r < 2 ? 2 * r + s : r + 2;
 }
-// Per chunk: e^G, e^(G_C - G), beta, and G as a sum of two floats.
-template <int C> constexpr int kDeltaVectors = 5 * C;
+// Per chunk: e^G, e^(G_C - G), beta; sixteen factors, by which a triangle's tiles are
+// to be multiplied (N's and P's of a row of tiles, or N^T's of a row and P^T's of a
+// step of columns, four each; for gradients then N's); for gradients G as a sum of
+// two floats.  fp32 triangles have no factors.
+template <int C> constexpr int kDeltaVectors = 5 * C + 16;
+template <int C> constexpr int kDeltaFactors = 3 * C;
+template <int C> constexpr int kDeltaSums = 3 * C + 16;
+constexpr int kFactorsN = 8;
+// What a walk takes of these.
+template <typename D, int C> constexpr int kWalkVectors = sizeof(typename D::storage) == 2 ? 3 * C + 8 : 3 * C;
 
 // States of a chunk (checkpoints, and their gradients) lie as accumulator
 // tiles: per row and value head ceil(V / 16) x ceil(K / 16) tiles of 1 KB, a
@@ -110,6 +121,28 @@ __host__ __device__ constexpr int64_t delta_state_floats(int32_t K, int32_t V) {
 
 // ---------------------------------------------------------------- operands
 
+// The larger value of the four groups of 16 lanes, for each lane of a group.
+__device__ __forceinline__ float groups_max(float v) {
+  uint32_t b = __float_as_uint(v);
+  const auto x = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const float m = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+  b = __float_as_uint(m);
+  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
+__device__ __forceinline__ float max4(const f32x4& a, float m) {
+  return fmaxf(fmaxf(fmaxf(m, fabsf(a[0])), fmaxf(fabsf(a[1]), fabsf(a[2]))), fabsf(a[3]));
+}
+// A power of two that brings `most` to [2^14, 2^15) (a value below 2^-111 less
+// far), and 1 / it.
+struct Pow2 {
+  float up, down;
+  explicit __device__ __forceinline__ Pow2(float most) {
+    const uint32_t b = min(268u - (__float_as_uint(most) >> 23), 253u);
+    up = __uint_as_float(b << 23), down = __uint_as_float((254u - b) << 23);
+  }
+};
+
 template <typename D> struct Tile;
 
 template <> struct Tile<Bf16> {
@@ -117,7 +150,33 @@ template <> struct Tile<Bf16> {
   struct Exact { bf16x8 v; };
   struct Split { bf16x8 hi, lo; };
   struct Fine { bf16x8 hi, mid, lo; };
+  struct Pair { f16x8 hi, lo; };
+  struct Half { f16x8 v; };
+  static constexpr bool kScaled = true;
 
+  static __device__ __forceinline__ Pair pair(const f32x4& a, const f32x4& b, float up) {
+    Pair o;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const f32x2 x = (e < 4 ? (f32x2){a[e], a[e + 1]} : (f32x2){b[e - 4], b[e - 3]}) * up;
+      const f16x2 h = __builtin_convertvector(x, f16x2);
+      const f16x2 l = __builtin_convertvector(x - __builtin_convertvector(h, f32x2), f16x2);
+      o.hi[e] = h[0], o.hi[e + 1] = h[1];
+      o.lo[e] = l[0], o.lo[e + 1] = l[1];
+    }
+    return o;
+  }
+  // of values of 8 bits
+  static __device__ __forceinline__ Half half(const f32x4& a, const f32x4& b, float up) {
+    Half o;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const f32x2 x = (e < 4 ? (f32x2){a[e], a[e + 1]} : (f32x2){b[e - 4], b[e - 3]}) * up;
+      const f16x2 h = __builtin_convertvector(x, f16x2);
+      o.v[e] = h[0], o.v[e + 1] = h[1];
+    }
+    return o;
+  }
   static __device__ __forceinline__ Fine fine(const f32x4& a, const f32x4& b) {
     Fine o;
 #pragma unroll
@@ -153,7 +212,7 @@ template <> struct Tile<Bf16> {
   // A product's instructions one by one, the small parts first, so that a
   // caller can let those of several tiles alternate: one that waits for the
   // last one's sum leaves the matrix core idle.
-  static constexpr int kExactSplit = 2, kSplitSplit = 3, kExactFine = 3, kSplitExact = 2;
+  static constexpr int kExactSplit = 2, kSplitSplit = 3, kExactFine = 3, kSplitExact = 2, kPairPair = 3, kPairHalf = 2;
   template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Split& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, P == 0 ? b.lo : b.hi, c, 0, 0, 0);
   }
@@ -164,14 +223,19 @@ template <> struct Tile<Bf16> {
   template <int P> static __device__ __forceinline__ f32x4 part(const Split& a, const Split& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(P == 0 ? a.lo : a.hi, P == 1 ? b.lo : b.hi, c, 0, 0, 0);
   }
+  template <int P> static __device__ __forceinline__ f32x4 part(const Pair& a, const Pair& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(P == 0 ? a.lo : a.hi, P == 1 ? b.lo : b.hi, c, 0, 0, 0);
+  }
+  template <int P> static __device__ __forceinline__ f32x4 part(const Pair& a, const Half& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(P == 0 ? a.lo : a.hi, b.v, c, 0, 0, 0);
+  }
   template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Fine& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, P == 0 ? b.lo : P == 1 ? b.mid : b.hi, c, 0, 0, 0);
   }
   static __device__ __forceinline__ f32x4 mul(const Exact& a, const Exact& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
   }
-  // by whole words: entries taken from the bf16 vector itself under a condition
-  // have all come out as the first one
+  // by whole words: a bit cast of one entry of a vector has come out as that of its first
   static __device__ __forceinline__ float value(const Exact& a, int e) {
     const uint32_t w = __builtin_bit_cast(u32x4, a.v)[e / 2];
     return __uint_as_float(e % 2 ? w & 0xFFFF0000u : w << 16);
@@ -186,13 +250,13 @@ template <> struct Tile<Bf16> {
     return {__builtin_bit_cast(bf16x8, w)};
   }
   // A frag as it lies in memory: 64 lanes x 16 bytes of the high parts, then the low ones.
-  static __device__ __forceinline__ void put(char* frag, int lane, const Split& s) {
+  static __device__ __forceinline__ void put(char* frag, int lane, const Pair& s) {
     *reinterpret_cast<u32x4*>(frag + lane * 16) = __builtin_bit_cast(u32x4, s.hi);
     *reinterpret_cast<u32x4*>(frag + 1024 + lane * 16) = __builtin_bit_cast(u32x4, s.lo);
   }
-  static __device__ __forceinline__ Split get(const char* frag, int lane) {
-    return {__builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(frag + lane * 16)),
-            __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(frag + 1024 + lane * 16))};
+  static __device__ __forceinline__ Pair get(const char* frag, int lane) {
+    return {__builtin_bit_cast(f16x8, *reinterpret_cast<const u32x4*>(frag + lane * 16)),
+            __builtin_bit_cast(f16x8, *reinterpret_cast<const u32x4*>(frag + 1024 + lane * 16))};
   }
 };
 
@@ -201,14 +265,19 @@ template <> struct Tile<F32> {
   struct Exact { f32x4 a, b; };
   using Split = Exact;
   using Fine = Exact;
+  using Pair = Exact;
+  using Half = Exact;
+  static constexpr bool kScaled = false;
 
-  static constexpr int kExactSplit = 8, kSplitSplit = 8, kExactFine = 8, kSplitExact = 8;
+  static constexpr int kExactSplit = 8, kSplitSplit = 8, kExactFine = 8, kSplitExact = 8, kPairPair = 8, kPairHalf = 8;
   template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Exact& b, f32x4 c) {
     if constexpr (P < 4) return __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[P], b.a[P], c, 0, 0, 0);
     else return __builtin_amdgcn_mfma_f32_16x16x4f32(a.b[P - 4], b.b[P - 4], c, 0, 0, 0);
   }
   static __device__ __forceinline__ Split split(const f32x4& a, const f32x4& b) { return {a, b}; }
   static __device__ __forceinline__ Fine fine(const f32x4& a, const f32x4& b) { return {a, b}; }
+  static __device__ __forceinline__ Pair pair(const f32x4& a, const f32x4& b, float) { return {a, b}; }
+  static __device__ __forceinline__ Half half(const f32x4& a, const f32x4& b, float) { return {a, b}; }
   static __device__ __forceinline__ f32x4 mul(const Exact& a, const Exact& b, f32x4 c) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[e], b.a[e], c, 0, 0, 0);

@@ -1,5 +1,5 @@
 // delta_walk.h -- how the kernels that walk a sequence's chunks bring a chunk
-// into LDS: K, Q, two sets of frags, three vectors and the workgroup's columns
+// into LDS: K, Q, two sets of frags, their vectors and the workgroup's columns
 // of one more tensor.
 //
 // Where the walks fill the chip (eight waves a workgroup), a chunk's loads go
@@ -36,7 +36,7 @@ template <typename D, int KP, int NW> struct WalkLds {
   __attribute__((aligned(16))) S q[C * Rows::LD];
   __attribute__((aligned(16))) S x[C * Cols::LD];
   __attribute__((aligned(16))) char f[2 * kDeltaFrags<C> * kFragBytes];
-  __attribute__((aligned(16))) float v[3 * C];
+  __attribute__((aligned(16))) float v[kWalkVectors<D, C>];
 };
 
 template <typename D, int KP, int NW, bool VEC> struct WalkStage {
@@ -47,10 +47,11 @@ template <typename D, int KP, int NW, bool VEC> struct WalkStage {
   static constexpr int XW = 2 * NW;  // octets of a row of x
   static constexpr int KN = C * KP / 8, XN = C * XW, FN = 2 * kDeltaFrags<C> * kFragBytes / 16;
   static constexpr int KO = (KN + THREADS - 1) / THREADS, XO = XN / THREADS, FO = FN / THREADS;
-  static_assert(XN % THREADS == 0 && FN % THREADS == 0 && 3 * C <= THREADS);
+  static constexpr int VN = kWalkVectors<D, C>, VO = (VN + THREADS - 1) / THREADS;
+  static_assert(XN % THREADS == 0 && FN % THREADS == 0);
   E k[KO], q[KO], x[XO];
   u32x4 f[FO];
-  float v;
+  float v[VO];
 
   // A thread's column of each tensor in bytes (fp32: of its second half too),
   // made once; a chunk's rows end at `end`, and lanes behind it load its last.
@@ -90,7 +91,7 @@ template <typename D, int KP, int NW, bool VEC> struct WalkStage {
                                         const char* frags, const float* vectors) {
     const S *rk = tk + t0 * p.k_t, *rq = tq + t0 * p.q_t, *rx = tx + t0 * x_t;
     const int32_t last = end - t0 - 1;
-    constexpr int ALL = 2 * KO + XO + FO + 1, LO = ALL * P / N, HI = ALL * (P + 1) / N;
+    constexpr int ALL = 2 * KO + XO + FO + VO, LO = ALL * P / N, HI = ALL * (P + 1) / N;
     // hidden, or all these addresses would be made ahead of the loop and held
     const int tid = VEC ? id : (int)lane_offset(id);
     auto rows = [&](const S* m, int64_t ld, int i, int wide, const uint32_t (&c)[2], int c0, int W) {
@@ -110,7 +111,8 @@ template <typename D, int KP, int NW, bool VEC> struct WalkStage {
         const int o = n - 2 * KO - XO;
         f[o] = *reinterpret_cast<const u32x4*>(in_row(frags + o * THREADS * 16, id * 16u));
       } else {
-        v = *in_row(vectors, (id < 3 * C ? id : 0) * 4u);
+        const int o = n - 2 * KO - XO - FO, at = id + o * THREADS;
+        v[o] = *in_row(vectors, (at < VN ? at : 0) * 4u);
       }
     }
   }
@@ -137,7 +139,9 @@ template <typename D, int KP, int NW, bool VEC> struct WalkStage {
     else stage_rows<true>(l, p, len);
 #pragma unroll
     for (int o = 0; o < FO; ++o) reinterpret_cast<u32x4*>(l.f)[id + o * THREADS] = f[o];
-    if (id < 3 * C) l.v[id] = v;
+#pragma unroll
+    for (int o = 0; o < VO; ++o)
+      if ((o + 1) * THREADS <= VN || id + o * THREADS < VN) l.v[id + o * THREADS] = v[o];
   }
 };
 
@@ -206,12 +210,12 @@ __device__ __forceinline__ void rows_times_state(const typename D::storage* lk, 
                                                  f32x4 (&y)[NT], int lane, F&& last, G&& piece) {
   using T = Tile<D>;
   typename T::Exact kf[2][NT], qf[NT];
-  typename T::Split sp[2];
+  typename T::Fine sp[2];
   auto load = [&](const typename D::storage* m, int c, typename T::Exact (&to)[NT]) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) to[t] = Rows::rows(m, 16 * t, 32 * c, lane);
   };
-  auto split = [&](int c) { sp[c & 1] = T::split(s[2 * c], s[2 * c + 1]); };
+  auto split = [&](int c) { sp[c & 1] = T::fine(s[2 * c], s[2 * c + 1]); };
   load(lk, 0, kf[0]);
 #pragma unroll
   for (int t = 0; t < NT; ++t) x[t] = y[t] = zero4();
@@ -227,7 +231,7 @@ __device__ __forceinline__ void rows_times_state(const typename D::storage* lk, 
     piece(std::integral_constant<int, BOTH ? 2 * c : c>());
     keep_order();
     if constexpr (!BOTH && c + 1 < KS) split(c + 1);
-    each_part<T::kExactSplit>([&](auto P) {
+    each_part<T::kExactFine>([&](auto P) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) x[t] = T::template part<P>(kf[c & B][t], sp[c & 1], x[t]);
     });
@@ -238,7 +242,7 @@ __device__ __forceinline__ void rows_times_state(const typename D::storage* lk, 
       piece(std::integral_constant<int, 2 * c + 1>());
       keep_order();
       if constexpr (c + 1 < KS) split(c + 1);
-      each_part<T::kExactSplit>([&](auto P) {
+      each_part<T::kExactFine>([&](auto P) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) y[t] = T::template part<P>(qf[t], sp[c & 1], y[t]);
       });
@@ -248,32 +252,49 @@ __device__ __forceinline__ void rows_times_state(const typename D::storage* lk, 
 }
 
 // x += (the triangle's frags) y: lower rows meet columns of steps c <= t / 2,
-// upper ones c >= t / 2.
+// upper ones c >= t / 2.  y is an operand made with the factor whose inverse is
+// `down`; rows: the inverses of the factors of the triangle's rows of tiles.
 template <typename D, bool LOWER, int NF, typename Y, int NT>
-__device__ __forceinline__ void triangle_times(const typename Tile<D>::Split (&tri)[NF],
-                                               const Y (&y)[NT / 2], f32x4 (&x)[NT]) {
+__device__ __forceinline__ void triangle_times(const typename Tile<D>::Pair (&tri)[NF], const Y (&y)[NT / 2],
+                                               f32x4 (&x)[NT], float down, const f32x4& rows) {
   using T = Tile<D>;
   constexpr int C = 16 * NT, CS = NT / 2;
-  constexpr int N = std::is_same<Y, typename T::Split>::value ? T::kSplitSplit : T::kSplitExact;
+  constexpr int N = std::is_same<Y, typename T::Pair>::value ? T::kPairPair : T::kPairHalf;
+  f32x4 own[NT];
+  if constexpr (T::kScaled) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) own[t] = zero4();
+  }
+  f32x4(&to)[NT] = T::kScaled ? own : x;
   each_part<CS * N>([&](auto P) {
     constexpr int c = P / N;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       if (LOWER ? c <= t / 2 : c >= t / 2)
-        x[t] = T::template part<P % N>(tri[LOWER ? lower_frag<C>(t, c) : upper_frag<C>(t, c)], y[c], x[t]);
+        to[t] = T::template part<P % N>(tri[LOWER ? lower_frag<C>(t, c) : upper_frag<C>(t, c)], y[c], to[t]);
   });
+  if constexpr (T::kScaled) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) x[t] += own[t] * (rows[t] * down);
+  }
 }
 
 template <typename D, int NF>
-__device__ __forceinline__ void load_triangle(typename Tile<D>::Split (&tri)[NF], const char* f, int lane) {
+__device__ __forceinline__ void load_triangle(typename Tile<D>::Pair (&tri)[NF], const char* f, int lane) {
 #pragma unroll
   for (int x = 0; x < NF; ++x) tri[x] = Tile<D>::get(f + x * kFragBytes, lane);
 }
 
+// A column's tiles as operands beside a triangle; returns the inverse of their factor.
 template <typename D, int NT>
-__device__ __forceinline__ void split_tiles(const f32x4 (&u)[NT], typename Tile<D>::Split (&o)[NT / 2]) {
+__device__ __forceinline__ float pair_tiles(const f32x4 (&u)[NT], typename Tile<D>::Pair (&o)[NT / 2]) {
+  float most = 0.f;
 #pragma unroll
-  for (int c = 0; c < NT / 2; ++c) o[c] = Tile<D>::split(u[2 * c], u[2 * c + 1]);
+  for (int t = 0; t < NT; ++t) most = max4(u[t], most);
+  const Pow2 by(Tile<D>::kScaled ? groups_max(most) : 1.f);
+#pragma unroll
+  for (int c = 0; c < NT / 2; ++c) o[c] = Tile<D>::pair(u[2 * c], u[2 * c + 1], by.up);
+  return by.down;
 }
 
 template <typename D, int NT>

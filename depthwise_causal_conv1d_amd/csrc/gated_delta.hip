@@ -106,7 +106,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
              (ends / 16 - 1) * tiles16(p.K) * 256;
     f32x4 u[NT], y[NT];  // K S, then R, then U; Q S, then O
     typename T::Exact vv[CS];
-    typename T::Split tri[NF], us[CS];
+    typename T::Pair tri[NF], us[CS];
     rows_times_state<D, Rows, KS, NT, true>(
         l.k, l.q, s, u, y, lane,
         [&] {
@@ -127,12 +127,12 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
         y[t][e] *= p.scale * gam[e];
       }
     }
-    split_tiles<D>(u, us);
-    triangle_times<D, true>(tri, us, u);
+    float down = pair_tiles<D>(u, us);
+    triangle_times<D, true>(tri, us, u, down, lds4(l.v + kDeltaFactors<C>));
     keep_order();
     load_triangle<D>(tri, l.f + NF * kFragBytes, lane);
     keep_order();
-    split_tiles<D>(u, us);
+    down = pair_tiles<D>(u, us);
     const float whole = l.v[C - 1];
     typename T::Fine fine[CS];
 #pragma unroll
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
     fine_tiles<D>(u, fine);
 #pragma unroll
     for (int t = 0; t < KT; ++t) s[t] *= whole;
-    triangle_times<D, true>(tri, us, y);
+    triangle_times<D, true>(tri, us, y, down, lds4(l.v + kDeltaFactors<C> + 4));
     keep_order();
     cols_times<D, Rows>(l.k, fine, s, lane);
 #pragma unroll

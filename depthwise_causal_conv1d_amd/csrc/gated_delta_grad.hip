@@ -117,7 +117,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
     float* mark = a.dstates + at * delta_state_floats(p.K, p.V) + (ends / 16 - 1) * tiles16(p.K) * 256;
     f32x4 u[NT], none[NT];    // K dS, then dU, then dR
     typename T::Exact go[CS]; // dO
-    typename T::Split tri[NF], us[CS];
+    typename T::Pair tri[NF], us[CS];
     rows_times_state<D, Rows, KS, NT, false>(
         l.k, l.q, s, u, none, lane,
         [&] {
@@ -131,11 +131,32 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
         });
 #pragma unroll
     for (int t = 0; t < NT; ++t) u[t] *= lds4(l.v + C + 16 * t + 4 * g);
-    triangle_times<D, false>(tri, go, u);
+    {  // P^T dO; the factors of P^T's columns go by dO's rows
+      const f32x4 steps = lds4(l.v + kDeltaFactors<C> + 4);
+      f32x4 y[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = T::value(go[t / 2], 4 * (t & 1) + e);
+          y[t][e] = T::kScaled ? x * steps[t / 2] : x;
+        }
+      float most = 0.f;
+      if constexpr (T::kScaled) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) most = max4(y[t], most);
+        most = groups_max(most);
+      }
+      const Pow2 by(most);
+      typename T::Half half[CS];
+#pragma unroll
+      for (int c = 0; c < CS; ++c) half[c] = T::half(y[2 * c], y[2 * c + 1], by.up);
+      triangle_times<D, false>(tri, half, u, by.down, (f32x4){1.f, 1.f, 1.f, 1.f});
+    }
     keep_order();
     load_triangle<D>(tri, l.f, lane);
     keep_order();
-    split_tiles<D>(u, us);
+    const float down = pair_tiles<D>(u, us);
     const float whole = l.v[C - 1];
     typename T::Fine fine[CS];
 #pragma unroll
@@ -151,7 +172,7 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
       }
       fine[c] = T::fine(y[0], y[1]);
     }
-    triangle_times<D, false>(tri, us, u);
+    triangle_times<D, false>(tri, us, u, down, lds4(l.v + kDeltaFactors<C>));
     keep_order();
     cols_times<D, Rows>(l.q, fine, s, lane);
     if (ends - 16 < p.V) {
@@ -439,7 +460,7 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
       f32x4 u[NT], none[NT];
       float rv[4 * NT];
       typename T::Exact vv[CS];
-      typename T::Split tri[NF];
+      typename T::Pair tri[NF];
       rows_times_state<D, Rows, KS, NT, false>(l.k, l.q, st, u, none, lane, [&] {
 #pragma unroll
         for (int c = 0; c < CS; ++c) vv[c] = Rows::cols(l.u, 32 * c, c16, lane);
@@ -461,9 +482,9 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         if (r < 4 * NT) *to = first ? sv : *to + sv;
       }
       {
-        typename T::Split us[CS];
-        split_tiles<D>(u, us);
-        triangle_times<D, true>(tri, us, u);
+        typename T::Pair us[CS];
+        const float down = pair_tiles<D>(u, us);
+        triangle_times<D, true>(tri, us, u, down, lds4(l.v + kDeltaFactors<C> + kFactorsN));
       }
       // the first step's rows of S0 and dS1 are on their way over the barrier
       const int steps = (min(KP, p.V - v0) + 31) / 32;
@@ -577,7 +598,8 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         for (int e = 0; e < 4; ++e) {
           const int i = 16 * I + 4 * g + e, x = i * Tri::LD + Tri::pos(j);
           constexpr float kLog2e = 1.44269504088896340736f;
-          const float d = (l.v[3 * C + i] - l.v[3 * C + j]) + (l.v[4 * C + i] - l.v[4 * C + j]);
+          const float* G = l.v + kDeltaSums<C>;
+          const float d = (G[i] - G[j]) + (G[C + i] - G[C + j]);
           const float dec = __builtin_amdgcn_exp2f(i >= j ? d * kLog2e : 0.f);
           const float pv = i >= j ? p.scale * dec * ep[m][e] : 0.f;
           const float av = i > j ? dec * ea[m][e] : 0.f;

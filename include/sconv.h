@@ -804,8 +804,9 @@ int rms_norm_bwd(const void* dout, int64_t dout_stride_r, const void* x, int64_t
  *
  * q, k, v and out share one element type; g and beta are of that type or fp32
  * (gate_dtype); states, checkpoints and their gradients are fp32.  All sums
- * are fp32.  bf16 inputs: values computed in fp32 enter the matrix products as
- * the sum of two bf16 parts (16 bits of them), fp32 inputs as they are.
+ * are fp32.  bf16 inputs: values computed in fp32 enter the matrix products in
+ * parts that hold 22 bits of them or more, in the products that make a chunk's
+ * gradients from its states and values 16 bits; fp32 inputs enter as they are.
  * A g below -200 counts as -200, whose exponential is zero (-inf closes the
  * state).  An infinite or NaN input makes the rest of its sequence, and the
  * chunk of 64 tokens (fp32: 32) that it lies in, NaN or infinite for all value

@@ -53,3 +53,81 @@ def test_gradients_of_nearly_closed_gates(dtype, shape):
     bad = (off > lim).nonzero()
     assert not len(bad), [(int(t), int(h), float(c.g[t, h]), float(off[t, h]), float(want[t, h]), float(lim[t, h]))
                           for t, h in bad[:4]]
+
+
+def off(got, want):
+    """Relative error in the 2-norm."""
+    return float((got.double() - want).norm() / want.norm())
+
+
+def in_64_bits(c, grads=False):
+    """Outputs of c's one sequence from the definition in 64 bits on the GPU, token
+    by token; with gradients too, the states kept at every 64th token."""
+    group = c.vh // c.kh
+    f = lambda t: t.cuda().double()  # noqa: E731
+    q, k = (f(t).repeat_interleave(group, 1) for t in (c.q, c.k))
+    v, g, beta, dout = (f(t) for t in (c.v, c.g, c.beta, c.dout))
+
+    def step(s, t):
+        old = s * torch.exp(g[t])[:, None, None]
+        err = v[t] - (old * k[t][:, :, None]).sum(1)
+        new = old + k[t][:, :, None] * (beta[t][:, None] * err)[:, None, :]
+        return old, err, new
+
+    s = f(c.h0[0]) * float(c.has[0])
+    out, marks = torch.empty_like(v), []
+    for t in range(c.T):
+        if t % 64 == 0:
+            marks.append(s)
+        s = step(s, t)[2]
+        out[t] = c.scale * (s * q[t][:, :, None]).sum(1)
+    got = dict(out=out, last=s)
+    if not grads:
+        return got
+    ds = f(c.dfinal[0])
+    dq, dk, dv, dg, db = (torch.empty_like(t) for t in (q, k, v, g, beta))
+    for m in range(len(marks) - 1, -1, -1):
+        lo, hi, s, kept = 64 * m, min(64 * m + 64, c.T), marks[m], []
+        for t in range(lo, hi):
+            kept.append(step(s, t))
+            s = kept[-1][2]
+        for t in range(hi - 1, lo - 1, -1):
+            old, err, new = kept[t - lo]
+            dq[t] = c.scale * (new * dout[t][:, None, :]).sum(2)
+            ds = ds + c.scale * q[t][:, :, None] * dout[t][:, None, :]
+            du = (ds * k[t][:, :, None]).sum(1)
+            db[t] = (du * err).sum(1)
+            dv[t] = beta[t][:, None] * du
+            dk[t] = (ds * (beta[t][:, None] * err)[:, None, :]).sum(2) - (old * dv[t][:, None, :]).sum(2)
+            ds = ds - k[t][:, :, None] * dv[t][:, None, :]
+            dg[t] = (ds * old).sum((1, 2))
+            ds = ds * torch.exp(g[t])[:, None, None]
+    pair = lambda t: t.unflatten(1, (c.kh, group)).sum(2)  # noqa: E731
+    return got | dict(dq=pair(dq), dk=pair(dk), dv=dv, dg=dg, dbeta=db, dinitial=ds * float(c.has[0]))
+
+
+# In norms, of sums of many terms of either sign: a value that enters a product rounded to
+# half a step e is off by e / 3 in the root mean square, of three factors so rounded and
+# fp32 sums of 128 and 64 terms (sqrt(128) EPS / 2) each.  Operands of 22 bits or more: e is
+# 2^-22.  A state of decays of 0.999 adds up what some 1000 tokens' chunks (16 of 64) left in
+# it at random: four times as much.  Twice that for gradients, behind two walks.
+VALUES = (3 * 2.0 ** -22 / 3) + 6 * D.EPS
+LONG = [("bf16", 1, 2, 128, 128), ("bf16", 1, 1, 64, 40), ("f32", 1, 1, 128, 77)]
+
+
+@pytest.mark.parametrize("dtype,kh,vh,K,V", LONG)
+@pytest.mark.parametrize("decay", [0.999, 0.99])
+def test_states_of_many_chunks_keep_32_bits(dtype, kh, vh, K, V, decay):
+    """4096 tokens of slow decays: what a state is off by is that of fp32 sums, not of
+    what operands leave out of it (two bf16 parts of each: 2e-6)."""
+    c = Case([4096], kh, vh, K, V, dtype, seed=33, inits=(0,), rate=0.0)
+    c.g[:] = torch.log(torch.tensor(decay))
+    d = c.gpu()
+    out, _ = c.forward(d, marks=False)
+    want = in_64_bits(c)
+    assert off(d["pool"][int(c.slots[0])], want["last"]) < 4 * VALUES
+    assert off(out, want["out"]) < 4 * VALUES + R.half_step(out.dtype)
+    if dtype == "bf16":
+        # one output in 2000 rounds to the other neighbour: an error e moves a share of
+        # e / 2^-8 of the values by a step, 2^-7 to 2^-8 of them (two parts: 1.1e-4)
+        assert off(out, want["out"].bfloat16().double()) < (4 * VALUES / 2.0 ** -8) ** 0.5 * 2.0 ** -8
