@@ -134,12 +134,12 @@ __device__ __forceinline__ float max4(const f32x4& a, float m) {
   return fmaxf(fmaxf(fmaxf(m, fabsf(a[0])), fmaxf(fabsf(a[1]), fabsf(a[2]))), fabsf(a[3]));
 }
 // A power of two that brings `most` to [2^14, 2^15) (a value below 2^-111 less
-// far), and 1 / it.
+// far), and 1 / it.  An infinite value leaves nothing of those beside it: NaN for all.
 struct Pow2 {
   float up, down;
   explicit __device__ __forceinline__ Pow2(float most) {
     const uint32_t b = min(268u - (__float_as_uint(most) >> 23), 253u);
-    up = __uint_as_float(b << 23), down = __uint_as_float((254u - b) << 23);
+    up = __uint_as_float(b << 23) + (most - most), down = __uint_as_float((254u - b) << 23);
   }
 };
 

@@ -131,3 +131,38 @@ def test_states_of_many_chunks_keep_32_bits(dtype, kh, vh, K, V, decay):
         # one output in 2000 rounds to the other neighbour: an error e moves a share of
         # e / 2^-8 of the values by a step, 2^-7 to 2^-8 of them (two parts: 1.1e-4)
         assert off(out, want["out"].bfloat16().double()) < (4 * VALUES / 2.0 ** -8) ** 0.5 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v", "g", "beta"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_an_infinite_input_spoils_no_value_silently(dtype, where):
+    """Every output ahead of an infinite (or huge) input, and beside an infinite q, is
+    what it is without it, or not finite; sequences and value heads that do not read it
+    keep their bits."""
+    c = Case([100, 90], 1, 2, 64, 48, dtype, seed=35, inits=(0, 1))
+    d = c.gpu()
+    clean, m = c.forward(d)
+    keep = d["pool"].clone()
+    c2 = Case([100, 90], 1, 2, 64, 48, dtype, seed=35, inits=(0, 1))
+    at = getattr(c2, where)
+    spot = (70, 0, 5) if at.dim() == 3 else (70, 0)
+    at[spot] = -1e38 if where == "beta" else float("inf")
+    if where == "g":
+        at[spot] = float("nan")
+    d2 = c2.gpu()
+    out, _ = c2.forward(d2)
+    assert torch.equal(R.bits(out[100:]), R.bits(clean[100:]))
+    other = 1 if where in ("v", "g", "beta") else None
+    if other is not None:
+        assert torch.equal(R.bits(out[:, other]), R.bits(clean[:, other]))
+    # a value beside it may be rounded with it: by a share of the row that it is in
+    fine = out.isfinite()
+    near = (out.float() - clean.float()).abs() <= 2.0 ** -6 * clean.float().abs().amax(2, keepdim=True)
+    before = torch.zeros_like(fine)
+    before[:70] = True  # tokens ahead of it see nothing of it
+    assert bool((near | ~fine)[before].all())
+    if where == "q":  # it enters one token's output alone
+        assert bool((near | ~fine).all())
+        assert torch.equal(R.bits(d2["pool"][c2.slots[0].long()]), R.bits(keep[c.slots[0].long()]))
+    if where != "beta":  # -1e38 is finite, and so may what it makes be
+        assert not bool(out[70, 0].isfinite().all())
