@@ -26,8 +26,8 @@
 // state), and beside each other (R, U, N, P) as the sum of two fp16 parts of the
 // value times a power of two that brings the largest of its tile or column to 2^14:
 // 22 bits, down to 2^-17 of that largest.  Three products of such parts take what
-// three of two bf16 parts do, which hold 16 bits.  Sums are fp32.  fp32 inputs:
-// fp32 matrix instructions, nothing is split.
+// three of two bf16 parts do, which hold 16 bits and are left where only bf16 dq and dk
+// come of them.  Sums are fp32.  fp32 inputs: fp32 matrix instructions, nothing is split.
 #pragma once
 
 #include <type_traits>
@@ -166,6 +166,32 @@ template <> struct Tile<Bf16> {
     }
     return o;
   }
+  static __device__ __forceinline__ Half as_half(const Exact& a) { return {__builtin_bit_cast(f16x8, a.v)}; }
+  static __device__ __forceinline__ Pair as_pair(const Exact& hi, const Exact& lo) {
+    return {__builtin_bit_cast(f16x8, hi.v), __builtin_bit_cast(f16x8, lo.v)};
+  }
+  // The larger sizes of eight entries and of `most` (pairs of them).
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  static __device__ __forceinline__ u16x2 larger(const Exact& x, u16x2 most) {
+    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+    const u16x8 w = __builtin_bit_cast(u16x8, __builtin_bit_cast(u32x4, x.v) & 0x7FFF7FFFu);
+    return __builtin_elementwise_max(__builtin_elementwise_max(__builtin_elementwise_max(w.s01, w.s23), most),
+                                     __builtin_elementwise_max(w.s45, w.s67));
+  }
+  // Eight entries times a power of two as fp16, which has their 8 bits.
+  static __device__ __forceinline__ Exact scaled(const Exact& x, float up) {
+    f32x4 a, b;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = value(x, e), b[e] = value(x, e + 4);
+    return {__builtin_bit_cast(bf16x8, half(a, b, up).v)};
+  }
+  // One entry of a pair in storage, and back.
+  static __device__ __forceinline__ void put_pair(uint16_t& hi, uint16_t& lo, float x) {
+    const _Float16 h = (_Float16)x;
+    hi = __builtin_bit_cast(uint16_t, h);
+    lo = __builtin_bit_cast(uint16_t, (_Float16)(x - (float)h));
+  }
+  static __device__ __forceinline__ float value(const Pair& a, int e) { return (float)a.hi[e] + (float)a.lo[e]; }
   // of values of 8 bits
   static __device__ __forceinline__ Half half(const f32x4& a, const f32x4& b, float up) {
     Half o;
@@ -195,39 +221,22 @@ template <> struct Tile<Bf16> {
     }
     return o;
   }
-  static __device__ __forceinline__ Split split(const f32x4& a, const f32x4& b) {
-    Split o;
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const f32x2 x = e < 4 ? (f32x2){a[e], a[e + 1]} : (f32x2){b[e - 4], b[e - 3]};
-      const bf16x2 h = __builtin_convertvector(x, bf16x2);
-      const uint32_t w = __builtin_bit_cast(uint32_t, h);
-      const f32x2 rest = {x[0] - __uint_as_float(w << 16), x[1] - __uint_as_float(w & 0xFFFF0000u)};
-      const bf16x2 l = __builtin_convertvector(rest, bf16x2);
-      o.hi[e] = h[0], o.hi[e + 1] = h[1];
-      o.lo[e] = l[0], o.lo[e + 1] = l[1];
-    }
-    return o;
-  }
   // A product's instructions one by one, the small parts first, so that a
   // caller can let those of several tiles alternate: one that waits for the
   // last one's sum leaves the matrix core idle.
-  static constexpr int kExactSplit = 2, kSplitSplit = 3, kExactFine = 3, kSplitExact = 2, kPairPair = 3, kPairHalf = 2;
-  template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Split& b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, P == 0 ? b.lo : b.hi, c, 0, 0, 0);
-  }
+  static constexpr int kExactFine = 3, kSplitExact = 2, kPairPair = 3, kPairHalf = 2, kHalfPair = 2;
   template <int P> static __device__ __forceinline__ f32x4 part(const Split& a, const Exact& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(P == 0 ? a.lo : a.hi, b.v, c, 0, 0, 0);
   }
   // the product of the two small parts is below what the parts leave out
-  template <int P> static __device__ __forceinline__ f32x4 part(const Split& a, const Split& b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(P == 0 ? a.lo : a.hi, P == 1 ? b.lo : b.hi, c, 0, 0, 0);
-  }
   template <int P> static __device__ __forceinline__ f32x4 part(const Pair& a, const Pair& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(P == 0 ? a.lo : a.hi, P == 1 ? b.lo : b.hi, c, 0, 0, 0);
   }
   template <int P> static __device__ __forceinline__ f32x4 part(const Pair& a, const Half& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(P == 0 ? a.lo : a.hi, b.v, c, 0, 0, 0);
+  }
+  template <int P> static __device__ __forceinline__ f32x4 part(const Half& a, const Pair& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v, P == 0 ? b.lo : b.hi, c, 0, 0, 0);
   }
   template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Fine& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, P == 0 ? b.lo : P == 1 ? b.mid : b.hi, c, 0, 0, 0);
@@ -269,15 +278,15 @@ template <> struct Tile<F32> {
   using Half = Exact;
   static constexpr bool kScaled = false;
 
-  static constexpr int kExactSplit = 8, kSplitSplit = 8, kExactFine = 8, kSplitExact = 8, kPairPair = 8, kPairHalf = 8;
+  static constexpr int kExactFine = 8, kSplitExact = 8, kPairPair = 8, kPairHalf = 8, kHalfPair = 8;
   template <int P> static __device__ __forceinline__ f32x4 part(const Exact& a, const Exact& b, f32x4 c) {
     if constexpr (P < 4) return __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[P], b.a[P], c, 0, 0, 0);
     else return __builtin_amdgcn_mfma_f32_16x16x4f32(a.b[P - 4], b.b[P - 4], c, 0, 0, 0);
   }
-  static __device__ __forceinline__ Split split(const f32x4& a, const f32x4& b) { return {a, b}; }
   static __device__ __forceinline__ Fine fine(const f32x4& a, const f32x4& b) { return {a, b}; }
   static __device__ __forceinline__ Pair pair(const f32x4& a, const f32x4& b, float) { return {a, b}; }
   static __device__ __forceinline__ Half half(const f32x4& a, const f32x4& b, float) { return {a, b}; }
+  static __device__ __forceinline__ Half as_half(const Exact& a) { return a; }
   static __device__ __forceinline__ f32x4 mul(const Exact& a, const Exact& b, f32x4 c) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[e], b.a[e], c, 0, 0, 0);

@@ -270,8 +270,8 @@ __device__ __forceinline__ float sum_groups(float v) {
 // Row of tile n of a lower triangle of 4 x 4 tiles, counted row by row.
 __device__ __forceinline__ int tile_row(int n) { return n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0; }
 
-// LDS of a workgroup below: K, Q, dO, the parts of U and dR (later of three
-// triangles), vectors, sums of the waves.
+// LDS of a workgroup below: K, Q, dO (bf16: as fp16), the parts of U and dR (later of
+// three triangles), vectors, sums of the waves.
 template <typename D, int KP> struct GradLds {
   using S = typename D::storage;
   static constexpr int C = kDeltaChunk<D>, NW = KP / 16, PARTS = sizeof(S) == 2 ? 2 : 1;
@@ -287,6 +287,10 @@ template <typename D, int KP> struct GradLds {
   __attribute__((aligned(16))) char f[kDeltaFrags<C> * kFragBytes];  // N
   __attribute__((aligned(16))) float v[kDeltaVectors<C>];
   float part[NW][4][C], dots[NW];
+  // the waves' largest |dO|, |dR| and |U| of a block of columns
+  float most[NW][3];
+  // row sums of E_A k.k
+  __attribute__((aligned(16))) float za[C / 16 * (C / 16 + 1) / 2][16];
   // of a tile of z: its rows' and columns' sums (of one on the diagonal, in place
   // of the latter, what passes each of its gates)
   __attribute__((aligned(16))) float z[2][C / 16 * (C / 16 + 1) / 2][16];
@@ -295,14 +299,18 @@ template <typename D, int KP> struct GradLds {
 // One workgroup: all gradients of a chunk's tokens for one key head, its value
 // heads one after another (dq and dk add up in registers, in that order).
 // Columns come in blocks of KP, 16 a wave; then a wave owns 16 of K.
-// 2 x 8192 tokens of 16 heads of 128 x 128 bf16: 428 us for 1.4 GB, 3.4 TB/s.  One
-// workgroup a CU (its tiles take 150 KB of LDS), whose loads (20000 of 58000
-// cycles) and products therefore do not overlap: LDS, then registers (256), bound
-// how many run.  Two parts a value, not three, in the products: a third would
-// take 50 KB more LDS.  It leaves fp32 dg and dbeta of bf16 inputs 4e-6 of their
-// norm off (fp32 inputs: 4e-7); dq, dk and dv round to bf16 at 2e-3.
-template <typename D, int KP, bool GROUPED, bool VEC>
-__global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a) {
+// 2 x 8192 tokens of 16 heads of 128 x 128 bf16: 465 us for 1.4 GB, 3.0 TB/s.  One
+// workgroup a CU (its tiles take 150 KB of LDS), whose loads and products therefore
+// do not overlap: LDS, then registers, bound how many run.  ONE: the value channels are
+// one block, so what adds up over blocks lives behind its first products alone and
+// nothing is spilled (182 of 256 registers, 251 with shared key heads; with blocks 32
+// to 79 are: 8 x 4096 tokens, 16 key and 32 value heads, all of backward 2590 us so,
+// 2270 with ONE).  bf16: dO, dR, U and the states enter as fp16 parts with one factor a
+// block (states: a channel and step) of 22 bits; the triangles E beside K and Q as two
+// bf16 parts, 16 bits, which only dq and dk, rounded to bf16, take.  So fp32 dg and
+// dbeta are 3.5e-7 and 2.9e-7 of their norm off (with 16 bits throughout 4e-6).
+template <typename D, int KP, bool GROUPED, bool ONE, bool VEC>
+__global__ __launch_bounds__(4 * KP, 2) void delta_grad_kernel(DeltaBwd a) {
   using T = Tile<D>;
   using S = typename D::storage;
   using L = GradLds<D, KP>;
@@ -338,10 +346,15 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
     }
   };
   auto rows2 = [&](const S* m, int t0, int c0) {
-    if constexpr (kB)
-      return typename T::Split{Rows::rows(m, t0, c0, lane).v, Rows::rows(m + BIG, t0, c0, lane).v};
-    else
-      return Rows::rows(m, t0, c0, lane);
+    if constexpr (kB) return T::as_pair(Rows::rows(m, t0, c0, lane), Rows::rows(m + BIG, t0, c0, lane));
+    else return Rows::rows(m, t0, c0, lane);
+  };
+  // The factor of a block of columns' U, dR or dO: from every wave's largest.
+  auto factor = [&](int which) {
+    float most = 0.f;
+#pragma unroll
+    for (int n = 0; n < NW; ++n) most = fmaxf(most, l.most[n][which]);
+    return Pow2(most);
   };
   auto tri_rows = [&](const S* m, int t0, int c0) {
     if constexpr (kB)
@@ -368,15 +381,19 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
       x2[o] = load8<D, VEC>(m2, ld2, t, ch.len, c0, W);
     }
   };
-  auto stage2 = [&](S* l1, S* l2, const Octets& x1, const Octets& x2, int w0, int W) {
+  auto masked = [&](const typename T::Exact& x, int o, int w0, int W) {
+    const int i = tid + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
+    return mask8<D>(x, t < ch.len ? W - w0 - c0 : 0);
+  };
+  auto stage2 = [&](S* l1, S* l2, const Octets& x1, const Octets& x2, int w0, int W, auto&& first) {
 #pragma unroll
     for (int o = 0; o < N8; ++o) {
       const int i = tid + o * THREADS, t = i / (KP / 8), c0 = i % (KP / 8) * 8;
-      const int n = t < ch.len ? W - w0 - c0 : 0;
-      Rows::put8(l1, t, c0, mask8<D>(x1[o], n));
-      Rows::put8(l2, t, c0, mask8<D>(x2[o], n));
+      Rows::put8(l1, t, c0, first(masked(x1[o], o, w0, W)));
+      Rows::put8(l2, t, c0, masked(x2[o], o, w0, W));
     }
   };
+  auto as_is = [](const typename T::Exact& x) { return x; };
   // a tile back to memory, 16 bytes a lane where rows are of such vectors
   auto put_tile = [&](S* m, int64_t ld, int w0, int W, auto&& octet) {
 #pragma unroll
@@ -412,7 +429,7 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
 #pragma unroll
     for (int m = 0; m < MINE; ++m) ep[m] = ea[m] = zero4();
 
-    for (int32_t v0 = 0; v0 < p.V; v0 += KP) {
+    for (int32_t v0 = 0; ONE ? v0 == 0 : v0 < p.V; v0 += KP) {
       hide();
       const int c16 = 16 * wave;
       // everything that the block needs from memory, before anything waits
@@ -445,9 +462,28 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
 #pragma unroll
         for (int o = 0; o < FO; ++o) nf[o] = from[min(tid + o * THREADS, F16 - 1)];
       }
+      if constexpr (kB) {  // behind the columns' end dR is zero
+        typename T::u16x2 o_most = 0;
+        float r_most = 0.f;
+#pragma unroll
+        for (int o = 0; o < N8; ++o) o_most = T::larger(masked(xo[o], o, v0, p.V), o_most);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) r_most = max4(y[t], r_most);
+        const float x = __uint_as_float((uint32_t)(o_most[0] > o_most[1] ? o_most[0] : o_most[1]) << 16);
+        const float dm = groups_max(lanes_reduce<16>(x, Larger())), rm = groups_max(lanes_reduce<16>(r_most, Larger()));
+        if (lane == 0) l.most[wave][0] = dm, l.most[wave][1] = rm;
+      }
       __syncthreads();  // the last reads of dO, U, dR and the triangles
-      if (gh == 0 && first) stage2(l.k, l.q, x1, x2, 0, p.K);
-      stage2(l.dout, l.u, xo, xv, v0, p.V);  // V lies in U's place until U replaces it
+      if (gh == 0 && first) stage2(l.k, l.q, x1, x2, 0, p.K, as_is);
+      // V lies in U's place until U replaces it
+      float o_down = 1.f, r_up = 1.f, r_down = 1.f, u_down = 1.f;
+      if constexpr (kB) {
+        const Pow2 by_o = factor(0), by_r = factor(1);
+        o_down = by_o.down, r_up = by_r.up, r_down = by_r.down;
+        stage2(l.dout, l.u, xo, xv, v0, p.V, [&](const typename T::Exact& x) { return T::scaled(x, by_o.up); });
+      } else {
+        stage2(l.dout, l.u, xo, xv, v0, p.V, as_is);
+      }
       if (first) {
 #pragma unroll
         for (int o = 0; o < FO; ++o)
@@ -501,13 +537,28 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         }
       };
       load_states(0);
+      float u_up = 1.f;
+      if constexpr (kB) {
+        float most = 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) most = max4(u[t], most);
+        most = groups_max(lanes_reduce<16>(most, Larger()));
+        if (lane == 0) l.most[wave][2] = most;
+        __syncthreads();
+        const Pow2 by_u = factor(2);
+        u_up = by_u.up, u_down = by_u.down;
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = (16 * t + 4 * g + e) * Rows::LD + Rows::pos(c16 + r);
-          put_split(l.u, BIG, i, u[t][e]);
-          put_split(l.r, BIG, i, y[t][e]);
+          if constexpr (kB) {
+            T::put_pair(l.u[i], l.u[i + BIG], u[t][e] * u_up);
+            T::put_pair(l.r[i], l.r[i + BIG], y[t][e] * r_up);
+          } else {
+            l.u[i] = u[t][e], l.r[i] = y[t][e];
+          }
         }
       __syncthreads();
       put_tile(static_cast<S*>(a.dv) + ch.t0 * a.dv_t + h * a.dv_h, a.dv_t, v0, p.V,
@@ -516,9 +567,10 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
                  S o[8];
                  const auto hi = Rows::get8(l.r, t, c0);
                  if constexpr (kB) {
-                   const auto lo = Rows::get8(l.r + BIG, t, c0);
+                   const auto dr = T::as_pair(hi, Rows::get8(l.r + BIG, t, c0));
+                   const float by = bt * r_down;
 #pragma unroll
-                   for (int e = 0; e < 8; ++e) o[e] = delta_round<D>(bt * (T::value(hi, e) + T::value(lo, e)));
+                   for (int e = 0; e < 8; ++e) o[e] = delta_round<D>(by * T::value(dr, e));
                  } else {
 #pragma unroll
                    for (int e = 0; e < 8; ++e) o[e] = bt * T::value(hi, e);
@@ -541,40 +593,63 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
           w[c & 1][o] = quad_transposed(w[c & 1][o], r);
           z[c & 1][o] = quad_transposed(z[c & 1][o], r);
         }
-        const auto sw = T::split(w[c & 1][0], w[c & 1][1]), sz = T::split(z[c & 1][0], z[c & 1][1]);
-        typename T::Exact fo[2];
-        typename T::Split fr[2], fu[2];
+        // a lane's channel of the states, its largest of these columns near 2^14
+        float w_most = 0.f, z_most = 0.f;
+        if constexpr (kB) {
+          w_most = groups_max(max4(w[c & 1][1], max4(w[c & 1][0], 0.f)));
+          z_most = groups_max(max4(z[c & 1][1], max4(z[c & 1][0], 0.f)));
+        }
+        const Pow2 by_w(w_most), by_z(z_most);
+        const auto sw = T::pair(w[c & 1][0], w[c & 1][1], by_w.up), sz = T::pair(z[c & 1][0], z[c & 1][1], by_z.up);
+        const float q_real = o_down * by_w.down, z_real = r_down * by_w.down, w_real = u_down * by_z.down;
+        typename T::Half fo[2];
+        typename T::Pair fr[2], fu[2];
         auto load_rows = [&](int t) {
-          fo[t & 1] = Rows::rows(l.dout, 16 * t, 32 * c, lane);
+          fo[t & 1] = T::as_half(Rows::rows(l.dout, 16 * t, 32 * c, lane));
           fr[t & 1] = rows2(l.r, 16 * t, 32 * c);
           fu[t & 1] = rows2(l.u, 16 * t, 32 * c);
         };
         load_rows(0);
+        f32x4 sums[2][3];
+        auto add_sums = [&](int t) {
+          if constexpr (kB) {
+            mq[t] += sums[t & 1][0] * q_real;
+            mz[t] += sums[t & 1][1] * z_real;
+            mw[t] += sums[t & 1][2] * w_real;
+          }
+        };
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           if (t + 1 < NT) load_rows(t + 1);
           keep_order();
-          each_part<T::kSplitSplit>([&](auto P) {
-            if constexpr (P < T::kExactSplit) mq[t] = T::template part<P>(fo[t & 1], sw, mq[t]);
-            mz[t] = T::template part<P>(fr[t & 1], sw, mz[t]);
-            mw[t] = T::template part<P>(fu[t & 1], sz, mw[t]);
+          if constexpr (kB) sums[t & 1][0] = sums[t & 1][1] = sums[t & 1][2] = zero4();
+          f32x4 &sq = kB ? sums[t & 1][0] : mq[t], &sr = kB ? sums[t & 1][1] : mz[t], &su = kB ? sums[t & 1][2] : mw[t];
+          each_part<T::kPairPair>([&](auto P) {
+            if constexpr (P < T::kHalfPair) sq = T::template part<P>(fo[t & 1], sw, sq);
+            sr = T::template part<P>(fr[t & 1], sw, sr);
+            su = T::template part<P>(fu[t & 1], sz, su);
           });
+          if (t > 0) add_sums(t - 1);
           keep_order();
         }
+        add_sums(NT - 1);
       }
 #pragma unroll
       for (int m = 0; m < MINE; ++m) {
         const int want = wave + m * NW;
         if (want >= TILES) break;
         const int I = tile_row(want), J = want - I * (I + 1) / 2;
+        f32x4 sp = kB ? zero4() : ep[m], sa = kB ? zero4() : ea[m];
         for (int c = 0; c < steps; ++c) {
           const auto uf = rows2(l.u, 16 * J, 32 * c), rf = rows2(l.r, 16 * I, 32 * c);
-          const auto of = Rows::rows(l.dout, 16 * I, 32 * c, lane);
-          each_part<T::kSplitSplit>([&](auto P) {
-            if constexpr (P < T::kExactSplit) ep[m] = T::template part<P>(of, uf, ep[m]);
-            ea[m] = T::template part<P>(rf, uf, ea[m]);
+          const auto of = T::as_half(Rows::rows(l.dout, 16 * I, 32 * c, lane));
+          each_part<T::kPairPair>([&](auto P) {
+            if constexpr (P < T::kHalfPair) sp = T::template part<P>(of, uf, sp);
+            sa = T::template part<P>(rf, uf, sa);
           });
         }
+        if constexpr (kB) ep[m] += sp * (o_down * u_down), ea[m] += sa * (r_down * u_down);
+        else ep[m] = sp, ea[m] = sa;
       }
     }
     __syncthreads();
@@ -587,7 +662,7 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         if (want >= TILES) break;
         const int I = tile_row(want), J = want - I * (I + 1) / 2;
         const int j = 16 * J + r;
-        f32x4 qk = zero4(), kk = zero4(), z;
+        f32x4 qk = zero4(), kk = zero4(), z, ak;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           const auto kj = Rows::rows(l.k, 16 * J, 32 * s, lane);
@@ -606,8 +681,12 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
           put_split(l.e, SMALL, x, pv);
           put_split(l.e + PARTS * SMALL, SMALL, x, av);
           put_split(l.e + 2 * PARTS * SMALL, SMALL, x, l.v[2 * C + i] * av);
-          z[e] = i > j ? pv * qk[e] - l.v[2 * C + i] * av * kk[e] : 0.f;
+          ak[e] = av * kk[e];
+          z[e] = i > j ? pv * qk[e] - l.v[2 * C + i] * ak[e] : 0.f;
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ak[e] = lanes_reduce<16>(ak[e], Add());
+        if (r == 0) *reinterpret_cast<f32x4*>(&l.za[want][4 * g]) = ak;
         if (I == J) {  // the tile's rows i >= t and columns j < t, lane r's t
           float passes = 0.f;
 #pragma unroll
@@ -658,6 +737,7 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
       return to_float<D>(l.q[i]) * mq[t][e] - bt * (to_float<D>(l.k[i]) * mz[t][e]);
     });
     row_sums(l.part[wave][1], [&](int t, int e, int i) { return to_float<D>(l.k[i]) * mw[t][e]; });
+    row_sums(l.part[wave][2], [&](int t, int e, int i) { return to_float<D>(l.k[i]) * mz[t][e]; });
     __syncthreads();
     f32x4 w[NT], neg[NT];
 #pragma unroll
@@ -685,7 +765,6 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) w[t] -= neg[t];
-    row_sums(l.part[wave][2], [&](int t, int e, int i) { return to_float<D>(l.k[i]) * mz[t][e]; });
     // dq and dk, over the value heads; this wave's channels of Q and K have
     // been read for the last time
 #pragma unroll
@@ -730,6 +809,11 @@ __global__ __launch_bounds__(4 * KP, KP / 64) void delta_grad_kernel(DeltaBwd a)
         }
       const float pairs = lanes_reduce<16>(whole, Add()) + sum_before(below) + sum_from(left) +
                           l.z[1][I * (I + 3) / 2][at16];
+      // k.Z of token t: what it reads of S0, and of the tokens ahead of it
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j <= i; ++j) sz += i == I ? l.za[i * (i + 1) / 2 + j][at16] : 0.f;
       float before = __shfl_up(km, 1, 64), after = own;
       before = lane > 0 ? before : 0.f;
 #pragma unroll
@@ -781,13 +865,18 @@ static int delta_backward(DeltaBwd a, int64_t rows, hipStream_t stream) {
     else hipLaunchKernelGGL((delta_back_kernel<D, KP, 4, true, false>), grid, walk, 0, stream, a);
   }
   if (int rc = check_launch(what)) return rc;
-  const dim3 chunks((uint32_t)rows, p.heads / p.group), threads(4 * KP);
-  if (!(vec && p.v_vec && a.grads_vec))
-    hipLaunchKernelGGL((delta_grad_kernel<D, KP, true, false>), chunks, threads, 0, stream, a);
-  else if (p.group > 1)
-    hipLaunchKernelGGL((delta_grad_kernel<D, KP, true, true>), chunks, threads, 0, stream, a);
-  else
-    hipLaunchKernelGGL((delta_grad_kernel<D, KP, false, true>), chunks, threads, 0, stream, a);
+  auto gradients = [&](auto one) {
+    constexpr bool ONE = decltype(one)::value;
+    const dim3 chunks((uint32_t)rows, p.heads / p.group), threads(4 * KP);
+    if (!(vec && p.v_vec && a.grads_vec))
+      hipLaunchKernelGGL((delta_grad_kernel<D, KP, true, ONE, false>), chunks, threads, 0, stream, a);
+    else if (p.group > 1)
+      hipLaunchKernelGGL((delta_grad_kernel<D, KP, true, ONE, true>), chunks, threads, 0, stream, a);
+    else
+      hipLaunchKernelGGL((delta_grad_kernel<D, KP, false, ONE, true>), chunks, threads, 0, stream, a);
+  };
+  if (p.V <= KP) gradients(std::true_type());
+  else gradients(std::false_type());
   return check_launch(what);
 }
 

@@ -805,8 +805,8 @@ int rms_norm_bwd(const void* dout, int64_t dout_stride_r, const void* x, int64_t
  * q, k, v and out share one element type; g and beta are of that type or fp32
  * (gate_dtype); states, checkpoints and their gradients are fp32.  All sums
  * are fp32.  bf16 inputs: values computed in fp32 enter the matrix products in
- * parts that hold 22 bits of them or more, in the products that make a chunk's
- * gradients from its states and values 16 bits; fp32 inputs enter as they are.
+ * parts that hold 22 bits of them or more, what token pairs of a chunk add to dq
+ * and dk 16 bits; fp32 inputs enter as they are.
  * What a chunk's tokens pass to each other keeps those 22 bits down to 2^-17 of the
  * largest of its value channel in the chunk, and below that 2^-39 of that largest.
  * A g below -200 counts as -200, whose exponential is zero (-inf closes the

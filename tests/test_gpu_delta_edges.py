@@ -166,3 +166,21 @@ def test_an_infinite_input_spoils_no_value_silently(dtype, where):
         assert torch.equal(R.bits(d2["pool"][c2.slots[0].long()]), R.bits(keep[c.slots[0].long()]))
     if where != "beta":  # -1e38 is finite, and so may what it makes be
         assert not bool(out[70, 0].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype,kh,vh,K,V", LONG + [("bf16", 1, 2, 128, 72), ("bf16", 1, 1, 64, 136)])
+@pytest.mark.parametrize("decay", [0.999, 0.9])
+def test_gradients_of_many_chunks_keep_32_bits(dtype, kh, vh, K, V, decay):
+    """fp32 gradients of gates, betas and states over 1500 tokens: behind two walks,
+    twice what values are off by, and a state's four times as above."""
+    c = Case([1500], kh, vh, K, V, dtype, seed=37, inits=(0,), rate=0.0)
+    c.g[:] = torch.log(torch.tensor(decay))
+    d = c.gpu()
+    _, m = c.forward(d)
+    got, di = c.backward(d, m)
+    want = in_64_bits(c, grads=True)
+    for n in ("dg", "dbeta"):
+        assert off(got[n], want[n]) < 2 * VALUES, n
+    assert off(di[int(c.slots[0])], want["dinitial"]) < 4 * VALUES
+    for n in ("dq", "dk", "dv"):
+        assert off(got[n], want[n]) < 4 * VALUES + R.half_step(got[n].dtype), n
