@@ -184,3 +184,57 @@ def test_gradients_of_many_chunks_keep_32_bits(dtype, kh, vh, K, V, decay):
     assert off(di[int(c.slots[0])], want["dinitial"]) < 4 * VALUES
     for n in ("dq", "dk", "dv"):
         assert off(got[n], want[n]) < 4 * VALUES + R.half_step(got[n].dtype), n
+
+
+def lengths(n):
+    """n sequences, most of a few tokens: around a chunk and its tiles, one empty."""
+    few = [1, 65, 17, 3, 64, 0, 130, 16, 33, 5]
+    return [few[i] if i < len(few) else 1 + i % 7 for i in range(n)]
+
+
+@pytest.mark.parametrize("layout", ["dense", "columns"])
+@pytest.mark.parametrize("n,kh,vh,K,V", [(33, 4, 8, 128, 128), (33, 2, 4, 77, 129), (17, 8, 8, 64, 136),
+                                         (40, 1, 4, 40, 72)])
+def test_walks_of_full_chips(n, kh, vh, K, V, layout):
+    """Enough workgroups for eight computing waves each (more than 256 of 64 columns), aligned
+    rows and others, both widths of K: against the reference, and bit for bit what
+    calls of two sequences, which take the other form, give."""
+    assert n * vh * -(-V // 64) > 256
+    c = Case(lengths(n), kh, vh, K, V, "bf16", seed=41, inits=range(0, n, 3), pads=(3,), trail=3)
+    d = c.gpu(layout)
+    out, m = c.forward(d, layout)
+    got, di = c.backward(d, m, layout)
+    some = Case.__new__(Case)
+    some.__dict__.update(c.__dict__)
+    some.live = [alive and b in (0, 2, 6, 8) for b, alive in enumerate(c.live)]
+    pool = d["pool"].cpu()
+    for b, s, v, e in some.ref():
+        slot = int(c.slots[b])
+        R.check(out[s], v["out"], e["out"], f"out {b}")
+        R.check(pool[slot], v["last"], e["last"][:, None].expand_as(v["last"]), f"state {b}")
+        R.check(di[slot], v["dinitial"], e["dinitial"][:, None].expand_as(v["dinitial"]), f"dinitial {b}")
+        for name, t in got.items():
+            R.check(t[s], v[name], e[name], f"{name} {b}")
+    same = lambda x, y: torch.equal(R.bits(x), R.bits(y))  # noqa: E731
+    for b in range(0, n - 1, 2):
+        two = Case.__new__(Case)
+        two.__dict__.update(c.__dict__)
+        lo, hi = c.bounds[b], c.bounds[b + 2]
+        two.lens, two.live, two.T = c.lens[b:b + 2], c.live[b:b + 2], hi - lo
+        two.slots, two.dfinal = c.slots[b:b + 2], c.dfinal[b:b + 2]
+        for t in ("q", "k", "v", "dout"):
+            setattr(two, t, getattr(c, t)[lo:hi])
+        part = {t: d[t][lo:hi] for t in ("q", "k", "v", "dout", "g", "beta")}
+        part |= dict(pool=c.pool.cuda(), slots=d["slots"][b:b + 2].contiguous(),
+                     has=d["has"][b:b + 2].contiguous(),
+                     qsl=(d["qsl"][b:b + 3] - lo).to(torch.int32).contiguous())
+        out2, m2 = two.forward(part, layout)
+        got2, di2 = two.backward(part, m2, layout)
+        inside = c.inside[lo:hi].cuda()
+        assert same(out[lo:hi][inside], out2[inside]), b
+        for name in got:
+            assert same(got[name][lo:hi][inside], got2[name][inside]), (b, name)
+        for k in (b, b + 1):
+            if c.live[k]:
+                slot = int(c.slots[k])
+                assert same(d["pool"][slot], part["pool"][slot]) and same(di[slot], di2[slot]), k
