@@ -68,17 +68,19 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
   };
 
   if (LOAD && wave >= NW) {
+    // aligned rows' loads are under way over the barrier before the one in which they are
+    // staged; behind the last chunk it is fetched again: a branch would make loads wait
     if (chunks > 0) {
       fetch(0, kFirst, kWhole);
       next.stage(lds[0], p, end - start);
+      if constexpr (VEC) fetch(min(1, chunks - 1), kFirst, kWhole);
     }
     __syncthreads();
     for (int32_t i = 0; i < chunks; ++i) {
-      // behind the last chunk it is fetched again: a branch here would make loads wait
-      fetch(min(i + 1, chunks - 1), kFirst, kWhole);
-      keep_order();
+      if constexpr (!VEC) fetch(min(i + 1, chunks - 1), kFirst, kWhole), keep_order();
       if (i > 0) put_out(i - 1, lds[(i + 1) & 1]);
       if (i + 1 < chunks) next.stage(lds[(i + 1) & 1], p, end - (start + (i + 1) * C));
+      if constexpr (VEC) keep_order(), fetch(min(i + 2, chunks - 1), kFirst, kWhole);
       __syncthreads();
     }
     if (chunks > 0) put_out(chunks - 1, lds[(chunks - 1) & 1]);

@@ -85,16 +85,17 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kerne
   constexpr std::integral_constant<int, 0> kFirst;
   constexpr std::integral_constant<int, 1> kWhole;
 
-  if (LOAD && wave >= NW) {
+  if (LOAD && wave >= NW) {  // as the forward's
     if (chunks > 0) {
       fetch(chunks - 1, kFirst, kWhole);
       stage(chunks - 1, lds[(chunks - 1) & 1]);
+      if constexpr (VEC) fetch(max(chunks - 2, 0), kFirst, kWhole);
     }
     __syncthreads();
     for (int32_t i = chunks - 1; i >= 0; --i) {
-      // ahead of the first chunk it is fetched again: a branch here would make loads wait
-      fetch(max(i - 1, 0), kFirst, kWhole);
+      if constexpr (!VEC) fetch(max(i - 1, 0), kFirst, kWhole);
       if (i > 0) stage(i - 1, lds[(i - 1) & 1]);
+      if constexpr (VEC) keep_order(), fetch(max(i - 2, 0), kFirst, kWhole);
       __syncthreads();
     }
     return;
