@@ -114,10 +114,12 @@ inline int delta_inputs(const DeltaCall& c, DeltaParams& p, const void* q, int64
 // Whether a workgroup of a walk has eight waves on 128 columns and no loaders
 // (else four on 64, and four loaders): it reads half as much LDS a product, on
 // half as many CUs.  Where the narrow ones all have a CU of 256 at once they win
-// (4 x 2048 tokens, 32 heads of 128 x 128 bf16: 156 us, wide 207), beyond that
-// the wide ones (5 x 2048: 219 us, narrow 246; 8 x 4096: 590 and 636).  Products
-// of 32-bit tiles take the same time either way (320 narrow workgroups: 329 us,
-// wide 359; 512: 339 and 336), so they have the narrow form only.
+// (all of forward, 4 x 2048 tokens, 32 heads of 128 x 128 bf16: 176 us, wide 238),
+// beyond that the wide ones (5 x 2048: 240 us, narrow 269; 8 x 4096: 573 and 627; of 64
+// x 128: 427 and 466), but for the few calls of which a little over 256 are wide (9 x
+// 2048 of 64 x 128, 288 of them: 342 and 309).  Products of 32-bit tiles take the
+// same time either way (320 narrow workgroups: 329 us, wide 359; 512: 339 and 336),
+// so they have the narrow form only.
 inline bool delta_wide(const DeltaParams& p) {
   return p.V > 64 && (int64_t)p.batch * p.heads * ((p.V + 63) / 64) > 256;
 }
@@ -125,10 +127,10 @@ inline bool delta_wide(const DeltaParams& p) {
 // Workgroups of a walk with `cols` blocks of columns.  Those of one sequence
 // and key head read the same K and Q, so they take one XCD's cache: numbers 8
 // apart, where that gives the XCDs even shares and they have 16 workgroups each (the
-// call of 8 x 4096 tokens, two value heads a key head: 512 us, in plain order 518; 3 x
-// 4096 of 128 x 256: 215 and 218).  With fewer nothing is gained (1 x 8192 x 16 heads:
-// 356 and 354), and with fewer pairs than XCDs the others idle (1 x 4096, 16 value
-// heads of one key head: 194 and 186; 4 of 8 x 256 columns: 184 and 181).
+// call of 8 x 4096 tokens, two value heads a key head: 585 us, in plain order 589; 3 x
+// 4096 of 128 x 256: 242 and 246).  With fewer nothing is gained (1 x 8192 x 16 heads:
+// 414 either way), and with fewer pairs than XCDs the others idle (1 x 4096, 16 value
+// heads of one key head: 229 and 214; 4 of 8 x 256 columns: 214 and 211).
 inline dim3 delta_walk_grid(DeltaParams& p, int32_t cols) {
   const int64_t pairs = (int64_t)p.batch * (p.heads / p.group), n = (int64_t)p.group * cols;
   const int64_t each = cdiv(pairs, 8);

@@ -105,9 +105,12 @@ template <int C, bool GRAD> constexpr int kPrepFrags = (GRAD ? 3 : 2) * kDeltaFr
 
 // One wave a chunk and value head.  Bound by latency: three waves a SIMD are
 // what the LDS of a triangle leaves room for (8 x 4096 tokens, 32 heads of 128
-// channels bf16: 169 us, 0.9 GB; with whole squares in LDS, which leave room
+// channels bf16: 172 us, 0.8 GB; with whole squares in LDS, which leave room
 // for two, 198 against 162 at the time).  The value heads of a key head
 // read the same rows, so they come 8 workgroups apart: on one XCD, soon after.
+// Rows that are not aligned come entry by entry and take registers for two waves; of
+// more than 64 channels they spill 17, with gradients 58 (4 x 2048 tokens, 8 heads of
+// 100: 48 and 57 us).
 template <typename D, int KP, bool GRAD, bool VEC>
 __global__ __launch_bounds__(64, VEC ? 3 : 2) void delta_prep_kernel(DeltaParams p) {
   using T = Tile<D>;

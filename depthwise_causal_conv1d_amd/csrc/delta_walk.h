@@ -6,8 +6,8 @@
 // out between the products of the chunk ahead of it and wait in registers.
 // Where they do not, a chain of chunks is what takes the time: four waves
 // compute and four more load, stage into a second buffer and store outputs
-// meanwhile (2 x 8192 tokens of 16 heads bf16, forward and backward walk: 524 and
-// 556 us, without them 597 and 640; 449 and 451 since states are stored as tiles).
+// meanwhile (2 x 8192 tokens of 16 heads bf16, forward and backward walk, with states
+// stored as rows: 524 and 556 us, without them 597 and 640; as they are now 443 and 471).
 #pragma once
 
 #include "delta_rule.h"

@@ -21,12 +21,11 @@ struct DeltaFwd {
 // LDS, in V's place, for the next one's staging.
 // Bound by the chain of chunks: a wave of the matrix cores' small tiles feeds
 // them from LDS, where every wave reads all of K and Q.  8 x 4096 tokens, 32 heads
-// of 128 x 128 bf16, eight waves: 364 us (428 when the clock falls in a long run),
-// 1.4 GB; of a chunk's 10600 cycles the products take 6200 (loads between them),
-// outputs and staging 1660, the wait for the last wave 2750.  2 x 8192 tokens
-// of 16 heads with checkpoints, four waves and loaders: 455 us, 3.5 us a chunk.
-// fp32 (16 x 16 x 4 matrix products, an eighth of the bf16 rate and chunks
-// of half the tokens): 3.4 us a chunk of 128 x 77.
+// of 128 x 128 bf16, eight waves: 434 us (546 when the clock falls in a long run),
+// 1.25 GB, 6.8 us a chunk; 364 us with states of two parts, which lose digits.
+// 2 x 8192 tokens of 16 heads with checkpoints, four waves and loaders: 443 us, 3.5 us
+// a chunk.  fp32 is bound by the rate of 16 x 16 x 4 products, an eighth of the bf16
+// ones': 224 of 32 cycles a wave are 3.0 of the 3.4 us of a chunk of 32 x 128 x 77.
 template <typename D, int KP, int NW, bool LOAD, bool VEC>
 __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kernel(DeltaFwd a) {
   using T = Tile<D>;
@@ -68,8 +67,10 @@ __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_walk_kerne
   };
 
   if (LOAD && wave >= NW) {
-    // aligned rows' loads are under way over the barrier before the one in which they are
-    // staged; behind the last chunk it is fetched again: a branch would make loads wait
+    // Aligned rows' loads are under way over the barrier before the one in which they are
+    // staged (1 x 8192 x 16 heads: 430 -> 414 us; entries of others take registers that
+    // are not there: 16 ragged fp32 prompts 253 -> 275).  Behind the last chunk it is
+    // fetched again: a branch would make loads wait.
     if (chunks > 0) {
       fetch(0, kFirst, kWhole);
       next.stage(lds[0], p, end - start);

@@ -47,7 +47,7 @@ __device__ __forceinline__ f32x4* delta_row_tiles(float* drows, int64_t at, int3
 
 // One workgroup walks a sequence's chunks from the last, for one value head
 // and 16 columns a wave of NW; LOAD: as many waves more load.  Bound as the
-// forward's walk: 2 x 8192 tokens, 16 heads of 128 x 128 bf16 in 452 us (640
+// forward's walk: 2 x 8192 tokens, 16 heads of 128 x 128 bf16 in 471 us (640
 // with rows of states stored as they lie and no loaders).
 template <typename D, int KP, int NW, bool LOAD, bool VEC>
 __global__ __launch_bounds__(LOAD ? 128 * NW : 64 * NW, 2) void delta_back_kernel(DeltaBwd a) {
@@ -300,13 +300,15 @@ template <typename D, int KP> struct GradLds {
 // One workgroup: all gradients of a chunk's tokens for one key head, its value
 // heads one after another (dq and dk add up in registers, in that order).
 // Columns come in blocks of KP, 16 a wave; then a wave owns 16 of K.
-// 2 x 8192 tokens of 16 heads of 128 x 128 bf16: 465 us for 1.4 GB, 3.0 TB/s.  One
+// 2 x 8192 tokens of 16 heads of 128 x 128 bf16: 469 us for 1.3 GB, 2.8 TB/s.  One
 // workgroup a CU (its tiles take 150 KB of LDS), whose loads and products therefore
 // do not overlap: LDS, then registers, bound how many run.  ONE: the value channels are
 // one block, so what adds up over blocks lives behind its first products alone and
 // nothing is spilled (182 of 256 registers, 251 with shared key heads; with blocks 32
 // to 79 are: 8 x 4096 tokens, 16 key and 32 value heads, all of backward 2590 us so,
-// 2270 with ONE).  bf16: dO, dR, U and the states enter as fp16 parts with one factor a
+// 2280 with ONE).  Registers are bounded for two workgroups a CU at KP = 64 too, where
+// bf16 tiles leave room for one: fp32 ones do for two (4 x 2048 tokens, heads of 64 x
+// 100: 396 us, with twice the registers 421).  bf16: dO, dR, U and the states enter as fp16 parts with one factor a
 // block (states: a channel and step) of 22 bits; the triangles E beside K and Q as two
 // bf16 parts, 16 bits, which only dq and dk, rounded to bf16, take.  So fp32 dg and
 // dbeta are 3.5e-7 and 2.9e-7 of their norm off (with 16 bits throughout 4e-6).

@@ -5,9 +5,13 @@
 // decide everything; the rest is a search per token.  Up to kMetaReqs
 // requests every workgroup makes both sums for itself in LDS: a few loads a
 // thread, against a second launch that would wait for the first.  Launches one
-// after another in a graph, one (two): 256 requests of one token 4.0 us (5.9), 64
-// of 256 tokens 3.9 (6.6), 1000 of 65 6.0 (11.7), 4096 of 16 13.7 (18.5), 4096 of 64
-// 33 (31).  Latency bounds all: 1000 requests' tokens are 2 MB, 0.4 us.
+// after another in a graph, one (two): 256 requests of one token 4.3 us (6.0), 64
+// of 256 tokens 4.2 (7.0), 1000 of 65 6.3 (10.5), 1000 of 4096 85 (330), 2000 of 512 64
+// (80), 4096 of 16 14.3 (18.1), of 64 34 (31), of 512 234 (181).  Latency bounds the
+// small ones (1000 requests' 65 tokens are 2 MB, 0.4 us).  Thousands of requests are
+// bound by their sums, which every workgroup of the one launch makes again; two make
+// them once, but their one workgroup of sums also fills every table, which takes longer
+// for all but the most.
 #include "sconv_device.h"
 #include "sconv_host.h"
 
