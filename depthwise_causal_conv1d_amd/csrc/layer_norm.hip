@@ -73,7 +73,8 @@ struct RowScale {
   float rest, rstd;
   __device__ __forceinline__ RowScale(float sum, float squares, float n, float eps) {
     rest = sum / n;
-    const float var = squares / n - rest * rest;
+    // fused: rest's square is not rounded, so infinite squares stay so (rstd 0)
+    const float var = __builtin_fmaf(-rest, rest, squares / n);
     rstd = 1.0f / sqrtf((var < 0.f ? 0.f : var) + eps);  // a NaN stays one
   }
   __device__ __forceinline__ float operator()(float d) const { return __builtin_fmaf(d, rstd, -(rest * rstd)); }
@@ -242,11 +243,11 @@ __global__ __launch_bounds__(kNormThreads) void layer_bwd_simple(const LayerBwdP
 // Rows in registers: T threads hold NV vectors of V channels of a row, walk
 // every kRows * gridDim-th row, and keep the weights' sums of their channels.
 // The next row's loads are issued before this row's sums are exchanged, so a
-// workgroup always has a row under way: bytes bound it (32768 x 4096 bf16 161 us,
+// workgroup always has a row under way: bytes bound it (32768 x 4096 bf16 162 us,
 // 5.0 TB/s; with dresidual 189, 5.7 TB/s), and for few rows two launches' latency
 // (1023 x 1001 fp32: 13 + 4 us).  16384 bf16 channels spill 45 registers of 512,
-// and are still faster than the two-pass kernel (4096 x 16384: 244 us; 4096 x
-// 12001, which that one takes, 463).
+// and are still faster than the two-pass kernel (4096 x 16384: 250 us; 4096 x
+// 12001, which that one takes, 462).
 template <typename D, int V, int NV, int T>
 __global__ __launch_bounds__(kNormThreads) void layer_bwd_kernel(const LayerBwdParams p) {
   using S = typename D::storage;
@@ -421,7 +422,7 @@ template <typename D, int V, typename... A> static void launch_layer_n(int nv, i
 // Workgroups of the backward pass; each writes its share of 2 dim sums, which
 // costs more than a workgroup gains below four rows (1000 x 4096 bf16: 20.0 us,
 // 25.9 with two rows each).  Where registers hold the rows one workgroup a CU
-// keeps memory busy (8192 x 8192 bf16: 87 us, two 100), but for short rows from
+// keeps memory busy (8192 x 8192 bf16: 90 us, two 100), but for short rows from
 // eight a workgroup on (2048 x 4096: 23 us, two 27): those of 8 KB (32768 x 4096
 // bf16: 161 us, one 184, four 188; 16384 x 4096 fp32: 150, two 156), or with a
 // fourth stream, dresidual, in vectors of 4 KB (8192 x 2048 bf16: 37, one 44;

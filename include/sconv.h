@@ -944,9 +944,10 @@ int gated_delta_rule_update(
  *            residual or x itself; so may out
  *
  * The variance is summed over differences from the mean, and the mean's rounding
- * is taken out of both: a row far from zero keeps its digits.  A row is read once
- * up to 16384 bf16 or 8192 fp32 channels where rows start and end on 16 bytes,
- * up to 8192 elsewhere; wider rows are read three times.
+ * is taken out of both: a row far from zero keeps its digits.  Where the squares'
+ * sum is beyond the largest float the variance counts as infinite.  A row is
+ * read once up to 16384 bf16 or 8192 fp32 channels where rows start and end on 16
+ * bytes, up to 8192 elsewhere; wider rows are read three times.
  *
  * Host errors (SCONV_ERR_INVALID): negative sizes, eps negative or not
  * finite, NULL required pointer, unknown dtype, partially overlapping buffers.

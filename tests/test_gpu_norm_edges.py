@@ -116,3 +116,21 @@ def test_weights_gradients_of_a_million_equal_rows(rows, dim):
     G, chain = R.f64(g) * rows, 256 * R.EPS
     R.check(db, G, (chain + 8 * R.EPS) * G.abs(), "dbias")
     R.check(dw, G * hat, (chain + 8 * R.EPS) * (G * hat).abs() + G * ehat, "dweight")
+
+
+@pytest.mark.parametrize("dim,odd", [(64, False), (1000, False), (4096, False), (4095, True), (20001, True)])
+@pytest.mark.parametrize("dtype", DT)
+def test_equal_channels_whose_squares_overflow(dtype, dim, odd):
+    """The differences of equal channels from their rounded mean are 0, or all one
+    number of a step of theirs at least, whose square is infinite from 1e28 on: 0
+    times weight plus bias either way, and no share in dweight.  dx is the formula's
+    with rstd = eps^-1/2 or, where squares are infinite, with 0: finite."""
+    x = torch.tensor([2.5e28, 1.1e30, -4.3e33], dtype=torch.float64)[:, None].expand(3, dim).to(DT[dtype])
+    w, b, g = rand(1, dim, dtype=DT[dtype]), rand(2, dim, dtype=DT[dtype]), rand(3, 3, dim, dtype=DT[dtype])
+    out = lib.layer_norm_fwd(on_gpu(x, odd), w.cuda(), b.cuda(), 1e-5, out=on_gpu(x, odd))
+    assert torch.equal(out.cpu(), b.expand(3, dim))
+    dx, dw, db = lib.layer_norm_bwd(on_gpu(g, odd), on_gpu(x, odd), w.cuda(), 1e-5, dx=on_gpu(x, odd))
+    assert dx.isfinite().all()
+    assert torch.equal(dw.cpu(), torch.zeros(dim))
+    # three terms
+    assert ((db.cpu() - g.double().sum(0)).abs() <= 3 * R.EPS * g.double().abs().sum(0)).all()
